@@ -26,9 +26,14 @@ __all__ = ["K3KDAError", "load_library", "library_path", "F32", "BF16", "L2_EPS"
            "k3kda_decode_status", "k3kda_workspace_status",
            "k3kda_backward_workspace_size", "k3kda_backward", "backward",
            "k3kda_decode_step", "prefill", "decode_step", "short_conv",
-           "k3mla_decode_workspace_size", "k3mla_decode_step", "k3mla_decode_step_slots", "mla_decode_step"]
+           "k3mla_decode_workspace_size", "k3mla_decode_step", "k3mla_decode_step_slots", "mla_decode_step",
+           "CACHE_BF16", "CACHE_I4", "RopeTable", "PagedCache", "rope_table", "rope", "rope_backward",
+           "paged_pool", "paged_append", "paged_read",
+           "k3mla_rope_table", "k3mla_rope", "k3mla_rope_backward", "k3mla_paged_block_bytes",
+           "k3mla_paged_append", "k3mla_paged_read"]
 
 F32, BF16 = 0, 1
+CACHE_BF16, CACHE_I4 = 1, 2
 L2_EPS = 1e-6
 _STATUS = {0: "OK", -1: "INVALID_ARG", -2: "UNSUPPORTED", -3: "ALIGNMENT", -4: "WORKSPACE",
            -5: "CUDA", -6: "TIMEOUT"}
@@ -109,8 +114,37 @@ def load_library(build_if_missing: bool = True):
         lib.k3mla_decode_step_slots.argtypes = [P, P, P, I, P, P, P, I, P, P, P, I, I, I, I, I, I, I, F, F, P, I, P,
                                                 Z, P]
         lib.k3mla_decode_step_slots.restype = I
+        D, R, V, C = ctypes.c_double, ctypes.POINTER(_RopeArgs), ctypes.POINTER(_View), ctypes.POINTER(_PagedArgs)
+        lib.k3mla_rope_table.argtypes = [I, D, I, D, D, D, D, P, P]
+        lib.k3mla_rope_table.restype = I
+        lib.k3mla_rope.argtypes = [V, V, I, V, V, I, I, P, I, I, R, P]
+        lib.k3mla_rope.restype = I
+        lib.k3mla_rope_backward.argtypes = [V, V, I, V, V, I, I, I, P, I, I, R, P]
+        lib.k3mla_rope_backward.restype = I
+        lib.k3mla_paged_block_bytes.argtypes = [I, I, I, I]
+        lib.k3mla_paged_block_bytes.restype = Z
+        lib.k3mla_paged_append.argtypes = [C, V, V, I, P, P, I, R, P]
+        lib.k3mla_paged_append.restype = I
+        lib.k3mla_paged_read.argtypes = [C, V, V, I, P, P, I, P]
+        lib.k3mla_paged_read.restype = I
         _lib = lib
         return lib
+
+
+class _RopeArgs(ctypes.Structure):
+    _fields_ = [("phase", ctypes.c_void_p), ("dim", ctypes.c_int), ("offset", ctypes.c_int), ("layout", ctypes.c_int),
+                ("mscale", ctypes.c_float)]
+
+
+class _View(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong)]
+
+
+class _PagedArgs(ctypes.Structure):
+    _fields_ = [("pool", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("block_table_host", ctypes.c_void_p), ("kv_len_host", ctypes.c_void_p), ("format", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("N", ctypes.c_int), ("heads", ctypes.c_int), ("dqk", ctypes.c_int), ("dv", ctypes.c_int)]
 
 
 class _ConvArgs(ctypes.Structure):
@@ -423,3 +457,206 @@ def mla_decode_step(q, k_new, v_new, k_cache, v_cache, cache_len, gate=None, sca
     k3mla_decode_step(q, k_new, v_new, gate, k_cache, v_cache, cache_len, N, H, dqk, dv, L_max, rope_dim, rope_theta,
                       scale, out, workspace, stream)
     return out
+
+
+# ---- rotary positions and the paged cache ----------------------------------
+
+_LAYOUTS = {"half": 0, "interleaved": 1}
+_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
+_FORMATS = {"bf16": CACHE_BF16, "i4": CACHE_I4}
+
+
+def _view(t, what, d=None):
+    """A [tokens, heads, channels] CUDA tensor of any token and head strides, its channels contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"k3mla: {what} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError("k3mla: tensors must live on a CUDA device (no CPU path exists)")
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"k3mla: {what} must be [tokens, heads, channels] with contiguous channels")
+    if d is not None and t.shape[2] != d:
+        raise ValueError(f"k3mla: {what} has {t.shape[2]} channels, not {d}")
+    return _View(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _i32(t, what, shape):
+    """A contiguous int32 CUDA tensor of the given shape, or None; its address."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise ValueError(f"k3mla: {what} must be a contiguous int32 CUDA tensor of shape {shape}")
+    return t.data_ptr()
+
+
+def _empty(shape, dtype, device, stream):
+    """An output: torch's allocator is told of the stream that writes it when that is not the current one."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+class RopeTable:
+    """The rotation's table: phases [dim/2] on the device (kept alive here), the rotated channels
+    [offset, offset + dim), their pair layout ("half" or "interleaved") and the factor mscale."""
+
+    def __init__(self, phase, dim, offset, layout, mscale):
+        self.phase, self.dim, self.offset, self.layout, self.mscale = phase, dim, offset, layout, mscale
+        self._args = _RopeArgs(phase.data_ptr(), dim, offset, _LAYOUTS[layout], mscale)
+
+
+def k3mla_rope_table(dim, theta, scaling="none", factor=1.0, original_length=0.0, beta_fast=32.0, beta_slow=1.0):
+    """(phases as a CPU int64 tensor of the 64-bit patterns, mscale); see include/k3kda.h."""
+    lib = load_library()
+    phase = torch.zeros(max(int(dim) // 2, 1), dtype=torch.int64)
+    mscale = ctypes.c_float(1.0)
+    st = lib.k3mla_rope_table(int(dim), float(theta), _SCALINGS[scaling], float(factor), float(original_length),
+                              float(beta_fast), float(beta_slow), phase.data_ptr(), ctypes.byref(mscale))
+    _check("k3mla_rope_table", st)
+    return phase, mscale.value
+
+
+def rope_table(dim, theta=10000.0, offset=0, layout="half", scaling="none", factor=1.0, original_length=0.0,
+               beta_fast=32.0, beta_slow=1.0, device="cuda") -> RopeTable:
+    """A rotation table for `dim` channels from `offset` on; scaling is "none", "linear", "ntk" or "by_parts"."""
+    phase, mscale = k3mla_rope_table(dim, theta, scaling, factor, original_length, beta_fast, beta_slow)
+    return RopeTable(phase.to(device), int(dim), int(offset), layout, mscale)
+
+
+def _rope_views(x, y, what):
+    if x is None:
+        return None, None, 0
+    if y.dtype != x.dtype or y.shape[0] != x.shape[0] or y.device != x.device:
+        raise ValueError(f"k3mla: {what} and its output differ in type, tokens or device")
+    return _view(x, what), _view(y, what, x.shape[2]), x.shape[1]
+
+
+def k3mla_rope(q, q_out, k, k_out, positions, table, stream=None):
+    """Rotate q [T, Hq, d] -> q_out and k [T, Hk, d] -> k_out (None: no k); an output may be its input."""
+    if k is not None and (k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2] or k.dtype != q.dtype):
+        raise ValueError("k3mla: q and k differ in tokens, channels or type")
+    if tuple(q_out.shape) != tuple(q.shape) or (k is not None and tuple(k_out.shape) != tuple(k.shape)):
+        raise ValueError("k3mla: an output has another shape than its input")
+    qv, qo, hq = _rope_views(q, q_out, "q")
+    kv, ko, hk = _rope_views(k, k_out, "k")
+    st = load_library().k3mla_rope(qv, qo, hq, kv, ko, hk, _dtype(q), _i32(positions, "positions", (q.shape[0],)),
+                                   q.shape[0], q.shape[2], table._args, _stream(stream))
+    _check("k3mla_rope", st)
+
+
+def k3mla_rope_backward(dq_out, dq, dk_out, dk, k_shared, positions, table, stream=None):
+    """The gradient of k3mla_rope; k_shared: k was one head for all, dk [T, 1, d] is the sum over heads."""
+    if dk_out is not None and (dk_out.shape[0] != dq_out.shape[0] or dk_out.shape[2] != dq_out.shape[2]
+                               or dk_out.dtype != dq_out.dtype):
+        raise ValueError("k3mla: dq_out and dk_out differ in tokens, channels or type")
+    if tuple(dq.shape) != tuple(dq_out.shape):
+        raise ValueError("k3mla: dq has another shape than dq_out")
+    if dk_out is not None and dk.shape[1] != (1 if k_shared else dk_out.shape[1]):
+        raise ValueError("k3mla: dk has the wrong number of heads")
+    qv, qo, hq = _rope_views(dq_out, dq, "dq_out")
+    kv, ko, hk = _rope_views(dk_out, dk, "dk_out")
+    st = load_library().k3mla_rope_backward(qv, qo, hq, kv, ko, hk, int(bool(k_shared)), _dtype(dq_out),
+                                            _i32(positions, "positions", (dq_out.shape[0],)), dq_out.shape[0],
+                                            dq_out.shape[2], table._args, _stream(stream))
+    _check("k3mla_rope_backward", st)
+
+
+def rope(q, positions, table, k=None, out=None, stream=None):
+    """q [T, Hq, d] (and k [T, Hk, d]) turned by positions int32 [T].  Returns q's rotation, or (q's, k's);
+    `out` (a tensor, or a pair with k) may be the inputs themselves.  Inputs may be strided views."""
+    if out is None:
+        out = _empty(q.shape, q.dtype, q.device, stream)
+        out = out if k is None else (out, _empty(k.shape, k.dtype, k.device, stream))
+    qo, ko = (out, None) if k is None else out
+    k3mla_rope(q, qo, k, ko, positions, table, stream)
+    return out
+
+
+def rope_backward(dq_out, positions, table, dk_out=None, k_shared=False, stream=None):
+    """Gradients of rope's inputs: dq, or (dq, dk); with k_shared dk is [T, 1, d], the sum over heads."""
+    dq = _empty(dq_out.shape, dq_out.dtype, dq_out.device, stream)
+    dk = None
+    if dk_out is not None:
+        dk = _empty((dk_out.shape[0], 1 if k_shared else dk_out.shape[1], dk_out.shape[2]), dk_out.dtype, dk_out.device, stream)
+    k3mla_rope_backward(dq_out, dq, dk_out, dk, k_shared, positions, table, stream)
+    return dq if dk is None else (dq, dk)
+
+
+def k3mla_paged_block_bytes(fmt, page_size, dqk, dv) -> int:
+    return int(load_library().k3mla_paged_block_bytes(_FORMATS.get(fmt, fmt), int(page_size), int(dqk), int(dv)))
+
+
+def paged_pool(num_pages, page_size, heads, dqk, dv, fmt="i4", device="cuda"):
+    """An empty pool: uint8 [num_pages, heads, block bytes]."""
+    n = k3mla_paged_block_bytes(fmt, page_size, dqk, dv)
+    if n == 0:
+        raise K3KDAError("k3mla_paged_block_bytes", -2)
+    return torch.zeros((num_pages, heads, n), dtype=torch.uint8, device=device)
+
+
+class PagedCache:
+    """A paged key/value cache as the calls take it: pool uint8 [num_pages, heads, block bytes], block_table
+    int32 [N, max_pages] and kv_len int32 [N] (lengths with the call's new tokens) on the device.  The tensors stay
+    the caller's: write to them in place (kv_len.add_(1)) between calls.  block_table_host and
+    kv_len_host: optional CPU copies that every call then checks."""
+
+    def __init__(self, pool, block_table, kv_len, page_size, dqk, dv, fmt="i4", block_table_host=None, kv_len_host=None):
+        if pool.dim() != 3 or pool.dtype != torch.uint8 or not pool.is_contiguous() or not pool.is_cuda:
+            raise ValueError("k3mla: pool must be a contiguous uint8 CUDA tensor [num_pages, heads, block bytes]")
+        block = k3mla_paged_block_bytes(fmt, page_size, dqk, dv)
+        if block == 0:
+            raise K3KDAError("k3mla_paged_block_bytes", -2, f"(format {fmt}, page_size {page_size}, dqk {dqk}, dv {dv})")
+        if pool.shape[2] != block:
+            raise ValueError(f"k3mla: a block has {block} bytes, the pool's have {pool.shape[2]}")
+        N, width = block_table.shape
+        tab, lens = _i32(block_table, "block_table", (N, width)), _i32(kv_len, "kv_len", (N,))
+        if tuple(getattr(block_table_host, "shape", (N, width))) != (N, width) or tuple(getattr(kv_len_host, "shape", (N,))) != (N,):
+            raise ValueError("k3mla: a host copy has another shape")
+        self.pool, self.block_table, self.kv_len = pool, block_table, kv_len
+        self.block_table_host, self.kv_len_host = block_table_host, kv_len_host
+        self.N, self.heads, self.page_size, self.dqk, self.dv, self.fmt = N, pool.shape[1], page_size, dqk, dv, fmt
+        self._args = _PagedArgs(pool.data_ptr(), tab, lens, _host_i32(block_table_host, "block_table_host"),
+                                _host_i32(kv_len_host, "kv_len_host"), _FORMATS.get(fmt, fmt), pool.shape[0], page_size, width, N,
+                                pool.shape[1], dqk, dv)
+
+
+def _packing(cache, cu_seqlens, cu_seqlens_host):
+    if cu_seqlens_host is not None and cu_seqlens_host.numel() != cache.N + 1:
+        raise ValueError("k3mla: cu_seqlens_host has another length")
+    return _i32(cu_seqlens, "cu_seqlens", (cache.N + 1,)), _host_i32(cu_seqlens_host, "cu_seqlens_host")
+
+
+def k3mla_paged_append(cache, k_new, v_new, cu_seqlens=None, cu_seqlens_host=None, rope=None, stream=None):
+    """Append rows k_new [T, heads, dqk], v_new [T, heads, dv] (see include/k3kda.h); rope: a RopeTable or None."""
+    if k_new.shape[:2] != v_new.shape[:2] or k_new.shape[1] != cache.heads or k_new.dtype != v_new.dtype:
+        raise ValueError("k3mla: k_new and v_new differ, or have other heads than the cache")
+    cu, cuh = _packing(cache, cu_seqlens, cu_seqlens_host)
+    st = load_library().k3mla_paged_append(cache._args, _view(k_new, "k_new", cache.dqk), _view(v_new, "v_new", cache.dv),
+                                           _dtype(k_new), cu, cuh, k_new.shape[0], None if rope is None else rope._args,
+                                           _stream(stream))
+    _check("k3mla_paged_append", st)
+
+
+def k3mla_paged_read(cache, k_out, v_out, cu_seqlens=None, cu_seqlens_host=None, stream=None):
+    """The last tokens' rows as values to k_out [T, heads, dqk] and v_out [T, heads, dv] (either may be None)."""
+    some = k_out if k_out is not None else v_out
+    if some is None or (k_out is not None and v_out is not None and (k_out.shape[:2] != v_out.shape[:2] or k_out.dtype != v_out.dtype)):
+        raise ValueError("k3mla: k_out and v_out differ, or both are None")
+    if some.shape[1] != cache.heads:
+        raise ValueError("k3mla: the outputs have other heads than the cache")
+    cu, cuh = _packing(cache, cu_seqlens, cu_seqlens_host)
+    st = load_library().k3mla_paged_read(cache._args, None if k_out is None else _view(k_out, "k_out", cache.dqk),
+                                         None if v_out is None else _view(v_out, "v_out", cache.dv), _dtype(some), cu, cuh,
+                                         some.shape[0], _stream(stream))
+    _check("k3mla_paged_read", st)
+
+
+paged_append = k3mla_paged_append
+
+
+def paged_read(cache, tokens, cu_seqlens=None, out_dtype=torch.bfloat16, stream=None):
+    """The last `tokens` packed rows (all sequences together) as values: (k [tokens, heads, dqk], v [tokens, heads, dv])."""
+    k = _empty((tokens, cache.heads, cache.dqk), out_dtype, cache.pool.device, stream)
+    v = _empty((tokens, cache.heads, cache.dv), out_dtype, cache.pool.device, stream)
+    k3mla_paged_read(cache, k, v, cu_seqlens, None, stream)
+    return k, v

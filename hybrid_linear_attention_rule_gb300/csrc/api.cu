@@ -69,6 +69,8 @@ size_t conv_buffer_bytes(int T, int H, int dk, int dv) {
 
 }  // namespace
 
+int k3kda::status_of(cudaError_t e) { return cuda_status(e); }
+
 void k3kda::count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
 namespace {

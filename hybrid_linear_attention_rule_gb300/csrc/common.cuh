@@ -67,6 +67,9 @@ inline cudaError_t smem_attr_once(const void *func, int bytes, std::atomic<uint6
     return e;
 }
 
+// K3KDA_OK, or K3KDA_ERR_CUDA with the error's text kept for k3kda_last_error.
+int status_of(cudaError_t e);
+
 // Counts every kernel this library launches (reported by k3kda_launch_count).
 void count_launch();
 
@@ -143,4 +146,13 @@ cudaError_t launch_mla_decode(const void *q, const void *k_new, const void *v_ne
                               int dv, int L_max, int rope_dim, float theta, float scale, void *out, int out_bf16,
                               void *ws, cudaStream_t st, const int32_t *slot = nullptr, int num_slots = 0);
 
+// rotary positions (csrc/rope.cu): sgn +1 forward, -1 gradient; shared: k_out is one head, the sum over Hk
+cudaError_t launch_rope(const k3mla_view *q, const k3mla_view *q_out, int Hq, const k3mla_view *k, const k3mla_view *k_out,
+                        int Hk, int shared, int bf16, const int32_t *pos, int T, int d, const k3mla_rope_args *rope,
+                        float sgn, cudaStream_t s);
+// the paged cache (csrc/paged_append.cu)
+cudaError_t launch_paged_append(const k3mla_paged_cache *c, const k3mla_view *k, const k3mla_view *v, int bf16, const int32_t *cu,
+                                int T, const k3mla_rope_args *rope, cudaStream_t s);
+cudaError_t launch_paged_read(const k3mla_paged_cache *c, const k3mla_view *k, const k3mla_view *v, int bf16, const int32_t *cu,
+                              int T, cudaStream_t s);
 }  // namespace k3kda

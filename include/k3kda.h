@@ -394,6 +394,128 @@ int k3mla_decode_step_slots(const void *q, const void *k_new, const void *v_new,
                             int N, int H, int dqk, int dv, int L_max, int rope_dim, float rope_theta, float scale,
                             void *out, int out_dtype, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- Rotary positions ------------------------------------------------------------------------
+ * The attention layers' position rotation by itself, for training and prompts: forward, gradient,
+ * both pair layouts, any contiguous part of the head, frequencies scaled for long contexts.  For a
+ * token at position p, pair i of `dim` rotated channels is turned by the angle p f_i:
+ *     (x, y) -> mscale (x cos - y sin, y cos + x sin)
+ * HALF pairs channels (offset + i, offset + i + dim/2), INTERLEAVED (offset + 2i, offset + 2i + 1);
+ * the channels outside [offset, offset + dim) pass through.  The rotation runs in FP32 and is
+ * rounded once, to the output's type.
+ *
+ * Frequencies: f_i = theta^(-2i/dim), scaled by one of
+ *     NONE      f_i as it is
+ *     LINEAR    f_i / factor
+ *     NTK       theta replaced by theta * factor^(dim/(dim-2))            (dim > 2)
+ *     BY_PARTS  with r = original_length f_i / 2 pi turns over the original context and
+ *               g = clamp((r - beta_slow) / (beta_fast - beta_slow), 0, 1):
+ *               f_i g + (f_i / factor) (1 - g); mscale = 0.1 ln(factor) + 1  (else mscale = 1)
+ * They are held as phases: the turns per position f_i / 2 pi in units of 2^-64, so that the turn of
+ * a position is one 64-bit product modulo 2^64 and keeps its accuracy at any int32 position
+ * (negative ones turn backwards).  k3mla_rope_table computes the dim/2 phases on the host; the
+ * caller keeps a copy in device memory for as long as its kernels run. */
+typedef enum { K3MLA_ROPE_HALF = 0, K3MLA_ROPE_INTERLEAVED = 1 } k3mla_rope_layout;
+typedef enum {
+    K3MLA_SCALE_NONE = 0, K3MLA_SCALE_LINEAR = 1, K3MLA_SCALE_NTK = 2, K3MLA_SCALE_BY_PARTS = 3
+} k3mla_rope_scale_kind;
+
+typedef struct k3mla_rope_args {
+    const uint64_t *phase;   /* [dim/2] device, 8-byte aligned                      */
+    int dim;                 /* rotated channels: even, 0 (none) to 512             */
+    int offset;              /* first of them                                       */
+    int layout;              /* k3mla_rope_layout                                   */
+    float mscale;            /* factor on the rotated channels                      */
+} k3mla_rope_args;
+
+/* A [tokens, heads, channels] array whose channels are contiguous and whose tokens and heads lie
+ * the given numbers of elements apart (slices of a fused projection; a head stride of 0 in an input
+ * is one head shared by all).  Aligned to its element type; arrays whose address and strides are
+ * multiples of 16 bytes are moved in 16-byte pieces. */
+typedef struct k3mla_view {
+    void *data;
+    long long token_stride, head_stride;
+} k3mla_view;
+
+/* Fill phase_host [dim/2] and *mscale (host memory).  Errors: INVALID_ARG for an odd dim or one
+ * outside 2..512, theta or factor not positive and finite, BY_PARTS without original_length > 0 and
+ * beta_fast > beta_slow, NTK with dim = 2, an unknown kind. */
+int k3mla_rope_table(int dim, double theta, int scale_kind, double factor, double original_length,
+                     double beta_fast, double beta_slow, uint64_t *phase_host, float *mscale);
+
+/* q [T, Hq, d] -> q_out, and k [T, Hk, d] -> k_out when k is given (k = k_out = NULL, Hk = 0: none),
+ * all of type dtype, turned by positions [T] (int32, device).  An output may be its input (then only
+ * the rotated channels are touched), else they may not overlap; output strides may not be 0 where
+ * there is more than one head or token.  One launch on `stream`.
+ * Errors: INVALID_ARG, UNSUPPORTED (d outside 1..1024), ALIGNMENT, CUDA.  T = 0 launches nothing. */
+int k3mla_rope(const k3mla_view *q, const k3mla_view *q_out, int Hq, const k3mla_view *k,
+               const k3mla_view *k_out, int Hk, int dtype, const int32_t *positions, int T, int d,
+               const k3mla_rope_args *rope, void *stream);
+
+/* The gradient: dq_out = dL/dq_out [T, Hq, d] -> dq, dk_out -> dk, each pair turned back by its angle
+ * (and times mscale), the other channels passed through.  With k_shared nonzero the forward's k was
+ * one head that every one of the Hk heads shared (head stride 0): dk is [T, 1, d], the sum over the
+ * heads, taken in FP32 before its one rounding, in an order that does not change from run to run
+ * (dk may then not be dk_out).  Arguments and errors otherwise as k3mla_rope. */
+int k3mla_rope_backward(const k3mla_view *dq_out, const k3mla_view *dq, int Hq, const k3mla_view *dk_out,
+                        const k3mla_view *dk, int Hk, int k_shared, int dtype, const int32_t *positions,
+                        int T, int d, const k3mla_rope_args *rope, void *stream);
+
+/* ---- A paged key/value cache, in bf16 or in 4 bits -------------------------------------------
+ * The attention layers' cache as pages of page_size tokens that sequences share out of one pool:
+ * page j of sequence n is block_table[n, j], its token p lies in page p / page_size.  Two calls use
+ * it: append (new rows, keys rotated on the way) and read (rows back as the values they stand for).
+ * Neither changes kv_len or block_table, which are the caller's: kv_len[n] is the
+ * sequence's length with the call's new tokens, so that a step's append and attend take the same
+ * array and the caller advances it once a step.
+ *
+ * Pool: [num_pages, heads] blocks of k3mla_paged_block_bytes, 16-byte aligned.  A block is page_size
+ * / 16 strips of 16 tokens; a strip is (dqk + dv) / 64 planes, the key's channels first; a plane
+ * holds 64 channels of 16 tokens:
+ *   K3MLA_CACHE_BF16  2048 bytes: 16 rows of 64 bf16 values, the 16-byte piece c of row r at piece
+ *                     c ^ (r & 7) (so that eight rows' pieces lie in different banks)
+ *   K3MLA_CACHE_I4    576 bytes: 16 rows of 32 bytes (channel 2i in the low half of byte i, 2i + 1 in
+ *                     the high half), then 16 pairs of fp16 (scale s, minimum m).  A group of 64
+ *                     channels x of a token is held as m = fp16(min x), s = fp16(max(max x - m, 0)/15),
+ *                     both kept within +-65504, codes clamp(rint((x - m) / s), 0, 15) (0 where s = 0),
+ *                     and stands for s code + m; every rounding to nearest, ties to even, of the exact
+ *                     value (the kernel settles cases that FP32 cannot tell in double).  A group
+ *                     with an infinity or a NaN has s = m = NaN.
+ * Data errors are reported in the data, as in k3mla_decode_step: a page number outside
+ * [0, num_pages), a length outside [0, max_pages * page_size] or a position below 0 is never
+ * dereferenced; append leaves such a token out, read and attend give NaN for it (attend for
+ * every row of the sequence that sees it). */
+typedef enum { K3MLA_CACHE_BF16 = 1, K3MLA_CACHE_I4 = 2 } k3mla_cache_format;
+
+typedef struct k3mla_paged_cache {
+    void *pool;                        /* [num_pages, heads] blocks                           */
+    const int32_t *block_table;        /* [N, max_pages] device                               */
+    const int32_t *kv_len;             /* [N] device: tokens with the call's new ones         */
+    const int32_t *block_table_host;   /* optional host copies: every page that kv_len reaches */
+    const int32_t *kv_len_host;        /* and every length is checked, INVALID_ARG if outside */
+    int format;                        /* k3mla_cache_format                                  */
+    int num_pages, page_size;          /* page_size: a multiple of 16, 16..256                */
+    int max_pages;                     /* columns of block_table                              */
+    int N, heads, dqk, dv;             /* dqk in {64, 128, 192, 256}, dv in {64, 128, 256}    */
+} k3mla_paged_cache;
+
+/* Bytes of one (page, head) block; 0 for unsupported arguments. */
+size_t k3mla_paged_block_bytes(int format, int page_size, int dqk, int dv);
+
+/* Append T packed new tokens: sequence n's are rows cu_seqlens[n] .. cu_seqlens[n+1]-1 of k_new
+ * [T, heads, dqk] and v_new [T, heads, dv] (in_dtype) and go to positions kv_len[n] - count .. kv_len[n]-1.
+ * cu_seqlens [N+1] (int32, device; cu_seqlens_host an optional host copy, checked) or NULL: one token for each
+ * sequence, T = N.  rope (or NULL): keys are rotated by their positions before they are stored.  Two sequences may share pages that neither appends to.
+ * One launch on `stream`.  Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, CUDA.  T = 0 launches nothing. */
+int k3mla_paged_append(const k3mla_paged_cache *cache, const k3mla_view *k_new, const k3mla_view *v_new, int in_dtype,
+                       const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int T, const k3mla_rope_args *rope,
+                       void *stream);
+
+/* The inverse: the last cu_seqlens[n+1]-cu_seqlens[n] tokens of every sequence, as the values the
+ * cache stands for (keys as stored, rotated), to k_out [T, heads, dqk] and v_out [T, heads, dv] in out_dtype
+ * (either may be NULL). */
+int k3mla_paged_read(const k3mla_paged_cache *cache, const k3mla_view *k_out, const k3mla_view *v_out, int out_dtype,
+                     const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int T, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
