@@ -28,9 +28,9 @@ __all__ = ["K3KDAError", "load_library", "library_path", "F32", "BF16", "L2_EPS"
            "k3kda_decode_step", "prefill", "decode_step", "short_conv",
            "k3mla_decode_workspace_size", "k3mla_decode_step", "k3mla_decode_step_slots", "mla_decode_step",
            "CACHE_BF16", "CACHE_I4", "RopeTable", "PagedCache", "rope_table", "rope", "rope_backward",
-           "paged_pool", "paged_append", "paged_read",
+           "paged_pool", "paged_append", "paged_read", "paged_attend", "paged_attend_workspace",
            "k3mla_rope_table", "k3mla_rope", "k3mla_rope_backward", "k3mla_paged_block_bytes",
-           "k3mla_paged_append", "k3mla_paged_read"]
+           "k3mla_paged_append", "k3mla_paged_read", "k3mla_paged_attend_workspace_size", "k3mla_paged_attend"]
 
 F32, BF16 = 0, 1
 CACHE_BF16, CACHE_I4 = 1, 2
@@ -127,6 +127,10 @@ def load_library(build_if_missing: bool = True):
         lib.k3mla_paged_append.restype = I
         lib.k3mla_paged_read.argtypes = [C, V, V, I, P, P, I, P]
         lib.k3mla_paged_read.restype = I
+        lib.k3mla_paged_attend_workspace_size.argtypes = [I, I, I, I]
+        lib.k3mla_paged_attend_workspace_size.restype = Z
+        lib.k3mla_paged_attend.argtypes = [C, V, I, I, P, P, I, I, R, F, V, P, I, P, Z, P]
+        lib.k3mla_paged_attend.restype = I
         _lib = lib
         return lib
 
@@ -660,3 +664,48 @@ def paged_read(cache, tokens, cu_seqlens=None, out_dtype=torch.bfloat16, stream=
     v = _empty((tokens, cache.heads, cache.dv), out_dtype, cache.pool.device, stream)
     k3mla_paged_read(cache, k, v, cu_seqlens, None, stream)
     return k, v
+
+
+def k3mla_paged_attend_workspace_size(Hq, heads, dqk, dv) -> int:
+    return int(load_library().k3mla_paged_attend_workspace_size(int(Hq), int(heads), int(dqk), int(dv)))
+
+
+def paged_attend_workspace(cache, Hq):
+    """A zero-filled workspace for k3mla_paged_attend on this cache, for one call at a time; any later call may reuse it."""
+    n = k3mla_paged_attend_workspace_size(Hq, cache.heads, cache.dqk, cache.dv)
+    return torch.zeros(n, dtype=torch.uint8, device=cache.pool.device)
+
+
+def k3mla_paged_attend(cache, q, gate, out, workspace, scale, cu_seqlens=None, cu_seqlens_host=None, max_new=1, rope=None,
+                       stream=None):
+    """Attention of the new tokens q [T, Hq, dqk] over the cache (see include/k3kda.h)."""
+    T, Hq = q.shape[:2]
+    if gate is not None and (tuple(gate.shape) != (T, Hq, cache.dv) or gate.dtype != q.dtype):
+        raise ValueError("k3mla: gate is not [tokens, query heads, dv] of q's type")
+    if tuple(out.shape) != (T, Hq, cache.dv):
+        raise ValueError("k3mla: out is not [tokens, query heads, dv]")
+    cu, cuh = _packing(cache, cu_seqlens, cu_seqlens_host)
+    st = load_library().k3mla_paged_attend(cache._args, _view(q, "q", cache.dqk), _dtype(q), Hq, cu, cuh, T, int(max_new),
+                                           None if rope is None else rope._args, scale,
+                                           None if gate is None else _view(gate, "gate"), _ptr(out), _dtype(out),
+                                           _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("k3mla_paged_attend", st)
+
+
+def paged_attend(cache, q, cu_seqlens=None, max_new=None, rope=None, scale=None, gate=None, out=None, out_dtype=None,
+                 workspace=None, stream=None):
+    """Attention of the T packed new tokens q [T, Hq, dqk] over the cache, which holds them already (append first).
+    max_new: at least the most new tokens of a sequence (default: T; 1 without cu_seqlens); scale
+    defaults to dqk^-1/2.  Returns out [T, Hq, dv]."""
+    if out is None:
+        out = _empty((q.shape[0], q.shape[1], cache.dv), out_dtype or q.dtype, q.device, stream)
+    if workspace is None:
+        workspace = paged_attend_workspace(cache, q.shape[1])
+        if stream is not None:                          # zeroed on the current stream, used on this one
+            stream.wait_stream(torch.cuda.current_stream())
+            workspace.record_stream(stream)
+    if max_new is None:
+        max_new = 1 if cu_seqlens is None else max(1, q.shape[0])
+    k3mla_paged_attend(cache, q, gate, out, workspace, cache.dqk ** -0.5 if scale is None else float(scale), cu_seqlens, None, max_new,
+                       rope, stream)
+    return out

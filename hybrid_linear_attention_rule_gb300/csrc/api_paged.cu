@@ -163,4 +163,31 @@ int k3mla_paged_read(const k3mla_paged_cache *cache, const k3mla_view *k_out, co
     return status_of(launch_paged_read(cache, k_out, v_out, out_dtype == K3KDA_BF16, cu_seqlens, T, static_cast<cudaStream_t>(stream)));
 }
 
+size_t k3mla_paged_attend_workspace_size(int Hq, int heads, int dqk, int dv) {
+    if (heads < 1 || Hq < heads || Hq % heads != 0 || !dims_ok(dqk, dv)) return 0;
+    return paged_attend_workspace(dv);
+}
+
+int k3mla_paged_attend(const k3mla_paged_cache *cache, const k3mla_view *q, int in_dtype, int Hq, const int32_t *cu_seqlens,
+                       const int32_t *cu_seqlens_host, int T, int max_new, const k3mla_rope_args *rope, float scale,
+                       const k3mla_view *gate, void *out, int out_dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!type_ok(in_dtype) || !type_ok(out_dtype)) return K3KDA_ERR_INVALID_ARG;
+    if (int e = check_cache(cache, cu_seqlens, cu_seqlens_host, T)) return e;
+    if (Hq < 1 || Hq % cache->heads != 0 || max_new < 1 || !isfinite(scale)) return K3KDA_ERR_INVALID_ARG;
+    if (Hq > 65536 || max_new > (1 << 24) || (long long)max_new * (Hq / cache->heads) > (1 << 28)) return K3KDA_ERR_UNSUPPORTED;
+    if (cu_seqlens_host)
+        for (int n = 0; n < cache->N; ++n)
+            if (cu_seqlens_host[n + 1] - cu_seqlens_host[n] > max_new) return K3KDA_ERR_INVALID_ARG;
+    if (int e = check_rope(rope, cache->dqk)) return e;
+    if (T == 0) return K3KDA_OK;
+    if (int e = check_view(q, in_dtype, T, Hq, false)) return e;
+    if (gate)
+        if (int e = check_view(gate, in_dtype, T, Hq, false)) return e;
+    if (!out) return K3KDA_ERR_INVALID_ARG;
+    if (!aligned(out, 16)) return K3KDA_ERR_ALIGNMENT;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < paged_attend_workspace(cache->dv)) return K3KDA_ERR_WORKSPACE;
+    return status_of(launch_paged_attend(cache, q, in_dtype == K3KDA_BF16, Hq, cu_seqlens, T, max_new, rope, scale, gate, out,
+                                         out_dtype == K3KDA_BF16, workspace, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

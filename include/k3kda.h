@@ -462,9 +462,9 @@ int k3mla_rope_backward(const k3mla_view *dq_out, const k3mla_view *dq, int Hq, 
 
 /* ---- A paged key/value cache, in bf16 or in 4 bits -------------------------------------------
  * The attention layers' cache as pages of page_size tokens that sequences share out of one pool:
- * page j of sequence n is block_table[n, j], its token p lies in page p / page_size.  Two calls use
- * it: append (new rows, keys rotated on the way) and read (rows back as the values they stand for).
- * Neither changes kv_len or block_table, which are the caller's: kv_len[n] is the
+ * page j of sequence n is block_table[n, j], its token p lies in page p / page_size.  Three calls use
+ * it: append (new rows, keys rotated on the way), read (rows back as the values they stand for) and
+ * attend.  None of them changes kv_len or block_table, which are the caller's: kv_len[n] is the
  * sequence's length with the call's new tokens, so that a step's append and attend take the same
  * array and the caller advances it once a step.
  *
@@ -515,6 +515,25 @@ int k3mla_paged_append(const k3mla_paged_cache *cache, const k3mla_view *k_new, 
  * (either may be NULL). */
 int k3mla_paged_read(const k3mla_paged_cache *cache, const k3mla_view *k_out, const k3mla_view *v_out, int out_dtype,
                      const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int T, void *stream);
+
+/* Attention of T packed new tokens over the cache, which holds them already (append first):
+ * token i of sequence n's c tokens sits at position p = kv_len[n] - c + i and sees keys 0..p;
+ * query head h reads key head h / (Hq / heads):
+ *     out = softmax_j(scale rope(q, p) . k_j) . v  (* sigmoid(gate) when gate is given)
+ * q [T, Hq, dqk], gate [T, Hq, dv] views of in_dtype, out [T, Hq, dv] dense, of out_dtype; cu_seqlens as for append;
+ * max_new: at least the largest number of new tokens of a sequence (1 with cu_seqlens NULL).  A row that sees
+ * no key (p < 0, an empty sequence) is 0.  Query rows, weights and sums keep FP32 accuracy (operands
+ * split in two where a tensor core takes them in 16 bits).  Results do not depend on the order in which
+ * parts of the work finish.
+ * workspace: k3mla_paged_attend_workspace_size bytes, 256-byte aligned, zero-filled before its first use, owned by
+ * one call at a time (calls of any shape may follow one another); its first word is the status word of
+ * k3kda_workspace_status: after a TIMEOUT zero-fill it again.  One launch on `stream`.
+ * Errors: INVALID_ARG (Hq not a multiple of heads), UNSUPPORTED, ALIGNMENT, WORKSPACE, CUDA. */
+size_t k3mla_paged_attend_workspace_size(int Hq, int heads, int dqk, int dv);
+int k3mla_paged_attend(const k3mla_paged_cache *cache, const k3mla_view *q, int in_dtype, int Hq,
+                       const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int T, int max_new,
+                       const k3mla_rope_args *rope, float scale, const k3mla_view *gate, void *out, int out_dtype,
+                       void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -119,3 +119,14 @@ def attend(q, k, v, seen, scale, gate=None):
                 p = np.exp(s - s.max())
                 out[i, h] = (p @ v[:n, h // G]) / p.sum()
         return out if gate is None else out / (1.0 + np.exp(-gate))
+
+
+def strips_bf16(rows):
+    """Rows [heads, page, d] that bf16 holds -> blocks' bytes [heads, block]."""
+    H, P, d = rows.shape
+    w = (np.ascontiguousarray(rows, np.float32).view(np.uint32) >> 16).astype(np.uint16).reshape(H, P // 16, 16, d // 64, 8, 8)
+    out = np.empty_like(w)
+    for r in range(16):
+        for c in range(8):
+            out[:, :, r, :, c ^ (r & 7)] = w[:, :, r, :, c]
+    return np.ascontiguousarray(out.transpose(0, 1, 3, 2, 4, 5)).view(np.uint8).reshape(H, -1)

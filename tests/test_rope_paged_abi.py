@@ -192,3 +192,33 @@ def test_plain_forms_agree_with_each_other():
     step = (rows.reshape(2, 32, 2, 64).max(-1) - rows.reshape(2, 32, 2, 64).min(-1)) / 15
     # half a step of the code, and fp16's rounding of the scale (15 of it) and the minimum (2^-11 of each)
     assert (np.abs(v - rows).reshape(2, 32, 2, 64).max(-1) <= 0.5 * step + 15 * step * 2.0 ** -11 + 4 * 2.0 ** -11).all()
+
+
+def _attend(lib, q=_v(), dtype=1, Hq=4, cu=A16, cu_h=None, T=3, max_new=2, rope=None, scale=1.0, gate=None, out=A16, out_dtype=0,
+            ws=0x10000, ws_bytes=1 << 30, **kw):
+    return lib.k3mla_paged_attend(_cache(**kw), q, dtype, Hq, cu, cu_h, T, max_new, rope, scale, gate, out, out_dtype, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,want", [b for b in BAD_CACHES if "v" not in b[0] and "k" not in b[0]], ids=str)
+def test_attend_refuses_bad_caches(lib, kw, want):
+    assert _attend(lib, **kw) == want
+
+
+def test_attend_refusals(lib):
+    assert _attend(lib, T=0) == 0
+    assert _attend(lib, Hq=3) == -1 and _attend(lib, Hq=0) == -1       # not a multiple of the key heads
+    assert _attend(lib, heads=1, Hq=1 << 17) == -2
+    assert _attend(lib, max_new=0) == -1 and _attend(lib, max_new=1 << 25) == -2
+    assert _attend(lib, scale=float("nan")) == -1
+    assert _attend(lib, out_dtype=3) == -1
+    assert _attend(lib, q=None) == -1 and _attend(lib, q=_v(MIS1)) == -3
+    assert _attend(lib, gate=_v(MIS1)) == -3 and _attend(lib, gate=_v(None)) == -1
+    assert _attend(lib, out=None) == -1 and _attend(lib, out=MIS4) == -3
+    assert _attend(lib, ws=None) == -4 and _attend(lib, ws=0x10010) == -4
+    assert _attend(lib, rope=K._RopeArgs(A16, 64, 96, 0, 1.0)) == -1
+    assert _attend(lib, max_new=1, cu_h=_adr(_host(0, 1, 3))) == -1    # a sequence has more than max_new
+    need = K.k3mla_paged_attend_workspace_size(4, 2, 128, 128)
+    assert _attend(lib, ws_bytes=need - 1) == -4
+    assert need % 16 == 0 and need > 0
+    for bad in ((3, 2, 128, 128), (4, 0, 128, 128), (4, 2, 100, 128), (4, 2, 128, 192)):
+        assert K.k3mla_paged_attend_workspace_size(*bad) == 0
