@@ -174,10 +174,13 @@ int k3mla_paged_attend(const k3mla_paged_cache *cache, const k3mla_view *q, int 
     if (!type_ok(in_dtype) || !type_ok(out_dtype)) return K3KDA_ERR_INVALID_ARG;
     if (int e = check_cache(cache, cu_seqlens, cu_seqlens_host, T)) return e;
     if (Hq < 1 || Hq % cache->heads != 0 || max_new < 1 || !isfinite(scale)) return K3KDA_ERR_INVALID_ARG;
-    if (Hq > 65536 || max_new > (1 << 24) || (long long)max_new * (Hq / cache->heads) > (1 << 28)) return K3KDA_ERR_UNSUPPORTED;
+    if (Hq > 65536 || max_new > (1 << 24) || (long long)T * (Hq / cache->heads) > (1 << 28)) return K3KDA_ERR_UNSUPPORTED;
     if (cu_seqlens_host)
         for (int n = 0; n < cache->N; ++n)
             if (cu_seqlens_host[n + 1] - cu_seqlens_host[n] > max_new) return K3KDA_ERR_INVALID_ARG;
+    // the kernel counts its units (16-token strips at the finest, and a few more for each head and 4-row block) in 31 bits
+    if (((double)T * (Hq / cache->heads) / 4 + cache->N) * cache->heads * ((double)cache->max_pages * cache->page_size / 16 + 4) > 2e9)
+        return K3KDA_ERR_UNSUPPORTED;
     if (int e = check_rope(rope, cache->dqk)) return e;
     if (T == 0) return K3KDA_OK;
     if (int e = check_view(q, in_dtype, T, Hq, false)) return e;

@@ -19,6 +19,8 @@ cudaError_t launch_paged_attend(const k3mla_paged_cache *c, const k3mla_view *q,
     A.cu = cu;
     A.r = make_rope(rope);
     A.qmul = scale * 1.4426950408889634f;
+    A.per_page = c->page_size / kStrip;
+    A.per_page_inv = A.per_page > 1 ? (unsigned)(((1ull << 32) + A.per_page - 1) / A.per_page) : 0;
     A.out = out;
     A.status = static_cast<unsigned *>(ws);
     A.counters = A.status + 64;

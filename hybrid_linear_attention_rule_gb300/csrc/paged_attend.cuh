@@ -21,8 +21,8 @@
 //   bits up; the powers of two go into Q (16 on the first) and into O.  So a group's scale and minimum are taken out
 //   of the product: s = sum_g scale_g (q_g . code_g) + min_g sum(q_g), and likewise scale_g goes into P before its
 //   split and sum_j p_j min_gj is kept in FP32.  S comes out with tokens on rows; movmatrix turns P to the operand.
-//   The running maximum is that of s + log2(scale), which bounds p scale by 2^14: nothing overflows fp16
-//   and what is far below it keeps 2^-38 of the largest weight.
+//   The running maximum is that of a tile's s plus the exponent of its largest scale less 14, which bounds p scale by
+//   2^14: nothing overflows fp16, and what is far below it keeps 2^-38 of that.
 // A tile's products start at 0 and are added to O in FP32 by fma (which also rescales O): tensor-core sums of
 // few terms, ordinary rounding over the long axis.
 #pragma once
@@ -32,6 +32,14 @@
 
 namespace k3kda {
 namespace attend {
+#ifndef XNS
+#define XNS 4
+#define XW 8
+#define XSS 4
+#endif
+#ifndef XEX
+#define XEX 2
+#endif
 
 constexpr int kMaxCtas = 608;                          // partials and counters of a workspace
 constexpr size_t kHeadBytes = 256 + 4096;              // status word, counters (4 B a CTA)
@@ -46,6 +54,8 @@ struct Args {
     const int32_t *cu;
     Rope r;
     float qmul;                                        // scale * log2(e)
+    int per_page;                                      // strips of a page
+    unsigned per_page_inv;                             // ceil(2^32 / per_page), exact for fewer than 2^28 strips; 0: one strip
     void *out;
     unsigned *status, *counters;
     float *partial;                                    // [kMaxCtas][2] records
@@ -57,44 +67,50 @@ template <int DQK_, int DV_, int RT_, bool I4_> struct Shape {
     static constexpr int PK = DQK / 64, PV = DV / 64, PL = PK + PV;
     static constexpr int ROWS = 4 * RT;
     static constexpr int PLANE = I4 ? kPlaneI4 : kPlaneBf16, STRIP = PL * PLANE;
-    static constexpr int NS = I4 ? (PL <= 2 ? 4 : 2) : (PL <= 2 ? 2 : 1);       // strips of a tile
-    static constexpr int TILE = NS * kStrip, STAGE = NS * STRIP;
-    static constexpr int WARPS = I4 ? (PL <= 4 ? (RT == 1 ? 12 : 8) : RT == 1 ? 8 : 4) : (PL <= 4 ? 6 : 4);
+    static constexpr int NS = I4 ? (PL <= 2 ? 4 : PL <= 4 ? XNS : 2) : (PL <= 2 ? 2 : 1);       // strips of a tile
+    static constexpr int SS = I4 && PL > 2 && PL <= 4 ? XSS : NS, TS = NS / SS;      // strips of a stage, stages of a tile
+    static constexpr int TILE = NS * kStrip, STAGE = SS * STRIP;
+    static constexpr int WARPS = I4 ? (PL <= 4 ? (RT == 1 ? XW : 8) : RT == 1 ? 8 : 4) : (PL <= 4 ? 6 : 4);
+    static constexpr int EXTRA = XEX;                                           // units of a block's start and end, in tiles
     static constexpr int QS = DQK + 8;                                          // floats between staged rows
     static constexpr int RECORD = ROWS * (DV + 2);                              // floats: m, l, O
     static constexpr int STAGED = ROWS * (QS + PK + 1);                         // floats: rows, their sums and exponents
     static constexpr int SLOT1 = RECORD > STAGED ? RECORD : STAGED;
     static constexpr int FIXED = ((RECORD + SLOT1) * 4 + 127) / 128 * 128;      // bytes of a warp beside its ring
-    static constexpr int COMMON = 1024 + 2 * WARPS * 48 + (WARPS * 32 + 2) * 8; // barriers, segments, prefix sums
-    static constexpr int ROOM = (232448 - 256 - COMMON) / WARPS / 128 * 128;
+    static constexpr int COMMON = 1024 + 2 * WARPS * 32 + (WARPS * 32 + 2) * 8; // barriers, segments, prefix sums
+    static constexpr int ROOM = (232448 - 256 - 2 * WARPS * ROWS * 8 - COMMON) / WARPS / 128 * 128;
     static constexpr int FIT = (ROOM - FIXED) / STAGE;
     static constexpr int STAGES = FIT > 6 ? 6 : FIT;
-    static_assert(STAGES >= 2 && STAGES * WARPS * 8 <= 1024 && STAGES * NS <= 32, "ring");
+    static_assert(STAGES >= 2 && STAGES >= TS && STAGES * WARPS * 8 <= 1024 && STAGES * SS <= 32, "ring");
     static constexpr int WARP_BYTES = STAGES * STAGE + FIXED;
     static constexpr int SMEM = COMMON + WARPS * WARP_BYTES;
     static_assert(STAGE % 128 == 0 || (STAGES * STAGE) % 64 == 0, "alignment");
 };
 
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1, bool f16) {
-    if (f16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// c = (FIRST ? 0 : c) + A B
+template <bool F16, bool FIRST> __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    const float x = FIRST ? 0.f : c[0], y = FIRST ? 0.f : c[1], z = FIRST ? 0.f : c[2], w = FIRST ? 0.f : c[3];
+    if constexpr (F16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(x), "f"(y), "f"(z), "f"(w));
     else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(x), "f"(y), "f"(z), "f"(w));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 __device__ __forceinline__ void ldmatrix4(uint32_t (&a)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]) : "r"(addr) : "memory");
+                 : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]) : "r"(addr));
 }
 __device__ __forceinline__ void ldmatrix4t(uint32_t (&a)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]) : "r"(addr) : "memory");
+                 : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]) : "r"(addr));
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -114,6 +130,24 @@ template <bool F16> __device__ __forceinline__ uint32_t split_pair(float x) {
         return *reinterpret_cast<const uint32_t *>(&p);
     }
 }
+// the same of two values
+template <bool F16> __device__ __forceinline__ void split_two(float x, float y, uint32_t &px, uint32_t &py) {
+    uint32_t hi, lo;
+    if constexpr (F16) {
+        const __half2 h = __floats2half2_rn(x, y);
+        const float2 f = __half22float2(h);
+        const __half2 r = __floats2half2_rn(x - f.x, y - f.y);
+        hi = *reinterpret_cast<const uint32_t *>(&h);
+        lo = *reinterpret_cast<const uint32_t *>(&r);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        hi = *reinterpret_cast<const uint32_t *>(&h);
+        const __nv_bfloat162 r = __floats2bfloat162_rn(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+        lo = *reinterpret_cast<const uint32_t *>(&r);
+    }
+    px = __byte_perm(hi, lo, 0x5410);
+    py = __byte_perm(hi, lo, 0x7632);
+}
 // the high (part 0) or low parts of two values
 template <bool F16> __device__ __forceinline__ uint32_t pack_part(float x, float y, int part) {
     const uint32_t a = split_pair<F16>(x), b = split_pair<F16>(y);
@@ -123,7 +157,7 @@ template <bool F16> __device__ __forceinline__ uint32_t pack_part(float x, float
 // one sequence's share of the work
 struct Seq {
     int len, q0, cnt, tiles, rbs;
-    __device__ __forceinline__ int64_t units(int heads) const { return (int64_t)tiles * rbs * heads; }
+    __device__ __forceinline__ unsigned pairs(int heads) const { return (unsigned)rbs * heads; }
 };
 template <class S> __device__ __forceinline__ Seq load_seq(const Args &A, int n) {
     Seq s;
@@ -133,7 +167,7 @@ template <class S> __device__ __forceinline__ Seq load_seq(const Args &A, int n)
     s.q0 = b;
     s.cnt = e - b;
     s.tiles = s.len > 0 ? (s.len + S::TILE - 1) / S::TILE : 1;   // an empty or bad sequence still writes its rows
-    s.rbs = (int)(((int64_t)s.cnt * A.G + S::ROWS - 1) / S::ROWS);
+    s.rbs = (int)(((unsigned)s.cnt * (unsigned)A.G + S::ROWS - 1) / S::ROWS);
     return s;
 }
 
@@ -141,33 +175,34 @@ template <class S> __device__ __forceinline__ Seq load_seq(const Args &A, int n)
 struct Cursor {
     int n, h, rb, t;
     Seq s;
-    // one past the last key that any row of the block sees, and that its first row sees
-    template <class S> __device__ __forceinline__ int seen_most(const Args &A) const {
-        const int last = min(s.cnt - 1, (int)(((int64_t)(rb + 1) * S::ROWS - 1) / A.G));
-        return s.len - s.cnt + last + 1;
-    }
-    template <class S> __device__ __forceinline__ int seen_least(const Args &A) const {
-        return s.len - s.cnt + (int)((int64_t)rb * S::ROWS / A.G) + 1;
+    int most, least;                                   // keys that some row of the block, and that its first row sees
+    template <class S> __device__ __forceinline__ void enter(const Args &A) {
+        const int r = rb * S::ROWS, last = min(s.cnt - 1, (r + S::ROWS - 1) / A.G);   // rows: below 2^28 (checked)
+        most = min(s.len, s.len - s.cnt + last + 1);
+        least = min(s.len, s.len - s.cnt + r / A.G + 1);
     }
     template <class S> __device__ __forceinline__ void advance(const Args &A) {
         if (++t < s.tiles) return;
         t = 0;
-        if (++rb < s.rbs) return;
-        rb = 0;
-        if (++h < A.P.heads) return;
-        h = 0;
-        while (++n < A.P.N) {
-            s = load_seq<S>(A, n);
-            if (s.rbs > 0) return;
+        if (++rb >= s.rbs) {
+            rb = 0;
+            if (++h >= A.P.heads) {
+                h = 0;
+                while (++n < A.P.N) {
+                    s = load_seq<S>(A, n);
+                    if (s.rbs > 0) break;
+                }
+            }
         }
+        enter<S>(A);
     }
 };
 
 // out = O / l (* sigmoid(gate)) for 4 channels of row r of a block; l = 0: a row that saw nothing
 template <class S> __device__ __forceinline__ void store4(const Args &A, const Cursor &c, int r, int ch, float4 o, float l) {
-    const int64_t R = (int64_t)c.rb * S::ROWS + r;
-    if (R >= (int64_t)c.s.cnt * A.G) return;
-    const int i = (int)(R / A.G), hq = c.h * A.G + (int)(R - (int64_t)i * A.G);
+    const int R = c.rb * S::ROWS + r;
+    if (R >= c.s.cnt * A.G) return;
+    const int i = R / A.G, hq = c.h * A.G + R - i * A.G;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     float x[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
     if (A.gate.p) {
@@ -196,32 +231,58 @@ template <class S> struct State {
     float o[S::RT][S::PV][4][2];
 };
 
-// Rows of a block: loaded, rotated, scaled, split and laid out as the operand.
-template <class S> __device__ __forceinline__ void load_rows(const Args &A, const Cursor &c, float *qs, State<S> &st) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int64_t rows = (int64_t)c.s.cnt * A.G, R0 = (int64_t)c.rb * S::ROWS;
-    const int size = A.in_bf16 ? 2 : 4;
-    __syncwarp();
+// A block's query rows and the rotation's phases on their way to registers.
+template <class S> struct Rows {
+    float x[S::ROWS][S::DQK / 32];        // lane's channels lane, lane + 32, ...
+    uint64_t phase[S::DQK / 64];          // of pairs lane, lane + 32, ...
+};
+template <class S> __device__ __forceinline__ void fetch_rows(const Args &A, const Cursor &c, Rows<S> &f) {
+    const int lane = threadIdx.x & 31, size = A.in_bf16 ? 2 : 4;
+    const int rows = c.s.cnt * A.G, R0 = c.rb * S::ROWS;
+    int i = R0 / A.G, g = R0 - i * A.G;                  // the row's token and head of the group
 #pragma unroll
     for (int r = 0; r < S::ROWS; ++r) {
         const bool ok = R0 + r < rows;
-        const int i = ok ? (int)((R0 + r) / A.G) : 0, hq = c.h * A.G + (ok ? (int)((R0 + r) - (int64_t)i * A.G) : 0);
-        const char *src = A.q.p + ((int64_t)(c.s.q0 + i) * A.q.ts + (int64_t)hq * A.q.hs) * size;
+        const char *src = A.q.p + ((int64_t)(c.s.q0 + i) * A.q.ts + (int64_t)(c.h * A.G + g) * A.q.hs) * size;
 #pragma unroll
-        for (int k = 0; k < S::DQK / 32; ++k)
-            qs[r * S::QS + lane + 32 * k] = ok ? load_elt(src, lane + 32 * k, A.in_bf16) * A.qmul : 0.f;
+        for (int k = 0; k < S::DQK / 32; ++k) f.x[r][k] = ok ? load_elt(src, lane + 32 * k, A.in_bf16) : 0.f;
+        if (++g == A.G) { g = 0; ++i; }
     }
+#pragma unroll
+    for (int k = 0; k < S::DQK / 64; ++k) f.phase[k] = lane + 32 * k < A.r.half ? A.r.phase[lane + 32 * k] : 0;
+}
+
+// Rows of a block: rotated, scaled, split and laid out as the operand.
+template <class S> __device__ __forceinline__ void load_rows(const Args &A, const Cursor &c, const Rows<S> &f, float *qs, State<S> &st) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int rows = c.s.cnt * A.G, R0 = c.rb * S::ROWS;
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < S::ROWS; ++r)
+#pragma unroll
+        for (int k = 0; k < S::DQK / 32; ++k) qs[r * S::QS + lane + 32 * k] = f.x[r][k] * A.qmul;
     __syncwarp();
     if (A.r.dim > 0) {
-        for (int x = lane; x < S::ROWS * A.r.half; x += 32) {
-            const int r = x / A.r.half, p = x - r * A.r.half;
-            if (R0 + r >= rows) continue;
-            const int pos = c.s.len - c.s.cnt + (int)((R0 + r) / A.G);
-            const float2 cs = rope_cs(A.r.phase[p], pos);
-            float *a = qs + r * S::QS + A.r.off + (A.r.inter ? 2 * p : p), *b = a + (A.r.inter ? 1 : A.r.half);
-            const float u = *a * A.r.mscale, v = *b * A.r.mscale;
-            *a = u * cs.x - v * cs.y;
-            *b = v * cs.x + u * cs.y;
+#pragma unroll
+        for (int k = 0; k < S::DQK / 64; ++k) {
+            const int p = lane + 32 * k;
+            if (p >= A.r.half) break;
+            float *a = qs + A.r.off + (A.r.inter ? 2 * p : p);
+            const int apart = A.r.inter ? 1 : A.r.half;
+            int head = R0 % A.G, pos = c.s.len - c.s.cnt + R0 / A.G;
+            float2 cs = rope_cs(f.phase[k], pos);
+#pragma unroll
+            for (int r = 0; r < S::ROWS; ++r) {
+                if (R0 + r >= rows) break;
+                float *x = a + r * S::QS, *y = x + apart;
+                const float u = *x * A.r.mscale, v = *y * A.r.mscale;
+                *x = u * cs.x - v * cs.y;
+                *y = v * cs.x + u * cs.y;
+                if (++head == A.G) {                     // the next row is another token's
+                    head = 0;
+                    cs = rope_cs(f.phase[k], ++pos);
+                }
+            }
         }
         __syncwarp();
     }
@@ -252,8 +313,8 @@ template <class S> __device__ __forceinline__ void load_rows(const Args &A, cons
     }
 #pragma unroll
     for (int rt = 0; rt < S::RT; ++rt) {
-        const int64_t R = R0 + 4 * rt + t;
-        st.vis[rt] = R < rows ? c.s.len - c.s.cnt + (int)(R / A.G) + 1 : 0;
+        const int R = R0 + 4 * rt + t;
+        st.vis[rt] = R < rows ? c.s.len - c.s.cnt + R / A.G + 1 : 0;
         st.m[rt] = -INFINITY;
         st.l[rt] = 0.f;
 #pragma unroll
@@ -298,7 +359,7 @@ template <class S> __device__ __forceinline__ void load_rows(const Args &A, cons
 __device__ __forceinline__ int order8(int r) { return r ^ (r >> 2); }
 
 // One tile.  j0: its first token; bad: strips on pages outside the pool.  MASK: some row does not see all of it.
-template <class S, bool MASK> __device__ __forceinline__ void tile(const Args &A, const char *stage, int j0, int len, unsigned bad, State<S> &st) {
+template <class S, bool MASK> __device__ __forceinline__ void tile(const Args &A, const char *const (&stage)[S::TS], int j0, int len, unsigned bad, State<S> &st) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int ta = S::I4 ? order8(g) : g;                // this lane's tokens of a strip: ta and ta + 8
     float p[S::NS][S::RT][2];
@@ -308,13 +369,10 @@ template <class S, bool MASK> __device__ __forceinline__ void tile(const Args &A
     for (int rt = 0; rt < S::RT; ++rt) top[rt] = -INFINITY;
 #pragma unroll
     for (int s = 0; s < S::NS; ++s) {
-        const char *sp = stage + s * S::STRIP;
+        const char *sp = stage[s / S::SS] + s % S::SS * S::STRIP;
         const int ja = j0 + 16 * s + ta;
-        float e0 = 0.f, e1 = 0.f;
         if constexpr (S::I4) {
             float ps[S::RT][2], pm[S::RT][2];
-#pragma unroll
-            for (int rt = 0; rt < S::RT; ++rt) ps[rt][0] = ps[rt][1] = pm[rt][0] = pm[rt][1] = 0.f;
 #pragma unroll
             for (int k = 0; k < S::PK; ++k) {
                 const char *pl = sp + k * kPlaneI4;
@@ -324,39 +382,31 @@ template <class S, bool MASK> __device__ __forceinline__ void tile(const Args &A
                 const float2 kb = __half22float2(*reinterpret_cast<const __half2 *>(pl + 544 + ta * 4));
                 float c[S::RT][4];
 #pragma unroll
-                for (int rt = 0; rt < S::RT; ++rt) c[rt][0] = c[rt][1] = c[rt][2] = c[rt][3] = 0.f;
-#pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t ua = (i < 2 ? wa.x : wa.y) >> (8 * (i & 1)), ub = (i < 2 ? wb.x : wb.y) >> (8 * (i & 1));
 #pragma unroll
-                    for (int rt = 0; rt < S::RT; ++rt)
-                        mma(c[rt], ua & 0x000F000Fu, ub & 0x000F000Fu, ua & 0x00F000F0u, ub & 0x00F000F0u, st.qf[rt][k][i][0],
-                            st.qf[rt][k][i][1], true);
+                    for (int rt = 0; rt < S::RT; ++rt) {
+                        if (i == 0)
+                            mma<true, true>(c[rt], ua & 0x000F000Fu, ub & 0x000F000Fu, ua & 0x00F000F0u, ub & 0x00F000F0u, st.qf[rt][k][i][0], st.qf[rt][k][i][1]);
+                        else
+                            mma<true, false>(c[rt], ua & 0x000F000Fu, ub & 0x000F000Fu, ua & 0x00F000F0u, ub & 0x00F000F0u, st.qf[rt][k][i][0], st.qf[rt][k][i][1]);
+                    }
                 }
 #pragma unroll
                 for (int rt = 0; rt < S::RT; ++rt) {
-                    ps[rt][0] = fmaf(ka.x, c[rt][0] + c[rt][1], ps[rt][0]);
-                    ps[rt][1] = fmaf(kb.x, c[rt][2] + c[rt][3], ps[rt][1]);
-                    pm[rt][0] = fmaf(ka.y, st.qsum[rt][k], pm[rt][0]);
-                    pm[rt][1] = fmaf(kb.y, st.qsum[rt][k], pm[rt][1]);
+                    const float sa = ka.x * (c[rt][0] + c[rt][1]), sb = kb.x * (c[rt][2] + c[rt][3]);
+                    ps[rt][0] = k ? ps[rt][0] + sa : sa;
+                    ps[rt][1] = k ? ps[rt][1] + sb : sb;
+                    pm[rt][0] = k ? fmaf(ka.y, st.qsum[rt][k], pm[rt][0]) : ka.y * st.qsum[rt][k];
+                    pm[rt][1] = k ? fmaf(kb.y, st.qsum[rt][k], pm[rt][1]) : kb.y * st.qsum[rt][k];
                 }
             }
-            __half2 big0 = __float2half2_rn(0.f), big1 = big0;
 #pragma unroll
             for (int v = 0; v < S::PV; ++v) {
                 const char *pl = sp + (S::PK + v) * kPlaneI4;
                 vp[s][v][0] = *reinterpret_cast<const __half2 *>(pl + 512 + ta * 4);
                 vp[s][v][1] = *reinterpret_cast<const __half2 *>(pl + 544 + ta * 4);
-                if (MASK) {                              // rows past the length hold anything, a NaN too
-                    if (ja >= len) vp[s][v][0] = __float2half2_rn(0.f);
-                    if (ja + 8 >= len) vp[s][v][1] = __float2half2_rn(0.f);
-                }
-                big0 = __hmax2(big0, vp[s][v][0]);
-                big1 = __hmax2(big1, vp[s][v][1]);
             }
-            // exponents of the largest scales (2^-24 at least): scale < 2^e
-            e0 = (float)((int)(__float_as_uint(fmaxf(__low2float(big0), 5.9604645e-8f)) >> 23) - 126);
-            e1 = (float)((int)(__float_as_uint(fmaxf(__low2float(big1), 5.9604645e-8f)) >> 23) - 126);
 #pragma unroll
             for (int rt = 0; rt < S::RT; ++rt) {
                 p[s][rt][0] = fmaf(ps[rt][0], st.fac[rt], pm[rt][0]);
@@ -364,8 +414,6 @@ template <class S, bool MASK> __device__ __forceinline__ void tile(const Args &A
             }
         } else {
             float c[S::RT][4];
-#pragma unroll
-            for (int rt = 0; rt < S::RT; ++rt) c[rt][0] = c[rt][1] = c[rt][2] = c[rt][3] = 0.f;
             const int tok = lane & 15, odd = lane >> 4;
 #pragma unroll
             for (int k = 0; k < S::PK; ++k)
@@ -374,8 +422,10 @@ template <class S, bool MASK> __device__ __forceinline__ void tile(const Args &A
                     uint32_t a[4];
                     ldmatrix4(a, tc::smem_u32(sp + k * kPlaneBf16 + tok * 128 + (((2 * i + odd) ^ (tok & 7)) << 4)));
 #pragma unroll
-                    for (int rt = 0; rt < S::RT; ++rt)
-                        mma(c[rt], a[0], a[1], a[2], a[3], st.qf[rt][k][i][0], st.qf[rt][k][i][1], false);
+                    for (int rt = 0; rt < S::RT; ++rt) {
+                        if (k + i == 0) mma<false, true>(c[rt], a[0], a[1], a[2], a[3], st.qf[rt][k][i][0], st.qf[rt][k][i][1]);
+                        else mma<false, false>(c[rt], a[0], a[1], a[2], a[3], st.qf[rt][k][i][0], st.qf[rt][k][i][1]);
+                    }
                 }
 #pragma unroll
             for (int rt = 0; rt < S::RT; ++rt) {
@@ -391,8 +441,33 @@ template <class S, bool MASK> __device__ __forceinline__ void tile(const Args &A
                 if (ja >= st.vis[rt]) p[s][rt][0] = -INFINITY;
                 if (ja + 8 >= st.vis[rt]) p[s][rt][1] = -INFINITY;
             }
-            top[rt] = fmaxf(top[rt], fmaxf(p[s][rt][0] + e0, p[s][rt][1] + e1));
+            top[rt] = fmaxf(top[rt], fmaxf(p[s][rt][0], p[s][rt][1]));
         }
+    }
+    // 4-bit: every value scale that the row sees here is below 2^e (their fp16 bits order as integers; NaN drops out)
+    [[maybe_unused]] float e[S::RT];
+    if constexpr (S::I4) {
+#pragma unroll
+        for (int rt = 0; rt < (MASK ? S::RT : 1); ++rt) {
+            __half2 big = __float2half2_rn(0.f);
+#pragma unroll
+            for (int s = 0; s < S::NS; ++s)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int v = 0; v < S::PV; ++v)
+                        if (!MASK || j0 + 16 * s + ta + 8 * x < st.vis[rt]) big = __hmax2(big, vp[s][v][x]);
+            unsigned bits = *reinterpret_cast<const uint32_t *>(&big) & 0xffffu;
+            if (MASK) {                                  // the row's own tokens only: lanes of the same t
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
+            } else {
+                bits = __reduce_max_sync(0xffffffffu, bits);
+            }
+            e[rt] = (float)max((int)(bits >> 10), 1) - 14.f;
+        }
+#pragma unroll
+        for (int rt = MASK ? S::RT : 1; rt < S::RT; ++rt) e[rt] = e[0];
     }
     float corr[S::RT];
 #pragma unroll
@@ -400,7 +475,7 @@ template <class S, bool MASK> __device__ __forceinline__ void tile(const Args &A
         top[rt] = fmaxf(top[rt], __shfl_xor_sync(0xffffffffu, top[rt], 4));
         top[rt] = fmaxf(top[rt], __shfl_xor_sync(0xffffffffu, top[rt], 8));
         top[rt] = fmaxf(top[rt], __shfl_xor_sync(0xffffffffu, top[rt], 16));
-        const float m = fmaxf(st.m[rt], S::I4 ? top[rt] - 14.f : top[rt]);
+        const float m = fmaxf(st.m[rt], S::I4 ? top[rt] + (e[rt] - 14.f) : top[rt]);
         const float base = m == -INFINITY ? 0.f : m;
         corr[rt] = ex2(st.m[rt] - base);
         st.m[rt] = m;
@@ -421,21 +496,25 @@ template <class S, bool MASK> __device__ __forceinline__ void tile(const Args &A
             for (int rt = 0; rt < S::RT; ++rt) {
                 float mn = st.mn[rt][v] * corr[rt];
 #pragma unroll
-                for (int s = 0; s < S::NS; ++s)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        float2 q = __half22float2(vp[s][v][x]);
-                        // a key the row does not see weighs 0 even against a NaN
-                        if (MASK && j0 + 16 * s + ta + 8 * x >= st.vis[rt]) q = make_float2(0.f, 0.f);
-                        mn = fmaf(p[s][rt][x], q.y, mn);
-                        b[s][rt][x] = transpose8x8(split_pair<true>(p[s][rt][x] * q.x));
+                for (int s = 0; s < S::NS; ++s) {
+                    float2 qa = __half22float2(vp[s][v][0]), qb = __half22float2(vp[s][v][1]);
+                    if (MASK) {                          // a key the row does not see weighs 0 even against a NaN
+                        if (j0 + 16 * s + ta >= st.vis[rt]) qa = make_float2(0.f, 0.f);
+                        if (j0 + 16 * s + ta + 8 >= st.vis[rt]) qb = make_float2(0.f, 0.f);
                     }
+                    mn = fmaf(p[s][rt][0], qa.y, mn);
+                    mn = fmaf(p[s][rt][1], qb.y, mn);
+                    uint32_t pa, pb;
+                    split_two<true>(p[s][rt][0] * qa.x, p[s][rt][1] * qb.x, pa, pb);
+                    b[s][rt][0] = transpose8x8(pa);
+                    b[s][rt][1] = transpose8x8(pb);
+                }
                 st.mn[rt][v] = mn;
             }
             uint32_t lo0[S::NS], hi0[S::NS], lo1[S::NS], hi1[S::NS];     // nibbles 0-3 and 4-7 of a token pair, a half each
 #pragma unroll
             for (int s = 0; s < S::NS; ++s) {
-                const char *pl = stage + s * S::STRIP + (S::PK + v) * kPlaneI4 + 4 * g;
+                const char *pl = stage[s / S::SS] + s % S::SS * S::STRIP + (S::PK + v) * kPlaneI4 + 4 * g;
                 const int a = order8(2 * t) * 32, c = order8(2 * t + 1) * 32;
                 const uint32_t wa = *reinterpret_cast<const uint32_t *>(pl + a), wb = *reinterpret_cast<const uint32_t *>(pl + c);
                 const uint32_t wc = *reinterpret_cast<const uint32_t *>(pl + 256 + a), wd = *reinterpret_cast<const uint32_t *>(pl + 256 + c);
@@ -448,13 +527,15 @@ template <class S, bool MASK> __device__ __forceinline__ void tile(const Args &A
             for (int j = 0; j < 4; ++j) {
                 float c[S::RT][4];
 #pragma unroll
-                for (int rt = 0; rt < S::RT; ++rt) c[rt][0] = c[rt][1] = c[rt][2] = c[rt][3] = 0.f;
-#pragma unroll
                 for (int s = 0; s < S::NS; ++s) {
                     const uint32_t u0 = (j < 2 ? lo0[s] : hi0[s]) >> (8 * (j & 1)), u1 = (j < 2 ? lo1[s] : hi1[s]) >> (8 * (j & 1));
 #pragma unroll
-                    for (int rt = 0; rt < S::RT; ++rt)
-                        mma(c[rt], u0 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x000F000Fu, u1 & 0x00F000F0u, b[s][rt][0], b[s][rt][1], true);
+                    for (int rt = 0; rt < S::RT; ++rt) {
+                        if (s == 0)
+                            mma<true, true>(c[rt], u0 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x000F000Fu, u1 & 0x00F000F0u, b[s][rt][0], b[s][rt][1]);
+                        else
+                            mma<true, false>(c[rt], u0 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x000F000Fu, u1 & 0x00F000F0u, b[s][rt][0], b[s][rt][1]);
+                    }
                 }
 #pragma unroll
                 for (int rt = 0; rt < S::RT; ++rt) {
@@ -468,19 +549,19 @@ template <class S, bool MASK> __device__ __forceinline__ void tile(const Args &A
             for (int s = 0; s < S::NS; ++s)
 #pragma unroll
                 for (int rt = 0; rt < S::RT; ++rt) {
-                    b[s][rt][0] = transpose8x8(split_pair<false>(p[s][rt][0]));
-                    b[s][rt][1] = transpose8x8(split_pair<false>(p[s][rt][1]));
+                    uint32_t pa, pb;
+                    split_two<false>(p[s][rt][0], p[s][rt][1], pa, pb);
+                    b[s][rt][0] = transpose8x8(pa);
+                    b[s][rt][1] = transpose8x8(pb);
                 }
             const int tok = (lane & 7) + ((lane >> 4) << 3), odd = (lane >> 3) & 1;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float c[S::RT][4];
 #pragma unroll
-                for (int rt = 0; rt < S::RT; ++rt) c[rt][0] = c[rt][1] = c[rt][2] = c[rt][3] = 0.f;
-#pragma unroll
                 for (int s = 0; s < S::NS; ++s) {
                     uint32_t a[4];
-                    ldmatrix4t(a, tc::smem_u32(stage + s * S::STRIP + (S::PK + v) * kPlaneBf16 + tok * 128 +
+                    ldmatrix4t(a, tc::smem_u32(stage[s / S::SS] + s % S::SS * S::STRIP + (S::PK + v) * kPlaneBf16 + tok * 128 +
                                                (((2 * j + odd) ^ (tok & 7)) << 4)));
                     if (MASK) {
                         // rows past the length hold anything; a value that is not finite goes to 0 here and makes
@@ -499,15 +580,18 @@ template <class S, bool MASK> __device__ __forceinline__ void tile(const Args &A
                             for (int rt = 0; rt < S::RT; ++rt) {
                                 const int ja = j0 + 16 * s + ta;
                                 const uint32_t s0 = transpose8x8(ja < st.vis[rt] ? 0x3f80u : 0u), s1 = transpose8x8(ja + 8 < st.vis[rt] ? 0x3f80u : 0u);
-                                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma(d, flag[0] & 0x3f803f80u, flag[1] & 0x3f803f80u, flag[2] & 0x3f803f80u, flag[3] & 0x3f803f80u, s0, s1, false);
+                                float d[4];
+                                mma<false, true>(d, flag[0] & 0x3f803f80u, flag[1] & 0x3f803f80u, flag[2] & 0x3f803f80u, flag[3] & 0x3f803f80u, s0, s1);
                                 if (d[0] > 0.f) st.o[rt][v][j][0] = __int_as_float(0x7fc00000);
                                 if (d[2] > 0.f) st.o[rt][v][j][1] = __int_as_float(0x7fc00000);
                             }
                         }
                     }
 #pragma unroll
-                    for (int rt = 0; rt < S::RT; ++rt) mma(c[rt], a[0], a[1], a[2], a[3], b[s][rt][0], b[s][rt][1], false);
+                    for (int rt = 0; rt < S::RT; ++rt) {
+                        if (s == 0) mma<false, true>(c[rt], a[0], a[1], a[2], a[3], b[s][rt][0], b[s][rt][1]);
+                        else mma<false, false>(c[rt], a[0], a[1], a[2], a[3], b[s][rt][0], b[s][rt][1]);
+                    }
                 }
 #pragma unroll
                 for (int rt = 0; rt < S::RT; ++rt) {
@@ -556,41 +640,90 @@ template <class S> __device__ __forceinline__ void write_record(State<S> &st, bo
 }
 
 struct Segment {                                        // what a warp leaves for the join
-    long long key;                                      // first unit of the (sequence, head, row block), -1: nothing
+    int key;                                            // units before the (sequence, head, row block)'s tiles, -1: nothing
+    int last;                                           // its last tile's unit
     int begins, ends;                                   // whether it holds its first and its last tile
     int n, h, rb, pad;
-    long long last;                                     // last unit
+};
+
+// The row of units.  A (sequence, head, row block) takes `extra` units for its start and end (rows loaded, rotated and
+// split; sums joined and stored) and one for each tile; with short sequences the former are most of the work.
+struct Line {
+    unsigned extra;
+    const unsigned *pre, *pre_tiles;                    // [THREADS + 1]: units and tiles before each thread's sequences
+    int per;                                            // sequences of a thread
+    // Where unit u lies: its sequence, the (head, row block) in it, the unit in that one; returns the tiles before u.
+    template <class S> __device__ __forceinline__ unsigned find(const Args &A, unsigned u, int threads, Seq &s, int &n, unsigned &pair, unsigned &at) const {
+        int slot = -1;
+        for (int i = threadIdx.x & 31; i < threads; i += 32)
+            if (pre[i] <= u && u < pre[i + 1]) slot = i;
+        slot = __reduce_max_sync(0xffffffffu, slot);
+        unsigned rest = u - pre[slot], tiles = pre_tiles[slot];
+        n = slot * per;
+        s = load_seq<S>(A, n);
+        unsigned have;
+        while (rest >= (have = s.pairs(A.P.heads) * (s.tiles + extra))) {
+            rest -= have;
+            tiles += s.pairs(A.P.heads) * s.tiles;
+            s = load_seq<S>(A, ++n);
+        }
+        pair = rest / (s.tiles + extra);
+        at = rest - pair * (s.tiles + extra);
+        return tiles + pair * s.tiles + (at > extra ? at - extra : 0);
+    }
+};
+
+// U units in equal runs over GW warps: the first `more` of them get one more than the others.
+struct Split {
+    unsigned base, more;
+    __device__ __forceinline__ Split(unsigned U, unsigned GW) : base(U / GW), more(U - U / GW * GW) {}
+    __device__ __forceinline__ unsigned begin(unsigned w) const { return w * base + min(w, more); }
+    __device__ __forceinline__ unsigned owner(unsigned u) const {
+        const unsigned edge = more * (base + 1);
+        return u < edge ? u / (base + 1) : more + (u - edge) / base;     // (base = 0: every unit is below the edge)
+    }
 };
 
 // weight of a record with maximum m under the common maximum top
 __device__ __forceinline__ float weight(float m, float top) { return m == -INFINITY ? 0.f : exp2f(m - top); }
 
-template <class S> __global__ void __launch_bounds__(S::WARPS * 32, 1) kernel(const __grid_constant__ Args A) {
+template <class S> __global__ void __launch_bounds__(S::WARPS * 32, 1) attend_kernel(const __grid_constant__ Args A) {
     extern __shared__ __align__(128) char smem[];
     constexpr int W = S::WARPS, THREADS = W * 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem);                                   // [W][STAGES]
     Segment *segs = reinterpret_cast<Segment *>(smem + 1024);                              // [2 W]
-    long long *pre = reinterpret_cast<long long *>(smem + 1024 + 2 * W * sizeof(Segment)); // [THREADS + 1]
-    static_assert(sizeof(Segment) == 48 || sizeof(Segment) == 40, "segment");
+    unsigned *pre = reinterpret_cast<unsigned *>(smem + 1024 + 2 * W * sizeof(Segment));   // [THREADS + 1]
+    unsigned *pre_tiles = pre + THREADS + 1;                                               // [THREADS + 1]
     char *mine = smem + S::COMMON + warp * S::WARP_BYTES;
     float *rec0 = reinterpret_cast<float *>(mine + S::STAGES * S::STAGE), *rec1 = rec0 + S::RECORD;
     const uint32_t bar = tc::smem_u32(bars + warp * S::STAGES);
-    __shared__ long long part_sum[W];
+    __shared__ unsigned part_sum[W], part_tiles[W];
     __shared__ unsigned arrived;
+    __shared__ float weights[2 * W][S::ROWS], sums[2 * W][S::ROWS];
 
     // ---- the call's units, and where each thread's sequences begin in their row
     const int per = (A.P.N + THREADS - 1) / THREADS;
     const int n_lo = min(A.P.N, (int)threadIdx.x * per), n_hi = min(A.P.N, n_lo + per);
-    long long own = 0;
-    for (int n = n_lo; n < n_hi; ++n) own += load_seq<S>(A, n).units(A.P.heads);
-    long long run = own;
+    unsigned own = 0, own_tiles = 0;                     // (sequence, head, row block)s, tiles
+    for (int n = n_lo; n < n_hi; ++n) {
+        const Seq q = load_seq<S>(A, n);
+        own += q.pairs(A.P.heads);
+        own_tiles += q.pairs(A.P.heads) * q.tiles;
+    }
+    unsigned run = own, run_tiles = own_tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += y;
+        const unsigned y = __shfl_up_sync(0xffffffffu, run, o), z = __shfl_up_sync(0xffffffffu, run_tiles, o);
+        if (lane >= o) {
+            run += y;
+            run_tiles += z;
+        }
     }
-    if (lane == 31) part_sum[warp] = run;
+    if (lane == 31) {
+        part_sum[warp] = run;
+        part_tiles[warp] = run_tiles;
+    }
     if (lane == 0) {
 #pragma unroll
         for (int s = 0; s < S::STAGES; ++s) tc::mbar_init(bar + 8 * s, 1);
@@ -598,117 +731,147 @@ template <class S> __global__ void __launch_bounds__(S::WARPS * 32, 1) kernel(co
         segs[2 * warp].key = segs[2 * warp + 1].key = -1;
     }
     __syncthreads();
-    long long before = 0, U = 0;
+    unsigned pairs = 0, tiles = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-        before += w < warp ? part_sum[w] : 0;
-        U += part_sum[w];
+        run += w < warp ? part_sum[w] : 0;
+        run_tiles += w < warp ? part_tiles[w] : 0;
+        pairs += part_sum[w];
+        tiles += part_tiles[w];
     }
-    pre[threadIdx.x] = before + run - own;
-    if (threadIdx.x == 0) pre[THREADS] = U;
+    // (a call with few tiles has a warp for each, and no runs to balance)
+    const unsigned extra = tiles > 2 * gridDim.x * W ? S::EXTRA : 0, U = tiles + extra * pairs;
+    pre_tiles[threadIdx.x] = run_tiles - own_tiles;
+    pre[threadIdx.x] = run_tiles - own_tiles + extra * (run - own);
+    if (threadIdx.x == 0) {
+        pre[THREADS] = U;
+        pre_tiles[THREADS] = tiles;
+    }
     __syncthreads();
     if (U == 0) return;
     // few units: as few CTAs as give every warp one, so that fewer joins leave the CTA
-    const long long C = min((long long)gridDim.x, (U + W - 1) / W);
-    if ((long long)blockIdx.x >= C) return;
-    const long long gw = (long long)blockIdx.x * W + warp, GW = C * W;
-    const long long u0 = gw * U / GW, u1 = (gw + 1) * U / GW;
-    const int total = (int)(u1 - u0);
-
+    const unsigned C = min(gridDim.x, (U + W - 1) / W);
+    if (blockIdx.x >= C) return;
+    const Split split(U, C * W);
+    const Line line{extra, pre, pre_tiles, per};
+    const unsigned gw = blockIdx.x * W + warp, u0 = split.begin(gw), u1 = split.begin(gw + 1);
+    int total = 0;                                       // this warp's tiles
+    unsigned pair = 0, at = 0, base = 0;                 // base: units before its first (sequence, head, row block)
+    Cursor pc;                                           // runs ahead: the tile whose copies come next
+    if (u1 > u0) {
+        const unsigned first = line.find<S>(A, u0, THREADS, pc.s, pc.n, pair, at);
+        Seq q;
+        int n;
+        unsigned p2, a2;
+        total = (int)((u1 < U ? line.find<S>(A, u1, THREADS, q, n, p2, a2) : tiles) - first);
+        base = u0 - at;
+        pc.t = at > extra ? (int)(at - extra) : 0;
+    }
     if (total > 0) {
-        Cursor pc;                                       // runs ahead: the tile whose copies come next
-        {
-            int at = -1;
-            for (int i = lane; i < THREADS; i += 32)
-                if (pre[i] <= u0 && u0 < pre[i + 1]) at = i;
-            at = __reduce_max_sync(0xffffffffu, at);
-            long long rest = u0 - pre[at];
-            pc.n = at * per;
-            pc.s = load_seq<S>(A, pc.n);
-            while (rest >= pc.s.units(A.P.heads)) {
-                rest -= pc.s.units(A.P.heads);
-                pc.s = load_seq<S>(A, ++pc.n);
-            }
-            const long long pair = rest / pc.s.tiles;
-            pc.t = (int)(rest - pair * pc.s.tiles);
-            pc.h = (int)(pair / pc.s.rbs);
-            pc.rb = (int)(pair - (long long)pc.h * pc.s.rbs);
-        }
+        pc.h = (int)(pair / pc.s.rbs);
+        pc.rb = (int)(pair - pc.h * pc.s.rbs);
+        pc.enter<S>(A);
         Cursor cc = pc;
-        int issued = 0;
-        unsigned bad_strips = 0;                         // NS bits a stage
-        int page = -2;                                   // lane s: page of strip s of the next tile; -1 bad, -2 none
-        int page_at = 0, page_h = 0;                     // its strip in the page, its head
-        auto look_up = [&]() {
-            page = -2;
-            const int tok = pc.t * S::TILE + 16 * lane;
-            if (lane < S::NS && tok < min(pc.s.len, pc.template seen_most<S>(A))) {
-                page = paged_page(A.P, pc.n, tok);
-                page_at = tok % A.P.page_size / kStrip;
-                page_h = pc.h;
+        const int stages = total * S::TS;
+        int issued = 0;                                  // stages
+        unsigned bad_strips = 0;                         // SS bits a stage
+        // lane s: strip s of a tile, its page (-1 bad, -2 none), its place in it and the head; a tile's pages are asked for
+        // while the one before it is issued
+        struct Where { int page, at, h; } now, next;
+        auto look_up = [&](bool more) {
+            next.page = -2;
+            const int strip = pc.t * S::NS + lane;
+            if (more && lane < S::NS && 16 * strip < pc.most) {
+                const int j = A.per_page_inv ? (int)__umulhi((unsigned)strip, A.per_page_inv) : strip;
+                const int pg = A.P.table[(int64_t)pc.n * A.P.max_pages + j];
+                next.page = pg >= 0 && pg < A.P.num_pages ? pg : -1;
+                next.at = strip - j * A.per_page;
+                next.h = pc.h;
             }
+        };
+        auto next_tile = [&](int tiles) {                // tiles: how many were looked up before this one
+            now = next;
+            if (tiles < total) pc.advance<S>(A);
+            look_up(tiles < total);
         };
         auto issue = [&]() {
-            const int s = issued % S::STAGES;
-            const unsigned have = __ballot_sync(0xffffffffu, page >= 0), bad = __ballot_sync(0xffffffffu, page == -1);
-            bad_strips = (bad_strips & ~(((1u << S::NS) - 1) << (s * S::NS))) | (bad << (s * S::NS));
+            const int s = issued % S::STAGES, sub = issued % S::TS;
+            const bool here = lane / S::SS == sub;
+            const unsigned have = __ballot_sync(0xffffffffu, here && now.page >= 0), bad = __ballot_sync(0xffffffffu, here && now.page == -1) >> (sub * S::SS);
+            bad_strips = (bad_strips & ~(((1u << S::SS) - 1) << (s * S::SS))) | (bad << (s * S::SS));
             if (lane == 0) tc::mbar_arrive_expect_tx(bar + 8 * s, __popc(have) * S::STRIP);
             __syncwarp();
-            if (page >= 0)
-                tc::bulk_g2s(tc::smem_u32(mine + s * S::STAGE + lane * S::STRIP),
-                             A.P.pool + (int64_t)page * A.P.page_bytes + (int64_t)page_h * A.P.block_bytes + (int64_t)page_at * S::STRIP,
-                             S::STRIP, bar + 8 * s);
-            if (++issued < total) {
-                pc.advance<S>(A);
-                look_up();
+            // strips of one page lie together: the first of them brings all
+            const int first = sub * S::SS;
+            if (here && now.page >= 0 && (lane == first || now.at == 0)) {
+                const int run = min(A.per_page - now.at, __popc(have >> lane));
+                tc::bulk_g2s(tc::smem_u32(mine + s * S::STAGE + (lane - first) * S::STRIP),
+                             A.P.pool + (int64_t)now.page * A.P.page_bytes + (int64_t)now.h * A.P.block_bytes + (int64_t)now.at * S::STRIP,
+                             run * S::STRIP, bar + 8 * s);
             }
+            ++issued;
+            if (issued % S::TS == 0) next_tile(issued / S::TS + 1);
         };
-        look_up();
-        while (issued < total && issued < S::STAGES) issue();
+        Rows<S> rows;
+        look_up(true);
+        fetch_rows<S>(A, cc, rows);                      // under the pages' and the copies' latency
+        next_tile(1);
+        while (issued < stages && issued < S::STAGES) issue();
 
         State<S> st;
         bool dead = false;                               // a wait ran out: nothing more is issued or used
-        long long first_unit = u0 - cc.t;                // first unit of the current segment
-        bool begins = true;
+        bool begins = cc.t == 0, fresh = true;           // fresh: the rows of a new block are on their way
         for (int k = 0; k < total; ++k) {
-            if (k == 0 || cc.t == 0) {
-                begins = cc.t == 0;
-                first_unit = u0 + k - cc.t;
-                load_rows<S>(A, cc, rec1, st);
-            }
-            const int s = k % S::STAGES;
-            if (!dead && !tc::mbar_wait_bounded(bar + 8 * s, (k / S::STAGES) & 1, kWaitTries)) {
-                dead = true;
-                if (lane == 0) atomicOr(A.status, 2u);
-            }
-            dead = __any_sync(0xffffffffu, dead);
-            const int j0 = cc.t * S::TILE, most = cc.template seen_most<S>(A);
-            const unsigned bad = (bad_strips >> (s * S::NS)) & ((1u << S::NS) - 1);
-            if (!dead && j0 < min(cc.s.len, most)) {
-                if (bad || j0 + S::TILE > min(cc.s.len, cc.template seen_least<S>(A)))
-                    tile<S, true>(A, mine + s * S::STAGE, j0, cc.s.len, bad, st);
-                else
-                    tile<S, false>(A, mine + s * S::STAGE, j0, cc.s.len, 0, st);
-            }
-            __syncwarp();
-            if (!dead && issued < total) issue();
-            const bool ends = cc.t == cc.s.tiles - 1;
-            if (ends || k == total - 1) {
-                const bool lost = cc.s.len < 0;
-                if (begins && ends) {
-                    write_record<S>(st, lost, rec1);
-                    for (int x = lane; x < S::ROWS * S::DV / 4; x += 32) {
-                        const int r = x / (S::DV / 4), ch = 4 * (x - r * (S::DV / 4));
-                        store4<S>(A, cc, r, ch, *reinterpret_cast<const float4 *>(rec1 + 2 * S::ROWS + r * S::DV + ch), rec1[S::ROWS + r]);
-                    }
-                    __syncwarp();
-                } else {
-                    write_record<S>(st, lost, begins ? rec1 : rec0);
-                    if (lane == 0)
-                        segs[2 * warp + (begins ? 1 : 0)] = Segment{first_unit, begins, ends, cc.n, cc.h, cc.rb, 0, first_unit + cc.s.tiles - 1};
+            if (fresh) load_rows<S>(A, cc, rows, rec1, st);
+            fresh = false;
+            const char *stage[S::TS];
+            unsigned bad = 0;
+#pragma unroll
+            for (int i = 0; i < S::TS; ++i) {
+                const int f = k * S::TS + i, s = f % S::STAGES;
+                stage[i] = mine + s * S::STAGE;
+                bad |= ((bad_strips >> (s * S::SS)) & ((1u << S::SS) - 1)) << (i * S::SS);
+                if (!dead && !tc::mbar_wait_bounded(bar + 8 * s, (f / S::STAGES) & 1, kWaitTries)) {
+                    dead = true;
+                    if (lane == 0) atomicOr(A.status, 2u);
                 }
             }
-            if (k + 1 < total) cc.advance<S>(A);
+            dead = __any_sync(0xffffffffu, dead);
+            const int j0 = cc.t * S::TILE;
+            if (!dead && j0 < cc.most) {
+                if (bad || j0 + S::TILE > cc.least) tile<S, true>(A, stage, j0, cc.s.len, bad, st);
+                else tile<S, false>(A, stage, j0, cc.s.len, 0, st);
+            }
+            __syncwarp();
+            if (!dead) {
+#pragma unroll
+                for (int i = 0; i < S::TS; ++i)
+                    if (issued < stages) issue();
+            }
+            if (cc.t < cc.s.tiles - 1 && k < total - 1) {
+                ++cc.t;
+                continue;
+            }
+            const bool ends = cc.t == cc.s.tiles - 1, lost = cc.s.len < 0;
+            Cursor done = cc;
+            if (k < total - 1) {
+                cc.advance<S>(A);
+                fetch_rows<S>(A, cc, rows);
+            }
+            if (begins && ends) {
+                write_record<S>(st, lost, rec1);
+                for (int x = lane; x < S::ROWS * S::DV / 4; x += 32) {
+                    const int r = x / (S::DV / 4), ch = 4 * (x - r * (S::DV / 4));
+                    store4<S>(A, done, r, ch, *reinterpret_cast<const float4 *>(rec1 + 2 * S::ROWS + r * S::DV + ch), rec1[S::ROWS + r]);
+                }
+                __syncwarp();
+            } else {
+                write_record<S>(st, lost, begins ? rec1 : rec0);
+                if (lane == 0)
+                    segs[2 * warp + (begins ? 1 : 0)] = Segment{(int)(base + extra), (int)(base + extra) + done.s.tiles - 1, begins, ends, done.n, done.h, done.rb, 0};
+            }
+            begins = fresh = true;
+            base += done.s.tiles + extra;
         }
         if (dead)                                        // copies in flight land before their memory goes
             for (int k = 0; k < issued; ++k)
@@ -717,86 +880,103 @@ template <class S> __global__ void __launch_bounds__(S::WARPS * 32, 1) kernel(co
     __syncthreads();
 
     // ---- join the warps' records; those of (sequence, head, row block)s that reach into other CTAs go on
-    long long out_key[2], out_last[2];
-    Cursor out_at[2];
-    int outs = 0;
+    auto record = [&](int y) {
+        return reinterpret_cast<const float *>(smem + S::COMMON + (y >> 1) * S::WARP_BYTES + S::STAGES * S::STAGE) + (y & 1) * S::RECORD;
+    };
+    // a record's weight under the maximum of its run, and the run's sum (kept at each of its records)
+    for (int x = threadIdx.x; x < 2 * W * S::ROWS; x += THREADS) {
+        const int y = x / S::ROWS, r = x - y * S::ROWS, key = segs[y].key;
+        if (key < 0) continue;
+        float top = -INFINITY, l = 0.f;
+#pragma unroll 4
+        for (int z = 0; z < 2 * W; ++z)
+            if (segs[z].key == key) top = fmaxf(top, record(z)[r]);
+        weights[y][r] = weight(record(y)[r], top);
+#pragma unroll 4
+        for (int z = 0; z < 2 * W; ++z)
+            if (segs[z].key == key) l = fmaf(weight(record(z)[r], top), record(z)[S::ROWS + r], l);
+        sums[y][r] = l;
+    }
+    __syncthreads();
+    Segment out[2];                                      // runs that reach out of the CTA, the first and the last one
+    out[0].key = out[1].key = -1;
     float *const my_partial = A.partial + (size_t)blockIdx.x * 2 * S::RECORD;
     for (int i = 0; i < 2 * W;) {
-        const long long key = segs[i].key;
+        const int key = segs[i].key;
         if (key < 0) { ++i; continue; }
         int j = i + 1, last = i;
         for (; j < 2 * W && (segs[j].key < 0 || segs[j].key == key); ++j)
             if (segs[j].key == key) last = j;
-        const bool begins = segs[i].begins != 0, ends = segs[last].ends != 0;
+        const Segment head = segs[i];
+        const bool begins = head.begins != 0, whole = begins && segs[last].ends != 0;
         Cursor c;
-        c.n = segs[i].n; c.h = segs[i].h; c.rb = segs[i].rb; c.t = 0;
-        c.s = load_seq<S>(A, c.n);
+        c.n = head.n; c.h = head.h; c.rb = head.rb; c.t = 0;
+        if (whole) c.s = load_seq<S>(A, c.n);
         float *dst = my_partial + (begins ? S::RECORD : 0);
         for (int x = threadIdx.x; x < S::ROWS * S::DV / 4; x += THREADS) {
             const int r = x / (S::DV / 4), ch = 4 * (x - r * (S::DV / 4));
-            float top = -INFINITY;
-            for (int y = i; y <= last; ++y)
-                if (segs[y].key == key) {
-                    const float *rec = reinterpret_cast<const float *>(smem + S::COMMON + (y >> 1) * S::WARP_BYTES + S::STAGES * S::STAGE) + (y & 1) * S::RECORD;
-                    top = fmaxf(top, rec[r]);
-                }
-            float l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int y = i; y <= last; ++y)
-                if (segs[y].key == key) {
-                    const float *rec = reinterpret_cast<const float *>(smem + S::COMMON + (y >> 1) * S::WARP_BYTES + S::STAGES * S::STAGE) + (y & 1) * S::RECORD;
-                    const float f = weight(rec[r], top);
-                    const float4 v = *reinterpret_cast<const float4 *>(rec + 2 * S::ROWS + r * S::DV + ch);
-                    l = fmaf(f, rec[S::ROWS + r], l);
-                    o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
-                }
-            if (begins && ends) {
-                store4<S>(A, c, r, ch, o, l);
+#pragma unroll 4
+            for (int y = i; y <= last; ++y) {
+                if (segs[y].key < 0) continue;
+                const float f = weights[y][r];
+                const float4 v = *reinterpret_cast<const float4 *>(record(y) + 2 * S::ROWS + r * S::DV + ch);
+                o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
+            }
+            if (whole) {
+                store4<S>(A, c, r, ch, o, sums[i][r]);
             } else {
                 *reinterpret_cast<float4 *>(dst + 2 * S::ROWS + r * S::DV + ch) = o;
-                if (ch == 0) { dst[r] = top; dst[S::ROWS + r] = l; }
+                if (ch == 0) {
+                    float top = -INFINITY;
+                    for (int y = i; y <= last; ++y)
+                        if (segs[y].key == key) top = fmaxf(top, record(y)[r]);
+                    dst[r] = top;
+                    dst[S::ROWS + r] = sums[i][r];
+                }
             }
         }
-        if (!(begins && ends) && outs < 2) {
-            out_key[outs] = key;
-            out_last[outs] = segs[i].last;
-            out_at[outs++] = c;
-        }
+        if (!whole) out[begins ? 1 : 0] = head;
         i = j;
     }
-    for (int i = 0; i < outs; ++i) {
-        // the CTA that holds unit u: the largest c with c U / C <= u
-        const long long first = ((out_key[i] + 1) * C - 1) / U, last = ((out_last[i] + 1) * C - 1) / U;
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        const Segment o2 = i ? out[1] : out[0];
+        if (o2.key < 0) continue;
+        const unsigned first = split.owner(o2.key) / W, last = split.owner(o2.last) / W;
         __threadfence();
         __syncthreads();
         if (threadIdx.x == 0) arrived = atomicAdd(A.counters + first, 1u);
         __syncthreads();
-        if ((long long)arrived != last - first) continue;
+        if (arrived != last - first) continue;
         __threadfence();
         if (threadIdx.x == 0) A.counters[first] = 0;     // as the next call needs it
+        Cursor c;
+        c.n = o2.n; c.h = o2.h; c.rb = o2.rb; c.t = 0;
+        c.s = load_seq<S>(A, c.n);
+        auto rec = [&](unsigned b) { return A.partial + ((size_t)b * 2 + (b == first ? 1 : 0)) * S::RECORD; };
         for (int x = threadIdx.x; x < S::ROWS * S::DV / 4; x += THREADS) {
             const int r = x / (S::DV / 4), ch = 4 * (x - r * (S::DV / 4));
-            auto rec = [&](long long c) { return A.partial + ((size_t)c * 2 + (c == first ? 1 : 0)) * S::RECORD; };
             float top = -INFINITY;
-#pragma unroll 4
-            for (long long c = first; c <= last; ++c) top = fmaxf(top, __ldcg(rec(c) + r));
+#pragma unroll 8
+            for (unsigned b = first; b <= last; ++b) top = fmaxf(top, __ldcg(rec(b) + r));
             float l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (long long c = first; c <= last; ++c) {
-                const float f = weight(__ldcg(rec(c) + r), top);
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(rec(c) + 2 * S::ROWS + r * S::DV + ch));
-                l = fmaf(f, __ldcg(rec(c) + S::ROWS + r), l);
+#pragma unroll 8
+            for (unsigned b = first; b <= last; ++b) {
+                const float f = weight(__ldcg(rec(b) + r), top);
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(rec(b) + 2 * S::ROWS + r * S::DV + ch));
+                l = fmaf(f, __ldcg(rec(b) + S::ROWS + r), l);
                 o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
             }
-            store4<S>(A, out_at[i], r, ch, o, l);
+            store4<S>(A, c, r, ch, o, l);
         }
     }
 }
 
 template <class S> cudaError_t launch(const Args &A, int max_new, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = smem_attr_once((const void *)kernel<S>, S::SMEM, done);
+    cudaError_t e = smem_attr_once((const void *)attend_kernel<S>, S::SMEM, done);
     if (e != cudaSuccess) return e;
     int dev = 0, sms = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
@@ -807,7 +987,7 @@ template <class S> cudaError_t launch(const Args &A, int max_new, cudaStream_t s
     const double ctas = most / S::WARPS + 1;
     int grid = sms < kMaxCtas ? sms : kMaxCtas;
     if (ctas < grid) grid = (int)ctas;
-    kernel<S><<<grid, S::WARPS * 32, S::SMEM, stream>>>(A);
+    attend_kernel<S><<<grid, S::WARPS * 32, S::SMEM, stream>>>(A);
     count_launch();
     return cudaGetLastError();
 }
