@@ -32,14 +32,6 @@
 
 namespace k3kda {
 namespace attend {
-#ifndef XNS
-#define XNS 4
-#define XW 8
-#define XSS 4
-#endif
-#ifndef XEX
-#define XEX 2
-#endif
 
 constexpr int kMaxCtas = 608;                          // partials and counters of a workspace
 constexpr size_t kHeadBytes = 256 + 4096;              // status word, counters (4 B a CTA)
@@ -67,21 +59,20 @@ template <int DQK_, int DV_, int RT_, bool I4_> struct Shape {
     static constexpr int PK = DQK / 64, PV = DV / 64, PL = PK + PV;
     static constexpr int ROWS = 4 * RT;
     static constexpr int PLANE = I4 ? kPlaneI4 : kPlaneBf16, STRIP = PL * PLANE;
-    static constexpr int NS = I4 ? (PL <= 2 ? 4 : PL <= 4 ? XNS : 2) : (PL <= 2 ? 2 : 1);       // strips of a tile
-    static constexpr int SS = I4 && PL > 2 && PL <= 4 ? XSS : NS, TS = NS / SS;      // strips of a stage, stages of a tile
-    static constexpr int TILE = NS * kStrip, STAGE = SS * STRIP;
-    static constexpr int WARPS = I4 ? (PL <= 4 ? (RT == 1 ? XW : 8) : RT == 1 ? 8 : 4) : (PL <= 4 ? 6 : 4);
-    static constexpr int EXTRA = XEX;                                           // units of a block's start and end, in tiles
+    static constexpr int NS = I4 ? (PL <= 4 ? 4 : 2) : (PL <= 2 ? 2 : 1);       // strips of a tile
+    static constexpr int TILE = NS * kStrip, STAGE = NS * STRIP;
+    static constexpr int WARPS = I4 ? (PL <= 4 ? 8 : RT == 1 ? 8 : 4) : (PL <= 4 ? 6 : 4);
+    static constexpr int EXTRA = 2;                                             // units of a block's start and end, in tiles
     static constexpr int QS = DQK + 8;                                          // floats between staged rows
     static constexpr int RECORD = ROWS * (DV + 2);                              // floats: m, l, O
     static constexpr int STAGED = ROWS * (QS + PK + 1);                         // floats: rows, their sums and exponents
     static constexpr int SLOT1 = RECORD > STAGED ? RECORD : STAGED;
     static constexpr int FIXED = ((RECORD + SLOT1) * 4 + 127) / 128 * 128;      // bytes of a warp beside its ring
-    static constexpr int COMMON = 1024 + 2 * WARPS * 32 + (WARPS * 32 + 2) * 8; // barriers, segments, prefix sums
-    static constexpr int ROOM = (232448 - 256 - 2 * WARPS * ROWS * 8 - COMMON) / WARPS / 128 * 128;
+    static constexpr int COMMON = 1024 + 2 * WARPS * 32 + (WARPS * 32 + 4) * 4; // barriers, segments, prefix sums
+    static constexpr int ROOM = (232448 - 256 - COMMON) / WARPS / 128 * 128;
     static constexpr int FIT = (ROOM - FIXED) / STAGE;
     static constexpr int STAGES = FIT > 6 ? 6 : FIT;
-    static_assert(STAGES >= 2 && STAGES >= TS && STAGES * WARPS * 8 <= 1024 && STAGES * SS <= 32, "ring");
+    static_assert(STAGES >= 2 && STAGES * WARPS * 8 <= 1024 && STAGES * NS <= 32, "ring");
     static constexpr int WARP_BYTES = STAGES * STAGE + FIXED;
     static constexpr int SMEM = COMMON + WARPS * WARP_BYTES;
     static_assert(STAGE % 128 == 0 || (STAGES * STAGE) % 64 == 0, "alignment");
@@ -198,19 +189,26 @@ struct Cursor {
     }
 };
 
-// out = O / l (* sigmoid(gate)) for 4 channels of row r of a block; l = 0: a row that saw nothing
-template <class S> __device__ __forceinline__ void store4(const Args &A, const Cursor &c, int r, int ch, float4 o, float l) {
-    const int R = c.rb * S::ROWS + r;
-    if (R >= c.s.cnt * A.G) return;
-    const int i = R / A.G, hq = c.h * A.G + R - i * A.G;
+// out = O / l (* sigmoid(gate)) for channels ch .. ch + 3 of row R of a (sequence, key head) whose tokens begin at q0;
+// l = 0: a row that saw nothing.
+__device__ __forceinline__ void store4(const Args &A, int dv, int q0, int h, int R, int ch, float4 o, float l) {
+    const int i = R / A.G, hq = h * A.G + R - i * A.G;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     float x[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
     if (A.gate.p) {
-        const char *g = A.gate.p + ((int64_t)(c.s.q0 + i) * A.gate.ts + (int64_t)hq * A.gate.hs + ch) * (A.in_bf16 ? 2 : 4);
+        const int64_t at = (int64_t)(q0 + i) * A.gate.ts + (int64_t)hq * A.gate.hs + ch;
+        float g[4];
+        if (A.in_bf16) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] *= sigmoidf_(load_elt(g, e, A.in_bf16));
+            for (int e = 0; e < 4; ++e) g[e] = load_elt(A.gate.p, at + e, 1);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) g[e] = load_elt(A.gate.p, at + e, 0);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] *= sigmoidf_(g[e]);
     }
-    const int64_t at = ((int64_t)(c.s.q0 + i) * A.Hq + hq) * S::DV + ch;
+    const int64_t at = ((int64_t)(q0 + i) * A.Hq + hq) * dv + ch;
     if (A.out_bf16) {
         const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
         *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(A.out) + at) =
@@ -240,13 +238,22 @@ template <class S> __device__ __forceinline__ void fetch_rows(const Args &A, con
     const int lane = threadIdx.x & 31, size = A.in_bf16 ? 2 : 4;
     const int rows = c.s.cnt * A.G, R0 = c.rb * S::ROWS;
     int i = R0 / A.G, g = R0 - i * A.G;                  // the row's token and head of the group
+    const char *src[S::ROWS];
 #pragma unroll
     for (int r = 0; r < S::ROWS; ++r) {
-        const bool ok = R0 + r < rows;
-        const char *src = A.q.p + ((int64_t)(c.s.q0 + i) * A.q.ts + (int64_t)(c.h * A.G + g) * A.q.hs) * size;
-#pragma unroll
-        for (int k = 0; k < S::DQK / 32; ++k) f.x[r][k] = ok ? load_elt(src, lane + 32 * k, A.in_bf16) : 0.f;
+        src[r] = R0 + r < rows ? A.q.p + ((int64_t)(c.s.q0 + i) * A.q.ts + (int64_t)(c.h * A.G + g) * A.q.hs + lane) * size : nullptr;
         if (++g == A.G) { g = 0; ++i; }
+    }
+    if (A.in_bf16) {
+#pragma unroll
+        for (int r = 0; r < S::ROWS; ++r)
+#pragma unroll
+            for (int k = 0; k < S::DQK / 32; ++k) f.x[r][k] = src[r] ? load_elt(src[r], 32 * k, 1) : 0.f;
+    } else {
+#pragma unroll
+        for (int r = 0; r < S::ROWS; ++r)
+#pragma unroll
+            for (int k = 0; k < S::DQK / 32; ++k) f.x[r][k] = src[r] ? load_elt(src[r], 32 * k, 0) : 0.f;
     }
 #pragma unroll
     for (int k = 0; k < S::DQK / 64; ++k) f.phase[k] = lane + 32 * k < A.r.half ? A.r.phase[lane + 32 * k] : 0;
@@ -271,13 +278,16 @@ template <class S> __device__ __forceinline__ void load_rows(const Args &A, cons
             const int apart = A.r.inter ? 1 : A.r.half;
             int head = R0 % A.G, pos = c.s.len - c.s.cnt + R0 / A.G;
             float2 cs = rope_cs(f.phase[k], pos);
+            float u[S::ROWS], v[S::ROWS];
 #pragma unroll
             for (int r = 0; r < S::ROWS; ++r) {
-                if (R0 + r >= rows) break;
-                float *x = a + r * S::QS, *y = x + apart;
-                const float u = *x * A.r.mscale, v = *y * A.r.mscale;
-                *x = u * cs.x - v * cs.y;
-                *y = v * cs.x + u * cs.y;
+                u[r] = a[r * S::QS] * A.r.mscale;
+                v[r] = a[r * S::QS + apart] * A.r.mscale;
+            }
+#pragma unroll
+            for (int r = 0; r < S::ROWS; ++r) {
+                a[r * S::QS] = u[r] * cs.x - v[r] * cs.y;
+                a[r * S::QS + apart] = v[r] * cs.x + u[r] * cs.y;
                 if (++head == A.G) {                     // the next row is another token's
                     head = 0;
                     cs = rope_cs(f.phase[k], ++pos);
@@ -359,7 +369,7 @@ template <class S> __device__ __forceinline__ void load_rows(const Args &A, cons
 __device__ __forceinline__ int order8(int r) { return r ^ (r >> 2); }
 
 // One tile.  j0: its first token; bad: strips on pages outside the pool.  MASK: some row does not see all of it.
-template <class S, bool MASK> __device__ __forceinline__ void tile(const Args &A, const char *const (&stage)[S::TS], int j0, int len, unsigned bad, State<S> &st) {
+template <class S, bool MASK> __device__ __forceinline__ void tile(const Args &A, const char *stage, int j0, int len, unsigned bad, State<S> &st) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int ta = S::I4 ? order8(g) : g;                // this lane's tokens of a strip: ta and ta + 8
     float p[S::NS][S::RT][2];
@@ -369,7 +379,7 @@ template <class S, bool MASK> __device__ __forceinline__ void tile(const Args &A
     for (int rt = 0; rt < S::RT; ++rt) top[rt] = -INFINITY;
 #pragma unroll
     for (int s = 0; s < S::NS; ++s) {
-        const char *sp = stage[s / S::SS] + s % S::SS * S::STRIP;
+        const char *sp = stage + s * S::STRIP;
         const int ja = j0 + 16 * s + ta;
         if constexpr (S::I4) {
             float ps[S::RT][2], pm[S::RT][2];
@@ -514,7 +524,7 @@ template <class S, bool MASK> __device__ __forceinline__ void tile(const Args &A
             uint32_t lo0[S::NS], hi0[S::NS], lo1[S::NS], hi1[S::NS];     // nibbles 0-3 and 4-7 of a token pair, a half each
 #pragma unroll
             for (int s = 0; s < S::NS; ++s) {
-                const char *pl = stage[s / S::SS] + s % S::SS * S::STRIP + (S::PK + v) * kPlaneI4 + 4 * g;
+                const char *pl = stage + s * S::STRIP + (S::PK + v) * kPlaneI4 + 4 * g;
                 const int a = order8(2 * t) * 32, c = order8(2 * t + 1) * 32;
                 const uint32_t wa = *reinterpret_cast<const uint32_t *>(pl + a), wb = *reinterpret_cast<const uint32_t *>(pl + c);
                 const uint32_t wc = *reinterpret_cast<const uint32_t *>(pl + 256 + a), wd = *reinterpret_cast<const uint32_t *>(pl + 256 + c);
@@ -561,7 +571,7 @@ template <class S, bool MASK> __device__ __forceinline__ void tile(const Args &A
 #pragma unroll
                 for (int s = 0; s < S::NS; ++s) {
                     uint32_t a[4];
-                    ldmatrix4t(a, tc::smem_u32(stage[s / S::SS] + s % S::SS * S::STRIP + (S::PK + v) * kPlaneBf16 + tok * 128 +
+                    ldmatrix4t(a, tc::smem_u32(stage + s * S::STRIP + (S::PK + v) * kPlaneBf16 + tok * 128 +
                                                (((2 * j + odd) ^ (tok & 7)) << 4)));
                     if (MASK) {
                         // rows past the length hold anything; a value that is not finite goes to 0 here and makes
@@ -642,34 +652,33 @@ template <class S> __device__ __forceinline__ void write_record(State<S> &st, bo
 struct Segment {                                        // what a warp leaves for the join
     int key;                                            // units before the (sequence, head, row block)'s tiles, -1: nothing
     int last;                                           // its last tile's unit
-    int begins, ends;                                   // whether it holds its first and its last tile
-    int n, h, rb, pad;
+    int flags;                                          // 1: it holds its first tile, 2: its last
+    int h, rb, q0, rows;                                // key head, row block, first token and rows of the sequence
+    int pad;
 };
 
 // The row of units.  A (sequence, head, row block) takes `extra` units for its start and end (rows loaded, rotated and
 // split; sums joined and stored) and one for each tile; with short sequences the former are most of the work.
 struct Line {
     unsigned extra;
-    const unsigned *pre, *pre_tiles;                    // [THREADS + 1]: units and tiles before each thread's sequences
+    const unsigned *pre;                                // [THREADS + 1]: units before each thread's sequences
     int per;                                            // sequences of a thread
-    // Where unit u lies: its sequence, the (head, row block) in it, the unit in that one; returns the tiles before u.
-    template <class S> __device__ __forceinline__ unsigned find(const Args &A, unsigned u, int threads, Seq &s, int &n, unsigned &pair, unsigned &at) const {
+    // Where unit u lies: its sequence, the (head, row block) in it, the unit in that one.
+    template <class S> __device__ __forceinline__ void find(const Args &A, unsigned u, int threads, Seq &s, int &n, unsigned &pair, unsigned &at) const {
         int slot = -1;
         for (int i = threadIdx.x & 31; i < threads; i += 32)
             if (pre[i] <= u && u < pre[i + 1]) slot = i;
         slot = __reduce_max_sync(0xffffffffu, slot);
-        unsigned rest = u - pre[slot], tiles = pre_tiles[slot];
+        unsigned rest = u - pre[slot];
         n = slot * per;
         s = load_seq<S>(A, n);
         unsigned have;
         while (rest >= (have = s.pairs(A.P.heads) * (s.tiles + extra))) {
             rest -= have;
-            tiles += s.pairs(A.P.heads) * s.tiles;
             s = load_seq<S>(A, ++n);
         }
         pair = rest / (s.tiles + extra);
         at = rest - pair * (s.tiles + extra);
-        return tiles + pair * s.tiles + (at > extra ? at - extra : 0);
     }
 };
 
@@ -694,13 +703,11 @@ template <class S> __global__ void __launch_bounds__(S::WARPS * 32, 1) attend_ke
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem);                                   // [W][STAGES]
     Segment *segs = reinterpret_cast<Segment *>(smem + 1024);                              // [2 W]
     unsigned *pre = reinterpret_cast<unsigned *>(smem + 1024 + 2 * W * sizeof(Segment));   // [THREADS + 1]
-    unsigned *pre_tiles = pre + THREADS + 1;                                               // [THREADS + 1]
     char *mine = smem + S::COMMON + warp * S::WARP_BYTES;
     float *rec0 = reinterpret_cast<float *>(mine + S::STAGES * S::STAGE), *rec1 = rec0 + S::RECORD;
     const uint32_t bar = tc::smem_u32(bars + warp * S::STAGES);
     __shared__ unsigned part_sum[W], part_tiles[W];
     __shared__ unsigned arrived;
-    __shared__ float weights[2 * W][S::ROWS], sums[2 * W][S::ROWS];
 
     // ---- the call's units, and where each thread's sequences begin in their row
     const int per = (A.P.N + THREADS - 1) / THREADS;
@@ -741,100 +748,95 @@ template <class S> __global__ void __launch_bounds__(S::WARPS * 32, 1) attend_ke
     }
     // (a call with few tiles has a warp for each, and no runs to balance)
     const unsigned extra = tiles > 2 * gridDim.x * W ? S::EXTRA : 0, U = tiles + extra * pairs;
-    pre_tiles[threadIdx.x] = run_tiles - own_tiles;
     pre[threadIdx.x] = run_tiles - own_tiles + extra * (run - own);
-    if (threadIdx.x == 0) {
-        pre[THREADS] = U;
-        pre_tiles[THREADS] = tiles;
-    }
+    if (threadIdx.x == 0) pre[THREADS] = U;
     __syncthreads();
     if (U == 0) return;
     // few units: as few CTAs as give every warp one, so that fewer joins leave the CTA
     const unsigned C = min(gridDim.x, (U + W - 1) / W);
     if (blockIdx.x >= C) return;
     const Split split(U, C * W);
-    const Line line{extra, pre, pre_tiles, per};
+    const Line line{extra, pre, per};
     const unsigned gw = blockIdx.x * W + warp, u0 = split.begin(gw), u1 = split.begin(gw + 1);
-    int total = 0;                                       // this warp's tiles
-    unsigned pair = 0, at = 0, base = 0;                 // base: units before its first (sequence, head, row block)
     Cursor pc;                                           // runs ahead: the tile whose copies come next
+    unsigned base = 0;                                   // units before its (sequence, head, row block)
     if (u1 > u0) {
-        const unsigned first = line.find<S>(A, u0, THREADS, pc.s, pc.n, pair, at);
-        Seq q;
-        int n;
-        unsigned p2, a2;
-        total = (int)((u1 < U ? line.find<S>(A, u1, THREADS, q, n, p2, a2) : tiles) - first);
+        unsigned pair, at;
+        line.find<S>(A, u0, THREADS, pc.s, pc.n, pair, at);
         base = u0 - at;
         pc.t = at > extra ? (int)(at - extra) : 0;
-    }
-    if (total > 0) {
         pc.h = (int)(pair / pc.s.rbs);
         pc.rb = (int)(pair - pc.h * pc.s.rbs);
         pc.enter<S>(A);
+    }
+    // (a run may hold nothing but a block's start)
+    if (u1 > u0 && base + extra + pc.t < u1) {
+        unsigned pbase = base;                           // pc's
         Cursor cc = pc;
-        const int stages = total * S::TS;
-        int issued = 0;                                  // stages
-        unsigned bad_strips = 0;                         // SS bits a stage
-        // lane s: strip s of a tile, its page (-1 bad, -2 none), its place in it and the head; a tile's pages are asked for
-        // while the one before it is issued
+        int issued = 0;                                  // tiles
+        unsigned bad_strips = 0;                         // NS bits a stage
+        // lane s: strip s of a tile, its page (not looked at before the copy: the load is on its way), its place in the
+        // page (-1: no strip) and the head; a tile's pages are asked for while the one before it is issued
         struct Where { int page, at, h; } now, next;
-        auto look_up = [&](bool more) {
-            next.page = -2;
+        bool ahead = true;                               // pc is in the run
+        auto look_up = [&]() {
+            next.at = -1;
             const int strip = pc.t * S::NS + lane;
-            if (more && lane < S::NS && 16 * strip < pc.most) {
+            if (ahead && lane < S::NS && 16 * strip < pc.most) {
                 const int j = A.per_page_inv ? (int)__umulhi((unsigned)strip, A.per_page_inv) : strip;
-                const int pg = A.P.table[(int64_t)pc.n * A.P.max_pages + j];
-                next.page = pg >= 0 && pg < A.P.num_pages ? pg : -1;
+                next.page = A.P.table[(int64_t)pc.n * A.P.max_pages + j];
                 next.at = strip - j * A.per_page;
                 next.h = pc.h;
             }
         };
-        auto next_tile = [&](int tiles) {                // tiles: how many were looked up before this one
+        bool ready = true;                               // `now` is a tile of the run
+        auto next_tile = [&]() {
             now = next;
-            if (tiles < total) pc.advance<S>(A);
-            look_up(tiles < total);
+            ready = ahead;
+            if (ahead) {
+                const unsigned then = pbase + pc.s.tiles + extra;
+                if (pc.t == pc.s.tiles - 1) pbase = then;
+                // the last unit of the run, or nothing but the next block's start after it
+                ahead = (pc.t == pc.s.tiles - 1 ? pbase + extra : pbase + extra + pc.t + 1) < u1;
+                if (ahead) pc.advance<S>(A);
+            }
+            look_up();
         };
         auto issue = [&]() {
-            const int s = issued % S::STAGES, sub = issued % S::TS;
-            const bool here = lane / S::SS == sub;
-            const unsigned have = __ballot_sync(0xffffffffu, here && now.page >= 0), bad = __ballot_sync(0xffffffffu, here && now.page == -1) >> (sub * S::SS);
-            bad_strips = (bad_strips & ~(((1u << S::SS) - 1) << (s * S::SS))) | (bad << (s * S::SS));
+            const int s = issued % S::STAGES;
+            const bool good = now.at >= 0 && now.page >= 0 && now.page < A.P.num_pages;
+            const unsigned have = __ballot_sync(0xffffffffu, good), bad = __ballot_sync(0xffffffffu, now.at >= 0 && !good);
+            bad_strips = (bad_strips & ~(((1u << S::NS) - 1) << (s * S::NS))) | (bad << (s * S::NS));
             if (lane == 0) tc::mbar_arrive_expect_tx(bar + 8 * s, __popc(have) * S::STRIP);
             __syncwarp();
             // strips of one page lie together: the first of them brings all
-            const int first = sub * S::SS;
-            if (here && now.page >= 0 && (lane == first || now.at == 0)) {
+            if (good && (lane == 0 || now.at == 0)) {
                 const int run = min(A.per_page - now.at, __popc(have >> lane));
-                tc::bulk_g2s(tc::smem_u32(mine + s * S::STAGE + (lane - first) * S::STRIP),
+                tc::bulk_g2s(tc::smem_u32(mine + s * S::STAGE + lane * S::STRIP),
                              A.P.pool + (int64_t)now.page * A.P.page_bytes + (int64_t)now.h * A.P.block_bytes + (int64_t)now.at * S::STRIP,
                              run * S::STRIP, bar + 8 * s);
             }
             ++issued;
-            if (issued % S::TS == 0) next_tile(issued / S::TS + 1);
+            next_tile();
         };
         Rows<S> rows;
-        look_up(true);
+        look_up();
         fetch_rows<S>(A, cc, rows);                      // under the pages' and the copies' latency
-        next_tile(1);
-        while (issued < stages && issued < S::STAGES) issue();
+        next_tile();
+        while (ready && issued < S::STAGES) issue();
 
         State<S> st;
         bool dead = false;                               // a wait ran out: nothing more is issued or used
         bool begins = cc.t == 0, fresh = true;           // fresh: the rows of a new block are on their way
-        for (int k = 0; k < total; ++k) {
+        for (int k = 0;; ++k) {
             if (fresh) load_rows<S>(A, cc, rows, rec1, st);
             fresh = false;
-            const char *stage[S::TS];
-            unsigned bad = 0;
-#pragma unroll
-            for (int i = 0; i < S::TS; ++i) {
-                const int f = k * S::TS + i, s = f % S::STAGES;
-                stage[i] = mine + s * S::STAGE;
-                bad |= ((bad_strips >> (s * S::SS)) & ((1u << S::SS) - 1)) << (i * S::SS);
-                if (!dead && !tc::mbar_wait_bounded(bar + 8 * s, (f / S::STAGES) & 1, kWaitTries)) {
-                    dead = true;
-                    if (lane == 0) atomicOr(A.status, 2u);
-                }
+            const int s = k % S::STAGES;
+            const char *stage = mine + s * S::STAGE;
+            const unsigned bad = (bad_strips >> (s * S::NS)) & ((1u << S::NS) - 1);
+            if (!dead && !tc::mbar_wait_bounded(bar + 8 * s, (k / S::STAGES) & 1, kWaitTries)) {
+                dead = true;
+                if (lane == 0) atomicOr(A.status, 2u);
             }
             dead = __any_sync(0xffffffffu, dead);
             const int j0 = cc.t * S::TILE;
@@ -843,35 +845,36 @@ template <class S> __global__ void __launch_bounds__(S::WARPS * 32, 1) attend_ke
                 else tile<S, false>(A, stage, j0, cc.s.len, 0, st);
             }
             __syncwarp();
-            if (!dead) {
-#pragma unroll
-                for (int i = 0; i < S::TS; ++i)
-                    if (issued < stages) issue();
-            }
-            if (cc.t < cc.s.tiles - 1 && k < total - 1) {
+            const bool ends = cc.t == cc.s.tiles - 1, stop = k + 1 == issued && !ready;
+            if (!dead && ready) issue();
+            if (!ends && !stop) {
                 ++cc.t;
                 continue;
             }
-            const bool ends = cc.t == cc.s.tiles - 1, lost = cc.s.len < 0;
-            Cursor done = cc;
-            if (k < total - 1) {
+            const bool lost = cc.s.len < 0;
+            const Segment done{(int)(base + extra), (int)(base + extra) + cc.s.tiles - 1, (begins ? 1 : 0) | (ends ? 2 : 0), cc.h, cc.rb,
+                               cc.s.q0, cc.s.cnt * A.G, 0};
+            const bool last = stop || dead;              // (a dead warp leaves its run: its outputs are invalid)
+            if (!last) {
+                base += cc.s.tiles + extra;
                 cc.advance<S>(A);
                 fetch_rows<S>(A, cc, rows);
             }
-            if (begins && ends) {
+            if (done.flags == 3) {
                 write_record<S>(st, lost, rec1);
+#pragma unroll 1
                 for (int x = lane; x < S::ROWS * S::DV / 4; x += 32) {
-                    const int r = x / (S::DV / 4), ch = 4 * (x - r * (S::DV / 4));
-                    store4<S>(A, done, r, ch, *reinterpret_cast<const float4 *>(rec1 + 2 * S::ROWS + r * S::DV + ch), rec1[S::ROWS + r]);
+                    const int r = x / (S::DV / 4), ch = 4 * (x - r * (S::DV / 4)), R = done.rb * S::ROWS + r;
+                    if (R < done.rows)
+                        store4(A, S::DV, done.q0, done.h, R, ch, *reinterpret_cast<const float4 *>(rec1 + 2 * S::ROWS + r * S::DV + ch), rec1[S::ROWS + r]);
                 }
                 __syncwarp();
             } else {
                 write_record<S>(st, lost, begins ? rec1 : rec0);
-                if (lane == 0)
-                    segs[2 * warp + (begins ? 1 : 0)] = Segment{(int)(base + extra), (int)(base + extra) + done.s.tiles - 1, begins, ends, done.n, done.h, done.rb, 0};
+                if (lane == 0) segs[2 * warp + (begins ? 1 : 0)] = done;
             }
+            if (last) break;
             begins = fresh = true;
-            base += done.s.tiles + extra;
         }
         if (dead)                                        // copies in flight land before their memory goes
             for (int k = 0; k < issued; ++k)
@@ -879,71 +882,72 @@ template <class S> __global__ void __launch_bounds__(S::WARPS * 32, 1) attend_ke
     }
     __syncthreads();
 
-    // ---- join the warps' records; those of (sequence, head, row block)s that reach into other CTAs go on
+    // ---- join the warps' records, a (sequence, head, row block)'s run of them by one warp; what reaches into other CTAs
+    // goes on to the workspace
+    static_assert(2 * W <= 32, "a lane for each record");
     auto record = [&](int y) {
         return reinterpret_cast<const float *>(smem + S::COMMON + (y >> 1) * S::WARP_BYTES + S::STAGES * S::STAGE) + (y & 1) * S::RECORD;
     };
-    // a record's weight under the maximum of its run, and the run's sum (kept at each of its records)
-    for (int x = threadIdx.x; x < 2 * W * S::ROWS; x += THREADS) {
-        const int y = x / S::ROWS, r = x - y * S::ROWS, key = segs[y].key;
-        if (key < 0) continue;
-        float top = -INFINITY, l = 0.f;
-#pragma unroll 4
-        for (int z = 0; z < 2 * W; ++z)
-            if (segs[z].key == key) top = fmaxf(top, record(z)[r]);
-        weights[y][r] = weight(record(y)[r], top);
-#pragma unroll 4
-        for (int z = 0; z < 2 * W; ++z)
-            if (segs[z].key == key) l = fmaf(weight(record(z)[r], top), record(z)[S::ROWS + r], l);
-        sums[y][r] = l;
-    }
-    __syncthreads();
-    Segment out[2];                                      // runs that reach out of the CTA, the first and the last one
-    out[0].key = out[1].key = -1;
+    const int key = lane < 2 * W ? segs[lane].key : -1;
+    const unsigned same = __match_any_sync(0xffffffffu, key);
+    const unsigned heads = __ballot_sync(0xffffffffu, key >= 0 && lane == __ffs(same) - 1);    // first records of runs
     float *const my_partial = A.partial + (size_t)blockIdx.x * 2 * S::RECORD;
-    for (int i = 0; i < 2 * W;) {
-        const int key = segs[i].key;
-        if (key < 0) { ++i; continue; }
-        int j = i + 1, last = i;
-        for (; j < 2 * W && (segs[j].key < 0 || segs[j].key == key); ++j)
-            if (segs[j].key == key) last = j;
-        const Segment head = segs[i];
-        const bool begins = head.begins != 0, whole = begins && segs[last].ends != 0;
-        Cursor c;
-        c.n = head.n; c.h = head.h; c.rb = head.rb; c.t = 0;
-        if (whole) c.s = load_seq<S>(A, c.n);
+    // a warp's item: 32 pieces of 4 channels of a run, in one row (or two of 64 channels)
+    constexpr int PIECES = S::DV / 4, PARTS = S::ROWS * PIECES / 32;
+    int part = 0;
+    unsigned left = heads;
+    for (int i = 0; part < PARTS && heads; ++i) {        // the runs' first pieces before their second ones: late rows may be empty
+        const int head = __ffs(left) - 1, x = 32 * part + lane;
+        left &= left - 1;
+        if (left == 0) {
+            left = heads;
+            ++part;
+        }
+        if (i % W != warp) continue;
+        const int r = x / PIECES, ch = 4 * (x - r * PIECES);
+        const unsigned members = __shfl_sync(0xffffffffu, same, head);
+        const Segment sg = segs[head];
+        const int R = sg.rb * S::ROWS + r;
+        if (sg.rb * S::ROWS + (x - lane) / PIECES >= sg.rows) continue;
+        const bool begins = sg.flags & 1, whole = begins && (segs[31 - __clz(members)].flags & 2);
         float *dst = my_partial + (begins ? S::RECORD : 0);
-        for (int x = threadIdx.x; x < S::ROWS * S::DV / 4; x += THREADS) {
-            const int r = x / (S::DV / 4), ch = 4 * (x - r * (S::DV / 4));
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        // in the records' order, the maximum first
+        float top = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int y0 = head, y1 = 31 - __clz(members);
 #pragma unroll 4
-            for (int y = i; y <= last; ++y) {
-                if (segs[y].key < 0) continue;
-                const float f = weights[y][r];
-                const float4 v = *reinterpret_cast<const float4 *>(record(y) + 2 * S::ROWS + r * S::DV + ch);
+        for (int y = y0; y <= y1; ++y)
+            if ((members >> y) & 1) top = fmaxf(top, record(y)[r]);
+#pragma unroll 4
+        for (int y = y0; y <= y1; ++y)
+            if ((members >> y) & 1) {
+                const float *rec = record(y);
+                const float f = weight(rec[r], top);
+                const float4 v = *reinterpret_cast<const float4 *>(rec + 2 * S::ROWS + r * S::DV + ch);
+                l = fmaf(f, rec[S::ROWS + r], l);
                 o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
             }
-            if (whole) {
-                store4<S>(A, c, r, ch, o, sums[i][r]);
-            } else {
-                *reinterpret_cast<float4 *>(dst + 2 * S::ROWS + r * S::DV + ch) = o;
-                if (ch == 0) {
-                    float top = -INFINITY;
-                    for (int y = i; y <= last; ++y)
-                        if (segs[y].key == key) top = fmaxf(top, record(y)[r]);
-                    dst[r] = top;
-                    dst[S::ROWS + r] = sums[i][r];
-                }
+        if (R >= sg.rows) continue;
+        if (whole) {
+            store4(A, S::DV, sg.q0, sg.h, R, ch, o, l);
+        } else {
+            *reinterpret_cast<float4 *>(dst + 2 * S::ROWS + r * S::DV + ch) = o;
+            if (ch == 0) {
+                dst[r] = top;
+                dst[S::ROWS + r] = l;
             }
         }
-        if (!whole) out[begins ? 1 : 0] = head;
-        i = j;
     }
+    // a run that reaches out is the CTA's first (it began earlier) or its last (it goes on)
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
-        const Segment o2 = i ? out[1] : out[0];
-        if (o2.key < 0) continue;
-        const unsigned first = split.owner(o2.key) / W, last = split.owner(o2.last) / W;
+        if (heads == 0) break;
+        const int head = i ? 31 - __clz(heads) : __ffs(heads) - 1;
+        const Segment sg = segs[head];
+        const unsigned members = __shfl_sync(0xffffffffu, same, head);
+        const bool begins = sg.flags & 1, ends = segs[31 - __clz(members)].flags & 2;
+        if ((begins && ends) || begins != (i == 1)) continue;
+        const unsigned first = split.owner(sg.key) / W, last = split.owner(sg.last) / W;
         __threadfence();
         __syncthreads();
         if (threadIdx.x == 0) arrived = atomicAdd(A.counters + first, 1u);
@@ -951,25 +955,23 @@ template <class S> __global__ void __launch_bounds__(S::WARPS * 32, 1) attend_ke
         if (arrived != last - first) continue;
         __threadfence();
         if (threadIdx.x == 0) A.counters[first] = 0;     // as the next call needs it
-        Cursor c;
-        c.n = o2.n; c.h = o2.h; c.rb = o2.rb; c.t = 0;
-        c.s = load_seq<S>(A, c.n);
         auto rec = [&](unsigned b) { return A.partial + ((size_t)b * 2 + (b == first ? 1 : 0)) * S::RECORD; };
         for (int x = threadIdx.x; x < S::ROWS * S::DV / 4; x += THREADS) {
-            const int r = x / (S::DV / 4), ch = 4 * (x - r * (S::DV / 4));
+            const int r = x / (S::DV / 4), ch = 4 * (x - r * (S::DV / 4)), R = sg.rb * S::ROWS + r;
+            if (R >= sg.rows) continue;
             float top = -INFINITY;
 #pragma unroll 8
             for (unsigned b = first; b <= last; ++b) top = fmaxf(top, __ldcg(rec(b) + r));
             float l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 4
             for (unsigned b = first; b <= last; ++b) {
                 const float f = weight(__ldcg(rec(b) + r), top);
                 const float4 v = __ldcg(reinterpret_cast<const float4 *>(rec(b) + 2 * S::ROWS + r * S::DV + ch));
                 l = fmaf(f, __ldcg(rec(b) + S::ROWS + r), l);
                 o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
             }
-            store4<S>(A, c, r, ch, o, l);
+            store4(A, S::DV, sg.q0, sg.h, R, ch, o, l);
         }
     }
 }
