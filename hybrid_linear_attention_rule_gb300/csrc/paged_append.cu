@@ -1,21 +1,24 @@
 // paged_append.cu -- new key and value rows into the paged cache (keys rotated on the way), and rows
 // back out of it as values, on sm_103a.
 //
-// Both move every element once and are bound by HBM.  A unit is 8 channels of one (token, head): one
-// 16-byte piece (bf16 in) or two (fp32 in); the 8 lanes of a group hold one plane's 64 channels of a token, whose
-// minimum and maximum three shuffles find.  A CTA takes kTokens tokens (fewer when there are
-// few), finds their sequence, position and page once (a 32-way search of cu_seqlens, one warp a
-// token) and forms their cosines and sines once for all heads.
+// Both move every element once; what they have to beat is their own arithmetic, some 15 instructions a channel.  Four
+// lanes hold a group (64 channels of a token and head), 16 channels each; a lane keeps its head and channels and
+// goes through its CTA's tokens, so that addresses, the rotation's layout and its table's place are worked out once.  Lanes of
+// a warp hold the same channels of eight heads, so that keys that turn and values that do not seldom share one.
+// A CTA finds its tokens' sequences and pages once (a 32-way search of cu_seqlens, one warp a token) and forms their cosines
+// and sines once for all heads.  Pairs of channels go through packed FP32 instructions (fma.rn.f32x2).
 //
 // 4-bit rounding.  The stored values are those of the definition in exact arithmetic, so that what
 // the cache holds does not hang on how FP32 rounds:
-//   - A group of channels that are not turned is exact in FP32: m = fp16(min) is one rounding, and a
-//     code is decided by the sign of (x - m) - (c + 1/2) s, where (c + 1/2) s has at most 16 bits: one
-//     fma and, only next to a tie, the rounding error of x - m.
-//   - A group that holds turned channels carries FP32 errors of up to kSlack of its largest
-//     magnitude.  Where m, s or a code lies that close to a rounding border (about one group in
-//     1000, by the borders' spacing) the group goes to the warp, which repeats it in double, two channels a
-//     lane, with the angle's sine and cosine in double.  The same path settles a scale next to a border.
+//   - The plain path rounds t = (x - m) / s to the nearest whole number by FP32 and keeps the largest distance to it; with
+//     that below 1/2 by more than FP32's error every code is right.  It also wants fp16's roundings of the minimum and
+//     the scale to be clear, and codes that need no clamp (a scale that is a normal fp16 number, a minimum whose rounding is
+//     small next to it).
+//   - Else, in a group of channels that are not turned (exact in FP32: m is one rounding, s was clear), a code is decided
+//     by the sign of (x - m) - (c + 1/2) s, where (c + 1/2) s has at most 16 bits: one fma and, next to a tie, the
+//     rounding error of x - m.  Ties are common there (bf16 values): one group in 30.
+//   - Else (turned channels, FP32 errors of up to kSlack of the pair; about one group in 500) the warp repeats the group in
+//     double, two channels a lane, with the angle's sine and cosine in double.
 #include <math.h>
 
 #include "paged.cuh"
@@ -24,10 +27,11 @@ namespace k3kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 4;                 // units a thread has in flight
+constexpr int kGroups = kThreads / 4;     // groups of a CTA
 constexpr int kTokens = 16;               // most tokens of a CTA
-// bound on the FP32 error of a turned channel, relative to the largest |x| + |y| of the group's pairs: three
-// roundings of the rotation and the error of the cosine and sine, 2^-22 in all, doubled
+// Bound on the FP32 error of a turned channel, relative to the largest of the pair's two channels (times mscale).  The cosine
+// and sine are off by at most 1.7e-7 each: 2^-24 from sincospif (1 ulp below 1), 4.7e-8 from the angle's own rounding
+// (at most 1/8 turn, 24 bits), 2^-24 from the factor mscale; two products add 2^-24 of one and 2^-24 sqrt(2) of the sum.
 constexpr float kSlack = 4.8e-7f;
 
 struct AppendArgs {
@@ -37,12 +41,12 @@ struct AppendArgs {
     int T;
     Rope r;
     int tokens;                           // tokens of a CTA
-    int parts;                            // CTAs that share the same tokens
-    int units;                            // units per token: heads * planes * 8
+    int parts;                            // CTAs that share the same tokens: kGroups of their heads * planes groups each
 };
 
 struct Place {                            // where a CTA's token goes; page < 0: nowhere
-    int n, pos, page;
+    int64_t at;                           // its strip in (page, head 0)'s block: bytes from the pool's start
+    int pos, page;
 };
 
 // Sequence of token t: the last n with cu[n] <= t; each round looks at 32 entries at once.
@@ -66,7 +70,7 @@ __device__ __forceinline__ void find_places(const Paged &P, const int32_t *cu, i
         const int t = t0 + i;
         const int n = cu ? find_seq(cu, P.N, t, lane) : t;
         if (lane == 0) {
-            Place w{n, -1, -1};
+            Place w{0, -1, -1};
             int b = t, e = t + 1;
             if (cu) seq_bounds(cu, n, T, b, e);
             const int len = paged_len(P, n);
@@ -74,32 +78,76 @@ __device__ __forceinline__ void find_places(const Paged &P, const int32_t *cu, i
             if (len >= 0 && t >= b && t < e && pos >= 0) {
                 w.pos = (int)pos;
                 w.page = paged_page(P, n, w.pos);
+                w.at = (int64_t)w.page * P.page_bytes + (int64_t)(w.pos % P.page_size / kStrip) * P.strip_bytes;
             }
             place[i] = w;
         }
     }
 }
 
-__device__ __forceinline__ char *plane_at(const Paged &P, const Place &w, int head, int plane, int plane_bytes) {
-    const int in_page = w.pos % P.page_size;
-    return P.pool + (int64_t)w.page * P.page_bytes + (int64_t)head * P.block_bytes +
-           (int64_t)(in_page / kStrip) * P.strip_bytes + plane * plane_bytes;
+// packed pairs of FP32
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pk(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 up(F2 x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// three-way maximum and minimum; a NaN stays
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
-template <typename T, bool VEC> __device__ __forceinline__ void load8(const T *p, float (&x)[8]) {
-    if constexpr (VEC && sizeof(T) == 2) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// 8 channels as they lie in memory
+template <typename T, bool VEC> struct Raw {
+    uint32_t w[2 * sizeof(T)];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (VEC) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float((e & 1) ? (u[e / 2] & 0xffff0000u) : (u[e / 2] << 16));
-    } else if constexpr (VEC) {
-        const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    } else {
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+                const uint4 x = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+                w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
+            }
+        } else if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = load_elt(p, e, sizeof(T) == 2);
+            for (int i = 0; i < 4; ++i)
+                w[i] = reinterpret_cast<const uint16_t *>(p)[2 * i] | (uint32_t)reinterpret_cast<const uint16_t *>(p)[2 * i + 1] << 16;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+        }
     }
-}
+    __device__ __forceinline__ F2 pair(int i) const {
+        if constexpr (sizeof(T) == 2) return pk(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        else return pk(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    }
+};
 
 // channel c's place in the rotation: its pair, its partner's channel and whether it is the second of the two
 struct Turn { int pair, partner; bool second; };
@@ -145,172 +193,275 @@ template <typename T> __device__ __noinline__ void group_in_double(const T *src,
         lo = fmin(lo, __shfl_xor_sync(0xffffffffu, lo, o));
         hi = fmax(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
-    const double m = half_sat(lo), s = half_sat(fmax(hi - m, 0.0) / 15.0);
+    const double m = half_sat(lo), range = fmax(hi - m, 0.0);
+    // fp16(range / 15): FP32's quotient is off by less than half a step of fp16, so the result is its rounding or the value next
+    // to it; 15 times the value between two neighbours is exact, and the comparison decides (a tie to the even one)
+    const float guess = half_sat((float)range * (1.f / 15.f));
+    const unsigned bits = __half_as_ushort(__float2half_rn(guess));
+    double s = guess;
+    const double above = (double)__half2float(__ushort_as_half((unsigned short)(bits + 1))), below = (double)__half2float(__ushort_as_half((unsigned short)(bits - 1)));
+    const double up_at = fma(-7.5, s + above, range), down_at = fma(-7.5, s + below, range);     // range - 15 (s + neighbour) / 2
+    if (bits < 0x7bff && (up_at > 0.0 || (up_at == 0.0 && (bits & 1)))) s = above;
+    else if (bits > 0 && (down_at < 0.0 || (down_at == 0.0 && (bits & 1)))) s = below;
     unsigned byte = 0;
+    const float inv = s > 0.0 ? 1.f / (float)s : 0.f;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        const double c = s > 0.0 ? fmin(fmax(rint((x[e] - m) / s), 0.0), 15.0) : 0.0;
-        byte |= (unsigned)c << (4 * e);
+        // FP32's quotient is within 1/4 of the exact one (or beyond the clamp): the code is f or f + 1 by the sign of
+        // (x - m) - (f + 1/2) s, f its whole part less 1/4
+        const double d = x[e] - m;
+        const float f = fminf(fmaxf(rintf((float)d * inv - 0.5f), 0.f), 14.f);
+        const double diff = fma(-((double)f + 0.5), s, d);
+        const unsigned code = s > 0.0 ? (unsigned)f + (diff > 0.0 || (diff == 0.0 && ((int)f & 1)) ? 1u : 0u) : 0u;
+        byte |= code << (4 * e);
     }
     reinterpret_cast<uint8_t *>(plane)[row * 32 + lane] = (uint8_t)byte;
     if (lane == 0) reinterpret_cast<__half2 *>(plane + 512)[row] = __halves2half2(__double2half(s), __double2half(m));
 }
 
+// How a lane's 8 channels c .. c + 7 turn.
+enum Mode { kStill, kPairs, kFirst, kSecond, kMixed };     // not; neighbours; as first or second halves; channel by channel
+__device__ __forceinline__ Mode mode_of(const Rope &r, int c, bool vec) {
+    const int end = r.off + r.dim;
+    if (c >= end || c + 8 <= r.off) return kStill;
+    const bool inside = vec && c >= r.off && c + 8 <= end;
+    if (inside && r.inter && ((c - r.off) & 7) == 0) return kPairs;
+    if (inside && !r.inter && (r.half & 7) == 0 && ((c - r.off) & 7) == 0) return c - r.off < r.half ? kFirst : kSecond;
+    return kMixed;
+}
+
 template <typename T, bool VEC, bool I4>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs A) {
-    extern __shared__ float2 cs[];                        // [tokens][dim/2]
+__global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_constant__ AppendArgs A) {
+    extern __shared__ __align__(16) float table[];        // [tokens][dim/2 cosines, then as many sines], rows of a multiple of 4
     __shared__ Place place[kTokens];
     const Paged &P = A.P;
     const int part = (int)(blockIdx.x % A.parts);
     const int t0 = (int)(blockIdx.x / A.parts) * A.tokens, n = min(A.tokens, A.T - t0);
     find_places(P, A.cu, A.T, t0, n, place);
+    // this lane's group: plane-major, so that a warp holds one plane of several heads
+    const int kplanes = P.dqk / 64, lane4 = threadIdx.x & 3;
+    const int gi = part * kGroups + (threadIdx.x >> 2);
+    const bool inside = gi < P.heads * P.planes;
+    const int plane = inside ? gi / P.heads : 0, head = inside ? gi - plane * P.heads : 0;
+    const bool key = plane < kplanes;
+    const int c0 = 64 * (key ? plane : plane - kplanes), c = c0 + 16 * lane4;
+    const View &src = key ? A.k : A.v;
+    const T *row = reinterpret_cast<const T *>(src.p) + (int64_t)t0 * src.ts + (int64_t)head * src.hs;
+    const bool turned = key && A.r.dim > 0 && c0 < A.r.off + A.r.dim && c0 + 64 > A.r.off;   // some channel of the group
+    const Mode mode0 = turned ? mode_of(A.r, c, VEC) : kStill, mode1 = turned ? mode_of(A.r, c + 8, VEC) : kStill;
+    const bool any_turned = __any_sync(0xffffffffu, turned);
+    const int tab_half = (A.r.half + 3) & ~3, tab_row = 2 * tab_half;
+    char *dst = P.pool + (int64_t)head * P.block_bytes + plane * (I4 ? kPlaneI4 : kPlaneBf16);
+    // the first token's rows are on their way before its angles are known
+    Raw<T, VEC> r0, r1, y0, y1;
+    auto fetch = [&](int t) {
+        const T *p = row + (int64_t)t * src.ts;
+        r0.load(p + c);
+        r1.load(p + c + 8);
+        if (mode0 == kFirst || mode0 == kSecond) y0.load(p + (mode0 == kFirst ? c + A.r.half : c - A.r.half));
+        if (mode1 == kFirst || mode1 == kSecond) y1.load(p + 8 + (mode1 == kFirst ? c + A.r.half : c - A.r.half));
+    };
+    if (inside) fetch(0);
     __syncthreads();
     for (int i = threadIdx.x; i < n * A.r.half; i += kThreads) {
-        const int t = i / A.r.half;
-        const float2 v = rope_cs(A.r.phase[i - t * A.r.half], place[t].pos);
-        cs[i] = make_float2(v.x * A.r.mscale, v.y * A.r.mscale);
+        const int t = i / A.r.half, p = i - t * A.r.half;
+        const float2 v = rope_cs(A.r.phase[p], place[t].pos);
+        table[t * tab_row + p] = v.x * A.r.mscale;
+        table[t * tab_row + tab_half + p] = v.y * A.r.mscale;
     }
     __syncthreads();
-    const int kplanes = P.dqk / 64, total = n * A.units;
-    // every lane of a warp runs every round: a group that needs the double path gets the whole warp
-    for (int base = part * kThreads; base < total; base += A.parts * kThreads) {
-        const int i = base + threadIdx.x;
-        const bool inside = i < total;
-        const int t = inside ? i / A.units : 0;
-        const int e = inside ? i - t * A.units : 0;
-        const int g = e & 7, hp = e >> 3, head = hp / P.planes, plane = hp - head * P.planes;
-        const bool key = plane < kplanes;
+#pragma unroll 1
+    for (int t = 0; t < n; ++t) {
         const Place w = place[t];
-        const bool live = inside && w.page >= 0;
-        const int c0 = key ? plane * 64 : (plane - kplanes) * 64;
-        const View &src = key ? A.k : A.v;
-        const T *row = reinterpret_cast<const T *>(src.p) + (int64_t)(t0 + t) * src.ts + (int64_t)head * src.hs;
-        float x[8];
+        F2 x[8];
+        float mag = 0.f;                                  // largest channel of the lane's pairs that turn
+        auto turn = [&](const Raw<T, VEC> &r, const Raw<T, VEC> &y, Mode mode, int cr, F2 *out) {
+            if (mode == kStill || mode == kMixed) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) x[q] = 0.f;
-        bool turned = false;                              // some channel of the group is
-        float mag = 0.f;                                  // largest |x| + |y| of the pairs
-        const int c = c0 + 8 * g, rend = A.r.off + A.r.dim;
-        if (live) {
-            load8<T, VEC>(row + c, x);
-            if (key && A.r.dim > 0) {
-                turned = c0 < rend && c0 + 64 > A.r.off;
-                if (c < rend && c + 8 > A.r.off) {
-                    const float2 *tab = cs + t * A.r.half;
-                    // runs of 8 channels that turn together with 8 partners; else channel by channel
-                    const bool whole = VEC && c >= A.r.off && c + 8 <= rend && (A.r.inter ? ((c - A.r.off) & 1) == 0 : (A.r.half & 7) == 0 && ((c - A.r.off) & 7) == 0);
-                    if (whole && A.r.inter) {
+                for (int q = 0; q < 4; ++q) out[q] = r.pair(q);
+                if (mode == kStill) return;
+                float v[8];                               // some channels turn, or the rows are not aligned: one at a time, from memory
+                const T *p = row + (int64_t)t * src.ts;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const float2 a = tab[(c - A.r.off) / 2 + q];
-                            mag = fmaxf(mag, fabsf(x[2 * q]) + fabsf(x[2 * q + 1]));
-                            const float u = x[2 * q] * a.x - x[2 * q + 1] * a.y, v = x[2 * q + 1] * a.x + x[2 * q] * a.y;
-                            x[2 * q] = u;
-                            x[2 * q + 1] = v;
-                        }
-                    } else if (whole) {
-                        const bool second = c - A.r.off >= A.r.half;
-                        const int pair = c - A.r.off - (second ? A.r.half : 0);
-                        float y[8];
-                        load8<T, VEC>(row + (second ? c - A.r.half : c + A.r.half), y);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const float2 a = tab[pair + q];
-                            mag = fmaxf(mag, fabsf(x[q]) + fabsf(y[q]));
-                            x[q] = second ? x[q] * a.x + y[q] * a.y : x[q] * a.x - y[q] * a.y;
-                        }
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            if (c + q < A.r.off || c + q >= rend) continue;
-                            const Turn tn = turn_of(A.r, c + q);
-                            const float2 a = tab[tn.pair];
-                            const float y = load_elt(row, tn.partner, sizeof(T) == 2);
-                            // its own value again: a neighbour's turn must not read what this loop wrote
-                            const float z = load_elt(row, c + q, sizeof(T) == 2);
-                            mag = fmaxf(mag, fabsf(z) + fabsf(y));
-                            x[q] = tn.second ? z * a.x + y * a.y : z * a.x - y * a.y;
-                        }
-                    }
+                for (int q = 0; q < 8; ++q) {
+                    v[q] = load_elt(p, cr + q, sizeof(T) == 2);
+                    if (cr + q < A.r.off || cr + q >= A.r.off + A.r.dim) continue;
+                    const Turn tn = turn_of(A.r, cr + q);
+                    const float u = load_elt(p, tn.partner, sizeof(T) == 2);
+                    const float cs = table[t * tab_row + tn.pair], sn = table[t * tab_row + tab_half + tn.pair];
+                    mag = fmaxf(mag, fmaxf(fabsf(v[q]), fabsf(u)));
+                    v[q] = tn.second ? v[q] * cs + u * sn : v[q] * cs - u * sn;
                 }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) out[q] = pk(v[2 * q], v[2 * q + 1]);
+                return;
             }
-        }
-        const int r16 = w.pos & (kStrip - 1);
-        if constexpr (!I4) {
-            if (live) {
-                uint32_t o[4];
+            const int i = cr - A.r.off, p = mode == kPairs ? i / 2 : mode == kFirst ? i : i - A.r.half;
+            const float *tc = table + t * tab_row + p, *ts = tc + tab_half;
+            if (mode == kPairs) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * q], x[2 * q + 1]);
-                    o[q] = *reinterpret_cast<const uint32_t *>(&b);
+                    const F2 a = r.pair(q);
+                    const float2 b = up(a);
+                    mag = fmaxf(mag, fmaxf(fabsf(b.x), fabsf(b.y)));
+                    out[q] = fma2(a, pk(tc[q], tc[q]), mul2(pk(b.y, b.x), pk(-ts[q], ts[q])));
                 }
-                *reinterpret_cast<uint4 *>(plane_at(P, w, head, plane, kPlaneBf16) + r16 * 128 + ((g ^ (r16 & 7)) << 4)) =
-                    make_uint4(o[0], o[1], o[2], o[3]);
+            } else {
+                const F2 sg = mode == kFirst ? pk(-1.f, -1.f) : pk(1.f, 1.f);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const F2 a = r.pair(q), b = y.pair(q);
+                    const float2 fa = up(a), fb = up(b), cs = *reinterpret_cast<const float2 *>(tc + 2 * q), sn = *reinterpret_cast<const float2 *>(ts + 2 * q);
+                    mag = fmaxf(mag, fmaxf(fmaxf(fabsf(fa.x), fabsf(fa.y)), fmaxf(fabsf(fb.x), fabsf(fb.y))));
+                    out[q] = fma2(a, pk(cs.x, cs.y), mul2(mul2(b, sg), pk(sn.x, sn.y)));
+                }
+            }
+        };
+        if (w.page < 0) {                                 // (the CTA agrees on it)
+            if (inside && t + 1 < n) fetch(t + 1);
+            continue;
+        }
+        if (inside) {
+            turn(r0, y0, mode0, c, x);
+            turn(r1, y1, mode1, c + 8, x + 4);
+            if (t + 1 < n) fetch(t + 1);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) x[q] = 0;
+        }
+        char *pl = dst + w.at;
+        const int r16 = w.pos & (kStrip - 1);
+        if constexpr (!I4) {
+            if (inside) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float2 v = up(x[4 * h + q]);
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+                        o[q] = *reinterpret_cast<const uint32_t *>(&b);
+                    }
+                    *reinterpret_cast<uint4 *>(pl + r16 * 128 + (((2 * lane4 + h) ^ (r16 & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
             }
         } else {
-            float lo = x[0], hi = x[0], sum = 0.f;        // sum: NaN when the group has a NaN or an infinity
+            float2 v = up(x[0]);
+            float lo = v.x, hi = v.x;
+            lo = min3(lo, v.y, v.y);
+            hi = max3(hi, v.y, v.y);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                lo = fminf(lo, x[q]);
-                hi = fmaxf(hi, x[q]);
-                sum = fmaf(x[q], 0.f, sum);
+            for (int q = 1; q < 8; ++q) {
+                v = up(x[q]);
+                lo = min3(lo, v.x, v.y);
+                hi = max3(hi, v.x, v.y);
             }
 #pragma unroll
-            for (int o = 1; o < 8; o <<= 1) {
-                lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-                hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-                sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, o));
+            for (int o = 1; o < 4; o <<= 1) {
+                const float a = __shfl_xor_sync(0xffffffffu, lo, o), b = __shfl_xor_sync(0xffffffffu, hi, o);
+                lo = min3(lo, a, a);
+                hi = max3(hi, b, b);
             }
-            const float err = turned ? fabsf(A.r.mscale) * mag * kSlack : 0.f;    // of a channel's value
-            const bool bad = !(sum == 0.f);
+            float err = 0.f;                              // of a channel's value
+            if (any_turned) {
+                mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
+                mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
+                err = turned ? fabsf(A.r.mscale) * mag * kSlack : 0.f;
+            }
+            const bool bad = !(hi - lo < INFINITY);       // a NaN or an infinity (or a range past FP32's)
             const float m = half_sat(lo), range = fmaxf(hi - m, 0.f);
-            const float sraw = range / 15.f, s = half_sat(sraw);
-            // what FP32 leaves open: the minimum, the scale (its own roundings are within 2^-23 of it) and, for
-            // turned channels, the codes
-            bool unsure = err > 0.f && half_unsure(lo, err);
-            unsure = unsure || half_unsure(sraw, fmaf(sraw, 2.4e-7f, err * 0.14f));
-            const float inv = s > 0.f ? 1.f / s : 0.f;
-            const float slack = err * inv;
-            unsigned word = 0;
+            const float sraw = range * (1.f / 15.f), s = half_sat(sraw);
+            // what FP32 leaves open: the minimum, and the scale (its own roundings are within 2^-22 of it)
+            const bool open_scale = half_unsure(sraw, fmaf(sraw, 2.4e-7f, err * 0.14f)) || (err > 0.f && half_unsure(lo, err));
+            float inv;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+            const float nm = -m * inv;
+            const bool normal = s >= 6.2e-5f && s < 65504.f && fmaf(lo, inv, nm) >= -0.45f;
+            // whole numbers next to t = x / s - m / s, and the largest distance to them
+            constexpr float kMagic = 12582912.f;          // 1.5 * 2^23: adding it rounds to a whole number
+            const F2 inv2 = pk(inv, inv), nm2 = pk(nm, nm), magic = pk(kMagic, kMagic), unmagic = pk(-kMagic, -kMagic);
+            const F2 minus = pk(-1.f, -1.f);
+            float away = 0.f;
+            F2 cd[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                const float d = x[q] - m;
-                const float f = fminf(fmaxf(floorf(d * inv), 0.f), 14.f);
-                const float half = (f + 0.5f) * s;        // exact: 5 bits times 11
-                float diff = fmaf(-1.f, half, d);         // sign decides f or f + 1
-                if (err > 0.f) {
-                    unsure = unsure || fabsf(diff) * inv <= slack + 1.5e-7f * (f + 1.f);
-                } else if (fabsf(diff) <= 1e-6f * fabsf(half)) {
-                    const float back = x[q] - d, lost = (x[q] - (d + back)) + (back - m);   // x - m = d + lost, exactly
-                    diff += lost;
-                }
-                const bool up = diff > 0.f || (diff == 0.f && ((int)f & 1));
-                word |= (s > 0.f ? (unsigned)f + (up ? 1u : 0u) : 0u) << (4 * q);
+                const F2 tt = fma2(x[q], inv2, nm2);
+                cd[q] = add2(add2(tt, magic), unmagic);
+                const float2 r = up(fma2(cd[q], minus, tt));
+                away = fmaxf(away, fmaxf(fabsf(r.x), fabsf(r.y)));
             }
-            const unsigned open = __ballot_sync(0xffffffffu, unsure && !bad && live);
-            if (live) {
-                char *pl = plane_at(P, w, head, plane, kPlaneI4);
-                const unsigned mine = (open >> (threadIdx.x & 24)) & 0xffu;
-                if (!mine) {
-                    reinterpret_cast<uint32_t *>(pl)[r16 * 8 + g] = bad ? 0u : word;
-                    if (g == 0) {
-                        const __half2 pr = bad ? __halves2half2(__ushort_as_half(0x7e00), __ushort_as_half(0x7e00))
-                                               : __halves2half2(__float2half_rn(s), __float2half_rn(m));
-                        reinterpret_cast<__half2 *>(pl + 512)[r16] = pr;
+            // t's own error, t below 15.1: 2^-23 of t from inv, 2^-24 of t from the fma, 2^-24 of m / s from nm
+            const float window = fmaf(fabsf(nm), 1.2e-7f, 3e-6f) + err * inv;
+            const bool plain = !bad && normal && !open_scale && away < 0.5f - window;
+            uint2 word;
+            {   // four codes to 16 bits: sums of whole numbers below 2^16
+                float h[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float2 a = up(cd[2 * q]), b = up(cd[2 * q + 1]);
+                    h[q] = fmaf(fmaf(fmaf(b.y, 16.f, b.x), 16.f, a.y), 16.f, a.x) + 8388608.f;
+                }
+                word.x = __byte_perm(__float_as_uint(h[0]), __float_as_uint(h[1]), 0x5410);
+                word.y = __byte_perm(__float_as_uint(h[2]), __float_as_uint(h[3]), 0x5410);
+            }
+            __half2 pr = __halves2half2(__float2half_rn(s), __float2half_rn(m));
+            const unsigned gmask = 0xfu << (threadIdx.x & 28);
+            const unsigned rest = __ballot_sync(0xffffffffu, inside && !plain);
+            unsigned open = 0;
+            if (rest) {
+                if (rest & gmask) {
+                    if (bad) {
+                        word = make_uint2(0, 0);
+                        pr = __halves2half2(__ushort_as_half(0x7e00), __ushort_as_half(0x7e00));
+                    } else if (err == 0.f && !open_scale && normal) {
+                        // ties, mostly: only the channels next to a border are looked at again
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            const float2 xv = up(x[q / 2]), cv = up(cd[q / 2]);
+                            const float xq = q & 1 ? xv.y : xv.x, c = q & 1 ? cv.y : cv.x, r = fmaf(xq, inv, nm) - c;
+                            if (fabsf(r) < 0.5f - window) continue;
+                            const float f = r > 0.f ? c : c - 1.f, d = xq - m;
+                            const float back = xq - d, lost = (xq - (d + back)) + (back - m);   // x - m = d + lost, exactly
+                            const float diff = (d - (f + 0.5f) * s) + lost;
+                            const int more = (f < c ? -1 : 0) + (diff > 0.f || (diff == 0.f && ((int)f & 1)) ? 1 : 0);
+                            (q < 8 ? word.x : word.y) += (unsigned)more << (4 * (q & 7));
+                        }
+                    } else if (err == 0.f && !open_scale) {
+                        word = make_uint2(0, 0);
+                        const float iv = s > 0.f ? 1.f / s : 0.f;
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            const float2 xv = up(x[q / 2]);
+                            const float xq = q & 1 ? xv.y : xv.x, d = xq - m;
+                            const float f = fminf(fmaxf(floorf(d * iv), 0.f), 14.f);
+                            const float half = (f + 0.5f) * s;    // exact: 5 bits times 11
+                            float diff = d - half;                // its sign decides f or f + 1
+                            if (fabsf(diff) <= 1e-6f * fabsf(half)) {
+                                const float back = xq - d, lost = (xq - (d + back)) + (back - m);   // x - m = d + lost, exactly
+                                diff += lost;
+                            }
+                            const bool more = diff > 0.f || (diff == 0.f && ((int)f & 1));
+                            const unsigned code = s > 0.f ? (unsigned)f + (more ? 1u : 0u) : 0u;
+                            if (q < 8) word.x |= code << (4 * q);
+                            else word.y |= code << (4 * (q - 8));
+                        }
                     }
                 }
+                open = __ballot_sync(0xffffffffu, inside && (rest & gmask) && !bad && !(err == 0.f && !open_scale));
             }
-            for (int q = 0; q < 32; q += 8) {
-                if (!((open >> q) & 0xffu)) continue;
-                const int ot = __shfl_sync(0xffffffffu, t, q), ohead = __shfl_sync(0xffffffffu, head, q),
-                          oplane = __shfl_sync(0xffffffffu, plane, q);
+            if (inside && !(open & gmask)) {
+                reinterpret_cast<uint2 *>(pl)[r16 * 4 + lane4] = word;
+                if (lane4 == 0) reinterpret_cast<__half2 *>(pl + 512)[r16] = pr;
+            }
+            for (unsigned left = open; left;) {
+                const int at = __ffs(left) - 1;
+                left &= ~(0xfu << (at & 28));
+                const int ohead = __shfl_sync(0xffffffffu, head, at), oplane = __shfl_sync(0xffffffffu, plane, at);
                 const bool okey = oplane < kplanes;
-                const Place ow = place[ot];
                 const View &os = okey ? A.k : A.v;
-                group_in_double<T>(reinterpret_cast<const T *>(os.p) + (int64_t)(t0 + ot) * os.ts + (int64_t)ohead * os.hs,
-                                   (okey ? oplane : oplane - kplanes) * 64, A.r, okey, ow.pos,
-                                   plane_at(P, ow, ohead, oplane, kPlaneI4), ow.pos & (kStrip - 1));
+                group_in_double<T>(reinterpret_cast<const T *>(os.p) + (int64_t)(t0 + t) * os.ts + (int64_t)ohead * os.hs,
+                                   64 * (okey ? oplane : oplane - kplanes), A.r, okey, w.pos,
+                                   P.pool + w.at + (int64_t)ohead * P.block_bytes + oplane * kPlaneI4, r16);
             }
         }
     }
@@ -318,21 +469,32 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 
 // ---- read ------------------------------------------------------------------------------------------
 
-template <typename T, bool VEC> __device__ __forceinline__ void store8(T *p, const float (&x)[8]) {
-    if constexpr (VEC && sizeof(T) == 2) {
+template <typename T, bool VEC> __device__ __forceinline__ void store8(T *p, const F2 (&x)[4]) {
+    if constexpr (sizeof(T) == 2) {
         uint32_t o[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * q], x[2 * q + 1]);
+            const float2 v = up(x[q]);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
             o[q] = *reinterpret_cast<const uint32_t *>(&b);
         }
-        *reinterpret_cast<uint4 *>(p) = make_uint4(o[0], o[1], o[2], o[3]);
-    } else if constexpr (VEC) {
-        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-        *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        if constexpr (VEC) *reinterpret_cast<uint4 *>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+        else
+#pragma unroll
+            for (int q = 0; q < 8; ++q) reinterpret_cast<uint16_t *>(p)[q] = (uint16_t)(o[q / 2] >> (16 * (q & 1)));
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) store_elt(p, e, x[e], sizeof(T) == 2);
+        for (int q = 0; q < 4; ++q) {
+            const float2 v = up(x[q]);
+            if constexpr (VEC) {
+                if (q & 1) continue;
+                const float2 u = up(x[q + 1]);
+                *reinterpret_cast<float4 *>(p + 2 * q) = make_float4(v.x, v.y, u.x, u.y);
+            } else {
+                p[2 * q] = v.x;
+                p[2 * q + 1] = v.y;
+            }
+        }
     }
 }
 
@@ -344,48 +506,69 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
     const int t0 = (int)(blockIdx.x / A.parts) * A.tokens, n = min(A.tokens, A.T - t0);
     find_places(P, A.cu, A.T, t0, n, place);
     __syncthreads();
-    const int kplanes = P.dqk / 64, total = n * A.units;
-    for (int i = part * kThreads + threadIdx.x; i < total; i += A.parts * kThreads) {
-        const int t = i / A.units, e = i - t * A.units;
-        const int g = e & 7, hp = e >> 3, head = hp / P.planes, plane = hp - head * P.planes;
-        const bool key = plane < kplanes;
-        const View &dst = key ? A.k : A.v;
-        if (!dst.p) continue;
+    const int kplanes = P.dqk / 64, lane4 = threadIdx.x & 3;
+    const int gi = part * kGroups + (threadIdx.x >> 2);
+    if (gi >= P.heads * P.planes) return;
+    // plane-fastest here: neighbouring lanes write neighbouring channels
+    const int head = gi / P.planes, plane = gi - head * P.planes;
+    const bool key = plane < kplanes;
+    const View &dst = key ? A.k : A.v;
+    if (!dst.p) return;
+    T *row = reinterpret_cast<T *>(dst.p) + (int64_t)t0 * dst.ts + (int64_t)head * dst.hs + 64 * (key ? plane : plane - kplanes) + 16 * lane4;
+    const char *src = P.pool + (int64_t)head * P.block_bytes + plane * (I4 ? kPlaneI4 : kPlaneBf16);
+    struct Held { uint4 a, b; uint32_t pr; };
+    auto fetch = [&](int t, Held &h) {
         const Place w = place[t];
-        float x[8];
-        if (w.page < 0) {
+        if (w.page < 0) return;
+        const char *pl = src + w.at;
+        const int r16 = w.pos & (kStrip - 1);
+        if constexpr (I4) {
+            const uint2 v = reinterpret_cast<const uint2 *>(pl)[r16 * 4 + lane4];
+            h.a.x = v.x;
+            h.a.y = v.y;
+            h.pr = reinterpret_cast<const uint32_t *>(pl + 512)[r16];
+        } else {
+            h.a = *reinterpret_cast<const uint4 *>(pl + r16 * 128 + (((2 * lane4) ^ (r16 & 7)) << 4));
+            h.b = *reinterpret_cast<const uint4 *>(pl + r16 * 128 + (((2 * lane4 + 1) ^ (r16 & 7)) << 4));
+        }
+    };
+    Held now, next;
+    fetch(0, now);
+#pragma unroll 1
+    for (int t = 0; t < n; ++t) {
+        if (t + 1 < n) fetch(t + 1, next);
+        F2 x[2][4];
+        if (place[t].page < 0) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) x[q] = __int_as_float(0x7fc00000);
-        } else if (I4) {
-            const char *pl = plane_at(P, w, head, plane, kPlaneI4);
-            const int r16 = w.pos & (kStrip - 1);
-            const uint32_t word = reinterpret_cast<const uint32_t *>(pl)[r16 * 8 + g];
-            const float2 pr = __half22float2(reinterpret_cast<const __half2 *>(pl + 512)[r16]);
+            for (int q = 0; q < 8; ++q) x[q / 4][q % 4] = pk(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000));
+        } else if constexpr (I4) {
+            const float2 pr = __half22float2(*reinterpret_cast<const __half2 *>(&now.pr));
+            const F2 s = pk(pr.x, pr.x), m = pk(pr.y, pr.y), off = pk(-8388608.f, -8388608.f);
             // s code is exact (15 bits), so the value is rounded once, then to the output's type
 #pragma unroll
-            for (int q = 0; q < 8; ++q) x[q] = fmaf((float)((word >> (4 * q)) & 15u), pr.x, pr.y);
+            for (int q = 0; q < 8; ++q) {
+                const uint32_t w = (q < 4 ? now.a.x : now.a.y) >> (8 * (q & 3));
+                const F2 c = pk(__uint_as_float((w & 15u) | 0x4B000000u), __uint_as_float(((w >> 4) & 15u) | 0x4B000000u));   // 2^23 + code
+                x[q / 4][q % 4] = fma2(add2(c, off), s, m);
+            }
         } else {
-            const int r16 = w.pos & (kStrip - 1);
-            load8<__nv_bfloat16, true>(reinterpret_cast<const __nv_bfloat16 *>(plane_at(P, w, head, plane, kPlaneBf16) + r16 * 128 +
-                                                                               ((g ^ (r16 & 7)) << 4)), x);
+            const uint32_t u[8] = {now.a.x, now.a.y, now.a.z, now.a.w, now.b.x, now.b.y, now.b.z, now.b.w};
+#pragma unroll
+            for (int q = 0; q < 8; ++q) x[q / 4][q % 4] = pk(__uint_as_float(u[q] << 16), __uint_as_float(u[q] & 0xffff0000u));
         }
-        const int c = (key ? plane * 64 : (plane - kplanes) * 64) + 8 * g;
-        store8<T, VEC>(reinterpret_cast<T *>(dst.p) + (int64_t)(t0 + t) * dst.ts + (int64_t)head * dst.hs + c, x);
+        T *p = row + (int64_t)t * dst.ts;
+        store8<T, VEC>(p, x[0]);
+        store8<T, VEC>(p + 8, x[1]);
+        now = next;
     }
 }
 
-// Tokens of a CTA and CTAs of a token: about kUnits units a thread, more tokens to a CTA (up to
-// kTokens) once all SMs have several CTAs, so that the places' search is shared.
+// Tokens of a CTA: as many (up to kTokens) as leave about 8 CTAs for each SM; the search for their places, their angles and
+// a lane's addresses are shared by them.
 void plan(AppendArgs &A, unsigned &grid) {
-    A.units = A.P.heads * A.P.planes * 8;
-    const long long total = (long long)A.T * A.units, full = (long long)kThreads * kUnits;
-    const long long want = total / (full * 152 * 4);              // four CTAs of work for each SM
-    int tokens = (int)(full / A.units > 1 ? full / A.units : 1);
-    if (want > 1) tokens = (int)(tokens * (want > kTokens ? kTokens : want));
-    A.tokens = tokens > kTokens ? kTokens : tokens;
-    const long long per = (long long)A.tokens * A.units;
-    A.parts = per > full * 4 ? (int)((per + full * 4 - 1) / (full * 4)) : 1;
-    if (total < full * 152) A.parts = (int)((per + kThreads - 1) / kThreads);   // few rows: a unit a thread
+    A.parts = (A.P.heads * A.P.planes + kGroups - 1) / kGroups;
+    const long long tokens = (long long)A.T * A.parts / (152 * 8);
+    A.tokens = tokens < 1 ? 1 : tokens > kTokens ? kTokens : (int)tokens;
     grid = (unsigned)(((long long)A.T + A.tokens - 1) / A.tokens * A.parts);
 }
 
@@ -409,7 +592,7 @@ cudaError_t launch_paged_append(const k3mla_paged_cache *c, const k3mla_view *k,
                        : (i4 ? append_kernel<__nv_bfloat16, false, true> : append_kernel<__nv_bfloat16, false, false>);
     else fn = vec ? (i4 ? append_kernel<float, true, true> : append_kernel<float, true, false>)
                   : (i4 ? append_kernel<float, false, true> : append_kernel<float, false, false>);
-    fn<<<grid, kThreads, (size_t)A.tokens * A.r.half * sizeof(float2), s>>>(A);
+    fn<<<grid, kThreads, (size_t)A.tokens * 2 * ((A.r.half + 3) & ~3) * sizeof(float), s>>>(A);
     count_launch();
     return cudaGetLastError();
 }
