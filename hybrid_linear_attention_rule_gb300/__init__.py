@@ -470,25 +470,34 @@ _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 _FORMATS = {"bf16": CACHE_BF16, "i4": CACHE_I4}
 
 
+# These calls are short on the GPU, so their marshalling is kept short too: few tensor attributes, the raw stream, argument
+# structures that the handles keep.
+
+def _raw_stream(stream, t):
+    """The stream's address; by default the current one of the tensor's device."""
+    return torch._C._cuda_getCurrentRawStream(t.device.index) if stream is None else stream.cuda_stream
+
+
 def _view(t, what, d=None):
     """A [tokens, heads, channels] CUDA tensor of any token and head strides, its channels contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"k3mla: {what} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError("k3mla: tensors must live on a CUDA device (no CPU path exists)")
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+    st = t.stride()
+    if len(st) != 3 or (st[2] != 1 and t.shape[2] > 1):
         raise ValueError(f"k3mla: {what} must be [tokens, heads, channels] with contiguous channels")
     if d is not None and t.shape[2] != d:
         raise ValueError(f"k3mla: {what} has {t.shape[2]} channels, not {d}")
-    return _View(t.data_ptr(), t.stride(0), t.stride(1))
+    return _View(t.data_ptr(), st[0], st[1])
 
 
 def _i32(t, what, shape):
     """A contiguous int32 CUDA tensor of the given shape, or None; its address."""
     if t is None:
         return None
-    if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != shape:
-        raise ValueError(f"k3mla: {what} must be a contiguous int32 CUDA tensor of shape {shape}")
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"k3mla: {what} must be a contiguous int32 CUDA tensor of shape {tuple(shape)}")
     return t.data_ptr()
 
 
@@ -527,50 +536,47 @@ def rope_table(dim, theta=10000.0, offset=0, layout="half", scaling="none", fact
     return RopeTable(phase.to(device), int(dim), int(offset), layout, mscale)
 
 
-def _rope_views(x, y, what):
-    if x is None:
-        return None, None, 0
-    if y.dtype != x.dtype or y.shape[0] != x.shape[0] or y.device != x.device:
-        raise ValueError(f"k3mla: {what} and its output differ in type, tokens or device")
-    return _view(x, what), _view(y, what, x.shape[2]), x.shape[1]
+def _rope_call(name, q, q_out, k, k_out, k_heads_out, positions, table, stream, *shared):
+    """Checks that belong to tensors, then the library's call."""
+    T, hq, d = q.shape
+    dt = q.dtype
+    if q_out.shape != q.shape or q_out.dtype != dt:
+        raise ValueError("k3mla: the first output has another shape or type than its input")
+    kv = ko = None
+    hk = 0
+    if k is not None:
+        hk = k.shape[1]
+        if k.shape[0] != T or k.shape[2] != d or k.dtype != dt:
+            raise ValueError("k3mla: the two inputs differ in tokens, channels or type")
+        if k_out.shape != (T, hk if k_heads_out is None else k_heads_out, d) or k_out.dtype != dt:
+            raise ValueError("k3mla: the second output has the wrong shape or type")
+        kv, ko = _view(k, "k"), _view(k_out, "k_out")
+    qv, qo = _view(q, "q"), _view(q_out, "q_out")
+    pos = _i32(positions, "positions", (T,))
+    st = getattr(_lib or load_library(), name)(qv, qo, hq, kv, ko, hk, *shared, _dtype(q), pos, T, d, table._args,
+                                               _raw_stream(stream, q))
+    if st:
+        _check(name, st)
 
 
 def k3mla_rope(q, q_out, k, k_out, positions, table, stream=None):
     """Rotate q [T, Hq, d] -> q_out and k [T, Hk, d] -> k_out (None: no k); an output may be its input."""
-    if k is not None and (k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2] or k.dtype != q.dtype):
-        raise ValueError("k3mla: q and k differ in tokens, channels or type")
-    if tuple(q_out.shape) != tuple(q.shape) or (k is not None and tuple(k_out.shape) != tuple(k.shape)):
-        raise ValueError("k3mla: an output has another shape than its input")
-    qv, qo, hq = _rope_views(q, q_out, "q")
-    kv, ko, hk = _rope_views(k, k_out, "k")
-    st = load_library().k3mla_rope(qv, qo, hq, kv, ko, hk, _dtype(q), _i32(positions, "positions", (q.shape[0],)),
-                                   q.shape[0], q.shape[2], table._args, _stream(stream))
-    _check("k3mla_rope", st)
+    _rope_call("k3mla_rope", q, q_out, k, k_out, None, positions, table, stream)
 
 
 def k3mla_rope_backward(dq_out, dq, dk_out, dk, k_shared, positions, table, stream=None):
     """The gradient of k3mla_rope; k_shared: k was one head for all, dk [T, 1, d] is the sum over heads."""
-    if dk_out is not None and (dk_out.shape[0] != dq_out.shape[0] or dk_out.shape[2] != dq_out.shape[2]
-                               or dk_out.dtype != dq_out.dtype):
-        raise ValueError("k3mla: dq_out and dk_out differ in tokens, channels or type")
-    if tuple(dq.shape) != tuple(dq_out.shape):
-        raise ValueError("k3mla: dq has another shape than dq_out")
-    if dk_out is not None and dk.shape[1] != (1 if k_shared else dk_out.shape[1]):
-        raise ValueError("k3mla: dk has the wrong number of heads")
-    qv, qo, hq = _rope_views(dq_out, dq, "dq_out")
-    kv, ko, hk = _rope_views(dk_out, dk, "dk_out")
-    st = load_library().k3mla_rope_backward(qv, qo, hq, kv, ko, hk, int(bool(k_shared)), _dtype(dq_out),
-                                            _i32(positions, "positions", (dq_out.shape[0],)), dq_out.shape[0],
-                                            dq_out.shape[2], table._args, _stream(stream))
-    _check("k3mla_rope_backward", st)
+    _rope_call("k3mla_rope_backward", dq_out, dq, dk_out, dk, 1 if k_shared else None, positions, table, stream,
+               1 if k_shared else 0)
 
 
 def rope(q, positions, table, k=None, out=None, stream=None):
     """q [T, Hq, d] (and k [T, Hk, d]) turned by positions int32 [T].  Returns q's rotation, or (q's, k's);
     `out` (a tensor, or a pair with k) may be the inputs themselves.  Inputs may be strided views."""
     if out is None:
-        out = _empty(q.shape, q.dtype, q.device, stream)
-        out = out if k is None else (out, _empty(k.shape, k.dtype, k.device, stream))
+        dev = q.device
+        out = _empty(q.shape, q.dtype, dev, stream)
+        out = out if k is None else (out, _empty(k.shape, k.dtype, dev, stream))
     qo, ko = (out, None) if k is None else out
     k3mla_rope(q, qo, k, ko, positions, table, stream)
     return out
@@ -627,18 +633,21 @@ class PagedCache:
 def _packing(cache, cu_seqlens, cu_seqlens_host):
     if cu_seqlens_host is not None and cu_seqlens_host.numel() != cache.N + 1:
         raise ValueError("k3mla: cu_seqlens_host has another length")
-    return _i32(cu_seqlens, "cu_seqlens", (cache.N + 1,)), _host_i32(cu_seqlens_host, "cu_seqlens_host")
+    return (None if cu_seqlens is None else _i32(cu_seqlens, "cu_seqlens", (cache.N + 1,)),
+            None if cu_seqlens_host is None else _host_i32(cu_seqlens_host, "cu_seqlens_host"))
 
 
 def k3mla_paged_append(cache, k_new, v_new, cu_seqlens=None, cu_seqlens_host=None, rope=None, stream=None):
     """Append rows k_new [T, heads, dqk], v_new [T, heads, dv] (see include/k3kda.h); rope: a RopeTable or None."""
-    if k_new.shape[:2] != v_new.shape[:2] or k_new.shape[1] != cache.heads or k_new.dtype != v_new.dtype:
+    T = k_new.shape[0]
+    if v_new.shape[0] != T or k_new.shape[1] != cache.heads or v_new.shape[1] != cache.heads or k_new.dtype != v_new.dtype:
         raise ValueError("k3mla: k_new and v_new differ, or have other heads than the cache")
     cu, cuh = _packing(cache, cu_seqlens, cu_seqlens_host)
-    st = load_library().k3mla_paged_append(cache._args, _view(k_new, "k_new", cache.dqk), _view(v_new, "v_new", cache.dv),
-                                           _dtype(k_new), cu, cuh, k_new.shape[0], None if rope is None else rope._args,
-                                           _stream(stream))
-    _check("k3mla_paged_append", st)
+    st = (_lib or load_library()).k3mla_paged_append(
+        cache._args, _view(k_new, "k_new", cache.dqk), _view(v_new, "v_new", cache.dv), _dtype(k_new), cu, cuh, T,
+        None if rope is None else rope._args, _raw_stream(stream, k_new))
+    if st:
+        _check("k3mla_paged_append", st)
 
 
 def k3mla_paged_read(cache, k_out, v_out, cu_seqlens=None, cu_seqlens_host=None, stream=None):
@@ -649,10 +658,11 @@ def k3mla_paged_read(cache, k_out, v_out, cu_seqlens=None, cu_seqlens_host=None,
     if some.shape[1] != cache.heads:
         raise ValueError("k3mla: the outputs have other heads than the cache")
     cu, cuh = _packing(cache, cu_seqlens, cu_seqlens_host)
-    st = load_library().k3mla_paged_read(cache._args, None if k_out is None else _view(k_out, "k_out", cache.dqk),
-                                         None if v_out is None else _view(v_out, "v_out", cache.dv), _dtype(some), cu, cuh,
-                                         some.shape[0], _stream(stream))
-    _check("k3mla_paged_read", st)
+    st = (_lib or load_library()).k3mla_paged_read(
+        cache._args, None if k_out is None else _view(k_out, "k_out", cache.dqk),
+        None if v_out is None else _view(v_out, "v_out", cache.dv), _dtype(some), cu, cuh, some.shape[0], _raw_stream(stream, some))
+    if st:
+        _check("k3mla_paged_read", st)
 
 
 paged_append = k3mla_paged_append
@@ -660,8 +670,9 @@ paged_append = k3mla_paged_append
 
 def paged_read(cache, tokens, cu_seqlens=None, out_dtype=torch.bfloat16, stream=None):
     """The last `tokens` packed rows (all sequences together) as values: (k [tokens, heads, dqk], v [tokens, heads, dv])."""
-    k = _empty((tokens, cache.heads, cache.dqk), out_dtype, cache.pool.device, stream)
-    v = _empty((tokens, cache.heads, cache.dv), out_dtype, cache.pool.device, stream)
+    dev = cache.pool.device
+    k = _empty((tokens, cache.heads, cache.dqk), out_dtype, dev, stream)
+    v = _empty((tokens, cache.heads, cache.dv), out_dtype, dev, stream)
     k3mla_paged_read(cache, k, v, cu_seqlens, None, stream)
     return k, v
 
@@ -680,16 +691,18 @@ def k3mla_paged_attend(cache, q, gate, out, workspace, scale, cu_seqlens=None, c
                        stream=None):
     """Attention of the new tokens q [T, Hq, dqk] over the cache (see include/k3kda.h)."""
     T, Hq = q.shape[:2]
-    if gate is not None and (tuple(gate.shape) != (T, Hq, cache.dv) or gate.dtype != q.dtype):
+    want = (T, Hq, cache.dv)
+    if gate is not None and (gate.shape != want or gate.dtype != q.dtype):
         raise ValueError("k3mla: gate is not [tokens, query heads, dv] of q's type")
-    if tuple(out.shape) != (T, Hq, cache.dv):
+    if out.shape != want:
         raise ValueError("k3mla: out is not [tokens, query heads, dv]")
     cu, cuh = _packing(cache, cu_seqlens, cu_seqlens_host)
-    st = load_library().k3mla_paged_attend(cache._args, _view(q, "q", cache.dqk), _dtype(q), Hq, cu, cuh, T, int(max_new),
-                                           None if rope is None else rope._args, scale,
-                                           None if gate is None else _view(gate, "gate"), _ptr(out), _dtype(out),
-                                           _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
-    _check("k3mla_paged_attend", st)
+    st = (_lib or load_library()).k3mla_paged_attend(
+        cache._args, _view(q, "q", cache.dqk), _dtype(q), Hq, cu, cuh, T, int(max_new), None if rope is None else rope._args,
+        scale, None if gate is None else _view(gate, "gate"), _ptr(out), _dtype(out), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _raw_stream(stream, q))
+    if st:
+        _check("k3mla_paged_attend", st)
 
 
 def paged_attend(cache, q, cu_seqlens=None, max_new=None, rope=None, scale=None, gate=None, out=None, out_dtype=None,
