@@ -33,7 +33,7 @@
 namespace k3kda {
 namespace attend {
 
-constexpr int kMaxCtas = 608;                          // partials and counters of a workspace
+constexpr int kMaxCtas = 160;                          // partials and counters of a workspace
 constexpr size_t kHeadBytes = 256 + 4096;              // status word, counters (4 B a CTA)
 constexpr int kMaxRows = 8;
 constexpr unsigned kWaitTries = 1u << 22;              // each try suspends for a while: seconds in all
@@ -59,15 +59,15 @@ template <int DQK_, int DV_, int RT_, bool I4_> struct Shape {
     static constexpr int PK = DQK / 64, PV = DV / 64, PL = PK + PV;
     static constexpr int ROWS = 4 * RT;
     static constexpr int PLANE = I4 ? kPlaneI4 : kPlaneBf16, STRIP = PL * PLANE;
-    static constexpr int NS = I4 ? (PL <= 4 ? 4 : 2) : (PL <= 2 ? 2 : 1);       // strips of a tile
+    static constexpr int NS = I4 ? (PL <= 4 ? 4 : 2) : (PL <= 2 ? 2 : 1);   // strips of a tile
     static constexpr int TILE = NS * kStrip, STAGE = NS * STRIP;
     static constexpr int WARPS = I4 ? (PL <= 4 ? 8 : RT == 1 ? 8 : 4) : (PL <= 4 ? 6 : 4);
     static constexpr int EXTRA = 2;                                             // units of a block's start and end, in tiles
     static constexpr int QS = DQK + 8;                                          // floats between staged rows
     static constexpr int RECORD = ROWS * (DV + 2);                              // floats: m, l, O
     static constexpr int STAGED = ROWS * (QS + PK + 1);                         // floats: rows, their sums and exponents
-    static constexpr int SLOT1 = RECORD > STAGED ? RECORD : STAGED;
-    static constexpr int FIXED = ((RECORD + SLOT1) * 4 + 127) / 128 * 128;      // bytes of a warp beside its ring
+    static constexpr int WORK = RECORD > STAGED ? RECORD : STAGED;
+    static constexpr int FIXED = ((RECORD + WORK) * 4 + 127) / 128 * 128;       // bytes of a warp beside its ring
     static constexpr int COMMON = 1024 + 2 * WARPS * 32 + (WARPS * 32 + 4) * 4; // barriers, segments, prefix sums
     static constexpr int ROOM = (232448 - 256 - COMMON) / WARPS / 128 * 128;
     static constexpr int FIT = (ROOM - FIXED) / STAGE;
@@ -75,7 +75,7 @@ template <int DQK_, int DV_, int RT_, bool I4_> struct Shape {
     static_assert(STAGES >= 2 && STAGES * WARPS * 8 <= 1024 && STAGES * NS <= 32, "ring");
     static constexpr int WARP_BYTES = STAGES * STAGE + FIXED;
     static constexpr int SMEM = COMMON + WARPS * WARP_BYTES;
-    static_assert(STAGE % 128 == 0 || (STAGES * STAGE) % 64 == 0, "alignment");
+    static_assert(STAGES * STAGE >= RECORD * 4 && STAGE % 64 == 0, "the ring holds a record at the end");
 };
 
 // c = (FIRST ? 0 : c) + A B
@@ -350,14 +350,15 @@ template <class S> __device__ __forceinline__ void load_rows(const Args &A, cons
         for (int p = 0; p < S::PK; ++p)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                uint32_t *f = st.qf[rt][p][i];
                 if constexpr (S::I4) {
                     const float *x = row + 64 * p + 16 * t + (i >> 1) * 8 + (i & 1) * 2;
-                    st.qf[rt][p][i][0] = pack_part<true>(x[0] * mul * 16.f, x[4] * mul * 16.f, g & 1);
-                    st.qf[rt][p][i][1] = pack_part<true>(x[1] * mul, x[5] * mul, g & 1);
+                    f[0] = pack_part<true>(x[0] * mul * 16.f, x[4] * mul * 16.f, g & 1);
+                    f[1] = pack_part<true>(x[1] * mul, x[5] * mul, g & 1);
                 } else {
                     const float *x = row + 64 * p + 16 * i + 2 * t;
-                    st.qf[rt][p][i][0] = pack_part<false>(x[0], x[1], g & 1);
-                    st.qf[rt][p][i][1] = pack_part<false>(x[8], x[9], g & 1);
+                    f[0] = pack_part<false>(x[0], x[1], g & 1);
+                    f[1] = pack_part<false>(x[8], x[9], g & 1);
                 }
             }
     }
@@ -396,10 +397,9 @@ template <class S, bool MASK> __device__ __forceinline__ void tile(const Args &A
                     const uint32_t ua = (i < 2 ? wa.x : wa.y) >> (8 * (i & 1)), ub = (i < 2 ? wb.x : wb.y) >> (8 * (i & 1));
 #pragma unroll
                     for (int rt = 0; rt < S::RT; ++rt) {
-                        if (i == 0)
-                            mma<true, true>(c[rt], ua & 0x000F000Fu, ub & 0x000F000Fu, ua & 0x00F000F0u, ub & 0x00F000F0u, st.qf[rt][k][i][0], st.qf[rt][k][i][1]);
-                        else
-                            mma<true, false>(c[rt], ua & 0x000F000Fu, ub & 0x000F000Fu, ua & 0x00F000F0u, ub & 0x00F000F0u, st.qf[rt][k][i][0], st.qf[rt][k][i][1]);
+                        const uint32_t *q = st.qf[rt][k][i];
+                        if (i == 0) mma<true, true>(c[rt], ua & 0x000F000Fu, ub & 0x000F000Fu, ua & 0x00F000F0u, ub & 0x00F000F0u, q[0], q[1]);
+                        else mma<true, false>(c[rt], ua & 0x000F000Fu, ub & 0x000F000Fu, ua & 0x00F000F0u, ub & 0x00F000F0u, q[0], q[1]);
                     }
                 }
 #pragma unroll
@@ -423,7 +423,8 @@ template <class S, bool MASK> __device__ __forceinline__ void tile(const Args &A
                 p[s][rt][1] = fmaf(ps[rt][1], st.fac[rt], pm[rt][1]);
             }
         } else {
-            float c[S::RT][4];
+            constexpr int CH = S::PK;                    // a chain of products for each plane
+            float ch[CH][S::RT][4], c[S::RT][4];
             const int tok = lane & 15, odd = lane >> 4;
 #pragma unroll
             for (int k = 0; k < S::PK; ++k)
@@ -433,12 +434,19 @@ template <class S, bool MASK> __device__ __forceinline__ void tile(const Args &A
                     ldmatrix4(a, tc::smem_u32(sp + k * kPlaneBf16 + tok * 128 + (((2 * i + odd) ^ (tok & 7)) << 4)));
 #pragma unroll
                     for (int rt = 0; rt < S::RT; ++rt) {
-                        if (k + i == 0) mma<false, true>(c[rt], a[0], a[1], a[2], a[3], st.qf[rt][k][i][0], st.qf[rt][k][i][1]);
-                        else mma<false, false>(c[rt], a[0], a[1], a[2], a[3], st.qf[rt][k][i][0], st.qf[rt][k][i][1]);
+                        const uint32_t *q = st.qf[rt][k][i];
+                        if (i == 0) mma<false, true>(ch[k][rt], a[0], a[1], a[2], a[3], q[0], q[1]);
+                        else mma<false, false>(ch[k][rt], a[0], a[1], a[2], a[3], q[0], q[1]);
                     }
                 }
 #pragma unroll
             for (int rt = 0; rt < S::RT; ++rt) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    c[rt][x] = ch[0][rt][x];
+#pragma unroll
+                    for (int k = 1; k < CH; ++k) c[rt][x] += ch[k][rt][x];
+                }
                 // an infinite key: the low part's product may be the opposite infinity
                 p[s][rt][0] = fabsf(c[rt][0]) < INFINITY ? c[rt][0] + c[rt][1] : c[rt][0];
                 p[s][rt][1] = fabsf(c[rt][2]) < INFINITY ? c[rt][2] + c[rt][3] : c[rt][2];
@@ -704,7 +712,8 @@ template <class S> __global__ void __launch_bounds__(S::WARPS * 32, 1) attend_ke
     Segment *segs = reinterpret_cast<Segment *>(smem + 1024);                              // [2 W]
     unsigned *pre = reinterpret_cast<unsigned *>(smem + 1024 + 2 * W * sizeof(Segment));   // [THREADS + 1]
     char *mine = smem + S::COMMON + warp * S::WARP_BYTES;
-    float *rec0 = reinterpret_cast<float *>(mine + S::STAGES * S::STAGE), *rec1 = rec0 + S::RECORD;
+    // a warp's memory: its ring (at the end its last record), its first record, and where rows are prepared and blocks finished
+    float *rec0 = reinterpret_cast<float *>(mine + S::STAGES * S::STAGE), *work = rec0 + S::RECORD;
     const uint32_t bar = tc::smem_u32(bars + warp * S::STAGES);
     __shared__ unsigned part_sum[W], part_tiles[W];
     __shared__ unsigned arrived;
@@ -829,7 +838,7 @@ template <class S> __global__ void __launch_bounds__(S::WARPS * 32, 1) attend_ke
         bool dead = false;                               // a wait ran out: nothing more is issued or used
         bool begins = cc.t == 0, fresh = true;           // fresh: the rows of a new block are on their way
         for (int k = 0;; ++k) {
-            if (fresh) load_rows<S>(A, cc, rows, rec1, st);
+            if (fresh) load_rows<S>(A, cc, rows, work, st);
             fresh = false;
             const int s = k % S::STAGES;
             const char *stage = mine + s * S::STAGE;
@@ -861,16 +870,17 @@ template <class S> __global__ void __launch_bounds__(S::WARPS * 32, 1) attend_ke
                 fetch_rows<S>(A, cc, rows);
             }
             if (done.flags == 3) {
-                write_record<S>(st, lost, rec1);
+                write_record<S>(st, lost, work);
 #pragma unroll 1
                 for (int x = lane; x < S::ROWS * S::DV / 4; x += 32) {
                     const int r = x / (S::DV / 4), ch = 4 * (x - r * (S::DV / 4)), R = done.rb * S::ROWS + r;
                     if (R < done.rows)
-                        store4(A, S::DV, done.q0, done.h, R, ch, *reinterpret_cast<const float4 *>(rec1 + 2 * S::ROWS + r * S::DV + ch), rec1[S::ROWS + r]);
+                        store4(A, S::DV, done.q0, done.h, R, ch, *reinterpret_cast<const float4 *>(work + 2 * S::ROWS + r * S::DV + ch), work[S::ROWS + r]);
                 }
                 __syncwarp();
             } else {
-                write_record<S>(st, lost, begins ? rec1 : rec0);
+                // (a block that begins but does not end here is the run's last: its tiles are read)
+                write_record<S>(st, lost, begins ? reinterpret_cast<float *>(mine) : rec0);
                 if (lane == 0) segs[2 * warp + (begins ? 1 : 0)] = done;
             }
             if (last) break;
@@ -886,7 +896,7 @@ template <class S> __global__ void __launch_bounds__(S::WARPS * 32, 1) attend_ke
     // goes on to the workspace
     static_assert(2 * W <= 32, "a lane for each record");
     auto record = [&](int y) {
-        return reinterpret_cast<const float *>(smem + S::COMMON + (y >> 1) * S::WARP_BYTES + S::STAGES * S::STAGE) + (y & 1) * S::RECORD;
+        return reinterpret_cast<const float *>(smem + S::COMMON + (y >> 1) * S::WARP_BYTES + (y & 1 ? 0 : S::STAGES * S::STAGE));
     };
     const int key = lane < 2 * W ? segs[lane].key : -1;
     const unsigned same = __match_any_sync(0xffffffffu, key);
