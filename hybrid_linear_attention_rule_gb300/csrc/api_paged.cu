@@ -165,7 +165,7 @@ int k3mla_paged_read(const k3mla_paged_cache *cache, const k3mla_view *k_out, co
 
 size_t k3mla_paged_attend_workspace_size(int Hq, int heads, int dqk, int dv) {
     if (heads < 1 || Hq < heads || Hq % heads != 0 || !dims_ok(dqk, dv)) return 0;
-    return paged_attend_workspace(dv);
+    return paged_attend_workspace(dqk, dv);
 }
 
 int k3mla_paged_attend(const k3mla_paged_cache *cache, const k3mla_view *q, int in_dtype, int Hq, const int32_t *cu_seqlens,
@@ -188,7 +188,7 @@ int k3mla_paged_attend(const k3mla_paged_cache *cache, const k3mla_view *q, int 
         if (int e = check_view(gate, in_dtype, T, Hq, false)) return e;
     if (!out) return K3KDA_ERR_INVALID_ARG;
     if (!aligned(out, 16)) return K3KDA_ERR_ALIGNMENT;
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < paged_attend_workspace(cache->dv)) return K3KDA_ERR_WORKSPACE;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < paged_attend_workspace(cache->dqk, cache->dv)) return K3KDA_ERR_WORKSPACE;
     return status_of(launch_paged_attend(cache, q, in_dtype == K3KDA_BF16, Hq, cu_seqlens, T, max_new, rope, scale, gate, out,
                                          out_dtype == K3KDA_BF16, workspace, static_cast<cudaStream_t>(stream)));
 }

@@ -156,7 +156,7 @@ cudaError_t launch_paged_append(const k3mla_paged_cache *c, const k3mla_view *k,
 cudaError_t launch_paged_read(const k3mla_paged_cache *c, const k3mla_view *k, const k3mla_view *v, int bf16, const int32_t *cu,
                               int T, cudaStream_t s);
 // attention over it (csrc/paged_attend.cu)
-size_t paged_attend_workspace(int dv);
+size_t paged_attend_workspace(int dqk, int dv);
 cudaError_t launch_paged_attend(const k3mla_paged_cache *c, const k3mla_view *q, int bf16, int Hq, const int32_t *cu, int T,
                                 int max_new, const k3mla_rope_args *rope, float scale, const k3mla_view *gate, void *out,
                                 int out_bf16, void *ws, cudaStream_t s);

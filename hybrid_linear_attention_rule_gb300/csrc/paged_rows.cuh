@@ -1,0 +1,771 @@
+// paged_rows.cuh -- attention of many new tokens over the paged cache on sm_103a: the same function as
+// paged_attend.cuh for blocks of 128 query rows (prompts in chunks, several tokens checked at once, large head groups), on tcgen05.
+//
+// With this many rows the products bound the time, not the cache's bytes, and a tile's unpacking is shared by 128 rows.
+// A CTA takes a run of 64-key tiles of (sequence, key head, row block)s (the same equal split, with partial results joined by the
+// CTA that finishes last) and its warps pass them on through mbarriers:
+//   producer (1 warp)  bulk copies of whole strips, whose pages it looks up
+//   helpers (8 warps)  4-bit: codes to fp16 operand tiles by one AND (paged_attend.cuh), scales and minima to FP32;
+//                      and, two tiles later, O = O corr + (the tile's product), 128 rows by half the channels a warpgroup, in registers
+//   MMA (1 thread)     S = Q K^T, O_tile = P V, each with Q and P as a high and a low 16-bit part: A = Q from shared memory,
+//                      P from TMEM where it took S's columns
+//   softmax (4 warps)  a row a thread: S out of TMEM, scales, running maximum, weights back in
+// 4-bit: a score group (64 channels) has columns of its own, s = sum_g scale_gj S_g + min_gj sum(q_g) on the way out; a
+// value group has weights of its own, p_j scale_gj, and sum_j p_j min_gj stays in FP32.  bf16 pages hold 64-channel planes
+// in the operands' own 128-byte swizzle (include/k3kda.h), so their strips are copied straight to the operand tiles.
+// What bounds it: per 64 keys and 128 rows 16 (dqk + dv) / 64 products of N = 64 (about 1300 cycles at 128 + 128 channels, those of
+// Q from shared memory at its bandwidth) beside 64 x (17 to 20) instructions of each softmax and 2 x 130 of each helper warp.
+#pragma once
+
+#include "paged_attend.cuh"
+
+namespace k3kda {
+namespace attend {
+
+template <int DQK_, int DV_, bool I4_> struct RowsShape {
+    static constexpr int DQK = DQK_, DV = DV_;
+    static constexpr bool I4 = I4_;
+    static constexpr int PK = DQK / 64, PV = DV / 64, PL = PK + PV;
+    static constexpr int ROWS = 128, NS = 4, TILE = 64, EXTRA = 4;
+    static constexpr int STRIP = PL * (I4 ? kPlaneI4 : kPlaneBf16);
+    static constexpr int GK = I4 ? PK : 1, GV = I4 ? PV : 1;                    // groups of scores, of weights
+    static constexpr int SB = 64 * (GK > GV ? GK : GV);                         // TMEM columns of a tile's scores, then weights
+    static constexpr int OB = 2 * SB + 2 * DV <= 512 ? 2 : 1;                   // buffers of a tile's product
+    static constexpr int COL_O = 2 * SB;
+    static_assert(2 * SB + OB * DV <= 512, "TMEM");
+    static constexpr int WARPS = 16, THREADS = WARPS * 32;                      // 4 softmax, 8 helpers, producer, MMA, 2 idle
+    static constexpr int RECORD = ROWS * (DV + 2);
+    // shared memory, in bytes from a 1024-byte boundary
+    static constexpr int Q_PART = PK * 16384, KV = PL * 8192;
+    static constexpr int RS = I4 ? 2 : 1, RAW = I4 ? NS * STRIP : 0;
+    static constexpr int PARAMS = I4 ? PL * 512 : 0;                            // scale[64], minimum[64] of each plane
+    static constexpr int SMALL = 4 * 128 * 4 + (2 + PV) * 128 * 4 + 128 * (PK + 1) * 4 + 1024 + 64 + (THREADS + 4) * 4;
+    static constexpr int FIT = (232448 - 1024 - 256 - 2 * Q_PART - RS * RAW - SMALL) / (KV + PARAMS + 64);
+    static constexpr int KB = FIT > 4 ? 4 : FIT;                                // operand tiles
+    static_assert(KB >= 2 && KV >= WARPS * DQK * 4 && KB * KV >= ROWS * (DV + 4) * 4, "operand tiles");
+    static constexpr int AT_KV = 2 * Q_PART, AT_RAW = AT_KV + KB * KV, AT_PAR = AT_RAW + RS * RAW, AT_TOP = AT_PAR + KB * PARAMS;
+    static constexpr int AT_CORR = AT_TOP + KB * 64, AT_FIN = AT_CORR + 4 * 128 * 4, AT_INFO = AT_FIN + (2 + PV) * 128 * 4;
+    static constexpr int AT_BAR = AT_INFO + 128 * (PK + 1) * 4, AT_BAD = AT_BAR + 512, AT_PRE = AT_BAD + 64;
+    static constexpr int SMEM = AT_PRE + (THREADS + 4) * 4 + 1024;
+    static_assert(SMEM + 256 <= 232448, "shared memory");
+};
+
+// kind::f16 instruction descriptor with fp16 (or bf16) operands, FP32 sums
+__host__ __device__ constexpr uint32_t idesc16(bool f16, int M, int N, bool b_mn) {
+    return f16 ? tc::idesc_bf16_f32(M, N, false, false, b_mn) & ~((1u << 7) | (1u << 10)) : tc::idesc_bf16_f32(M, N, false, false, b_mn);
+}
+
+// packed pairs of FP32
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pk(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 up(F2 x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Registers of a warpgroup: 128 a thread at launch, 4 x 128 of them in all.  192 + 2 x 128 + 64 = 512: what the last one gives
+// up the first one takes.
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 192;"); }
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 64;"); }
+
+// A bounded wait that also ends when another warp of the CTA has given up.
+__device__ __forceinline__ bool wait_for(uint32_t bar, int parity, volatile int *dead, unsigned *status) {
+    for (unsigned i = 0; i < kWaitTries; ++i) {
+        if (tc::mbar_try_wait(bar, parity & 1)) return true;
+        if ((i & 63) == 63 && *dead) return false;
+    }
+    *dead = 1;
+    atomicOr(status, 2u);
+    return false;
+}
+
+template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(const __grid_constant__ Args A) {
+    extern __shared__ char smem_raw[];
+    char *const sm = reinterpret_cast<char *>(tc::smem_align1024(reinterpret_cast<uint8_t *>(smem_raw)));
+    const uint32_t sm32 = tc::smem_u32(sm);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float *corr = reinterpret_cast<float *>(sm + S::AT_CORR), *fin = reinterpret_cast<float *>(sm + S::AT_FIN);
+    float *info = reinterpret_cast<float *>(sm + S::AT_INFO);                  // [128][PK sums, factor]
+    int *bad_of = reinterpret_cast<int *>(sm + S::AT_BAD);                     // [8] tiles' strips on pages outside the pool, [8] whether values were put to 0
+    unsigned *pre = reinterpret_cast<unsigned *>(sm + S::AT_PRE);
+    __shared__ unsigned part_sum[S::WARPS], part_tiles[S::WARPS], arrived, tslot;
+    __shared__ int dead_flag;
+    volatile int *dead = &dead_flag;
+    // barriers
+    const uint32_t bar = sm32 + S::AT_BAR;
+    const uint32_t raw_full = bar, raw_free = bar + 16, kv_full = bar + 32, kv_free = bar + 64, v_ok = bar + 96, s_full = bar + 128,
+                   p_full = bar + 144, o_full = bar + 160, o_free = bar + 176;
+
+    // ---- the call's units (as in paged_attend.cuh, a CTA a run)
+    const int per = (A.P.N + S::THREADS - 1) / S::THREADS;
+    const int n_lo = min(A.P.N, (int)threadIdx.x * per), n_hi = min(A.P.N, n_lo + per);
+    unsigned own = 0, own_tiles = 0;
+    for (int n = n_lo; n < n_hi; ++n) {
+        const Seq q = load_seq<S>(A, n);
+        own += q.pairs(A.P.heads);
+        own_tiles += q.pairs(A.P.heads) * q.tiles;
+    }
+    unsigned run = own, run_tiles = own_tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned y = __shfl_up_sync(0xffffffffu, run, o), z = __shfl_up_sync(0xffffffffu, run_tiles, o);
+        if (lane >= o) {
+            run += y;
+            run_tiles += z;
+        }
+    }
+    if (lane == 31) {
+        part_sum[warp] = run;
+        part_tiles[warp] = run_tiles;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(raw_full + 8 * i, 1);
+            tc::mbar_init(raw_free + 8 * i, 256);
+            tc::mbar_init(s_full + 8 * i, 1);
+            tc::mbar_init(p_full + 8 * i, 128);
+            tc::mbar_init(o_full + 8 * i, 1);
+            tc::mbar_init(o_free + 8 * i, 256);
+        }
+        for (int i = 0; i < 4; ++i) {
+            tc::mbar_init(kv_full + 8 * i, S::I4 ? 256 : 1);
+            tc::mbar_init(kv_free + 8 * i, 1);
+            tc::mbar_init(v_ok + 8 * i, 256);
+        }
+        tc::fence_mbar_init();
+        dead_flag = 0;
+    }
+    __syncthreads();
+    unsigned pairs = 0, tiles = 0;
+    for (int w = 0; w < S::WARPS; ++w) {
+        run += w < warp ? part_sum[w] : 0;
+        run_tiles += w < warp ? part_tiles[w] : 0;
+        pairs += part_sum[w];
+        tiles += part_tiles[w];
+    }
+    const unsigned extra = S::EXTRA, U = tiles + extra * pairs;
+    pre[threadIdx.x] = run_tiles - own_tiles + extra * (run - own);
+    if (threadIdx.x == 0) pre[S::THREADS] = U;
+    __syncthreads();
+    if (pairs == 0) return;
+    const unsigned C = min(gridDim.x, max(pairs, U / 8));                      // runs of 8 units at least, a block a CTA at most
+    if (blockIdx.x >= C) return;
+    const Split split(U, C);
+    const Line line{extra, pre, per};
+    const unsigned u0 = split.begin(blockIdx.x), u1 = split.begin(blockIdx.x + 1);
+    if (u0 == u1) return;
+    if (warp == 0) {
+        tc::tmem_alloc(tc::smem_u32(&tslot), 512);
+        tc::tmem_relinquish();
+    }
+    Cursor start;
+    unsigned pair, at;
+    line.find<S>(A, u0, S::THREADS, start.s, start.n, pair, at);
+    const unsigned base0 = u0 - at;
+    start.t = at > extra ? (int)(at - extra) : 0;
+    start.h = (int)(pair / start.s.rbs);
+    start.rb = (int)(pair - start.h * start.s.rbs);
+    start.enter<S>(A);
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tb = tslot;
+
+    // The rows of a block: rotated, scaled, split to the operand tiles (warps 0 to 11, each through DQK floats of its own).
+    auto prepare = [&](const Cursor &c) {
+        const int rows = c.s.cnt * A.G, R0 = c.rb * S::ROWS;
+        {
+            float *x = reinterpret_cast<float *>(sm + S::AT_KV) + warp * S::DQK;
+            const int size = A.in_bf16 ? 2 : 4;
+            uint64_t phase[(S::DQK / 2 + 31) / 32];
+#pragma unroll
+            for (int k = 0; k < (S::DQK / 2 + 31) / 32; ++k) phase[k] = lane + 32 * k < A.r.half ? A.r.phase[lane + 32 * k] : 0;
+#pragma unroll 1
+            for (int r = warp; r < S::ROWS; r += 12) {
+                const int R = R0 + r, i = R / A.G, hq = c.h * A.G + R - i * A.G;
+                const bool ok = R < rows;
+                const char *src = A.q.p + ((int64_t)(c.s.q0 + (ok ? i : 0)) * A.q.ts + (int64_t)(ok ? hq : 0) * A.q.hs + lane) * size;
+                float v[S::DQK / 32];
+                if (A.in_bf16) {
+#pragma unroll
+                    for (int k = 0; k < S::DQK / 32; ++k) v[k] = ok ? load_elt(src, 32 * k, 1) : 0.f;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < S::DQK / 32; ++k) v[k] = ok ? load_elt(src, 32 * k, 0) : 0.f;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < S::DQK / 32; ++k) x[lane + 32 * k] = v[k] * A.qmul;
+                __syncwarp();
+                if (A.r.dim > 0 && ok) {
+                    const int pos = c.s.len - c.s.cnt + i, apart = A.r.inter ? 1 : A.r.half;
+#pragma unroll
+                    for (int k = 0; k < (S::DQK / 2 + 31) / 32; ++k) {
+                        const int p = lane + 32 * k;
+                        if (p >= A.r.half) break;
+                        const float2 cs = rope_cs(phase[k], pos);
+                        float *a = x + A.r.off + (A.r.inter ? 2 * p : p);
+                        const float u = a[0] * A.r.mscale, w = a[apart] * A.r.mscale;
+                        a[0] = u * cs.x - w * cs.y;
+                        a[apart] = w * cs.x + u * cs.y;
+                    }
+                    __syncwarp();
+                }
+                float mul = 1.f;
+                if constexpr (S::I4) {
+                    float big = 0.f;
+#pragma unroll
+                    for (int p = 0; p < S::PK; ++p) {
+                        const float a = x[64 * p + lane], b = x[64 * p + 32 + lane];
+                        big = fmaxf(big, fmaxf(fabsf(a), fabsf(b)));
+                        const float sum = warp_sum(a + b);
+                        if (lane == 0) info[r * (S::PK + 1) + p] = sum;
+                    }
+                    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));   // (magnitudes order as integers)
+                    const int e = min(max(9 - ((int)(__float_as_uint(big) >> 23) - 127), -100), 120);
+                    mul = __int_as_float((e + 127) << 23);
+                    if (lane == 0) info[r * (S::PK + 1) + S::PK] = __int_as_float((20 - e + 127) << 23);
+                }
+                // 16-byte pieces: 8 channels (4-bit: in the order the codes come out, even ones by 16)
+                for (int w = lane; w < S::DQK / 8; w += 32) {
+                    const float *y = x + 8 * w;
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float a = S::I4 ? y[q] * mul * (q & 1 ? 1.f : 16.f) : y[2 * q], b = S::I4 ? y[q + 4] * mul * (q & 1 ? 1.f : 16.f) : y[2 * q + 1];
+                        const uint32_t pa = split_pair<S::I4>(a), pb = split_pair<S::I4>(b);
+                        hi[q] = __byte_perm(pa, pb, 0x5410);
+                        lo[q] = __byte_perm(pa, pb, 0x7632);
+                    }
+                    char *dst = sm + (w >> 3) * 16384 + r * 128 + (((w & 7) ^ (r & 7)) << 4);
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(dst + S::Q_PART) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+            }
+        }
+        tc::fence_async_smem();
+    };
+    // A role's way through the run: a segment is tiles t0 .. t1 of one block, of which the first T have keys that some row sees.
+    // Every warp of the CTA passes the same three barriers a segment; each role has a loop of its own, so that its registers
+    // are its own.
+    auto segments = [&](auto &&role, auto &&finish, bool rows_too) {
+        Cursor c = start;
+        unsigned base = base0, done = 0;                                       // done: tiles of earlier segments
+        while (base + extra + c.t < u1) {
+            const int t0 = c.t, t1 = (int)min((unsigned)c.s.tiles, u1 - (base + extra));
+            const int T = max(0, min(t1, (c.most + 63) / 64) - t0);
+            if (rows_too) prepare(c);
+            tc::named_bar(1, S::THREADS);
+            role(c, t0, T, done);
+            tc::named_bar(1, S::THREADS);
+            finish(c, base, t0, t1);
+            done += T;
+            base += c.s.tiles + extra;
+            c.t = c.s.tiles - 1;
+            const bool stop = *dead != 0;
+            tc::named_bar(1, S::THREADS);
+            if (stop || base + extra >= u1) break;
+            c.advance<S>(A);
+        }
+    };
+    auto nothing = [](const Cursor &, unsigned, int, int) {};
+
+    if (warp < 4) {
+        take_registers();
+        segments([&](const Cursor &c, int t0, int T, unsigned done) {
+            const int rows = c.s.cnt * A.G, R0 = c.rb * S::ROWS;
+            // ---- softmax: thread r has row r
+            const int r = threadIdx.x, R = R0 + r;
+            const int vis = R < rows ? c.s.len - c.s.cnt + R / A.G + 1 : 0;
+            float m = -INFINITY, l = 0.f, mn[S::PV];
+            F2 qs[S::PK];
+            float fac = 1.f;
+#pragma unroll
+            for (int v = 0; v < S::PV; ++v) mn[v] = 0.f;
+            if constexpr (S::I4) {
+#pragma unroll
+                for (int p = 0; p < S::PK; ++p) qs[p] = pk(info[r * (S::PK + 1) + p], info[r * (S::PK + 1) + p]);
+                fac = info[r * (S::PK + 1) + S::PK];
+            }
+            for (int k = 0; k < T; ++k) {
+                const unsigned use = done + k;
+                if (!wait_for(s_full + 8 * (use & 1), use >> 1, dead, A.status)) break;
+                tc::tc_fence_after();
+                const int j0 = (t0 + k) * 64, slot = use % S::KB;
+                const int bad = bad_of[use & 7];
+                const bool mask = bad || j0 + 64 > c.least;
+                const uint32_t ts = tb + ((uint32_t)(warp * 32) << 16) + (use & 1) * S::SB;
+                const float *par = reinterpret_cast<const float *>(sm + S::AT_PAR + slot * S::PARAMS);
+                F2 sc[32];
+                float top = -INFINITY, e = 0.f;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t x[S::GK][16];
+#pragma unroll
+                    for (int g = 0; g < S::GK; ++g) tc::tmem_ld16(ts + 64 * g + 16 * b, x[g]);
+                    float4 s4[S::GK][4], m4[S::GK][4];   // four tokens' scales and minima a load, the same for all rows
+                    if constexpr (S::I4) {
+#pragma unroll
+                        for (int g = 0; g < S::GK; ++g)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                s4[g][q] = *reinterpret_cast<const float4 *>(par + g * 128 + 16 * b + 4 * q);
+                                m4[g][q] = *reinterpret_cast<const float4 *>(par + g * 128 + 64 + 16 * b + 4 * q);
+                            }
+                    }
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        F2 v;
+                        if constexpr (S::I4) {
+                            F2 a, z;
+#pragma unroll
+                            for (int g = 0; g < S::GK; ++g) {
+                                const float4 s = s4[g][q / 2], m = m4[g][q / 2];
+                                const F2 s2 = q & 1 ? pk(s.z, s.w) : pk(s.x, s.y), m2 = q & 1 ? pk(m.z, m.w) : pk(m.x, m.y);
+                                const F2 y = pk(__uint_as_float(x[g][2 * q]), __uint_as_float(x[g][2 * q + 1]));
+                                a = g ? fma2(s2, y, a) : mul2(s2, y);
+                                z = g ? fma2(m2, qs[g], z) : mul2(m2, qs[g]);
+                            }
+                            v = fma2(a, pk(fac, fac), z);
+                        } else {
+                            v = pk(__uint_as_float(x[0][2 * q]), __uint_as_float(x[0][2 * q + 1]));
+                        }
+                        float2 f = up(v);
+                        if (mask) {
+                            const int j = j0 + 16 * b + 2 * q;
+                            if ((bad >> b) & 1) f.x = f.y = __int_as_float(0x7fc00000);
+                            if (j >= vis) f.x = -INFINITY;
+                            if (j + 1 >= vis) f.y = -INFINITY;
+                            v = pk(f.x, f.y);
+                        }
+                        sc[8 * b + q] = v;
+                        top = fmaxf(top, fmaxf(f.x, f.y));
+                    }
+                }
+                if constexpr (S::I4) {
+                    // every value scale that the row sees here is below 2^e (as in paged_attend.cuh)
+                    float big = 0.f;
+                    if (mask) {
+#pragma unroll 4
+                        for (int j = 0; j < 64; ++j)
+                            if (j0 + j < vis)
+#pragma unroll
+                                for (int v = 0; v < S::PV; ++v) big = fmaxf(big, par[(S::PK + v) * 128 + j]);
+                    } else {
+                        const float *tops = reinterpret_cast<const float *>(sm + S::AT_TOP) + slot * 16;
+#pragma unroll
+                        for (int w = 0; w < 8; ++w) big = fmaxf(big, tops[w]);
+                    }
+                    e = (float)(max((int)(__float_as_uint(big) >> 23), 113) - 126) - 14.f;
+                }
+                const float mnew = fmaxf(m, top + e), at_base = mnew == -INFINITY ? 0.f : mnew, cr = ex2(m - at_base);
+                m = mnew;
+                corr[(use & 3) * 128 + r] = cr;
+                F2 lsum = pk(0.f, 0.f), ms[S::PV];
+#pragma unroll
+                for (int v = 0; v < S::PV; ++v) ms[v] = pk(0.f, 0.f);
+                const F2 nb = pk(-at_base, -at_base);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t hi[S::GV][8], lo[S::GV][8];
+                    float4 s4[S::GV][4], m4[S::GV][4];
+                    if constexpr (S::I4) {
+#pragma unroll
+                        for (int g = 0; g < S::GV; ++g)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                s4[g][q] = *reinterpret_cast<const float4 *>(par + (S::PK + g) * 128 + 16 * b + 4 * q);
+                                m4[g][q] = *reinterpret_cast<const float4 *>(par + (S::PK + g) * 128 + 64 + 16 * b + 4 * q);
+                            }
+                    }
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float2 d = up(add2(sc[8 * b + q], nb));
+                        const F2 p = pk(ex2(d.x), ex2(d.y));
+                        lsum = add2(lsum, p);
+#pragma unroll
+                        for (int g = 0; g < S::GV; ++g) {
+                            F2 w = p;
+                            if constexpr (S::I4) {
+                                const float4 s = s4[g][q / 2], mm = m4[g][q / 2];
+                                float2 s2 = q & 1 ? make_float2(s.z, s.w) : make_float2(s.x, s.y), m2 = q & 1 ? make_float2(mm.z, mm.w) : make_float2(mm.x, mm.y);
+                                if (mask) {              // a key the row does not see weighs 0 even against a NaN
+                                    const int j = j0 + 16 * b + 2 * q;
+                                    if (j >= vis) s2.x = m2.x = 0.f;
+                                    if (j + 1 >= vis) s2.y = m2.y = 0.f;
+                                }
+                                w = mul2(p, pk(s2.x, s2.y));
+                                ms[g] = fma2(p, pk(m2.x, m2.y), ms[g]);
+                            }
+                            const float2 f = up(w);
+                            if constexpr (S::I4) {
+                                const __half2 h = __floats2half2_rn(f.x, f.y);
+                                const float2 back = __half22float2(h);
+                                const __half2 rest = __floats2half2_rn(f.x - back.x, f.y - back.y);
+                                hi[g][q] = *reinterpret_cast<const uint32_t *>(&h);
+                                lo[g][q] = *reinterpret_cast<const uint32_t *>(&rest);
+                            } else {
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+                                hi[g][q] = *reinterpret_cast<const uint32_t *>(&h);
+                                const __nv_bfloat162 rest = __floats2bfloat162_rn(f.x - __uint_as_float(hi[g][q] << 16), f.y - __uint_as_float(hi[g][q] & 0xffff0000u));
+                                lo[g][q] = *reinterpret_cast<const uint32_t *>(&rest);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int g = 0; g < S::GV; ++g) {
+                        tc::tmem_st8(ts + 64 * g + 8 * b, hi[g]);
+                        tc::tmem_st8(ts + 64 * g + 32 + 8 * b, lo[g]);
+                    }
+                }
+                const float2 ls = up(lsum);
+                l = fmaf(l, cr, ls.x + ls.y);
+                if constexpr (S::I4) {
+#pragma unroll
+                    for (int v = 0; v < S::PV; ++v) {
+                        const float2 x = up(ms[v]);
+                        mn[v] = fmaf(mn[v], cr, x.x + x.y);
+                    }
+                }
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
+                tc::mbar_arrive(p_full + 8 * (use & 1));
+            }
+            fin[r] = m;
+            fin[128 + r] = c.s.len < 0 ? __int_as_float(0x7fc00000) : l;
+#pragma unroll
+            for (int v = 0; v < S::PV; ++v) fin[(2 + v) * 128 + r] = mn[v];
+        }, nothing, true);
+        tc::named_bar(1, S::THREADS);
+        if (warp == 0) tc::tmem_dealloc(tb, 512);
+    } else if (warp < 12) {
+        float o[S::DV / 2];                                                    // a row, half the channels
+        Segment out[2];                                                        // what reaches out: the first segment, the last
+        out[0].key = out[1].key = -1;
+        segments([&](const Cursor &c, int t0, int T, unsigned done) {
+            const int rows = c.s.cnt * A.G, R0 = c.rb * S::ROWS;
+            // ---- helpers
+            const int ht = threadIdx.x - 128, r = 32 * (warp & 3) + lane, half = (warp - 4) >> 2;
+            const int vis = R0 + r < rows ? c.s.len - c.s.cnt + (R0 + r) / A.G + 1 : 0;
+#pragma unroll
+            for (int x = 0; x < S::DV / 2; ++x) o[x] = 0.f;
+            bool ok = true;
+            for (int k = 0; k < T + 2 && ok; ++k) {
+                if (k < T) {
+                    const unsigned use = done + k;
+                    const int slot = use % S::KB, j0 = (t0 + k) * 64;
+                    char *kv = sm + S::AT_KV + slot * S::KV;
+                    if constexpr (S::I4) {
+                        ok = wait_for(raw_full + 8 * (use & 1), use >> 1, dead, A.status);
+                        if (ok && use >= S::KB) ok = wait_for(kv_free + 8 * slot, use / S::KB - 1, dead, A.status);
+                        if (!ok) break;
+                        const char *raw = sm + S::AT_RAW + (use & 1) * S::RAW;
+                        for (int x = ht; x < S::PL * 128; x += 256) {
+                            const int p = x >> 7, tok = (x >> 1) & 63, hh = x & 1;
+                            const uint4 w = *reinterpret_cast<const uint4 *>(raw + (tok >> 4) * S::STRIP + p * kPlaneI4 + (tok & 15) * 32 + 16 * hh);
+                            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                            char *dst = kv + p * 8192 + tok * 128;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const uint32_t v = u[q] >> 8;
+                                *reinterpret_cast<uint4 *>(dst + (((4 * hh + q) ^ (tok & 7)) << 4)) =
+                                    make_uint4(u[q] & 0x000F000Fu, u[q] & 0x00F000F0u, v & 0x000F000Fu, v & 0x00F000F0u);
+                            }
+                        }
+                        float *par = reinterpret_cast<float *>(sm + S::AT_PAR + slot * S::PARAMS);
+                        float big = 0.f;
+                        for (int x = ht; x < S::PL * 64; x += 256) {
+                            const int p = x >> 6, tok = x & 63;
+                            float2 v = make_float2(0.f, 0.f);
+                            if (j0 + tok < c.most) v = __half22float2(*reinterpret_cast<const __half2 *>(raw + (tok >> 4) * S::STRIP + p * kPlaneI4 + 512 + (tok & 15) * 4));
+                            par[p * 128 + tok] = v.x;
+                            par[p * 128 + 64 + tok] = v.y;
+                            if (p >= S::PK) big = fmaxf(big, v.x);
+                        }
+                        big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));   // (not negative)
+                        if (lane == 0) reinterpret_cast<float *>(sm + S::AT_TOP)[slot * 16 + warp - 4] = big;
+                        tc::fence_async_smem();
+                        tc::mbar_arrive(kv_full + 8 * slot);
+                        tc::mbar_arrive(raw_free + 8 * (use & 1));
+                    } else {
+                        ok = wait_for(kv_full + 8 * slot, use / S::KB, dead, A.status);
+                        if (!ok) break;
+                        if (bad_of[use & 7] || j0 + 64 > c.least) {
+                            // value rows past what was brought hold anything, and a value that is not finite must not meet a
+                            // weight of 0: both go to 0 here, the latter remembered by the rows that see it
+                            const int t = ht >> 2, q4 = ht & 3;          // a token, a quarter of its channels
+                            const bool gone = j0 + t >= c.most || ((bad_of[use & 7] >> (t >> 4)) & 1);
+                            uint32_t found = 0;
+#pragma unroll
+                            for (int p = 0; p < S::PV; ++p)
+#pragma unroll
+                                for (int q = 0; q < 2; ++q) {
+                                    uint4 *at4 = reinterpret_cast<uint4 *>(kv + (S::PK + p) * 8192 + t * 128 + (((2 * q4 + q) ^ (t & 7)) << 4));
+                                    uint4 w = *at4;
+                                    uint32_t *u = &w.x;
+                                    bool touched = gone;
+#pragma unroll
+                                    for (int x = 0; x < 4; ++x) {
+                                        const uint32_t f = gone ? 0xffffffffu : __vcmpeq2(u[x] & 0x7f807f80u, 0x7f807f80u);
+                                        touched = touched || f;
+                                        u[x] &= ~f;
+                                        if (!gone) found |= f;
+                                    }
+                                    if (touched) *at4 = w;
+                                }
+                            if (found) atomicOr(bad_of + 8 + (use & 7), 1);
+                        }
+                        tc::fence_async_smem();
+                        tc::mbar_arrive(v_ok + 8 * slot);
+                    }
+                }
+                if (k >= 2) {
+                    const unsigned use = done + k - 2;
+                    const int ob = use % S::OB;
+                    ok = wait_for(o_full + 8 * ob, use / S::OB, dead, A.status);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    const float cr = corr[(use & 3) * 128 + r];
+                    const uint32_t to = tb + ((uint32_t)(32 * (warp & 3)) << 16) + S::COL_O + ob * S::DV + half * (S::DV / 2);
+#pragma unroll
+                    for (int b = 0; b < S::DV / 32; ++b) {
+                        uint32_t x[16];
+                        tc::tmem_ld16(to + 16 * b, x);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) o[16 * b + q] = fmaf(o[16 * b + q], cr, __uint_as_float(x[q]));
+                    }
+                    if (!S::I4 && bad_of[8 + (use & 7)]) {   // values that are not finite: from memory, for the rows that see them
+                        const int j0 = (t0 + k - 2) * 64;
+#pragma unroll 1
+                        for (int j = j0; j < min(j0 + 64, min(vis, c.most)); ++j) {
+                            const int pgi = j / A.P.page_size, pg = A.P.table[(int64_t)c.n * A.P.max_pages + pgi];
+                            if (pg < 0 || pg >= A.P.num_pages) continue;
+                            const char *plane = A.P.pool + (int64_t)pg * A.P.page_bytes + (int64_t)c.h * A.P.block_bytes +
+                                                (int64_t)((j - pgi * A.P.page_size) / kStrip) * S::STRIP + S::PK * kPlaneBf16;
+#pragma unroll
+                            for (int x = 0; x < S::DV / 2; ++x) {
+                                const int ch = half * (S::DV / 2) + x;
+                                const uint16_t v = *reinterpret_cast<const uint16_t *>(plane + (ch >> 6) * kPlaneBf16 + (j & 15) * 128 + ((((ch & 63) >> 3) ^ (j & 7)) << 4) + (ch & 7) * 2);
+                                if ((v & 0x7f80) == 0x7f80) o[x] = __int_as_float(0x7fc00000);
+                            }
+                        }
+                    }
+                    tc::tc_fence_before();
+                    tc::mbar_arrive(o_free + 8 * ob);
+                }
+            }
+        }, [&](const Cursor &c, unsigned base, int t0, int t1) {
+            // the segment's end: O through shared memory (over the operand tiles) to the output, or to the workspace
+            const int rows = c.s.cnt * A.G, R0 = c.rb * S::ROWS, ht = threadIdx.x - 128;
+            const bool begins = t0 == 0, ends = t1 == c.s.tiles;
+            float *stage = reinterpret_cast<float *>(sm + S::AT_KV);           // rows of DV + 4
+            const int r = 32 * (warp & 3) + lane, half = (warp - 4) >> 2;
+#pragma unroll
+            for (int w = 0; w < S::DV / 16; ++w) {
+                const int ch = half * (S::DV / 2) + 8 * w;
+                float x[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    if constexpr (S::I4) x[q] = fmaf(o[8 * w + (q < 4 ? 2 * q : 2 * q - 7)], q & 1 ? 1048576.f : 16777216.f, fin[(2 + ch / 64) * 128 + r]);
+                    else x[q] = o[8 * w + q];
+                }
+                float4 *dst = reinterpret_cast<float4 *>(stage + r * (S::DV + 4) + ch);
+                dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+                dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+            }
+            tc::named_bar(2, 256);
+            float *rec = A.partial + ((size_t)blockIdx.x * 2 + (begins ? 1 : 0)) * S::RECORD;
+            const int live = min(S::ROWS, rows - R0);
+#pragma unroll 1
+            for (int x = ht; x < live * (S::DV / 4); x += 256) {
+                const int rr = x / (S::DV / 4), ch = 4 * (x - rr * (S::DV / 4));
+                const float4 v = *reinterpret_cast<const float4 *>(stage + rr * (S::DV + 4) + ch);
+                if (begins && ends) {
+                    store4(A, S::DV, c.s.q0, c.h, R0 + rr, ch, v, fin[128 + rr]);
+                } else {
+                    *reinterpret_cast<float4 *>(rec + 256 + rr * S::DV + ch) = v;
+                    if (ch == 0) {
+                        rec[rr] = fin[rr];
+                        rec[128 + rr] = fin[128 + rr];
+                    }
+                }
+            }
+            if (!(begins && ends)) {
+                const int key = (int)(base + extra);
+                const Segment sg{key, key + c.s.tiles - 1, (begins ? 1 : 0) | (ends ? 2 : 0), c.h, c.rb, c.s.q0, rows, 0};
+                if (begins) out[1] = sg;
+                else out[0] = sg;
+            }
+        }, true);
+        tc::named_bar(1, S::THREADS);
+
+        // blocks that several CTAs share: the last of them to get here joins the records, in the row's order
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+            const Segment sg = i ? out[1] : out[0];
+            if (sg.key < 0) continue;
+            const unsigned first = split.owner(sg.key), last = split.owner(sg.last);
+            __threadfence();
+            tc::named_bar(2, 256);
+            if (threadIdx.x == 128) arrived = atomicAdd(A.counters + first, 1u);
+            tc::named_bar(2, 256);
+            if (arrived != last - first) continue;
+            __threadfence();
+            if (threadIdx.x == 128) A.counters[first] = 0;
+            auto rec = [&](unsigned b) { return A.partial + ((size_t)b * 2 + (b == first ? 1 : 0)) * S::RECORD; };
+            for (int x = threadIdx.x - 128; x < S::ROWS * S::DV / 4; x += 256) {
+                const int r = x / (S::DV / 4), ch = 4 * (x - r * (S::DV / 4)), R = sg.rb * S::ROWS + r;
+                if (R >= sg.rows) continue;
+                float top = -INFINITY, l = 0.f;
+                float4 v4 = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (unsigned b = first; b <= last; ++b) top = fmaxf(top, __ldcg(rec(b) + r));
+#pragma unroll 4
+                for (unsigned b = first; b <= last; ++b) {
+                    const float f = weight(__ldcg(rec(b) + r), top);
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(rec(b) + 256 + r * S::DV + ch));
+                    l = fmaf(f, __ldcg(rec(b) + 128 + r), l);
+                    v4.x = fmaf(f, v.x, v4.x); v4.y = fmaf(f, v.y, v4.y); v4.z = fmaf(f, v.z, v4.z); v4.w = fmaf(f, v.w, v4.w);
+                }
+                store4(A, S::DV, sg.q0, sg.h, R, ch, v4, l);
+            }
+        }
+    } else {
+        give_registers();
+        segments([&](const Cursor &c, int t0, int T, unsigned done) {
+            if (warp == 12) {
+                // ---- producer
+                for (int k = 0; k < T; ++k) {
+                    const unsigned use = done + k;
+                    const int strip = (t0 + k) * 4 + (S::I4 ? lane : lane / S::PL), slot = use % S::KB;
+                    const bool mine = (S::I4 ? lane < 4 : lane < 4 * S::PL) && 16 * strip < c.most;
+                    int pg = -1, j = 0;
+                    if (mine) {
+                        j = A.per_page_inv ? (int)__umulhi((unsigned)strip, A.per_page_inv) : strip;
+                        pg = A.P.table[(int64_t)c.n * A.P.max_pages + j];
+                    }
+                    bool ok = true;
+                    if (S::I4 ? use >= 2 : use >= S::KB)
+                        ok = S::I4 ? wait_for(raw_free + 8 * (use & 1), (use >> 1) - 1, dead, A.status) : wait_for(kv_free + 8 * slot, use / S::KB - 1, dead, A.status);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    const bool good = mine && pg >= 0 && pg < A.P.num_pages;
+                    const unsigned have = __ballot_sync(0xffffffffu, good), wrong = __ballot_sync(0xffffffffu, mine && !good);
+                    const uint32_t full = S::I4 ? raw_full + 8 * (use & 1) : kv_full + 8 * slot;
+                    if (lane == 0) {
+                        int bits = 0;
+                        for (int s = 0; s < 4; ++s) bits |= ((wrong >> (S::I4 ? s : s * S::PL)) & 1) << s;
+                        bad_of[use & 7] = bits;
+                        bad_of[8 + (use & 7)] = 0;
+                        tc::mbar_arrive_expect_tx(full, __popc(have) * (S::I4 ? S::STRIP : kPlaneBf16));
+                    }
+                    __syncwarp();
+                    if (good) {
+                        const char *src = A.P.pool + (int64_t)pg * A.P.page_bytes + (int64_t)c.h * A.P.block_bytes + (int64_t)(strip - j * A.per_page) * S::STRIP;
+                        if constexpr (S::I4) {
+                            tc::bulk_g2s(sm32 + S::AT_RAW + (use & 1) * S::RAW + lane * S::STRIP, src, S::STRIP, full);
+                        } else {
+                            const int p = lane % S::PL, s = lane / S::PL;
+                            tc::bulk_g2s(sm32 + S::AT_KV + slot * S::KV + p * 8192 + s * kPlaneBf16, src + p * kPlaneBf16, kPlaneBf16, full);
+                        }
+                    }
+                }
+            } else if (warp == 13 && lane == 0) {
+                // ---- MMA
+                constexpr uint32_t id_s = idesc16(S::I4, 128, 64, false), id_o = idesc16(S::I4, 128, 64, true);
+                bool ok = true;
+                for (int k = 0; k < T + 1 && ok; ++k) {
+                    if (k < T) {
+                        const unsigned use = done + k;
+                        const int slot = use % S::KB;
+                        ok = wait_for(kv_full + 8 * slot, use / S::KB, dead, A.status);
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                        const uint32_t ts = tb + (use & 1) * S::SB, kv = sm32 + S::AT_KV + slot * S::KV;
+    #pragma unroll
+                        for (int p = 0; p < S::PK; ++p) {
+                            const uint64_t dq = tc::sdesc_kmajor_sw128(sm32 + p * 16384), dl = tc::sdesc_kmajor_sw128(sm32 + S::Q_PART + p * 16384),
+                                           dk = tc::sdesc_kmajor_sw128(kv + p * 8192);
+    #pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t d = ts + (S::I4 ? 64 * p : 0);
+                                tc::mma_bf16(d, tc::dadd(dq, 32 * i), tc::dadd(dk, 32 * i), id_s, i != 0 || (!S::I4 && p != 0));
+                                tc::mma_bf16(d, tc::dadd(dl, 32 * i), tc::dadd(dk, 32 * i), id_s, 1);
+                            }
+                        }
+                        tc::mma_commit(s_full + 8 * (use & 1));
+                    }
+                    if (k >= 1) {
+                        const unsigned use = done + k - 1;
+                        const int slot = use % S::KB, ob = use % S::OB;
+                        ok = wait_for(p_full + 8 * (use & 1), use >> 1, dead, A.status);
+                        if (ok && use >= S::OB) ok = wait_for(o_free + 8 * ob, use / S::OB - 1, dead, A.status);
+                        if (ok && !S::I4) ok = wait_for(v_ok + 8 * slot, use / S::KB, dead, A.status);
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                        const uint32_t ts = tb + (use & 1) * S::SB, kv = sm32 + S::AT_KV + slot * S::KV;
+    #pragma unroll
+                        for (int v = 0; v < S::PV; ++v) {
+                            const uint64_t dv = tc::sdesc_mnmajor_sw128(kv + (S::PK + v) * 8192, 8192);
+                            const uint32_t d = tb + S::COL_O + ob * S::DV + 64 * v, p = ts + (S::I4 ? 64 * v : 0);
+    #pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                tc::mma_bf16_ta(d, p + 8 * i, tc::dadd(dv, 2048 * i), id_o, i != 0);
+                                tc::mma_bf16_ta(d, p + 32 + 8 * i, tc::dadd(dv, 2048 * i), id_o, 1);
+                            }
+                        }
+                        tc::mma_commit(o_full + 8 * ob);
+                        tc::mma_commit(kv_free + 8 * slot);
+                    }
+                }
+            }
+        }, nothing, false);
+        tc::named_bar(1, S::THREADS);
+    }
+}
+
+template <class S> cudaError_t launch_rows(const Args &A, cudaStream_t stream) {
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = smem_attr_once((const void *)rows_kernel<S>, S::SMEM, done);
+    if (e != cudaSuccess) return e;
+    int dev = 0, sms = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    rows_kernel<S><<<sms < kMaxCtas ? sms : kMaxCtas, S::THREADS, S::SMEM, stream>>>(A);
+    count_launch();
+    return cudaGetLastError();
+}
+
+// up to 192 and 128 channels: what fits tensor memory
+template <bool I4> cudaError_t pick_rows(int dqk, int dv, const Args &A, cudaStream_t s) {
+    if (dqk == 64) return dv == 64 ? launch_rows<RowsShape<64, 64, I4>>(A, s) : launch_rows<RowsShape<64, 128, I4>>(A, s);
+    if (dqk == 128) return dv == 64 ? launch_rows<RowsShape<128, 64, I4>>(A, s) : launch_rows<RowsShape<128, 128, I4>>(A, s);
+    return dv == 64 ? launch_rows<RowsShape<192, 64, I4>>(A, s) : launch_rows<RowsShape<192, 128, I4>>(A, s);
+}
+
+cudaError_t run_i4_rows(int dqk, int dv, const Args &A, cudaStream_t s);
+cudaError_t run_bf16_rows(int dqk, int dv, const Args &A, cudaStream_t s);
+
+}  // namespace attend
+}  // namespace k3kda

@@ -287,3 +287,90 @@ def test_append_then_attend_over_steps():
                 want = PP.attend(qr, _np(kr[at:at + t]), _np(vr[at:at + t]), [t], 128 ** -0.5)
                 assert np.abs(_np(got[n]) - want[0]).max() <= (1e-4 if fmt == "i4" else 2e-3)
                 at += t
+
+
+# ---- blocks of 128 rows (more than 16 query rows of a key head) ------------------------------------------------
+
+ROWS = [  # total, new, heads, group, dqk, dv, page, rope, gate
+    ([64], [17], 1, 1, 64, 64, 16, (0, 0, "half"), False),
+    ([200], [128], 1, 1, 128, 128, 64, (128, 0, "half"), True),
+    ([129, 0, 300, 31], [129, 0, 40, 31], 2, 1, 192, 128, 32, (64, 128, "interleaved"), True),
+    ([1, 65, 63, 64, 500], [1, 1, 1, 1, 1], 2, 20, 128, 64, 48, (32, 3, "half"), False),
+    ([300, 5], [6, 5], 3, 8, 64, 128, 16, (34, 5, "interleaved"), True),
+    ([77, 256, 257], [77, 3, 140], 1, 3, 192, 64, 256, (0, 0, "half"), False)]
+
+
+@pytest.mark.parametrize("case", ROWS, ids=str)
+@pytest.mark.parametrize("fmt", ["i4", "bf16"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_blocks_of_rows_against_the_64_bit_form(case, fmt, dtype):
+    total, new, heads, group, dqk, dv, page, rope, gate = case
+    c = Case(total, new, heads, group, dqk, dv, page, fmt, rope, dtype, gate, seed=sum(total))
+    want, tol = c.want()
+    for out in (torch.float32, torch.bfloat16):
+        _check(c.run(out), want, tol, out)
+
+
+@pytest.mark.parametrize("fmt", ["i4", "bf16"])
+def test_blocks_of_rows_that_many_ctas_share(fmt):
+    """Few (sequence, head)s and long contexts: a block's tiles over many CTAs; the same bits each time; no counter left."""
+    for total, new, heads, group in (([40000], [3], 1, 8), ([3000, 17, 9000], [40, 17, 1], 2, 17), ([900] * 30, [9] * 30, 4, 4)):
+        c = Case(total, new, heads, group, 128, 128, 64, fmt, (64, 0, "interleaved"), seed=21)
+        tol = np.concatenate([c._bound(n, PP.rotate(_np(c.q[int(c.cu[n]):int(c.cu[n + 1])]), np.arange(t - m, t), *c.rope), m)
+                              for n, (t, m) in enumerate(zip(total, new))])
+        ws = K.paged_attend_workspace(c.cache, heads * group)
+        got = c.run(ws=ws)
+        _check(got, _long(c), tol)
+        for _ in range(3):
+            assert torch.equal(got, c.run(ws=ws))
+        assert K.k3kda_workspace_status(ws) == 0 and not ws[256:4352].any()
+
+
+@pytest.mark.parametrize("fmt", ["i4", "bf16"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_blocks_of_rows_what_a_row_does_not_see_cannot_reach_it(fmt, value):
+    """A value that is not finite in the 11th of 20 new tokens: the tokens before it are as without, the others have it in
+    the channels that hold it (4-bit: its group), and nowhere else."""
+    def spoil(n, rows):
+        if n == 1:
+            rows[-10, 1, 128 + 70] = value
+    args = ([200, 37], [1, 20], 2, 3, 128, 128, 16, fmt)
+    clean, dirty = Case(*args, seed=8), Case(*args, seed=8, edit=spoil)
+    a, b = clean.run(), dirty.run()
+    assert torch.equal(a[:11], b[:11])
+    gone = ~torch.isfinite(b[11:])
+    assert not gone[:, :3].any()
+    seen = torch.zeros(128, dtype=torch.bool, device=DEV)
+    seen[64:128] = True
+    if fmt == "bf16":
+        seen[:] = False
+        seen[70] = True
+    assert torch.equal(gone[:, 3:], seen.expand(10, 3, 128))
+
+
+@pytest.mark.parametrize("fmt", ["i4", "bf16"])
+def test_blocks_of_rows_bad_pages_and_lengths(fmt):
+    total, new = [30, 0, 40, 100, 50], [30, 0, 20, 25, 20]
+    c = Case(total, new, 2, 2, 128, 128, 16, fmt, gate=True, seed=5)
+    want, tol = c.want()
+    c.cache.kv_len.copy_(_i([28, 0, -1, 100, 1000]))
+    tab = c.tab.copy()
+    tab[3, 5] = -1                                           # tokens 80..95: seen by tokens 80.. of 75..99
+    c.cache.block_table.copy_(_i(tab))
+    got = _np(c.run())
+    assert (got[:2] == 0).all() and np.isfinite(got[2:30]).all()       # two rows before position 0
+    assert np.isnan(got[30:50]).all() and np.isnan(got[75:]).all()
+    assert (np.abs(got[50:55] - want[50:55]) <= tol[50:55] + 2.0 ** -23 * np.abs(want[50:55])).all()
+    assert np.isnan(got[55:75]).all()
+
+
+def test_blocks_of_rows_values_of_every_size():
+    def edit(n, rows):
+        r = np.random.default_rng(9)
+        rows[..., 128:] *= 10.0 ** r.integers(-5, 4, rows.shape[:2] + (1,))
+        rows[..., :128] *= 6
+    c = Case([3000, 50], [9, 20], 2, 2, 128, 128, 64, "i4", seed=10, edit=edit)
+    tol = np.concatenate([c._bound(n, _np(c.q[int(c.cu[n]):int(c.cu[n + 1])]), m) for n, m in enumerate(c.new)])
+    _check(c.run(), _long(c), tol)
+    c = Case([700], [40], 1, 1, 128, 128, 64, "i4", seed=11, edit=lambda n, rows: rows[..., 128:].__imul__(1e-4))
+    _check(c.run(), _long(c), c._bound(0, _np(c.q), 40))
