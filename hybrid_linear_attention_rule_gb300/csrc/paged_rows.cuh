@@ -39,13 +39,13 @@ template <int DQK_, int DV_, bool I4_> struct RowsShape {
     static constexpr int Q_PART = PK * 16384, KV = PL * 8192;
     static constexpr int RS = I4 ? 2 : 1, RAW = I4 ? NS * STRIP : 0;
     static constexpr int PARAMS = I4 ? PL * 512 : 0;                            // scale[64], minimum[64] of each plane
-    static constexpr int SMALL = 4 * 128 * 4 + (2 + PV) * 128 * 4 + 128 * (PK + 1) * 4 + 1024 + 64 + (THREADS + 4) * 4;
+    static constexpr int SMALL = 4 * 128 * 4 + (2 + PV) * 128 * 4 + 128 * (PK + 1) * 4 + 1024 + 64 + 8 * PV * 8 + (THREADS + 4) * 4;
     static constexpr int FIT = (232448 - 1024 - 256 - 2 * Q_PART - RS * RAW - SMALL) / (KV + PARAMS + 64);
     static constexpr int KB = FIT > 4 ? 4 : FIT;                                // operand tiles
     static_assert(KB >= 2 && KV >= WARPS * DQK * 4 && KB * KV >= ROWS * (DV + 4) * 4, "operand tiles");
     static constexpr int AT_KV = 2 * Q_PART, AT_RAW = AT_KV + KB * KV, AT_PAR = AT_RAW + RS * RAW, AT_TOP = AT_PAR + KB * PARAMS;
     static constexpr int AT_CORR = AT_TOP + KB * 64, AT_FIN = AT_CORR + 4 * 128 * 4, AT_INFO = AT_FIN + (2 + PV) * 128 * 4;
-    static constexpr int AT_BAR = AT_INFO + 128 * (PK + 1) * 4, AT_BAD = AT_BAR + 512, AT_PRE = AT_BAD + 64;
+    static constexpr int AT_BAR = AT_INFO + 128 * (PK + 1) * 4, AT_BAD = AT_BAR + 512, AT_PRE = AT_BAD + 64 + 8 * PV * 8;
     static constexpr int SMEM = AT_PRE + (THREADS + 4) * 4 + 1024;
     static_assert(SMEM + 256 <= 232448, "shared memory");
 };
@@ -107,6 +107,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
     float *corr = reinterpret_cast<float *>(sm + S::AT_CORR), *fin = reinterpret_cast<float *>(sm + S::AT_FIN);
     float *info = reinterpret_cast<float *>(sm + S::AT_INFO);                  // [128][PK sums, factor]
     int *bad_of = reinterpret_cast<int *>(sm + S::AT_BAD);                     // [8] tiles' strips on pages outside the pool, [8] whether values were put to 0
+    unsigned long long *poison = reinterpret_cast<unsigned long long *>(sm + S::AT_BAD + 64);   // [8][PV]: tokens whose value group is not finite
     unsigned *pre = reinterpret_cast<unsigned *>(sm + S::AT_PRE);
     __shared__ unsigned part_sum[S::WARPS], part_tiles[S::WARPS], arrived, tslot;
     __shared__ int dead_flag;
@@ -200,24 +201,39 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
             uint64_t phase[(S::DQK / 2 + 31) / 32];
 #pragma unroll
             for (int k = 0; k < (S::DQK / 2 + 31) / 32; ++k) phase[k] = lane + 32 * k < A.r.half ? A.r.phase[lane + 32 * k] : 0;
-#pragma unroll 1
-            for (int r = warp; r < S::ROWS; r += 12) {
+            float v[S::DQK / 32], next[S::DQK / 32];     // the next row is on its way while one is prepared
+            auto fetch = [&](int r, float (&f)[S::DQK / 32]) {
                 const int R = R0 + r, i = R / A.G, hq = c.h * A.G + R - i * A.G;
-                const bool ok = R < rows;
-                const char *src = A.q.p + ((int64_t)(c.s.q0 + (ok ? i : 0)) * A.q.ts + (int64_t)(ok ? hq : 0) * A.q.hs + lane) * size;
-                float v[S::DQK / 32];
+                if (R >= rows || r >= S::ROWS) return;
+                const char *src = A.q.p + ((int64_t)(c.s.q0 + i) * A.q.ts + (int64_t)hq * A.q.hs + lane) * size;
                 if (A.in_bf16) {
 #pragma unroll
-                    for (int k = 0; k < S::DQK / 32; ++k) v[k] = ok ? load_elt(src, 32 * k, 1) : 0.f;
+                    for (int k = 0; k < S::DQK / 32; ++k) f[k] = load_elt(src, 32 * k, 1);
                 } else {
 #pragma unroll
-                    for (int k = 0; k < S::DQK / 32; ++k) v[k] = ok ? load_elt(src, 32 * k, 0) : 0.f;
+                    for (int k = 0; k < S::DQK / 32; ++k) f[k] = load_elt(src, 32 * k, 0);
                 }
+            };
+            fetch(warp, next);
+#pragma unroll 1
+            for (int r = warp; r < S::ROWS; r += 12) {
+                const int i = (R0 + r) / A.G;
+                if (R0 + r >= rows) {                    // a row of nothing
+                    for (int w = lane; w < S::DQK / 8; w += 32) {
+                        char *dst = sm + (w >> 3) * 16384 + r * 128 + (((w & 7) ^ (r & 7)) << 4);
+                        *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<uint4 *>(dst + S::Q_PART) = make_uint4(0, 0, 0, 0);
+                    }
+                    if (S::I4 && lane <= S::PK) info[r * (S::PK + 1) + lane] = 0.f;
+                    continue;
+                }
+#pragma unroll
+                for (int k = 0; k < S::DQK / 32; ++k) v[k] = next[k];
+                fetch(r + 12, next);
                 __syncwarp();
 #pragma unroll
                 for (int k = 0; k < S::DQK / 32; ++k) x[lane + 32 * k] = v[k] * A.qmul;
                 __syncwarp();
-                if (A.r.dim > 0 && ok) {
+                if (A.r.dim > 0) {
                     const int pos = c.s.len - c.s.cnt + i, apart = A.r.inter ? 1 : A.r.half;
 #pragma unroll
                     for (int k = 0; k < (S::DQK / 2 + 31) / 32; ++k) {
@@ -316,50 +332,54 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                 const bool mask = bad || j0 + 64 > c.least;
                 const uint32_t ts = tb + ((uint32_t)(warp * 32) << 16) + (use & 1) * S::SB;
                 const float *par = reinterpret_cast<const float *>(sm + S::AT_PAR + slot * S::PARAMS);
-                F2 sc[32];
-                float top = -INFINITY, e = 0.f;
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    uint32_t x[S::GK][16];
+                // 16 keys' scores out of TMEM; both passes form them (2.5 instructions a key) so that neither holds 64 of them: a
+                // loop short enough for the instruction cache
+                uint32_t x[S::GK][16];
+                auto bring = [&](int b) {
 #pragma unroll
                     for (int g = 0; g < S::GK; ++g) tc::tmem_ld16(ts + 64 * g + 16 * b, x[g]);
-                    float4 s4[S::GK][4], m4[S::GK][4];   // four tokens' scales and minima a load, the same for all rows
-                    if constexpr (S::I4) {
-#pragma unroll
-                        for (int g = 0; g < S::GK; ++g)
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                s4[g][q] = *reinterpret_cast<const float4 *>(par + g * 128 + 16 * b + 4 * q);
-                                m4[g][q] = *reinterpret_cast<const float4 *>(par + g * 128 + 64 + 16 * b + 4 * q);
-                            }
-                    }
+                };
+                auto scores = [&](int b, F2 (&sc)[8]) {
                     tc::tmem_wait_ld();
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
-                        F2 v;
                         if constexpr (S::I4) {
                             F2 a, z;
 #pragma unroll
                             for (int g = 0; g < S::GK; ++g) {
-                                const float4 s = s4[g][q / 2], m = m4[g][q / 2];
+                                // four tokens' scales and minima a load, the same for all rows
+                                const float4 s = *reinterpret_cast<const float4 *>(par + g * 128 + 16 * b + 4 * (q / 2)), m = *reinterpret_cast<const float4 *>(par + g * 128 + 64 + 16 * b + 4 * (q / 2));
                                 const F2 s2 = q & 1 ? pk(s.z, s.w) : pk(s.x, s.y), m2 = q & 1 ? pk(m.z, m.w) : pk(m.x, m.y);
                                 const F2 y = pk(__uint_as_float(x[g][2 * q]), __uint_as_float(x[g][2 * q + 1]));
                                 a = g ? fma2(s2, y, a) : mul2(s2, y);
                                 z = g ? fma2(m2, qs[g], z) : mul2(m2, qs[g]);
                             }
-                            v = fma2(a, pk(fac, fac), z);
+                            sc[q] = fma2(a, pk(fac, fac), z);
                         } else {
-                            v = pk(__uint_as_float(x[0][2 * q]), __uint_as_float(x[0][2 * q + 1]));
+                            sc[q] = pk(__uint_as_float(x[0][2 * q]), __uint_as_float(x[0][2 * q + 1]));
                         }
-                        float2 f = up(v);
-                        if (mask) {
-                            const int j = j0 + 16 * b + 2 * q;
+                    }
+                    if (mask) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            float2 f = up(sc[q]);
                             if ((bad >> b) & 1) f.x = f.y = __int_as_float(0x7fc00000);
-                            if (j >= vis) f.x = -INFINITY;
-                            if (j + 1 >= vis) f.y = -INFINITY;
-                            v = pk(f.x, f.y);
+                            if (j0 + 16 * b + 2 * q >= vis) f.x = -INFINITY;
+                            if (j0 + 16 * b + 2 * q + 1 >= vis) f.y = -INFINITY;
+                            sc[q] = pk(f.x, f.y);
                         }
-                        sc[8 * b + q] = v;
+                    }
+                };
+                float top = -INFINITY, e = 0.f;
+                bring(0);
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {
+                    F2 sc[8];
+                    scores(b, sc);
+                    bring((b + 1) & 3);                  // (the last one for the second pass)
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float2 f = up(sc[q]);
                         top = fmaxf(top, fmaxf(f.x, f.y));
                     }
                 }
@@ -386,37 +406,25 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
 #pragma unroll
                 for (int v = 0; v < S::PV; ++v) ms[v] = pk(0.f, 0.f);
                 const F2 nb = pk(-at_base, -at_base);
-#pragma unroll
+#pragma unroll 1
                 for (int b = 0; b < 4; ++b) {
                     uint32_t hi[S::GV][8], lo[S::GV][8];
-                    float4 s4[S::GV][4], m4[S::GV][4];
-                    if constexpr (S::I4) {
-#pragma unroll
-                        for (int g = 0; g < S::GV; ++g)
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                s4[g][q] = *reinterpret_cast<const float4 *>(par + (S::PK + g) * 128 + 16 * b + 4 * q);
-                                m4[g][q] = *reinterpret_cast<const float4 *>(par + (S::PK + g) * 128 + 64 + 16 * b + 4 * q);
-                            }
-                    }
+                    F2 sc[8];
+                    scores(b, sc);
+                    if (b < 3) bring(b + 1);
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
-                        const float2 d = up(add2(sc[8 * b + q], nb));
+                        const float2 d = up(add2(sc[q], nb));
                         const F2 p = pk(ex2(d.x), ex2(d.y));
                         lsum = add2(lsum, p);
 #pragma unroll
                         for (int g = 0; g < S::GV; ++g) {
                             F2 w = p;
                             if constexpr (S::I4) {
-                                const float4 s = s4[g][q / 2], mm = m4[g][q / 2];
-                                float2 s2 = q & 1 ? make_float2(s.z, s.w) : make_float2(s.x, s.y), m2 = q & 1 ? make_float2(mm.z, mm.w) : make_float2(mm.x, mm.y);
-                                if (mask) {              // a key the row does not see weighs 0 even against a NaN
-                                    const int j = j0 + 16 * b + 2 * q;
-                                    if (j >= vis) s2.x = m2.x = 0.f;
-                                    if (j + 1 >= vis) s2.y = m2.y = 0.f;
-                                }
-                                w = mul2(p, pk(s2.x, s2.y));
-                                ms[g] = fma2(p, pk(m2.x, m2.y), ms[g]);
+                                const float4 s = *reinterpret_cast<const float4 *>(par + (S::PK + g) * 128 + 16 * b + 4 * (q / 2)), mm = *reinterpret_cast<const float4 *>(par + (S::PK + g) * 128 + 64 + 16 * b + 4 * (q / 2));
+                                const F2 s2 = q & 1 ? pk(s.z, s.w) : pk(s.x, s.y), m2 = q & 1 ? pk(mm.z, mm.w) : pk(mm.x, mm.y);
+                                w = mul2(p, s2);
+                                ms[g] = fma2(p, m2, ms[g]);
                             }
                             const float2 f = up(w);
                             if constexpr (S::I4) {
@@ -435,8 +443,9 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                     }
 #pragma unroll
                     for (int g = 0; g < S::GV; ++g) {
-                        tc::tmem_st8(ts + 64 * g + 8 * b, hi[g]);
-                        tc::tmem_st8(ts + 64 * g + 32 + 8 * b, lo[g]);
+                        // the columns of these keys' scores: 8 of the high parts, 8 of the low ones, one step of the product
+                        tc::tmem_st8(ts + 64 * g + 16 * b, hi[g]);
+                        tc::tmem_st8(ts + 64 * g + 16 * b + 8, lo[g]);
                     }
                 }
                 const float2 ls = up(lsum);
@@ -446,6 +455,12 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                     for (int v = 0; v < S::PV; ++v) {
                         const float2 x = up(ms[v]);
                         mn[v] = fmaf(mn[v], cr, x.x + x.y);
+                        // value groups that are not finite were put to 0: the rows that see one
+                        const unsigned long long gone = poison[(use & 7) * S::PV + v];
+                        if (gone) {
+                            const int n = vis - j0;
+                            if (gone & (n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1)) mn[v] = __int_as_float(0x7fc00000);
+                        }
                     }
                 }
                 tc::tmem_wait_st();
@@ -499,6 +514,13 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                             const int p = x >> 6, tok = x & 63;
                             float2 v = make_float2(0.f, 0.f);
                             if (j0 + tok < c.most) v = __half22float2(*reinterpret_cast<const __half2 *>(raw + (tok >> 4) * S::STRIP + p * kPlaneI4 + 512 + (tok & 15) * 4));
+                            if (p >= S::PK) {            // a weight of 0 must not meet a NaN: such a group is 0 here and remembered
+                                const bool gone = !(fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY);
+                                if (gone) {
+                                    v = make_float2(0.f, 0.f);
+                                    atomicOr(&poison[(use & 7) * S::PV + p - S::PK], 1ull << tok);
+                                }
+                            }
                             par[p * 128 + tok] = v.x;
                             par[p * 128 + 64 + tok] = v.y;
                             if (p >= S::PK) big = fmaxf(big, v.x);
@@ -678,6 +700,8 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                         for (int s = 0; s < 4; ++s) bits |= ((wrong >> (S::I4 ? s : s * S::PL)) & 1) << s;
                         bad_of[use & 7] = bits;
                         bad_of[8 + (use & 7)] = 0;
+                    if constexpr (S::I4)
+                        for (int v = 0; v < S::PV; ++v) poison[(use & 7) * S::PV + v] = 0;
                         tc::mbar_arrive_expect_tx(full, __popc(have) * (S::I4 ? S::STRIP : kPlaneBf16));
                     }
                     __syncwarp();
@@ -693,7 +717,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                 }
             } else if (warp == 13 && lane == 0) {
                 // ---- MMA
-                constexpr uint32_t id_s = idesc16(S::I4, 128, 64, false), id_o = idesc16(S::I4, 128, 64, true);
+                constexpr uint32_t id_s = idesc16(S::I4, 128, 64, false), id_o = idesc16(S::I4, 128, S::I4 ? 64 : S::DV, true);
                 bool ok = true;
                 for (int k = 0; k < T + 1 && ok; ++k) {
                     if (k < T) {
@@ -726,13 +750,13 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                         tc::tc_fence_after();
                         const uint32_t ts = tb + (use & 1) * S::SB, kv = sm32 + S::AT_KV + slot * S::KV;
     #pragma unroll
-                        for (int v = 0; v < S::PV; ++v) {
+                        for (int v = 0; v < S::GV; ++v) {        // (bf16: all value channels at once)
                             const uint64_t dv = tc::sdesc_mnmajor_sw128(kv + (S::PK + v) * 8192, 8192);
-                            const uint32_t d = tb + S::COL_O + ob * S::DV + 64 * v, p = ts + (S::I4 ? 64 * v : 0);
-    #pragma unroll
+                            const uint32_t d = tb + S::COL_O + ob * S::DV + 64 * v, p = ts + 64 * v;
+#pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                tc::mma_bf16_ta(d, p + 8 * i, tc::dadd(dv, 2048 * i), id_o, i != 0);
-                                tc::mma_bf16_ta(d, p + 32 + 8 * i, tc::dadd(dv, 2048 * i), id_o, 1);
+                                tc::mma_bf16_ta(d, p + 16 * i, tc::dadd(dv, 2048 * i), id_o, i != 0);
+                                tc::mma_bf16_ta(d, p + 16 * i + 8, tc::dadd(dv, 2048 * i), id_o, 1);
                             }
                         }
                         tc::mma_commit(o_full + 8 * ob);
