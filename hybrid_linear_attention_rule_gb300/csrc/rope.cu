@@ -3,15 +3,15 @@
 //   (x, y) -> m (x cos - y sin, y cos + x sin),   angle = position * f_i            (forward)
 //   (x, y) -> m (x cos + y sin, y cos - x sin)                                      (gradient: the transpose)
 //
-// Bound by HBM: each element is read and written once.  A thread's item is two 16-byte pieces of one
-// (token, head) row: the two halves' pieces i and i + dim/2 (HALF), two neighbouring pieces
-// (INTERLEAVED), or two pieces that pass through.  A CTA takes kThreads * kItems items of
-// consecutive (token, head) rows, issues their loads, and only then forms its tokens' cosines and
-// sines in shared memory, once for all heads, so that the angles' arithmetic lies under the loads.
+// Bound by HBM: each element is read and written once.  A thread's item is two 16-byte pieces of a
+// head: the two halves' pieces i and i + dim/2 (HALF), two neighbouring pieces
+// (INTERLEAVED), or two pieces that pass through.  A thread keeps its item of its head and goes through its CTA's tokens,
+// so that its place is worked out once and the next token's pieces are on their way while one is turned; the
+// tokens' cosines and sines are formed once a CTA, for all heads, under the first loads.
 // Rows that are not 16-byte aligned go one element at a time (V = 1) through the same code.
 //
-// A key head that all heads shared gets the sum of their gradients: the CTA's threads divide the
-// heads among themselves, add their sums in shared memory in a fixed order and turn the total.
+// A key head that all heads shared gets the sum of their gradients: a thread adds an item's heads, or, with few
+// tokens, kSplit threads divide them, add their sums in shared memory in a fixed order and turn the total.
 #include <math.h>
 
 #include "rope.cuh"
@@ -20,9 +20,9 @@ namespace k3kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kItems = 2;                 // items of a thread
 constexpr int kTable = 4096;              // most (cos, sin) pairs of a CTA's tokens (32 KB)
-constexpr int kSplit = 8;                 // threads that divide a shared head's sum
+constexpr int kTokens = 16;               // most tokens a thread goes through
+constexpr int kSplit = 8;                 // threads that divide a shared head's sum where there are few
 
 struct RopeJob {                          // one array's rotation
     View in, out;
@@ -39,9 +39,12 @@ struct RopeArgs {
     int T;
     Rope r;
     int per_token;                        // items per token (a and, unless shared, b)
-    int block_items;                      // items of a CTA
+    int parts;                            // CTAs that share a token's items
+    int side;                             // tokens side by side in a CTA (1 when a token fills it)
+    int tokens;                           // tokens of a CTA, a multiple of side
     unsigned main_blocks;                 // CTAs of the plain rotation; the rest form the shared sums
-    int shared_tokens;                    // tokens of a CTA of the shared sums
+    int shared_side;                      // tokens of a CTA of the shared sums
+    int split;                            // threads that share an item's sum
     int table;                            // (cos, sin) pairs in shared memory
     float sgn;                            // +1 forward, -1 gradient
 };
@@ -100,108 +103,113 @@ __device__ __forceinline__ void fill_table(const RopeArgs &A, float2 *cs, int t0
 }
 
 template <typename T, int V> __device__ void plain_block(const RopeArgs &A, float2 *cs) {
-    // items of all tokens in one row; a CTA's run of them spans at most block_items / per_token + 2 tokens
-    const int64_t base = (int64_t)blockIdx.x * A.block_items, all = (int64_t)A.T * A.per_token;
-    const int count = (int)min((int64_t)A.block_items, all - base);
-    const int t0 = (int)(base / A.per_token), e0 = (int)(base - (int64_t)t0 * A.per_token);
-    const int n = (e0 + count - 1) / A.per_token + 1;
+    const int part = (int)(blockIdx.x % A.parts);
+    const int t0 = (int)(blockIdx.x / A.parts) * A.tokens, n = min(A.tokens, A.T - t0);
+    // this thread's item: which token of those side by side, which array, head and pieces
+    int e = part * kThreads + threadIdx.x;
+    const int st0 = e / A.per_token;
+    e -= st0 * A.per_token;
     const int na = A.a.heads * A.a.items;
-    T *dst[kItems];
-    int c0[kItems], c1[kItems], pair[kItems];
-    Piece<T, V> x[kItems], y[kItems];
+    const bool second = e >= na;
+    const RopeJob &j = second ? A.b : A.a;
+    e -= second ? na : 0;
+    const int h = e / j.items, it = e - h * j.items;
+    int c0, c1;
+    const bool turned = item_at<V>(A.r, j, it, c0, c1);
+    const T *src = reinterpret_cast<const T *>(j.in.p) + (int64_t)t0 * j.in.ts + (int64_t)h * j.in.hs;
+    T *dst = reinterpret_cast<T *>(j.out.p) + (int64_t)t0 * j.out.ts + (int64_t)h * j.out.hs;
+    const bool live = st0 < A.side && (A.parts == 1 || part * kThreads + (int)threadIdx.x < A.per_token);
+    Piece<T, V> x, y, nx, ny;
+    auto fetch = [&](int t) {
+        nx = ld<T, V>(src + (int64_t)t * j.in.ts + c0);
+        if (c1 >= 0) ny = ld<T, V>(src + (int64_t)t * j.in.ts + c1);
+    };
+    int t = st0;
+    if (live && t < n) fetch(t);
+    fill_table(A, cs, t0, n);
+    __syncthreads();
+    if (!live) return;
+#pragma unroll 1
+    for (; t < n; t += A.side) {
+        x = nx;
+        y = ny;
+        if (t + A.side < n) fetch(t + A.side);
+        if (turned) {
+            float a[V], b[V];
 #pragma unroll
-    for (int u = 0; u < kItems; ++u) {
-        const int i = u * kThreads + threadIdx.x;
-        pair[u] = -2;
-        if (i >= count) continue;
-        const int t = (e0 + i) / A.per_token;
-        int e = e0 + i - t * A.per_token;
-        const bool second = e >= na;
-        const RopeJob &j = second ? A.b : A.a;
-        e -= second ? na : 0;
-        const int h = e / j.items, it = e - h * j.items;
-        const bool turned = item_at<V>(A.r, j, it, c0[u], c1[u]);
-        const T *src = reinterpret_cast<const T *>(j.in.p) + (int64_t)(t0 + t) * j.in.ts + (int64_t)h * j.in.hs;
-        dst[u] = reinterpret_cast<T *>(j.out.p) + (int64_t)(t0 + t) * j.out.ts + (int64_t)h * j.out.hs;
-        x[u] = ld<T, V>(src + c0[u]);
-        if (c1[u] >= 0) y[u] = ld<T, V>(src + c1[u]);
-        pair[u] = turned ? t * A.r.half + V * it : -1;
+            for (int q = 0; q < V; ++q) { a[q] = tof(x.x[q]); b[q] = tof(y.x[q]); }
+            turn<V>(a, b, cs + t * A.r.half, V * it, A.r.inter, A.sgn);
+#pragma unroll
+            for (int q = 0; q < V; ++q) { x.x[q] = fromf<T>(a[q]); y.x[q] = fromf<T>(b[q]); }
+        }
+        st<T, V>(dst + (int64_t)t * j.out.ts + c0, x);
+        if (c1 >= 0) st<T, V>(dst + (int64_t)t * j.out.ts + c1, y);
+    }
+}
+
+// The gradient of a shared head: an item of a token is summed over the heads by `split` threads (heads s, s + split, ...),
+// whose sums meet in shared memory: one thread where there are items enough to fill the SMs, else kSplit.
+template <typename T, int V> __device__ void shared_block(const RopeArgs &A, float2 *cs, float *part) {
+    const RopeJob &j = A.b;
+    const int per = kThreads / A.split;                   // items at a time
+    const int rounds = (j.items + per - 1) / per;         // more than one: a token's items take several CTAs
+    const int round = (int)((blockIdx.x - A.main_blocks) % rounds);
+    const int t0 = (int)((blockIdx.x - A.main_blocks) / rounds) * A.shared_side, n = min(A.shared_side, A.T - t0);
+    const int slot = threadIdx.x % per, s = threadIdx.x / per, e = round * per + slot;
+    const int t = rounds > 1 ? 0 : e / j.items, it = rounds > 1 ? e : e - t * j.items;
+    const bool live = t < n && it < j.items;
+    int c0 = 0, c1 = -1;
+    const bool turned = item_at<V>(A.r, j, live ? it : 0, c0, c1);
+    float a[V], b[V];
+#pragma unroll
+    for (int q = 0; q < V; ++q) a[q] = b[q] = 0.f;
+    if (live) {
+        const T *src = reinterpret_cast<const T *>(j.in.p) + (int64_t)(t0 + t) * j.in.ts;
+#pragma unroll 4
+        for (int h = s; h < j.heads; h += A.split) {
+            const Piece<T, V> x = ld<T, V>(src + (int64_t)h * j.in.hs + c0);
+            Piece<T, V> y = x;
+            if (c1 >= 0) y = ld<T, V>(src + (int64_t)h * j.in.hs + c1);
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                a[q] += tof(x.x[q]);
+                b[q] += tof(y.x[q]);
+            }
+        }
     }
     fill_table(A, cs, t0, n);
     __syncthreads();
+    if (A.split > 1) {
 #pragma unroll
-    for (int u = 0; u < kItems; ++u) {
-        if (pair[u] == -2) continue;
-        if (pair[u] >= 0) {
-            float a[V], b[V];
-#pragma unroll
-            for (int e = 0; e < V; ++e) { a[e] = tof(x[u].x[e]); b[e] = tof(y[u].x[e]); }
-            turn<V>(a, b, cs, pair[u], A.r.inter, A.sgn);
-#pragma unroll
-            for (int e = 0; e < V; ++e) { x[u].x[e] = fromf<T>(a[e]); y[u].x[e] = fromf<T>(b[e]); }
-        }
-        st<T, V>(dst[u] + c0[u], x[u]);
-        if (c1[u] >= 0) st<T, V>(dst[u] + c1[u], y[u]);
-    }
-}
-
-// The gradient of a shared head: item i of the CTA's tokens is summed over the heads by kSplit
-// threads (heads s, s + kSplit, ...), whose sums meet in shared memory.
-template <typename T, int V> __device__ void shared_block(const RopeArgs &A, float2 *cs, float *part) {
-    const int t0 = (int)(blockIdx.x - A.main_blocks) * A.shared_tokens, n = min(A.shared_tokens, A.T - t0);
-    const RopeJob &j = A.b;
-    fill_table(A, cs, t0, n);
-    constexpr int kPer = kThreads / kSplit;               // items at a time
-    const int slot = threadIdx.x % kPer, s = threadIdx.x / kPer;
-    for (int base = 0; base < n * j.items; base += kPer) {
-        const int i = base + slot;
-        const bool live = i < n * j.items;
-        const int t = live ? i / j.items : 0, it = live ? i - t * j.items : 0;
-        int c0 = 0, c1 = -1;
-        const bool turned = item_at<V>(A.r, j, it, c0, c1);
-        float a[V], b[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) a[e] = b[e] = 0.f;
-        if (live) {
-            const T *src = reinterpret_cast<const T *>(j.in.p) + (int64_t)(t0 + t) * j.in.ts;
-#pragma unroll 4
-            for (int h = s; h < j.heads; h += kSplit) {
-                const Piece<T, V> x = ld<T, V>(src + (int64_t)h * j.in.hs + c0);
-                Piece<T, V> y = x;
-                if (c1 >= 0) y = ld<T, V>(src + (int64_t)h * j.in.hs + c1);
-#pragma unroll
-                for (int e = 0; e < V; ++e) { a[e] += tof(x.x[e]); b[e] += tof(y.x[e]); }
-            }
-        }
-        __syncthreads();                                  // the table is there; the last round's sums are read
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            part[(2 * e) * kThreads + threadIdx.x] = a[e];
-            part[(2 * e + 1) * kThreads + threadIdx.x] = b[e];
+        for (int q = 0; q < V; ++q) {
+            part[(2 * q) * kThreads + threadIdx.x] = a[q];
+            part[(2 * q + 1) * kThreads + threadIdx.x] = b[q];
         }
         __syncthreads();
-        if (s != 0 || !live) continue;
+        if (s != 0) return;
+        for (int k = 1; k < A.split; ++k) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            for (int k = 1; k < kSplit; ++k) {
-                a[e] += part[(2 * e) * kThreads + k * kPer + slot];
-                b[e] += part[(2 * e + 1) * kThreads + k * kPer + slot];
+            for (int q = 0; q < V; ++q) {
+                a[q] += part[(2 * q) * kThreads + k * per + slot];
+                b[q] += part[(2 * q + 1) * kThreads + k * per + slot];
             }
         }
-        if (turned) turn<V>(a, b, cs, t * A.r.half + V * it, A.r.inter, A.sgn);
-        T *dst = reinterpret_cast<T *>(j.out.p) + (int64_t)(t0 + t) * j.out.ts;
-        Piece<T, V> x, y;
-#pragma unroll
-        for (int e = 0; e < V; ++e) { x.x[e] = fromf<T>(a[e]); y.x[e] = fromf<T>(b[e]); }
-        st<T, V>(dst + c0, x);
-        if (c1 >= 0) st<T, V>(dst + c1, y);
     }
+    if (!live) return;
+    if (turned) turn<V>(a, b, cs + t * A.r.half, V * it, A.r.inter, A.sgn);
+    T *dst = reinterpret_cast<T *>(j.out.p) + (int64_t)(t0 + t) * j.out.ts;
+    Piece<T, V> x, y;
+#pragma unroll
+    for (int q = 0; q < V; ++q) { x.x[q] = fromf<T>(a[q]); y.x[q] = fromf<T>(b[q]); }
+    st<T, V>(dst + c0, x);
+    if (c1 >= 0) st<T, V>(dst + c1, y);
 }
 
-template <typename T, int V> __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs A) {
+// SHARED: the shared sums' CTAs follow the plain ones in one launch (a kernel of its own: the plain path alone takes half the registers)
+template <typename T, int V, bool SHARED> __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant__ RopeArgs A) {
     extern __shared__ float2 cs[];
-    if (blockIdx.x < A.main_blocks) plain_block<T, V>(A, cs);
-    else shared_block<T, V>(A, cs, reinterpret_cast<float *>(cs + A.table));
+    if (!SHARED || blockIdx.x < A.main_blocks) plain_block<T, V>(A, cs);
+    else if constexpr (SHARED) shared_block<T, V>(A, cs, reinterpret_cast<float *>(cs + A.table));
 }
 
 RopeJob make_job(const k3mla_view *in, const k3mla_view *out, int H, int d, const Rope &r, int V, bool in_place) {
@@ -241,31 +249,46 @@ cudaError_t launch_rope(const k3mla_view *q, const k3mla_view *q_out, int Hq, co
     A.a = make_job(q, q_out, Hq, d, r, V, Hq && same(q, q_out));
     A.b = make_job(k, k_out, Hk, d, r, V, Hk && !shared && same(k, k_out));
     A.per_token = A.a.heads * A.a.items + (shared ? 0 : A.b.heads * A.b.items);
-    // a CTA's items, fewer where many tokens' tables would not fit
+    // Tokens a thread goes through: as many as leave several CTAs for each SM (up to kTokens), and fit the table.
     const int fit = r.half > 0 ? kTable / r.half : 1 << 20;
-    const long long most = (long long)(fit - 2) * A.per_token;
-    A.block_items = (int)(most < kThreads * kItems ? most : kThreads * kItems);
-    const long long main_blocks = A.per_token ? ((long long)T * A.per_token + A.block_items - 1) / A.block_items : 0;
-    int spans = A.per_token ? A.block_items / A.per_token + 2 : 0;
-    // shared sums: as many tokens as fill kThreads / kSplit items
-    A.shared_tokens = 1;
-    long long shared_blocks = 0;
-    if (shared) {
-        A.shared_tokens = kThreads / kSplit / A.b.items;
-        A.shared_tokens = A.shared_tokens < 1 ? 1 : A.shared_tokens > fit ? fit : A.shared_tokens;
-        shared_blocks = (T + A.shared_tokens - 1) / A.shared_tokens;
-        spans = spans > A.shared_tokens ? spans : A.shared_tokens;
+    auto depth = [&](long long ctas_at_one, int side) {
+        long long d = ctas_at_one / (152 * 8);
+        d = d < 1 ? 1 : d > kTokens ? kTokens : d;
+        while (d > 1 && d * side > fit) --d;
+        return (int)d;
+    };
+    long long main_blocks = 0, shared_blocks = 0;
+    int table_tokens = 0;
+    if (A.per_token) {
+        A.parts = (A.per_token + kThreads - 1) / kThreads;
+        A.side = A.parts > 1 ? 1 : kThreads / A.per_token;
+        A.side = A.side > fit ? fit : A.side;
+        const long long rows = ((long long)T + A.side - 1) / A.side;
+        A.tokens = A.side * depth(rows * A.parts, A.side);
+        main_blocks = ((long long)T + A.tokens - 1) / A.tokens * A.parts;
+        table_tokens = A.tokens;
     }
-    A.table = r.half * (spans < T ? spans : T);
+    if (shared) {
+        // one thread an item reads at 16-byte pieces in flight alone from 512 threads an SM on; below, kSplit of them share it
+        A.split = (long long)T * A.b.items >= 152 * 512 ? 1 : kSplit;
+        const int per = kThreads / A.split, rounds = (A.b.items + per - 1) / per;
+        A.shared_side = rounds > 1 ? 1 : per / A.b.items;
+        A.shared_side = A.shared_side > fit ? fit : A.shared_side;
+        shared_blocks = ((long long)T + A.shared_side - 1) / A.shared_side * rounds;
+        table_tokens = table_tokens > A.shared_side ? table_tokens : A.shared_side;
+    }
+    A.table = r.half * (table_tokens < T ? table_tokens : T);
     const size_t smem = (size_t)A.table * sizeof(float2) + (shared ? (size_t)2 * V * kThreads * sizeof(float) : 0);
     if (main_blocks + shared_blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (main_blocks + shared_blocks == 0) return cudaSuccess;      // everything in place and nothing to turn
     A.main_blocks = (unsigned)main_blocks;
     const unsigned grid = (unsigned)(main_blocks + shared_blocks);
-    if (bf16 && V > 1) rope_kernel<__nv_bfloat16, 8><<<grid, kThreads, smem, s>>>(A);
-    else if (bf16) rope_kernel<__nv_bfloat16, 1><<<grid, kThreads, smem, s>>>(A);
-    else if (V > 1) rope_kernel<float, 4><<<grid, kThreads, smem, s>>>(A);
-    else rope_kernel<float, 1><<<grid, kThreads, smem, s>>>(A);
+    void (*fn)(const RopeArgs);
+    if (bf16) fn = V > 1 ? (shared ? rope_kernel<__nv_bfloat16, 8, true> : rope_kernel<__nv_bfloat16, 8, false>)
+                         : (shared ? rope_kernel<__nv_bfloat16, 1, true> : rope_kernel<__nv_bfloat16, 1, false>);
+    else fn = V > 1 ? (shared ? rope_kernel<float, 4, true> : rope_kernel<float, 4, false>)
+                    : (shared ? rope_kernel<float, 1, true> : rope_kernel<float, 1, false>);
+    fn<<<grid, kThreads, smem, s>>>(A);
     count_launch();
     return cudaGetLastError();
 }
