@@ -3,10 +3,11 @@
 
 namespace k3kda {
 
-#ifndef XR
-#define XR 16
-#endif
-static constexpr int kRowsFrom = XR;
+// From how many query rows of a key head on blocks of 128 rows take over from blocks of 8.  The latter's time grows with every
+// 8 rows, the former's hardly up to 128.  Measured on 32 sequences of 4000 keys, 4 heads of 128 + 128 channels, 8-row blocks
+// against 128-row blocks: 4-bit pages 109 against 155 us at 40 rows, 144 against 162 at 56, 199 against 172 at 80; 192 + 128 channels
+// (16 sequences) 95 against 98 at 32, 136 against 107 at 48; bf16 pages 96 against 97 at 16, 135 against 100 at 24.
+static int rows_from(bool i4, int dqk) { return !i4 ? 16 : dqk <= 128 ? 56 : 32; }
 
 // whether blocks of 128 rows fit tensor memory
 static bool wide_ok(int dqk, int dv) { return dqk <= 192 && dv <= 128; }
@@ -36,11 +37,10 @@ cudaError_t launch_paged_attend(const k3mla_paged_cache *c, const k3mla_view *q,
     A.counters = A.status + 64;
     A.partial = reinterpret_cast<float *>(static_cast<char *>(ws) + attend::kHeadBytes);
     if (!cu) max_new = 1;
-    // Four rows at a time where no sequence has more (half the products and registers), else eight; from kRowsFrom rows on blocks
-    // of 128 on tcgen05, whose rows beyond the sequence's cost nothing more.
+    // four rows at a time where no sequence has more (half the products and registers), else eight, else blocks of 128 on tcgen05
     const long long rows = (long long)max_new * A.G;
     const bool i4 = c->format == K3MLA_CACHE_I4;
-    if (rows > kRowsFrom && wide_ok(c->dqk, c->dv)) return i4 ? attend::run_i4_rows(c->dqk, c->dv, A, s) : attend::run_bf16_rows(c->dqk, c->dv, A, s);
+    if (rows > rows_from(i4, c->dqk) && wide_ok(c->dqk, c->dv)) return i4 ? attend::run_i4_rows(c->dqk, c->dv, A, s) : attend::run_bf16_rows(c->dqk, c->dv, A, s);
     if (i4) return rows <= 4 ? attend::run_i4_r4(c->dqk, c->dv, A, max_new, s) : attend::run_i4_r8(c->dqk, c->dv, A, max_new, s);
     return rows <= 4 ? attend::run_bf16_r4(c->dqk, c->dv, A, max_new, s) : attend::run_bf16_r8(c->dqk, c->dv, A, max_new, s);
 }

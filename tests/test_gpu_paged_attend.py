@@ -374,3 +374,36 @@ def test_blocks_of_rows_values_of_every_size():
     _check(c.run(), _long(c), tol)
     c = Case([700], [40], 1, 1, 128, 128, 64, "i4", seed=11, edit=lambda n, rows: rows[..., 128:].__imul__(1e-4))
     _check(c.run(), _long(c), c._bound(0, _np(c.q), 40))
+
+
+MORE_ROWS = [  # blocks of 128 rows for 4-bit pages too: more than 56 rows (32 beyond 128 key channels)
+    ([64], [57], 1, 1, 64, 64, 16, (0, 0, "half"), False),
+    ([63, 1, 200], [1, 1, 1], 2, 60, 128, 128, 48, (128, 0, "half"), True),
+    ([300, 130], [16, 5], 2, 8, 64, 128, 16, (34, 5, "interleaved"), True),
+    ([40, 257], [9, 3], 3, 13, 192, 64, 32, (64, 128, "half"), False),
+    ([128, 129, 127], [128, 64, 127], 1, 1, 128, 64, 128, (32, 16, "interleaved"), False)]
+
+
+@pytest.mark.parametrize("case", MORE_ROWS, ids=str)
+@pytest.mark.parametrize("fmt", ["i4", "bf16"])
+def test_more_blocks_of_rows_against_the_64_bit_form(case, fmt):
+    total, new, heads, group, dqk, dv, page, rope, gate = case
+    c = Case(total, new, heads, group, dqk, dv, page, fmt, rope, torch.bfloat16, gate, seed=sum(new))
+    want, tol = c.want()
+    for out in (torch.float32, torch.bfloat16):
+        _check(c.run(out), want, tol, out)
+
+
+def test_more_blocks_of_rows_long_shared_and_of_every_size():
+    def edit(n, rows):
+        r = np.random.default_rng(9)
+        rows[..., 128:] *= 10.0 ** r.integers(-5, 4, rows.shape[:2] + (1,))
+        rows[..., :128] *= 6
+    for total, new, heads, group, kw in (([30000], [8], 1, 8, {}), ([900] * 20, [10] * 20, 4, 6, {}), ([3000, 90], [9, 20], 2, 8, dict(edit=edit)),
+                                         ([700], [80], 1, 1, dict(edit=lambda n, rows: rows[..., 128:].__imul__(1e-4)))):
+        c = Case(total, new, heads, group, 128, 128, 64, "i4", seed=23, **kw)
+        tol = np.concatenate([c._bound(n, _np(c.q[int(c.cu[n]):int(c.cu[n + 1])]), m) for n, m in enumerate(new)])
+        ws = K.paged_attend_workspace(c.cache, heads * group)
+        got = c.run(ws=ws)
+        _check(got, _long(c), tol)
+        assert torch.equal(got, c.run(ws=ws)) and not ws[256:4352].any()
