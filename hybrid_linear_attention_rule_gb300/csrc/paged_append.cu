@@ -33,6 +33,7 @@ constexpr int kTokens = 16;               // most tokens of a CTA
 // and sine are off by at most 1.7e-7 each: 2^-24 from sincospif (1 ulp below 1), 4.7e-8 from the angle's own rounding
 // (at most 1/8 turn, 24 bits), 2^-24 from the factor mscale; two products add 2^-24 of one and 2^-24 sqrt(2) of the sum.
 constexpr float kSlack = 4.8e-7f;
+constexpr float kSlackPlain = 3.6e-7f;    // without the factor: 1.1e-7 each
 
 struct AppendArgs {
     Paged P;
@@ -167,8 +168,12 @@ __device__ __forceinline__ double half_sat(double x) {
     return (double)__half2float(__double2half(x));
 }
 
-// Whether the fp16 rounding of some value within d of x may differ from that of x.
-__device__ __forceinline__ bool half_unsure(float x, float d) { return half_sat(x - d) != half_sat(x + d); }
+// Whether the fp16 rounding h of x may differ from that of some value within d of x: x lies that close to the middle of two
+// fp16 numbers, half their spacing (2^-11 of x's power of two, 2^-25 at least) away from h.
+__device__ __forceinline__ bool half_unsure(float x, float h, float d) {
+    const float gap = fmaxf(__uint_as_float((__float_as_uint(x) & 0x7f800000u) - (11u << 23)), 2.9802322e-8f);
+    return fabsf(fabsf(x - h) - gap) <= d;
+}
 
 // A group in double by the whole warp: lane l takes channels 2l and 2l + 1 of the plane.  src: the (token, head) row's
 // key or value; c0: the plane's first channel in it.
@@ -366,13 +371,13 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
             if (any_turned) {
                 mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
                 mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
-                err = turned ? fabsf(A.r.mscale) * mag * kSlack : 0.f;
+                err = turned ? fabsf(A.r.mscale) * mag * (A.r.mscale == 1.f ? kSlackPlain : kSlack) : 0.f;
             }
             const bool bad = !(hi - lo < INFINITY);       // a NaN or an infinity (or a range past FP32's)
             const float m = half_sat(lo), range = fmaxf(hi - m, 0.f);
             const float sraw = range * (1.f / 15.f), s = half_sat(sraw);
             // what FP32 leaves open: the minimum, and the scale (its own roundings are within 2^-22 of it)
-            const bool open_scale = half_unsure(sraw, fmaf(sraw, 2.4e-7f, err * 0.14f)) || (err > 0.f && half_unsure(lo, err));
+            const bool open_scale = half_unsure(sraw, s, fmaf(sraw, 2.4e-7f, err * 0.14f)) || (err > 0.f && half_unsure(lo, m, err));
             float inv;
             asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
             const float nm = -m * inv;
@@ -398,8 +403,8 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
                 float h[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const float2 a = up(cd[2 * q]), b = up(cd[2 * q + 1]);
-                    h[q] = fmaf(fmaf(fmaf(b.y, 16.f, b.x), 16.f, a.y), 16.f, a.x) + 8388608.f;
+                    const float2 u = up(fma2(cd[2 * q + 1], pk(256.f, 256.f), cd[2 * q]));
+                    h[q] = fmaf(u.y, 16.f, u.x) + 8388608.f;
                 }
                 word.x = __byte_perm(__float_as_uint(h[0]), __float_as_uint(h[1]), 0x5410);
                 word.y = __byte_perm(__float_as_uint(h[2]), __float_as_uint(h[3]), 0x5410);
