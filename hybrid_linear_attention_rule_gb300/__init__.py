@@ -515,7 +515,19 @@ class RopeTable:
 
     def __init__(self, phase, dim, offset, layout, mscale):
         self.phase, self.dim, self.offset, self.layout, self.mscale = phase, dim, offset, layout, mscale
-        self._args = _RopeArgs(phase.data_ptr(), dim, offset, _LAYOUTS[layout], mscale)
+        self._args = _RopeArgs(phase.data_ptr(), dim, offset, _named(_LAYOUTS, layout, "layout"), mscale)
+
+    def __setattr__(self, name, value):
+        if hasattr(self, "_args"):
+            raise AttributeError("k3mla: a RopeTable is fixed; make another")
+        super().__setattr__(name, value)
+
+
+def _named(names, key, what):
+    try:
+        return names[key]
+    except KeyError:
+        raise ValueError(f"k3mla: {what} is one of {sorted(names)}, not {key!r}") from None
 
 
 def k3mla_rope_table(dim, theta, scaling="none", factor=1.0, original_length=0.0, beta_fast=32.0, beta_slow=1.0):
@@ -523,7 +535,7 @@ def k3mla_rope_table(dim, theta, scaling="none", factor=1.0, original_length=0.0
     lib = load_library()
     phase = torch.zeros(max(int(dim) // 2, 1), dtype=torch.int64)
     mscale = ctypes.c_float(1.0)
-    st = lib.k3mla_rope_table(int(dim), float(theta), _SCALINGS[scaling], float(factor), float(original_length),
+    st = lib.k3mla_rope_table(int(dim), float(theta), _named(_SCALINGS, scaling, "scaling"), float(factor), float(original_length),
                               float(beta_fast), float(beta_slow), phase.data_ptr(), ctypes.byref(mscale))
     _check("k3mla_rope_table", st)
     return phase, mscale.value
@@ -628,6 +640,12 @@ class PagedCache:
         self._args = _PagedArgs(pool.data_ptr(), tab, lens, _host_i32(block_table_host, "block_table_host"),
                                 _host_i32(kv_len_host, "kv_len_host"), _FORMATS.get(fmt, fmt), pool.shape[0], page_size, width, N,
                                 pool.shape[1], dqk, dv)
+
+    def __setattr__(self, name, value):
+        # the calls take the addresses that were given first
+        if hasattr(self, "_args"):
+            raise AttributeError("k3mla: a PagedCache's tensors are fixed; write to them in place, or make another")
+        super().__setattr__(name, value)
 
 
 def _packing(cache, cu_seqlens, cu_seqlens_host):

@@ -222,3 +222,14 @@ def test_attend_refusals(lib):
     assert need % 16 == 0 and need > 0
     for bad in ((3, 2, 128, 128), (4, 0, 128, 128), (4, 2, 100, 128), (4, 2, 128, 192)):
         assert K.k3mla_paged_attend_workspace_size(*bad) == 0
+
+
+def test_handles_are_fixed_and_names_are_checked():
+    import torch
+    table = K.RopeTable(torch.zeros(32, dtype=torch.int64), 64, 0, "half", 1.0)
+    with pytest.raises(AttributeError):
+        table.phase = None
+    with pytest.raises(ValueError):
+        K.RopeTable(torch.zeros(32, dtype=torch.int64), 64, 0, "quarter", 1.0)
+    with pytest.raises(ValueError):
+        K.k3mla_rope_table(64, 10000.0, scaling="other")
