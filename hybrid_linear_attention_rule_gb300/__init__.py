@@ -548,47 +548,63 @@ def rope_table(dim, theta=10000.0, offset=0, layout="half", scaling="none", fact
     return RopeTable(phase.to(device), int(dim), int(offset), layout, mscale)
 
 
-def _rope_call(name, q, q_out, k, k_out, k_heads_out, positions, table, stream, *shared):
-    """Checks that belong to tensors, then the library's call."""
+def _dense(shape, dtype, device, stream):
+    """A new [tokens, heads, channels] output and its view (nothing about it needs a check)."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t, _View(t.data_ptr(), shape[1] * shape[2], shape[2])
+
+
+def _rope_call(name, q, qo, k, ko, positions, table, stream, *shared):
+    """The library's call on inputs q, k and the outputs' views qo, ko."""
     T, hq, d = q.shape
-    dt = q.dtype
-    if q_out.shape != q.shape or q_out.dtype != dt:
-        raise ValueError("k3mla: the first output has another shape or type than its input")
-    kv = ko = None
-    hk = 0
+    dt = _dtype(q)
+    kv, hk = None, 0
     if k is not None:
-        hk = k.shape[1]
-        if k.shape[0] != T or k.shape[2] != d or k.dtype != dt:
+        tk, hk, dk = k.shape
+        if tk != T or dk != d or k.dtype != q.dtype:
             raise ValueError("k3mla: the two inputs differ in tokens, channels or type")
-        if k_out.shape != (T, hk if k_heads_out is None else k_heads_out, d) or k_out.dtype != dt:
-            raise ValueError("k3mla: the second output has the wrong shape or type")
-        kv, ko = _view(k, "k"), _view(k_out, "k_out")
-    qv, qo = _view(q, "q"), _view(q_out, "q_out")
-    pos = _i32(positions, "positions", (T,))
-    st = getattr(_lib or load_library(), name)(qv, qo, hq, kv, ko, hk, *shared, _dtype(q), pos, T, d, table._args,
-                                               _raw_stream(stream, q))
+        kv = _view(k, "k")
+    qv = _view(q, "q")
+    st = getattr(_lib or load_library(), name)(qv, qo, hq, kv, ko, hk, *shared, dt, _i32(positions, "positions", (T,)), T, d,
+                                               table._args, _raw_stream(stream, q))
     if st:
         _check(name, st)
 
 
+def _rope_checked(name, q, q_out, k, k_out, k_heads_out, positions, table, stream, *shared):
+    """The same with outputs that the caller gave."""
+    if q_out.shape != q.shape or q_out.dtype != q.dtype:
+        raise ValueError("k3mla: the first output has another shape or type than its input")
+    if k is not None and (k_out.shape != (k.shape[0], k.shape[1] if k_heads_out is None else k_heads_out, k.shape[2]) or k_out.dtype != k.dtype):
+        raise ValueError("k3mla: the second output has the wrong shape or type")
+    _rope_call(name, q, _view(q_out, "q_out"), k, None if k is None else _view(k_out, "k_out"), positions, table, stream, *shared)
+
+
 def k3mla_rope(q, q_out, k, k_out, positions, table, stream=None):
     """Rotate q [T, Hq, d] -> q_out and k [T, Hk, d] -> k_out (None: no k); an output may be its input."""
-    _rope_call("k3mla_rope", q, q_out, k, k_out, None, positions, table, stream)
+    _rope_checked("k3mla_rope", q, q_out, k, k_out, None, positions, table, stream)
 
 
 def k3mla_rope_backward(dq_out, dq, dk_out, dk, k_shared, positions, table, stream=None):
     """The gradient of k3mla_rope; k_shared: k was one head for all, dk [T, 1, d] is the sum over heads."""
-    _rope_call("k3mla_rope_backward", dq_out, dq, dk_out, dk, 1 if k_shared else None, positions, table, stream,
-               1 if k_shared else 0)
+    _rope_checked("k3mla_rope_backward", dq_out, dq, dk_out, dk, 1 if k_shared else None, positions, table, stream,
+                  1 if k_shared else 0)
 
 
 def rope(q, positions, table, k=None, out=None, stream=None):
     """q [T, Hq, d] (and k [T, Hk, d]) turned by positions int32 [T].  Returns q's rotation, or (q's, k's);
     `out` (a tensor, or a pair with k) may be the inputs themselves.  Inputs may be strided views."""
     if out is None:
-        dev = q.device
-        out = _empty(q.shape, q.dtype, dev, stream)
-        out = out if k is None else (out, _empty(k.shape, k.dtype, dev, stream))
+        dev, dt = q.device, q.dtype
+        qo, qv = _dense(q.shape, dt, dev, stream)
+        if k is None:
+            _rope_call("k3mla_rope", q, qv, None, None, positions, table, stream)
+            return qo
+        ko, kv = _dense(k.shape, dt, dev, stream)
+        _rope_call("k3mla_rope", q, qv, k, kv, positions, table, stream)
+        return qo, ko
     qo, ko = (out, None) if k is None else out
     k3mla_rope(q, qo, k, ko, positions, table, stream)
     return out
@@ -596,12 +612,15 @@ def rope(q, positions, table, k=None, out=None, stream=None):
 
 def rope_backward(dq_out, positions, table, dk_out=None, k_shared=False, stream=None):
     """Gradients of rope's inputs: dq, or (dq, dk); with k_shared dk is [T, 1, d], the sum over heads."""
-    dq = _empty(dq_out.shape, dq_out.dtype, dq_out.device, stream)
-    dk = None
-    if dk_out is not None:
-        dk = _empty((dk_out.shape[0], 1 if k_shared else dk_out.shape[1], dk_out.shape[2]), dk_out.dtype, dk_out.device, stream)
-    k3mla_rope_backward(dq_out, dq, dk_out, dk, k_shared, positions, table, stream)
-    return dq if dk is None else (dq, dk)
+    dev, dt = dq_out.device, dq_out.dtype
+    dq, qv = _dense(dq_out.shape, dt, dev, stream)
+    if dk_out is None:
+        _rope_call("k3mla_rope_backward", dq_out, qv, None, None, positions, table, stream, 0)
+        return dq
+    T, H, d = dk_out.shape
+    dk, kv = _dense((T, 1 if k_shared else H, d), dt, dev, stream)
+    _rope_call("k3mla_rope_backward", dq_out, qv, dk_out, kv, positions, table, stream, 1 if k_shared else 0)
+    return dq, dk
 
 
 def k3mla_paged_block_bytes(fmt, page_size, dqk, dv) -> int:
@@ -688,10 +707,13 @@ paged_append = k3mla_paged_append
 
 def paged_read(cache, tokens, cu_seqlens=None, out_dtype=torch.bfloat16, stream=None):
     """The last `tokens` packed rows (all sequences together) as values: (k [tokens, heads, dqk], v [tokens, heads, dv])."""
-    dev = cache.pool.device
-    k = _empty((tokens, cache.heads, cache.dqk), out_dtype, dev, stream)
-    v = _empty((tokens, cache.heads, cache.dv), out_dtype, dev, stream)
-    k3mla_paged_read(cache, k, v, cu_seqlens, None, stream)
+    dev, heads = cache.pool.device, cache.heads
+    k, kv = _dense((tokens, heads, cache.dqk), out_dtype, dev, stream)
+    v, vv = _dense((tokens, heads, cache.dv), out_dtype, dev, stream)
+    cu, _ = _packing(cache, cu_seqlens, None)
+    st = (_lib or load_library()).k3mla_paged_read(cache._args, kv, vv, _dtype(k), cu, None, tokens, _raw_stream(stream, k))
+    if st:
+        _check("k3mla_paged_read", st)
     return k, v
 
 

@@ -27,8 +27,9 @@ namespace k3kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kGroups = kThreads / 4;     // groups of a CTA
-constexpr int kTokens = 16;               // most tokens of a CTA
+constexpr int kGroups = kThreads / 4;     // most groups of a CTA
+constexpr int kDepth = 16;                // most tokens a lane goes through
+constexpr int kTokens = 128;              // most tokens of a CTA
 // Bound on the FP32 error of a turned channel, relative to the largest of the pair's two channels (times mscale).  The cosine
 // and sine are off by at most 1.7e-7 each: 2^-24 from sincospif (1 ulp below 1), 4.7e-8 from the angle's own rounding
 // (at most 1/8 turn, 24 bits), 2^-24 from the factor mscale; two products add 2^-24 of one and 2^-24 sqrt(2) of the sum.
@@ -42,7 +43,9 @@ struct AppendArgs {
     int T;
     Rope r;
     int tokens;                           // tokens of a CTA
-    int parts;                            // CTAs that share the same tokens: kGroups of their heads * planes groups each
+    int parts;                            // CTAs that share the same tokens
+    int groups;                           // groups of a CTA: its share of heads * planes, at most kGroups
+    int warps, side;                      // warps for them, and how many tokens lie side by side (warps * side <= 8)
 };
 
 struct Place {                            // where a CTA's token goes; page < 0: nowhere
@@ -67,7 +70,7 @@ __device__ __forceinline__ int find_seq(const int32_t *cu, int N, int t, int lan
 // One warp per token of the CTA: its place.  A malformed cu_seqlens cannot send it outside the table.
 __device__ __forceinline__ void find_places(const Paged &P, const int32_t *cu, int T, int t0, int count, Place *place) {
     const int lane = threadIdx.x & 31;
-    for (int i = threadIdx.x >> 5; i < count; i += kThreads / 32) {
+    for (int i = threadIdx.x >> 5; i < count; i += (int)blockDim.x >> 5) {
         const int t = t0 + i;
         const int n = cu ? find_seq(cu, P.N, t, lane) : t;
         if (lane == 0) {
@@ -245,8 +248,9 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
     find_places(P, A.cu, A.T, t0, n, place);
     // this lane's group: plane-major, so that a warp holds one plane of several heads
     const int kplanes = P.dqk / 64, lane4 = threadIdx.x & 3;
-    const int gi = part * kGroups + (threadIdx.x >> 2);
-    const bool inside = gi < P.heads * P.planes;
+    const int row_set = (int)(threadIdx.x >> 5) / A.warps, mine = ((int)(threadIdx.x >> 5) - row_set * A.warps) * 8 + (int)(threadIdx.x & 31) / 4;
+    const int gi = part * A.groups + mine;
+    const bool inside = mine < A.groups && gi < P.heads * P.planes;
     const int plane = inside ? gi / P.heads : 0, head = inside ? gi - plane * P.heads : 0;
     const bool key = plane < kplanes;
     const int c0 = 64 * (key ? plane : plane - kplanes), c = c0 + 16 * lane4;
@@ -266,9 +270,9 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
         if (mode0 == kFirst || mode0 == kSecond) y0.load(p + (mode0 == kFirst ? c + A.r.half : c - A.r.half));
         if (mode1 == kFirst || mode1 == kSecond) y1.load(p + 8 + (mode1 == kFirst ? c + A.r.half : c - A.r.half));
     };
-    if (inside) fetch(0);
+    if (inside && row_set < n) fetch(row_set);
     __syncthreads();
-    for (int i = threadIdx.x; i < n * A.r.half; i += kThreads) {
+    for (int i = threadIdx.x; i < n * A.r.half; i += blockDim.x) {
         const int t = i / A.r.half, p = i - t * A.r.half;
         const float2 v = rope_cs(A.r.phase[p], place[t].pos);
         table[t * tab_row + p] = v.x * A.r.mscale;
@@ -276,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
     }
     __syncthreads();
 #pragma unroll 1
-    for (int t = 0; t < n; ++t) {
+    for (int t = row_set; t < n; t += A.side) {
         const Place w = place[t];
         F2 x[8];
         float mag = 0.f;                                  // largest channel of the lane's pairs that turn
@@ -322,14 +326,14 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
                 }
             }
         };
-        if (w.page < 0) {                                 // (the CTA agrees on it)
-            if (inside && t + 1 < n) fetch(t + 1);
+        if (w.page < 0) {                                 // (the warp agrees on it)
+            if (inside && t + A.side < n) fetch(t + A.side);
             continue;
         }
         if (inside) {
             turn(r0, y0, mode0, c, x);
             turn(r1, y1, mode1, c + 8, x + 4);
-            if (t + 1 < n) fetch(t + 1);
+            if (t + A.side < n) fetch(t + A.side);
         } else {
 #pragma unroll
             for (int q = 0; q < 8; ++q) x[q] = 0;
@@ -512,8 +516,9 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
     find_places(P, A.cu, A.T, t0, n, place);
     __syncthreads();
     const int kplanes = P.dqk / 64, lane4 = threadIdx.x & 3;
-    const int gi = part * kGroups + (threadIdx.x >> 2);
-    if (gi >= P.heads * P.planes) return;
+    const int row_set = (int)(threadIdx.x >> 5) / A.warps, mine = ((int)(threadIdx.x >> 5) - row_set * A.warps) * 8 + (int)(threadIdx.x & 31) / 4;
+    const int gi = part * A.groups + mine;
+    if (mine >= A.groups || gi >= P.heads * P.planes || row_set >= n) return;
     // plane-fastest here: neighbouring lanes write neighbouring channels
     const int head = gi / P.planes, plane = gi - head * P.planes;
     const bool key = plane < kplanes;
@@ -538,10 +543,10 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
         }
     };
     Held now, next;
-    fetch(0, now);
+    fetch(row_set, now);
 #pragma unroll 1
-    for (int t = 0; t < n; ++t) {
-        if (t + 1 < n) fetch(t + 1, next);
+    for (int t = row_set; t < n; t += A.side) {
+        if (t + A.side < n) fetch(t + A.side, next);
         F2 x[2][4];
         if (place[t].page < 0) {
 #pragma unroll
@@ -568,12 +573,22 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
     }
 }
 
-// Tokens of a CTA: as many (up to kTokens) as leave about 8 CTAs for each SM; the search for their places, their angles and
-// a lane's addresses are shared by them.
-void plan(AppendArgs &A, unsigned &grid) {
-    A.parts = (A.P.heads * A.P.planes + kGroups - 1) / kGroups;
-    const long long tokens = (long long)A.T * A.parts / (152 * 8);
-    A.tokens = tokens < 1 ? 1 : tokens > kTokens ? kTokens : (int)tokens;
+// A CTA's groups (an equal share of heads * planes), its warps and tokens.  A lane goes through as many tokens (up to
+// kDepth) as leave about 16 CTAs for each SM (three are resident; with 8, prompts in bf16 took 56 us instead of 49); the search for their places, their angles and a lane's addresses are shared by
+// them.  With few groups several tokens lie side by side.
+void plan(AppendArgs &A, unsigned &grid, unsigned &threads, size_t &table) {
+    const int all = A.P.heads * A.P.planes;
+    A.parts = (all + kGroups - 1) / kGroups;
+    A.groups = (all + A.parts - 1) / A.parts;
+    A.warps = (A.groups + 7) / 8;
+    A.side = kThreads / 32 / A.warps;
+    const size_t row = 2 * (size_t)((A.r.half + 3) & ~3) * sizeof(float);
+    long long depth = (long long)A.T * A.parts / ((long long)A.side * 152 * 16);
+    depth = depth < 1 ? 1 : depth > kDepth ? kDepth : depth;
+    while (depth > 1 && (depth * A.side > kTokens || depth * A.side * row > 32768)) --depth;
+    A.tokens = (int)depth * A.side;
+    table = A.tokens * row;
+    threads = (unsigned)(A.warps * A.side * 32);
     grid = (unsigned)(((long long)A.T + A.tokens - 1) / A.tokens * A.parts);
 }
 
@@ -588,8 +603,9 @@ cudaError_t launch_paged_append(const k3mla_paged_cache *c, const k3mla_view *k,
     A.cu = cu;
     A.T = T;
     A.r = make_rope(rope);
-    unsigned grid;
-    plan(A, grid);
+    unsigned grid, threads;
+    size_t table;
+    plan(A, grid, threads, table);
     const int size = bf16 ? 2 : 4;
     const bool vec = view_vec(k, size, T, c->heads) && view_vec(v, size, T, c->heads), i4 = c->format == K3MLA_CACHE_I4;
     void (*fn)(const AppendArgs);
@@ -597,7 +613,7 @@ cudaError_t launch_paged_append(const k3mla_paged_cache *c, const k3mla_view *k,
                        : (i4 ? append_kernel<__nv_bfloat16, false, true> : append_kernel<__nv_bfloat16, false, false>);
     else fn = vec ? (i4 ? append_kernel<float, true, true> : append_kernel<float, true, false>)
                   : (i4 ? append_kernel<float, false, true> : append_kernel<float, false, false>);
-    fn<<<grid, kThreads, (size_t)A.tokens * 2 * ((A.r.half + 3) & ~3) * sizeof(float), s>>>(A);
+    fn<<<grid, threads, table, s>>>(A);
     count_launch();
     return cudaGetLastError();
 }
@@ -611,8 +627,9 @@ cudaError_t launch_paged_read(const k3mla_paged_cache *c, const k3mla_view *k, c
     A.cu = cu;
     A.T = T;
     A.r = make_rope(nullptr);
-    unsigned grid;
-    plan(A, grid);
+    unsigned grid, threads;
+    size_t table;
+    plan(A, grid, threads, table);
     const int size = bf16 ? 2 : 4;
     const bool vec = (!k || view_vec(k, size, T, c->heads)) && (!v || view_vec(v, size, T, c->heads)), i4 = c->format == K3MLA_CACHE_I4;
     void (*fn)(const AppendArgs);
@@ -620,7 +637,7 @@ cudaError_t launch_paged_read(const k3mla_paged_cache *c, const k3mla_view *k, c
                        : (i4 ? read_kernel<__nv_bfloat16, false, true> : read_kernel<__nv_bfloat16, false, false>);
     else fn = vec ? (i4 ? read_kernel<float, true, true> : read_kernel<float, true, false>)
                   : (i4 ? read_kernel<float, false, true> : read_kernel<float, false, false>);
-    fn<<<grid, kThreads, 0, s>>>(A);
+    fn<<<grid, threads, 0, s>>>(A);
     count_launch();
     return cudaGetLastError();
 }
