@@ -19,6 +19,11 @@
 //     rounding error of x - m.  Ties are common there (bf16 values): one group in 30.
 //   - Else (turned channels, FP32 errors of up to kSlack of the pair; about one group in 500) the warp repeats the group in
 //     double, two channels a lane, with the angle's sine and cosine in double.
+//
+// Measured (26,339 prompt tokens, 32 heads of 128 + 128 channels): append 250 us for 492 MB, where instruction issue is the bound
+// (56 M warp instructions for a quarter of it, HBM at a fifth of its rate); read 105 us, 4.7 TB/s, near a mixed copy's.
+// FP32 rows of 9,366 tokens, 8 heads of 192 + 128 channels, into bf16 pages and back: 49 us, 3.9 TB/s.  CTAs of 128 and 64
+// threads, or scalar FP32 in place of the packed instructions: 385 to 612 us for the first append and read instead of 358.
 #include <math.h>
 
 #include "paged.cuh"
@@ -574,8 +579,9 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
 }
 
 // A CTA's groups (an equal share of heads * planes), its warps and tokens.  A lane goes through as many tokens (up to
-// kDepth) as leave about 16 CTAs for each SM (three are resident; with 8, prompts in bf16 took 56 us instead of 49); the search for their places, their angles and a lane's addresses are shared by
-// them.  With few groups several tokens lie side by side.
+// kDepth) as leave about 16 CTAs for each of the GPU's 152 SMs (three are resident; with 8, appending and reading 9,366 tokens
+// of 8 heads of 192 + 128 channels, bf16 pages, took 56 us instead of 49);
+// the search for their places, their angles and a lane's addresses are shared by them.  With few groups several tokens lie side by side.
 void plan(AppendArgs &A, unsigned &grid, unsigned &threads, size_t &table) {
     const int all = A.P.heads * A.P.planes;
     A.parts = (all + kGroups - 1) / kGroups;

@@ -13,8 +13,11 @@
 // 4-bit: a score group (64 channels) has columns of its own, s = sum_g scale_gj S_g + min_gj sum(q_g) on the way out; a
 // value group has weights of its own, p_j scale_gj, and sum_j p_j min_gj stays in FP32.  bf16 pages hold 64-channel planes
 // in the operands' own 128-byte swizzle (include/k3kda.h), so their strips are copied straight to the operand tiles.
-// What bounds it: per 64 keys and 128 rows 16 (dqk + dv) / 64 products of N = 64 (about 1300 cycles at 128 + 128 channels, those of
-// Q from shared memory at its bandwidth) beside 64 x (17 to 20) instructions of each softmax and 2 x 130 of each helper warp.
+// What bounds it, measured in cycles a tile of 64 keys and 128 rows at 128 + 128 channels: 4-bit pages, the softmax warps (4100; the
+// products take 2400, and a block's start, with its rows' rotation and split, 14,000); bf16 pages, the products' issue (2450: N = 64
+// products of Q take 54 cycles each instead of 32, those of V run on all its channels at once).  462 new tokens of 4
+// sequences (13,365 cached), 8 heads of 4 query heads, 4-bit pages: 179 us.  153 new tokens of 48 sequences (82,739 cached),
+// 4 heads of 8 query heads of 192 + 128 channels, bf16 pages: 217 MB in 112 us.
 #pragma once
 
 #include "paged_attend.cuh"

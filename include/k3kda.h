@@ -504,7 +504,8 @@ size_t k3mla_paged_block_bytes(int format, int page_size, int dqk, int dv);
 /* Append T packed new tokens: sequence n's are rows cu_seqlens[n] .. cu_seqlens[n+1]-1 of k_new
  * [T, heads, dqk] and v_new [T, heads, dv] (in_dtype) and go to positions kv_len[n] - count .. kv_len[n]-1.
  * cu_seqlens [N+1] (int32, device; cu_seqlens_host an optional host copy, checked) or NULL: one token for each
- * sequence, T = N.  rope (or NULL): keys are rotated by their positions before they are stored.  Two sequences may share pages that neither appends to.
+ * sequence, T = N.  rope (or NULL): keys are rotated by their positions before they are stored.  Sequences may share
+ * pages that none of them appends to.
  * One launch on `stream`.  Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, CUDA.  T = 0 launches nothing. */
 int k3mla_paged_append(const k3mla_paged_cache *cache, const k3mla_view *k_new, const k3mla_view *v_new, int in_dtype,
                        const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int T, const k3mla_rope_args *rope,
@@ -522,11 +523,13 @@ int k3mla_paged_read(const k3mla_paged_cache *cache, const k3mla_view *k_out, co
  *     out = softmax_j(scale rope(q, p) . k_j) . v  (* sigmoid(gate) when gate is given)
  * q [T, Hq, dqk], gate [T, Hq, dv] views of in_dtype, out [T, Hq, dv] dense, of out_dtype; cu_seqlens as for append;
  * max_new: at least the largest number of new tokens of a sequence (1 with cu_seqlens NULL).  A row that sees
- * no key (p < 0, an empty sequence) is 0.  Query rows, weights and sums keep FP32 accuracy (operands
- * split in two where a tensor core takes them in 16 bits).  Results do not depend on the order in which
- * parts of the work finish.
- * workspace: k3mla_paged_attend_workspace_size bytes, 256-byte aligned, zero-filled before its first use, owned by
- * one call at a time (calls of any shape may follow one another); its first word is the status word of
+ * no key (p < 0, an empty sequence) is 0.  Scores, maxima, sums and outputs are held in FP32; where a tensor core
+ * takes query rows and weights in 16 bits they are given as a high and a low part: 22 bits together with 4-bit pages
+ * (fp16 parts, scaled so that none overflows), 16 bits with bf16 pages (bf16 parts; the cached values themselves have 8).
+ * A key that a row sees and that holds an infinity or a NaN takes part as in a plain softmax; one that it does not see
+ * changes nothing.  Results do not depend on the order in which parts of the work finish.
+ * workspace: k3mla_paged_attend_workspace_size bytes (the same for every shape, 21.3 MB), 256-byte aligned, zero-filled
+ * before its first use, owned by one call at a time (calls of any shape may follow one another); its first word is the status word of
  * k3kda_workspace_status: after a TIMEOUT zero-fill it again.  One launch on `stream`.
  * Errors: INVALID_ARG (Hq not a multiple of heads), UNSUPPORTED, ALIGNMENT, WORKSPACE, CUDA. */
 size_t k3mla_paged_attend_workspace_size(int Hq, int heads, int dqk, int dv);

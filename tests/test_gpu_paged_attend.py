@@ -407,3 +407,16 @@ def test_more_blocks_of_rows_long_shared_and_of_every_size():
         got = c.run(ws=ws)
         _check(got, _long(c), tol)
         assert torch.equal(got, c.run(ws=ws)) and not ws[256:4352].any()
+
+
+@pytest.mark.parametrize("fmt", ["i4", "bf16"])
+@pytest.mark.parametrize("new", [1, 70])
+def test_offsets_past_32_bits(fmt, new):
+    """The same pages at the end of a pool of more than 2^32 bytes: the same bits."""
+    c = Case([300, 90], [new, new], 2, 2, 128, 128, 64, fmt, (128, 0, "half"), seed=31)
+    small, own = c.run(), c.pool.shape[0]
+    pages = (1 << 32) // c.pool[0].numel() + own + 1
+    pool = torch.empty((pages,) + tuple(c.pool.shape[1:]), dtype=torch.uint8, device=DEV)
+    pool[-own:] = c.pool
+    c.cache = K.PagedCache(pool, _i(np.where(c.tab >= 0, c.tab + pages - own, c.tab)), _i(c.total), 64, 128, 128, fmt)
+    assert torch.equal(c.run(), small)
