@@ -36,20 +36,26 @@ template <int DQK_, int DV_, bool I4_> struct RowsShape {
     static constexpr int OB = 2 * SB + 2 * DV <= 512 ? 2 : 1;                   // buffers of a tile's product
     static constexpr int COL_O = 2 * SB;
     static_assert(2 * SB + OB * DV <= 512, "TMEM");
-    static constexpr int WARPS = 16, THREADS = WARPS * 32;                      // 4 softmax, 8 helpers, producer, MMA, 2 idle
+    // softmax warpgroups (each takes its share of a tile's keys), two of helpers, one of producer, MMA and idle warps
+    static constexpr int SW = I4 ? 2 : 1, KEYS = 64 / SW;
+    static constexpr int HELP = 4 * SW, PROD = HELP + 8, WARPS = PROD + 4, THREADS = WARPS * 32;
+    // Registers a thread: at launch (65,536 over the threads, in eights), then of each role; what the last warpgroup gives up the others take.
+    static constexpr int LAUNCH = 65536 / THREADS / 8 * 8, R_SOFT = SW == 2 ? 112 : 192, R_HELP = SW == 2 ? 104 : 128, R_REST = SW == 2 ? 48 : 64;
+    static_assert(4 * SW * R_SOFT + 8 * R_HELP + 4 * R_REST <= WARPS * LAUNCH, "registers");
     static constexpr int RECORD = ROWS * (DV + 2);
     // shared memory, in bytes from a 1024-byte boundary
     static constexpr int Q_PART = PK * 16384, KV = PL * 8192;
     static constexpr int RS = I4 ? 2 : 1, RAW = I4 ? NS * STRIP : 0;
     static constexpr int PARAMS = I4 ? PL * 512 : 0;                            // scale[64], minimum[64] of each plane
-    static constexpr int SMALL = 4 * 128 * 4 + (2 + PV) * 128 * 4 + 128 * (PK + 1) * 4 + 1024 + 64 + 8 * PV * 8 + (THREADS + 4) * 4;
+    static constexpr int SMALL = 4 * 128 * 4 + (2 + PV) * 128 * 4 + 128 * (PK + 1) * 4 + 1024 + 64 + 8 * PV * 8 + (THREADS + 4) * 4 + (SW > 1 ? 4 * 128 * 4 : 0);
     static constexpr int FIT = (232448 - 1024 - 256 - 2 * Q_PART - RS * RAW - SMALL) / (KV + PARAMS + 64);
     static constexpr int KB = FIT > 4 ? 4 : FIT;                                // operand tiles
     static_assert(KB >= 2 && KV >= WARPS * DQK * 4 && KB * KV >= ROWS * (DV + 4) * 4, "operand tiles");
     static constexpr int AT_KV = 2 * Q_PART, AT_RAW = AT_KV + KB * KV, AT_PAR = AT_RAW + RS * RAW, AT_TOP = AT_PAR + KB * PARAMS;
     static constexpr int AT_CORR = AT_TOP + KB * 64, AT_FIN = AT_CORR + 4 * 128 * 4, AT_INFO = AT_FIN + (2 + PV) * 128 * 4;
     static constexpr int AT_BAR = AT_INFO + 128 * (PK + 1) * 4, AT_BAD = AT_BAR + 512, AT_PRE = AT_BAD + 64 + 8 * PV * 8;
-    static constexpr int SMEM = AT_PRE + (THREADS + 4) * 4 + 1024;
+    static constexpr int AT_XCH = AT_PRE + (THREADS + 4) * 4;                   // what the softmax warpgroups tell one another: [4][128]
+    static constexpr int SMEM = AT_XCH + (SW > 1 ? 4 * 128 * 4 : 0) + 1024;
     static_assert(SMEM + 256 <= 232448, "shared memory");
 };
 
@@ -86,10 +92,26 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
     return r;
 }
 
-// Registers of a warpgroup: 128 a thread at launch, 4 x 128 of them in all.  192 + 2 x 128 + 64 = 512: what the last one gives
-// up the first one takes.
-__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 192;"); }
-__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 64;"); }
+template <int N> __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
+template <int N> __device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
+
+// A pair as two 16-bit parts of each: rounded, and what that left (exact in FP32) rounded.
+template <bool F16> __device__ __forceinline__ void split2(float2 w, uint32_t &hi, uint32_t &lo) {
+    float a, b;
+    if constexpr (F16) {
+        const __half2 h = __floats2half2_rn(w.x, w.y);
+        hi = *reinterpret_cast<const uint32_t *>(&h);
+        asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(a) : "h"(__half_as_ushort(__low2half(h))), "h"((uint16_t)0xBC00), "f"(w.x));
+        asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(b) : "h"(__half_as_ushort(__high2half(h))), "h"((uint16_t)0xBC00), "f"(w.y));
+        const __half2 rest = __floats2half2_rn(a, b);
+        lo = *reinterpret_cast<const uint32_t *>(&rest);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(w.x, w.y);
+        hi = *reinterpret_cast<const uint32_t *>(&h);
+        const __nv_bfloat162 rest = __floats2bfloat162_rn(w.x - __uint_as_float(hi << 16), w.y - __uint_as_float(hi & 0xffff0000u));
+        lo = *reinterpret_cast<const uint32_t *>(&rest);
+    }
+}
 
 // A bounded wait that also ends when another warp of the CTA has given up.
 __device__ __forceinline__ bool wait_for(uint32_t bar, int parity, volatile int *dead, unsigned *status) {
@@ -147,7 +169,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
             tc::mbar_init(raw_full + 8 * i, 1);
             tc::mbar_init(raw_free + 8 * i, 256);
             tc::mbar_init(s_full + 8 * i, 1);
-            tc::mbar_init(p_full + 8 * i, 128);
+            tc::mbar_init(p_full + 8 * i, 128 * S::SW);
             tc::mbar_init(o_full + 8 * i, 1);
             tc::mbar_init(o_free + 8 * i, 256);
         }
@@ -195,7 +217,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
     tc::tc_fence_after();
     const uint32_t tb = tslot;
 
-    // The rows of a block: rotated, scaled, split to the operand tiles (warps 0 to 11, each through DQK floats of its own).
+    // The rows of a block: rotated, scaled, split to the operand tiles (softmax and helper warps, each through DQK floats of its own).
     auto prepare = [&](const Cursor &c) {
         const int rows = c.s.cnt * A.G, R0 = c.rb * S::ROWS;
         {
@@ -219,7 +241,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
             };
             fetch(warp, next);
 #pragma unroll 1
-            for (int r = warp; r < S::ROWS; r += 12) {
+            for (int r = warp; r < S::ROWS; r += S::PROD) {
                 const int i = (R0 + r) / A.G;
                 if (R0 + r >= rows) {                    // a row of nothing
                     for (int w = lane; w < S::DQK / 8; w += 32) {
@@ -231,7 +253,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                 }
 #pragma unroll
                 for (int k = 0; k < S::DQK / 32; ++k) v[k] = next[k];
-                fetch(r + 12, next);
+                fetch(r + S::PROD, next);
                 __syncwarp();
 #pragma unroll
                 for (int k = 0; k < S::DQK / 32; ++k) x[lane + 32 * k] = v[k] * A.qmul;
@@ -309,12 +331,14 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
     };
     auto nothing = [](const Cursor &, unsigned, int, int) {};
 
-    if (warp < 4) {
-        take_registers();
+    if (warp < S::HELP) {
+        take_registers<S::R_SOFT>();
         segments([&](const Cursor &c, int t0, int T, unsigned done) {
             const int rows = c.s.cnt * A.G, R0 = c.rb * S::ROWS;
-            // ---- softmax: thread r has row r
-            const int r = threadIdx.x, R = R0 + r;
+            // ---- softmax: thread r has row r, with two warpgroups the first or the last 32 keys of a tile
+            const int r = threadIdx.x & 127, R = R0 + r, wg = S::SW > 1 ? threadIdx.x >> 7 : 0, b0 = wg * (S::KEYS / 16);
+            float *xch = reinterpret_cast<float *>(sm + S::AT_XCH);
+            bool ok = true;
             const int vis = R < rows ? c.s.len - c.s.cnt + R / A.G + 1 : 0;
             float m = -INFINITY, l = 0.f, mn[S::PV];
             F2 qs[S::PK];
@@ -328,12 +352,18 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
             }
             for (int k = 0; k < T; ++k) {
                 const unsigned use = done + k;
-                if (!wait_for(s_full + 8 * (use & 1), use >> 1, dead, A.status)) break;
+                // (a warp that gave up still comes to the warpgroups' barriers)
+                ok = ok && __all_sync(0xffffffffu, wait_for(s_full + 8 * (use & 1), use >> 1, dead, A.status));
+                if (!ok) {
+                    if (S::SW == 1) break;
+                    tc::named_bar(3, 256);
+                    continue;
+                }
                 tc::tc_fence_after();
                 const int j0 = (t0 + k) * 64, slot = use % S::KB;
                 const int bad = bad_of[use & 7];
                 const bool mask = bad || j0 + 64 > c.least;
-                const uint32_t ts = tb + ((uint32_t)(warp * 32) << 16) + (use & 1) * S::SB;
+                const uint32_t ts = tb + ((uint32_t)((warp & 3) * 32) << 16) + (use & 1) * S::SB;
                 const float *par = reinterpret_cast<const float *>(sm + S::AT_PAR + slot * S::PARAMS);
                 // 16 keys' scores out of TMEM; both passes form them (2.5 instructions a key) so that neither holds 64 of them: a
                 // loop short enough for the instruction cache
@@ -373,18 +403,28 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                         }
                     }
                 };
+                // With 32 keys a thread their scores stay in registers, with 64 both passes form them (bf16: they are what TMEM holds).
+                constexpr int BLOCKS = S::KEYS / 16;
+                F2 kept[S::SW > 1 ? BLOCKS : 1][8];
                 float top = -INFINITY, e = 0.f;
-                bring(0);
-#pragma unroll 1
-                for (int b = 0; b < 4; ++b) {
-                    F2 sc[8];
-                    scores(b, sc);
-                    bring((b + 1) & 3);                  // (the last one for the second pass)
+                bring(b0);
+#pragma unroll(S::SW > 1 ? BLOCKS : 1)
+                for (int i = 0; i < BLOCKS; ++i) {
+                    F2 (&sc)[8] = kept[S::SW > 1 ? i : 0];
+                    scores(b0 + i, sc);
+                    if (i + 1 < BLOCKS) bring(b0 + i + 1);
+                    else if (S::SW == 1) bring(b0);              // (for the second pass)
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
                         const float2 f = up(sc[q]);
                         top = fmaxf(top, fmaxf(f.x, f.y));
                     }
+                }
+                if constexpr (S::SW > 1) {
+                    float *at2 = xch + (use & 1) * 256;
+                    at2[wg * 128 + r] = top;
+                    tc::named_bar(3, 256);
+                    top = fmaxf(top, at2[(wg ^ 1) * 128 + r]);
                 }
                 if constexpr (S::I4) {
                     // every value scale that the row sees here is below 2^e (as in paged_attend.cuh)
@@ -404,17 +444,20 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                 }
                 const float mnew = fmaxf(m, top + e), at_base = mnew == -INFINITY ? 0.f : mnew, cr = ex2(m - at_base);
                 m = mnew;
-                corr[(use & 3) * 128 + r] = cr;
+                if (wg == 0) corr[(use & 3) * 128 + r] = cr;
                 F2 lsum = pk(0.f, 0.f), ms[S::PV];
 #pragma unroll
                 for (int v = 0; v < S::PV; ++v) ms[v] = pk(0.f, 0.f);
                 const F2 nb = pk(-at_base, -at_base);
-#pragma unroll 1
-                for (int b = 0; b < 4; ++b) {
+#pragma unroll(S::SW > 1 ? BLOCKS : 1)
+                for (int i = 0; i < BLOCKS; ++i) {
+                    const int b = b0 + i;
                     uint32_t hi[S::GV][8], lo[S::GV][8];
-                    F2 sc[8];
-                    scores(b, sc);
-                    if (b < 3) bring(b + 1);
+                    F2 (&sc)[8] = kept[S::SW > 1 ? i : 0];
+                    if constexpr (S::SW == 1) {
+                        scores(b, sc);
+                        if (i + 1 < BLOCKS) bring(b + 1);
+                    }
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
                         const float2 d = up(add2(sc[q], nb));
@@ -429,19 +472,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                                 w = mul2(p, s2);
                                 ms[g] = fma2(p, m2, ms[g]);
                             }
-                            const float2 f = up(w);
-                            if constexpr (S::I4) {
-                                const __half2 h = __floats2half2_rn(f.x, f.y);
-                                const float2 back = __half22float2(h);
-                                const __half2 rest = __floats2half2_rn(f.x - back.x, f.y - back.y);
-                                hi[g][q] = *reinterpret_cast<const uint32_t *>(&h);
-                                lo[g][q] = *reinterpret_cast<const uint32_t *>(&rest);
-                            } else {
-                                const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
-                                hi[g][q] = *reinterpret_cast<const uint32_t *>(&h);
-                                const __nv_bfloat162 rest = __floats2bfloat162_rn(f.x - __uint_as_float(hi[g][q] << 16), f.y - __uint_as_float(hi[g][q] & 0xffff0000u));
-                                lo[g][q] = *reinterpret_cast<const uint32_t *>(&rest);
-                            }
+                            split2<S::I4>(up(w), hi[g][q], lo[g][q]);
                         }
                     }
 #pragma unroll
@@ -470,6 +501,19 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                 tc::tc_fence_before();
                 tc::mbar_arrive(p_full + 8 * (use & 1));
             }
+            if constexpr (S::SW > 1) {                       // the last keys' sums to the first warpgroup
+                tc::named_bar(3, 256);
+                if (wg == 1) {
+                    xch[r] = l;
+#pragma unroll
+                    for (int v = 0; v < S::PV; ++v) xch[(1 + v) * 128 + r] = mn[v];
+                }
+                tc::named_bar(3, 256);
+                if (wg == 1) return;
+                l += xch[r];
+#pragma unroll
+                for (int v = 0; v < S::PV; ++v) mn[v] += xch[(1 + v) * 128 + r];
+            }
             fin[r] = m;
             fin[128 + r] = c.s.len < 0 ? __int_as_float(0x7fc00000) : l;
 #pragma unroll
@@ -477,14 +521,15 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
         }, nothing, true);
         tc::named_bar(1, S::THREADS);
         if (warp == 0) tc::tmem_dealloc(tb, 512);
-    } else if (warp < 12) {
+    } else if (warp < S::PROD) {
+        if constexpr (S::R_HELP > S::LAUNCH) take_registers<S::R_HELP>();
         float o[S::DV / 2];                                                    // a row, half the channels
         Segment out[2];                                                        // what reaches out: the first segment, the last
         out[0].key = out[1].key = -1;
         segments([&](const Cursor &c, int t0, int T, unsigned done) {
             const int rows = c.s.cnt * A.G, R0 = c.rb * S::ROWS;
             // ---- helpers
-            const int ht = threadIdx.x - 128, r = 32 * (warp & 3) + lane, half = (warp - 4) >> 2;
+            const int ht = threadIdx.x - 32 * S::HELP, r = 32 * (warp & 3) + lane, half = (warp - S::HELP) >> 2;
             const int vis = R0 + r < rows ? c.s.len - c.s.cnt + (R0 + r) / A.G + 1 : 0;
 #pragma unroll
             for (int x = 0; x < S::DV / 2; ++x) o[x] = 0.f;
@@ -529,7 +574,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                             if (p >= S::PK) big = fmaxf(big, v.x);
                         }
                         big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));   // (not negative)
-                        if (lane == 0) reinterpret_cast<float *>(sm + S::AT_TOP)[slot * 16 + warp - 4] = big;
+                        if (lane == 0) reinterpret_cast<float *>(sm + S::AT_TOP)[slot * 16 + warp - S::HELP] = big;
                         tc::fence_async_smem();
                         tc::mbar_arrive(kv_full + 8 * slot);
                         tc::mbar_arrive(raw_free + 8 * (use & 1));
@@ -603,10 +648,10 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
             }
         }, [&](const Cursor &c, unsigned base, int t0, int t1) {
             // the segment's end: O through shared memory (over the operand tiles) to the output, or to the workspace
-            const int rows = c.s.cnt * A.G, R0 = c.rb * S::ROWS, ht = threadIdx.x - 128;
+            const int rows = c.s.cnt * A.G, R0 = c.rb * S::ROWS, ht = threadIdx.x - 32 * S::HELP;
             const bool begins = t0 == 0, ends = t1 == c.s.tiles;
             float *stage = reinterpret_cast<float *>(sm + S::AT_KV);           // rows of DV + 4
-            const int r = 32 * (warp & 3) + lane, half = (warp - 4) >> 2;
+            const int r = 32 * (warp & 3) + lane, half = (warp - S::HELP) >> 2;
 #pragma unroll
             for (int w = 0; w < S::DV / 16; ++w) {
                 const int ch = half * (S::DV / 2) + 8 * w;
@@ -654,13 +699,13 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
             const unsigned first = split.owner(sg.key), last = split.owner(sg.last);
             __threadfence();
             tc::named_bar(2, 256);
-            if (threadIdx.x == 128) arrived = atomicAdd(A.counters + first, 1u);
+            if (threadIdx.x == 32 * S::HELP) arrived = atomicAdd(A.counters + first, 1u);
             tc::named_bar(2, 256);
             if (arrived != last - first) continue;
             __threadfence();
-            if (threadIdx.x == 128) A.counters[first] = 0;
+            if (threadIdx.x == 32 * S::HELP) A.counters[first] = 0;
             auto rec = [&](unsigned b) { return A.partial + ((size_t)b * 2 + (b == first ? 1 : 0)) * S::RECORD; };
-            for (int x = threadIdx.x - 128; x < S::ROWS * S::DV / 4; x += 256) {
+            for (int x = threadIdx.x - 32 * S::HELP; x < S::ROWS * S::DV / 4; x += 256) {
                 const int r = x / (S::DV / 4), ch = 4 * (x - r * (S::DV / 4)), R = sg.rb * S::ROWS + r;
                 if (R >= sg.rows) continue;
                 float top = -INFINITY, l = 0.f;
@@ -678,9 +723,9 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
             }
         }
     } else {
-        give_registers();
+        give_registers<S::R_REST>();
         segments([&](const Cursor &c, int t0, int T, unsigned done) {
-            if (warp == 12) {
+            if (warp == S::PROD) {
                 // ---- producer
                 for (int k = 0; k < T; ++k) {
                     const unsigned use = done + k;
@@ -718,7 +763,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                         }
                     }
                 }
-            } else if (warp == 13 && lane == 0) {
+            } else if (warp == S::PROD + 1 && lane == 0) {
                 // ---- MMA
                 constexpr uint32_t id_s = idesc16(S::I4, 128, 64, false), id_o = idesc16(S::I4, 128, S::I4 ? 64 : S::DV, true);
                 bool ok = true;
