@@ -29,13 +29,14 @@ template <int DQK_, int DV_, bool I4_> struct RowsShape {
     static constexpr int DQK = DQK_, DV = DV_;
     static constexpr bool I4 = I4_;
     static constexpr int PK = DQK / 64, PV = DV / 64, PL = PK + PV;
-    static constexpr int ROWS = 128, NS = 4, TILE = 64, EXTRA = 4;
+    static constexpr int ROWS = 128, NS = 4, TILE = 64, EXTRA = 10;
     static constexpr int STRIP = PL * (I4 ? kPlaneI4 : kPlaneBf16);
     static constexpr int GK = I4 ? PK : 1, GV = I4 ? PV : 1;                    // groups of scores, of weights
     static constexpr int SB = 64 * (GK > GV ? GK : GV);                         // TMEM columns of a tile's scores, then weights
-    static constexpr int OB = 2 * SB + 2 * DV <= 512 ? 2 : 1;                   // buffers of a tile's product
-    static constexpr int COL_O = 2 * SB;
-    static_assert(2 * SB + OB * DV <= 512, "TMEM");
+    static constexpr bool QT = 2 * SB + DQK + DV <= 512;                        // the rows' operand stands in TMEM where it fits
+    static constexpr int COL_Q = 2 * SB, COL_O = COL_Q + (QT ? DQK : 0);
+    static constexpr int OB = COL_O + 2 * DV <= 512 ? 2 : 1;                    // buffers of a tile's product
+    static_assert(COL_O + OB * DV <= 512, "TMEM");
     // softmax warpgroups (each takes its share of a tile's keys), two of helpers, one of producer, MMA and idle warps
     static constexpr int SW = I4 ? 2 : 1, KEYS = 64 / SW;
     static constexpr int HELP = 4 * SW, PROD = HELP + 8, WARPS = PROD + 4, THREADS = WARPS * 32;
@@ -48,14 +49,17 @@ template <int DQK_, int DV_, bool I4_> struct RowsShape {
     static constexpr int RS = I4 ? 2 : 1, RAW = I4 ? NS * STRIP : 0;
     static constexpr int PARAMS = I4 ? PL * 512 : 0;                            // scale[64], minimum[64] of each plane
     static constexpr int SMALL = 4 * 128 * 4 + (2 + PV) * 128 * 4 + 128 * (PK + 1) * 4 + 1024 + 64 + 8 * PV * 8 + (THREADS + 4) * 4 + (SW > 1 ? 4 * 128 * 4 : 0);
-    static constexpr int FIT = (232448 - 1024 - 256 - 2 * Q_PART - RS * RAW - SMALL) / (KV + PARAMS + 64);
+    static constexpr int FIT = (232448 - 1024 - 256 - (QT ? 0 : 2 * Q_PART) - RS * RAW - SMALL) / (KV + PARAMS + 64);
     static constexpr int KB = FIT > 4 ? 4 : FIT;                                // operand tiles
-    static_assert(KB >= 2 && KV >= WARPS * DQK * 4 && KB * KV >= ROWS * (DV + 4) * 4, "operand tiles");
-    static constexpr int AT_KV = 2 * Q_PART, AT_RAW = AT_KV + KB * KV, AT_PAR = AT_RAW + RS * RAW, AT_TOP = AT_PAR + KB * PARAMS;
+    static_assert(KB >= 2 && KV >= WARPS * DQK * 4 && KB * KV >= ROWS * (DV + 4) * 4 && (!QT || KB * KV >= WARPS * DQK * 4 + 2 * Q_PART), "operand tiles");
+    // (rows on their way to TMEM pass through the operand tiles, behind the warps' floats)
+    static constexpr int AT_KV = QT ? 0 : 2 * Q_PART, AT_Q = QT ? WARPS * DQK * 4 : 0, AT_RAW = AT_KV + KB * KV, AT_PAR = AT_RAW + RS * RAW, AT_TOP = AT_PAR + KB * PARAMS;
     static constexpr int AT_CORR = AT_TOP + KB * 64, AT_FIN = AT_CORR + 4 * 128 * 4, AT_INFO = AT_FIN + (2 + PV) * 128 * 4;
     static constexpr int AT_BAR = AT_INFO + 128 * (PK + 1) * 4, AT_BAD = AT_BAR + 512, AT_PRE = AT_BAD + 64 + 8 * PV * 8;
     static constexpr int AT_XCH = AT_PRE + (THREADS + 4) * 4;                   // what the softmax warpgroups tell one another: [4][128]
-    static constexpr int SMEM = AT_XCH + (SW > 1 ? 4 * 128 * 4 : 0) + 1024;
+    // the join's weights of records: over the operand tiles where they end before the barriers, else behind everything
+    static constexpr int USED = AT_XCH + (SW > 1 ? 4 * 128 * 4 : 0), JOIN = (kMaxCtas + 1) * 128 * 4;
+    static constexpr int AT_JOIN = AT_BAR >= JOIN ? 0 : USED, SMEM = (AT_JOIN ? USED + JOIN : USED) + 1024;
     static_assert(SMEM + 256 <= 232448, "shared memory");
 };
 
@@ -122,6 +126,12 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, int parity, volatile int 
     *dead = 1;
     atomicOr(status, 2u);
     return false;
+}
+
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(const __grid_constant__ Args A) {
@@ -245,7 +255,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                 const int i = (R0 + r) / A.G;
                 if (R0 + r >= rows) {                    // a row of nothing
                     for (int w = lane; w < S::DQK / 8; w += 32) {
-                        char *dst = sm + (w >> 3) * 16384 + r * 128 + (((w & 7) ^ (r & 7)) << 4);
+                        char *dst = sm + S::AT_Q + (w >> 3) * 16384 + r * 128 + (((w & 7) ^ (r & 7)) << 4);
                         *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<uint4 *>(dst + S::Q_PART) = make_uint4(0, 0, 0, 0);
                     }
                     if (S::I4 && lane <= S::PK) info[r * (S::PK + 1) + lane] = 0.f;
@@ -298,10 +308,27 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                         hi[q] = __byte_perm(pa, pb, 0x5410);
                         lo[q] = __byte_perm(pa, pb, 0x7632);
                     }
-                    char *dst = sm + (w >> 3) * 16384 + r * 128 + (((w & 7) ^ (r & 7)) << 4);
+                    char *dst = sm + S::AT_Q + (w >> 3) * 16384 + r * 128 + (((w & 7) ^ (r & 7)) << 4);
                     *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4 *>(dst + S::Q_PART) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
+            }
+        }
+        if constexpr (S::QT) {                           // thread r copies row r to TMEM: the high parts, the low parts
+            tc::named_bar(4, 32 * S::PROD);
+            if (warp < S::HELP) {
+                const int r = threadIdx.x & 127;
+#pragma unroll 1
+                for (int part = S::SW > 1 ? (int)(threadIdx.x >> 7) : 0; part < (S::SW > 1 ? (int)(threadIdx.x >> 7) + 1 : 2); ++part)
+#pragma unroll 2
+                    for (int w = 0; w < S::DQK / 8; w += 2) {
+                        const char *src = sm + S::AT_Q + part * S::Q_PART + (w >> 3) * 16384 + r * 128;
+                        const uint4 a = *reinterpret_cast<const uint4 *>(src + (((w & 7) ^ (r & 7)) << 4)), b = *reinterpret_cast<const uint4 *>(src + ((((w + 1) & 7) ^ (r & 7)) << 4));
+                        const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                        tc::tmem_st8(tb + ((uint32_t)((warp & 3) * 32) << 16) + S::COL_Q + part * (S::DQK / 2) + 4 * w, x);
+                    }
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
             }
         }
         tc::fence_async_smem();
@@ -705,22 +732,47 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
             __threadfence();
             if (threadIdx.x == 32 * S::HELP) A.counters[first] = 0;
             auto rec = [&](unsigned b) { return A.partial + ((size_t)b * 2 + (b == first ? 1 : 0)) * S::RECORD; };
-            for (int x = threadIdx.x - 32 * S::HELP; x < S::ROWS * S::DV / 4; x += 256) {
-                const int r = x / (S::DV / 4), ch = 4 * (x - r * (S::DV / 4)), R = sg.rb * S::ROWS + r;
-                if (R >= sg.rows) continue;
+            // each row's weights of the records, then the weighted sums, several loads on their way at a time
+            float *wt = reinterpret_cast<float *>(sm + S::AT_JOIN);            // [records][128], then the rows' sums
+            const int ht = threadIdx.x - 32 * S::HELP, live = min(S::ROWS, sg.rows - sg.rb * S::ROWS);
+            const unsigned count = last - first + 1;
+            if (ht < live) {
                 float top = -INFINITY, l = 0.f;
-                float4 v4 = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                for (unsigned b = 0; b < count; ++b) top = fmaxf(top, __ldcg(rec(first + b) + ht));
 #pragma unroll 4
-                for (unsigned b = first; b <= last; ++b) top = fmaxf(top, __ldcg(rec(b) + r));
-#pragma unroll 4
-                for (unsigned b = first; b <= last; ++b) {
-                    const float f = weight(__ldcg(rec(b) + r), top);
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(rec(b) + 256 + r * S::DV + ch));
-                    l = fmaf(f, __ldcg(rec(b) + 128 + r), l);
-                    v4.x = fmaf(f, v.x, v4.x); v4.y = fmaf(f, v.y, v4.y); v4.z = fmaf(f, v.z, v4.z); v4.w = fmaf(f, v.w, v4.w);
+                for (unsigned b = 0; b < count; ++b) {
+                    const float f = weight(__ldcg(rec(first + b) + ht), top);
+                    l = fmaf(f, __ldcg(rec(first + b) + 128 + ht), l);
+                    wt[b * 128 + ht] = f;
                 }
-                store4(A, S::DV, sg.q0, sg.h, R, ch, v4, l);
+                wt[count * 128 + ht] = l;
             }
+            tc::named_bar(2, 256);
+            constexpr int C4 = S::DV / 4, ITEMS = 4;
+            for (int x0 = ht; x0 < live * C4; x0 += 256 * ITEMS) {
+                float4 v4[ITEMS];
+#pragma unroll
+                for (int q = 0; q < ITEMS; ++q) v4[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                for (unsigned b = 0; b < count; ++b) {
+                    const float *from = rec(first + b) + 256;
+#pragma unroll
+                    for (int q = 0; q < ITEMS; ++q) {
+                        const int x = x0 + 256 * q;
+                        if (x >= live * C4) break;
+                        const float f = wt[b * 128 + x / C4];
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(from) + x);
+                        v4[q].x = fmaf(f, v.x, v4[q].x); v4[q].y = fmaf(f, v.y, v4[q].y); v4[q].z = fmaf(f, v.z, v4[q].z); v4[q].w = fmaf(f, v.w, v4[q].w);
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < ITEMS; ++q) {
+                    const int x = x0 + 256 * q, r = x / C4;
+                    if (x < live * C4) store4(A, S::DV, sg.q0, sg.h, sg.rb * S::ROWS + r, 4 * (x - r * C4), v4[q], wt[count * 128 + r]);
+                }
+            }
+            tc::named_bar(2, 256);
         }
     } else {
         give_registers<S::R_REST>();
@@ -763,30 +815,38 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                         }
                     }
                 }
-            } else if (warp == S::PROD + 1 && lane == 0) {
+            } else if (warp == S::PROD + 1) {
                 // ---- MMA
                 constexpr uint32_t id_s = idesc16(S::I4, 128, 64, false), id_o = idesc16(S::I4, 128, S::I4 ? 64 : S::DV, true);
                 bool ok = true;
+                const uint32_t tq = __shfl_sync(0xffffffffu, tb, 0) + S::COL_Q;
                 for (int k = 0; k < T + 1 && ok; ++k) {
                     if (k < T) {
                         const unsigned use = done + k;
                         const int slot = use % S::KB;
-                        ok = wait_for(kv_full + 8 * slot, use / S::KB, dead, A.status);
-                        if (!ok) break;
+                        ok = __all_sync(0xffffffffu, wait_for(kv_full + 8 * slot, use / S::KB, dead, A.status));
+                        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                         tc::tc_fence_after();
-                        const uint32_t ts = tb + (use & 1) * S::SB, kv = sm32 + S::AT_KV + slot * S::KV;
-    #pragma unroll
+                        const uint32_t ts = __shfl_sync(0xffffffffu, tb + (use & 1) * S::SB, 0), kv = __shfl_sync(0xffffffffu, sm32 + S::AT_KV + slot * S::KV, 0);
+                        if (elect()) {
+#pragma unroll
                         for (int p = 0; p < S::PK; ++p) {
                             const uint64_t dq = tc::sdesc_kmajor_sw128(sm32 + p * 16384), dl = tc::sdesc_kmajor_sw128(sm32 + S::Q_PART + p * 16384),
                                            dk = tc::sdesc_kmajor_sw128(kv + p * 8192);
-    #pragma unroll
+#pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const uint32_t d = ts + (S::I4 ? 64 * p : 0);
-                                tc::mma_bf16(d, tc::dadd(dq, 32 * i), tc::dadd(dk, 32 * i), id_s, i != 0 || (!S::I4 && p != 0));
-                                tc::mma_bf16(d, tc::dadd(dl, 32 * i), tc::dadd(dk, 32 * i), id_s, 1);
+                                const uint32_t d = ts + (S::I4 ? 64 * p : 0), acc = i != 0 || (!S::I4 && p != 0);
+                                if constexpr (S::QT) {
+                                    const uint32_t a = tq + 32 * p + 8 * i;
+                                    tc::mma_bf16_ta(d, a, tc::dadd(dk, 32 * i), id_s, acc);
+                                    tc::mma_bf16_ta(d, a + S::DQK / 2, tc::dadd(dk, 32 * i), id_s, 1);
+                                } else {
+                                    tc::mma_bf16(d, tc::dadd(dq, 32 * i), tc::dadd(dk, 32 * i), id_s, acc);
+                                    tc::mma_bf16(d, tc::dadd(dl, 32 * i), tc::dadd(dk, 32 * i), id_s, 1);
+                                }
                             }
                         }
-                        tc::mma_commit(s_full + 8 * (use & 1));
+                        tc::mma_commit(s_full + 8 * (use & 1)); }
                     }
                     if (k >= 1) {
                         const unsigned use = done + k - 1;
@@ -794,9 +854,10 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                         ok = wait_for(p_full + 8 * (use & 1), use >> 1, dead, A.status);
                         if (ok && use >= S::OB) ok = wait_for(o_free + 8 * ob, use / S::OB - 1, dead, A.status);
                         if (ok && !S::I4) ok = wait_for(v_ok + 8 * slot, use / S::KB, dead, A.status);
-                        if (!ok) break;
+                        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                         tc::tc_fence_after();
-                        const uint32_t ts = tb + (use & 1) * S::SB, kv = sm32 + S::AT_KV + slot * S::KV;
+                        const uint32_t ts = __shfl_sync(0xffffffffu, tb + (use & 1) * S::SB, 0), kv = __shfl_sync(0xffffffffu, sm32 + S::AT_KV + slot * S::KV, 0);
+                        if (elect()) {
     #pragma unroll
                         for (int v = 0; v < S::GV; ++v) {        // (bf16: all value channels at once)
                             const uint64_t dv = tc::sdesc_mnmajor_sw128(kv + (S::PK + v) * 8192, 8192);
@@ -808,7 +869,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                             }
                         }
                         tc::mma_commit(o_full + 8 * ob);
-                        tc::mma_commit(kv_free + 8 * slot);
+                        tc::mma_commit(kv_free + 8 * slot); }
                     }
                 }
             }
