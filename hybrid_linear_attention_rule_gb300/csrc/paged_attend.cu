@@ -4,10 +4,12 @@
 namespace k3kda {
 
 // From how many query rows of a key head on blocks of 128 rows take over from blocks of 8.  The latter's time grows with every
-// 8 rows, the former's hardly up to 128.  Measured on 32 sequences of 4000 keys, 4 heads of 128 + 128 channels, 8-row blocks
-// against 128-row blocks: 4-bit pages 109 against 155 us at 40 rows, 144 against 162 at 56, 199 against 172 at 80; 192 + 128 channels
-// (16 sequences) 95 against 98 at 32, 136 against 107 at 48; bf16 pages 96 against 97 at 16, 135 against 100 at 24.
-static int rows_from(bool i4, int dqk) { return !i4 ? 16 : dqk <= 128 ? 56 : 32; }
+// 8 rows, the former's hardly up to 128, and the wider keys are the more its products gain.  Measured in us, 8-row blocks against
+// 128-row blocks: 4-bit pages of 128 + 128 channels, 32 sequences of 4000 keys, 4 heads: 90 / 106 at 32 rows, 109 / 108 at 40,
+// 126 / 108 at 48; one sequence of 60,000, 8 heads: 83 / 95 at 32, 97 / 99 at 40, 115 / 100 at 48; 16 sequences of 4000 with 64 + 64
+// channels 41 / 47 at 40, 48 / 47 at 48, with 192 + 128 78 / 91 at 24, 96 / 92 at 32.  bf16 pages, 32 sequences of 4000: 57 / 85 at 8 rows,
+// 95 / 86 at 12; one of 60,000: 69 / 78 at 8, 86 / 80 at 12; 64 of 300: 46 / 52 at 12, 61 / 55 at 24.
+static int rows_from(bool i4, int dqk) { return i4 ? 52 - dqk / 8 : 8; }
 
 // whether blocks of 128 rows fit tensor memory
 static bool wide_ok(int dqk, int dv) { return dqk <= 192 && dv <= 128; }

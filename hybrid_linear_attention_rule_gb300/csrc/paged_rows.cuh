@@ -7,17 +7,19 @@
 //   producer (1 warp)  bulk copies of whole strips, whose pages it looks up
 //   helpers (8 warps)  4-bit: codes to fp16 operand tiles by one AND (paged_attend.cuh), scales and minima to FP32;
 //                      and, two tiles later, O = O corr + (the tile's product), 128 rows by half the channels a warpgroup, in registers
-//   MMA (1 thread)     S = Q K^T, O_tile = P V, each with Q and P as a high and a low 16-bit part: A = Q from shared memory,
-//                      P from TMEM where it took S's columns
-//   softmax (4 warps)  a row a thread: S out of TMEM, scales, running maximum, weights back in
+//   MMA (1 warp)       S = Q K^T, O_tile = P V, each with Q and P as a high and a low 16-bit part: A = Q from TMEM where it
+//                      fits there (32 cycles a product of N = 64 against 48 from shared memory, and as much room there for
+//                      the ring), P from TMEM where it took S's columns
+//   softmax            a row a thread: S out of TMEM, scales, running maximum, weights back in.  bf16 pages 4 warps; 4-bit
+//                      pages, with 30 instructions a key, 8 warps with half the tile's keys each, whose scores stay in registers
 // 4-bit: a score group (64 channels) has columns of its own, s = sum_g scale_gj S_g + min_gj sum(q_g) on the way out; a
 // value group has weights of its own, p_j scale_gj, and sum_j p_j min_gj stays in FP32.  bf16 pages hold 64-channel planes
 // in the operands' own 128-byte swizzle (include/k3kda.h), so their strips are copied straight to the operand tiles.
-// What bounds it, measured in cycles a tile of 64 keys and 128 rows at 128 + 128 channels: 4-bit pages, the softmax warps (4100; the
-// products take 2400, and a block's start, with its rows' rotation and split, 14,000); bf16 pages, the products' issue (2450: N = 64
-// products of Q take 54 cycles each instead of 32, those of V run on all its channels at once).  462 new tokens of 4
-// sequences (13,365 cached), 8 heads of 4 query heads, 4-bit pages: 179 us.  153 new tokens of 48 sequences (82,739 cached),
-// 4 heads of 8 query heads of 192 + 128 channels, bf16 pages: 217 MB in 112 us.
+// What bounds it, measured in cycles a tile of 64 keys and 128 rows: 4-bit pages of 128 + 128 channels, the softmax warps (2900 beside
+// 1600 of products; with 4 warps and both passes forming the scores it was 4100); bf16 pages of 192 + 128, the products (1700)
+// and the softmax (2100) in turn.  A block's start, its rows' rotation and split, takes 8,000 to 12,000, the join of a shared
+// block 15,000.  462 new tokens of 4 sequences (13,365 cached), 8 heads of 4 query heads, 4-bit pages: 113 us.  153 new tokens of 48
+// sequences (82,739 cached), 4 heads of 8 query heads of 192 + 128 channels, bf16 pages: 217 MB in 86 us.
 #pragma once
 
 #include "paged_attend.cuh"
@@ -29,7 +31,8 @@ template <int DQK_, int DV_, bool I4_> struct RowsShape {
     static constexpr int DQK = DQK_, DV = DV_;
     static constexpr bool I4 = I4_;
     static constexpr int PK = DQK / 64, PV = DV / 64, PL = PK + PV;
-    static constexpr int ROWS = 128, NS = 4, TILE = 64, EXTRA = 10;
+    static constexpr int ROWS = 128, NS = 4, TILE = 64;
+    static constexpr int EXTRA = 10;                                            // a block's start and end in tiles (few tokens, bf16 pages: 4: 112 us, 6: 97, 10: 89, 14: 89)
     static constexpr int STRIP = PL * (I4 ? kPlaneI4 : kPlaneBf16);
     static constexpr int GK = I4 ? PK : 1, GV = I4 ? PV : 1;                    // groups of scores, of weights
     static constexpr int SB = 64 * (GK > GV ? GK : GV);                         // TMEM columns of a tile's scores, then weights
@@ -115,6 +118,15 @@ template <bool F16> __device__ __forceinline__ void split2(float2 w, uint32_t &h
         const __nv_bfloat162 rest = __floats2bfloat162_rn(w.x - __uint_as_float(hi << 16), w.y - __uint_as_float(hi & 0xffff0000u));
         lo = *reinterpret_cast<const uint32_t *>(&rest);
     }
+}
+
+// x as a bf16 pair, the high part in the low half, with parts of the same sign and none 0 but for x = 0: each times an infinite key is
+// the same infinity, as x times it is.  The high part is cut off, not rounded, so together they have 16 bits; 2^-100 adds nothing.
+__device__ __forceinline__ uint32_t split_same_sign(float x) {
+    const uint32_t hi = __float_as_uint(x) & 0xffff0000u;
+    const float rest = x - __uint_as_float(hi);
+    const uint32_t lo = __bfloat16_as_ushort(__float2bfloat16_rn(rest == 0.f && hi << 1 ? __uint_as_float((hi & 0x80000000u) | 0x0d800000u) : rest));
+    return hi >> 16 | lo << 16;
 }
 
 // A bounded wait that also ends when another warp of the CTA has given up.
@@ -239,7 +251,6 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
             float v[S::DQK / 32], next[S::DQK / 32];     // the next row is on its way while one is prepared
             auto fetch = [&](int r, float (&f)[S::DQK / 32]) {
                 const int R = R0 + r, i = R / A.G, hq = c.h * A.G + R - i * A.G;
-                if (R >= rows || r >= S::ROWS) return;
                 const char *src = A.q.p + ((int64_t)(c.s.q0 + i) * A.q.ts + (int64_t)hq * A.q.hs + lane) * size;
                 if (A.in_bf16) {
 #pragma unroll
@@ -249,21 +260,23 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                     for (int k = 0; k < S::DQK / 32; ++k) f[k] = load_elt(src, 32 * k, 0);
                 }
             };
-            fetch(warp, next);
-#pragma unroll 1
-            for (int r = warp; r < S::ROWS; r += S::PROD) {
-                const int i = (R0 + r) / A.G;
-                if (R0 + r >= rows) {                    // a row of nothing
-                    for (int w = lane; w < S::DQK / 8; w += 32) {
-                        char *dst = sm + S::AT_Q + (w >> 3) * 16384 + r * 128 + (((w & 7) ^ (r & 7)) << 4);
-                        *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<uint4 *>(dst + S::Q_PART) = make_uint4(0, 0, 0, 0);
-                    }
-                    if (S::I4 && lane <= S::PK) info[r * (S::PK + 1) + lane] = 0.f;
-                    continue;
+            const int live = min(S::ROWS, rows - R0), each = (live + S::PROD - 1) / S::PROD, r1 = min(live, (warp + 1) * each);
+            float2 cs[(S::DQK / 2 + 31) / 32];
+            int turned = -1;                             // the token whose cosines and sines they are
+            for (int r = live + warp; r < S::ROWS; r += S::PROD) {             // rows of nothing
+                for (int w = lane; w < S::DQK / 8; w += 32) {
+                    char *dst = sm + S::AT_Q + (w >> 3) * 16384 + r * 128 + (((w & 7) ^ (r & 7)) << 4);
+                    *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<uint4 *>(dst + S::Q_PART) = make_uint4(0, 0, 0, 0);
                 }
+                if (S::I4 && lane <= S::PK) info[r * (S::PK + 1) + lane] = 0.f;
+            }
+            if (warp * each < r1) fetch(warp * each, next);
+#pragma unroll 1
+            for (int r = warp * each; r < r1; ++r) {
+                const int i = (R0 + r) / A.G;
 #pragma unroll
                 for (int k = 0; k < S::DQK / 32; ++k) v[k] = next[k];
-                fetch(r + S::PROD, next);
+                if (r + 1 < r1) fetch(r + 1, next);
                 __syncwarp();
 #pragma unroll
                 for (int k = 0; k < S::DQK / 32; ++k) x[lane + 32 * k] = v[k] * A.qmul;
@@ -274,12 +287,13 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                     for (int k = 0; k < (S::DQK / 2 + 31) / 32; ++k) {
                         const int p = lane + 32 * k;
                         if (p >= A.r.half) break;
-                        const float2 cs = rope_cs(phase[k], pos);
+                        if (turned != i) cs[k] = rope_cs(phase[k], pos);
                         float *a = x + A.r.off + (A.r.inter ? 2 * p : p);
                         const float u = a[0] * A.r.mscale, w = a[apart] * A.r.mscale;
-                        a[0] = u * cs.x - w * cs.y;
-                        a[apart] = w * cs.x + u * cs.y;
+                        a[0] = u * cs[k].x - w * cs[k].y;
+                        a[apart] = w * cs[k].x + u * cs[k].y;
                     }
+                    turned = i;
                     __syncwarp();
                 }
                 float mul = 1.f;
@@ -304,7 +318,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const float a = S::I4 ? y[q] * mul * (q & 1 ? 1.f : 16.f) : y[2 * q], b = S::I4 ? y[q + 4] * mul * (q & 1 ? 1.f : 16.f) : y[2 * q + 1];
-                        const uint32_t pa = split_pair<S::I4>(a), pb = split_pair<S::I4>(b);
+                        const uint32_t pa = S::I4 ? split_pair<true>(a) : split_same_sign(a), pb = S::I4 ? split_pair<true>(b) : split_same_sign(b);
                         hi[q] = __byte_perm(pa, pb, 0x5410);
                         lo[q] = __byte_perm(pa, pb, 0x7632);
                     }
@@ -392,8 +406,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                 const bool mask = bad || j0 + 64 > c.least;
                 const uint32_t ts = tb + ((uint32_t)((warp & 3) * 32) << 16) + (use & 1) * S::SB;
                 const float *par = reinterpret_cast<const float *>(sm + S::AT_PAR + slot * S::PARAMS);
-                // 16 keys' scores out of TMEM; both passes form them (2.5 instructions a key) so that neither holds 64 of them: a
-                // loop short enough for the instruction cache
+                // 16 keys' scores out of TMEM
                 uint32_t x[S::GK][16];
                 auto bring = [&](int b) {
 #pragma unroll
@@ -430,7 +443,8 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                         }
                     }
                 };
-                // With 32 keys a thread their scores stay in registers, with 64 both passes form them (bf16: they are what TMEM holds).
+                // With 32 keys a thread their scores stay in registers; with 64 (bf16: they are what TMEM holds) both passes read
+                // them, in loops short enough for the instruction cache.
                 constexpr int BLOCKS = S::KEYS / 16;
                 F2 kept[S::SW > 1 ? BLOCKS : 1][8];
                 float top = -INFINITY, e = 0.f;
@@ -756,14 +770,18 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                 for (int q = 0; q < ITEMS; ++q) v4[q] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
                 for (unsigned b = 0; b < count; ++b) {
-                    const float *from = rec(first + b) + 256;
+                    const float4 *from = reinterpret_cast<const float4 *>(rec(first + b) + 256);
+                    float4 v[ITEMS];
+                    float f[ITEMS];
 #pragma unroll
                     for (int q = 0; q < ITEMS; ++q) {
-                        const int x = x0 + 256 * q;
-                        if (x >= live * C4) break;
-                        const float f = wt[b * 128 + x / C4];
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(from) + x);
-                        v4[q].x = fmaf(f, v.x, v4[q].x); v4[q].y = fmaf(f, v.y, v4[q].y); v4[q].z = fmaf(f, v.z, v4[q].z); v4[q].w = fmaf(f, v.w, v4[q].w);
+                        const int x = min(x0 + 256 * q, live * C4 - 1);
+                        v[q] = __ldcg(from + x);
+                        f[q] = wt[b * 128 + x / C4];
+                    }
+#pragma unroll
+                    for (int q = 0; q < ITEMS; ++q) {
+                        v4[q].x = fmaf(f[q], v[q].x, v4[q].x); v4[q].y = fmaf(f[q], v[q].y, v4[q].y); v4[q].z = fmaf(f[q], v[q].z, v4[q].z); v4[q].w = fmaf(f[q], v[q].w, v4[q].w);
                     }
                 }
 #pragma unroll
@@ -816,60 +834,56 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                     }
                 }
             } else if (warp == S::PROD + 1) {
-                // ---- MMA
+                // ---- MMA: the whole warp comes along, so that addresses are uniform, and one thread issues
                 constexpr uint32_t id_s = idesc16(S::I4, 128, 64, false), id_o = idesc16(S::I4, 128, S::I4 ? 64 : S::DV, true);
-                bool ok = true;
-                const uint32_t tq = __shfl_sync(0xffffffffu, tb, 0) + S::COL_Q;
-                for (int k = 0; k < T + 1 && ok; ++k) {
+                const uint32_t tu = __shfl_sync(0xffffffffu, tb, 0);
+                for (int k = 0; k < T + 1; ++k) {
                     if (k < T) {
                         const unsigned use = done + k;
                         const int slot = use % S::KB;
-                        ok = __all_sync(0xffffffffu, wait_for(kv_full + 8 * slot, use / S::KB, dead, A.status));
-                        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                        if (!__all_sync(0xffffffffu, wait_for(kv_full + 8 * slot, use / S::KB, dead, A.status))) break;
                         tc::tc_fence_after();
-                        const uint32_t ts = __shfl_sync(0xffffffffu, tb + (use & 1) * S::SB, 0), kv = __shfl_sync(0xffffffffu, sm32 + S::AT_KV + slot * S::KV, 0);
+                        const uint32_t ts = tu + __shfl_sync(0xffffffffu, (use & 1) * S::SB, 0), kv = __shfl_sync(0xffffffffu, sm32 + S::AT_KV + slot * S::KV, 0);
                         if (elect()) {
 #pragma unroll
-                        for (int p = 0; p < S::PK; ++p) {
-                            const uint64_t dq = tc::sdesc_kmajor_sw128(sm32 + p * 16384), dl = tc::sdesc_kmajor_sw128(sm32 + S::Q_PART + p * 16384),
-                                           dk = tc::sdesc_kmajor_sw128(kv + p * 8192);
+                            for (int p = 0; p < S::PK; ++p) {
+                                const uint64_t dk = tc::sdesc_kmajor_sw128(kv + p * 8192);
+                                const uint32_t d = ts + (S::I4 ? 64 * p : 0);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t d = ts + (S::I4 ? 64 * p : 0), acc = i != 0 || (!S::I4 && p != 0);
-                                if constexpr (S::QT) {
-                                    const uint32_t a = tq + 32 * p + 8 * i;
-                                    tc::mma_bf16_ta(d, a, tc::dadd(dk, 32 * i), id_s, acc);
-                                    tc::mma_bf16_ta(d, a + S::DQK / 2, tc::dadd(dk, 32 * i), id_s, 1);
-                                } else {
-                                    tc::mma_bf16(d, tc::dadd(dq, 32 * i), tc::dadd(dk, 32 * i), id_s, acc);
-                                    tc::mma_bf16(d, tc::dadd(dl, 32 * i), tc::dadd(dk, 32 * i), id_s, 1);
-                                }
+                                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                    for (int part = 0; part < 2; ++part) {
+                                        const uint32_t more = i != 0 || part != 0 || (!S::I4 && p != 0);
+                                        if constexpr (S::QT) tc::mma_bf16_ta(d, tu + S::COL_Q + part * (S::DQK / 2) + 32 * p + 8 * i, tc::dadd(dk, 32 * i), id_s, more);
+                                        else tc::mma_bf16(d, tc::dadd(tc::sdesc_kmajor_sw128(sm32 + part * S::Q_PART + p * 16384), 32 * i), tc::dadd(dk, 32 * i), id_s, more);
+                                    }
                             }
+                            tc::mma_commit(s_full + 8 * (use & 1));
                         }
-                        tc::mma_commit(s_full + 8 * (use & 1)); }
                     }
                     if (k >= 1) {
                         const unsigned use = done + k - 1;
                         const int slot = use % S::KB, ob = use % S::OB;
-                        ok = wait_for(p_full + 8 * (use & 1), use >> 1, dead, A.status);
+                        bool ok = wait_for(p_full + 8 * (use & 1), use >> 1, dead, A.status);
                         if (ok && use >= S::OB) ok = wait_for(o_free + 8 * ob, use / S::OB - 1, dead, A.status);
                         if (ok && !S::I4) ok = wait_for(v_ok + 8 * slot, use / S::KB, dead, A.status);
-                        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                        if (!__all_sync(0xffffffffu, ok)) break;
                         tc::tc_fence_after();
-                        const uint32_t ts = __shfl_sync(0xffffffffu, tb + (use & 1) * S::SB, 0), kv = __shfl_sync(0xffffffffu, sm32 + S::AT_KV + slot * S::KV, 0);
+                        const uint32_t ts = tu + __shfl_sync(0xffffffffu, (use & 1) * S::SB, 0), kv = __shfl_sync(0xffffffffu, sm32 + S::AT_KV + slot * S::KV, 0),
+                                       to = tu + __shfl_sync(0xffffffffu, S::COL_O + ob * S::DV, 0);
                         if (elect()) {
-    #pragma unroll
-                        for (int v = 0; v < S::GV; ++v) {        // (bf16: all value channels at once)
-                            const uint64_t dv = tc::sdesc_mnmajor_sw128(kv + (S::PK + v) * 8192, 8192);
-                            const uint32_t d = tb + S::COL_O + ob * S::DV + 64 * v, p = ts + 64 * v;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                tc::mma_bf16_ta(d, p + 16 * i, tc::dadd(dv, 2048 * i), id_o, i != 0);
-                                tc::mma_bf16_ta(d, p + 16 * i + 8, tc::dadd(dv, 2048 * i), id_o, 1);
+                            for (int v = 0; v < S::GV; ++v) {    // (bf16: all value channels at once)
+                                const uint64_t dv = tc::sdesc_mnmajor_sw128(kv + (S::PK + v) * 8192, 8192);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                    for (int part = 0; part < 2; ++part)
+                                        tc::mma_bf16_ta(to + 64 * v, ts + 64 * v + 16 * i + 8 * part, tc::dadd(dv, 2048 * i), id_o, i != 0 || part != 0);
                             }
+                            tc::mma_commit(o_full + 8 * ob);
+                            tc::mma_commit(kv_free + 8 * slot);
                         }
-                        tc::mma_commit(o_full + 8 * ob);
-                        tc::mma_commit(kv_free + 8 * slot); }
                     }
                 }
             }

@@ -526,8 +526,8 @@ int k3mla_paged_read(const k3mla_paged_cache *cache, const k3mla_view *k_out, co
  * no key (p < 0, an empty sequence) is 0.  Scores, maxima, sums and outputs are held in FP32; where a tensor core
  * takes query rows and weights in 16 bits they are given as a high and a low part: 22 bits together with 4-bit pages
  * (fp16 parts, scaled so that none overflows), 16 bits with bf16 pages (bf16 parts; the cached values themselves have 8).
- * A key that a row sees and that holds an infinity or a NaN takes part as in a plain softmax; one that it does not see
- * changes nothing.  Results do not depend on the order in which parts of the work finish.
+ * A token that a row sees and that holds an infinity or a NaN acts as in a plain softmax, except that an output that an
+ * infinite value reaches may be NaN; one that the row does not see changes nothing.  Results do not depend on the order in which parts of the work finish.
  * workspace: k3mla_paged_attend_workspace_size bytes (the same for every shape, 21.3 MB), 256-byte aligned, zero-filled
  * before its first use, owned by one call at a time (calls of any shape may follow one another); its first word is the status word of
  * k3kda_workspace_status: after a TIMEOUT zero-fill it again.  One launch on `stream`.

@@ -420,3 +420,21 @@ def test_offsets_past_32_bits(fmt, new):
     pool[-own:] = c.pool
     c.cache = K.PagedCache(pool, _i(np.where(c.tab >= 0, c.tab + pages - own, c.tab)), _i(c.total), 64, 128, 128, fmt)
     assert torch.equal(c.run(), small)
+
+
+@pytest.mark.parametrize("fmt", ["i4", "bf16"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("new", [4, 20])
+def test_a_key_that_is_not_finite_scores_as_its_product_does(fmt, value, new):
+    """A bf16 key with an infinity scores plus or minus infinity by the sign of the query's channel, whatever parts the query
+    is held in (some channels need only one): a row that it scores minus infinity is as without it."""
+    def spoil(n, rows):
+        if n == 1:
+            rows[-2, 1, 3] = value
+    c = Case([200, 37], [1, new], 2, 4, 128, 128, 16, fmt, seed=12, edit=spoil)
+    c.q[:, :, 3] = torch.where(torch.arange(8, device=DEV) % 2 == 0, 0.5, -0.75).bfloat16()
+    want, tol = c.want()
+    got = _np(c.run())
+    finite = np.isfinite(want)
+    assert np.array_equal(np.isfinite(got), finite)
+    assert (np.abs(got - want)[finite] <= (tol + 2.0 ** -23 * np.abs(want))[finite]).all()
