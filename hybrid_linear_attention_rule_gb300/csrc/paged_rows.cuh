@@ -894,8 +894,15 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
 
 template <class S> cudaError_t launch_rows(const Args &A, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = smem_attr_once((const void *)rows_kernel<S>, S::SMEM, done);
-    if (e != cudaSuccess) return e;
+    static std::atomic<bool> fits{false};
+    cudaError_t e;
+    if (!fits.load(std::memory_order_acquire)) {         // roles take registers that others give: the launch must have had them
+        cudaFuncAttributes attr;
+        if ((e = cudaFuncGetAttributes(&attr, (const void *)rows_kernel<S>)) != cudaSuccess) return e;
+        if (attr.numRegs < S::LAUNCH) return cudaErrorInvalidConfiguration;
+        fits.store(true, std::memory_order_release);
+    }
+    if ((e = smem_attr_once((const void *)rows_kernel<S>, S::SMEM, done)) != cudaSuccess) return e;
     int dev = 0, sms = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
