@@ -29,7 +29,7 @@
 // Measured, 4-bit pages, 128 + 128 channels.  64 sequences of 4 to 8,153 tokens, 32 heads, a query row each: 1,218 MB in 224 us,
 // 5.4 TB/s (80 % of a copy's rate); the copies alone took 220 us and the arithmetic alone, in an earlier state, 248: both bind.
 // One sequence of 250,008 tokens, 8 heads of 4 query rows: 288 MB in 67 us, of which some 12,000 cycles pass before the
-// first product and 10,000 in the join.
+// first product and 8,000 in the join.
 #pragma once
 
 #include "paged.cuh"
@@ -974,17 +974,34 @@ template <class S> __global__ void __launch_bounds__(S::WARPS * 32, 1) attend_ke
         for (int x = threadIdx.x; x < S::ROWS * S::DV / 4; x += THREADS) {
             const int r = x / (S::DV / 4), ch = 4 * (x - r * (S::DV / 4)), R = sg.rb * S::ROWS + r;
             if (R >= sg.rows) continue;
-            float top = -INFINITY;
-#pragma unroll 8
-            for (unsigned b = first; b <= last; ++b) top = fmaxf(top, __ldcg(rec(b) + r));
-            float l = 0.f;
+            // eight records on their way at a time, under a running maximum
+            float top = -INFINITY, l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (unsigned b = first; b <= last; ++b) {
-                const float f = weight(__ldcg(rec(b) + r), top);
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(rec(b) + 2 * S::ROWS + r * S::DV + ch));
-                l = fmaf(f, __ldcg(rec(b) + S::ROWS + r), l);
-                o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
+#pragma unroll 1
+            for (unsigned b0 = first; b0 <= last; b0 += 8) {
+                float m[8], sum[8];
+                float4 v[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float *from = rec(min(b0 + q, last));
+                    m[q] = __ldcg(from + r);
+                    sum[q] = __ldcg(from + S::ROWS + r);
+                    v[q] = __ldcg(reinterpret_cast<const float4 *>(from + 2 * S::ROWS + r * S::DV + ch));
+                }
+                float next = top;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) next = fmaxf(next, m[q]);          // (the last one again changes no maximum)
+                const float old = weight(top, next);
+                top = next;
+                l *= old;
+                o.x *= old; o.y *= old; o.z *= old; o.w *= old;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    if (b0 + q > last) break;
+                    const float f = weight(m[q], top);
+                    l = fmaf(f, sum[q], l);
+                    o.x = fmaf(f, v[q].x, o.x); o.y = fmaf(f, v[q].y, o.y); o.z = fmaf(f, v[q].z, o.z); o.w = fmaf(f, v[q].w, o.w);
+                }
             }
             store4(A, S::DV, sg.q0, sg.h, R, ch, o, l);
         }
