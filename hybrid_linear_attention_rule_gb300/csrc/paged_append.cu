@@ -427,8 +427,9 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
                     if (bad) {
                         word = make_uint2(0, 0);
                         pr = __halves2half2(__ushort_as_half(0x7e00), __ushort_as_half(0x7e00));
-                    } else if (err == 0.f && !open_scale && normal) {
-                        // ties, mostly: only the channels next to a border are looked at again
+                    } else if (err == 0.f && !open_scale && normal && fabsf(nm) < 1e6f) {
+                        // ties, mostly: only the channels next to a border are looked at again (t is off by less than 1/8, so a code is the
+                        // whole number next to it or the one on the other side of the border)
 #pragma unroll
                         for (int q = 0; q < 16; ++q) {
                             const float2 xv = up(x[q / 2]), cv = up(cd[q / 2]);
@@ -441,6 +442,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
                             (q < 8 ? word.x : word.y) += (unsigned)more << (4 * (q & 7));
                         }
                     } else if (err == 0.f && !open_scale) {
+                        // codes that need a clamp, or a minimum of so many steps that t has lost its fraction: x - m first, which has not
                         word = make_uint2(0, 0);
                         const float iv = s > 0.f ? 1.f / s : 0.f;
 #pragma unroll
