@@ -188,6 +188,7 @@ __device__ __forceinline__ bool half_unsure(float x, float h, float d) {
 template <typename T> __device__ __noinline__ void group_in_double(const T *src, int c0, const Rope r, bool key, int pos, char *plane, int row) {
     const int lane = threadIdx.x & 31;
     double x[2];
+    bool bad = false;                                     // a channel that is not finite
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int c = c0 + 2 * lane + e;
@@ -199,7 +200,9 @@ template <typename T> __device__ __noinline__ void group_in_double(const T *src,
             rope_cs_f64(r.phase[t.pair], pos, cs, sn);
             x[e] = (double)r.mscale * (t.second ? x[e] * cs + y * sn : x[e] * cs - y * sn);
         }
+        bad = bad || !isfinite(x[e]);
     }
+    bad = __any_sync(0xffffffffu, bad);
     double lo = fmin(x[0], x[1]), hi = fmax(x[0], x[1]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -228,8 +231,9 @@ template <typename T> __device__ __noinline__ void group_in_double(const T *src,
         const unsigned code = s > 0.0 ? (unsigned)f + (diff > 0.0 || (diff == 0.0 && ((int)f & 1)) ? 1u : 0u) : 0u;
         byte |= code << (4 * e);
     }
-    reinterpret_cast<uint8_t *>(plane)[row * 32 + lane] = (uint8_t)byte;
-    if (lane == 0) reinterpret_cast<__half2 *>(plane + 512)[row] = __halves2half2(__double2half(s), __double2half(m));
+    const __half nan = __ushort_as_half(0x7e00);
+    reinterpret_cast<uint8_t *>(plane)[row * 32 + lane] = bad ? 0 : (uint8_t)byte;
+    if (lane == 0) reinterpret_cast<__half2 *>(plane + 512)[row] = bad ? __halves2half2(nan, nan) : __halves2half2(__double2half(s), __double2half(m));
 }
 
 // How a lane's 8 channels c .. c + 7 turn.
@@ -382,7 +386,6 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
                 mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
                 err = turned ? fabsf(A.r.mscale) * mag * (A.r.mscale == 1.f ? kSlackPlain : kSlack) : 0.f;
             }
-            const bool bad = !(hi - lo < INFINITY);       // a NaN or an infinity (or a range past FP32's)
             const float m = half_sat(lo), range = fmaxf(hi - m, 0.f);
             const float sraw = range * (1.f / 15.f), s = half_sat(sraw);
             // what FP32 leaves open: the minimum, and the scale (its own roundings are within 2^-22 of it)
@@ -406,7 +409,8 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
             }
             // t's own error, t below 15.1: 2^-23 of t from inv, 2^-24 of t from the fma, 2^-24 of m / s from nm
             const float window = fmaf(fabsf(nm), 1.2e-7f, 3e-6f) + err * inv;
-            const bool plain = !bad && normal && !open_scale && away < 0.5f - window;
+            // (a group with a NaN, an infinity or a rotation that FP32 overflows has no normal scale, or a window too wide)
+            const bool plain = normal && !open_scale && away < 0.5f - window;
             uint2 word;
             {   // four codes to 16 bits: sums of whole numbers below 2^16
                 float h[4];
@@ -423,7 +427,10 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
             const unsigned rest = __ballot_sync(0xffffffffu, inside && !plain);
             unsigned open = 0;
             if (rest) {
-                if (rest & gmask) {
+                // wild: the rotation may have overflowed FP32 (or met an infinity: the path in double tells); bad: a NaN or an infinity
+                const bool wild = turned && !(fabsf(A.r.mscale) * mag <= 8e37f);
+                const bool bad = !wild && !(fabsf(lo) < INFINITY && fabsf(hi) < INFINITY);
+                if ((rest & gmask) && !wild) {
                     if (bad) {
                         word = make_uint2(0, 0);
                         pr = __halves2half2(__ushort_as_half(0x7e00), __ushort_as_half(0x7e00));
@@ -463,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
                         }
                     }
                 }
-                open = __ballot_sync(0xffffffffu, inside && (rest & gmask) && !bad && !(err == 0.f && !open_scale));
+                open = __ballot_sync(0xffffffffu, inside && (rest & gmask) && (wild || (!bad && !(err == 0.f && !open_scale))));
             }
             if (inside && !(open & gmask)) {
                 reinterpret_cast<uint2 *>(pl)[r16 * 4 + lane4] = word;

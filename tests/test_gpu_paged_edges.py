@@ -32,3 +32,37 @@ def test_groups_far_from_zero_and_narrow(base, step, most):
     c = Append([0, 9], [64, 30], 4, 128, 64, 32, "i4", torch.float32, make=lambda *s: base + step * rng.integers(0, most + 1, s))
     K.paged_append(c.cache, c.k, c.v, c.cu)
     assert np.array_equal(c.rows(), _stored(c, _np(c.k)))
+
+
+def _wide(s, rng):
+    """Finite channels up to FP32's largest: groups of both signs, of one sign, and of a few such channels among ordinary ones."""
+    x = rng.standard_normal(s)
+    kind = rng.integers(0, 4, s[:2] + (1,))
+    big = rng.uniform(1.8e38, 3.3e38, s) * np.where(rng.random(s) < 0.5, -1.0, 1.0)
+    some = rng.random(s) < 0.05
+    return np.where(kind == 0, big, np.where(kind == 1, np.abs(big), np.where((kind == 2) & some, big, x)))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("rope", [None, dict(dim=128), dict(dim=64, offset=64, layout="interleaved"),
+                                  dict(dim=34, offset=5, scaling="by_parts", factor=16.0, original_length=4096.0)], ids=str)
+def test_finite_groups_wider_than_fp32(rope, dtype):
+    """Groups whose range, or whose rotation, exceeds FP32's largest value hold no infinity: their scale and minimum saturate."""
+    rng = np.random.default_rng(3)
+    c = Append([0, 40], [64, 50], 4, 128, 64, 32, "i4", dtype, make=lambda *s: _wide(s, rng))
+    K.paged_append(c.cache, c.k, c.v, c.cu, rope=K.rope_table(device=DEV, **rope) if rope else None)
+    k = PP.rotate(_np(c.k), c.pos, **rope) if rope else _np(c.k)
+    got = c.rows()
+    assert np.isfinite(got).all()
+    assert np.array_equal(got, _stored(c, k))
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_a_turned_channel_that_is_not_finite_beside_wide_ones(value):
+    """Of the two groups of each turned head, those that a channel which is not finite reaches are NaN, the others are not."""
+    rng = np.random.default_rng(4)
+    c = Append([3], [20], 2, 128, 64, 16, "i4", torch.float32, make=lambda *s: _wide(s, rng))
+    c.k[4, 1, 70], c.k[7, 0, 3] = value, value                # half layout over 64 channels: 70 does not turn, 3 turns with 35
+    K.paged_append(c.cache, c.k, c.v, c.cu, rope=K.rope_table(64, device=DEV))
+    gone = np.isnan(c.rows()).reshape(20, 2, 3, 64)
+    assert gone[4, 1, 1].all() and gone[7, 0, 0].all() and gone.sum() == 128
