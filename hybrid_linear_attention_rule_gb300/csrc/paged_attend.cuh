@@ -194,11 +194,11 @@ struct Cursor {
     }
 };
 
-// out = O / l (* sigmoid(gate)) for channels ch .. ch + 3 of row R of a (sequence, key head) whose tokens begin at q0;
-// l = 0: a row that saw nothing.
-__device__ __forceinline__ void store4(const Args &A, int dv, int q0, int h, int R, int ch, float4 o, float l) {
+// out = O / l (* sigmoid(gate)) for channels ch .. ch + 3 of row R of a (sequence, key head) whose new tokens begin at q0, behind `past`
+// keys.  l = 0: a row that sees no key gives 0, one whose keys all score minus infinity 0 / 0.
+__device__ __forceinline__ void store4(const Args &A, int dv, int q0, int past, int h, int R, int ch, float4 o, float l) {
     const int i = R / A.G, hq = h * A.G + R - i * A.G;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = l == 0.f ? (past + i >= 0 ? __int_as_float(0x7fc00000) : 0.f) : 1.f / l;
     float x[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
     if (A.gate.p) {
         const int64_t at = (int64_t)(q0 + i) * A.gate.ts + (int64_t)hq * A.gate.hs + ch;
@@ -667,7 +667,7 @@ struct Segment {                                        // what a warp leaves fo
     int last;                                           // its last tile's unit
     int flags;                                          // 1: it holds its first tile, 2: its last
     int h, rb, q0, rows;                                // key head, row block, first token and rows of the sequence
-    int pad;
+    int past;                                           // keys before its first new token (negative: it has fewer than new ones)
 };
 
 // The row of units.  A (sequence, head, row block) takes `extra` units for its start and end (rows loaded, rotated and
@@ -867,7 +867,7 @@ template <class S> __global__ void __launch_bounds__(S::WARPS * 32, 1) attend_ke
             }
             const bool lost = cc.s.len < 0;
             const Segment done{(int)(base + extra), (int)(base + extra) + cc.s.tiles - 1, (begins ? 1 : 0) | (ends ? 2 : 0), cc.h, cc.rb,
-                               cc.s.q0, cc.s.cnt * A.G, 0};
+                               cc.s.q0, cc.s.cnt * A.G, cc.s.len - cc.s.cnt};
             const bool last = stop || dead;              // (a dead warp leaves its run: its outputs are invalid)
             if (!last) {
                 base += cc.s.tiles + extra;
@@ -880,7 +880,7 @@ template <class S> __global__ void __launch_bounds__(S::WARPS * 32, 1) attend_ke
                 for (int x = lane; x < S::ROWS * S::DV / 4; x += 32) {
                     const int r = x / (S::DV / 4), ch = 4 * (x - r * (S::DV / 4)), R = done.rb * S::ROWS + r;
                     if (R < done.rows)
-                        store4(A, S::DV, done.q0, done.h, R, ch, *reinterpret_cast<const float4 *>(work + 2 * S::ROWS + r * S::DV + ch), work[S::ROWS + r]);
+                        store4(A, S::DV, done.q0, done.past, done.h, R, ch, *reinterpret_cast<const float4 *>(work + 2 * S::ROWS + r * S::DV + ch), work[S::ROWS + r]);
                 }
                 __syncwarp();
             } else {
@@ -944,7 +944,7 @@ template <class S> __global__ void __launch_bounds__(S::WARPS * 32, 1) attend_ke
             }
         if (R >= sg.rows) continue;
         if (whole) {
-            store4(A, S::DV, sg.q0, sg.h, R, ch, o, l);
+            store4(A, S::DV, sg.q0, sg.past, sg.h, R, ch, o, l);
         } else {
             *reinterpret_cast<float4 *>(dst + 2 * S::ROWS + r * S::DV + ch) = o;
             if (ch == 0) {
@@ -1003,7 +1003,7 @@ template <class S> __global__ void __launch_bounds__(S::WARPS * 32, 1) attend_ke
                     o.x = fmaf(f, v[q].x, o.x); o.y = fmaf(f, v[q].y, o.y); o.z = fmaf(f, v[q].z, o.z); o.w = fmaf(f, v[q].w, o.w);
                 }
             }
-            store4(A, S::DV, sg.q0, sg.h, R, ch, o, l);
+            store4(A, S::DV, sg.q0, sg.past, sg.h, R, ch, o, l);
         }
     }
 }

@@ -714,7 +714,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                 const int rr = x / (S::DV / 4), ch = 4 * (x - rr * (S::DV / 4));
                 const float4 v = *reinterpret_cast<const float4 *>(stage + rr * (S::DV + 4) + ch);
                 if (begins && ends) {
-                    store4(A, S::DV, c.s.q0, c.h, R0 + rr, ch, v, fin[128 + rr]);
+                    store4(A, S::DV, c.s.q0, c.s.len - c.s.cnt, c.h, R0 + rr, ch, v, fin[128 + rr]);
                 } else {
                     *reinterpret_cast<float4 *>(rec + 256 + rr * S::DV + ch) = v;
                     if (ch == 0) {
@@ -725,7 +725,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
             }
             if (!(begins && ends)) {
                 const int key = (int)(base + extra);
-                const Segment sg{key, key + c.s.tiles - 1, (begins ? 1 : 0) | (ends ? 2 : 0), c.h, c.rb, c.s.q0, rows, 0};
+                const Segment sg{key, key + c.s.tiles - 1, (begins ? 1 : 0) | (ends ? 2 : 0), c.h, c.rb, c.s.q0, rows, c.s.len - c.s.cnt};
                 if (begins) out[1] = sg;
                 else out[0] = sg;
             }
@@ -787,7 +787,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
 #pragma unroll
                 for (int q = 0; q < ITEMS; ++q) {
                     const int x = x0 + 256 * q, r = x / C4;
-                    if (x < live * C4) store4(A, S::DV, sg.q0, sg.h, sg.rb * S::ROWS + r, 4 * (x - r * C4), v4[q], wt[count * 128 + r]);
+                    if (x < live * C4) store4(A, S::DV, sg.q0, sg.past, sg.h, sg.rb * S::ROWS + r, 4 * (x - r * C4), v4[q], wt[count * 128 + r]);
                 }
             }
             tc::named_bar(2, 256);

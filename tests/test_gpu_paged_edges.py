@@ -9,6 +9,7 @@ pytestmark = pytest.mark.gpu
 import hybrid_linear_attention_rule_gb300 as K  # noqa: E402
 import paged_plain as PP  # noqa: E402
 from test_gpu_paged_append import Case as Append  # noqa: E402
+from test_gpu_paged_attend import Case as Attend, _check  # noqa: E402
 
 DEV = "cuda:0"
 
@@ -66,3 +67,19 @@ def test_a_turned_channel_that_is_not_finite_beside_wide_ones(value):
     K.paged_append(c.cache, c.k, c.v, c.cu, rope=K.rope_table(64, device=DEV))
     gone = np.isnan(c.rows()).reshape(20, 2, 3, 64)
     assert gone[4, 1, 1].all() and gone[7, 0, 0].all() and gone.sum() == 128
+
+
+@pytest.mark.parametrize("total,new,heads,group", [([37, 2], [37, 1], 2, 1), ([40, 3], [4, 3], 2, 1), ([30], [12], 2, 4), ([5000], [12], 1, 1), ([5000], [3], 1, 2)], ids=str)
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_a_row_whose_keys_all_score_minus_infinity(total, new, heads, group, out):
+    """As in a plain softmax: NaN while no key scores more, ordinary once one does."""
+    spoiled = [t - c + min(3, c - 1) if c > 1 else t for t, c in zip(total, new)]      # keys 0 .. of each sequence
+
+    def spoil(n, rows):
+        rows[:spoiled[n], 0, 3] = float("inf")
+    c = Attend(total, new, heads, group, 128, 128, 16, "bf16", seed=12, edit=spoil)
+    c.q[:, :, 3] = -0.75
+    want, tol = c.want()
+    got = c.run(out)
+    assert np.isnan(want).any() and np.isfinite(want).any()
+    _check(got, want, tol, out)
