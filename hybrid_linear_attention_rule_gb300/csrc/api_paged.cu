@@ -178,9 +178,7 @@ int k3mla_paged_attend(const k3mla_paged_cache *cache, const k3mla_view *q, int 
     if (cu_seqlens_host)
         for (int n = 0; n < cache->N; ++n)
             if (cu_seqlens_host[n + 1] - cu_seqlens_host[n] > max_new) return K3KDA_ERR_INVALID_ARG;
-    // the kernel counts its units (16-token strips at the finest, and a few more for each head and 4-row block) in 31 bits
-    if (((double)T * (Hq / cache->heads) / 4 + cache->N) * cache->heads * ((double)cache->max_pages * cache->page_size / 16 + 4) > 2e9)
-        return K3KDA_ERR_UNSUPPORTED;
+    if (paged_attend_units(cache, Hq / cache->heads, T, max_new, cu_seqlens != nullptr) > 2147483647.0) return K3KDA_ERR_UNSUPPORTED;
     if (int e = check_rope(rope, cache->dqk)) return e;
     if (T == 0) return K3KDA_OK;
     if (int e = check_view(q, in_dtype, T, Hq, false)) return e;

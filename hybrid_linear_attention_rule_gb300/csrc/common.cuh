@@ -157,6 +157,7 @@ cudaError_t launch_paged_read(const k3mla_paged_cache *c, const k3mla_view *k, c
                               int T, cudaStream_t s);
 // attention over it (csrc/paged_attend.cu)
 size_t paged_attend_workspace(int dqk, int dv);
+double paged_attend_units(const k3mla_paged_cache *c, int G, int T, int max_new, bool packed);   // at most so many units of work
 cudaError_t launch_paged_attend(const k3mla_paged_cache *c, const k3mla_view *q, int bf16, int Hq, const int32_t *cu, int T,
                                 int max_new, const k3mla_rope_args *rope, float scale, const k3mla_view *gate, void *out,
                                 int out_bf16, void *ws, cudaStream_t s);

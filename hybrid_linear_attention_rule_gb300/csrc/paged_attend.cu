@@ -14,6 +14,24 @@ static int rows_from(bool i4, int dqk) { return i4 ? 52 - dqk / 8 : 8; }
 // whether blocks of 128 rows fit tensor memory
 static bool wide_ok(int dqk, int dv) { return dqk <= 192 && dv <= 128; }
 
+// Which kernel takes a call: four rows at a time where no sequence has more (half the products and registers), else eight, else
+// blocks of 128 on tcgen05.
+static int rows_at_once(bool i4, int dqk, int dv, long long rows) {
+    return rows > rows_from(i4, dqk) && wide_ok(dqk, dv) ? 128 : rows <= 4 ? 4 : 8;
+}
+
+// What the call's units (paged_attend.cuh) cannot exceed, whatever the lengths are: every row block of every sequence with the tiles of
+// the whole table, one block begun for each sequence that has a token.  The kernels count them in 31 bits.
+double paged_attend_units(const k3mla_paged_cache *c, int G, int T, int max_new, bool packed) {
+    const bool i4 = c->format == K3MLA_CACHE_I4;
+    const int rows = rows_at_once(i4, c->dqk, c->dv, (long long)(packed ? max_new : 1) * G);
+    const int tile = rows == 128 ? attend::kRowsTile : attend::few_strips(i4, (c->dqk + c->dv) / 64) * kStrip;
+    const int extra = rows == 128 ? attend::kRowsExtra : attend::kExtra;
+    const long long width = (long long)c->max_pages * c->page_size, tiles = width > tile ? (width + tile - 1) / tile : 1;
+    const double blocks = (double)((long long)T * G / rows) + (T < c->N ? T : c->N);
+    return blocks * c->heads * (double)(tiles + extra);
+}
+
 // Status word and counters, then two records a CTA: its first and its last (sequence, head, row block).  One size for all
 // shapes, that of the largest records, so that any call may follow any other in one workspace.
 size_t paged_attend_workspace(int, int) {
@@ -39,12 +57,11 @@ cudaError_t launch_paged_attend(const k3mla_paged_cache *c, const k3mla_view *q,
     A.counters = A.status + 64;
     A.partial = reinterpret_cast<float *>(static_cast<char *>(ws) + attend::kHeadBytes);
     if (!cu) max_new = 1;
-    // four rows at a time where no sequence has more (half the products and registers), else eight, else blocks of 128 on tcgen05
-    const long long rows = (long long)max_new * A.G;
     const bool i4 = c->format == K3MLA_CACHE_I4;
-    if (rows > rows_from(i4, c->dqk) && wide_ok(c->dqk, c->dv)) return i4 ? attend::run_i4_rows(c->dqk, c->dv, A, s) : attend::run_bf16_rows(c->dqk, c->dv, A, s);
-    if (i4) return rows <= 4 ? attend::run_i4_r4(c->dqk, c->dv, A, max_new, s) : attend::run_i4_r8(c->dqk, c->dv, A, max_new, s);
-    return rows <= 4 ? attend::run_bf16_r4(c->dqk, c->dv, A, max_new, s) : attend::run_bf16_r8(c->dqk, c->dv, A, max_new, s);
+    const int rows = rows_at_once(i4, c->dqk, c->dv, (long long)max_new * A.G);
+    if (rows == 128) return i4 ? attend::run_i4_rows(c->dqk, c->dv, A, s) : attend::run_bf16_rows(c->dqk, c->dv, A, s);
+    if (i4) return rows == 4 ? attend::run_i4_r4(c->dqk, c->dv, A, max_new, s) : attend::run_i4_r8(c->dqk, c->dv, A, max_new, s);
+    return rows == 4 ? attend::run_bf16_r4(c->dqk, c->dv, A, max_new, s) : attend::run_bf16_r8(c->dqk, c->dv, A, max_new, s);
 }
 
 }  // namespace k3kda

@@ -41,6 +41,8 @@ namespace attend {
 constexpr int kMaxCtas = 160;                          // partials and counters of a workspace
 constexpr size_t kHeadBytes = 256 + 4096;              // status word, counters (4 B a CTA)
 constexpr int kMaxRows = 8;
+constexpr int kExtra = 2, kRowsExtra = 10;             // units of a block's start and end, in tiles: few rows, 128-row blocks
+constexpr int kRowsTile = 64;                          // keys of a tile of 128-row blocks
 constexpr unsigned kWaitTries = 1u << 22;              // each try suspends for a while: seconds in all
 static_assert(kMaxCtas * 4 <= 4096, "counters");
 
@@ -58,16 +60,19 @@ struct Args {
     float *partial;                                    // [kMaxCtas][2] records
 };
 
+// strips of a tile of the few-row kernel, pages with pl planes
+constexpr int few_strips(bool i4, int pl) { return i4 ? (pl <= 4 ? 4 : 2) : (pl <= 2 ? 2 : 1); }
+
 template <int DQK_, int DV_, int RT_, bool I4_> struct Shape {
     static constexpr int DQK = DQK_, DV = DV_, RT = RT_;
     static constexpr bool I4 = I4_;
     static constexpr int PK = DQK / 64, PV = DV / 64, PL = PK + PV;
     static constexpr int ROWS = 4 * RT;
     static constexpr int PLANE = I4 ? kPlaneI4 : kPlaneBf16, STRIP = PL * PLANE;
-    static constexpr int NS = I4 ? (PL <= 4 ? 4 : 2) : (PL <= 2 ? 2 : 1);   // strips of a tile
+    static constexpr int NS = few_strips(I4, PL);                              // strips of a tile
     static constexpr int TILE = NS * kStrip, STAGE = NS * STRIP;
     static constexpr int WARPS = I4 ? (PL <= 4 ? 8 : RT == 1 ? 8 : 4) : (PL <= 4 ? 6 : 4);
-    static constexpr int EXTRA = 2;                                             // units of a block's start and end, in tiles
+    static constexpr int EXTRA = kExtra;
     static constexpr int QS = DQK + 8;                                          // floats between staged rows
     static constexpr int RECORD = ROWS * (DV + 2);                              // floats: m, l, O
     static constexpr int STAGED = ROWS * (QS + PK + 1);                         // floats: rows, their sums and exponents

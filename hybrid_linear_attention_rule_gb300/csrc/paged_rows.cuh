@@ -31,8 +31,8 @@ template <int DQK_, int DV_, bool I4_> struct RowsShape {
     static constexpr int DQK = DQK_, DV = DV_;
     static constexpr bool I4 = I4_;
     static constexpr int PK = DQK / 64, PV = DV / 64, PL = PK + PV;
-    static constexpr int ROWS = 128, NS = 4, TILE = 64;
-    static constexpr int EXTRA = 10;                                            // a block's start and end in tiles (few tokens, bf16 pages: 4: 112 us, 6: 97, 10: 89, 14: 89)
+    static constexpr int ROWS = 128, NS = 4, TILE = kRowsTile;
+    static constexpr int EXTRA = kRowsExtra;                                    // (few tokens, bf16 pages: 4: 112 us, 6: 97, 10: 89, 14: 89)
     static constexpr int STRIP = PL * (I4 ? kPlaneI4 : kPlaneBf16);
     static constexpr int GK = I4 ? PK : 1, GV = I4 ? PV : 1;                    // groups of scores, of weights
     static constexpr int SB = 64 * (GK > GV ? GK : GV);                         // TMEM columns of a tile's scores, then weights

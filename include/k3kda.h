@@ -531,7 +531,13 @@ int k3mla_paged_read(const k3mla_paged_cache *cache, const k3mla_view *k_out, co
  * workspace: k3mla_paged_attend_workspace_size bytes (the same for every shape, 21.3 MB), 256-byte aligned, zero-filled
  * before its first use, owned by one call at a time (calls of any shape may follow one another); its first word is the status word of
  * k3kda_workspace_status: after a TIMEOUT zero-fill it again.  One launch on `stream`.
- * Errors: INVALID_ARG (Hq not a multiple of heads), UNSUPPORTED, ALIGNMENT, WORKSPACE, CUDA. */
+ * Errors: INVALID_ARG (Hq not a multiple of heads), UNSUPPORTED, ALIGNMENT, WORKSPACE, CUDA.
+ * UNSUPPORTED: Hq > 65536, max_new > 2^24, T Hq / heads > 2^28, or more than 2^31 - 1 units of work,
+ *     (floor(T (Hq / heads) / R) + min(N, T)) heads (ceil(max_pages page_size / K) + E),
+ * where R rows by K keys is what a kernel takes at a time, E a block's start: with max_new (Hq / heads) query rows above 8 (bf16 pages)
+ * or 52 - dqk / 8 (4 bits), dqk <= 192 and dv <= 128, R = 128, K = 64, E = 10 (65,536 tokens of 32 heads over a
+ * table of 1 M tokens are an eighth of it); else R = 8 (4 up to 4 rows), E = 2 and K = 16 (bf16, 32 with dqk = dv = 64) or 32 (4 bits, 64 up to
+ * dqk + dv = 256). */
 size_t k3mla_paged_attend_workspace_size(int Hq, int heads, int dqk, int dv);
 int k3mla_paged_attend(const k3mla_paged_cache *cache, const k3mla_view *q, int in_dtype, int Hq,
                        const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int T, int max_new,

@@ -9,7 +9,7 @@ pytestmark = pytest.mark.gpu
 import hybrid_linear_attention_rule_gb300 as K  # noqa: E402
 import paged_plain as PP  # noqa: E402
 from test_gpu_paged_append import Case as Append  # noqa: E402
-from test_gpu_paged_attend import Case as Attend, _check  # noqa: E402
+from test_gpu_paged_attend import Case as Attend, _check, _long  # noqa: E402
 
 DEV = "cuda:0"
 
@@ -83,3 +83,24 @@ def test_a_row_whose_keys_all_score_minus_infinity(total, new, heads, group, out
     got = c.run(out)
     assert np.isnan(want).any() and np.isfinite(want).any()
     _check(got, want, tol, out)
+
+
+def _bounds(c):
+    """The attention cases' bounds for all rows."""
+    return np.concatenate([c._bound(n, PP.rotate(_np(c.q[int(c.cu[n]):int(c.cu[n + 1])]), np.arange(t - m, t), *c.rope), m)
+                           for n, (t, m) in enumerate(zip(c.total, c.new))])
+
+
+@pytest.mark.parametrize("fmt", ["i4", "bf16"])
+@pytest.mark.parametrize("total,new,heads,group,width", [([3001], [3001], 2, 4, 1 << 20), ([2048, 1500], [2048, 1400], 8, 8, 1 << 18),
+                                                         ([1030, 7, 4000], [1030, 7, 3333], 3, 1, 1 << 22)], ids=str)
+def test_long_prompts_under_wide_tables(fmt, total, new, heads, group, width):
+    """Prompts of thousands of tokens, from position 0 and behind cached ones, with a block table made for long contexts: against the
+    64-bit form, and the bits of a narrow table."""
+    c = Attend(total, new, heads, group, 128, 128, 64, fmt, (128, 0, "half"), seed=41)
+    narrow = c.run()
+    _check(narrow, _long(c), _bounds(c))
+    tab = np.full((len(total), width // 64), -3, np.int32)
+    tab[:, :c.tab.shape[1]] = c.tab
+    c.cache = K.PagedCache(c.pool, torch.from_numpy(tab).to(DEV), c.cache.kv_len, 64, 128, 128, fmt)
+    assert torch.equal(c.run(), narrow)
