@@ -199,6 +199,18 @@ struct Cursor {
     }
 };
 
+// Whether sequence n begins behind its end.  Without such a sequence the sequences' rows lie apart, T at most, and the units are as many as
+// the call was checked for; with one, sums of them could pass 32 bits.
+__device__ __forceinline__ bool decreases(const Args &A, int n) { return A.cu && A.cu[n + 1] < A.cu[n]; }
+
+// A call whose cu_seqlens decreases: NaN for all rows.
+__device__ __forceinline__ void all_nan(const Args &A, int dv) {
+    const unsigned x = A.out_bf16 ? 0x7fc07fc0u : 0x7fc00000u;
+    const int64_t pieces = (int64_t)A.T * A.Hq * dv / (A.out_bf16 ? 8 : 4);
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * blockDim.x)
+        reinterpret_cast<uint4 *>(A.out)[i] = make_uint4(x, x, x, x);
+}
+
 // out = O / l (* sigmoid(gate)) for channels ch .. ch + 3 of row R of a (sequence, key head) whose new tokens begin at q0, behind `past`
 // keys.  l = 0: a row that sees no key gives 0, one whose keys all score minus infinity 0 / 0.
 __device__ __forceinline__ void store4(const Args &A, int dv, int q0, int past, int h, int R, int ch, float4 o, float l) {
@@ -732,8 +744,10 @@ template <class S> __global__ void __launch_bounds__(S::WARPS * 32, 1) attend_ke
     const int per = (A.P.N + THREADS - 1) / THREADS;
     const int n_lo = min(A.P.N, (int)threadIdx.x * per), n_hi = min(A.P.N, n_lo + per);
     unsigned own = 0, own_tiles = 0;                     // (sequence, head, row block)s, tiles
+    bool bent = false;
     for (int n = n_lo; n < n_hi; ++n) {
         const Seq q = load_seq<S>(A, n);
+        bent = bent || decreases(A, n);
         own += q.pairs(A.P.heads);
         own_tiles += q.pairs(A.P.heads) * q.tiles;
     }
@@ -756,7 +770,7 @@ template <class S> __global__ void __launch_bounds__(S::WARPS * 32, 1) attend_ke
         tc::fence_mbar_init();
         segs[2 * warp].key = segs[2 * warp + 1].key = -1;
     }
-    __syncthreads();
+    if (__syncthreads_or(bent)) return all_nan(A, S::DV);
     unsigned pairs = 0, tiles = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {

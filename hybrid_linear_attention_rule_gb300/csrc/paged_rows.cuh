@@ -168,8 +168,10 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
     const int per = (A.P.N + S::THREADS - 1) / S::THREADS;
     const int n_lo = min(A.P.N, (int)threadIdx.x * per), n_hi = min(A.P.N, n_lo + per);
     unsigned own = 0, own_tiles = 0;
+    bool bent = false;
     for (int n = n_lo; n < n_hi; ++n) {
         const Seq q = load_seq<S>(A, n);
+        bent = bent || decreases(A, n);
         own += q.pairs(A.P.heads);
         own_tiles += q.pairs(A.P.heads) * q.tiles;
     }
@@ -203,7 +205,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
         tc::fence_mbar_init();
         dead_flag = 0;
     }
-    __syncthreads();
+    if (__syncthreads_or(bent)) return all_nan(A, S::DV);
     unsigned pairs = 0, tiles = 0;
     for (int w = 0; w < S::WARPS; ++w) {
         run += w < warp ? part_sum[w] : 0;

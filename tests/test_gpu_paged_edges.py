@@ -104,3 +104,17 @@ def test_long_prompts_under_wide_tables(fmt, total, new, heads, group, width):
     tab[:, :c.tab.shape[1]] = c.tab
     c.cache = K.PagedCache(c.pool, torch.from_numpy(tab).to(DEV), c.cache.kv_len, 64, 128, 128, fmt)
     assert torch.equal(c.run(), narrow)
+
+
+@pytest.mark.parametrize("fmt", ["i4", "bf16"])
+@pytest.mark.parametrize("max_new", [1, 6, 60])
+@pytest.mark.parametrize("cu", [[0, 60, 0, 60, 0, 60], [0, 20, 10, 30, 40, 60], [0, 60, 60, 60, 60, 59], [7, 5, 60, 60, 60, 60]], ids=str)
+def test_a_packing_that_decreases(cu, max_new, fmt):
+    """Sequences that overlap count more rows than the call has: nothing is attended to, every output is NaN."""
+    c = Attend([100] * 5, [12] * 5, 2, 4, 128, 128, 16, fmt, seed=2)
+    right = c.run()
+    ws = K.paged_attend_workspace(c.cache, 8)
+    bad = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    for out in (torch.float32, torch.bfloat16):
+        assert torch.isnan(K.paged_attend(c.cache, c.q, bad, max_new, scale=c.scale, out_dtype=out, workspace=ws)).all()
+    assert torch.equal(c.run(ws=ws), right) and K.k3kda_workspace_status(ws) == 0
