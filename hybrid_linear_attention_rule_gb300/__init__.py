@@ -10,6 +10,10 @@ importing the binding's functions raises: there is no CPU fallback.
 Layouts (row-major, contiguous): q, k, g [T, H, dk]; v, gate, out [T, H, dv];
 beta [T, H]; states [N, H, dk, dv] fp32; cu_seqlens int32 [N+1]; conv weights
 [2*H*dk + H*dv, W] fp32; conv state [N, W-1, 2*H*dk + H*dv] fp32.
+
+A call runs on the current stream, or on the one it is given.  Then what it allocates is that stream's
+(outputs are kept for the current stream too), and the caller orders the two: the stream waits for the inputs,
+the current stream for the outputs.
 """
 from __future__ import annotations
 
@@ -180,6 +184,30 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on(stream):
+    """Where a call on `stream` allocates and fills what it needs: on that stream (None: the current one).  A block that the current
+    stream's pool hands out may still be in use by that stream's pending kernels, which `stream` does not wait for."""
+    return torch.cuda.stream(stream)
+
+
+def _handed_out(stream, *tensors):
+    """Outputs made on `stream` for the caller's current stream: their blocks are not handed out again before that has used them."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(torch.cuda.current_stream(t.device))
+
+
+def _empty(shape, dtype, device, stream):
+    """A call's output."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    _handed_out(stream, t)
+    return t
+
+
 def _check(fn, st):
     if st != 0:
         lib = load_library()
@@ -303,12 +331,14 @@ def backward(q, k, v, g, beta, dO, initial_state=None, dS_final=None, cu_seqlens
     else:
         cu_host = cu_seqlens.to("cpu", torch.int32)
     N = int(cu_host.numel()) - 1
-    cu_dev = cu_host.to(q.device)
     scale = float(dk) ** -0.5 if scale is None else float(scale)
     f32 = dict(dtype=torch.float32, device=q.device)
-    out = dict(dq=torch.empty(T, H, dk, **f32), dk=torch.empty(T, H, dk, **f32), dv=torch.empty(T, H, dv, **f32),
-               dg=torch.empty(T, H, dk, **f32), dbeta=torch.empty(T, H, **f32), dS0=torch.empty(N, H, dk, dv, **f32))
-    ws = torch.empty(k3kda_backward_workspace_size(N, T, H, dk, dv), dtype=torch.uint8, device=q.device)
+    with _on(stream):
+        cu_dev = cu_host.to(q.device)
+        out = dict(dq=torch.empty(T, H, dk, **f32), dk=torch.empty(T, H, dk, **f32), dv=torch.empty(T, H, dv, **f32),
+                   dg=torch.empty(T, H, dk, **f32), dbeta=torch.empty(T, H, **f32), dS0=torch.empty(N, H, dk, dv, **f32))
+        ws = torch.empty(k3kda_backward_workspace_size(N, T, H, dk, dv), dtype=torch.uint8, device=q.device)
+    _handed_out(stream, *out.values())
     k3kda_backward(q, k, v, g, beta, initial_state, cu_dev, cu_host, N, T, H, dk, dv, scale, dO, dS_final,
                    out["dq"], out["dk"], out["dv"], out["dg"], out["dbeta"], out["dS0"], ws, stream)
     return out
@@ -375,16 +405,18 @@ def prefill(q, k, v, g, beta, initial_state=None, cu_seqlens=None, chunk=64, sca
         cu_h = torch.tensor([0, T], dtype=torch.int32)
     else:
         cu_h = cu_seqlens.to("cpu", torch.int32).contiguous()
-    cu_d = cu_h.to(dev)
     N = cu_h.numel() - 1
-    out = torch.empty((T, H, dv), dtype=out_dtype or q.dtype, device=dev)
-    fs = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev) if return_final_state else None
     W = 0 if conv_weight is None else conv_weight.shape[1]
-    if workspace is None:
-        size_fn = k3kda_prefill_workspace_min if min_workspace else k3kda_prefill_workspace_size
-        nbytes = size_fn(N, T, H, dk, dv, chunk, _dtype(q), conv_weight is not None)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        workspace[:256].zero_()                     # the status word; the rest is written before it is read
+    with _on(stream):
+        cu_d = cu_h.to(dev)
+        out = torch.empty((T, H, dv), dtype=out_dtype or q.dtype, device=dev)
+        fs = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev) if return_final_state else None
+        if workspace is None:
+            size_fn = k3kda_prefill_workspace_min if min_workspace else k3kda_prefill_workspace_size
+            nbytes = size_fn(N, T, H, dk, dv, chunk, _dtype(q), conv_weight is not None)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            workspace[:256].zero_()                 # the status word; the rest is written before it is read
+    _handed_out(stream, out, fs)
     k3kda_prefill(q, k, v, g, beta, initial_state, cu_d, cu_h, N, T, H, dk, dv, chunk,
                   dk ** -0.5 if scale is None else scale, use_qk_l2norm, conv_weight, conv_state, W,
                   gate, out, fs, workspace, stream)
@@ -396,7 +428,7 @@ def decode_step(q, k, v, g, beta, state, gate=None, conv_weight=None, conv_state
     """Run k3kda_decode_step; state and conv_state are updated in place.  Returns out."""
     N, H, dk = q.shape
     dv = v.shape[2]
-    out = torch.empty((N, H, dv), dtype=out_dtype or q.dtype, device=q.device)
+    out = _empty((N, H, dv), out_dtype or q.dtype, q.device, stream)
     W = 0 if conv_weight is None else conv_weight.shape[1]
     k3kda_decode_step(q, k, v, g, beta, gate, conv_weight, conv_state, state, N, H, dk, dv, W,
                       dk ** -0.5 if scale is None else scale, use_qk_l2norm, out, stream)
@@ -407,9 +439,10 @@ def short_conv(x, weight, conv_state=None, cu_seqlens=None, apply_silu=True, out
     """Run k3kda_short_conv over x [T, D]; conv_state is updated in place.  Returns out."""
     T, D = x.shape
     W = weight.shape[1]
-    cu = None if cu_seqlens is None else cu_seqlens.to(x.device, torch.int32)
+    with _on(stream):
+        cu = None if cu_seqlens is None else cu_seqlens.to(x.device, torch.int32)
     N = 1 if cu is None else cu.numel() - 1
-    out = torch.empty((T, D), dtype=out_dtype or x.dtype, device=x.device)
+    out = _empty((T, D), out_dtype or x.dtype, x.device, stream)
     k3kda_short_conv(x, weight, conv_state, cu, N, T, D, W, apply_silu, out, stream)
     return out
 
@@ -455,9 +488,10 @@ def mla_decode_step(q, k_new, v_new, k_cache, v_cache, cache_len, gate=None, sca
     dv = v_new.shape[-1]
     L_max = k_cache.shape[2]
     scale = float(dqk) ** -0.5 if scale is None else float(scale)
-    out = torch.empty(N, H, dv, dtype=out_dtype or q.dtype, device=q.device)
+    out = _empty((N, H, dv), out_dtype or q.dtype, q.device, stream)
     if workspace is None:
-        workspace = torch.empty(k3mla_decode_workspace_size(N, H, dqk, dv, L_max), dtype=torch.uint8, device=q.device)
+        with _on(stream):
+            workspace = torch.empty(k3mla_decode_workspace_size(N, H, dqk, dv, L_max), dtype=torch.uint8, device=q.device)
     k3mla_decode_step(q, k_new, v_new, gate, k_cache, v_cache, cache_len, N, H, dqk, dv, L_max, rope_dim, rope_theta,
                       scale, out, workspace, stream)
     return out
@@ -501,14 +535,6 @@ def _i32(t, what, shape):
     return t.data_ptr()
 
 
-def _empty(shape, dtype, device, stream):
-    """An output: torch's allocator is told of the stream that writes it when that is not the current one."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
 class RopeTable:
     """The rotation's table: phases [dim/2] on the device (kept alive here), the rotated channels
     [offset, offset + dim), their pair layout ("half" or "interleaved") and the factor mscale."""
@@ -550,9 +576,7 @@ def rope_table(dim, theta=10000.0, offset=0, layout="half", scaling="none", fact
 
 def _dense(shape, dtype, device, stream):
     """A new [tokens, heads, channels] output and its view (nothing about it needs a check)."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
+    t = _empty(shape, dtype, device, stream)
     return t, _View(t.data_ptr(), shape[1] * shape[2], shape[2])
 
 
@@ -753,10 +777,10 @@ def paged_attend(cache, q, cu_seqlens=None, max_new=None, rope=None, scale=None,
     if out is None:
         out = _empty((q.shape[0], q.shape[1], cache.dv), out_dtype or q.dtype, q.device, stream)
     if workspace is None:
-        workspace = paged_attend_workspace(cache, q.shape[1])
-        if stream is not None:                          # zeroed on the current stream, used on this one
+        if stream is not None:                          # (without a workspace the call has always waited for the current stream)
             stream.wait_stream(torch.cuda.current_stream())
-            workspace.record_stream(stream)
+        with _on(stream):
+            workspace = paged_attend_workspace(cache, q.shape[1])
     if max_new is None:
         max_new = 1 if cu_seqlens is None else max(1, q.shape[0])
     k3mla_paged_attend(cache, q, gate, out, workspace, cache.dqk ** -0.5 if scale is None else float(scale), cu_seqlens, None, max_new,
