@@ -9,6 +9,8 @@ using namespace k3kda;
 
 namespace {
 
+std::atomic<unsigned> g_paged_test_timeout{0};
+
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool type_ok(int t) { return t == K3KDA_F32 || t == K3KDA_BF16; }
 int size_of(int t) { return t == K3KDA_BF16 ? 2 : 4; }
@@ -90,7 +92,14 @@ int check_cache(const k3mla_paged_cache *c, const int32_t *cu, const int32_t *cu
 
 }  // namespace
 
+unsigned k3kda::take_paged_test_timeout() { return g_paged_test_timeout.exchange(0u); }
+
 extern "C" {
+
+// Test hook, beside k3kda_test_arm_wait_timeout: the next attention in blocks of 128 rows asks for none of its first tile's
+// copies in CTA 0, which gives up the wait for them after `tries` polls (0 disarms; a small call's CTA 0 may have no tile).  Only for tests on a working GPU: the armed call's outputs are
+// invalid by design.
+void k3kda_test_arm_paged_wait_timeout(unsigned tries) { g_paged_test_timeout.store(tries); }
 
 int k3mla_rope_table(int dim, double theta, int scale_kind, double factor, double original_length, double beta_fast,
                      double beta_slow, uint64_t *phase_host, float *mscale) {

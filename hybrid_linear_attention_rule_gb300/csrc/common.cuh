@@ -80,6 +80,8 @@ void count_launch();
 // (status recorded, nothing left in flight, TMEM freed) on a GPU that is working normally.
 enum TestTimeout { kTestScan = 0, kTestSinglePass = 1, kTestDecode = 2, kTestBackward = 3, kTestKinds = 4 };
 unsigned take_test_timeout(int which);
+// The same for the paged attention's blocks of 128 rows, armed by k3kda_test_arm_paged_wait_timeout.
+unsigned take_paged_test_timeout();
 
 // ---- launchers (defined in the kernel files, called by the C ABI layer) ----
 

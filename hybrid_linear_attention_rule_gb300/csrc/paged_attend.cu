@@ -59,6 +59,7 @@ cudaError_t launch_paged_attend(const k3mla_paged_cache *c, const k3mla_view *q,
     if (!cu) max_new = 1;
     const bool i4 = c->format == K3MLA_CACHE_I4;
     const int rows = rows_at_once(i4, c->dqk, c->dv, (long long)max_new * A.G);
+    A.test_limit = rows == 128 ? take_paged_test_timeout() : 0;
     if (rows == 128) return i4 ? attend::run_i4_rows(c->dqk, c->dv, A, s) : attend::run_bf16_rows(c->dqk, c->dv, A, s);
     if (i4) return rows == 4 ? attend::run_i4_r4(c->dqk, c->dv, A, max_new, s) : attend::run_i4_r8(c->dqk, c->dv, A, max_new, s);
     return rows == 4 ? attend::run_bf16_r4(c->dqk, c->dv, A, max_new, s) : attend::run_bf16_r8(c->dqk, c->dv, A, max_new, s);

@@ -58,6 +58,7 @@ struct Args {
     void *out;
     unsigned *status, *counters;
     float *partial;                                    // [kMaxCtas][2] records
+    unsigned test_limit;                               // 128-row blocks: 0; else the armed test hook's tries (common.cuh)
 };
 
 // strips of a tile of the few-row kernel, pages with pl planes

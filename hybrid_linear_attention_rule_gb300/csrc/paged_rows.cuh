@@ -585,6 +585,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                     if constexpr (S::I4) {
                         ok = wait_for(raw_full + 8 * (use & 1), use >> 1, dead, A.status);
                         if (ok && use >= S::KB) ok = wait_for(kv_free + 8 * slot, use / S::KB - 1, dead, A.status);
+                        ok = __all_sync(0xffffffffu, ok);    // (a warp gives up as one: what follows is the whole warp's)
                         if (!ok) break;
                         const char *raw = sm + S::AT_RAW + (use & 1) * S::RAW;
                         for (int x = ht; x < S::PL * 128; x += 256) {
@@ -622,7 +623,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                         tc::mbar_arrive(kv_full + 8 * slot);
                         tc::mbar_arrive(raw_free + 8 * (use & 1));
                     } else {
-                        ok = wait_for(kv_full + 8 * slot, use / S::KB, dead, A.status);
+                        ok = __all_sync(0xffffffffu, wait_for(kv_full + 8 * slot, use / S::KB, dead, A.status));
                         if (!ok) break;
                         if (bad_of[use & 7] || j0 + 64 > c.least) {
                             // value rows past what was brought hold anything, and a value that is not finite must not meet a
@@ -656,7 +657,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                 if (k >= 2) {
                     const unsigned use = done + k - 2;
                     const int ob = use % S::OB;
-                    ok = wait_for(o_full + 8 * ob, use / S::OB, dead, A.status);
+                    ok = __all_sync(0xffffffffu, wait_for(o_full + 8 * ob, use / S::OB, dead, A.status));
                     if (!ok) break;
                     tc::tc_fence_after();
                     const float cr = corr[(use & 3) * 128 + r];
@@ -796,6 +797,8 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
         }
     } else {
         give_registers<S::R_REST>();
+        const bool starve = A.test_limit != 0 && blockIdx.x == 0;
+        unsigned issued = 0, scored = 0, weighed = 0;    // tiles whose copies, scores' and outputs' products are issued
         segments([&](const Cursor &c, int t0, int T, unsigned done) {
             if (warp == S::PROD) {
                 // ---- producer
@@ -815,17 +818,19 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                     const bool good = mine && pg >= 0 && pg < A.P.num_pages;
                     const unsigned have = __ballot_sync(0xffffffffu, good), wrong = __ballot_sync(0xffffffffu, mine && !good);
                     const uint32_t full = S::I4 ? raw_full + 8 * (use & 1) : kv_full + 8 * slot;
+                    const bool skip = starve && use == 0;
                     if (lane == 0) {
                         int bits = 0;
                         for (int s = 0; s < 4; ++s) bits |= ((wrong >> (S::I4 ? s : s * S::PL)) & 1) << s;
                         bad_of[use & 7] = bits;
                         bad_of[8 + (use & 7)] = 0;
-                    if constexpr (S::I4)
-                        for (int v = 0; v < S::PV; ++v) poison[(use & 7) * S::PV + v] = 0;
-                        tc::mbar_arrive_expect_tx(full, __popc(have) * (S::I4 ? S::STRIP : kPlaneBf16));
+                        if constexpr (S::I4)
+                            for (int v = 0; v < S::PV; ++v) poison[(use & 7) * S::PV + v] = 0;
+                        if (!skip) tc::mbar_arrive_expect_tx(full, __popc(have) * (S::I4 ? S::STRIP : kPlaneBf16));
                     }
                     __syncwarp();
-                    if (good) {
+                    issued = use + 1;
+                    if (good && !skip) {
                         const char *src = A.P.pool + (int64_t)pg * A.P.page_bytes + (int64_t)c.h * A.P.block_bytes + (int64_t)(strip - j * A.per_page) * S::STRIP;
                         if constexpr (S::I4) {
                             tc::bulk_g2s(sm32 + S::AT_RAW + (use & 1) * S::RAW + lane * S::STRIP, src, S::STRIP, full);
@@ -833,6 +838,13 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                             const int p = lane % S::PL, s = lane / S::PL;
                             tc::bulk_g2s(sm32 + S::AT_KV + slot * S::KV + p * 8192 + s * kPlaneBf16, src + p * kPlaneBf16, kPlaneBf16, full);
                         }
+                    }
+                    if (starve && use == 1) {            // (with the second tile's copies in flight)
+                        if (!tc::mbar_wait_bounded(S::I4 ? raw_full : kv_full, 0, A.test_limit) && lane == 0) {
+                            *dead = 1;
+                            atomicOr(A.status, 2u);
+                        }
+                        break;
                     }
                 }
             } else if (warp == S::PROD + 1) {
@@ -862,6 +874,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                             }
                             tc::mma_commit(s_full + 8 * (use & 1));
                         }
+                        scored = use + 1;
                     }
                     if (k >= 1) {
                         const unsigned use = done + k - 1;
@@ -886,10 +899,28 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) rows_kernel(
                             tc::mma_commit(o_full + 8 * ob);
                             tc::mma_commit(kv_free + 8 * slot);
                         }
+                        weighed = use + 1;
                     }
                 }
             }
-        }, nothing, false);
+        }, [&](const Cursor &, unsigned, int, int) {
+            if (*dead == 0) return;
+            // the CTA gives up: what is in flight ends before its shared and tensor memory go
+            constexpr unsigned RING = S::I4 ? 2 : S::KB;
+            if (warp == S::PROD)
+                for (unsigned use = issued > RING ? issued - RING : 0; use < issued; ++use) {
+                    if (starve && use == 0) continue;
+                    tc::mbar_wait_bounded((S::I4 ? raw_full : kv_full) + 8 * (use % RING), (use / RING) & 1, kWaitTries);
+                }
+            if (warp == S::PROD + 1) {
+                const unsigned s = scored - 1, o = weighed - 1;
+                if (scored > 0) tc::mbar_wait_bounded(s_full + 8 * (s & 1), (s >> 1) & 1, kWaitTries);
+                if (weighed > 0) {
+                    tc::mbar_wait_bounded(o_full + 8 * (o % S::OB), (o / S::OB) & 1, kWaitTries);
+                    tc::mbar_wait_bounded(kv_free + 8 * (o % S::KB), (o / S::KB) & 1, kWaitTries);
+                }
+            }
+        }, false);
         tc::named_bar(1, S::THREADS);
     }
 }
