@@ -123,6 +123,7 @@ int k3mla_rope_table(int dim, double theta, int scale_kind, double factor, doubl
         }
         // whole turns a position do not show; the rest is at most 2^64 - 2^11 after the product (53 bits)
         double turns = f / kTwoPi;
+        if (!isfinite(turns)) return K3KDA_ERR_INVALID_ARG;
         turns -= floor(turns);
         phase_host[i] = (uint64_t)(turns * 18446744073709551616.0);
     }

@@ -438,7 +438,7 @@ typedef struct k3mla_view {
 
 /* Fill phase_host [dim/2] and *mscale (host memory).  Errors: INVALID_ARG for an odd dim or one
  * outside 2..512, theta or factor not positive and finite, BY_PARTS without original_length > 0 and
- * beta_fast > beta_slow, NTK with dim = 2, an unknown kind. */
+ * beta_fast > beta_slow, NTK with dim = 2, an unknown kind, a frequency that is not finite. */
 int k3mla_rope_table(int dim, double theta, int scale_kind, double factor, double original_length,
                      double beta_fast, double beta_slow, uint64_t *phase_host, float *mscale);
 

@@ -49,3 +49,20 @@ def test_no_tokens_and_one_each(lib):
     assert _call(lib, 0, 128, 8, 1 << 24, N=100000, max_new=1) == 0
     assert _call(lib, 4096, 8, 4, 1 << 20, N=4096, max_new=1, cu=None) == WORKSPACE
     assert _call(lib, 65536, 32, 4, 1 << 20, N=65536, max_new=1, cu=None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw", [dict(theta=1e-320), dict(scaling="linear", factor=1e-310), dict(theta=1e-300, scaling="linear", factor=1e-20),
+                                dict(theta=1e-300, scaling="by_parts", factor=1e-300, original_length=4096.0)], ids=str)
+def test_table_refuses_frequencies_that_are_not_finite(kw):
+    """Their turns have no fraction to hold."""
+    with pytest.raises(K.K3KDAError) as e:
+        K.k3mla_rope_table(**{"dim": 128, "theta": 10000.0, **kw})
+    assert e.value.status == -1
+
+
+def test_table_takes_frequencies_up_to_the_largest():
+    """Whole turns a position leave a phase of 0, and an infinite base the first pair alone."""
+    phase, _ = K.k3mla_rope_table(4, 1e-300)
+    assert phase[1] == 0 and phase[0] != 0
+    phase, _ = K.k3mla_rope_table(8, 1e300, scaling="ntk", factor=1e30)
+    assert phase[0] != 0 and not phase[1:].any()
