@@ -65,7 +65,8 @@ int check_cache(const k3mla_paged_cache *c, const int32_t *cu, const int32_t *cu
     if (!c || c->N < 0 || c->heads < 1 || c->num_pages < 0 || c->max_pages < 0 || T < 0) return K3KDA_ERR_INVALID_ARG;
     if (c->format != K3MLA_CACHE_BF16 && c->format != K3MLA_CACHE_I4) return K3KDA_ERR_INVALID_ARG;
     if (!dims_ok(c->dqk, c->dv) || !page_ok(c->page_size) || c->heads > 65536) return K3KDA_ERR_UNSUPPORTED;
-    if ((long long)c->max_pages * c->page_size > 0x7fffffffLL) return K3KDA_ERR_UNSUPPORTED;
+    // (positions and the ends of their tiles are counted in 31 bits)
+    if ((long long)c->max_pages * c->page_size > (1LL << 31) - 256) return K3KDA_ERR_UNSUPPORTED;
     if (T > 0 && c->N == 0) return K3KDA_ERR_INVALID_ARG;
     if (!cu && T != c->N) return K3KDA_ERR_INVALID_ARG;
     if (cu_host) {

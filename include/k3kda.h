@@ -494,7 +494,8 @@ typedef struct k3mla_paged_cache {
     const int32_t *kv_len_host;        /* and every length is checked, INVALID_ARG if outside */
     int format;                        /* k3mla_cache_format                                  */
     int num_pages, page_size;          /* page_size: a multiple of 16, 16..256                */
-    int max_pages;                     /* columns of block_table                              */
+    int max_pages;                     /* columns of block_table; max_pages * page_size is at
+                                          most 2^31 - 256                                     */
     int N, heads, dqk, dv;             /* dqk in {64, 128, 192, 256}, dv in {64, 128, 256}    */
 } k3mla_paged_cache;
 

@@ -66,3 +66,10 @@ def test_table_takes_frequencies_up_to_the_largest():
     assert phase[1] == 0 and phase[0] != 0
     phase, _ = K.k3mla_rope_table(8, 1e300, scaling="ntk", factor=1e30)
     assert phase[0] != 0 and not phase[1:].any()
+
+
+@pytest.mark.parametrize("page,width,want", [(16, (1 << 27) - 16, 0), (16, (1 << 27) - 15, UNSUPPORTED), (16, (1 << 27) - 1, UNSUPPORTED), (256, (1 << 23) - 1, 0),
+                                             (240, (1 << 31) // 240, UNSUPPORTED)])
+def test_tables_whose_last_tile_would_pass_31_bits_are_refused(lib, page, width, want):
+    """A tile holds up to 64 tokens: with 2^31 - 16 positions the last one's end has no int."""
+    assert _attend(lib, T=0, page=page, width=width) == want
