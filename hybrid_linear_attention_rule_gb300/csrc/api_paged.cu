@@ -72,7 +72,7 @@ int check_cache(const k3mla_paged_cache *c, const int32_t *cu, const int32_t *cu
     if (cu_host) {
         if (cu_host[0] != 0 || cu_host[c->N] != T) return K3KDA_ERR_INVALID_ARG;
         for (int n = 0; n < c->N; ++n)
-            if (cu_host[n + 1] < cu_host[n]) return K3KDA_ERR_INVALID_ARG;
+            if (cu_host[n + 1] < cu_host[n] || (!cu && cu_host[n + 1] != n + 1)) return K3KDA_ERR_INVALID_ARG;
     }
     if (c->kv_len_host)
         for (int n = 0; n < c->N; ++n) {

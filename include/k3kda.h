@@ -505,7 +505,7 @@ size_t k3mla_paged_block_bytes(int format, int page_size, int dqk, int dv);
 /* Append T packed new tokens: sequence n's are rows cu_seqlens[n] .. cu_seqlens[n+1]-1 of k_new
  * [T, heads, dqk] and v_new [T, heads, dv] (in_dtype) and go to positions kv_len[n] - count .. kv_len[n]-1.
  * cu_seqlens [N+1] (int32, device; cu_seqlens_host an optional host copy, checked) or NULL: one token for each
- * sequence, T = N.  rope (or NULL): keys are rotated by their positions before they are stored.  Sequences may share
+ * sequence, T = N (a host copy then has to say so too).  rope (or NULL): keys are rotated by their positions before they are stored.  Sequences may share
  * pages that none of them appends to.
  * One launch on `stream`.  Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, CUDA.  T = 0 launches nothing. */
 int k3mla_paged_append(const k3mla_paged_cache *cache, const k3mla_view *k_new, const k3mla_view *v_new, int in_dtype,

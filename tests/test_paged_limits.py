@@ -3,7 +3,7 @@ attention from the one on its workspace)."""
 import pytest
 
 import hybrid_linear_attention_rule_gb300 as K
-from test_rope_paged_abi import _attend, _v
+from test_rope_paged_abi import _adr, _attend, _calls, _host, _v
 
 UNSUPPORTED, WORKSPACE = -2, -4
 
@@ -73,3 +73,10 @@ def test_table_takes_frequencies_up_to_the_largest():
 def test_tables_whose_last_tile_would_pass_31_bits_are_refused(lib, page, width, want):
     """A tile holds up to 64 tokens: with 2^31 - 16 positions the last one's end has no int."""
     assert _attend(lib, T=0, page=page, width=width) == want
+
+
+def test_a_host_packing_alone_is_not_taken_for_one_token_each(lib):
+    """Without the device array every sequence has one token, whatever the host copy says; one that says otherwise is refused."""
+    for cu, want in (((0, 2, 2), -1), ((0, 0, 2), -1), ((0, 1, 2), WORKSPACE)):
+        assert _attend(lib, T=2, cu=None, cu_h=_adr(_host(*cu)), ws_bytes=0) == want
+    assert _calls(lib, T=2, cu=None, cu_h=_adr(_host(0, 2, 2))) == (-1, -1)
