@@ -772,8 +772,9 @@ def k3mla_paged_attend(cache, q, gate, out, workspace, scale, cu_seqlens=None, c
 def paged_attend(cache, q, cu_seqlens=None, max_new=None, rope=None, scale=None, gate=None, out=None, out_dtype=None,
                  workspace=None, stream=None):
     """Attention of the T packed new tokens q [T, Hq, dqk] over the cache, which holds them already (append first).
-    max_new: at least the most new tokens of a sequence (default: T; 1 without cu_seqlens); scale
-    defaults to dqk^-1/2.  Returns out [T, Hq, dv]."""
+    max_new: the most new tokens of a sequence; it chooses the kernel, so a wrong one costs time only (default: 1 without
+    cu_seqlens or with no more tokens than sequences, else T).  scale defaults to dqk^-1/2.  Returns out [T, Hq, dv].
+    Without a workspace one is made for the call, and its status word (k3kda_workspace_status) goes with it."""
     if out is None:
         out = _empty((q.shape[0], q.shape[1], cache.dv), out_dtype or q.dtype, q.device, stream)
     if workspace is None:
@@ -782,7 +783,7 @@ def paged_attend(cache, q, cu_seqlens=None, max_new=None, rope=None, scale=None,
         with _on(stream):
             workspace = paged_attend_workspace(cache, q.shape[1])
     if max_new is None:
-        max_new = 1 if cu_seqlens is None else max(1, q.shape[0])
+        max_new = 1 if cu_seqlens is None or q.shape[0] <= cache.N else q.shape[0]
     k3mla_paged_attend(cache, q, gate, out, workspace, cache.dqk ** -0.5 if scale is None else float(scale), cu_seqlens, None, max_new,
                        rope, stream)
     return out

@@ -523,7 +523,8 @@ int k3mla_paged_read(const k3mla_paged_cache *cache, const k3mla_view *k_out, co
  * query head h reads key head h / (Hq / heads):
  *     out = softmax_j(scale rope(q, p) . k_j) . v  (* sigmoid(gate) when gate is given)
  * q [T, Hq, dqk], gate [T, Hq, dv] views of in_dtype, out [T, Hq, dv] dense, of out_dtype; cu_seqlens as for append;
- * max_new: at least the largest number of new tokens of a sequence (1 with cu_seqlens NULL).  A row that sees
+ * max_new: the largest number of new tokens of a sequence (1 with cu_seqlens NULL).  It chooses the kernel: without
+ * a host copy to check it against, a wrong one costs time, not results.  A row that sees
  * no key (p < 0, an empty sequence) is 0.  A cu_seqlens that decreases makes every row NaN; rows of no sequence are not written.  Scores, maxima, sums and outputs are held in FP32; where a tensor core
  * takes query rows and weights in 16 bits they are given as a high and a low part: 22 bits together with 4-bit pages
  * (fp16 parts, scaled so that none overflows), 16 bits with bf16 pages (bf16 parts; the cached values themselves have 8).

@@ -118,3 +118,21 @@ def test_a_packing_that_decreases(cu, max_new, fmt):
     for out in (torch.float32, torch.bfloat16):
         assert torch.isnan(K.paged_attend(c.cache, c.q, bad, max_new, scale=c.scale, out_dtype=out, workspace=ws)).all()
     assert torch.equal(c.run(ws=ws), right) and K.k3kda_workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("fmt", ["i4", "bf16"])
+@pytest.mark.parametrize("max_new", [None, 1, 3, 9, 400])
+@pytest.mark.parametrize("new,group", [([1, 0, 40, 2, 0, 0, 0, 7], 2), ([1, 0, 3, 2, 0, 0, 0, 1], 4), ([0, 8, 0, 0, 0, 0, 0, 0], 1)], ids=str)
+def test_max_new_chooses_a_kernel_and_changes_no_result(new, group, max_new, fmt):
+    """Too small or too large: whichever kernel takes the call reads the counts that there are."""
+    c = Attend([60 + 30 * i for i in range(8)], new, 2, group, 128, 128, 32, fmt, (64, 0, "interleaved"), gate=True, seed=15)
+    want, tol = [], []
+    for n, (t, m) in enumerate(zip(c.total, new)):
+        if m:
+            at = slice(int(c.cu[n]), int(c.cu[n + 1]))
+            q = PP.rotate(_np(c.q[at]), np.arange(t - m, t), *c.rope)
+            want.append(PP.attend(q, c.k[n], c.v[n], t - m + 1 + np.arange(m), c.scale, _np(c.gate[at])))
+            tol.append(c._bound(n, q, m))
+    want, tol = np.concatenate(want), np.concatenate(tol)
+    table = K.rope_table(64, layout="interleaved", device=DEV)
+    _check(K.paged_attend(c.cache, c.q, c.cu, max_new, table, gate=c.gate, out_dtype=torch.float32), want, tol)

@@ -80,3 +80,16 @@ def test_a_host_packing_alone_is_not_taken_for_one_token_each(lib):
     for cu, want in (((0, 2, 2), -1), ((0, 0, 2), -1), ((0, 1, 2), WORKSPACE)):
         assert _attend(lib, T=2, cu=None, cu_h=_adr(_host(*cu)), ws_bytes=0) == want
     assert _calls(lib, T=2, cu=None, cu_h=_adr(_host(0, 2, 2))) == (-1, -1)
+
+
+@pytest.mark.parametrize("tokens,sequences,packed,want", [(64, 64, True, 1), (5, 64, True, 1), (65, 64, True, 65), (64, 64, False, 1), (0, 3, True, 1)])
+def test_what_a_call_without_max_new_takes(monkeypatch, tokens, sequences, packed, want):
+    """A decode batch that is packed is one token a sequence, not one sequence of all tokens: the kernel for few rows."""
+    import types
+
+    import torch
+    taken = []
+    monkeypatch.setattr(K, "k3mla_paged_attend", lambda cache, q, gate, out, ws, scale, cu, cu_host, max_new, rope, stream: taken.append(max_new))
+    cache, q = types.SimpleNamespace(N=sequences, dqk=64, dv=64), torch.zeros(tokens, 1, 64)
+    K.paged_attend(cache, q, torch.zeros(sequences + 1, dtype=torch.int32) if packed else None, out=q, workspace=q)
+    assert taken == [want]
