@@ -136,3 +136,45 @@ def test_max_new_chooses_a_kernel_and_changes_no_result(new, group, max_new, fmt
     want, tol = np.concatenate(want), np.concatenate(tol)
     table = K.rope_table(64, layout="interleaved", device=DEV)
     _check(K.paged_attend(c.cache, c.q, c.cu, max_new, table, gate=c.gate, out_dtype=torch.float32), want, tol)
+
+
+@pytest.mark.parametrize("fmt", ["i4", "bf16"])
+@pytest.mark.parametrize("dqk,rows", [(64, 4), (64, 5), (64, 8), (64, 9), (64, 44), (64, 45), (128, 36), (128, 37), (192, 28), (192, 29), (256, 60)])
+def test_both_sides_of_the_borders_between_the_kernels(dqk, rows, fmt):
+    """4-bit pages: four rows, eight, then blocks of 128 from 45, 37 and 29 rows on; bf16 pages from 9; keys of 256 channels never.  Short
+    sequences and ones that many CTAs share."""
+    for total, new, heads, group in (([300, rows, 77], [rows] * 3, 2, 1), ([15000], [1], 2, rows)):
+        c = Attend(total, new, heads, group, dqk, 128, 64, fmt, (64, 0, "half"), seed=rows)
+        _check(c.run(), _long(c), _bounds(c))
+
+
+@pytest.mark.parametrize("fmt,group", [("i4", 4), ("i4", 8), ("i4", 64), ("bf16", 4), ("bf16", 8), ("bf16", 64)])
+@pytest.mark.parametrize("what", ["queries", "weights"])
+def test_both_parts_of_queries_and_weights_count(what, fmt, group):
+    """Two keys a sequence: the first scores 0, the second what the difference of two large products leaves ("queries", so that an error of
+    2^-16 of either shows) or one small product ("weights").  Values of 0 and of 0..15.
+
+    Bounds: parts of 16 bits leave 2^-16 of a query's channel or of a weight, parts of 22 bits 2^-22, FP32's sums and exponentials 2^-20;
+    a score's error d moves p = 1 / (1 + e^-s) by at most d / 4.  One part alone is off by 2^-9 or 2^-12: a hundred times the bound."""
+    large = 4096.0 if fmt == "bf16" else 7680.0                            # 15 * 512: its group's scale is exact
+    key = large if what == "queries" else 1.0 if fmt == "bf16" else 15.0
+
+    def edit(n, rows):
+        rows[...] = 0
+        rows[1, :, :2] = key
+        rows[1, :, 128:] = np.arange(128) % 16
+    c = Attend([2] * 8, [1] * 8, 16, group, 128, 128, 16, fmt, dtype=torch.float32, seed=1, edit=edit)
+    rng = np.random.default_rng(group)
+    q = np.zeros(tuple(c.q.shape))
+    if what == "queries":
+        q[..., 1] = rng.uniform(0.5, 2.0, q.shape[:2])
+        q[..., 0] = rng.uniform(-2.0, 2.0, q.shape[:2]) / (key * c.scale) - q[..., 1]
+    else:
+        q[..., 0] = rng.uniform(-3.0, 3.0, q.shape[:2]) / (key * c.scale)
+    c.q.copy_(torch.from_numpy(q.astype(np.float32)))
+    want, _ = c.want()
+    part = (2.0 ** -16 if fmt == "bf16" else 2.0 ** -22) + 2.0 ** -20
+    score = key * c.scale * np.abs(_np(c.q)[..., :2]).sum(-1, keepdims=True) * part
+    p = want[..., 15:16] / 15
+    err = np.abs(_np(c.run()) - want)
+    assert (err <= (np.arange(128) % 16) * (score / 4 + p * part)).all(), f"{(err.max(-1) / (15 * (score[..., 0] / 4 + p[..., 0] * part))).max():.2f}"
