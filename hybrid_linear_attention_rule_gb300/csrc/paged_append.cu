@@ -1,9 +1,10 @@
 // paged_append.cu -- new key and value rows into the paged cache (keys rotated on the way), and rows
 // back out of it as values, on sm_103a.
 //
-// Both move every element once; what they have to beat is their own arithmetic, some 15 instructions a channel.  Four
-// lanes hold a group (64 channels of a token and head), 16 channels each; a lane keeps its head and channels and
-// goes through its CTA's tokens, so that addresses, the rotation's layout and its table's place are worked out once.  Lanes of
+// Both move every element once; what they have to beat is their own arithmetic, appending some 34 instructions a channel (by the
+// profile: the slow paths below take a whole warp of eight groups when one group needs them).  Four lanes hold a group (64
+// channels of a token and head), 16 channels each; a lane keeps its head and channels and goes through its CTA's tokens, so
+// that addresses, the rotation's layout and its table's place are worked out once.  Lanes of
 // a warp hold the same channels of eight heads, so that keys that turn and values that do not seldom share one.
 // A CTA finds its tokens' sequences and pages once (a 32-way search of cu_seqlens, one warp a token) and forms their cosines
 // and sines once for all heads.  Pairs of channels go through packed FP32 instructions (fma.rn.f32x2).
@@ -16,14 +17,16 @@
 //     small next to it).
 //   - Else, in a group of channels that are not turned (exact in FP32: m is one rounding, s was clear), a code is decided
 //     by the sign of (x - m) - (c + 1/2) s, where (c + 1/2) s has at most 16 bits: one fma and, next to a tie, the
-//     rounding error of x - m.  Ties are common there (bf16 values): one group in 30.
-//   - Else (turned channels, FP32 errors of up to kSlack of the pair; about one group in 500) the warp repeats the group in
-//     double, two channels a lane, with the angle's sine and cosine in double.
+//     rounding error of x - m.  Ties are common there (bf16 values): one group in 30.  c comes from t, or, where a clamp is
+//     needed or m is more than 10^6 s (x / s - m / s has no fraction left), from x - m.
+//   - Else (turned channels, FP32 errors of up to kSlack of the pair: about one group in 500; or a rotation that FP32 may
+//     overflow) the warp repeats the group in double, two channels a lane, with the angle's sine and cosine in double.
 //
-// Measured (26,339 prompt tokens, 32 heads of 128 + 128 channels): append 250 us for 492 MB, where instruction issue is the bound
-// (56 M warp instructions for a quarter of it, HBM at a fifth of its rate); read 105 us, 4.7 TB/s, near a mixed copy's.
-// FP32 rows of 9,366 tokens, 8 heads of 192 + 128 channels, into bf16 pages and back: 49 us, 3.9 TB/s.  CTAs of 128 and 64
-// threads, or scalar FP32 in place of the packed instructions: 385 to 612 us for the first append and read instead of 358.
+// Measured (26,339 prompt tokens, 32 heads of 128 + 128 channels, 553 MB each way): append 248 us, 2.2 TB/s, where instruction
+// issue is the bound (57 M warp instructions for a quarter of it, HBM at a fifth of its rate); read 113 us, 4.9 TB/s, 72 % of
+// a copy's rate.  FP32 rows of 9,366 tokens, 8 heads of 192 + 128 channels, into bf16 pages and back: 50 us (append 34, read 19).
+// CTAs of 128 and 64 threads, or scalar FP32 in place of the packed instructions: 385 to 612 us for the first append and read
+// instead of 358.
 #include <math.h>
 
 #include "paged.cuh"

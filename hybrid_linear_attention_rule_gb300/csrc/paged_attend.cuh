@@ -26,9 +26,9 @@
 // A tile's products start at 0 and are added to O in FP32 by fma (which also rescales O): tensor-core sums of
 // few terms, ordinary rounding over the long axis.
 //
-// Measured, 4-bit pages, 128 + 128 channels.  64 sequences of 4 to 8,153 tokens, 32 heads, a query row each: 1,218 MB in 224 us,
-// 5.4 TB/s (80 % of a copy's rate); the copies alone took 220 us and the arithmetic alone, in an earlier state, 248: both bind.
-// One sequence of 250,008 tokens, 8 heads of 4 query rows: 288 MB in 67 us, of which some 12,000 cycles pass before the
+// Measured, 4-bit pages, 128 + 128 channels.  64 sequences of 4 to 8,153 tokens, 32 heads, a query row each: 1,218 MB in 221 us,
+// 5.5 TB/s (81 % of a copy's rate); the copies alone took 220 us and the arithmetic alone, in an earlier state, 248: both bind.
+// One sequence of 250,008 tokens, 8 heads of 4 query rows: 288 MB in 68 us, of which some 12,000 cycles pass before the
 // first product and 8,000 in the join.
 #pragma once
 

@@ -19,7 +19,9 @@
 // 1600 of products; with 4 warps and both passes forming the scores it was 4100); bf16 pages of 192 + 128, the products (1700)
 // and the softmax (2100) in turn.  A block's start, its rows' rotation and split, takes 8,000 to 12,000, the join of a shared
 // block 15,000.  462 new tokens of 4 sequences (13,365 cached), 8 heads of 4 query heads, 4-bit pages: 113 us.  153 new tokens of 48
-// sequences (82,739 cached), 4 heads of 8 query heads of 192 + 128 channels, bf16 pages: 217 MB in 86 us.
+// sequences (82,739 cached), 4 heads of 8 query heads of 192 + 128 channels, bf16 pages: 217 MB in 88 us.
+// A row block's tiles are those of the whole sequence; those that none of its rows sees are skipped, but the division into runs counts
+// them, so that a prompt from position 0 leaves the CTAs unevenly loaded: 8,192 tokens, 8 heads of 4 query heads, 4-bit pages 2,801 us.
 #pragma once
 
 #include "paged_attend.cuh"

@@ -482,8 +482,8 @@ int k3mla_rope_backward(const k3mla_view *dq_out, const k3mla_view *dq, int Hq, 
  *                     with an infinity or a NaN has s = m = NaN.
  * Data errors are reported in the data, as in k3mla_decode_step: a page number outside
  * [0, num_pages), a length outside [0, max_pages * page_size] or a position below 0 is never
- * dereferenced; append leaves such a token out, read and attend give NaN for it (attend for
- * every row of the sequence that sees it). */
+ * dereferenced; append leaves such a token out, read gives NaN for it.  Attend gives NaN to the rows
+ * that see such a page and to all rows of such a length; a row below position 0 sees nothing and is 0. */
 typedef enum { K3MLA_CACHE_BF16 = 1, K3MLA_CACHE_I4 = 2 } k3mla_cache_format;
 
 typedef struct k3mla_paged_cache {
@@ -527,7 +527,8 @@ int k3mla_paged_read(const k3mla_paged_cache *cache, const k3mla_view *k_out, co
  * a host copy to check it against, a wrong one costs time, not results.  A row that sees
  * no key (p < 0, an empty sequence) is 0.  A cu_seqlens that decreases makes every row NaN; rows of no sequence are not written.  Scores, maxima, sums and outputs are held in FP32; where a tensor core
  * takes query rows and weights in 16 bits they are given as a high and a low part: 22 bits together with 4-bit pages
- * (fp16 parts, scaled so that none overflows), 16 bits with bf16 pages (bf16 parts; the cached values themselves have 8).
+ * (fp16 parts, scaled so that none overflows; a weight times a value scale far below the largest of its 32 or 64 keys keeps 2^-38 of
+ * that one), 16 bits with bf16 pages (bf16 parts; the cached values themselves have 8).
  * A token that a row sees and that holds an infinity or a NaN acts as in a plain softmax, except that an output that an
  * infinite value reaches may be NaN; one that the row does not see changes nothing.  Results do not depend on the order in which parts of the work finish.
  * workspace: k3mla_paged_attend_workspace_size bytes (the same for every shape, 21.3 MB), 256-byte aligned, zero-filled
