@@ -34,7 +34,11 @@ __all__ = ["K3KDAError", "load_library", "library_path", "F32", "BF16", "L2_EPS"
            "CACHE_BF16", "CACHE_I4", "RopeTable", "PagedCache", "rope_table", "rope", "rope_backward",
            "paged_pool", "paged_append", "paged_read", "paged_attend", "paged_attend_workspace",
            "k3mla_rope_table", "k3mla_rope", "k3mla_rope_backward", "k3mla_paged_block_bytes",
-           "k3mla_paged_append", "k3mla_paged_read", "k3mla_paged_attend_workspace_size", "k3mla_paged_attend"]
+           "k3mla_paged_append", "k3mla_paged_read", "k3mla_paged_attend_workspace_size", "k3mla_paged_attend",
+           "k3lin_prefill_workspace_size", "k3lin_prefill", "k3lin_decode_step", "k3lin_backward_workspace_size", "k3lin_backward",
+           "lin_prefill_workspace", "lin_prefill", "lin_decode_step", "lin_backward_workspace", "lin_backward",
+           "k3blk_norm", "k3blk_norm_backward_workspace_size", "k3blk_norm_backward",
+           "block_norm", "block_norm_workspace", "block_norm_backward"]
 
 F32, BF16 = 0, 1
 CACHE_BF16, CACHE_I4 = 1, 2
@@ -135,6 +139,22 @@ def load_library(build_if_missing: bool = True):
         lib.k3mla_paged_attend_workspace_size.restype = Z
         lib.k3mla_paged_attend.argtypes = [C, V, I, I, P, P, I, I, R, F, V, P, I, P, Z, P]
         lib.k3mla_paged_attend.restype = I
+        L = ctypes.c_longlong
+        for name in ("k3lin_prefill_workspace_size", "k3lin_backward_workspace_size"):
+            getattr(lib, name).argtypes = [I] * 7
+            getattr(lib, name).restype = Z
+        lib.k3lin_prefill.argtypes = [P, P, P, I, P, I, P, P, P, I, P, P, I, I, I, I, I, I, F, P, I, P, P, Z, P]
+        lib.k3lin_prefill.restype = I
+        lib.k3lin_decode_step.argtypes = [P, P, P, I, P, I, P, P, P, I, I, I, I, I, I, F, P, I, P]
+        lib.k3lin_decode_step.restype = I
+        lib.k3lin_backward.argtypes = [P, P, P, I, P, I, P, P, P, I, I, I, I, I, I, F, P, P, P, P, P, P, P, P, Z, P]
+        lib.k3lin_backward.restype = I
+        lib.k3blk_norm.argtypes = [P, I, P, P, I, P, P, L, I, F, F, P, P, P]
+        lib.k3blk_norm.restype = I
+        lib.k3blk_norm_backward_workspace_size.argtypes = [L, I]
+        lib.k3blk_norm_backward_workspace_size.restype = Z
+        lib.k3blk_norm_backward.argtypes = [P, I, P, P, P, P, I, P, P, L, I, F, F, P, P, P, P, P, P, Z, P]
+        lib.k3blk_norm_backward.restype = I
         _lib = lib
         return lib
 
@@ -787,3 +807,264 @@ def paged_attend(cache, q, cu_seqlens=None, max_new=None, rope=None, scale=None,
     k3mla_paged_attend(cache, q, gate, out, workspace, cache.dqk ** -0.5 if scale is None else float(scale), cu_seqlens, None, max_new,
                        rope, stream)
     return out
+
+
+# ---- linear attention with one decay a head ---------------------------------
+
+def k3lin_prefill_workspace_size(N, T, Hk, H, dk, dv, in_dtype) -> int:
+    return int(load_library().k3lin_prefill_workspace_size(int(N), int(T), int(Hk), int(H), int(dk), int(dv), int(in_dtype)))
+
+
+def k3lin_backward_workspace_size(N, T, Hk, H, dk, dv, in_dtype) -> int:
+    return int(load_library().k3lin_backward_workspace_size(int(N), int(T), int(Hk), int(H), int(dk), int(dv), int(in_dtype)))
+
+
+def _of(t, what, shape, dtype):
+    """The address of a contiguous CUDA tensor of this shape and type, or of None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"k3lin: {what} must be a torch.Tensor or None")
+    if not t.is_cuda:
+        raise ValueError("k3lin: tensors must live on a CUDA device (no CPU path exists)")
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"k3lin: {what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _lin_sizes(q, k, v):
+    """(T, Hk, H, dk, dv) of q, k [T, Hk, dk] and v [T, H, dv]."""
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("k3lin: q, k and v must be [tokens, heads, channels]")
+    T, Hk, dk = q.shape
+    return T, Hk, v.shape[1], dk, v.shape[2]
+
+
+def _lin_decay(g, T, H):
+    """(address, whether it is one decay a head) of g [T, H] or [H]."""
+    fixed = g.dim() == 1
+    return _of(g, "g", (H,) if fixed else (T, H), torch.float32), 1 if fixed else 0
+
+
+def _lin_packing(cu_seqlens, cu_seqlens_host, T):
+    if cu_seqlens is None and cu_seqlens_host is None:
+        return 1, None, None
+    N = (cu_seqlens if cu_seqlens is not None else cu_seqlens_host).numel() - 1
+    if cu_seqlens_host is not None and cu_seqlens_host.numel() != N + 1:
+        raise ValueError("k3lin: cu_seqlens_host has another length")
+    return N, _of(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32), _host_i32(cu_seqlens_host, "cu_seqlens_host")
+
+
+def _lin_slots(state_idx, state_idx_host, N, what, *pools):
+    """(slots, addresses of the map and its copy); the pools' first size is the number of slots."""
+    slots = {p.shape[0] for p in pools if p is not None}
+    if len(slots) > 1:
+        raise ValueError(f"k3lin: {what} have different numbers of slots")
+    n = slots.pop() if slots else N
+    if state_idx is None and n != N:
+        raise ValueError(f"k3lin: {what} must hold {N} states, not {n}")
+    if state_idx_host is not None and state_idx_host.numel() != N:
+        raise ValueError("k3lin: state_idx_host has another length")
+    return n, _of(state_idx, "state_idx", (N,), torch.int32), _host_i32(state_idx_host, "state_idx_host")
+
+
+def k3lin_prefill(q, k, v, g, initial_state, cu_seqlens, scale, out, final_state, workspace, state_idx=None, state_idx_host=None,
+                  cu_seqlens_host=None, stream=None):
+    """Linear attention over packed sequences (see include/k3kda.h): q, k [T, Hk, dk], v [T, H, dv], g [T, H] or [H]."""
+    T, Hk, H, dk, dv = _lin_sizes(q, k, v)
+    dt = q.dtype
+    gp, fixed = _lin_decay(g, T, H)
+    N, cu, cuh = _lin_packing(cu_seqlens, cu_seqlens_host, T)
+    slots, idx, idxh = _lin_slots(state_idx, state_idx_host, N, "initial_state and final_state", initial_state, final_state)
+    f32 = torch.float32
+    st = (_lib or load_library()).k3lin_prefill(
+        _of(q, "q", q.shape, dt), _of(k, "k", q.shape, dt), _of(v, "v", (T, H, dv), dt), _dtype(q), gp, fixed,
+        _of(initial_state, "initial_state", (slots, H, dk, dv), f32), idx, idxh, slots, cu, cuh, N, T, Hk, H, dk, dv, float(scale),
+        _of(out, "out", (T, H, dv), out.dtype), _dtype(out), _of(final_state, "final_state", (slots, H, dk, dv), f32), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _raw_stream(stream, q))
+    if st:
+        _check("k3lin_prefill", st)
+
+
+def _lin_workspace(n, device, stream=None):
+    if n == 0:
+        raise K3KDAError("k3lin_workspace_size", -2)
+    with _on(stream):
+        w = torch.empty(n, dtype=torch.uint8, device=device)
+        w[:256].zero_()                                     # the status word; the rest is written before it is read
+    return w
+
+
+def _lin_type(dtype):
+    return {torch.bfloat16: BF16, torch.float32: F32}.get(dtype, dtype)
+
+
+def lin_prefill_workspace(N, T, Hk, H, dk, dv, dtype=torch.bfloat16, device="cuda"):
+    """A workspace for lin_prefill on N sequences of T tokens in all, for one call at a time."""
+    return _lin_workspace(k3lin_prefill_workspace_size(N, T, Hk, H, dk, dv, _lin_type(dtype)), device)
+
+
+def _lin_cu(cu_seqlens, device, stream):
+    """(device array, host copy or None) of cu_seqlens: one on the device is taken as it is, without a copy to the host."""
+    if cu_seqlens is None or cu_seqlens.is_cuda:
+        return cu_seqlens, None
+    host = cu_seqlens.to(torch.int32).contiguous()
+    with _on(stream):
+        return host.to(device), host
+
+
+def lin_prefill(q, k, v, g, initial_state=None, cu_seqlens=None, scale=None, out_dtype=None, return_final_state=True, state_idx=None,
+                workspace=None, stream=None):
+    """Linear attention with a decay a head over packed sequences: q, k [T, Hk, dk], v [T, H, dv], g (log decay) [T, H] or [H];
+    cu_seqlens int32 [N + 1] on the device (or the host).  Returns (out [T, H, dv], final_state [N, H, dk, dv] or None).  With
+    state_idx [N], initial_state is a pool of slots that is read and updated in place, and is what is returned for the state."""
+    T, Hk, H, dk, dv = _lin_sizes(q, k, v)
+    dev = q.device
+    cu, cuh = _lin_cu(cu_seqlens, dev, stream)
+    N = 1 if cu is None else cu.numel() - 1
+    out = _empty((T, H, dv), out_dtype or q.dtype, dev, stream)
+    if state_idx is not None and initial_state is None:
+        raise ValueError("k3lin: state_idx needs initial_state, the pool of states")
+    last = initial_state if state_idx is not None else _empty((N, H, dk, dv), torch.float32, dev, stream) if return_final_state else None
+    if workspace is None:
+        workspace = _lin_workspace(k3lin_prefill_workspace_size(N, T, Hk, H, dk, dv, _dtype(q)), dev, stream)
+    k3lin_prefill(q, k, v, g, initial_state, cu, dk ** -0.5 if scale is None else scale, out, last, workspace, state_idx, None, cuh, stream)
+    return out, last
+
+
+def k3lin_decode_step(q, k, v, g, state, scale, out, state_idx=None, state_idx_host=None, stream=None):
+    """One token of linear attention for N sequences (see include/k3kda.h); state is updated in place."""
+    N, Hk, H, dk, dv = _lin_sizes(q, k, v)
+    dt = q.dtype
+    gp, fixed = _lin_decay(g, N, H)
+    slots, idx, idxh = _lin_slots(state_idx, state_idx_host, N, "state", state)
+    st = (_lib or load_library()).k3lin_decode_step(
+        _of(q, "q", q.shape, dt), _of(k, "k", q.shape, dt), _of(v, "v", (N, H, dv), dt), _dtype(q), gp, fixed,
+        _of(state, "state", (slots, H, dk, dv), torch.float32), idx, idxh, slots, N, Hk, H, dk, dv, float(scale),
+        _of(out, "out", (N, H, dv), out.dtype), _dtype(out), _raw_stream(stream, q))
+    if st:
+        _check("k3lin_decode_step", st)
+
+
+def lin_decode_step(q, k, v, g, state, state_idx=None, scale=None, out_dtype=None, stream=None):
+    """One token for each of N sequences: q, k [N, Hk, dk], v [N, H, dv], g [N, H] or [H]; state [N, H, dk, dv] (with state_idx
+    a pool of slots) is updated in place.  Returns out [N, H, dv]."""
+    out = _empty(v.shape, out_dtype or q.dtype, q.device, stream)
+    k3lin_decode_step(q, k, v, g, state, q.shape[-1] ** -0.5 if scale is None else scale, out, state_idx, None, stream)
+    return out
+
+
+def k3lin_backward(q, k, v, g, dO, initial_state, dS_final, cu_seqlens, scale, dq, dk_out, dv_out, dg, dS0, workspace,
+                   cu_seqlens_host=None, stream=None):
+    """Gradients of k3lin_prefill (see include/k3kda.h); dg and dS0 may be None."""
+    T, Hk, H, dk, dv = _lin_sizes(q, k, v)
+    dt, f32 = q.dtype, torch.float32
+    gp, fixed = _lin_decay(g, T, H)
+    N, cu, cuh = _lin_packing(cu_seqlens, cu_seqlens_host, T)
+    states = (N, H, dk, dv)
+    st = (_lib or load_library()).k3lin_backward(
+        _of(q, "q", q.shape, dt), _of(k, "k", q.shape, dt), _of(v, "v", (T, H, dv), dt), _dtype(q), gp, fixed,
+        _of(initial_state, "initial_state", states, f32), cu, cuh, N, T, Hk, H, dk, dv, float(scale), _of(dO, "dO", (T, H, dv), dt),
+        _of(dS_final, "dS_final", states, f32), _of(dq, "dq", q.shape, dt), _of(dk_out, "dk_out", q.shape, dt),
+        _of(dv_out, "dv_out", (T, H, dv), dt), _of(dg, "dg", g.shape, f32), _of(dS0, "dS0", states, f32), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _raw_stream(stream, q))
+    if st:
+        _check("k3lin_backward", st)
+
+
+def lin_backward_workspace(N, T, Hk, H, dk, dv, dtype=torch.bfloat16, device="cuda"):
+    """A workspace for lin_backward on N sequences of T tokens in all, for one call at a time."""
+    return _lin_workspace(k3lin_backward_workspace_size(N, T, Hk, H, dk, dv, _lin_type(dtype)), device)
+
+
+def lin_backward(q, k, v, g, dO, initial_state=None, dS_final=None, cu_seqlens=None, scale=None, need_dg=True, workspace=None,
+                 stream=None):
+    """Gradients of lin_prefill for dO [T, H, dv] (q's type) and dS_final [N, H, dk, dv]: a dict of dq, dk, dv (q's type), dg (FP32, in
+    g's shape, or None) and dS0 (FP32)."""
+    T, Hk, H, dk, dv = _lin_sizes(q, k, v)
+    dev, dt = q.device, q.dtype
+    cu, cuh = _lin_cu(cu_seqlens, dev, stream)
+    N = 1 if cu is None else cu.numel() - 1
+    if workspace is None:
+        workspace = _lin_workspace(k3lin_backward_workspace_size(N, T, Hk, H, dk, dv, _dtype(q)), dev, stream)
+    d = {"dq": _empty(q.shape, dt, dev, stream), "dk": _empty(q.shape, dt, dev, stream), "dv": _empty(v.shape, dt, dev, stream),
+         "dg": _empty(g.shape, torch.float32, dev, stream) if need_dg else None, "dS0": _empty((N, H, dk, dv), torch.float32, dev, stream)}
+    k3lin_backward(q, k, v, g, dO, initial_state, dS_final, cu, dk ** -0.5 if scale is None else scale, d["dq"], d["dk"], d["dv"], d["dg"],
+                   d["dS0"], workspace, cuh, stream)
+    return d
+
+
+# ---- the norms around a block ------------------------------------------------
+
+_GATES = {"sigmoid": 0, "silu": 1}
+
+
+def _norm_rows(first, post_weight, pre_weight, **like):
+    """(rows, D) of `first` [..., D] and the addresses of what has its shape and type, and of the weights."""
+    if first.dim() < 1:
+        raise ValueError("k3blk: arrays must be [..., channels]")
+    D = first.shape[-1]
+    rows = first.numel() // D if D else 0
+    at = {name: _of(t, name, first.shape, first.dtype) for name, t in like.items()}
+    return rows, D, at, _of(post_weight, "post_weight", (D,), torch.float32), _of(pre_weight, "pre_weight", (D,), torch.float32)
+
+
+def k3blk_norm(x, residual, gate, gate_act, post_weight, pre_weight, alpha, eps, sum_out, out, stream=None):
+    """The norms around a block with its gate and residual (see include/k3kda.h); gate_act "sigmoid" or "silu"."""
+    rows, D, at, post, pre = _norm_rows(x, post_weight, pre_weight, x=x, residual=residual, gate=gate, sum_out=sum_out, out=out)
+    st = (_lib or load_library()).k3blk_norm(at["x"], _dtype(x), at["residual"], at["gate"], _named(_GATES, gate_act, "gate_act"), post, pre,
+                                             rows, D, float(alpha), float(eps), at["sum_out"], at["out"], _raw_stream(stream, x))
+    if st:
+        _check("k3blk_norm", st)
+
+
+def block_norm(x, residual=None, gate=None, gate_act="sigmoid", post_weight=None, pre_weight=None, alpha=1.0, eps=1e-6, stream=None):
+    """s = residual + alpha norm(x; post_weight) act(gate) and, with pre_weight, y = norm(s; pre_weight), each [..., D] as x; norms are
+    root-mean-square norms over the last dimension, what is None is left out.  Returns s, or (s, y)."""
+    s = _empty(x.shape, x.dtype, x.device, stream)
+    y = None if pre_weight is None else _empty(x.shape, x.dtype, x.device, stream)
+    k3blk_norm(x, residual, gate, gate_act, post_weight, pre_weight, alpha, eps, s, y, stream)
+    return s if y is None else (s, y)
+
+
+def k3blk_norm_backward_workspace_size(rows, D) -> int:
+    return int(load_library().k3blk_norm_backward_workspace_size(int(rows), int(D)))
+
+
+def block_norm_workspace(rows, D, device="cuda"):
+    """A workspace for block_norm_backward, for one call at a time."""
+    n = k3blk_norm_backward_workspace_size(rows, D)
+    if n == 0:
+        raise K3KDAError("k3blk_norm_backward_workspace_size", -2)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def k3blk_norm_backward(x, ds, dy, sum, gate, gate_act, post_weight, pre_weight, alpha, eps, dx, dresidual, dgate, dpost_weight, dpre_weight,
+                        workspace, stream=None):
+    """The gradients of k3blk_norm (see include/k3kda.h)."""
+    rows, D, at, post, pre = _norm_rows(ds, post_weight, pre_weight, x=x, ds=ds, dy=dy, sum=sum, gate=gate, dx=dx, dresidual=dresidual, dgate=dgate)
+    st = (_lib or load_library()).k3blk_norm_backward(
+        at["x"], _dtype(ds), at["ds"], at["dy"], at["sum"], at["gate"], _named(_GATES, gate_act, "gate_act"), post, pre, rows, D, float(alpha),
+        float(eps), at["dx"], at["dresidual"], at["dgate"], _of(dpost_weight, "dpost_weight", (D,), torch.float32),
+        _of(dpre_weight, "dpre_weight", (D,), torch.float32), _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _raw_stream(stream, ds))
+    if st:
+        _check("k3blk_norm_backward", st)
+
+
+def block_norm_backward(x, ds, dy=None, sum=None, gate=None, gate_act="sigmoid", post_weight=None, pre_weight=None, alpha=1.0, eps=1e-6,
+                        residual=True, workspace=None, stream=None):
+    """Gradients of block_norm from ds = dL/ds (without y's share) and, with pre_weight, dy = dL/dy and the forward's s (`sum`): a dict of dx,
+    dresidual (None unless `residual`), dgate, and in FP32 dpost and dpre (None without what they belong to)."""
+    dev, D = ds.device, ds.shape[-1]
+    weights = post_weight is not None or pre_weight is not None
+    if weights and workspace is None:
+        with _on(stream):
+            workspace = block_norm_workspace(ds.numel() // D if D else 0, D, dev)
+    d = {"dx": _empty(ds.shape, ds.dtype, dev, stream), "dresidual": _empty(ds.shape, ds.dtype, dev, stream) if residual else None,
+         "dgate": None if gate is None else _empty(ds.shape, ds.dtype, dev, stream),
+         "dpost": None if post_weight is None else _empty((D,), torch.float32, dev, stream),
+         "dpre": None if pre_weight is None else _empty((D,), torch.float32, dev, stream)}
+    k3blk_norm_backward(x, ds, dy, sum, gate, gate_act, post_weight, pre_weight, alpha, eps, d["dx"], d["dresidual"], d["dgate"], d["dpost"],
+                        d["dpre"], workspace if weights else None, stream)
+    return d

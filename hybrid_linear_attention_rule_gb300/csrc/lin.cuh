@@ -1,0 +1,112 @@
+// lin.cuh -- linear attention with one decay a head: what its kernels share.
+//
+// Prefill and the three large gradients are one operator on different arrays, a "job".  For every sequence and value head,
+// with S [a, b] the state, x, y rows of a channels and z rows of b channels,
+//     forward in time    S_t = e^{g_t} S_{t-1} + y_t z_t^T          out_t = x_t S_t
+//     backward in time   R_t = y_t z_t^T + e^{g_{t+1}} R_{t+1}      out_t = x_t R_t
+// and, with state K^T V and its gradient R = sum_u e^{G_u - G_t} scale q_u do_u^T:
+//     o  = job(x = q,  y = k, z = v)            dv = job(x = k, y = q,  z = do) backward in time
+//     dq = job(x = do, y = v, z = k)            dk = job(x = v, y = do, z = q)  backward in time
+// In chunks, G the sum of g from the chunk's first token on (that token's own included), G_end the whole chunk's:
+//     out_i = c_i x_i S + sum_j D_ij (x_i . y_j) z_j,   S' = e^{G_end} S + sum_j w_j y_j z_j^T
+// forward: D_ij = e^{G_i - G_j} for j <= i, c_i = e^{G_i}, w_j = e^{G_end - G_j}; backward in time: D_ij = e^{G_j - G_i} for
+// j >= i, c_i = e^{G_end - G_i}, w_j = e^{G_j}.  No exponent is positive while g <= 0.
+#pragma once
+
+#include "common.cuh"
+
+namespace k3kda {
+namespace lin {
+
+// Sums of g are kept as 64-bit integers in units of 2^-32 of a power of two: differences of any two are exact, whatever lies
+// between, and the order of the sum does not matter.  One decay counts as at most 4096 powers of two (e^g = 0 in FP32 long
+// before: minus infinity is a reset), so 64 of them fit many times.
+__device__ __forceinline__ long long decay_units(float g) {
+    constexpr float kLog2e = 1.442695040888963f, kRest = 1.925963033500e-8f;       // log2(e) and what its FP32 value leaves
+    const float p = g * kLog2e;
+    if (!(fabsf(p) < 4096.f)) return p != p ? 0 : p < 0.f ? -(4096LL << 32) : 4096LL << 32;
+    const float e = fmaf(g, kLog2e, -p) + g * kRest;
+    return __float2ll_rn(p * 4294967296.f) + __float2ll_rn(e * 4294967296.f);
+}
+__device__ __forceinline__ float exp2_units(long long v) { return exp2f((float)v * 2.3283064365386963e-10f); }
+// The sum as two floats whose pairwise differences keep FP32 accuracy.
+__device__ __forceinline__ float2 two_floats(long long v) {
+    const float hi = (float)v;
+    return make_float2(hi * 2.3283064365386963e-10f, (float)(v - (long long)hi) * 2.3283064365386963e-10f);
+}
+
+// Tokens between the anchors at which the gradient of the decays starts its sums anew (see lin_grad.cu).
+constexpr int kAnchor = 512;
+// Slots of the anchors of sequence n from `first` on: slot + floor(tokens before its end / kAnchor) is never shared, as
+// ceil(len / kAnchor) <= floor((start + len) / kAnchor) - floor(start / kAnchor) + 1.
+__host__ __device__ inline long long anchor_slot(int start, int n) { return start / kAnchor + (long long)n; }
+inline size_t anchor_slots(int N, int T) { return (size_t)(T / kAnchor) + N + 2; }
+
+struct Rows {              // [T, H / share, d]
+    const void *p;
+    int share;             // value heads that share one head of it
+};
+
+struct Job {
+    Rows x, y, z;
+    int a, b;              // channels of x and y, of z
+    int reverse;
+    float sp, sc, sw;      // factors on D, on c and on w
+    const float *first;    // [slots, H, ...] or null: element (a, b) of a state lies at a * first_sa + b * first_sb
+    float *last;           // likewise, or null
+    int sa, sb;
+    void *out;             // [T, H, b]
+    int out_bf16;
+    int exact;             // operands of the tensor cores in three parts instead of two
+    // for the gradient of the decays: dots[t, h] = sum_c r[t, c] (out[t, c] without the term j = i), and the states at the anchors
+    Rows r;
+    float *dots;           // [slices][T, H], or null
+    float *anchors;        // [anchor_slots, H, a, b], or null; the state entering the anchor (forward) or leaving it (backward)
+    int last_anchor;       // forward: the last state is an anchor too
+};
+
+struct Call {
+    Job job[3];
+    int jobs;
+    int bf16;              // type of x, y, z, r
+    const float *g;        // [T, H], or [H] when fixed
+    int fixed;
+    const int32_t *cu;
+    int N, T, H;
+    const int32_t *slot;   // of first and last, or null
+    int num_slots;
+    unsigned *status;
+    void *pieces;          // the tensor-core path's part of the workspace
+};
+
+// The slices of the output's channels that one CTA of the CUDA-core path takes; dots has one row of [T, H] for each.
+constexpr int kSlice = 32;
+inline int slices(int b) { return (b + kSlice - 1) / kSlice; }
+
+cudaError_t launch_scan_f32(const Call &c, cudaStream_t s);
+
+}  // namespace lin
+
+cudaError_t launch_lin_decode(const void *q, const void *k, const void *v, int bf16, const float *g, int fixed, float *state,
+                              const int32_t *slot, int num_slots, int N, int Hk, int H, int dk, int dv, float scale, void *out,
+                              int out_bf16, cudaStream_t s);
+size_t lin_workspace(int N, int T, int Hk, int H, int dk, int dv, int bf16, int backward);
+
+struct LinArgs {
+    const void *q, *k, *v;
+    int bf16;
+    const float *g;
+    int fixed;
+    const float *first;
+    const int32_t *slot;
+    int num_slots;
+    const int32_t *cu;
+    int N, T, Hk, H, dk, dv;
+    float scale;
+    void *ws;
+};
+cudaError_t launch_lin_prefill(const LinArgs &a, void *out, int out_bf16, float *last, cudaStream_t s);
+cudaError_t launch_lin_backward(const LinArgs &a, const void *dO, const float *dlast, void *dq, void *dk, void *dv, float *dg,
+                                float *dfirst, cudaStream_t s);
+
+}  // namespace k3kda

@@ -1,0 +1,329 @@
+// lin_grad.cu -- linear attention's prefill and gradients as jobs (lin.cuh), and the gradient of the decays.
+//
+// The gradient of g_t is what passes over it: f(t) = sum over s < t <= u of e^{G_u - G_s} (q_u . k_s) (do_u . v_s) scale, with
+// the first state as a token before the first and the last state's gradient as one behind the last.  f(t) - f(t + 1) =
+// r1_t - r2_t, r1 the pairs that end at t (q_t . dq_t without s = t), r2 those that begin there (v_t . dv_t without u = t): the
+// jobs write both.  Summed from the sequence's end alone, the rounding of every later token would stay in f(t); so at anchors,
+// every 512 tokens, f is worked out directly as <S, R> of the two states that the jobs left there, and the sums, in 64
+// bits, start anew.  Leaving the pairs s = t = u out keeps them from cancelling where the decay is strong.
+#include "lin.cuh"
+
+namespace k3kda {
+namespace lin {
+namespace {
+
+// f at the anchors: <S, R> with S [dv, dk] and R [dk, dv].  A CTA for each (anchor, head); tiles of 32 x 32 turned in shared memory.
+struct AnchorArgs {
+    const float *S, *R, *dlast;       // dlast [N, H, dk, dv] or null
+    double *f;                        // [slots, H]
+    const int32_t *cu;
+    int N, T, H, dk, dv;
+};
+
+__global__ void __launch_bounds__(256) anchor_kernel(const __grid_constant__ AnchorArgs A) {
+    __shared__ float turned[32][33];
+    __shared__ double part[8];
+    const int h = blockIdx.y, tx = threadIdx.x % 32, ty = threadIdx.x / 32;
+    for (int n = blockIdx.x; n < A.N; n += gridDim.x) {
+        int begin, end;
+        seq_bounds(A.cu, n, A.T, begin, end);
+        const int count = max(1, (end - begin + kAnchor - 1) / kAnchor);
+        for (int k = blockIdx.z; k < count; k += gridDim.z) {
+            const size_t at = (size_t)(anchor_slot(begin, n) + k) * A.H + h;
+            const bool last = k == count - 1;
+            const float *R = last ? (A.dlast ? A.dlast + ((size_t)n * A.H + h) * A.dk * A.dv : nullptr) : A.R + at * A.dk * A.dv;
+            double sum = 0.0;
+            if (R) {
+                const float *S = A.S + at * A.dk * A.dv;
+                for (int i = 0; i < A.dk; i += 32)
+                    for (int j = 0; j < A.dv; j += 32) {
+                        __syncthreads();
+                        for (int u = ty; u < 32; u += 8) turned[u][tx] = j + u < A.dv && i + tx < A.dk ? S[(size_t)(j + u) * A.dk + i + tx] : 0.f;
+                        __syncthreads();
+                        float acc = 0.f;
+                        for (int u = ty; u < 32; u += 8)
+                            if (i + u < A.dk && j + tx < A.dv) acc = fmaf(turned[tx][u], R[(size_t)(i + u) * A.dv + j + tx], acc);
+                        sum += acc;
+                    }
+                for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (tx == 0) part[ty] = sum;
+            }
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                sum = 0.0;
+                if (R)
+                    for (int u = 0; u < 8; ++u) sum += part[u];
+                A.f[at] = sum;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// dg: a CTA sums one stretch between anchors for 32 heads, a head a lane, 16 runs of tokens a warp each.
+struct SumArgs {
+    const float *r1, *r2;             // [slices][T, H]
+    int n1, n2;                       // slices
+    const double *f;
+    float *dg;                        // [T, H]
+    const int32_t *cu;
+    int N, T, H;
+};
+
+__global__ void __launch_bounds__(512) sum_kernel(const __grid_constant__ SumArgs A) {
+    __shared__ double part[16][33];
+    constexpr int RUN = kAnchor / 16;
+    const int lane = threadIdx.x % 32, ty = threadIdx.x / 32, h = blockIdx.y * 32 + lane;
+    const size_t TH = (size_t)A.T * A.H;
+    for (int n = blockIdx.x; n < A.N; n += gridDim.x) {
+        int begin, end;
+        seq_bounds(A.cu, n, A.T, begin, end);
+        const int count = (end - begin + kAnchor - 1) / kAnchor;
+        for (int k = blockIdx.z; k < count; k += gridDim.z) {
+            const int t0 = begin + k * kAnchor + ty * RUN, t1 = min(t0 + RUN, end);
+            float x[RUN];
+            double sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) {
+                x[i] = 0.f;
+                if (h < A.H && t0 + i < t1) {
+                    const size_t at = (size_t)(t0 + i) * A.H + h;
+                    float p = 0.f, q = 0.f;
+                    for (int u = 0; u < A.n1; ++u) p += A.r1[u * TH + at];
+                    for (int u = 0; u < A.n2; ++u) q += A.r2[u * TH + at];
+                    x[i] = p - q;
+                }
+                sum += x[i];
+            }
+            part[ty][lane] = sum;
+            __syncthreads();
+            if (h < A.H) {
+                double f = A.f[(size_t)(anchor_slot(begin, n) + k) * A.H + h];
+                for (int u = 15; u > ty; --u) f += part[u][lane];
+#pragma unroll
+                for (int i = RUN - 1; i >= 0; --i) {
+                    f += x[i];
+                    if (t0 + i < t1) A.dg[(size_t)(t0 + i) * A.H + h] = (float)f;
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// One decay a head for all tokens: its gradient is the sum over them, in 64 bits and in a fixed order.  A CTA a head.
+__global__ void __launch_bounds__(512) fixed_kernel(const float *dg, float *out, const int32_t *cu, int N, int T, int H) {
+    __shared__ double part[16];
+    const int h = blockIdx.x;
+    double sum = 0.0;
+    for (int n = 0; n < N; ++n) {
+        int begin, end;
+        seq_bounds(cu, n, T, begin, end);
+        for (int t = begin + (int)threadIdx.x; t < end; t += 512) sum += dg[(size_t)t * H + h];
+    }
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        sum = 0.0;
+        for (int u = 0; u < 16; ++u) sum += part[u];
+        out[h] = (float)sum;
+    }
+}
+
+// Gradients of shared heads: out[t, hk, c] = sum over its group of part[t, h, c], rounded once.  Tokens of no sequence are left alone.
+__global__ void __launch_bounds__(256) group_kernel(const float *p1, const float *p2, void *o1, void *o2, int bf16, const int32_t *cu, int N, int T,
+                                                    int Hk, int group, int d) {
+    const int n = blockIdx.z;
+    int begin, end;
+    seq_bounds(cu, n, T, begin, end);
+    const float *part = blockIdx.y ? p2 : p1;
+    void *out = blockIdx.y ? o2 : o1;
+    const size_t row = (size_t)Hk * (d / 4), i0 = begin * row, i1 = end * row;
+    for (size_t i = i0 + blockIdx.x * 256 + threadIdx.x; i < i1; i += (size_t)gridDim.x * 256) {
+        const size_t head = i / (d / 4), c = i % (d / 4) * 4;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int u = 0; u < group; ++u) {
+            const float4 v = *reinterpret_cast<const float4 *>(part + (head * group + u) * d + c);
+            s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+        }
+        if (bf16) {
+            __nv_bfloat162 r[2] = {__floats2bfloat162_rn(s.x, s.y), __floats2bfloat162_rn(s.z, s.w)};
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(out) + head * d + c) = *reinterpret_cast<uint2 *>(r);
+        } else {
+            *reinterpret_cast<float4 *>(static_cast<float *>(out) + head * d + c) = s;
+        }
+    }
+}
+
+size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
+
+// The workspace: the status word, what the tensor-core path keeps, and the gradient's parts.
+struct Space {
+    size_t pieces, r1, r2, S, R, f, dg, pq, pk, total;
+    Space(int N, int T, int Hk, int H, int dk, int dv, int bf16, bool backward) {
+        size_t at = 256;
+        auto take = [&](size_t bytes) {
+            const size_t was = at;
+            at += round256(bytes);
+            return was;
+        };
+        const size_t TH = (size_t)T * H, slots = anchor_slots(N, T);
+        pieces = take(0);
+        (void)bf16;
+        r1 = r2 = S = R = f = dg = pq = pk = at;
+        if (backward) {
+            r1 = take(TH * slices(dk) * 4);
+            r2 = take(TH * slices(dv) * 4);
+            S = take(slots * H * dk * dv * 4);
+            R = take(slots * H * dk * dv * 4);
+            f = take(slots * H * 8);
+            dg = take(TH * 4);
+            if (H > Hk) {
+                pq = take(TH * dk * 4);
+                pk = take(TH * dk * 4);
+            }
+        }
+        total = at;
+    }
+};
+
+Call call_of(const LinArgs &a, const Space &w) {
+    Call c{};
+    c.bf16 = a.bf16;
+    c.g = a.g;
+    c.fixed = a.fixed;
+    c.cu = a.cu;
+    c.N = a.N;
+    c.T = a.T;
+    c.H = a.H;
+    c.slot = a.slot;
+    c.num_slots = a.num_slots;
+    c.status = static_cast<unsigned *>(a.ws);
+    c.pieces = static_cast<char *>(a.ws) + w.pieces;
+    return c;
+}
+
+cudaError_t launch_scan(const Call &c, cudaStream_t s) { return launch_scan_f32(c, s); }
+
+}  // namespace
+}  // namespace lin
+
+using namespace lin;
+
+size_t lin_workspace(int N, int T, int Hk, int H, int dk, int dv, int bf16, int backward) {
+    return Space(N, T, Hk, H, dk, dv, bf16, backward != 0).total;
+}
+
+cudaError_t launch_lin_prefill(const LinArgs &a, void *out, int out_bf16, float *last, cudaStream_t s) {
+    const Space w(a.N, a.T, a.Hk, a.H, a.dk, a.dv, a.bf16, false);
+    const int group = a.H / a.Hk;
+    Call c = call_of(a, w);
+    c.jobs = 1;
+    Job &j = c.job[0];
+    j.x = {a.q, group};
+    j.y = {a.k, group};
+    j.z = {a.v, 1};
+    j.a = a.dk;
+    j.b = a.dv;
+    j.sp = j.sc = a.scale;
+    j.sw = 1.f;
+    j.first = a.first;
+    j.last = last;
+    j.sa = a.dv;
+    j.sb = 1;
+    j.out = out;
+    j.out_bf16 = out_bf16;
+    j.exact = !out_bf16;
+    return launch_scan(c, s);
+}
+
+cudaError_t launch_lin_backward(const LinArgs &a, const void *dO, const float *dlast, void *dq, void *dk, void *dv, float *dg,
+                                float *dfirst, cudaStream_t s) {
+    const Space w(a.N, a.T, a.Hk, a.H, a.dk, a.dv, a.bf16, true);
+    const int group = a.H / a.Hk;
+    char *ws = static_cast<char *>(a.ws);
+    auto part = [&](size_t at) { return reinterpret_cast<float *>(ws + at); };
+    Call c = call_of(a, w);
+    c.jobs = 3;
+    Job &jq = c.job[0], &jv = c.job[1], &jk = c.job[2];
+    jq.x = {dO, 1};
+    jq.y = {a.v, 1};
+    jq.z = {a.k, group};
+    jq.a = a.dv;
+    jq.b = a.dk;
+    jq.sp = jq.sc = a.scale;
+    jq.sw = 1.f;
+    jq.first = a.first;
+    jq.sa = 1;
+    jq.sb = a.dv;
+    jv.x = {a.k, group};
+    jv.y = {a.q, group};
+    jv.z = {dO, 1};
+    jv.a = a.dk;
+    jv.b = a.dv;
+    jv.reverse = 1;
+    jv.sp = jv.sw = a.scale;
+    jv.sc = 1.f;
+    jv.first = dlast;
+    jv.last = dfirst;
+    jv.sa = a.dv;
+    jv.sb = 1;
+    jk.x = {a.v, 1};
+    jk.y = {dO, 1};
+    jk.z = {a.q, group};
+    jk.a = a.dv;
+    jk.b = a.dk;
+    jk.reverse = 1;
+    jk.sp = jk.sw = a.scale;
+    jk.sc = 1.f;
+    jk.first = dlast;
+    jk.sa = 1;
+    jk.sb = a.dv;
+    // gradients of shared heads are summed in FP32 first
+    jq.out = group > 1 ? part(w.pq) : dq;
+    jk.out = group > 1 ? part(w.pk) : dk;
+    jv.out = dv;
+    jq.out_bf16 = jk.out_bf16 = group > 1 ? 0 : a.bf16;
+    jv.out_bf16 = a.bf16;
+    if (dg) {
+        jq.r = {a.q, group};
+        jq.dots = part(w.r1);
+        jq.anchors = part(w.S);
+        jq.last_anchor = dlast != nullptr;
+        jq.exact = 1;
+        jv.r = {a.v, 1};
+        jv.dots = part(w.r2);
+        jv.anchors = part(w.R);
+        jv.exact = 1;
+    }
+    if (cudaError_t e = launch_scan(c, s)) return e;
+    const unsigned seqs = (unsigned)(a.N < 1024 ? a.N : 1024);
+    if (dg) {
+        const unsigned deep = (unsigned)(a.T / kAnchor / seqs + 1 < 256 ? a.T / kAnchor / seqs + 1 : 256);
+        double *f = reinterpret_cast<double *>(ws + w.f);
+        const AnchorArgs g{part(w.S), part(w.R), dlast, f, a.cu, a.N, a.T, a.H, a.dk, a.dv};
+        anchor_kernel<<<dim3(seqs, a.H, deep), 256, 0, s>>>(g);
+        count_launch();
+        float *to = a.fixed ? part(w.dg) : dg;
+        const SumArgs u{part(w.r1), part(w.r2), slices(a.dk), slices(a.dv), f, to, a.cu, a.N, a.T, a.H};
+        sum_kernel<<<dim3(seqs, (a.H + 31) / 32, deep), 512, 0, s>>>(u);
+        count_launch();
+        if (a.fixed) {
+            fixed_kernel<<<a.H, 512, 0, s>>>(to, dg, a.cu, a.N, a.T, a.H);
+            count_launch();
+        }
+    }
+    if (group > 1) {
+        const size_t rows = (size_t)a.T * a.Hk * (a.dk / 4) / a.N / 256 + 1;
+        for (int n = 0; n < a.N; n += 65535) {
+            const int here = a.N - n < 65535 ? a.N - n : 65535;
+            group_kernel<<<dim3((unsigned)(rows < 2048 ? rows : 2048), 2, here), 256, 0, s>>>(part(w.pq), part(w.pk), dq, dk, a.bf16,
+                                                                                            a.cu ? a.cu + n : nullptr, here, a.T, a.Hk, group, a.dk);
+            count_launch();
+        }
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace k3kda

@@ -547,6 +547,76 @@ int k3mla_paged_attend(const k3mla_paged_cache *cache, const k3mla_view *q, int 
                        const k3mla_rope_args *rope, float scale, const k3mla_view *gate, void *out, int out_dtype,
                        void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- Linear attention with one decay a head ---------------------------------------------------
+ * The recurrence without the delta rule's erase and with a scalar decay, for layers that stand where the
+ * KDA mixer does (retention and scalar-gated linear attention).  Per sequence and value head h, S in
+ * R^{dk x dv} in FP32, key head h / (H / Hk):
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,      o_t = scale S_t^T q_t
+ *   q, k   [T, Hk, dk], v, out [T, H, dv]   in_dtype (out: out_dtype); H a multiple of Hk
+ *   g      [T, H] FP32, or with g_per_head nonzero [H], the same decay for all tokens.  Any g <= 0, minus infinity
+ *          (e^g = 0: the state starts anew) among them; above 0 the state grows, as far as FP32 holds it
+ *   dk, dv multiples of 16 in 16..128 (UNSUPPORTED otherwise)
+ *   cu_seqlens [N+1] int32 device (NULL only when N == 1: one sequence of T tokens), cu_seqlens_host an
+ *          optional host copy, checked.  A device array is never trusted with an address: its entries
+ *          are clamped to 0..T.  Tokens of no sequence (behind cu_seqlens[N]) are neither read nor written.
+ *   states FP32; state_idx [N] int32 device or NULL: sequence n's state is slot state_idx[n] of a pool of
+ *          num_slots (n itself without it).  An entry outside the pool is never dereferenced: that sequence
+ *          starts from zero and writes no state (decode: its output is zero).  state_idx_host, an optional
+ *          host copy, is checked for range and repetition (repeated entries race).
+ * A value (q, k, v, a state) that is infinite or NaN reaches only what the recurrence lets it reach, where it
+ * may be NaN instead of infinite; rows before it and other sequences are as without it.
+ * BF16 inputs run on the tensor cores in chunks of 64 tokens: every operand that is not itself an input (decayed scores, decayed
+ * keys, the state) is taken as a sum of two BF16 numbers (17 bits or more; the keys that go into the state, and
+ * everything for outputs in FP32 and for the gradient of g, as three: 24 bits).  FP32 inputs run in FP32 on the CUDA cores.  Results do not change from run to run.
+ *
+ * k3lin_prefill -- packed sequences from initial_state (NULL: zero) on; final_state (or NULL) may be
+ * initial_state.  workspace: k3lin_prefill_workspace_size bytes, 256-byte aligned, its first 256 bytes zero before the first use,
+ * owned by one call at a time (calls of any shape may follow one another); its first word is the status word of
+ * k3kda_workspace_status.
+ * k3lin_decode_step -- one token for each of N sequences, the state (required) updated in place.  One launch.
+ * k3lin_backward -- gradients for dO [T, H, dv] (in_dtype) and dS_final [N, H, dk, dv] (FP32, or NULL: zero):
+ * dq, dk_out [T, Hk, dk], dv_out [T, H, dv] in in_dtype, those of shared heads summed in FP32 before their one rounding; dg (or NULL)
+ * FP32 in g's shape; dS0 (or NULL) [N, H, dk, dv] FP32.  q, k, v, g, initial_state are the forward's.
+ * Errors: INVALID_ARG, UNSUPPORTED (also H > 65535, N H > 2^28, num_slots H > 2^31 - 1), ALIGNMENT (16 bytes; g, dg, cu_seqlens,
+ * state_idx: 4), WORKSPACE, CUDA. */
+size_t k3lin_prefill_workspace_size(int N, int T, int Hk, int H, int dk, int dv, int in_dtype);
+int k3lin_prefill(const void *q, const void *k, const void *v, int in_dtype, const float *g, int g_per_head,
+                  const float *initial_state, const int32_t *state_idx, const int32_t *state_idx_host, int num_slots,
+                  const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int N, int T, int Hk, int H, int dk, int dv,
+                  float scale, void *out, int out_dtype, float *final_state, void *workspace, size_t workspace_bytes,
+                  void *stream);
+int k3lin_decode_step(const void *q, const void *k, const void *v, int in_dtype, const float *g, int g_per_head, float *state,
+                      const int32_t *state_idx, const int32_t *state_idx_host, int num_slots, int N, int Hk, int H, int dk,
+                      int dv, float scale, void *out, int out_dtype, void *stream);
+size_t k3lin_backward_workspace_size(int N, int T, int Hk, int H, int dk, int dv, int in_dtype);
+int k3lin_backward(const void *q, const void *k, const void *v, int in_dtype, const float *g, int g_per_head,
+                   const float *initial_state, const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int N, int T, int Hk,
+                   int H, int dk, int dv, float scale, const void *dO, const float *dS_final, void *dq, void *dk_out,
+                   void *dv_out, float *dg, float *dS0, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- The norms around a block ------------------------------------------------------------------
+ * What stands between one block (a mixer, an MLP) and the next, in one pass over rows of D channels:
+ *     u = x rsqrt(mean x^2 + eps) post_weight     (u = x when post_weight is NULL)
+ *     s = residual + alpha u act(gate)            (residual NULL: 0; gate NULL: act = 1)
+ *     y = s rsqrt(mean s^2 + eps) pre_weight      (only with pre_weight)
+ * x, residual, gate, s (sum_out, may be NULL with pre_weight), y (out, given with pre_weight) [rows, D] of type dtype, weights [D] FP32, D in 1..16384.
+ * A mixer's heads are normed one by one as rows [T H, dv].  FP32 inside, each output rounded once (y comes from s before its rounding).
+ * k3blk_norm_backward: from ds = dL/ds without y's share and dy = dL/dy (with pre_weight), and the forward's x (with post_weight or
+ * gate), sum (with pre_weight: s as it was stored), gate: dx, dresidual (or NULL; the whole gradient of s), dgate (with gate) and, in FP32, dpost_weight and
+ * dpre_weight (given with their weights), summed over the rows in an order that does not change from run to run.
+ * workspace: k3blk_norm_backward_workspace_size bytes, 256-byte aligned, scratch; needed with a weight's gradient only.
+ * An output may be the input of its shape that it replaces (the same address), else they may not overlap.  Squares are summed in FP32.
+ * Errors: INVALID_ARG, UNSUPPORTED (D, rows above 2^31 - 1), ALIGNMENT (to the element; arrays of 16-byte alignment and a D of whole 16-byte pieces
+ * move in 16-byte pieces), WORKSPACE, CUDA.  rows = 0 launches nothing (the backward writes zero weights' gradients). */
+typedef enum { K3BLK_GATE_SIGMOID = 0, K3BLK_GATE_SILU = 1 } k3blk_gate_act;
+int k3blk_norm(const void *x, int dtype, const void *residual, const void *gate, int gate_act, const float *post_weight,
+               const float *pre_weight, long long rows, int D, float alpha, float eps, void *sum_out, void *out, void *stream);
+size_t k3blk_norm_backward_workspace_size(long long rows, int D);
+int k3blk_norm_backward(const void *x, int dtype, const void *ds, const void *dy, const void *sum, const void *gate, int gate_act,
+                        const float *post_weight, const float *pre_weight, long long rows, int D, float alpha, float eps, void *dx,
+                        void *dresidual, void *dgate, float *dpost_weight, float *dpre_weight, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
