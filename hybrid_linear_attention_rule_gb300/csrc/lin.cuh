@@ -84,6 +84,9 @@ constexpr int kSlice = 32;
 inline int slices(int b) { return (b + kSlice - 1) / kSlice; }
 
 cudaError_t launch_scan_f32(const Call &c, cudaStream_t s);
+// The tensor-core path (lin_tc.cu): BF16, T > 0; dots has one row.
+size_t tc_workspace();
+cudaError_t launch_scan_tc(const Call &c, cudaStream_t s);
 
 }  // namespace lin
 

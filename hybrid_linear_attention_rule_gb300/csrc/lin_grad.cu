@@ -169,8 +169,7 @@ struct Space {
             return was;
         };
         const size_t TH = (size_t)T * H, slots = anchor_slots(N, T);
-        pieces = take(0);
-        (void)bf16;
+        pieces = take(bf16 ? tc_workspace() : 0);
         r1 = r2 = S = R = f = dg = pq = pk = at;
         if (backward) {
             r1 = take(TH * slices(dk) * 4);
@@ -204,7 +203,8 @@ Call call_of(const LinArgs &a, const Space &w) {
     return c;
 }
 
-cudaError_t launch_scan(const Call &c, cudaStream_t s) { return launch_scan_f32(c, s); }
+bool on_tensor_cores(const Call &c) { return c.bf16 && c.T > 0; }
+cudaError_t launch_scan(const Call &c, cudaStream_t s) { return on_tensor_cores(c) ? launch_scan_tc(c, s) : launch_scan_f32(c, s); }
 
 }  // namespace
 }  // namespace lin
@@ -306,7 +306,7 @@ cudaError_t launch_lin_backward(const LinArgs &a, const void *dO, const float *d
         anchor_kernel<<<dim3(seqs, a.H, deep), 256, 0, s>>>(g);
         count_launch();
         float *to = a.fixed ? part(w.dg) : dg;
-        const SumArgs u{part(w.r1), part(w.r2), slices(a.dk), slices(a.dv), f, to, a.cu, a.N, a.T, a.H};
+        const SumArgs u{part(w.r1), part(w.r2), on_tensor_cores(c) ? 1 : slices(a.dk), on_tensor_cores(c) ? 1 : slices(a.dv), f, to, a.cu, a.N, a.T, a.H};
         sum_kernel<<<dim3(seqs, (a.H + 31) / 32, deep), 512, 0, s>>>(u);
         count_launch();
         if (a.fixed) {

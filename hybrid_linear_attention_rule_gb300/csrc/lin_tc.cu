@@ -1,0 +1,841 @@
+// lin_tc.cu -- linear attention's jobs (lin.cuh) on the tensor cores: BF16 inputs, chunks of 64 tokens.
+//
+// Widths are padded to 128 by the copies' zero fill.  Everything is kept turned, channels of z in the 128 rows of an accumulator:
+//     PT  = Y X^T                      scores, token j a row
+//     ACC = Z^T [Yw | P]               the chunk's part of S^T [b, a] and of out^T [b, i], in one product of N = 192
+//     O1  = S^T X^T                    what the state gives, S^T as an operand in tensor memory
+// so that z, x and y are operands just as the copies laid them down, S^T lives in the registers of 256 threads (a row a lane, two
+// threads a row) in FP32, and only the decayed scores P and keys Yw pass through shared memory, each as a sum of two or three BF16 numbers:
+// the inputs are exact, so a product of three parts is FP32's accuracy, of two 2^-17.
+//
+// Roles of a CTA, joined by mbarriers: a copy warp (TMA, and the chunk's decays), an MMA warp, eight warps that prepare P and Yw, eight
+// that hold S, write its operand, fold ACC into it and put out rows.
+//
+// The chunks of all (sequence, head) pairs stand in one line, cut evenly over the CTAs ("pieces").  A piece that begins within a pair
+// needs the state there: a first pass (STATES) runs the pieces that end within a pair for their state alone, `join_kernel` chains
+// those of a pair, and the second pass starts from them.  The decay of a piece is one number a head, so the chain is a sum.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "lin.cuh"
+#include "tc_ptx.cuh"
+
+namespace k3kda {
+namespace lin {
+namespace {
+
+using namespace tc;
+
+constexpr int C = 64, D = 128, THREADS = 640, CTL = 128, PREP = 256, HOLD = 256;
+constexpr int PREP_WARP = CTL / 32, HOLD_WARP = (CTL + PREP) / 32;
+// A CTA's registers at its launch are THREADS x 96; the roles' shares may not be more.
+constexpr int REG_CTL = 32, REG_PREP = 80, REG_HOLD = 144;
+static_assert(CTL * REG_CTL + PREP * REG_PREP + HOLD * REG_HOLD <= THREADS * 96, "shares of the registers");
+constexpr uint32_t kTries = 1u << 20;            // a second or two
+
+// shared memory
+constexpr uint32_t TILE = C * 128;                                 // 64 rows of 64 BF16 values
+constexpr uint32_t AT_Y = 0, AT_X = TILE, ATOM = 2 * TILE, AT_Z = 4 * TILE, STAGE = 6 * TILE;     // y0 x0 y1 x1 z0 z1
+constexpr uint32_t AT_OPS = 2 * STAGE, PART = 3 * TILE;            // three parts of [Yw0 | Yw1 | P]
+constexpr uint32_t AT_OUT = AT_OPS + 3 * PART;                     // FP32 [64][OUT_PITCH]
+constexpr int OUT_PITCH = D + 4;
+constexpr uint32_t AT_INFO = AT_OUT + C * OUT_PITCH * 4;
+
+struct Info {                  // of one stage
+    float2 g[C];               // sums of the decays, as two floats
+    float c[C], w[C];
+    float own[C];              // P's diagonal, where it is kept apart
+    float keep;                // the chunk's decay
+    unsigned long long lost;   // tokens whose decay is NaN
+    int n, h, t0, valid, chunk, flags;
+    int dirty;                 // some z is not finite:
+    int poison[D];             // the channel's first such token in the job's direction
+};
+constexpr int NONE = 1 << 20;
+enum { kFromFirst = 1, kFromPiece = 2, kEnds = 4, kOpen = 8 };        // kOpen: the pair begins here and ends in another piece
+
+struct Shared {
+    Info info[2];
+    unsigned long long full[2], empty[2], pt_full, pt_free, prep_full, acc_full, acc_free, sop_full, o1_full, drain;
+    uint32_t tmem;
+    int dead;
+    long long part[THREADS / 32];
+    int part_end[THREADS / 32];
+    int n[2], h[2], pos[2], chunks[2], begin[2], len[2], floor[2];     // where the piece begins, and where it ends
+};
+constexpr uint32_t SMEM = AT_INFO + sizeof(Shared) + 1024;
+
+// tensor memory
+constexpr uint32_t PT = 0, ACC = 64, ACC_O = ACC + D, O1 = 256, SOP = 320;
+
+struct Head {                  // of a piece's state
+    float keep;
+    int ends_within, goes_on;  // whether the piece ends within a pair; whether it began within the same
+};
+
+struct TcArgs {
+    CUtensorMap map[4];
+    Call c;
+    int x[3], y[3], z[3];      // the jobs' maps
+    int rows;                  // of a copy's box
+    int pieces;                // a job
+    int least;                 // chunks of a piece, at least, where there are more pieces than pairs
+    Head *head;                // [jobs][pieces]
+    float *state;              // [jobs][pieces][a][D]
+    float *kept;               // likewise, or null: the first states of the pairs that a piece leaves open, when they may be written over
+};
+
+template <int N> __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// A pair as BF16 numbers that add up to it; the rests are exact in FP32.
+__device__ __forceinline__ uint32_t peel(float &x, float &y) {
+    const uint32_t w = pack(x, y);
+    x -= low(w);
+    y -= high(w);
+    return w;
+}
+
+struct Waiter {
+    volatile int *dead;
+    unsigned *status;
+    // (by a whole warp: the same answer for all its lanes)
+    __device__ __forceinline__ bool operator()(const unsigned long long &bar, int parity) const {
+        const uint32_t at = smem_u32(&bar);
+        bool ok = mbar_try_wait(at, parity & 1);
+        for (uint32_t i = 1; !ok && i < kTries && !((i & 63) == 0 && *dead); ++i) ok = mbar_try_wait(at, parity & 1);
+        if (__all_sync(0xffffffffu, ok)) return true;
+        if (!ok && !*dead) {
+            *dead = 1;
+            atomicOr(status, 2u);
+        }
+        return false;
+    }
+};
+
+// The line of chunks: sequence n has max(1, ceil(len / C)) for each head, so that an empty one hands its state on.  Its bounds never
+// run backwards, whatever the array holds (an end is at least the ends before it), so that no token is taken twice.
+struct Line {
+    const int32_t *cu;
+    int T;
+    __device__ __forceinline__ int bound(int i) const { return min(max(cu[i], 0), T); }
+};
+
+template <bool STATES> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(const __grid_constant__ TcArgs A) {
+    extern __shared__ uint8_t raw[];
+    uint8_t *const sm = smem_align1024(raw);
+    const uint32_t sm32 = smem_u32(sm);
+    Shared &sh = *reinterpret_cast<Shared *>(sm + AT_INFO);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int job = blockIdx.x / A.pieces, piece = blockIdx.x % A.pieces;
+    const Job &J = A.c.job[job];
+    const int N = A.c.N, H = A.c.H;
+    const Waiter wait{&sh.dead, A.c.status};
+
+    // ---- where the piece begins and ends
+    const int per = (N + THREADS - 1) / THREADS, n0 = min(N, tid * per), n1 = min(N, n0 + per);
+    const Line line{A.c.cu, A.c.T};
+    auto length = [&](int n, int &floor, int &begin) {               // of sequence n; floor: the ends before it
+        if (!line.cu) {
+            begin = 0;
+            return A.c.T;
+        }
+        begin = max(line.bound(n), floor);
+        floor = max(floor, line.bound(n + 1));
+        return floor - begin;
+    };
+    int own_end = 0;
+    if (line.cu)
+        for (int n = n0; n < n1; ++n) own_end = max(own_end, line.bound(n + 1));
+    int run_end = own_end;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int e = __shfl_up_sync(0xffffffffu, run_end, o);
+        if (lane >= o) run_end = max(run_end, e);
+    }
+    if (lane == 31) sh.part_end[warp] = run_end;
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&sh.full[s]), 1);
+            mbar_init(smem_u32(&sh.empty[s]), 1 + HOLD / 32);
+            sh.info[s].dirty = 0;
+        }
+        mbar_init(smem_u32(&sh.pt_full), 1);
+        mbar_init(smem_u32(&sh.pt_free), 4);
+        mbar_init(smem_u32(&sh.prep_full), PREP / 32);
+        mbar_init(smem_u32(&sh.acc_full), 2);
+        mbar_init(smem_u32(&sh.acc_free), HOLD / 32);
+        mbar_init(smem_u32(&sh.sop_full), HOLD / 32);
+        mbar_init(smem_u32(&sh.o1_full), 1);
+        mbar_init(smem_u32(&sh.drain), 1);
+        fence_mbar_init();
+        sh.dead = 0;
+    }
+    if (tid < 2 * D) sh.info[tid / D].poison[tid % D] = NONE;
+    __syncthreads();
+    int floor0 = __shfl_up_sync(0xffffffffu, run_end, 1);
+    if (lane == 0) floor0 = 0;
+    for (int w = 0; w < warp; ++w) floor0 = max(floor0, sh.part_end[w]);
+    long long own = 0;
+    {
+        int f = floor0, b;
+        for (int n = n0; n < n1; ++n) own += max(1, (length(n, f, b) + C - 1) / C);
+    }
+    long long run = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long e = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += e;
+    }
+    if (lane == 31) sh.part[warp] = run;
+    __syncthreads();
+    long long before = run - own, total = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += sh.part[w];
+        total += sh.part[w];
+    }
+    const long long U = total * H, most = max((long long)N * H, U / A.least);
+    const int count_pieces = (int)min((long long)A.pieces, most);
+    if (piece >= count_pieces) {
+        if (STATES && tid == 0) A.head[job * A.pieces + piece] = Head{0.f, 0, 0};
+        return;
+    }
+    long long u0 = U * piece / count_pieces;
+    const long long u1 = U * (piece + 1) / count_pieces;
+    {
+        long long at = before;
+        int f = floor0, b;
+        for (int n = n0; n < n1; ++n) {
+            const int f_was = f, len = length(n, f, b), chunks = max(1, (len + C - 1) / C);
+            for (int e = 0; e < 2; ++e) {
+                const long long u = (e ? u1 : u0) - at * H;
+                if (u < 0 || u >= (long long)chunks * H) continue;
+                sh.n[e] = n;
+                sh.h[e] = (int)(u / chunks);
+                sh.pos[e] = (int)(u % chunks);
+                sh.chunks[e] = chunks;
+                sh.begin[e] = b;
+                sh.len[e] = len;
+                sh.floor[e] = f_was;
+            }
+            at += chunks;
+        }
+    }
+    __syncthreads();
+    int start = 0;                                                   // which of the two places the work begins at
+    bool goes_on = false;
+    if constexpr (STATES) {
+        const bool within = u1 < U && sh.pos[1] > 0;
+        if (within) {
+            goes_on = u1 - sh.pos[1] < u0;
+            if (!goes_on) {
+                u0 = u1 - sh.pos[1];
+                start = 1;
+            }
+        }
+        if (tid == 0) {
+            Head &hd = A.head[job * A.pieces + piece];
+            hd.ends_within = within;
+            hd.goes_on = goes_on;
+        }
+        if (!within) return;
+    }
+    const int items = (int)(u1 - u0);
+    const int pos0 = STATES && start == 1 ? 0 : sh.pos[start];
+
+    if (warp == 0) {
+        tmem_alloc(smem_u32(&sh.tmem), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = sh.tmem;
+    const int parts = STATES ? 2 : J.exact ? 3 : 2;                  // of P and S
+
+    if (warp < PREP_WARP) {
+        give_registers<REG_CTL>();
+        if (warp == 0) {
+            // ---------------- copies and decays ----------------
+            int n = sh.n[start], h = sh.h[start], pos = pos0, chunks = sh.chunks[start], begin = sh.begin[start], len = sh.len[start];
+            int floor = sh.floor[start];
+            {
+                int b;
+                length(n, floor, b);
+            }
+            long long sum = 0;                                       // STATES: the whole piece's decay
+            bool sum_lost = false;
+            const void *mx = &A.map[A.x[job]], *my = &A.map[A.y[job]], *mz = &A.map[A.z[job]];
+            int it = 0;
+            for (; it < items; ++it) {
+                const int s = it & 1, chunk = J.reverse ? chunks - 1 - pos : pos, t0 = begin + chunk * C, valid = min(C, len - chunk * C);
+                Info &I = sh.info[s];
+                float g[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int t = 2 * lane + u;
+                    g[u] = t < valid ? __ldg(A.c.g + (A.c.fixed ? (size_t)h : (size_t)(t0 + t) * H + h)) : 0.f;
+                }
+                if (it >= 2 && !wait(sh.empty[s], (it >> 1) - 1)) break;
+                if (lane == 0) {
+                    const uint32_t bar = smem_u32(&sh.full[s]), to = sm32 + s * STAGE;
+                    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"((uint32_t)(STATES ? 4 : 6) * A.rows * 128) : "memory");
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        if (!STATES) tma_load_3d(to + AT_X + u * ATOM, mx, 64 * u, h / J.x.share, t0, bar);
+                        tma_load_3d(to + AT_Y + u * ATOM, my, 64 * u, h / J.y.share, t0, bar);
+                        tma_load_3d(to + AT_Z + u * TILE, mz, 64 * u, h / J.z.share, t0, bar);
+                    }
+                }
+                const long long d0 = decay_units(g[0]), d1 = decay_units(g[1]);
+                long long v = d0 + d1;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long e = __shfl_up_sync(0xffffffffu, v, o);
+                    if (lane >= o) v += e;
+                }
+                const long long all = __shfl_sync(0xffffffffu, v, 31);
+                const unsigned bad0 = __ballot_sync(0xffffffffu, g[0] != g[0]), bad1 = __ballot_sync(0xffffffffu, g[1] != g[1]);
+                unsigned long long bad = 0;
+                if (bad0 | bad1)
+                    for (int i = 0; i < 32; ++i) bad |= (unsigned long long)((bad0 >> i & 1) | (bad1 >> i & 1) << 1) << (2 * i);
+                const float nan = __int_as_float(0x7fffffff);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int t = 2 * lane + u;
+                    const long long vt = u ? v : v - d1;
+                    const unsigned long long upto = ~0ull >> (63 - t);
+                    const float up = bad & upto ? nan : exp2_units(vt), down = bad & ~upto ? nan : exp2_units(all - vt);
+                    I.g[t] = two_floats(vt);
+                    I.c[t] = J.sc * (J.reverse ? down : up);
+                    I.w[t] = J.sw * (J.reverse ? up : down);
+                }
+                sum += all;
+                sum_lost = sum_lost || bad;
+                if (lane == 0) {
+                    I.keep = bad ? nan : exp2_units(all);
+                    I.lost = bad;
+                    I.n = n;
+                    I.h = h;
+                    I.t0 = t0;
+                    I.valid = valid;
+                    I.chunk = chunk;
+                    I.flags = (pos == 0 ? kFromFirst : it == 0 ? kFromPiece : 0) | (pos == chunks - 1 ? kEnds : 0) |
+                              (pos == 0 && chunks > items - it ? kOpen : 0);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.full[s]));
+                if (++pos == chunks) {
+                    pos = 0;
+                    if (++h == H) {
+                        h = 0;
+                        ++n;
+                        if (it + 1 < items) {
+                            len = length(n, floor, begin);
+                            chunks = max(1, (len + C - 1) / C);
+                        }
+                    }
+                }
+            }
+            // (after a wait that gave up: nothing may be on its way into shared memory when the CTA ends)
+            for (int k = max(0, it - 2); k < it; ++k)
+                for (uint32_t i = 0; i < kTries && !mbar_try_wait(smem_u32(&sh.full[k & 1]), (k >> 1) & 1); ++i) {}
+            if (STATES && lane == 0) A.head[job * A.pieces + piece].keep = sum_lost ? __int_as_float(0x7fffffff) : exp2_units(sum);
+        } else if (warp == 1) {
+            // ---------------- products ----------------
+            const bool one = lane == 0;
+            const int ka = (J.a + 15) / 16;
+            const uint32_t id_pt = idesc_bf16_f32(128, 64), id_o1 = idesc_bf16_f32(128, 64);
+            const uint32_t id_192 = idesc_bf16_f32(128, 192, false, true, true), id_128 = idesc_bf16_f32(128, 128, false, true, true);
+            auto scores = [&](int it) {
+                const int s = it & 1;
+                if (!wait(sh.full[s], it >> 1) || (it > 0 && !wait(sh.pt_free, it - 1))) return false;
+                tc_fence_after();
+                if (one) {
+                    const uint32_t at = sm32 + s * STAGE;
+                    for (int k = 0; k < ka; ++k) {
+                        const uint32_t step = (k >> 2) * ATOM + (k & 3) * 32;
+                        mma_bf16(tm + PT, sdesc_kmajor_sw128(at + AT_Y + step), sdesc_kmajor_sw128(at + AT_X + step), id_pt, k > 0);
+                    }
+                    mma_commit(smem_u32(&sh.pt_full));
+                }
+                __syncwarp();
+                return true;
+            };
+            bool ok = STATES || scores(0);
+            for (int it = 0; ok && it < items; ++it) {
+                const int s = it & 1;
+                if (!wait(sh.prep_full, it) || (it > 0 && !wait(sh.acc_free, it - 1))) break;
+                if (STATES && !wait(sh.full[s], it >> 1)) break;
+                tc_fence_after();
+                if (one) {
+                    const uint32_t z = sm32 + s * STAGE + AT_Z;
+                    // the parts of less weight first
+#pragma unroll
+                    for (int u = 0; u < 3; ++u) {
+                        const int p = u == 0 ? 1 : u == 1 ? 2 : 0;
+                        const uint32_t ops = sm32 + AT_OPS + p * PART, id = STATES || p >= parts ? id_128 : id_192;
+#pragma unroll
+                        for (int k = 0; k < C / 16; ++k)
+                            mma_bf16(tm + ACC, sdesc_mnmajor_sw128(z + k * 2048, TILE), sdesc_mnmajor_sw128(ops + k * 2048, TILE), id, u + k > 0);
+                    }
+                    mma_commit(smem_u32(&sh.acc_full));
+                    mbar_arrive(smem_u32(&sh.acc_full));             // (what the preparing warps noted is passed on by a plain arrival)
+                    if (STATES) mma_commit(smem_u32(&sh.empty[s]));
+                }
+                __syncwarp();
+                if constexpr (!STATES) {
+                    if (it + 1 < items && !scores(it + 1)) break;
+                    if (!wait(sh.sop_full, it)) break;
+                    tc_fence_after();
+                    if (one) {
+                        const uint32_t x = sm32 + s * STAGE + AT_X;
+                        for (int u = 0; u < parts; ++u) {
+                            const int p = u + 1 < parts ? u + 1 : 0;
+                            for (int k = 0; k < ka; ++k)
+                                mma_bf16_ta(tm + O1, tm + SOP + p * 64 + k * 8, sdesc_kmajor_sw128(x + (k >> 2) * ATOM + (k & 3) * 32), id_o1, u + k > 0);
+                        }
+                        mma_commit(smem_u32(&sh.o1_full));
+                        mma_commit(smem_u32(&sh.empty[s]));
+                    }
+                    __syncwarp();
+                }
+            }
+            // every product has ended before the CTA does
+            if (one) mma_commit(smem_u32(&sh.drain));
+            for (uint32_t i = 0; i < kTries && !mbar_try_wait(smem_u32(&sh.drain), 0); ++i) {}
+        }
+    } else if (warp < HOLD_WARP) {
+        // ---------------- scores and keys as operands ----------------
+        give_registers<REG_PREP>();
+        const int pw = warp - PREP_WARP, quarter = warp & 3;
+        const bool keys = STATES || quarter >= 2;
+        // keys: row `t` of atom `atom`, pieces from `c0`; scores: row `t`, columns from `i0`
+        const int kw = STATES ? pw : (pw >> 2) * 2 + (quarter & 1);
+        const int t = keys ? 32 * (kw & 1) + lane : 32 * quarter + lane;
+        const int atom = (kw >> 1) & 1, c0 = STATES ? (kw >> 2) * 4 : 0, i0 = 32 * (pw >> 2);
+        constexpr int PIECES = STATES ? 4 : 8;
+        for (int it = 0; it < items; ++it) {
+            const int s = it & 1;
+            if (!wait(sh.full[s], it >> 1)) break;
+            Info &I = sh.info[s];
+            const int valid = I.valid;
+            uint8_t *const row_at = sm + AT_OPS + (uint32_t)t * 128;
+            if (keys) {
+                // z: rows behind the sequence are put to 0, and what is not finite, which is noted
+                uint8_t *const z = sm + s * STAGE + AT_Z + atom * TILE + (uint32_t)t * 128;
+                if (t >= valid) {
+#pragma unroll
+                    for (int c = 0; c < PIECES; ++c) *reinterpret_cast<uint4 *>(z + (c0 + c) * 16) = make_uint4(0, 0, 0, 0);
+                } else {
+                    uint32_t most = 0;
+#pragma unroll
+                    for (int c = 0; c < PIECES; ++c) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(z + (c0 + c) * 16);
+                        most = __vmaxu2(__vmaxu2(most, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
+                        most = __vmaxu2(__vmaxu2(most, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
+                    }
+                    if ((most & 0xffffu) >= 0x7f80u || most >= 0x7f800000u) {
+                        for (int e = 0; e < PIECES * 8; ++e) {
+                            unsigned short *p = reinterpret_cast<unsigned short *>(z + c0 * 16) + e;
+                            if ((*p & 0x7fffu) < 0x7f80u) continue;
+                            *p = 0;
+                            // (piece c of row t lies at piece c ^ (t & 7))
+                            const int channel = atom * 64 + (((c0 + e / 8) ^ (t & 7)) * 8 + e % 8);
+                            atomicMin(&I.poison[channel], J.reverse ? C - 1 - t : t);
+                            I.dirty = 1;
+                        }
+                    }
+                }
+                if (it > 0 && !wait(sh.acc_full, it - 1)) break;     // the operands' last reader
+                const uint8_t *const y = sm + s * STAGE + AT_Y + atom * ATOM + (uint32_t)t * 128;
+                uint8_t *const to = row_at + atom * TILE;
+                const float w = I.w[t];
+#pragma unroll
+                for (int c = 0; c < PIECES; ++c) {
+                    uint4 v = make_uint4(0, 0, 0, 0), p[3];
+                    if (t < valid) v = *reinterpret_cast<const uint4 *>(y + (c0 + c) * 16);
+                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t out[3][4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        float a = low(in[u]) * w, b = high(in[u]) * w;
+                        if (t >= valid) a = b = 0.f;
+                        out[0][u] = peel(a, b);
+                        out[1][u] = peel(a, b);
+                        out[2][u] = pack(a, b);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 3; ++u) {
+                        p[u] = make_uint4(out[u][0], out[u][1], out[u][2], out[u][3]);
+                        *reinterpret_cast<uint4 *>(to + u * PART + (c0 + c) * 16) = p[u];
+                    }
+                }
+            } else {
+                if (!wait(sh.pt_full, it)) break;
+                tc_fence_after();
+                float p[32];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t r[16];
+                    tmem_ld16(tm + ((uint32_t)quarter * 32 << 16) + PT + i0 + 16 * u, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) p[16 * u + e] = __uint_as_float(r[e]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.pt_free));
+                const float2 gj = I.g[t];
+                const unsigned long long lost = I.lost;
+                const float sign = J.reverse ? -1.f : 1.f;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const int i = i0 + e;
+                    const float2 gi = I.g[i];
+                    float d = sign * ((gi.x - gj.x) + (gi.y - gj.y));
+                    if (lost && ((~0ull >> (63 - i)) ^ (~0ull >> (63 - t))) & lost) d = __int_as_float(0x7fffffff);
+                    const bool seen = (J.reverse ? t >= i : t <= i) && t < valid;
+                    p[e] = seen ? J.sp * ex2(d) * p[e] : 0.f;
+                    if (J.dots && i == t) {
+                        I.own[t] = p[e];
+                        p[e] = 0.f;
+                    }
+                }
+                if (it > 0 && !wait(sh.acc_full, it - 1)) break;
+                uint8_t *const to = row_at + 2 * TILE;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t at = (uint32_t)(((i0 >> 3) + c) ^ (t & 7)) * 16;
+                    for (int u = 0; u < parts; ++u) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[e] = peel(p[8 * c + 2 * e], p[8 * c + 2 * e + 1]);
+                        *reinterpret_cast<uint4 *>(to + u * PART + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.prep_full));
+        }
+    } else {
+        // ---------------- the state, and what is put out ----------------
+        take_registers<REG_HOLD>();
+        const int hw = warp - HOLD_WARP, half = hw >> 2, b = 32 * (warp & 3) + lane, a0 = 64 * half;
+        const uint32_t lanes = tm + ((uint32_t)(warp & 3) * 32 << 16);
+        const bool in_b = b < J.b;
+        float S[64];
+#pragma unroll
+        for (int i = 0; i < 64; ++i) S[i] = 0.f;
+        float *const out_at = reinterpret_cast<float *>(sm + AT_OUT);
+        float *const own_state = A.state + ((size_t)job * A.pieces + piece) * D * D;
+        bool ok = true;
+        // a warp that gives up still comes to the others' barriers, and touches nothing
+        auto give_up = [&] {
+            ok = false;
+            named_bar(1, HOLD);
+            if (!STATES) named_bar(1, HOLD);
+        };
+        for (int it = 0; it < items; ++it) {
+            const int s = it & 1;
+            if (!ok || !wait(sh.full[s], it >> 1)) {
+                give_up();
+                continue;
+            }
+            Info &I = sh.info[s];
+            const int flags = I.flags, n = I.n, h = I.h, t0 = I.t0, valid = I.valid, chunk = I.chunk;
+            const int slot = flags & (kFromFirst | kEnds) ? seq_slot(A.c.slot, A.c.num_slots, n) : 0;
+            const size_t state = ((size_t)max(slot, 0) * H + h) * J.a * J.b;
+            float *const kept = A.kept && (flags & kOpen) ? A.kept + ((size_t)job * A.pieces + piece) * D * D + b : nullptr;
+            if (!STATES && kept) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) S[i] = kept[(size_t)(a0 + i) * D];
+            } else if (flags & kFromFirst) {
+                const float *from = J.first && slot >= 0 && in_b ? J.first + state + (size_t)b * J.sb : nullptr;
+                if (J.sa == 1) {
+#pragma unroll
+                    for (int i = 0; i < 64; i += 4) {
+                        const float4 v = from && a0 + i < J.a ? *reinterpret_cast<const float4 *>(from + a0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        S[i] = v.x;
+                        S[i + 1] = v.y;
+                        S[i + 2] = v.z;
+                        S[i + 3] = v.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) S[i] = from && a0 + i < J.a ? from[(size_t)(a0 + i) * J.sa] : 0.f;
+                }
+                if (STATES && kept)
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) kept[(size_t)(a0 + i) * D] = S[i];
+            } else if (flags & kFromPiece) {
+                if (STATES) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) S[i] = 0.f;
+                } else {
+                    const float *from = own_state - D * D + b;       // the state that the piece before this one leaves
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) S[i] = __ldg(from + (size_t)(a0 + i) * D);
+                }
+            }
+            auto dump = [&](float *to) {                             // [a][b] dense
+                if (in_b)
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        if (a0 + i < J.a) to[(size_t)(a0 + i) * J.b + b] = S[i];
+            };
+            if constexpr (!STATES) {
+                if (J.anchors && !J.reverse && chunk > 0 && chunk * C % kAnchor == 0)
+                    dump(J.anchors + ((size_t)(anchor_slot(t0 - chunk * C, n) + chunk * C / kAnchor - 1) * H + h) * J.a * J.b);
+                // S as an operand: a pair of columns a word
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t w[3][16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float x = S[32 * q + 2 * i], y = S[32 * q + 2 * i + 1];
+                        w[0][i] = peel(x, y);
+                        w[1][i] = peel(x, y);
+                        w[2][i] = pack(x, y);
+                    }
+                    tmem_st16(lanes + SOP + a0 / 2 + 16 * q, w[0]);
+                    tmem_st16(lanes + SOP + 64 + a0 / 2 + 16 * q, w[1]);
+                    if (parts == 3) tmem_st16(lanes + SOP + 128 + a0 / 2 + 16 * q, w[2]);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.sop_full));
+            }
+            if (!wait(sh.acc_full, it)) {
+                give_up();
+                continue;
+            }
+            tc_fence_after();
+            const float keep = I.keep;
+            const bool dirty = I.dirty;
+            const int poison = dirty ? I.poison[b] : NONE;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t r[16];
+                tmem_ld16(lanes + ACC + a0 + 16 * q, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S[16 * q + i] = fmaf(keep, S[16 * q + i], __uint_as_float(r[i]));
+            }
+            if (poison != NONE)
+#pragma unroll
+                for (int i = 0; i < 64; ++i) S[i] = __int_as_float(0x7fffffff);
+            if constexpr (STATES) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.acc_free));
+                named_bar(1, HOLD);                                  // (dirty has been read by all)
+                if (dirty) {
+                    I.poison[b] = NONE;
+                    I.dirty = 0;
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));
+            } else {
+                float o[32];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t r[16];
+                    tmem_ld16(lanes + ACC_O + 32 * half + 16 * q, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[16 * q + i] = __uint_as_float(r[i]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.acc_free));
+                if (!wait(sh.o1_full, it)) {
+                    give_up();
+                    continue;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t r[16];
+                    tmem_ld16(lanes + O1 + 32 * half + 16 * q, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int t = 32 * half + 16 * q + i;
+                        float v = fmaf(I.c[t], __uint_as_float(r[i]), o[16 * q + i]);
+                        if (poison != NONE && (J.reverse ? C - 1 - t : t) >= poison) v = __int_as_float(0x7fffffff);
+                        out_at[t * OUT_PITCH + b] = v;
+                    }
+                }
+                tc_fence_before();
+                named_bar(1, HOLD);
+                // rows: 8 a warp, 4 channels a lane
+                const int c = 4 * lane;
+                const bool in_c = c < J.b;
+#pragma unroll 4
+                for (int u = 0; u < 8; ++u) {
+                    const int t = 8 * hw + u;
+                    if (t >= valid) break;
+                    float4 v = *reinterpret_cast<const float4 *>(out_at + t * OUT_PITCH + c);
+                    const size_t row = (size_t)(t0 + t) * H + h;
+                    if (J.dots) {
+                        float dot = 0.f;
+                        if (in_c) {
+                            const uint2 r = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(J.r.p) +
+                                                                                  ((size_t)(t0 + t) * (H / J.r.share) + h / J.r.share) * J.b + c));
+                            dot = fmaf(high(r.y), v.w, fmaf(low(r.y), v.z, fmaf(high(r.x), v.y, low(r.x) * v.x)));
+                            // the term of the token itself
+                            const uint2 z = *reinterpret_cast<const uint2 *>(sm + s * STAGE + AT_Z + (lane >> 4) * TILE + sw128_offset(t, c & 63));
+                            const float p = I.own[t];
+                            v = make_float4(fmaf(p, low(z.x), v.x), fmaf(p, high(z.x), v.y), fmaf(p, low(z.y), v.z), fmaf(p, high(z.y), v.w));
+                        }
+                        dot = warp_sum(dot);
+                        if (lane == 0) J.dots[row] = dot;
+                    }
+                    if (!in_c) continue;
+                    if (J.out_bf16) {
+                        __stcs(reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(J.out) + row * J.b + c), make_uint2(pack(v.x, v.y), pack(v.z, v.w)));
+                    } else {
+                        __stcs(reinterpret_cast<float4 *>(static_cast<float *>(J.out) + row * J.b + c), v);
+                    }
+                }
+                named_bar(1, HOLD);                                  // (the rows are read, and dirty by all)
+                if (dirty) {
+                    I.poison[b] = NONE;
+                    I.dirty = 0;
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));
+                if (J.anchors && J.reverse && chunk > 0 && chunk * C % kAnchor == 0)
+                    dump(J.anchors + ((size_t)(anchor_slot(t0 - chunk * C, n) + chunk * C / kAnchor - 1) * H + h) * J.a * J.b);
+                if (flags & kEnds) {
+                    if (J.anchors && J.last_anchor)
+                        dump(J.anchors + ((size_t)(anchor_slot(t0 - chunk * C, n) + max(0, chunk * C + valid - 1) / kAnchor) * H + h) * J.a * J.b);
+                    if (J.last && slot >= 0 && in_b) {
+                        float *to = J.last + state + (size_t)b * J.sb;
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (a0 + i < J.a) to[(size_t)(a0 + i) * J.sa] = S[i];
+                    }
+                }
+            }
+        }
+        if constexpr (STATES) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) own_state[(size_t)(a0 + i) * D + b] = S[i];
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tm, 512);
+    }
+}
+
+// The states that pieces leave, one after the other within a pair: S_piece += decay_piece S_before, from the piece that holds the pair's
+// start on.  A CTA a slice of the state and first piece.
+__global__ void __launch_bounds__(256) join_kernel(const Head *head, float *state, int pieces) {
+    head += (size_t)blockIdx.z * pieces;
+    state += ((size_t)blockIdx.z * pieces) * D * D + (size_t)blockIdx.x * 1024 + threadIdx.x * 4;
+    int c = blockIdx.y;
+    if (!head[c].ends_within || head[c].goes_on) return;
+    float4 v = *reinterpret_cast<float4 *>(state + (size_t)c * D * D);
+    for (++c; c < pieces && head[c].ends_within && head[c].goes_on; ++c) {
+        float4 *at = reinterpret_cast<float4 *>(state + (size_t)c * D * D);
+        const float k = head[c].keep;
+        const float4 w = *at;
+        v = make_float4(fmaf(k, v.x, w.x), fmaf(k, v.y, w.y), fmaf(k, v.z, w.z), fmaf(k, v.w, w.w));
+        *at = v;
+    }
+}
+
+std::atomic<PFN_cuTensorMapEncodeTiled_v12000> g_encode{nullptr};
+std::atomic<uint64_t> g_attr_states{0}, g_attr_main{0};
+
+// [T, heads, d] BF16 in boxes of 64 channels of one head and `rows` tokens; channels and tokens outside read 0.
+cudaError_t make_map(CUtensorMap *m, const void *base, int T, int heads, int d, int rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = g_encode.load(std::memory_order_acquire);
+    if (!encode) {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+        if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !fn) return e != cudaSuccess ? e : cudaErrorSymbolNotFound;
+        encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+        g_encode.store(encode, std::memory_order_release);
+    }
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)T};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
+    const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)rows}, ones[3] = {1u, 1u, 1u};
+    const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, ones,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+constexpr int MOST_PIECES = 160;
+
+}  // namespace
+
+size_t tc_workspace() { return (size_t)MOST_PIECES * (2 * D * D * sizeof(float) + sizeof(Head)); }
+
+cudaError_t launch_scan_tc(const Call &c, cudaStream_t s) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<true>, (int)SMEM, g_attr_states);
+    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<false>, (int)SMEM, g_attr_main);
+    if (e != cudaSuccess) return e;
+    TcArgs A{};
+    A.c = c;
+    A.rows = c.T < C ? (c.T < 1 ? 1 : c.T) : C;
+    int maps = 0;
+    const void *of[4] = {};
+    for (int j = 0; j < c.jobs; ++j) {
+        const Rows *rows[3] = {&c.job[j].x, &c.job[j].y, &c.job[j].z};
+        int *at[3] = {&A.x[j], &A.y[j], &A.z[j]};
+        for (int u = 0; u < 3; ++u) {
+            int m = 0;
+            while (m < maps && of[m] != rows[u]->p) ++m;
+            if (m == maps) {
+                of[maps++] = rows[u]->p;
+                if ((e = make_map(&A.map[m], rows[u]->p, c.T, c.H / rows[u]->share, u == 2 ? c.job[j].b : c.job[j].a, A.rows)) != cudaSuccess) return e;
+            }
+            *at[u] = m;
+        }
+    }
+    A.pieces = (sms < MOST_PIECES ? sms : MOST_PIECES) / c.jobs;
+    A.least = 16;
+    A.state = static_cast<float *>(c.pieces);
+    A.kept = A.state + (size_t)MOST_PIECES * D * D;
+    A.head = reinterpret_cast<Head *>(A.kept + (size_t)MOST_PIECES * D * D);
+    if (!c.job[0].first || c.job[0].first != c.job[0].last) A.kept = nullptr;
+    // one short sequence: every piece is a whole pair
+    const long long longest = c.T / C + 1;
+    const bool cut = !(c.N == 1 && longest <= A.least && c.H <= A.pieces);
+    if (cut) {
+        tc_kernel<true><<<A.pieces * c.jobs, THREADS, SMEM, s>>>(A);
+        count_launch();
+        join_kernel<<<dim3(D * D / 1024, A.pieces, c.jobs), 256, 0, s>>>(A.head, A.state, A.pieces);
+        count_launch();
+    }
+    tc_kernel<false><<<A.pieces * c.jobs, THREADS, SMEM, s>>>(A);
+    count_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace lin
+}  // namespace k3kda
