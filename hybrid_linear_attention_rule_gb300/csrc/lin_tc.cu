@@ -8,8 +8,9 @@
 // threads a row) in FP32, and only the decayed scores P and keys Yw pass through shared memory, each as a sum of two or three BF16 numbers:
 // the inputs are exact, so a product of three parts is FP32's accuracy, of two 2^-17.
 //
-// Roles of a CTA, joined by mbarriers: a copy warp (TMA, and the chunk's decays), an MMA warp, eight warps that prepare P and Yw, eight
-// that hold S, write its operand, fold ACC into it and put out rows.
+// Roles of a CTA, joined by mbarriers: a warp that walks the chunks and sums their decays, ahead of the others; a copy warp (TMA); an MMA
+// warp for PT and ACC and one for O1, so that neither chain waits for the other's operands; eight warps that prepare P and
+// Yw, eight that hold S, write its operand, fold ACC into it and put out rows.
 //
 // The chunks of all (sequence, head) pairs stand in one line, cut evenly over the CTAs ("pieces").  A piece that begins within a pair
 // needs the state there: a first pass (STATES) runs the pieces that end within a pair for their state alone, `join_kernel` chains
@@ -41,8 +42,8 @@ constexpr uint32_t AT_OUT = AT_OPS + 3 * PART;                     // FP32 [64][
 constexpr int OUT_PITCH = D + 4;
 constexpr uint32_t AT_INFO = AT_OUT + C * OUT_PITCH * 4;
 
-struct Info {                  // of one stage
-    float2 g[C];               // sums of the decays, as two floats
+struct Info {                  // of one chunk
+    float2 g[C];               // sums of the decays, as two floats; negative backward in time, so that d = g_i - g_j either way
     float c[C], w[C];
     float own[C];              // P's diagonal, where it is kept apart
     float keep;                // the chunk's decay
@@ -51,12 +52,12 @@ struct Info {                  // of one stage
     int dirty;                 // some z is not finite:
     int poison[D];             // the channel's first such token in the job's direction
 };
-constexpr int NONE = 1 << 20;
+constexpr int NONE = 1 << 20, INFOS = 4;
 enum { kFromFirst = 1, kFromPiece = 2, kEnds = 4, kOpen = 8 };        // kOpen: the pair begins here and ends in another piece
 
 struct Shared {
-    Info info[2];
-    unsigned long long full[2], empty[2], pt_full, pt_free, prep_full, acc_full, acc_free, sop_full, o1_full, drain;
+    Info info[INFOS];
+    unsigned long long info_full[INFOS], info_free[INFOS], full[2], empty[2], pt_full, pt_free, prep_full, acc_full, acc_free, sop_full, o1_full, drain[2];
     uint32_t tmem;
     int dead;
     long long part[THREADS / 32];
@@ -107,14 +108,25 @@ __device__ __forceinline__ uint32_t peel(float &x, float &y) {
     return w;
 }
 
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// The same value in all lanes, and known to be: the MMA warps' addresses stay in uniform registers, whose instructions take nothing else.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 struct Waiter {
     volatile int *dead;
     unsigned *status;
     // (by a whole warp: the same answer for all its lanes)
     __device__ __forceinline__ bool operator()(const unsigned long long &bar, int parity) const {
         const uint32_t at = smem_u32(&bar);
-        bool ok = mbar_try_wait(at, parity & 1);
-        for (uint32_t i = 1; !ok && i < kTries && !((i & 63) == 0 && *dead); ++i) ok = mbar_try_wait(at, parity & 1);
+        bool ok;
+        uint32_t i = 0;
+#pragma unroll 1
+        do ok = mbar_try_wait(at, parity & 1);
+        while (!ok && ++i < kTries && !*dead);
         if (__all_sync(0xffffffffu, ok)) return true;
         if (!ok && !*dead) {
             *dead = 1;
@@ -132,7 +144,11 @@ struct Line {
     __device__ __forceinline__ int bound(int i) const { return min(max(cu[i], 0), T); }
 };
 
-template <bool STATES> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(const __grid_constant__ TcArgs A) {
+// The kernels: states alone; jobs whose operands are in two parts and that put out nothing beside their rows; any.
+enum Kind { kStates, kPlain, kFull };
+
+template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(const __grid_constant__ TcArgs A) {
+    constexpr bool STATES = KIND == kStates, FULL = KIND == kFull;
     extern __shared__ uint8_t raw[];
     uint8_t *const sm = smem_align1024(raw);
     const uint32_t sm32 = smem_u32(sm);
@@ -157,6 +173,7 @@ template <bool STATES> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(c
     };
     int own_end = 0;
     if (line.cu)
+#pragma unroll 1
         for (int n = n0; n < n1; ++n) own_end = max(own_end, line.bound(n + 1));
     int run_end = own_end;
 #pragma unroll
@@ -168,8 +185,13 @@ template <bool STATES> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(c
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&sh.full[s]), 1);
-            mbar_init(smem_u32(&sh.empty[s]), 1 + HOLD / 32);
-            sh.info[s].dirty = 0;
+            mbar_init(smem_u32(&sh.empty[s]), (STATES ? 1 : 2) + HOLD / 32);
+            mbar_init(smem_u32(&sh.drain[s]), 1);
+        }
+        for (int i = 0; i < INFOS; ++i) {
+            mbar_init(smem_u32(&sh.info_full[i]), 1);
+            mbar_init(smem_u32(&sh.info_free[i]), HOLD / 32);
+            sh.info[i].dirty = 0;
         }
         mbar_init(smem_u32(&sh.pt_full), 1);
         mbar_init(smem_u32(&sh.pt_free), 4);
@@ -178,18 +200,19 @@ template <bool STATES> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(c
         mbar_init(smem_u32(&sh.acc_free), HOLD / 32);
         mbar_init(smem_u32(&sh.sop_full), HOLD / 32);
         mbar_init(smem_u32(&sh.o1_full), 1);
-        mbar_init(smem_u32(&sh.drain), 1);
         fence_mbar_init();
         sh.dead = 0;
     }
-    if (tid < 2 * D) sh.info[tid / D].poison[tid % D] = NONE;
+    if (tid < INFOS * D) sh.info[tid / D].poison[tid % D] = NONE;
     __syncthreads();
     int floor0 = __shfl_up_sync(0xffffffffu, run_end, 1);
     if (lane == 0) floor0 = 0;
+#pragma unroll 1
     for (int w = 0; w < warp; ++w) floor0 = max(floor0, sh.part_end[w]);
     long long own = 0;
     {
         int f = floor0, b;
+#pragma unroll 1
         for (int n = n0; n < n1; ++n) own += max(1, (length(n, f, b) + C - 1) / C);
     }
     long long run = own;
@@ -201,6 +224,7 @@ template <bool STATES> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(c
     if (lane == 31) sh.part[warp] = run;
     __syncthreads();
     long long before = run - own, total = 0;
+#pragma unroll 1
     for (int w = 0; w < THREADS / 32; ++w) {
         if (w < warp) before += sh.part[w];
         total += sh.part[w];
@@ -216,8 +240,10 @@ template <bool STATES> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(c
     {
         long long at = before;
         int f = floor0, b;
+#pragma unroll 1
         for (int n = n0; n < n1; ++n) {
             const int f_was = f, len = length(n, f, b), chunks = max(1, (len + C - 1) / C);
+#pragma unroll 1
             for (int e = 0; e < 2; ++e) {
                 const long long u = (e ? u1 : u0) - at * H;
                 if (u < 0 || u >= (long long)chunks * H) continue;
@@ -262,12 +288,13 @@ template <bool STATES> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(c
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = sh.tmem;
-    const int parts = STATES ? 2 : J.exact ? 3 : 2;                  // of P and S
+    // (in registers: read where they are used, they would be fetched anew from the parameters each time)
+    const bool reverse = J.reverse, dots = FULL && J.dots, exact = FULL && J.exact;
 
     if (warp < PREP_WARP) {
         give_registers<REG_CTL>();
         if (warp == 0) {
-            // ---------------- copies and decays ----------------
+            // ---------------- chunks and their decays ----------------
             int n = sh.n[start], h = sh.h[start], pos = pos0, chunks = sh.chunks[start], begin = sh.begin[start], len = sh.len[start];
             int floor = sh.floor[start];
             {
@@ -276,27 +303,17 @@ template <bool STATES> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(c
             }
             long long sum = 0;                                       // STATES: the whole piece's decay
             bool sum_lost = false;
-            const void *mx = &A.map[A.x[job]], *my = &A.map[A.y[job]], *mz = &A.map[A.z[job]];
-            int it = 0;
-            for (; it < items; ++it) {
-                const int s = it & 1, chunk = J.reverse ? chunks - 1 - pos : pos, t0 = begin + chunk * C, valid = min(C, len - chunk * C);
-                Info &I = sh.info[s];
+            const float *const g_at = A.c.g;
+            const int fixed = A.c.fixed;
+            const float sc = J.sc, sw = J.sw;
+            for (int it = 0; it < items; ++it) {
+                const int chunk = reverse ? chunks - 1 - pos : pos, t0 = begin + chunk * C, valid = min(C, len - chunk * C);
+                Info &I = sh.info[it % INFOS];
                 float g[2];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int t = 2 * lane + u;
-                    g[u] = t < valid ? __ldg(A.c.g + (A.c.fixed ? (size_t)h : (size_t)(t0 + t) * H + h)) : 0.f;
-                }
-                if (it >= 2 && !wait(sh.empty[s], (it >> 1) - 1)) break;
-                if (lane == 0) {
-                    const uint32_t bar = smem_u32(&sh.full[s]), to = sm32 + s * STAGE;
-                    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"((uint32_t)(STATES ? 4 : 6) * A.rows * 128) : "memory");
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        if (!STATES) tma_load_3d(to + AT_X + u * ATOM, mx, 64 * u, h / J.x.share, t0, bar);
-                        tma_load_3d(to + AT_Y + u * ATOM, my, 64 * u, h / J.y.share, t0, bar);
-                        tma_load_3d(to + AT_Z + u * TILE, mz, 64 * u, h / J.z.share, t0, bar);
-                    }
+                    g[u] = t < valid ? __ldg(g_at + (fixed ? (size_t)h : (size_t)(t0 + t) * H + h)) : 0.f;
                 }
                 const long long d0 = decay_units(g[0]), d1 = decay_units(g[1]);
                 long long v = d0 + d1;
@@ -309,17 +326,19 @@ template <bool STATES> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(c
                 const unsigned bad0 = __ballot_sync(0xffffffffu, g[0] != g[0]), bad1 = __ballot_sync(0xffffffffu, g[1] != g[1]);
                 unsigned long long bad = 0;
                 if (bad0 | bad1)
+#pragma unroll 1
                     for (int i = 0; i < 32; ++i) bad |= (unsigned long long)((bad0 >> i & 1) | (bad1 >> i & 1) << 1) << (2 * i);
                 const float nan = __int_as_float(0x7fffffff);
+                if (it >= INFOS && !wait(sh.info_free[it % INFOS], it / INFOS - 1)) break;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int t = 2 * lane + u;
                     const long long vt = u ? v : v - d1;
                     const unsigned long long upto = ~0ull >> (63 - t);
                     const float up = bad & upto ? nan : exp2_units(vt), down = bad & ~upto ? nan : exp2_units(all - vt);
-                    I.g[t] = two_floats(vt);
-                    I.c[t] = J.sc * (J.reverse ? down : up);
-                    I.w[t] = J.sw * (J.reverse ? up : down);
+                    I.g[t] = two_floats(reverse ? -vt : vt);
+                    I.c[t] = sc * (reverse ? down : up);
+                    I.w[t] = sw * (reverse ? up : down);
                 }
                 sum += all;
                 sum_lost = sum_lost || bad;
@@ -335,7 +354,7 @@ template <bool STATES> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(c
                               (pos == 0 && chunks > items - it ? kOpen : 0);
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.full[s]));
+                if (lane == 0) mbar_arrive(smem_u32(&sh.info_full[it % INFOS]));
                 if (++pos == chunks) {
                     pos = 0;
                     if (++h == H) {
@@ -348,73 +367,116 @@ template <bool STATES> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(c
                     }
                 }
             }
-            // (after a wait that gave up: nothing may be on its way into shared memory when the CTA ends)
-            for (int k = max(0, it - 2); k < it; ++k)
-                for (uint32_t i = 0; i < kTries && !mbar_try_wait(smem_u32(&sh.full[k & 1]), (k >> 1) & 1); ++i) {}
             if (STATES && lane == 0) A.head[job * A.pieces + piece].keep = sum_lost ? __int_as_float(0x7fffffff) : exp2_units(sum);
         } else if (warp == 1) {
-            // ---------------- products ----------------
-            const bool one = lane == 0;
-            const int ka = (J.a + 15) / 16;
-            const uint32_t id_pt = idesc_bf16_f32(128, 64), id_o1 = idesc_bf16_f32(128, 64);
-            const uint32_t id_192 = idesc_bf16_f32(128, 192, false, true, true), id_128 = idesc_bf16_f32(128, 128, false, true, true);
-            auto scores = [&](int it) {
+            // ---------------- copies ----------------
+            const void *mx = &A.map[A.x[job]], *my = &A.map[A.y[job]], *mz = &A.map[A.z[job]];
+            const int sx = J.x.share, sy = J.y.share, sz = J.z.share;
+            const uint32_t bytes = (uint32_t)(STATES ? 4 : 6) * A.rows * 128;
+            int it = 0;
+            for (; it < items; ++it) {
                 const int s = it & 1;
-                if (!wait(sh.full[s], it >> 1) || (it > 0 && !wait(sh.pt_free, it - 1))) return false;
-                tc_fence_after();
-                if (one) {
-                    const uint32_t at = sm32 + s * STAGE;
-                    for (int k = 0; k < ka; ++k) {
-                        const uint32_t step = (k >> 2) * ATOM + (k & 3) * 32;
-                        mma_bf16(tm + PT, sdesc_kmajor_sw128(at + AT_Y + step), sdesc_kmajor_sw128(at + AT_X + step), id_pt, k > 0);
+                if (!wait(sh.info_full[it % INFOS], it / INFOS)) break;
+                const Info &I = sh.info[it % INFOS];
+                const int h = I.h, t0 = I.t0, hx = sx == 1 ? h : h / sx, hy = sy == 1 ? h : h / sy, hz = sz == 1 ? h : h / sz;
+                if (it >= 2 && !wait(sh.empty[s], (it >> 1) - 1)) break;
+                if (lane == 0) {
+                    const uint32_t bar = smem_u32(&sh.full[s]), to = sm32 + s * STAGE;
+                    mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        tma_load_3d(to + AT_Y + u * ATOM, my, 64 * u, hy, t0, bar);
+                        if (!STATES) tma_load_3d(to + AT_X + u * ATOM, mx, 64 * u, hx, t0, bar);
                     }
-                    mma_commit(smem_u32(&sh.pt_full));
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) tma_load_3d(to + AT_Z + u * TILE, mz, 64 * u, hz, t0, bar);
                 }
                 __syncwarp();
-                return true;
-            };
-            bool ok = STATES || scores(0);
-            for (int it = 0; ok && it < items; ++it) {
-                const int s = it & 1;
-                if (!wait(sh.prep_full, it) || (it > 0 && !wait(sh.acc_free, it - 1))) break;
-                if (STATES && !wait(sh.full[s], it >> 1)) break;
-                tc_fence_after();
-                if (one) {
-                    const uint32_t z = sm32 + s * STAGE + AT_Z;
-                    // the parts of less weight first
-#pragma unroll
-                    for (int u = 0; u < 3; ++u) {
-                        const int p = u == 0 ? 1 : u == 1 ? 2 : 0;
-                        const uint32_t ops = sm32 + AT_OPS + p * PART, id = STATES || p >= parts ? id_128 : id_192;
-#pragma unroll
-                        for (int k = 0; k < C / 16; ++k)
-                            mma_bf16(tm + ACC, sdesc_mnmajor_sw128(z + k * 2048, TILE), sdesc_mnmajor_sw128(ops + k * 2048, TILE), id, u + k > 0);
-                    }
-                    mma_commit(smem_u32(&sh.acc_full));
-                    mbar_arrive(smem_u32(&sh.acc_full));             // (what the preparing warps noted is passed on by a plain arrival)
-                    if (STATES) mma_commit(smem_u32(&sh.empty[s]));
-                }
-                __syncwarp();
-                if constexpr (!STATES) {
-                    if (it + 1 < items && !scores(it + 1)) break;
-                    if (!wait(sh.sop_full, it)) break;
+            }
+            // (after a wait that gave up: nothing may be on its way into shared memory when the CTA ends)
+            for (int k = max(0, it - 2); k < it; ++k)
+#pragma unroll 1
+    #pragma unroll 1
+            for (uint32_t i = 0; i < kTries && !mbar_try_wait(smem_u32(&sh.full[k & 1]), (k >> 1) & 1); ++i) {}
+        } else if (warp == 2) {
+            // ---------------- products: scores; the chunk's parts of the state and of the outputs ----------------
+            const bool wide_a = J.a > 64;
+            const uint32_t tu = uniform(tm), base = uniform(sm32);
+            for (int it = STATES ? 0 : -1; it < items; ++it) {
+                if (it >= 0) {
+                    const int s = it & 1;
+                    if (!wait(sh.prep_full, it) || (it > 0 && !wait(sh.acc_free, it - 1))) break;
+                    if (STATES && !wait(sh.full[s], it >> 1)) break;
                     tc_fence_after();
-                    if (one) {
-                        const uint32_t x = sm32 + s * STAGE + AT_X;
-                        for (int u = 0; u < parts; ++u) {
-                            const int p = u + 1 < parts ? u + 1 : 0;
-                            for (int k = 0; k < ka; ++k)
-                                mma_bf16_ta(tm + O1, tm + SOP + p * 64 + k * 8, sdesc_kmajor_sw128(x + (k >> 2) * ATOM + (k & 3) * 32), id_o1, u + k > 0);
+                    const uint32_t stage = uniform(base + s * STAGE);
+                    if (elect()) {
+                        constexpr uint32_t wide = idesc_bf16_f32(128, 192, false, true, true), narrow = idesc_bf16_f32(128, 128, false, true, true);
+                        const uint64_t z = sdesc_mnmajor_sw128(stage + AT_Z, TILE), ops = sdesc_mnmajor_sw128(base + AT_OPS, TILE);
+                        // parts 1, 2, 0: those of less weight first
+#pragma unroll
+                        for (int u = 0; u < 3; ++u) {
+                            const int p = u == 0 ? 1 : u == 1 ? 2 : 0;
+                            const uint32_t id = STATES || (p == 2 && !exact) ? narrow : wide;
+#pragma unroll
+                            for (int k = 0; k < C / 16; ++k) mma_bf16(tu + ACC, dadd(z, k * 2048), dadd(ops, p * PART + k * 2048), id, u + k > 0);
                         }
-                        mma_commit(smem_u32(&sh.o1_full));
+                        mma_commit(smem_u32(&sh.acc_full));
+                        mbar_arrive(smem_u32(&sh.acc_full));         // (what the preparing warps noted is passed on by a plain arrival)
                         mma_commit(smem_u32(&sh.empty[s]));
+                    }
+                    __syncwarp();
+                }
+                if (!STATES && it + 1 < items) {
+                    const int s = (it + 1) & 1;
+                    if (!wait(sh.full[s], (it + 1) >> 1) || (it >= 0 && !wait(sh.pt_free, it))) break;
+                    tc_fence_after();
+                    const uint32_t stage = uniform(base + s * STAGE);
+                    if (elect()) {
+                        const uint64_t y = sdesc_kmajor_sw128(stage + AT_Y), x = sdesc_kmajor_sw128(stage + AT_X);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+                            if (half == 0 || wide_a)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    mma_bf16(tu + PT, dadd(y, half * ATOM + k * 32), dadd(x, half * ATOM + k * 32), idesc_bf16_f32(128, 64), half + k > 0);
+                        mma_commit(smem_u32(&sh.pt_full));
                     }
                     __syncwarp();
                 }
             }
             // every product has ended before the CTA does
-            if (one) mma_commit(smem_u32(&sh.drain));
-            for (uint32_t i = 0; i < kTries && !mbar_try_wait(smem_u32(&sh.drain), 0); ++i) {}
+            if (elect()) mma_commit(smem_u32(&sh.drain[0]));
+#pragma unroll 1
+            for (uint32_t i = 0; i < kTries && !mbar_try_wait(smem_u32(&sh.drain[0]), 0); ++i) {}
+        } else if (!STATES) {
+            // ---------------- products: what the state gives ----------------
+            const bool wide_a = J.a > 64;
+            const uint32_t tu = uniform(tm), base = uniform(sm32);
+            for (int it = 0; it < items; ++it) {
+                const int s = it & 1;
+                if (!wait(sh.sop_full, it) || !wait(sh.full[s], it >> 1)) break;
+                tc_fence_after();
+                const uint32_t stage = uniform(base + s * STAGE);
+                if (elect()) {
+                    const uint64_t x = sdesc_kmajor_sw128(stage + AT_X);
+                    if (exact)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (k < 4 || wide_a) mma_bf16_ta(tu + O1, tu + SOP + 128 + k * 8, dadd(x, (k >> 2) * ATOM + (k & 3) * 32), idesc_bf16_f32(128, 64), k > 0);
+#pragma unroll
+                    for (int p = 1; p >= 0; --p)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (k < 4 || wide_a)
+                                mma_bf16_ta(tu + O1, tu + SOP + p * 64 + k * 8, dadd(x, (k >> 2) * ATOM + (k & 3) * 32), idesc_bf16_f32(128, 64), p == 0 || k > 0 || exact);
+                    mma_commit(smem_u32(&sh.o1_full));
+                    mma_commit(smem_u32(&sh.empty[s]));
+                }
+                __syncwarp();
+            }
+            if (elect()) mma_commit(smem_u32(&sh.drain[1]));
+#pragma unroll 1
+            for (uint32_t i = 0; i < kTries && !mbar_try_wait(smem_u32(&sh.drain[1]), 0); ++i) {}
         }
     } else if (warp < HOLD_WARP) {
         // ---------------- scores and keys as operands ----------------
@@ -426,34 +488,36 @@ template <bool STATES> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(c
         const int t = keys ? 32 * (kw & 1) + lane : 32 * quarter + lane;
         const int atom = (kw >> 1) & 1, c0 = STATES ? (kw >> 2) * 4 : 0, i0 = 32 * (pw >> 2);
         constexpr int PIECES = STATES ? 4 : 8;
+        const float sp = J.sp;
+        uint8_t *const row_at = sm + AT_OPS + (uint32_t)t * 128;
         for (int it = 0; it < items; ++it) {
             const int s = it & 1;
-            if (!wait(sh.full[s], it >> 1)) break;
-            Info &I = sh.info[s];
+            if (!wait(sh.info_full[it % INFOS], it / INFOS)) break;
+            Info &I = sh.info[it % INFOS];
             const int valid = I.valid;
-            uint8_t *const row_at = sm + AT_OPS + (uint32_t)t * 128;
             if (keys) {
-                // z: rows behind the sequence are put to 0, and what is not finite, which is noted
+                if (!wait(sh.full[s], it >> 1)) break;
+                // z: rows behind the sequence are put to 0, and what is not finite, which is noted.  (Piece c of row t lies at piece
+                // c ^ (t & 7): the lanes' rows, taken in that order, lie in different banks.)
                 uint8_t *const z = sm + s * STAGE + AT_Z + atom * TILE + (uint32_t)t * 128;
                 if (t >= valid) {
 #pragma unroll
-                    for (int c = 0; c < PIECES; ++c) *reinterpret_cast<uint4 *>(z + (c0 + c) * 16) = make_uint4(0, 0, 0, 0);
+                    for (int c = 0; c < PIECES; ++c) *reinterpret_cast<uint4 *>(z + ((c0 + c) ^ (t & 7)) * 16) = make_uint4(0, 0, 0, 0);
                 } else {
                     uint32_t most = 0;
 #pragma unroll
                     for (int c = 0; c < PIECES; ++c) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(z + (c0 + c) * 16);
+                        const uint4 v = *reinterpret_cast<const uint4 *>(z + ((c0 + c) ^ (t & 7)) * 16);
                         most = __vmaxu2(__vmaxu2(most, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
                         most = __vmaxu2(__vmaxu2(most, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
                     }
                     if ((most & 0xffffu) >= 0x7f80u || most >= 0x7f800000u) {
+#pragma unroll 1
                         for (int e = 0; e < PIECES * 8; ++e) {
-                            unsigned short *p = reinterpret_cast<unsigned short *>(z + c0 * 16) + e;
+                            unsigned short *p = reinterpret_cast<unsigned short *>(z + ((c0 + e / 8) ^ (t & 7)) * 16) + e % 8;
                             if ((*p & 0x7fffu) < 0x7f80u) continue;
                             *p = 0;
-                            // (piece c of row t lies at piece c ^ (t & 7))
-                            const int channel = atom * 64 + (((c0 + e / 8) ^ (t & 7)) * 8 + e % 8);
-                            atomicMin(&I.poison[channel], J.reverse ? C - 1 - t : t);
+                            atomicMin(&I.poison[atom * 64 + c0 * 8 + e], reverse ? C - 1 - t : t);
                             I.dirty = 1;
                         }
                     }
@@ -461,70 +525,72 @@ template <bool STATES> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(c
                 if (it > 0 && !wait(sh.acc_full, it - 1)) break;     // the operands' last reader
                 const uint8_t *const y = sm + s * STAGE + AT_Y + atom * ATOM + (uint32_t)t * 128;
                 uint8_t *const to = row_at + atom * TILE;
-                const float w = I.w[t];
-#pragma unroll
+                const bool in = t < valid;
+                const float w = in ? I.w[t] : 0.f;
+#pragma unroll 2
                 for (int c = 0; c < PIECES; ++c) {
-                    uint4 v = make_uint4(0, 0, 0, 0), p[3];
-                    if (t < valid) v = *reinterpret_cast<const uint4 *>(y + (c0 + c) * 16);
-                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                    const int at = ((c0 + c) ^ (t & 7)) * 16;
+                    uint4 v = *reinterpret_cast<const uint4 *>(y + at);
+                    if (!in) v = make_uint4(0, 0, 0, 0);
+                    const uint32_t in4[4] = {v.x, v.y, v.z, v.w};
                     uint32_t out[3][4];
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
-                        float a = low(in[u]) * w, b = high(in[u]) * w;
-                        if (t >= valid) a = b = 0.f;
+                        float a = low(in4[u]) * w, b = high(in4[u]) * w;
                         out[0][u] = peel(a, b);
                         out[1][u] = peel(a, b);
                         out[2][u] = pack(a, b);
                     }
 #pragma unroll
-                    for (int u = 0; u < 3; ++u) {
-                        p[u] = make_uint4(out[u][0], out[u][1], out[u][2], out[u][3]);
-                        *reinterpret_cast<uint4 *>(to + u * PART + (c0 + c) * 16) = p[u];
-                    }
+                    for (int u = 0; u < 3; ++u) *reinterpret_cast<uint4 *>(to + u * PART + at) = make_uint4(out[u][0], out[u][1], out[u][2], out[u][3]);
                 }
             } else {
                 if (!wait(sh.pt_full, it)) break;
                 tc_fence_after();
-                float p[32];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    uint32_t r[16];
-                    tmem_ld16(tm + ((uint32_t)quarter * 32 << 16) + PT + i0 + 16 * u, r);
+                if (it > 0 && !wait(sh.acc_full, it - 1)) break;
+                const float2 gj = I.g[t];
+                const unsigned long long lost = I.lost;
+                // columns that row t is seen by: from `from` up to `upto`
+                const int from = reverse ? 0 : t, upto = t >= valid ? 0 : reverse ? t + 1 : C;
+                uint8_t *const to = row_at + 2 * TILE;
+#pragma unroll 1
+                for (int i = i0; i < i0 + 32; i += 8) {
+                    uint32_t r[8];
+                    float p[8];
+                    tmem_ld8(tm + ((uint32_t)quarter * 32 << 16) + PT + i, r);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) p[16 * u + e] = __uint_as_float(r[e]);
+                    for (int e = 0; e < 8; e += 2) {
+                        const float4 gi = *reinterpret_cast<const float4 *>(&I.g[i + e]);       // of two columns
+                        p[e] = i + e >= from && i + e < upto ? sp * ex2((gi.x - gj.x) + (gi.y - gj.y)) * __uint_as_float(r[e]) : 0.f;
+                        p[e + 1] = i + e + 1 >= from && i + e + 1 < upto ? sp * ex2((gi.z - gj.x) + (gi.w - gj.y)) * __uint_as_float(r[e + 1]) : 0.f;
+                    }
+                    if (lost) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (i + e >= from && i + e < upto && ((~0ull >> (63 - i - e)) ^ (~0ull >> (63 - t))) & lost) p[e] = __int_as_float(0x7fffffff);
+                    }
+                    if (dots) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (i + e == t) {
+                                I.own[t] = p[e];
+                                p[e] = 0.f;
+                            }
+                    }
+                    const uint32_t at = (uint32_t)((i >> 3) ^ (t & 7)) * 16;
+#pragma unroll
+                    for (int u = 0; u < 3; ++u) {
+                        if (u == 2 && !exact) break;
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[e] = peel(p[2 * e], p[2 * e + 1]);
+                        *reinterpret_cast<uint4 *>(to + u * PART + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.pt_free));
-                const float2 gj = I.g[t];
-                const unsigned long long lost = I.lost;
-                const float sign = J.reverse ? -1.f : 1.f;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const int i = i0 + e;
-                    const float2 gi = I.g[i];
-                    float d = sign * ((gi.x - gj.x) + (gi.y - gj.y));
-                    if (lost && ((~0ull >> (63 - i)) ^ (~0ull >> (63 - t))) & lost) d = __int_as_float(0x7fffffff);
-                    const bool seen = (J.reverse ? t >= i : t <= i) && t < valid;
-                    p[e] = seen ? J.sp * ex2(d) * p[e] : 0.f;
-                    if (J.dots && i == t) {
-                        I.own[t] = p[e];
-                        p[e] = 0.f;
-                    }
-                }
-                if (it > 0 && !wait(sh.acc_full, it - 1)) break;
-                uint8_t *const to = row_at + 2 * TILE;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint32_t at = (uint32_t)(((i0 >> 3) + c) ^ (t & 7)) * 16;
-                    for (int u = 0; u < parts; ++u) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) w[e] = peel(p[8 * c + 2 * e], p[8 * c + 2 * e + 1]);
-                        *reinterpret_cast<uint4 *>(to + u * PART + at) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                }
             }
             fence_async_smem();
             __syncwarp();
@@ -535,207 +601,254 @@ template <bool STATES> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(c
         take_registers<REG_HOLD>();
         const int hw = warp - HOLD_WARP, half = hw >> 2, b = 32 * (warp & 3) + lane, a0 = 64 * half;
         const uint32_t lanes = tm + ((uint32_t)(warp & 3) * 32 << 16);
-        const bool in_b = b < J.b;
+        const int ja = J.a, jb = J.b, sa = J.sa, sb = J.sb;
+        const bool in_b = b < jb, out_bf16 = J.out_bf16;
+        const float *const first = J.first;
+        float *const last = J.last, *const anchors = FULL ? J.anchors : nullptr, *const dots_at = J.dots;
+        const bool last_anchor = J.last_anchor;
+        char *const out = static_cast<char *>(J.out);
+        const __nv_bfloat16 *const dot_rows = static_cast<const __nv_bfloat16 *>(J.r.p);
+        const int dot_share = dots ? J.r.share : 1;
         float S[64];
 #pragma unroll
         for (int i = 0; i < 64; ++i) S[i] = 0.f;
         float *const out_at = reinterpret_cast<float *>(sm + AT_OUT);
         float *const own_state = A.state + ((size_t)job * A.pieces + piece) * D * D;
-        bool ok = true;
-        // a warp that gives up still comes to the others' barriers, and touches nothing
-        auto give_up = [&] {
-            ok = false;
-            named_bar(1, HOLD);
-            if (!STATES) named_bar(1, HOLD);
-        };
-        for (int it = 0; it < items; ++it) {
-            const int s = it & 1;
-            if (!ok || !wait(sh.full[s], it >> 1)) {
-                give_up();
-                continue;
-            }
-            Info &I = sh.info[s];
-            const int flags = I.flags, n = I.n, h = I.h, t0 = I.t0, valid = I.valid, chunk = I.chunk;
-            const int slot = flags & (kFromFirst | kEnds) ? seq_slot(A.c.slot, A.c.num_slots, n) : 0;
-            const size_t state = ((size_t)max(slot, 0) * H + h) * J.a * J.b;
-            float *const kept = A.kept && (flags & kOpen) ? A.kept + ((size_t)job * A.pieces + piece) * D * D + b : nullptr;
-            if (!STATES && kept) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i) S[i] = kept[(size_t)(a0 + i) * D];
-            } else if (flags & kFromFirst) {
-                const float *from = J.first && slot >= 0 && in_b ? J.first + state + (size_t)b * J.sb : nullptr;
-                if (J.sa == 1) {
-#pragma unroll
-                    for (int i = 0; i < 64; i += 4) {
-                        const float4 v = from && a0 + i < J.a ? *reinterpret_cast<const float4 *>(from + a0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-                        S[i] = v.x;
-                        S[i + 1] = v.y;
-                        S[i + 2] = v.z;
-                        S[i + 3] = v.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) S[i] = from && a0 + i < J.a ? from[(size_t)(a0 + i) * J.sa] : 0.f;
-                }
-                if (STATES && kept)
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) kept[(size_t)(a0 + i) * D] = S[i];
-            } else if (flags & kFromPiece) {
+        // the state that chunk `it` begins with
+        auto enter = [&](const Info &I) {
+            const int flags = I.flags;
+            if (!(flags & (kFromFirst | kFromPiece))) return;
+            const int slot = seq_slot(A.c.slot, A.c.num_slots, I.n);
+            const size_t state = ((size_t)max(slot, 0) * H + I.h) * ja * jb;
+            // element a of it is at from[a * step]; nothing (zero) without one
+            const float *from = flags & kFromFirst ? (first && slot >= 0 && in_b ? first + state + (size_t)b * sb : nullptr)
+                                                   : (STATES ? nullptr : own_state - D * D + b);
+            int step = flags & kFromFirst ? sa : D;
+            if (A.kept && (flags & kOpen)) {
+                float *const kept = A.kept + ((size_t)job * A.pieces + piece) * D * D + b;
                 if (STATES) {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) S[i] = 0.f;
+#pragma unroll 4
+                    for (int i = a0; i < min(ja, a0 + 64); ++i) kept[(size_t)i * D] = from ? from[(size_t)i * step] : 0.f;
                 } else {
-                    const float *from = own_state - D * D + b;       // the state that the piece before this one leaves
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) S[i] = __ldg(from + (size_t)(a0 + i) * D);
+                    from = kept;
+                    step = D;
                 }
             }
-            auto dump = [&](float *to) {                             // [a][b] dense
-                if (in_b)
+            if (from) from += (size_t)a0 * step;
+            const int rows = from ? ja - a0 : 0;
 #pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (a0 + i < J.a) to[(size_t)(a0 + i) * J.b + b] = S[i];
-            };
-            if constexpr (!STATES) {
-                if (J.anchors && !J.reverse && chunk > 0 && chunk * C % kAnchor == 0)
-                    dump(J.anchors + ((size_t)(anchor_slot(t0 - chunk * C, n) + chunk * C / kAnchor - 1) * H + h) * J.a * J.b);
-                // S as an operand: a pair of columns a word
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t w[3][16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float x = S[32 * q + 2 * i], y = S[32 * q + 2 * i + 1];
-                        w[0][i] = peel(x, y);
-                        w[1][i] = peel(x, y);
-                        w[2][i] = pack(x, y);
-                    }
-                    tmem_st16(lanes + SOP + a0 / 2 + 16 * q, w[0]);
-                    tmem_st16(lanes + SOP + 64 + a0 / 2 + 16 * q, w[1]);
-                    if (parts == 3) tmem_st16(lanes + SOP + 128 + a0 / 2 + 16 * q, w[2]);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.sop_full));
+            for (int i = 0; i < 64; ++i) {
+                S[i] = i < rows ? *from : 0.f;
+                from += step;
             }
-            if (!wait(sh.acc_full, it)) {
-                give_up();
-                continue;
-            }
-            tc_fence_after();
-            const float keep = I.keep;
-            const bool dirty = I.dirty;
-            const int poison = dirty ? I.poison[b] : NONE;
+        };
+        // S as an operand: a pair of columns a word
+        auto hand_over = [&] {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                uint32_t r[16];
-                tmem_ld16(lanes + ACC + a0 + 16 * q, r);
-                tmem_wait_ld();
+                uint32_t w[3][8];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) S[16 * q + i] = fmaf(keep, S[16 * q + i], __uint_as_float(r[i]));
+                for (int i = 0; i < 8; ++i) {
+                    float x = S[16 * q + 2 * i], y = S[16 * q + 2 * i + 1];
+                    w[0][i] = peel(x, y);
+                    if (exact) {
+                        w[1][i] = peel(x, y);
+                        w[2][i] = pack(x, y);
+                    } else {
+                        w[1][i] = pack(x, y);
+                    }
+                }
+                tmem_st8(lanes + SOP + a0 / 2 + 8 * q, w[0]);
+                tmem_st8(lanes + SOP + 64 + a0 / 2 + 8 * q, w[1]);
+                if (exact) tmem_st8(lanes + SOP + 128 + a0 / 2 + 8 * q, w[2]);
             }
-            if (poison != NONE)
-#pragma unroll
-                for (int i = 0; i < 64; ++i) S[i] = __int_as_float(0x7fffffff);
-            if constexpr (STATES) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.acc_free));
-                named_bar(1, HOLD);                                  // (dirty has been read by all)
-                if (dirty) {
-                    I.poison[b] = NONE;
-                    I.dirty = 0;
-                    __syncwarp();
-                }
-                if (lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));
-            } else {
-                float o[32];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t r[16];
-                    tmem_ld16(lanes + ACC_O + 32 * half + 16 * q, r);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[16 * q + i] = __uint_as_float(r[i]);
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.acc_free));
-                if (!wait(sh.o1_full, it)) {
-                    give_up();
-                    continue;
-                }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.sop_full));
+        };
+        bool ok = true;
+        for (int it = -1; it < items; ++it) {                        // (-1: only the first state goes out)
+            const int s = it & 1;
+            Info &I = sh.info[it & (INFOS - 1)];
+            int flags = 0, n = 0, h = 0, t0 = 0, valid = 0, chunk = 0;
+            bool dirty = false;
+            float o[32];
+            if (it >= 0) ok = ok && wait(sh.acc_full, it);
+            if (ok && it >= 0) {
                 tc_fence_after();
+                flags = I.flags;
+                n = I.n;
+                h = I.h;
+                t0 = I.t0;
+                valid = I.valid;
+                chunk = I.chunk;
+                dirty = I.dirty;
+                const float keep = I.keep;
+                const int poison = dirty ? I.poison[b] : NONE;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t r[16];
-                    tmem_ld16(lanes + O1 + 32 * half + 16 * q, r);
+                for (int q = 0; q < 4; q += 2) {
+                    uint32_t r[16], v[16];
+                    tmem_ld16(lanes + ACC + a0 + 16 * q, r);
+                    tmem_ld16(lanes + ACC + a0 + 16 * q + 16, v);
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const int t = 32 * half + 16 * q + i;
-                        float v = fmaf(I.c[t], __uint_as_float(r[i]), o[16 * q + i]);
-                        if (poison != NONE && (J.reverse ? C - 1 - t : t) >= poison) v = __int_as_float(0x7fffffff);
-                        out_at[t * OUT_PITCH + b] = v;
+                        S[16 * q + i] = fmaf(keep, S[16 * q + i], __uint_as_float(r[i]));
+                        S[16 * q + 16 + i] = fmaf(keep, S[16 * q + 16 + i], __uint_as_float(v[i]));
+                    }
+                }
+                if (poison != NONE)
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) S[i] = __int_as_float(0x7fffffff);
+                if constexpr (!STATES) {
+                    uint32_t r[16], v[16];
+                    tmem_ld16(lanes + ACC_O + 32 * half, r);
+                    tmem_ld16(lanes + ACC_O + 32 * half + 16, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        o[i] = __uint_as_float(r[i]);
+                        o[16 + i] = __uint_as_float(v[i]);
                     }
                 }
                 tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&sh.acc_free));
+                    if (!dots) mbar_arrive(smem_u32(&sh.empty[s]));  // (with them z is read below)
+                }
+                if constexpr (!STATES) {
+                    ok = wait(sh.o1_full, it);
+                    if (ok) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t r[16];
+                            tmem_ld16(lanes + O1 + 32 * half + 16 * q, r);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; i += 4) {
+                                const float4 c = *reinterpret_cast<const float4 *>(&I.c[32 * half + 16 * q + i]);
+                                float *const v = o + 16 * q + i;
+                                v[0] = fmaf(c.x, __uint_as_float(r[i]), v[0]);
+                                v[1] = fmaf(c.y, __uint_as_float(r[i + 1]), v[1]);
+                                v[2] = fmaf(c.z, __uint_as_float(r[i + 2]), v[2]);
+                                v[3] = fmaf(c.w, __uint_as_float(r[i + 3]), v[3]);
+                            }
+                        }
+                        if (poison != NONE)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if ((reverse ? C - 1 - 32 * half - i : 32 * half + i) >= poison) o[i] = __int_as_float(0x7fffffff);
+                    }
+                }
+            }
+            if (ok) {
+                // where the state goes: to an anchor, to the caller, to the piece that goes on
+                const int behind = reverse ? chunk * C : chunk * C + valid, begin = t0 - chunk * C;
+                const bool at_anchor = anchors && it >= 0 && (reverse ? chunk > 0 && behind % kAnchor == 0 : (flags & kEnds) ? last_anchor : behind % kAnchor == 0);
+                const bool to_last = !STATES && (flags & kEnds) && last, to_piece = STATES && it == items - 1;       // (flags of -1: none)
+                if (at_anchor || to_last || to_piece) {
+#pragma unroll 1
+                    for (int k = 0; k < 2; ++k) {
+                        float *to = nullptr;
+                        int step = 0;
+                        if (k == 0 && at_anchor) {
+                            to = anchors + ((size_t)(anchor_slot(begin, n) + max(0, behind - 1) / kAnchor) * H + h) * ja * jb + b;
+                            step = jb;
+                        }
+                        if (k == 1 && to_last) {
+                            const int slot = seq_slot(A.c.slot, A.c.num_slots, n);
+                            if (slot >= 0) to = last + ((size_t)slot * H + h) * ja * jb + (size_t)b * sb;
+                            step = sa;
+                        }
+                        if (k == 1 && to_piece) {
+                            to = own_state + b;
+                            step = D;
+                        }
+                        if (!to || !(in_b || STATES)) continue;
+                        const int rows = (STATES ? D : ja) - a0;
+                        to += (size_t)a0 * step;
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) {
+                            if (i < rows) *to = S[i];
+                            to += step;
+                        }
+                    }
+                }
+                // the next chunk's state goes out before this one's rows: the products with it run meanwhile
+                if (it + 1 < items) {
+                    ok = wait(sh.info_full[(it + 1) % INFOS], (it + 1) / INFOS);
+                    if (ok) {
+                        enter(sh.info[(it + 1) % INFOS]);
+                        if (!STATES) hand_over();
+                    }
+                }
+            }
+            if (it < 0) continue;
+            // (a warp that has given up still comes to the others' barriers, and touches nothing)
+            named_bar(1, HOLD);                                      // the rows of the chunk before are read; all know what is dirty
+            if constexpr (!STATES) {
+                if (ok)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) out_at[(32 * half + i) * OUT_PITCH + b] = o[i];
                 named_bar(1, HOLD);
+            }
+            if (!ok) continue;
+            if constexpr (!STATES) {
                 // rows: 8 a warp, 4 channels a lane
                 const int c = 4 * lane;
-                const bool in_c = c < J.b;
-#pragma unroll 4
-                for (int u = 0; u < 8; ++u) {
-                    const int t = 8 * hw + u;
-                    if (t >= valid) break;
-                    float4 v = *reinterpret_cast<const float4 *>(out_at + t * OUT_PITCH + c);
-                    const size_t row = (size_t)(t0 + t) * H + h;
-                    if (J.dots) {
-                        float dot = 0.f;
-                        if (in_c) {
-                            const uint2 r = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(J.r.p) +
-                                                                                  ((size_t)(t0 + t) * (H / J.r.share) + h / J.r.share) * J.b + c));
-                            dot = fmaf(high(r.y), v.w, fmaf(low(r.y), v.z, fmaf(high(r.x), v.y, low(r.x) * v.x)));
+                const bool in_c = c < jb;
+#pragma unroll 1
+                for (int u0 = 0; u0 < 8; u0 += 4) {
+                    float4 v[4];
+                    uint2 r[4];
+                    const int t1 = 8 * hw + u0;
+                    if (dots)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            r[u] = make_uint2(0, 0);
+                            if (in_c && t1 + u < valid)
+                                r[u] = __ldg(reinterpret_cast<const uint2 *>(dot_rows + ((size_t)(t0 + t1 + u) * (H / dot_share) + h / dot_share) * jb + c));
+                        }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) v[u] = *reinterpret_cast<const float4 *>(out_at + (t1 + u) * OUT_PITCH + c);
+                    if (dots) {
+                        float dot[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int t = t1 + u;
+                            dot[u] = in_c ? fmaf(high(r[u].y), v[u].w, fmaf(low(r[u].y), v[u].z, fmaf(high(r[u].x), v[u].y, low(r[u].x) * v[u].x))) : 0.f;
                             // the term of the token itself
                             const uint2 z = *reinterpret_cast<const uint2 *>(sm + s * STAGE + AT_Z + (lane >> 4) * TILE + sw128_offset(t, c & 63));
                             const float p = I.own[t];
-                            v = make_float4(fmaf(p, low(z.x), v.x), fmaf(p, high(z.x), v.y), fmaf(p, low(z.y), v.z), fmaf(p, high(z.y), v.w));
+                            v[u] = make_float4(fmaf(p, low(z.x), v[u].x), fmaf(p, high(z.x), v[u].y), fmaf(p, low(z.y), v[u].z), fmaf(p, high(z.y), v[u].w));
                         }
-                        dot = warp_sum(dot);
-                        if (lane == 0) J.dots[row] = dot;
-                    }
-                    if (!in_c) continue;
-                    if (J.out_bf16) {
-                        __stcs(reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(J.out) + row * J.b + c), make_uint2(pack(v.x, v.y), pack(v.z, v.w)));
-                    } else {
-                        __stcs(reinterpret_cast<float4 *>(static_cast<float *>(J.out) + row * J.b + c), v);
-                    }
-                }
-                named_bar(1, HOLD);                                  // (the rows are read, and dirty by all)
-                if (dirty) {
-                    I.poison[b] = NONE;
-                    I.dirty = 0;
-                    __syncwarp();
-                }
-                if (lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));
-                if (J.anchors && J.reverse && chunk > 0 && chunk * C % kAnchor == 0)
-                    dump(J.anchors + ((size_t)(anchor_slot(t0 - chunk * C, n) + chunk * C / kAnchor - 1) * H + h) * J.a * J.b);
-                if (flags & kEnds) {
-                    if (J.anchors && J.last_anchor)
-                        dump(J.anchors + ((size_t)(anchor_slot(t0 - chunk * C, n) + max(0, chunk * C + valid - 1) / kAnchor) * H + h) * J.a * J.b);
-                    if (J.last && slot >= 0 && in_b) {
-                        float *to = J.last + state + (size_t)b * J.sb;
 #pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            if (a0 + i < J.a) to[(size_t)(a0 + i) * J.sa] = S[i];
+                        for (int q = 16; q; q >>= 1)
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], q);
+                        if (lane < 4 && t1 + lane < valid) dots_at[(size_t)(t0 + t1 + lane) * H + h] = lane == 0 ? dot[0] : lane == 1 ? dot[1] : lane == 2 ? dot[2] : dot[3];
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        if (!in_c || t1 + u >= valid) continue;
+                        const size_t at = ((size_t)(t0 + t1 + u) * H + h) * jb + c;
+                        if (out_bf16) __stcs(reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(out) + at), make_uint2(pack(v[u].x, v[u].y), pack(v[u].z, v[u].w)));
+                        else __stcs(reinterpret_cast<float4 *>(reinterpret_cast<float *>(out) + at), v[u]);
                     }
                 }
             }
-        }
-        if constexpr (STATES) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i) own_state[(size_t)(a0 + i) * D + b] = S[i];
+            if (dirty) {
+                I.poison[b] = NONE;
+                I.dirty = 0;
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&sh.info_free[it % INFOS]));
+                if (dots) mbar_arrive(smem_u32(&sh.empty[s]));
+            }
         }
     }
     tc_fence_before();
@@ -764,7 +877,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Head *head, float *stat
 }
 
 std::atomic<PFN_cuTensorMapEncodeTiled_v12000> g_encode{nullptr};
-std::atomic<uint64_t> g_attr_states{0}, g_attr_main{0};
+std::atomic<uint64_t> g_attr[3];
 
 // [T, heads, d] BF16 in boxes of 64 channels of one head and `rows` tokens; channels and tokens outside read 0.
 cudaError_t make_map(CUtensorMap *m, const void *base, int T, int heads, int d, int rows) {
@@ -796,8 +909,9 @@ cudaError_t launch_scan_tc(const Call &c, cudaStream_t s) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<true>, (int)SMEM, g_attr_states);
-    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<false>, (int)SMEM, g_attr_main);
+    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kStates>, (int)SMEM, g_attr[0]);
+    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kPlain>, (int)SMEM, g_attr[1]);
+    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kFull>, (int)SMEM, g_attr[2]);
     if (e != cudaSuccess) return e;
     TcArgs A{};
     A.c = c;
@@ -827,12 +941,15 @@ cudaError_t launch_scan_tc(const Call &c, cudaStream_t s) {
     const long long longest = c.T / C + 1;
     const bool cut = !(c.N == 1 && longest <= A.least && c.H <= A.pieces);
     if (cut) {
-        tc_kernel<true><<<A.pieces * c.jobs, THREADS, SMEM, s>>>(A);
+        tc_kernel<kStates><<<A.pieces * c.jobs, THREADS, SMEM, s>>>(A);
         count_launch();
         join_kernel<<<dim3(D * D / 1024, A.pieces, c.jobs), 256, 0, s>>>(A.head, A.state, A.pieces);
         count_launch();
     }
-    tc_kernel<false><<<A.pieces * c.jobs, THREADS, SMEM, s>>>(A);
+    bool plain = true;
+    for (int j = 0; j < c.jobs; ++j) plain = plain && !c.job[j].exact && !c.job[j].dots && !c.job[j].anchors;
+    if (plain) tc_kernel<kPlain><<<A.pieces * c.jobs, THREADS, SMEM, s>>>(A);
+    else tc_kernel<kFull><<<A.pieces * c.jobs, THREADS, SMEM, s>>>(A);
     count_launch();
     return cudaGetLastError();
 }
