@@ -28,11 +28,18 @@ __device__ __forceinline__ long long decay_units(float g) {
     const float e = fmaf(g, kLog2e, -p) + g * kRest;
     return __float2ll_rn(p * 4294967296.f) + __float2ll_rn(e * 4294967296.f);
 }
-__device__ __forceinline__ float exp2_units(long long v) { return exp2f((float)v * 2.3283064365386963e-10f); }
-// The sum as two floats whose pairwise differences keep FP32 accuracy.
+// The sum's whole and remaining powers of two, apart: differences of two such pairs keep an accuracy of 2^-24 however large the sums.
 __device__ __forceinline__ float2 two_floats(long long v) {
-    const float hi = (float)v;
-    return make_float2(hi * 2.3283064365386963e-10f, (float)(v - (long long)hi) * 2.3283064365386963e-10f);
+    return make_float2((float)(int)(v >> 32), (float)(unsigned)v * 2.3283064365386963e-10f);
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float exp2_units(long long v) {
+    const float2 f = two_floats(v);
+    return ex2(f.x) * ex2(f.y);
 }
 
 // Tokens between the anchors at which the gradient of the decays starts its sums anew (see lin_grad.cu).

@@ -4,13 +4,13 @@
 //     PT  = Y X^T                      scores, token j a row
 //     ACC = Z^T [Yw | P]               the chunk's part of S^T [b, a] and of out^T [b, i], in one product of N = 192
 //     O1  = S^T X^T                    what the state gives, S^T as an operand in tensor memory
-// so that z, x and y are operands just as the copies laid them down, S^T lives in the registers of 256 threads (a row a lane, two
+// so that z, x and y are operands just as the copies laid them down, S^T lives in the registers of 512 threads (a row a lane, four
 // threads a row) in FP32, and only the decayed scores P and keys Yw pass through shared memory, each as a sum of two or three BF16 numbers:
 // the inputs are exact, so a product of three parts is FP32's accuracy, of two 2^-17.
 //
 // Roles of a CTA, joined by mbarriers: a warp that walks the chunks and sums their decays, ahead of the others; a copy warp (TMA); an MMA
 // warp for PT and ACC and one for O1, so that neither chain waits for the other's operands; eight warps that prepare P and
-// Yw, eight that hold S, write its operand, fold ACC into it and put out rows.
+// Yw, sixteen that hold S, write its operand, fold ACC into it and put out rows.
 //
 // The chunks of all (sequence, head) pairs stand in one line, cut evenly over the CTAs ("pieces").  A piece that begins within a pair
 // needs the state there: a first pass (STATES) runs the pieces that end within a pair for their state alone, `join_kernel` chains
@@ -27,20 +27,27 @@ namespace {
 
 using namespace tc;
 
-constexpr int C = 64, D = 128, THREADS = 640, CTL = 128, PREP = 256, HOLD = 256;
+constexpr int C = 64, D = 128, CTL = 128, PREP = 256, HOLD = 512, THREADS = CTL + PREP + HOLD;
 constexpr int PREP_WARP = CTL / 32, HOLD_WARP = (CTL + PREP) / 32;
-// A CTA's registers at its launch are THREADS x 96; the roles' shares may not be more.
-constexpr int REG_CTL = 32, REG_PREP = 80, REG_HOLD = 144;
-static_assert(CTL * REG_CTL + PREP * REG_PREP + HOLD * REG_HOLD <= THREADS * 96, "shares of the registers");
+// A CTA's registers at its launch are THREADS x 72; the roles' shares may not be more.
+constexpr int REG_CTL = 40, REG_PREP = 72, REG_HOLD = 80;
+static_assert(CTL * REG_CTL + PREP * REG_PREP + HOLD * REG_HOLD <= THREADS * 72, "shares of the registers");
+constexpr int COLS = 32, TOKENS = 16;                              // of the state and of the outputs that one of the holding threads has
 constexpr uint32_t kTries = 1u << 20;            // a second or two
 
-// shared memory
+enum Kind { kStates, kPlain, kFull };      // states alone; jobs whose operands are in two parts and that put out nothing but BF16 rows; any
+
 constexpr uint32_t TILE = C * 128;                                 // 64 rows of 64 BF16 values
-constexpr uint32_t AT_Y = 0, AT_X = TILE, ATOM = 2 * TILE, AT_Z = 4 * TILE, STAGE = 6 * TILE;     // y0 x0 y1 x1 z0 z1
-constexpr uint32_t AT_OPS = 2 * STAGE, PART = 3 * TILE;            // three parts of [Yw0 | Yw1 | P]
-constexpr uint32_t AT_OUT = AT_OPS + 3 * PART;                     // FP32 [64][OUT_PITCH]
 constexpr int OUT_PITCH = D + 4;
-constexpr uint32_t AT_INFO = AT_OUT + C * OUT_PITCH * 4;
+// Shared memory: a ring of copies (y0 [x0] y1 [x1] z0 z1), parts of [Yw0 | Yw1 | P] (twice for the states, whose products then have no gap),
+// the rows on their way out (only where they are summed up for dots, or in FP32).
+template <Kind K> struct Map {
+    static constexpr bool X = K != kStates;
+    static constexpr int STAGES = K == kFull ? 2 : 3, SETS = K == kStates ? 2 : 1;
+    static constexpr uint32_t Y = 0, XT = TILE, ATOM = (X ? 2 : 1) * TILE, Z = 2 * ATOM, STAGE = Z + 2 * TILE;
+    static constexpr uint32_t OPS = STAGES * STAGE, PART = (X ? 3 : 2) * TILE, SET = K == kPlain ? 2 * PART + 2 * TILE : 3 * PART;
+    static constexpr uint32_t OUT = OPS + SETS * SET, INFO = OUT + (K == kFull ? C * OUT_PITCH * 4 : 0);
+};
 
 struct Info {                  // of one chunk
     float2 g[C];               // sums of the decays, as two floats; negative backward in time, so that d = g_i - g_j either way
@@ -57,17 +64,18 @@ enum { kFromFirst = 1, kFromPiece = 2, kEnds = 4, kOpen = 8 };        // kOpen: 
 
 struct Shared {
     Info info[INFOS];
-    unsigned long long info_full[INFOS], info_free[INFOS], full[2], empty[2], pt_full, pt_free, prep_full, acc_full, acc_free, sop_full, o1_full, drain[2];
+    unsigned long long info_full[INFOS], info_free[INFOS], full[3], empty[3], pt_full, pt_free, prep_full, acc_full[2], acc_free[2], sop_full, o1_full, drain[2];
     uint32_t tmem;
     int dead;
     long long part[THREADS / 32];
     int part_end[THREADS / 32];
     int n[2], h[2], pos[2], chunks[2], begin[2], len[2], floor[2];     // where the piece begins, and where it ends
 };
-constexpr uint32_t SMEM = AT_INFO + sizeof(Shared) + 1024;
+template <Kind K> constexpr uint32_t kSmem = Map<K>::INFO + sizeof(Shared) + 1024;
+static_assert(kSmem<kStates> <= 232448 && kSmem<kPlain> <= 232448 && kSmem<kFull> <= 232448, "shared memory");
 
 // tensor memory
-constexpr uint32_t PT = 0, ACC = 64, ACC_O = ACC + D, O1 = 256, SOP = 320;
+constexpr uint32_t PT = 0, ACC = 64, ACC_O = ACC + D, O1 = 256, SOP = 320, ACC_STEP = 192;     // (states: two sets of ACC)
 
 struct Head {                  // of a piece's state
     float keep;
@@ -89,11 +97,6 @@ struct TcArgs {
 template <int N> __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
@@ -144,15 +147,14 @@ struct Line {
     __device__ __forceinline__ int bound(int i) const { return min(max(cu[i], 0), T); }
 };
 
-// The kernels: states alone; jobs whose operands are in two parts and that put out nothing beside their rows; any.
-enum Kind { kStates, kPlain, kFull };
-
 template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(const __grid_constant__ TcArgs A) {
     constexpr bool STATES = KIND == kStates, FULL = KIND == kFull;
+    using M = Map<KIND>;
+    constexpr int STAGES = M::STAGES, SETS = M::SETS;
     extern __shared__ uint8_t raw[];
     uint8_t *const sm = smem_align1024(raw);
     const uint32_t sm32 = smem_u32(sm);
-    Shared &sh = *reinterpret_cast<Shared *>(sm + AT_INFO);
+    Shared &sh = *reinterpret_cast<Shared *>(sm + M::INFO);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int job = blockIdx.x / A.pieces, piece = blockIdx.x % A.pieces;
     const Job &J = A.c.job[job];
@@ -183,10 +185,14 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
     }
     if (lane == 31) sh.part_end[warp] = run_end;
     if (tid == 0) {
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&sh.full[s]), 1);
-            mbar_init(smem_u32(&sh.empty[s]), (STATES ? 1 : 2) + HOLD / 32);
+            mbar_init(smem_u32(&sh.empty[s]), (STATES ? 1 : 2) + (FULL && J.dots ? HOLD / 32 : 0));    // (with dots the rows' last step reads z)
+        }
+        for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&sh.drain[s]), 1);
+            mbar_init(smem_u32(&sh.acc_full[s]), 2);
+            mbar_init(smem_u32(&sh.acc_free[s]), HOLD / 32);
         }
         for (int i = 0; i < INFOS; ++i) {
             mbar_init(smem_u32(&sh.info_full[i]), 1);
@@ -196,8 +202,6 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
         mbar_init(smem_u32(&sh.pt_full), 1);
         mbar_init(smem_u32(&sh.pt_free), 4);
         mbar_init(smem_u32(&sh.prep_full), PREP / 32);
-        mbar_init(smem_u32(&sh.acc_full), 2);
-        mbar_init(smem_u32(&sh.acc_free), HOLD / 32);
         mbar_init(smem_u32(&sh.sop_full), HOLD / 32);
         mbar_init(smem_u32(&sh.o1_full), 1);
         fence_mbar_init();
@@ -329,7 +333,14 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
 #pragma unroll 1
                     for (int i = 0; i < 32; ++i) bad |= (unsigned long long)((bad0 >> i & 1) | (bad1 >> i & 1) << 1) << (2 * i);
                 const float nan = __int_as_float(0x7fffffff);
-                if (it >= INFOS && !wait(sh.info_free[it % INFOS], it / INFOS - 1)) break;
+                if (it >= INFOS) {
+                    if (!wait(sh.info_free[it % INFOS], it / INFOS - 1)) break;
+                    if (I.dirty) {
+                        for (int i = lane; i < D; i += 32) I.poison[i] = NONE;
+                        __syncwarp();
+                        I.dirty = 0;
+                    }
+                }
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int t = 2 * lane + u;
@@ -375,104 +386,112 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
             const uint32_t bytes = (uint32_t)(STATES ? 4 : 6) * A.rows * 128;
             int it = 0;
             for (; it < items; ++it) {
-                const int s = it & 1;
+                const int s = it % STAGES;
                 if (!wait(sh.info_full[it % INFOS], it / INFOS)) break;
                 const Info &I = sh.info[it % INFOS];
                 const int h = I.h, t0 = I.t0, hx = sx == 1 ? h : h / sx, hy = sy == 1 ? h : h / sy, hz = sz == 1 ? h : h / sz;
-                if (it >= 2 && !wait(sh.empty[s], (it >> 1) - 1)) break;
+                if (it >= STAGES && !wait(sh.empty[s], it / STAGES - 1)) break;
                 if (lane == 0) {
-                    const uint32_t bar = smem_u32(&sh.full[s]), to = sm32 + s * STAGE;
+                    const uint32_t bar = smem_u32(&sh.full[s]), to = sm32 + s * M::STAGE;
                     mbar_arrive_expect_tx(bar, bytes);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        tma_load_3d(to + AT_Y + u * ATOM, my, 64 * u, hy, t0, bar);
-                        if (!STATES) tma_load_3d(to + AT_X + u * ATOM, mx, 64 * u, hx, t0, bar);
+                        tma_load_3d(to + M::Y + u * M::ATOM, my, 64 * u, hy, t0, bar);
+                        if (!STATES) tma_load_3d(to + M::XT + u * M::ATOM, mx, 64 * u, hx, t0, bar);
                     }
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) tma_load_3d(to + AT_Z + u * TILE, mz, 64 * u, hz, t0, bar);
+                    for (int u = 0; u < 2; ++u) tma_load_3d(to + M::Z + u * TILE, mz, 64 * u, hz, t0, bar);
                 }
                 __syncwarp();
+                // the next chunk on its way to L2: its copy, once there is room for it, is then a short one
+                if (it + 1 < items) {
+                    if (!wait(sh.info_full[(it + 1) % INFOS], (it + 1) / INFOS)) break;
+                    const Info &F = sh.info[(it + 1) % INFOS];
+                    const int h = F.h, t0 = F.t0, hx = sx == 1 ? h : h / sx, hy = sy == 1 ? h : h / sy, hz = sz == 1 ? h : h / sz;
+                    if (lane < 2) {
+                        if (!STATES) tma_prefetch_3d(mx, 64 * lane, hx, t0);
+                        tma_prefetch_3d(my, 64 * lane, hy, t0);
+                        tma_prefetch_3d(mz, 64 * lane, hz, t0);
+                    }
+                    __syncwarp();
+                }
             }
             // (after a wait that gave up: nothing may be on its way into shared memory when the CTA ends)
-            for (int k = max(0, it - 2); k < it; ++k)
+            for (int k = max(0, it - STAGES); k < it; ++k)
 #pragma unroll 1
-    #pragma unroll 1
-            for (uint32_t i = 0; i < kTries && !mbar_try_wait(smem_u32(&sh.full[k & 1]), (k >> 1) & 1); ++i) {}
+                for (uint32_t i = 0; i < kTries && !mbar_try_wait(smem_u32(&sh.full[k % STAGES]), (k / STAGES) & 1); ++i) {}
         } else if (warp == 2) {
-            // ---------------- products: scores; the chunk's parts of the state and of the outputs ----------------
-            const bool wide_a = J.a > 64;
+            // ---------------- products: the chunk's parts of the state and of the outputs ----------------
             const uint32_t tu = uniform(tm), base = uniform(sm32);
-            for (int it = STATES ? 0 : -1; it < items; ++it) {
-                if (it >= 0) {
-                    const int s = it & 1;
-                    if (!wait(sh.prep_full, it) || (it > 0 && !wait(sh.acc_free, it - 1))) break;
-                    if (STATES && !wait(sh.full[s], it >> 1)) break;
-                    tc_fence_after();
-                    const uint32_t stage = uniform(base + s * STAGE);
-                    if (elect()) {
-                        constexpr uint32_t wide = idesc_bf16_f32(128, 192, false, true, true), narrow = idesc_bf16_f32(128, 128, false, true, true);
-                        const uint64_t z = sdesc_mnmajor_sw128(stage + AT_Z, TILE), ops = sdesc_mnmajor_sw128(base + AT_OPS, TILE);
-                        // parts 1, 2, 0: those of less weight first
+            for (int it = 0; it < items; ++it) {
+                const int s = it % STAGES, set = it % SETS;
+                if (!wait(sh.prep_full, it) || (it >= SETS && !wait(sh.acc_free[set], it / SETS - 1)) || !wait(sh.full[s], it / STAGES)) break;
+                tc_fence_after();
+                const uint32_t stage = uniform(base + s * M::STAGE), at = uniform(base + M::OPS + set * M::SET), to = uniform(tu + ACC + set * ACC_STEP);
+                if (elect()) {
+                    constexpr uint32_t wide = idesc_bf16_f32(128, 192, false, true, true), narrow = idesc_bf16_f32(128, 128, false, true, true);
+                    const uint64_t z = sdesc_mnmajor_sw128(stage + M::Z, TILE), ops = sdesc_mnmajor_sw128(at, TILE);
+                    // parts 1, 2, 0: those of less weight first
 #pragma unroll
-                        for (int u = 0; u < 3; ++u) {
-                            const int p = u == 0 ? 1 : u == 1 ? 2 : 0;
-                            const uint32_t id = STATES || (p == 2 && !exact) ? narrow : wide;
+                    for (int u = 0; u < 3; ++u) {
+                        const int p = u == 0 ? 1 : u == 1 ? 2 : 0;
+                        const uint32_t id = STATES || (p == 2 && !exact) ? narrow : wide;
 #pragma unroll
-                            for (int k = 0; k < C / 16; ++k) mma_bf16(tu + ACC, dadd(z, k * 2048), dadd(ops, p * PART + k * 2048), id, u + k > 0);
-                        }
-                        mma_commit(smem_u32(&sh.acc_full));
-                        mbar_arrive(smem_u32(&sh.acc_full));         // (what the preparing warps noted is passed on by a plain arrival)
-                        mma_commit(smem_u32(&sh.empty[s]));
+                        for (int k = 0; k < C / 16; ++k) mma_bf16(to, dadd(z, k * 2048), dadd(ops, p * M::PART + k * 2048), id, u + k > 0);
                     }
-                    __syncwarp();
+                    mma_commit(smem_u32(&sh.acc_full[set]));
+                    mbar_arrive(smem_u32(&sh.acc_full[set]));        // (what the preparing warps noted is passed on by a plain arrival)
+                    mma_commit(smem_u32(&sh.empty[s]));
                 }
-                if (!STATES && it + 1 < items) {
-                    const int s = (it + 1) & 1;
-                    if (!wait(sh.full[s], (it + 1) >> 1) || (it >= 0 && !wait(sh.pt_free, it))) break;
-                    tc_fence_after();
-                    const uint32_t stage = uniform(base + s * STAGE);
-                    if (elect()) {
-                        const uint64_t y = sdesc_kmajor_sw128(stage + AT_Y), x = sdesc_kmajor_sw128(stage + AT_X);
-#pragma unroll
-                        for (int half = 0; half < 2; ++half)
-                            if (half == 0 || wide_a)
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    mma_bf16(tu + PT, dadd(y, half * ATOM + k * 32), dadd(x, half * ATOM + k * 32), idesc_bf16_f32(128, 64), half + k > 0);
-                        mma_commit(smem_u32(&sh.pt_full));
-                    }
-                    __syncwarp();
-                }
+                __syncwarp();
             }
             // every product has ended before the CTA does
             if (elect()) mma_commit(smem_u32(&sh.drain[0]));
 #pragma unroll 1
             for (uint32_t i = 0; i < kTries && !mbar_try_wait(smem_u32(&sh.drain[0]), 0); ++i) {}
         } else if (!STATES) {
-            // ---------------- products: what the state gives ----------------
+            // ---------------- products: what the state gives; the next chunk's scores ----------------
             const bool wide_a = J.a > 64;
             const uint32_t tu = uniform(tm), base = uniform(sm32);
-            for (int it = 0; it < items; ++it) {
-                const int s = it & 1;
-                if (!wait(sh.sop_full, it) || !wait(sh.full[s], it >> 1)) break;
-                tc_fence_after();
-                const uint32_t stage = uniform(base + s * STAGE);
-                if (elect()) {
-                    const uint64_t x = sdesc_kmajor_sw128(stage + AT_X);
-                    if (exact)
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (k < 4 || wide_a) mma_bf16_ta(tu + O1, tu + SOP + 128 + k * 8, dadd(x, (k >> 2) * ATOM + (k & 3) * 32), idesc_bf16_f32(128, 64), k > 0);
-#pragma unroll
-                    for (int p = 1; p >= 0; --p)
+            constexpr uint32_t id = idesc_bf16_f32(128, 64);
+            for (int it = -1; it < items; ++it) {
+                if (it + 1 < items) {
+                    const int s = (it + 1) % STAGES;
+                    if (!wait(sh.full[s], (it + 1) / STAGES) || (it >= 0 && !wait(sh.pt_free, it))) break;
+                    tc_fence_after();
+                    const uint32_t stage = uniform(base + s * M::STAGE);
+                    if (elect()) {
+                        const uint64_t y = sdesc_kmajor_sw128(stage + M::Y), x = sdesc_kmajor_sw128(stage + M::XT);
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             if (k < 4 || wide_a)
-                                mma_bf16_ta(tu + O1, tu + SOP + p * 64 + k * 8, dadd(x, (k >> 2) * ATOM + (k & 3) * 32), idesc_bf16_f32(128, 64), p == 0 || k > 0 || exact);
-                    mma_commit(smem_u32(&sh.o1_full));
-                    mma_commit(smem_u32(&sh.empty[s]));
+                                mma_bf16(tu + PT, dadd(y, (k >> 2) * M::ATOM + (k & 3) * 32), dadd(x, (k >> 2) * M::ATOM + (k & 3) * 32), id, k > 0);
+                        mma_commit(smem_u32(&sh.pt_full));
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (it >= 0) {
+                    const int s = it % STAGES;
+                    if (!wait(sh.sop_full, it)) break;
+                    tc_fence_after();
+                    const uint32_t stage = uniform(base + s * M::STAGE);
+                    if (elect()) {
+                        const uint64_t x = sdesc_kmajor_sw128(stage + M::XT);
+                        if (exact)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                if (k < 4 || wide_a) mma_bf16_ta(tu + O1, tu + SOP + 128 + k * 8, dadd(x, (k >> 2) * M::ATOM + (k & 3) * 32), id, k > 0);
+#pragma unroll
+                        for (int p = 1; p >= 0; --p)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                if (k < 4 || wide_a)
+                                    mma_bf16_ta(tu + O1, tu + SOP + p * 64 + k * 8, dadd(x, (k >> 2) * M::ATOM + (k & 3) * 32), id, p == 0 || k > 0 || exact);
+                        mma_commit(smem_u32(&sh.o1_full));
+                        mma_commit(smem_u32(&sh.empty[s]));
+                    }
+                    __syncwarp();
+                }
             }
             if (elect()) mma_commit(smem_u32(&sh.drain[1]));
 #pragma unroll 1
@@ -480,40 +499,43 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
         }
     } else if (warp < HOLD_WARP) {
         // ---------------- scores and keys as operands ----------------
-        give_registers<REG_PREP>();
+        if (REG_PREP < 72) give_registers<REG_PREP>();
+        // Both operands are free once the chunk before has been summed.  Until then the scores are worked out into registers, and z is
+        // looked through; then all warps write, those with scores fewer of the keys.
         const int pw = warp - PREP_WARP, quarter = warp & 3;
         const bool keys = STATES || quarter >= 2;
-        // keys: row `t` of atom `atom`, pieces from `c0`; scores: row `t`, columns from `i0`
+        // keys: row `t` of atom `atom`, pieces c0 to c1; scores: row `t`, columns from `i0`, and the last pieces of a keys warp
         const int kw = STATES ? pw : (pw >> 2) * 2 + (quarter & 1);
-        const int t = keys ? 32 * (kw & 1) + lane : 32 * quarter + lane;
-        const int atom = (kw >> 1) & 1, c0 = STATES ? (kw >> 2) * 4 : 0, i0 = 32 * (pw >> 2);
-        constexpr int PIECES = STATES ? 4 : 8;
+        const int t = 32 * (kw & 1) + lane, atom = (kw >> 1) & 1, i0 = 32 * atom;
+        const int c0 = STATES ? (kw >> 2) * 4 : keys ? 0 : 5, c1 = STATES ? c0 + 4 : keys ? 5 : 8;
+        constexpr int SCAN = STATES ? 4 : 8;                         // pieces of z that a warp looks through
         const float sp = J.sp;
-        uint8_t *const row_at = sm + AT_OPS + (uint32_t)t * 128;
         for (int it = 0; it < items; ++it) {
-            const int s = it & 1;
+            const int s = it % STAGES, set = it % SETS;
+            uint8_t *const row_at = sm + M::OPS + set * M::SET + (uint32_t)t * 128, *const stage = sm + s * M::STAGE;
             if (!wait(sh.info_full[it % INFOS], it / INFOS)) break;
             Info &I = sh.info[it % INFOS];
             const int valid = I.valid;
+            uint32_t part[FULL ? 3 : 2][16];
             if (keys) {
-                if (!wait(sh.full[s], it >> 1)) break;
+                if (!wait(sh.full[s], it / STAGES)) break;
                 // z: rows behind the sequence are put to 0, and what is not finite, which is noted.  (Piece c of row t lies at piece
                 // c ^ (t & 7): the lanes' rows, taken in that order, lie in different banks.)
-                uint8_t *const z = sm + s * STAGE + AT_Z + atom * TILE + (uint32_t)t * 128;
+                uint8_t *const z = stage + M::Z + atom * TILE + (uint32_t)t * 128;
                 if (t >= valid) {
 #pragma unroll
-                    for (int c = 0; c < PIECES; ++c) *reinterpret_cast<uint4 *>(z + ((c0 + c) ^ (t & 7)) * 16) = make_uint4(0, 0, 0, 0);
+                    for (int c = 0; c < SCAN; ++c) *reinterpret_cast<uint4 *>(z + ((c0 + c) ^ (t & 7)) * 16) = make_uint4(0, 0, 0, 0);
                 } else {
                     uint32_t most = 0;
 #pragma unroll
-                    for (int c = 0; c < PIECES; ++c) {
+                    for (int c = 0; c < SCAN; ++c) {
                         const uint4 v = *reinterpret_cast<const uint4 *>(z + ((c0 + c) ^ (t & 7)) * 16);
                         most = __vmaxu2(__vmaxu2(most, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
                         most = __vmaxu2(__vmaxu2(most, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
                     }
                     if ((most & 0xffffu) >= 0x7f80u || most >= 0x7f800000u) {
 #pragma unroll 1
-                        for (int e = 0; e < PIECES * 8; ++e) {
+                        for (int e = 0; e < SCAN * 8; ++e) {
                             unsigned short *p = reinterpret_cast<unsigned short *>(z + ((c0 + e / 8) ^ (t & 7)) * 16) + e % 8;
                             if ((*p & 0x7fffu) < 0x7f80u) continue;
                             *p = 0;
@@ -522,75 +544,91 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                         }
                     }
                 }
-                if (it > 0 && !wait(sh.acc_full, it - 1)) break;     // the operands' last reader
-                const uint8_t *const y = sm + s * STAGE + AT_Y + atom * ATOM + (uint32_t)t * 128;
-                uint8_t *const to = row_at + atom * TILE;
-                const bool in = t < valid;
-                const float w = in ? I.w[t] : 0.f;
-#pragma unroll 2
-                for (int c = 0; c < PIECES; ++c) {
-                    const int at = ((c0 + c) ^ (t & 7)) * 16;
-                    uint4 v = *reinterpret_cast<const uint4 *>(y + at);
-                    if (!in) v = make_uint4(0, 0, 0, 0);
-                    const uint32_t in4[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t out[3][4];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        float a = low(in4[u]) * w, b = high(in4[u]) * w;
-                        out[0][u] = peel(a, b);
-                        out[1][u] = peel(a, b);
-                        out[2][u] = pack(a, b);
-                    }
-#pragma unroll
-                    for (int u = 0; u < 3; ++u) *reinterpret_cast<uint4 *>(to + u * PART + at) = make_uint4(out[u][0], out[u][1], out[u][2], out[u][3]);
-                }
-            } else {
-                if (!wait(sh.pt_full, it)) break;
+            } else if constexpr (!STATES) {
+                if (!wait(sh.full[s], it / STAGES) || !wait(sh.pt_full, it)) break;
                 tc_fence_after();
-                if (it > 0 && !wait(sh.acc_full, it - 1)) break;
                 const float2 gj = I.g[t];
                 const unsigned long long lost = I.lost;
-                // columns that row t is seen by: from `from` up to `upto`
-                const int from = reverse ? 0 : t, upto = t >= valid ? 0 : reverse ? t + 1 : C;
-                uint8_t *const to = row_at + 2 * TILE;
-#pragma unroll 1
-                for (int i = i0; i < i0 + 32; i += 8) {
+                // columns that row t is seen by, in the thread's 32: from `from` up to `upto`
+                const int from = reverse ? 0 : t - i0, upto = t >= valid ? 0 : reverse ? t - i0 + 1 : 32;
+#pragma unroll
+                for (int g = 0; g < 32; g += 8) {
                     uint32_t r[8];
                     float p[8];
-                    tmem_ld8(tm + ((uint32_t)quarter * 32 << 16) + PT + i, r);
+                    tmem_ld8(tm + ((uint32_t)quarter * 32 << 16) + PT + i0 + g, r);
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 8; e += 2) {
-                        const float4 gi = *reinterpret_cast<const float4 *>(&I.g[i + e]);       // of two columns
-                        p[e] = i + e >= from && i + e < upto ? sp * ex2((gi.x - gj.x) + (gi.y - gj.y)) * __uint_as_float(r[e]) : 0.f;
-                        p[e + 1] = i + e + 1 >= from && i + e + 1 < upto ? sp * ex2((gi.z - gj.x) + (gi.w - gj.y)) * __uint_as_float(r[e + 1]) : 0.f;
+                        const float4 gi = *reinterpret_cast<const float4 *>(&I.g[i0 + g + e]);      // of two columns
+                        p[e] = g + e >= from && g + e < upto ? sp * ex2((gi.x - gj.x) + (gi.y - gj.y)) * __uint_as_float(r[e]) : 0.f;
+                        p[e + 1] = g + e + 1 >= from && g + e + 1 < upto ? sp * ex2((gi.z - gj.x) + (gi.w - gj.y)) * __uint_as_float(r[e + 1]) : 0.f;
                     }
                     if (lost) {
+#pragma unroll 1
+                        for (int e = 0; e < 8; ++e) {
+                            const int i = i0 + g + e;
+                            if (g + e >= from && g + e < upto && ((~0ull >> (63 - i)) ^ (~0ull >> (63 - t))) & lost)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (i + e >= from && i + e < upto && ((~0ull >> (63 - i - e)) ^ (~0ull >> (63 - t))) & lost) p[e] = __int_as_float(0x7fffffff);
+                                for (int u = 0; u < 8; ++u)
+                                    if (u == e) p[u] = __int_as_float(0x7fffffff);
+                        }
                     }
-                    if (dots) {
+                    if (dots && i0 == 32 * quarter) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            if (i + e == t) {
+                            if (g + e == lane) {
                                 I.own[t] = p[e];
                                 p[e] = 0.f;
                             }
                     }
-                    const uint32_t at = (uint32_t)((i >> 3) ^ (t & 7)) * 16;
 #pragma unroll
-                    for (int u = 0; u < 3; ++u) {
-                        if (u == 2 && !exact) break;
-                        uint32_t w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) w[e] = peel(p[2 * e], p[2 * e + 1]);
-                        *reinterpret_cast<uint4 *>(to + u * PART + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int e = 0; e < 4; ++e) {
+                        part[0][g / 2 + e] = peel(p[2 * e], p[2 * e + 1]);
+                        if (exact) {
+                            part[1][g / 2 + e] = peel(p[2 * e], p[2 * e + 1]);
+                            if constexpr (FULL) part[2][g / 2 + e] = pack(p[2 * e], p[2 * e + 1]);
+                        } else {
+                            part[1][g / 2 + e] = pack(p[2 * e], p[2 * e + 1]);
+                        }
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.pt_free));
+            }
+            if (it >= SETS && !wait(sh.acc_full[set], it / SETS - 1)) break;      // the operands' last reader
+            if constexpr (!STATES)
+                if (!keys) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint8_t *const to = row_at + 2 * TILE + (uint32_t)(((i0 >> 3) + c) ^ (t & 7)) * 16;
+#pragma unroll
+                        for (int u = 0; u < (FULL ? 3 : 2); ++u) {
+                            if (u == 2 && !exact) break;
+                            *reinterpret_cast<uint4 *>(to + u * M::PART) = make_uint4(part[u][4 * c], part[u][4 * c + 1], part[u][4 * c + 2], part[u][4 * c + 3]);
+                        }
+                    }
+                }
+            const uint8_t *const y = stage + M::Y + atom * M::ATOM + (uint32_t)t * 128;
+            uint8_t *const to = row_at + atom * TILE;
+            const bool in = t < valid;
+            const float w = in ? I.w[t] : 0.f;
+#pragma unroll 1
+            for (int c = c0; c < c1; ++c) {
+                const int at = (c ^ (t & 7)) * 16;
+                uint4 v = *reinterpret_cast<const uint4 *>(y + at);
+                if (!in) v = make_uint4(0, 0, 0, 0);
+                const uint32_t in4[4] = {v.x, v.y, v.z, v.w};
+                uint32_t out[3][4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    float a = low(in4[u]) * w, b = high(in4[u]) * w;
+                    out[0][u] = peel(a, b);
+                    out[1][u] = peel(a, b);
+                    out[2][u] = pack(a, b);
+                }
+#pragma unroll
+                for (int u = 0; u < 3; ++u) *reinterpret_cast<uint4 *>(to + u * M::PART + at) = make_uint4(out[u][0], out[u][1], out[u][2], out[u][3]);
             }
             fence_async_smem();
             __syncwarp();
@@ -599,7 +637,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
     } else {
         // ---------------- the state, and what is put out ----------------
         take_registers<REG_HOLD>();
-        const int hw = warp - HOLD_WARP, half = hw >> 2, b = 32 * (warp & 3) + lane, a0 = 64 * half;
+        const int hw = warp - HOLD_WARP, part = hw >> 2, b = 32 * (warp & 3) + lane, a0 = COLS * part;
         const uint32_t lanes = tm + ((uint32_t)(warp & 3) * 32 << 16);
         const int ja = J.a, jb = J.b, sa = J.sa, sb = J.sb;
         const bool in_b = b < jb, out_bf16 = J.out_bf16;
@@ -609,10 +647,10 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
         char *const out = static_cast<char *>(J.out);
         const __nv_bfloat16 *const dot_rows = static_cast<const __nv_bfloat16 *>(J.r.p);
         const int dot_share = dots ? J.r.share : 1;
-        float S[64];
+        float S[COLS];
 #pragma unroll
-        for (int i = 0; i < 64; ++i) S[i] = 0.f;
-        float *const out_at = reinterpret_cast<float *>(sm + AT_OUT);
+        for (int i = 0; i < COLS; ++i) S[i] = 0.f;
+        float *const out_at = reinterpret_cast<float *>(sm + M::OUT);
         float *const own_state = A.state + ((size_t)job * A.pieces + piece) * D * D;
         // the state that chunk `it` begins with
         auto enter = [&](const Info &I) {
@@ -628,7 +666,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 float *const kept = A.kept + ((size_t)job * A.pieces + piece) * D * D + b;
                 if (STATES) {
 #pragma unroll 4
-                    for (int i = a0; i < min(ja, a0 + 64); ++i) kept[(size_t)i * D] = from ? from[(size_t)i * step] : 0.f;
+                    for (int i = a0; i < min(ja, a0 + COLS); ++i) kept[(size_t)i * D] = from ? from[(size_t)i * step] : 0.f;
                 } else {
                     from = kept;
                     step = D;
@@ -637,7 +675,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
             if (from) from += (size_t)a0 * step;
             const int rows = from ? ja - a0 : 0;
 #pragma unroll
-            for (int i = 0; i < 64; ++i) {
+            for (int i = 0; i < COLS; ++i) {
                 S[i] = i < rows ? *from : 0.f;
                 from += step;
             }
@@ -645,7 +683,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
         // S as an operand: a pair of columns a word
         auto hand_over = [&] {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < COLS / 16; ++q) {
                 uint32_t w[3][8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -669,12 +707,13 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
         };
         bool ok = true;
         for (int it = -1; it < items; ++it) {                        // (-1: only the first state goes out)
-            const int s = it & 1;
+            const int set = it & (SETS - 1);
+            const uint32_t acc = lanes + ACC + set * ACC_STEP;
             Info &I = sh.info[it & (INFOS - 1)];
             int flags = 0, n = 0, h = 0, t0 = 0, valid = 0, chunk = 0;
             bool dirty = false;
-            float o[32];
-            if (it >= 0) ok = ok && wait(sh.acc_full, it);
+            float o[TOKENS];
+            if (it >= 0) ok = ok && wait(sh.acc_full[set], it / SETS);
             if (ok && it >= 0) {
                 tc_fence_after();
                 flags = I.flags;
@@ -687,60 +726,45 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 const float keep = I.keep;
                 const int poison = dirty ? I.poison[b] : NONE;
 #pragma unroll
-                for (int q = 0; q < 4; q += 2) {
-                    uint32_t r[16], v[16];
-                    tmem_ld16(lanes + ACC + a0 + 16 * q, r);
-                    tmem_ld16(lanes + ACC + a0 + 16 * q + 16, v);
+                for (int q = 0; q < COLS / 16; ++q) {
+                    uint32_t r[16];
+                    tmem_ld16(acc + a0 + 16 * q, r);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        S[16 * q + i] = fmaf(keep, S[16 * q + i], __uint_as_float(r[i]));
-                        S[16 * q + 16 + i] = fmaf(keep, S[16 * q + 16 + i], __uint_as_float(v[i]));
-                    }
+                    for (int i = 0; i < 16; ++i) S[16 * q + i] = fmaf(keep, S[16 * q + i], __uint_as_float(r[i]));
                 }
                 if (poison != NONE)
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) S[i] = __int_as_float(0x7fffffff);
+                    for (int i = 0; i < COLS; ++i) S[i] = __int_as_float(0x7fffffff);
                 if constexpr (!STATES) {
-                    uint32_t r[16], v[16];
-                    tmem_ld16(lanes + ACC_O + 32 * half, r);
-                    tmem_ld16(lanes + ACC_O + 32 * half + 16, v);
+                    uint32_t r[16];
+                    tmem_ld16(lanes + ACC_O + TOKENS * part, r);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        o[i] = __uint_as_float(r[i]);
-                        o[16 + i] = __uint_as_float(v[i]);
-                    }
+                    for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(r[i]);
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&sh.acc_free));
-                    if (!dots) mbar_arrive(smem_u32(&sh.empty[s]));  // (with them z is read below)
-                }
+                if (lane == 0) mbar_arrive(smem_u32(&sh.acc_free[set]));
                 if constexpr (!STATES) {
                     ok = wait(sh.o1_full, it);
                     if (ok) {
                         tc_fence_after();
+                        uint32_t r[16];
+                        tmem_ld16(lanes + O1 + TOKENS * part, r);
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            uint32_t r[16];
-                            tmem_ld16(lanes + O1 + 32 * half + 16 * q, r);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 16; i += 4) {
-                                const float4 c = *reinterpret_cast<const float4 *>(&I.c[32 * half + 16 * q + i]);
-                                float *const v = o + 16 * q + i;
-                                v[0] = fmaf(c.x, __uint_as_float(r[i]), v[0]);
-                                v[1] = fmaf(c.y, __uint_as_float(r[i + 1]), v[1]);
-                                v[2] = fmaf(c.z, __uint_as_float(r[i + 2]), v[2]);
-                                v[3] = fmaf(c.w, __uint_as_float(r[i + 3]), v[3]);
-                            }
+                        for (int i = 0; i < 16; i += 4) {
+                            const float4 c = *reinterpret_cast<const float4 *>(&I.c[TOKENS * part + i]);
+                            o[i] = fmaf(c.x, __uint_as_float(r[i]), o[i]);
+                            o[i + 1] = fmaf(c.y, __uint_as_float(r[i + 1]), o[i + 1]);
+                            o[i + 2] = fmaf(c.z, __uint_as_float(r[i + 2]), o[i + 2]);
+                            o[i + 3] = fmaf(c.w, __uint_as_float(r[i + 3]), o[i + 3]);
                         }
                         if (poison != NONE)
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if ((reverse ? C - 1 - 32 * half - i : 32 * half + i) >= poison) o[i] = __int_as_float(0x7fffffff);
+                            for (int i = 0; i < TOKENS; ++i)
+                                if ((reverse ? C - 1 - TOKENS * part - i : TOKENS * part + i) >= poison) o[i] = __int_as_float(0x7fffffff);
                     }
                 }
             }
@@ -771,7 +795,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                         const int rows = (STATES ? D : ja) - a0;
                         to += (size_t)a0 * step;
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) {
+                        for (int i = 0; i < COLS; ++i) {
                             if (i < rows) *to = S[i];
                             to += step;
                         }
@@ -787,67 +811,77 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 }
             }
             if (it < 0) continue;
-            // (a warp that has given up still comes to the others' barriers, and touches nothing)
-            named_bar(1, HOLD);                                      // the rows of the chunk before are read; all know what is dirty
-            if constexpr (!STATES) {
+            if constexpr (STATES) {
+                __syncwarp();
+                if (ok && lane == 0) mbar_arrive(smem_u32(&sh.info_free[it % INFOS]));
+                if (!ok) break;
+            } else if constexpr (!FULL) {
+                // a channel a lane, a token a store: 64 bytes of a row a warp
+                if (!ok) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.info_free[it % INFOS]));     // (an arrival behind the stores would wait for them)
+                const int left = in_b ? valid - TOKENS * part : 0;
+                __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(out) + ((size_t)(t0 + TOKENS * part) * H + h) * jb + b;
+                const size_t step = (size_t)H * jb;
+#pragma unroll
+                for (int i = 0; i < TOKENS; ++i, to += step)
+                    if (i < left) *to = __float2bfloat16_rn(o[i]);
+            } else {
+                // (a warp that has given up still comes to the others' barriers, and touches nothing)
+                named_bar(1, HOLD);                                  // the rows of the chunk before are read
                 if (ok)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) out_at[(32 * half + i) * OUT_PITCH + b] = o[i];
+                    for (int i = 0; i < TOKENS; ++i) out_at[(TOKENS * part + i) * OUT_PITCH + b] = o[i];
                 named_bar(1, HOLD);
-            }
-            if (!ok) continue;
-            if constexpr (!STATES) {
-                // rows: 8 a warp, 4 channels a lane
-                const int c = 4 * lane;
+                if (!ok) continue;
+                // rows: 4 a warp, 4 channels a lane
+                const int s = it % STAGES, c = 4 * lane, t1 = 4 * hw;
                 const bool in_c = c < jb;
-#pragma unroll 1
-                for (int u0 = 0; u0 < 8; u0 += 4) {
-                    float4 v[4];
-                    uint2 r[4];
-                    const int t1 = 8 * hw + u0;
-                    if (dots)
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            r[u] = make_uint2(0, 0);
-                            if (in_c && t1 + u < valid)
-                                r[u] = __ldg(reinterpret_cast<const uint2 *>(dot_rows + ((size_t)(t0 + t1 + u) * (H / dot_share) + h / dot_share) * jb + c));
-                        }
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) v[u] = *reinterpret_cast<const float4 *>(out_at + (t1 + u) * OUT_PITCH + c);
-                    if (dots) {
-                        float dot[4];
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const int t = t1 + u;
-                            dot[u] = in_c ? fmaf(high(r[u].y), v[u].w, fmaf(low(r[u].y), v[u].z, fmaf(high(r[u].x), v[u].y, low(r[u].x) * v[u].x))) : 0.f;
-                            // the term of the token itself
-                            const uint2 z = *reinterpret_cast<const uint2 *>(sm + s * STAGE + AT_Z + (lane >> 4) * TILE + sw128_offset(t, c & 63));
-                            const float p = I.own[t];
-                            v[u] = make_float4(fmaf(p, low(z.x), v[u].x), fmaf(p, high(z.x), v[u].y), fmaf(p, low(z.y), v[u].z), fmaf(p, high(z.y), v[u].w));
-                        }
-#pragma unroll
-                        for (int q = 16; q; q >>= 1)
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], q);
-                        if (lane < 4 && t1 + lane < valid) dots_at[(size_t)(t0 + t1 + lane) * H + h] = lane == 0 ? dot[0] : lane == 1 ? dot[1] : lane == 2 ? dot[2] : dot[3];
-                    }
+                float4 v[4];
+                uint2 r[4];
+                if (dots)
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
-                        if (!in_c || t1 + u >= valid) continue;
-                        const size_t at = ((size_t)(t0 + t1 + u) * H + h) * jb + c;
-                        if (out_bf16) __stcs(reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(out) + at), make_uint2(pack(v[u].x, v[u].y), pack(v[u].z, v[u].w)));
-                        else __stcs(reinterpret_cast<float4 *>(reinterpret_cast<float *>(out) + at), v[u]);
+                        r[u] = make_uint2(0, 0);
+                        if (in_c && t1 + u < valid)
+                            r[u] = __ldg(reinterpret_cast<const uint2 *>(dot_rows + ((size_t)(t0 + t1 + u) * (H / dot_share) + h / dot_share) * jb + c));
+                    }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) v[u] = *reinterpret_cast<const float4 *>(out_at + (t1 + u) * OUT_PITCH + c);
+                float dot[4];
+                if (dots) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int t = t1 + u;
+                        dot[u] = in_c ? fmaf(high(r[u].y), v[u].w, fmaf(low(r[u].y), v[u].z, fmaf(high(r[u].x), v[u].y, low(r[u].x) * v[u].x))) : 0.f;
+                        // the term of the token itself
+                        const uint2 z = *reinterpret_cast<const uint2 *>(sm + s * M::STAGE + M::Z + (lane >> 4) * TILE + sw128_offset(t, c & 63));
+                        const float p = I.own[t];
+                        v[u] = make_float4(fmaf(p, low(z.x), v[u].x), fmaf(p, high(z.x), v[u].y), fmaf(p, low(z.y), v[u].z), fmaf(p, high(z.y), v[u].w));
                     }
                 }
-            }
-            if (dirty) {
-                I.poison[b] = NONE;
-                I.dirty = 0;
-            }
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(smem_u32(&sh.info_free[it % INFOS]));
-                if (dots) mbar_arrive(smem_u32(&sh.empty[s]));
+                // (an arrival behind the stores would wait for them)
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&sh.info_free[it % INFOS]));
+                    if (dots) mbar_arrive(smem_u32(&sh.empty[s]));
+                }
+                if (dots) {
+#pragma unroll
+                    for (int q = 16; q; q >>= 1)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], q);
+                    if (lane < 4 && t1 + lane < valid) dots_at[(size_t)(t0 + t1 + lane) * H + h] = lane == 0 ? dot[0] : lane == 1 ? dot[1] : lane == 2 ? dot[2] : dot[3];
+                }
+                const int left = in_c ? valid - t1 : 0;
+                char *to = out + (((size_t)(t0 + t1) * H + h) * jb + c) * (out_bf16 ? 2 : 4);
+                const size_t step = (size_t)H * jb * (out_bf16 ? 2 : 4);
+#pragma unroll
+                for (int u = 0; u < 4; ++u, to += step) {
+                    if (u >= left) continue;
+                    if (out_bf16) __stcs(reinterpret_cast<uint2 *>(to), make_uint2(pack(v[u].x, v[u].y), pack(v[u].z, v[u].w)));
+                    else __stcs(reinterpret_cast<float4 *>(to), v[u]);
+                }
             }
         }
     }
@@ -909,9 +943,9 @@ cudaError_t launch_scan_tc(const Call &c, cudaStream_t s) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kStates>, (int)SMEM, g_attr[0]);
-    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kPlain>, (int)SMEM, g_attr[1]);
-    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kFull>, (int)SMEM, g_attr[2]);
+    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kStates>, (int)kSmem<kStates>, g_attr[0]);
+    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kPlain>, (int)kSmem<kPlain>, g_attr[1]);
+    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kFull>, (int)kSmem<kFull>, g_attr[2]);
     if (e != cudaSuccess) return e;
     TcArgs A{};
     A.c = c;
@@ -941,15 +975,15 @@ cudaError_t launch_scan_tc(const Call &c, cudaStream_t s) {
     const long long longest = c.T / C + 1;
     const bool cut = !(c.N == 1 && longest <= A.least && c.H <= A.pieces);
     if (cut) {
-        tc_kernel<kStates><<<A.pieces * c.jobs, THREADS, SMEM, s>>>(A);
+        tc_kernel<kStates><<<A.pieces * c.jobs, THREADS, kSmem<kStates>, s>>>(A);
         count_launch();
         join_kernel<<<dim3(D * D / 1024, A.pieces, c.jobs), 256, 0, s>>>(A.head, A.state, A.pieces);
         count_launch();
     }
     bool plain = true;
-    for (int j = 0; j < c.jobs; ++j) plain = plain && !c.job[j].exact && !c.job[j].dots && !c.job[j].anchors;
-    if (plain) tc_kernel<kPlain><<<A.pieces * c.jobs, THREADS, SMEM, s>>>(A);
-    else tc_kernel<kFull><<<A.pieces * c.jobs, THREADS, SMEM, s>>>(A);
+    for (int j = 0; j < c.jobs; ++j) plain = plain && c.job[j].out_bf16 && !c.job[j].exact && !c.job[j].dots && !c.job[j].anchors;
+    if (plain) tc_kernel<kPlain><<<A.pieces * c.jobs, THREADS, kSmem<kPlain>, s>>>(A);
+    else tc_kernel<kFull><<<A.pieces * c.jobs, THREADS, kSmem<kFull>, s>>>(A);
     count_launch();
     return cudaGetLastError();
 }
