@@ -25,8 +25,8 @@ __device__ __forceinline__ long long decay_units(float g) {
     constexpr float kLog2e = 1.442695040888963f, kRest = 1.925963033500e-8f;       // log2(e) and what its FP32 value leaves
     const float p = g * kLog2e;
     if (!(fabsf(p) < 4096.f)) return p != p ? 0 : p < 0.f ? -(4096LL << 32) : 4096LL << 32;
-    const float e = fmaf(g, kLog2e, -p) + g * kRest;
-    return __float2ll_rn(p * 4294967296.f) + __float2ll_rn(e * 4294967296.f);
+    const float whole = rintf(p), rest = (p - whole) + (fmaf(g, kLog2e, -p) + g * kRest);        // |rest| < 0.51
+    return ((long long)(int)whole << 32) + 2LL * __float2int_rn(rest * 2147483648.f);
 }
 // The sum's whole and remaining powers of two, apart: differences of two such pairs keep an accuracy of 2^-24 however large the sums.
 __device__ __forceinline__ float2 two_floats(long long v) {
@@ -64,7 +64,7 @@ struct Job {
     int sa, sb;
     void *out;             // [T, H, b]
     int out_bf16;
-    int exact;             // operands of the tensor cores in three parts instead of two
+    int exact;             // operands of the tensor cores in three parts instead of two, of all jobs of a call if of one
     // for the gradient of the decays: dots[t, h] = sum_c r[t, c] (out[t, c] without the term j = i), and the states at the anchors
     Rows r;
     float *dots;           // [slices][T, H], or null

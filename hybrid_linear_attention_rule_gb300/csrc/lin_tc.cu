@@ -49,13 +49,15 @@ template <Kind K> struct Map {
     static constexpr uint32_t OUT = OPS + SETS * SET, INFO = OUT + (K == kFull ? C * OUT_PITCH * 4 : 0);
 };
 
-struct Info {                  // of one chunk
+struct alignas(16) Info {      // of one chunk; its arrays are read in 16-byte pieces
     float2 g[C];               // sums of the decays, as two floats; negative backward in time, so that d = g_i - g_j either way
     float c[C], w[C];
+    float fi[C], fj[C];        // D_ij = fi[i] fj[j], the scale in fj, where the chunk's decay leaves both in range (`plain`)
     float own[C];              // P's diagonal, where it is kept apart
     float keep;                // the chunk's decay
     unsigned long long lost;   // tokens whose decay is NaN
-    int n, h, t0, valid, chunk, flags;
+    int n, h, hk, t0, valid, chunk, flags;      // hk: h / group
+    int plain;
     int dirty;                 // some z is not finite:
     int poison[D];             // the channel's first such token in the job's direction
 };
@@ -87,6 +89,7 @@ struct TcArgs {
     Call c;
     int x[3], y[3], z[3];      // the jobs' maps
     int rows;                  // of a copy's box
+    int group;                 // value heads that share a key head
     int pieces;                // a job
     int least;                 // chunks of a piece, at least, where there are more pieces than pairs
     Head *head;                // [jobs][pieces]
@@ -119,23 +122,20 @@ __device__ __forceinline__ bool elect() {
 // The same value in all lanes, and known to be: the MMA warps' addresses stay in uniform registers, whose instructions take nothing else.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
+// A bounded wait of a whole warp, with the same answer for all its lanes; one that gives up ends the others' too.  (Short: the kernel's
+// loops have to stay in the instruction cache.)
 struct Waiter {
     volatile int *dead;
-    unsigned *status;
-    // (by a whole warp: the same answer for all its lanes)
     __device__ __forceinline__ bool operator()(const unsigned long long &bar, int parity) const {
-        const uint32_t at = smem_u32(&bar);
-        bool ok;
-        uint32_t i = 0;
+        const uint32_t at = smem_u32(&bar), odd = parity & 1;
+        uint32_t i = kTries;
 #pragma unroll 1
-        do ok = mbar_try_wait(at, parity & 1);
-        while (!ok && ++i < kTries && !*dead);
-        if (__all_sync(0xffffffffu, ok)) return true;
-        if (!ok && !*dead) {
-            *dead = 1;
-            atomicOr(status, 2u);
-        }
-        return false;
+        while (!__all_sync(0xffffffffu, mbar_try_wait(at, odd)))
+            if (__any_sync(0xffffffffu, --i == 0 || *dead)) {
+                *dead = 1;
+                return false;
+            }
+        return true;
     }
 };
 
@@ -159,7 +159,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
     const int job = blockIdx.x / A.pieces, piece = blockIdx.x % A.pieces;
     const Job &J = A.c.job[job];
     const int N = A.c.N, H = A.c.H;
-    const Waiter wait{&sh.dead, A.c.status};
+    const Waiter wait{&sh.dead};
 
     // ---- where the piece begins and ends
     const int per = (N + THREADS - 1) / THREADS, n0 = min(N, tid * per), n1 = min(N, n0 + per);
@@ -200,7 +200,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
             sh.info[i].dirty = 0;
         }
         mbar_init(smem_u32(&sh.pt_full), 1);
-        mbar_init(smem_u32(&sh.pt_free), 4);
+        mbar_init(smem_u32(&sh.pt_free), 3);
         mbar_init(smem_u32(&sh.prep_full), PREP / 32);
         mbar_init(smem_u32(&sh.sop_full), HOLD / 32);
         mbar_init(smem_u32(&sh.o1_full), 1);
@@ -293,7 +293,8 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
     tc_fence_after();
     const uint32_t tm = sh.tmem;
     // (in registers: read where they are used, they would be fetched anew from the parameters each time)
-    const bool reverse = J.reverse, dots = FULL && J.dots, exact = FULL && J.exact;
+    const bool reverse = J.reverse, dots = FULL && J.dots;
+    constexpr bool exact = FULL;
 
     if (warp < PREP_WARP) {
         give_registers<REG_CTL>();
@@ -305,11 +306,12 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 int b;
                 length(n, floor, b);
             }
+            int hk = h / A.group, left = A.group - (h - hk * A.group);       // left: heads that still share hk
             long long sum = 0;                                       // STATES: the whole piece's decay
             bool sum_lost = false;
             const float *const g_at = A.c.g;
             const int fixed = A.c.fixed;
-            const float sc = J.sc, sw = J.sw;
+            const float sc = J.sc, sw = J.sw, sp = J.sp;
             for (int it = 0; it < items; ++it) {
                 const int chunk = reverse ? chunks - 1 - pos : pos, t0 = begin + chunk * C, valid = min(C, len - chunk * C);
                 Info &I = sh.info[it % INFOS];
@@ -350,14 +352,22 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                     I.g[t] = two_floats(reverse ? -vt : vt);
                     I.c[t] = sc * (reverse ? down : up);
                     I.w[t] = sw * (reverse ? up : down);
+                    const float2 f = two_floats(reverse ? -vt : vt), b = two_floats(reverse ? vt : -vt);
+                    I.fi[t] = ex2(f.x) * ex2(f.y);
+                    I.fj[t] = sp * ex2(b.x) * ex2(b.y);
                 }
+                // (sums of up to 100 powers of two: neither factor leaves FP32's range, and their product is D's)
+                const long long far = max(llabs(v - d1), llabs(v));
+                const bool plain = __all_sync(0xffffffffu, far < (100LL << 32)) && !bad;
                 sum += all;
                 sum_lost = sum_lost || bad;
                 if (lane == 0) {
                     I.keep = bad ? nan : exp2_units(all);
+                    I.plain = plain;
                     I.lost = bad;
                     I.n = n;
                     I.h = h;
+                    I.hk = hk;
                     I.t0 = t0;
                     I.valid = valid;
                     I.chunk = chunk;
@@ -368,8 +378,12 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 if (lane == 0) mbar_arrive(smem_u32(&sh.info_full[it % INFOS]));
                 if (++pos == chunks) {
                     pos = 0;
+                    if (--left == 0) {
+                        left = A.group;
+                        ++hk;
+                    }
                     if (++h == H) {
-                        h = 0;
+                        h = hk = 0;
                         ++n;
                         if (it + 1 < items) {
                             len = length(n, floor, begin);
@@ -382,14 +396,14 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
         } else if (warp == 1) {
             // ---------------- copies ----------------
             const void *mx = &A.map[A.x[job]], *my = &A.map[A.y[job]], *mz = &A.map[A.z[job]];
-            const int sx = J.x.share, sy = J.y.share, sz = J.z.share;
+            const bool sx = J.x.share > 1, sy = J.y.share > 1, sz = J.z.share > 1;
             const uint32_t bytes = (uint32_t)(STATES ? 4 : 6) * A.rows * 128;
             int it = 0;
             for (; it < items; ++it) {
                 const int s = it % STAGES;
                 if (!wait(sh.info_full[it % INFOS], it / INFOS)) break;
                 const Info &I = sh.info[it % INFOS];
-                const int h = I.h, t0 = I.t0, hx = sx == 1 ? h : h / sx, hy = sy == 1 ? h : h / sy, hz = sz == 1 ? h : h / sz;
+                const int h = I.h, hk = I.hk, t0 = I.t0, hx = sx ? hk : h, hy = sy ? hk : h, hz = sz ? hk : h;
                 if (it >= STAGES && !wait(sh.empty[s], it / STAGES - 1)) break;
                 if (lane == 0) {
                     const uint32_t bar = smem_u32(&sh.full[s]), to = sm32 + s * M::STAGE;
@@ -407,7 +421,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 if (it + 1 < items) {
                     if (!wait(sh.info_full[(it + 1) % INFOS], (it + 1) / INFOS)) break;
                     const Info &F = sh.info[(it + 1) % INFOS];
-                    const int h = F.h, t0 = F.t0, hx = sx == 1 ? h : h / sx, hy = sy == 1 ? h : h / sy, hz = sz == 1 ? h : h / sz;
+                    const int h = F.h, hk = F.hk, t0 = F.t0, hx = sx ? hk : h, hy = sy ? hk : h, hz = sz ? hk : h;
                     if (lane < 2) {
                         if (!STATES) tma_prefetch_3d(mx, 64 * lane, hx, t0);
                         tma_prefetch_3d(my, 64 * lane, hy, t0);
@@ -500,19 +514,22 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
     } else if (warp < HOLD_WARP) {
         // ---------------- scores and keys as operands ----------------
         if (REG_PREP < 72) give_registers<REG_PREP>();
-        // Both operands are free once the chunk before has been summed.  Until then the scores are worked out into registers, and z is
-        // looked through; then all warps write, those with scores fewer of the keys.
+        // Both operands are free once the chunk before has been summed.  Until then the scores are worked out into registers (by three
+        // warps: one quarter of them is not seen and stays 0), and z is looked through by four; then all write.  The keys are 32 units of 32
+        // rows and 8 channels, shared out so that all warps end together.
         const int pw = warp - PREP_WARP, quarter = warp & 3;
         const bool keys = STATES || quarter >= 2;
-        // keys: row `t` of atom `atom`, pieces c0 to c1; scores: row `t`, columns from `i0`, and the last pieces of a keys warp
         const int kw = STATES ? pw : (pw >> 2) * 2 + (quarter & 1);
-        const int t = 32 * (kw & 1) + lane, atom = (kw >> 1) & 1, i0 = 32 * atom;
-        const int c0 = STATES ? (kw >> 2) * 4 : keys ? 0 : 5, c1 = STATES ? c0 + 4 : keys ? 5 : 8;
+        // z: row `t` of atom `atom`, pieces from c0; scores: row `t`, columns from `i0`
+        const int t = 32 * (kw & 1) + lane, atom = (kw >> 1) & 1, i0 = 32 * atom, c0 = STATES ? (kw >> 2) * 4 : 0;
+        const int unseen = reverse ? 1 : 2, block = 2 * (quarter & 1) + atom;            // (blocks: 2 row half + column half)
+        const bool zero = !keys && block == unseen;
+        const int u0 = STATES ? 4 * pw : keys ? 5 * kw : zero ? 26 : 20 + 2 * (block - (block > unseen)), u1 = u0 + (STATES ? 4 : keys ? 5 : zero ? 6 : 2);
         constexpr int SCAN = STATES ? 4 : 8;                         // pieces of z that a warp looks through
         const float sp = J.sp;
         for (int it = 0; it < items; ++it) {
             const int s = it % STAGES, set = it % SETS;
-            uint8_t *const row_at = sm + M::OPS + set * M::SET + (uint32_t)t * 128, *const stage = sm + s * M::STAGE;
+            uint8_t *const ops = sm + M::OPS + set * M::SET, *const row_at = ops + (uint32_t)t * 128, *const stage = sm + s * M::STAGE;
             if (!wait(sh.info_full[it % INFOS], it / INFOS)) break;
             Info &I = sh.info[it % INFOS];
             const int valid = I.valid;
@@ -523,11 +540,11 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 // c ^ (t & 7): the lanes' rows, taken in that order, lie in different banks.)
                 uint8_t *const z = stage + M::Z + atom * TILE + (uint32_t)t * 128;
                 if (t >= valid) {
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < SCAN; ++c) *reinterpret_cast<uint4 *>(z + ((c0 + c) ^ (t & 7)) * 16) = make_uint4(0, 0, 0, 0);
                 } else {
                     uint32_t most = 0;
-#pragma unroll
+#pragma unroll 2
                     for (int c = 0; c < SCAN; ++c) {
                         const uint4 v = *reinterpret_cast<const uint4 *>(z + ((c0 + c) ^ (t & 7)) * 16);
                         most = __vmaxu2(__vmaxu2(most, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
@@ -544,35 +561,46 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                         }
                     }
                 }
+            } else if (zero) {
+                if (!wait(sh.full[s], it / STAGES)) break;
+#pragma unroll
+                for (int u = 0; u < (FULL ? 3 : 2); ++u)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) part[u][e] = 0;
             } else if constexpr (!STATES) {
                 if (!wait(sh.full[s], it / STAGES) || !wait(sh.pt_full, it)) break;
                 tc_fence_after();
-                const float2 gj = I.g[t];
-                const unsigned long long lost = I.lost;
-                // columns that row t is seen by, in the thread's 32: from `from` up to `upto`
-                const int from = reverse ? 0 : t - i0, upto = t >= valid ? 0 : reverse ? t - i0 + 1 : 32;
+                // columns that row t is seen by, in the thread's 32, as bits
+                const uint32_t lower = 0xffffffffu >> (31 - lane), mask = t >= valid ? 0u : i0 != 32 * quarter ? 0xffffffffu : reverse ? lower : ~(lower >> 1);
+                const float fj = I.fj[t];
+                const bool plain = I.plain;
 #pragma unroll
                 for (int g = 0; g < 32; g += 8) {
                     uint32_t r[8];
                     float p[8];
                     tmem_ld8(tm + ((uint32_t)quarter * 32 << 16) + PT + i0 + g, r);
-                    tmem_wait_ld();
+                    if (plain) {
+                        *reinterpret_cast<float4 *>(p) = *reinterpret_cast<const float4 *>(&I.fi[i0 + g]);
+                        *reinterpret_cast<float4 *>(p + 4) = *reinterpret_cast<const float4 *>(&I.fi[i0 + g + 4]);
 #pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        const float4 gi = *reinterpret_cast<const float4 *>(&I.g[i0 + g + e]);      // of two columns
-                        p[e] = g + e >= from && g + e < upto ? sp * ex2((gi.x - gj.x) + (gi.y - gj.y)) * __uint_as_float(r[e]) : 0.f;
-                        p[e + 1] = g + e + 1 >= from && g + e + 1 < upto ? sp * ex2((gi.z - gj.x) + (gi.w - gj.y)) * __uint_as_float(r[e + 1]) : 0.f;
-                    }
-                    if (lost) {
+                        for (int e = 0; e < 8; ++e) p[e] *= fj;
+                    } else {
+                        const float2 gj = I.g[t];
+                        const unsigned long long lost = I.lost;
 #pragma unroll 1
                         for (int e = 0; e < 8; ++e) {
                             const int i = i0 + g + e;
-                            if (g + e >= from && g + e < upto && ((~0ull >> (63 - i)) ^ (~0ull >> (63 - t))) & lost)
+                            const float2 gi = I.g[i];
+                            const bool cut = ((~0ull >> (63 - i)) ^ (~0ull >> (63 - t))) & lost;
+                            const float v = cut ? __int_as_float(0x7fffffff) : sp * ex2((gi.x - gj.x) + (gi.y - gj.y));
 #pragma unroll
-                                for (int u = 0; u < 8; ++u)
-                                    if (u == e) p[u] = __int_as_float(0x7fffffff);
+                            for (int u = 0; u < 8; ++u)
+                                if (u == e) p[u] = v;
                         }
                     }
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) p[e] = mask >> (g + e) & 1 ? p[e] * __uint_as_float(r[e]) : 0.f;
                     if (dots && i0 == 32 * quarter) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
@@ -598,7 +626,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
             }
             if (it >= SETS && !wait(sh.acc_full[set], it / SETS - 1)) break;      // the operands' last reader
             if constexpr (!STATES)
-                if (!keys) {
+                if (!keys && !(zero && it > 0)) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint8_t *const to = row_at + 2 * TILE + (uint32_t)(((i0 >> 3) + c) ^ (t & 7)) * 16;
@@ -609,26 +637,26 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                         }
                     }
                 }
-            const uint8_t *const y = stage + M::Y + atom * M::ATOM + (uint32_t)t * 128;
-            uint8_t *const to = row_at + atom * TILE;
-            const bool in = t < valid;
-            const float w = in ? I.w[t] : 0.f;
 #pragma unroll 1
-            for (int c = c0; c < c1; ++c) {
-                const int at = (c ^ (t & 7)) * 16;
-                uint4 v = *reinterpret_cast<const uint4 *>(y + at);
-                if (!in) v = make_uint4(0, 0, 0, 0);
+            for (int u = u0; u < u1; ++u) {
+                const int row = 32 * (u >> 3 & 1) + lane, half = u >> 4, at = row * 128 + ((u & 7) ^ (row & 7)) * 16;
+                uint4 v = *reinterpret_cast<const uint4 *>(stage + M::Y + half * M::ATOM + at);
+                float w = I.w[row];
+                if (row >= valid) {
+                    v = make_uint4(0, 0, 0, 0);
+                    w = 0.f;
+                }
                 const uint32_t in4[4] = {v.x, v.y, v.z, v.w};
                 uint32_t out[3][4];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    float a = low(in4[u]) * w, b = high(in4[u]) * w;
-                    out[0][u] = peel(a, b);
-                    out[1][u] = peel(a, b);
-                    out[2][u] = pack(a, b);
+                for (int e = 0; e < 4; ++e) {
+                    float a = low(in4[e]) * w, b = high(in4[e]) * w;
+                    out[0][e] = peel(a, b);
+                    out[1][e] = peel(a, b);
+                    out[2][e] = pack(a, b);
                 }
 #pragma unroll
-                for (int u = 0; u < 3; ++u) *reinterpret_cast<uint4 *>(to + u * M::PART + at) = make_uint4(out[u][0], out[u][1], out[u][2], out[u][3]);
+                for (int e = 0; e < 3; ++e) *reinterpret_cast<uint4 *>(ops + half * TILE + e * M::PART + at) = make_uint4(out[e][0], out[e][1], out[e][2], out[e][3]);
             }
             fence_async_smem();
             __syncwarp();
@@ -887,6 +915,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
     }
     tc_fence_before();
     __syncthreads();
+    if (tid == 0 && sh.dead) atomicOr(A.c.status, 2u);
     if (warp == 0) {
         tc_fence_after();
         tmem_dealloc(tm, 512);
@@ -949,6 +978,10 @@ cudaError_t launch_scan_tc(const Call &c, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     TcArgs A{};
     A.c = c;
+    A.group = 1;
+    for (int j = 0; j < c.jobs; ++j)
+        for (const Rows *r : {&c.job[j].x, &c.job[j].y, &c.job[j].z})
+            if (r->share > A.group) A.group = r->share;
     A.rows = c.T < C ? (c.T < 1 ? 1 : c.T) : C;
     int maps = 0;
     const void *of[4] = {};
