@@ -49,6 +49,14 @@ template <Kind K> struct Map {
     static constexpr uint32_t OUT = OPS + SETS * SET, INFO = OUT + (K == kFull ? C * OUT_PITCH * 4 : 0);
 };
 
+struct Item {
+    int n, h, hk, t0, valid, chunk, flags;      // hk: h / group
+};
+struct Place {                 // a chunk on the way to its Info
+    float g[C];
+    Item item;
+};
+constexpr int AHEAD = 4, PLACES = 8;
 struct alignas(16) Info {      // of one chunk; its arrays are read in 16-byte pieces
     float2 g[C];               // sums of the decays, as two floats; negative backward in time, so that d = g_i - g_j either way
     float c[C], w[C];
@@ -56,7 +64,7 @@ struct alignas(16) Info {      // of one chunk; its arrays are read in 16-byte p
     float own[C];              // P's diagonal, where it is kept apart
     float keep;                // the chunk's decay
     unsigned long long lost;   // tokens whose decay is NaN
-    int n, h, hk, t0, valid, chunk, flags;      // hk: h / group
+    Item item;
     int plain;
     int dirty;                 // some z is not finite:
     int poison[D];             // the channel's first such token in the job's direction
@@ -66,6 +74,7 @@ enum { kFromFirst = 1, kFromPiece = 2, kEnds = 4, kOpen = 8 };        // kOpen: 
 
 struct Shared {
     Info info[INFOS];
+    Place place[PLACES];
     unsigned long long info_full[INFOS], info_free[INFOS], full[3], empty[3], pt_full, pt_free, prep_full, acc_full[2], acc_free[2], sop_full, o1_full, drain[2];
     uint32_t tmem;
     int dead;
@@ -312,15 +321,44 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
             const float *const g_at = A.c.g;
             const int fixed = A.c.fixed;
             const float sc = J.sc, sw = J.sw, sp = J.sp;
-            for (int it = 0; it < items; ++it) {
-                const int chunk = reverse ? chunks - 1 - pos : pos, t0 = begin + chunk * C, valid = min(C, len - chunk * C);
-                Info &I = sh.info[it % INFOS];
-                float g[2];
+            // (a chunk's decays are a word of every row of g: on their way while those of the chunks before are summed)
+            for (int it = -AHEAD; it < items; ++it) {
+                const int at = it + AHEAD;
+                if (at < items) {
+                    if (at > 0 && ++pos == chunks) {
+                        pos = 0;
+                        if (--left == 0) {
+                            left = A.group;
+                            ++hk;
+                        }
+                        if (++h == H) {
+                            h = hk = 0;
+                            ++n;
+                            len = length(n, floor, begin);
+                            chunks = max(1, (len + C - 1) / C);
+                        }
+                    }
+                    const int chunk = reverse ? chunks - 1 - pos : pos, t0 = begin + chunk * C, valid = min(C, len - chunk * C);
+                    Place &P = sh.place[at % PLACES];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int t = 2 * lane + u;
-                    g[u] = t < valid ? __ldg(g_at + (fixed ? (size_t)h : (size_t)(t0 + t) * H + h)) : 0.f;
+                    for (int u = 0; u < 2; ++u) {
+                        const int t = 2 * lane + u;
+                        const bool in = t < valid;
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&P.g[t])), "l"(g_at + (fixed ? (size_t)h : in ? (size_t)(t0 + t) * H + h : 0)),
+                                     "r"(in ? 4 : 0)
+                                     : "memory");
+                    }
+                    if (lane == 0)
+                        P.item = Item{n, h, hk, t0, valid, chunk, (pos == 0 ? kFromFirst : at == 0 ? kFromPiece : 0) | (pos == chunks - 1 ? kEnds : 0) |
+                                                                     (pos == 0 && chunks > items - at ? kOpen : 0)};
                 }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                if (it < 0) continue;
+                asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD) : "memory");
+                __syncwarp();
+                Info &I = sh.info[it % INFOS];
+                const Place &P = sh.place[it % PLACES];
+                const float g[2] = {P.g[2 * lane], P.g[2 * lane + 1]};
                 const long long d0 = decay_units(g[0]), d1 = decay_units(g[1]);
                 long long v = d0 + d1;
 #pragma unroll
@@ -348,13 +386,12 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                     const int t = 2 * lane + u;
                     const long long vt = u ? v : v - d1;
                     const unsigned long long upto = ~0ull >> (63 - t);
-                    const float up = bad & upto ? nan : exp2_units(vt), down = bad & ~upto ? nan : exp2_units(all - vt);
+                    const float grow = exp2_units(vt), up = bad & upto ? nan : grow, down = bad & ~upto ? nan : exp2_units(all - vt), shrink = exp2_units(-vt);
                     I.g[t] = two_floats(reverse ? -vt : vt);
                     I.c[t] = sc * (reverse ? down : up);
                     I.w[t] = sw * (reverse ? up : down);
-                    const float2 f = two_floats(reverse ? -vt : vt), b = two_floats(reverse ? vt : -vt);
-                    I.fi[t] = ex2(f.x) * ex2(f.y);
-                    I.fj[t] = sp * ex2(b.x) * ex2(b.y);
+                    I.fi[t] = reverse ? shrink : grow;
+                    I.fj[t] = sp * (reverse ? grow : shrink);
                 }
                 // (sums of up to 100 powers of two: neither factor leaves FP32's range, and their product is D's)
                 const long long far = max(llabs(v - d1), llabs(v));
@@ -365,32 +402,10 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                     I.keep = bad ? nan : exp2_units(all);
                     I.plain = plain;
                     I.lost = bad;
-                    I.n = n;
-                    I.h = h;
-                    I.hk = hk;
-                    I.t0 = t0;
-                    I.valid = valid;
-                    I.chunk = chunk;
-                    I.flags = (pos == 0 ? kFromFirst : it == 0 ? kFromPiece : 0) | (pos == chunks - 1 ? kEnds : 0) |
-                              (pos == 0 && chunks > items - it ? kOpen : 0);
+                    I.item = P.item;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.info_full[it % INFOS]));
-                if (++pos == chunks) {
-                    pos = 0;
-                    if (--left == 0) {
-                        left = A.group;
-                        ++hk;
-                    }
-                    if (++h == H) {
-                        h = hk = 0;
-                        ++n;
-                        if (it + 1 < items) {
-                            len = length(n, floor, begin);
-                            chunks = max(1, (len + C - 1) / C);
-                        }
-                    }
-                }
             }
             if (STATES && lane == 0) A.head[job * A.pieces + piece].keep = sum_lost ? __int_as_float(0x7fffffff) : exp2_units(sum);
         } else if (warp == 1) {
@@ -403,7 +418,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 const int s = it % STAGES;
                 if (!wait(sh.info_full[it % INFOS], it / INFOS)) break;
                 const Info &I = sh.info[it % INFOS];
-                const int h = I.h, hk = I.hk, t0 = I.t0, hx = sx ? hk : h, hy = sy ? hk : h, hz = sz ? hk : h;
+                const int h = I.item.h, hk = I.item.hk, t0 = I.item.t0, hx = sx ? hk : h, hy = sy ? hk : h, hz = sz ? hk : h;
                 if (it >= STAGES && !wait(sh.empty[s], it / STAGES - 1)) break;
                 if (lane == 0) {
                     const uint32_t bar = smem_u32(&sh.full[s]), to = sm32 + s * M::STAGE;
@@ -421,12 +436,8 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 if (it + 1 < items) {
                     if (!wait(sh.info_full[(it + 1) % INFOS], (it + 1) / INFOS)) break;
                     const Info &F = sh.info[(it + 1) % INFOS];
-                    const int h = F.h, hk = F.hk, t0 = F.t0, hx = sx ? hk : h, hy = sy ? hk : h, hz = sz ? hk : h;
-                    if (lane < 2) {
-                        if (!STATES) tma_prefetch_3d(mx, 64 * lane, hx, t0);
-                        tma_prefetch_3d(my, 64 * lane, hy, t0);
-                        tma_prefetch_3d(mz, 64 * lane, hz, t0);
-                    }
+                    const bool share = lane < 2 ? sy : lane < 4 ? sz : sx;
+                    if (lane < (STATES ? 4 : 6)) tma_prefetch_3d(lane < 2 ? my : lane < 4 ? mz : mx, 64 * (lane & 1), share ? F.item.hk : F.item.h, F.item.t0);
                     __syncwarp();
                 }
             }
@@ -532,7 +543,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
             uint8_t *const ops = sm + M::OPS + set * M::SET, *const row_at = ops + (uint32_t)t * 128, *const stage = sm + s * M::STAGE;
             if (!wait(sh.info_full[it % INFOS], it / INFOS)) break;
             Info &I = sh.info[it % INFOS];
-            const int valid = I.valid;
+            const int valid = I.item.valid;
             uint32_t part[FULL ? 3 : 2][16];
             if (keys) {
                 if (!wait(sh.full[s], it / STAGES)) break;
@@ -682,10 +693,10 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
         float *const own_state = A.state + ((size_t)job * A.pieces + piece) * D * D;
         // the state that chunk `it` begins with
         auto enter = [&](const Info &I) {
-            const int flags = I.flags;
+            const int flags = I.item.flags;
             if (!(flags & (kFromFirst | kFromPiece))) return;
-            const int slot = seq_slot(A.c.slot, A.c.num_slots, I.n);
-            const size_t state = ((size_t)max(slot, 0) * H + I.h) * ja * jb;
+            const int slot = seq_slot(A.c.slot, A.c.num_slots, I.item.n);
+            const size_t state = ((size_t)max(slot, 0) * H + I.item.h) * ja * jb;
             // element a of it is at from[a * step]; nothing (zero) without one
             const float *from = flags & kFromFirst ? (first && slot >= 0 && in_b ? first + state + (size_t)b * sb : nullptr)
                                                    : (STATES ? nullptr : own_state - D * D + b);
@@ -744,12 +755,12 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
             if (it >= 0) ok = ok && wait(sh.acc_full[set], it / SETS);
             if (ok && it >= 0) {
                 tc_fence_after();
-                flags = I.flags;
-                n = I.n;
-                h = I.h;
-                t0 = I.t0;
-                valid = I.valid;
-                chunk = I.chunk;
+                flags = I.item.flags;
+                n = I.item.n;
+                h = I.item.h;
+                t0 = I.item.t0;
+                valid = I.item.valid;
+                chunk = I.item.chunk;
                 dirty = I.dirty;
                 const float keep = I.keep;
                 const int poison = dirty ? I.poison[b] : NONE;
