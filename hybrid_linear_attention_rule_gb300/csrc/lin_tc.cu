@@ -372,10 +372,13 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 if (bad0 | bad1)
 #pragma unroll 1
                     for (int i = 0; i < 32; ++i) bad |= (unsigned long long)((bad0 >> i & 1) | (bad1 >> i & 1) << 1) << (2 * i);
-                const float nan = __int_as_float(0x7fffffff);
+                const float2 whole = two_floats(all);
+                const float sign = reverse ? -1.f : 1.f;
+                bool plain = true;
                 if (it >= INFOS) {
                     if (!wait(sh.info_free[it % INFOS], it / INFOS - 1)) break;
                     if (I.dirty) {
+#pragma unroll 1
                         for (int i = lane; i < D; i += 32) I.poison[i] = NONE;
                         __syncwarp();
                         I.dirty = 0;
@@ -384,22 +387,29 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int t = 2 * lane + u;
-                    const long long vt = u ? v : v - d1;
-                    const unsigned long long upto = ~0ull >> (63 - t);
-                    const float grow = exp2_units(vt), up = bad & upto ? nan : grow, down = bad & ~upto ? nan : exp2_units(all - vt), shrink = exp2_units(-vt);
-                    I.g[t] = two_floats(reverse ? -vt : vt);
+                    const float2 f = two_floats(u ? v : v - d1);
+                    const float up = ex2(f.x) * ex2(f.y), down = ex2(whole.x - f.x) * ex2(whole.y - f.y), inverse = ex2(-f.x) * ex2(-f.y);
+                    I.g[t] = make_float2(sign * f.x, sign * f.y);
                     I.c[t] = sc * (reverse ? down : up);
                     I.w[t] = sw * (reverse ? up : down);
-                    I.fi[t] = reverse ? shrink : grow;
-                    I.fj[t] = sp * (reverse ? grow : shrink);
+                    I.fi[t] = reverse ? inverse : up;
+                    I.fj[t] = sp * (reverse ? up : inverse);
+                    plain = plain && fabsf(f.x) < 100.f;
                 }
                 // (sums of up to 100 powers of two: neither factor leaves FP32's range, and their product is D's)
-                const long long far = max(llabs(v - d1), llabs(v));
-                const bool plain = __all_sync(0xffffffffu, far < (100LL << 32)) && !bad;
+                plain = __all_sync(0xffffffffu, plain) && !bad;
+                const float nan = __int_as_float(0x7fffffff);
+                if (bad)
+#pragma unroll 1
+                    for (int t = 2 * lane; t < 2 * lane + 2; ++t) {
+                        const unsigned long long upto = ~0ull >> (63 - t);
+                        if (bad & (reverse ? ~upto : upto)) I.c[t] = nan;
+                        if (bad & (reverse ? upto : ~upto)) I.w[t] = nan;
+                    }
                 sum += all;
                 sum_lost = sum_lost || bad;
                 if (lane == 0) {
-                    I.keep = bad ? nan : exp2_units(all);
+                    I.keep = bad ? nan : ex2(whole.x) * ex2(whole.y);
                     I.plain = plain;
                     I.lost = bad;
                     I.item = P.item;
@@ -418,26 +428,33 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 const int s = it % STAGES;
                 if (!wait(sh.info_full[it % INFOS], it / INFOS)) break;
                 const Info &I = sh.info[it % INFOS];
-                const int h = I.item.h, hk = I.item.hk, t0 = I.item.t0, hx = sx ? hk : h, hy = sy ? hk : h, hz = sz ? hk : h;
+                const int t0 = uniform(I.item.t0), h = uniform(I.item.h), hk = uniform(I.item.hk);
                 if (it >= STAGES && !wait(sh.empty[s], it / STAGES - 1)) break;
-                if (lane == 0) {
-                    const uint32_t bar = smem_u32(&sh.full[s]), to = sm32 + s * M::STAGE;
+                const uint32_t bar = uniform(smem_u32(&sh.full[s])), to = uniform(sm32 + s * M::STAGE);
+                if (elect()) {
                     mbar_arrive_expect_tx(bar, bytes);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        tma_load_3d(to + M::Y + u * M::ATOM, my, 64 * u, hy, t0, bar);
-                        if (!STATES) tma_load_3d(to + M::XT + u * M::ATOM, mx, 64 * u, hx, t0, bar);
+                        tma_load_3d(to + M::Y + u * M::ATOM, my, 64 * u, sy ? hk : h, t0, bar);
+                        if (!STATES) tma_load_3d(to + M::XT + u * M::ATOM, mx, 64 * u, sx ? hk : h, t0, bar);
                     }
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) tma_load_3d(to + M::Z + u * TILE, mz, 64 * u, hz, t0, bar);
+                    for (int u = 0; u < 2; ++u) tma_load_3d(to + M::Z + u * TILE, mz, 64 * u, sz ? hk : h, t0, bar);
                 }
                 __syncwarp();
                 // the next chunk on its way to L2: its copy, once there is room for it, is then a short one
                 if (it + 1 < items) {
                     if (!wait(sh.info_full[(it + 1) % INFOS], (it + 1) / INFOS)) break;
                     const Info &F = sh.info[(it + 1) % INFOS];
-                    const bool share = lane < 2 ? sy : lane < 4 ? sz : sx;
-                    if (lane < (STATES ? 4 : 6)) tma_prefetch_3d(lane < 2 ? my : lane < 4 ? mz : mx, 64 * (lane & 1), share ? F.item.hk : F.item.h, F.item.t0);
+                    const int t0 = uniform(F.item.t0), h = uniform(F.item.h), hk = uniform(F.item.hk);
+                    if (elect()) {
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            tma_prefetch_3d(my, 64 * u, sy ? hk : h, t0);
+                            if (!STATES) tma_prefetch_3d(mx, 64 * u, sx ? hk : h, t0);
+                            tma_prefetch_3d(mz, 64 * u, sz ? hk : h, t0);
+                        }
+                    }
                     __syncwarp();
                 }
             }
@@ -544,7 +561,6 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
             if (!wait(sh.info_full[it % INFOS], it / INFOS)) break;
             Info &I = sh.info[it % INFOS];
             const int valid = I.item.valid;
-            uint32_t part[FULL ? 3 : 2][16];
             if (keys) {
                 if (!wait(sh.full[s], it / STAGES)) break;
                 // z: rows behind the sequence are put to 0, and what is not finite, which is noted.  (Piece c of row t lies at piece
@@ -572,13 +588,15 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                         }
                     }
                 }
+                if (it >= SETS && !wait(sh.acc_full[set], it / SETS - 1)) break;      // the operands' last reader
             } else if (zero) {
-                if (!wait(sh.full[s], it / STAGES)) break;
-#pragma unroll
-                for (int u = 0; u < (FULL ? 3 : 2); ++u)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) part[u][e] = 0;
+                if (!wait(sh.full[s], it / STAGES) || (it >= SETS && !wait(sh.acc_full[set], it / SETS - 1))) break;
+                if (it == 0)
+#pragma unroll 1
+                    for (int c = 0; c < 12; ++c)
+                        if (c < (FULL ? 12 : 8)) *reinterpret_cast<uint4 *>(row_at + 2 * TILE + (c >> 2) * M::PART + (((i0 >> 3) + (c & 3)) ^ (t & 7)) * 16) = make_uint4(0, 0, 0, 0);
             } else if constexpr (!STATES) {
+                uint32_t part[FULL ? 3 : 2][16];
                 if (!wait(sh.full[s], it / STAGES) || !wait(sh.pt_full, it)) break;
                 tc_fence_after();
                 // columns that row t is seen by, in the thread's 32, as bits
@@ -634,20 +652,14 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.pt_free));
-            }
-            if (it >= SETS && !wait(sh.acc_full[set], it / SETS - 1)) break;      // the operands' last reader
-            if constexpr (!STATES)
-                if (!keys && !(zero && it > 0)) {
+                if (it >= SETS && !wait(sh.acc_full[set], it / SETS - 1)) break;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint8_t *const to = row_at + 2 * TILE + (uint32_t)(((i0 >> 3) + c) ^ (t & 7)) * 16;
+                for (int c = 0; c < 4; ++c) {
+                    uint8_t *const to = row_at + 2 * TILE + (uint32_t)(((i0 >> 3) + c) ^ (t & 7)) * 16;
 #pragma unroll
-                        for (int u = 0; u < (FULL ? 3 : 2); ++u) {
-                            if (u == 2 && !exact) break;
-                            *reinterpret_cast<uint4 *>(to + u * M::PART) = make_uint4(part[u][4 * c], part[u][4 * c + 1], part[u][4 * c + 2], part[u][4 * c + 3]);
-                        }
-                    }
+                    for (int u = 0; u < (FULL ? 3 : 2); ++u) *reinterpret_cast<uint4 *>(to + u * M::PART) = make_uint4(part[u][4 * c], part[u][4 * c + 1], part[u][4 * c + 2], part[u][4 * c + 3]);
                 }
+            }
 #pragma unroll 1
             for (int u = u0; u < u1; ++u) {
                 const int row = 32 * (u >> 3 & 1) + lane, half = u >> 4, at = row * 128 + ((u & 7) ^ (row & 7)) * 16;
@@ -686,6 +698,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
         char *const out = static_cast<char *>(J.out);
         const __nv_bfloat16 *const dot_rows = static_cast<const __nv_bfloat16 *>(J.r.p);
         const int dot_share = dots ? J.r.share : 1;
+        const uint32_t row_step = (uint32_t)H * jb * 2;
         float S[COLS];
 #pragma unroll
         for (int i = 0; i < COLS; ++i) S[i] = 0.f;
@@ -859,12 +872,19 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 if (!ok) break;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.info_free[it % INFOS]));     // (an arrival behind the stores would wait for them)
-                const int left = in_b ? valid - TOKENS * part : 0;
-                __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(out) + ((size_t)(t0 + TOKENS * part) * H + h) * jb + b;
-                const size_t step = (size_t)H * jb;
+                // (one address for the warp and 32-bit offsets: short code)
+                const size_t first_row = ((size_t)(t0 + TOKENS * part) * H + h) * jb * 2;
+                char *const rows = out + ((unsigned long long)uniform((uint32_t)(first_row >> 32)) << 32 | uniform((uint32_t)first_row));
+                uint32_t at = 2 * b;
+                if (valid == C && jb == D) {
 #pragma unroll
-                for (int i = 0; i < TOKENS; ++i, to += step)
-                    if (i < left) *to = __float2bfloat16_rn(o[i]);
+                    for (int i = 0; i < TOKENS; ++i, at += row_step) *reinterpret_cast<__nv_bfloat16 *>(rows + at) = __float2bfloat16_rn(o[i]);
+                } else {
+                    const int left = in_b ? valid - TOKENS * part : 0;
+#pragma unroll
+                    for (int i = 0; i < TOKENS; ++i, at += row_step)
+                        if (i < left) *reinterpret_cast<__nv_bfloat16 *>(rows + at) = __float2bfloat16_rn(o[i]);
+                }
             } else {
                 // (a warp that has given up still comes to the others' barriers, and touches nothing)
                 named_bar(1, HOLD);                                  // the rows of the chunk before are read
