@@ -64,7 +64,7 @@ struct Job {
     int sa, sb;
     void *out;             // [T, H, b]
     int out_bf16;
-    int exact;             // operands of the tensor cores in three parts instead of two, of all jobs of a call if of one
+    int exact;             // operands of the tensor cores in three parts instead of two (of all jobs of a call if of one)
     // for the gradient of the decays: dots[t, h] = sum_c r[t, c] (out[t, c] without the term j = i), and the states at the anchors
     Rows r;
     float *dots;           // [slices][T, H], or null
@@ -91,7 +91,7 @@ constexpr int kSlice = 32;
 inline int slices(int b) { return (b + kSlice - 1) / kSlice; }
 
 cudaError_t launch_scan_f32(const Call &c, cudaStream_t s);
-// The tensor-core path (lin_tc.cu): BF16, T > 0; dots has one row.
+// The tensor-core path (lin_tc.cu): BF16, T > 0; dots has a row for each 32 channels too (four, whatever the width).
 size_t tc_workspace();
 cudaError_t launch_scan_tc(const Call &c, cudaStream_t s);
 

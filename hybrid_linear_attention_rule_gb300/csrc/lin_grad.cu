@@ -172,8 +172,8 @@ struct Space {
         pieces = take(bf16 ? tc_workspace() : 0);
         r1 = r2 = S = R = f = dg = pq = pk = at;
         if (backward) {
-            r1 = take(TH * slices(dk) * 4);
-            r2 = take(TH * slices(dv) * 4);
+            r1 = take(TH * (bf16 ? 4 : slices(dk)) * 4);
+            r2 = take(TH * (bf16 ? 4 : slices(dv)) * 4);
             S = take(slots * H * dk * dv * 4);
             R = take(slots * H * dk * dv * 4);
             f = take(slots * H * 8);
@@ -297,6 +297,14 @@ cudaError_t launch_lin_backward(const LinArgs &a, const void *dO, const float *d
         jv.anchors = part(w.R);
         jv.exact = 1;
     }
+    // dk by itself where the others need more: its rows are all that it puts out
+    if (dg && on_tensor_cores(c)) {
+        Call k = c;
+        k.jobs = 1;
+        k.job[0] = jk;
+        c.jobs = 2;
+        if (cudaError_t e = launch_scan(k, s)) return e;
+    }
     if (cudaError_t e = launch_scan(c, s)) return e;
     const unsigned seqs = (unsigned)(a.N < 1024 ? a.N : 1024);
     if (dg) {
@@ -306,7 +314,7 @@ cudaError_t launch_lin_backward(const LinArgs &a, const void *dO, const float *d
         anchor_kernel<<<dim3(seqs, a.H, deep), 256, 0, s>>>(g);
         count_launch();
         float *to = a.fixed ? part(w.dg) : dg;
-        const SumArgs u{part(w.r1), part(w.r2), on_tensor_cores(c) ? 1 : slices(a.dk), on_tensor_cores(c) ? 1 : slices(a.dv), f, to, a.cu, a.N, a.T, a.H};
+        const SumArgs u{part(w.r1), part(w.r2), on_tensor_cores(c) ? 4 : slices(a.dk), on_tensor_cores(c) ? 4 : slices(a.dv), f, to, a.cu, a.N, a.T, a.H};
         sum_kernel<<<dim3(seqs, (a.H + 31) / 32, deep), 512, 0, s>>>(u);
         count_launch();
         if (a.fixed) {

@@ -35,18 +35,16 @@ static_assert(CTL * REG_CTL + PREP * REG_PREP + HOLD * REG_HOLD <= THREADS * 72,
 constexpr int COLS = 32, TOKENS = 16;                              // of the state and of the outputs that one of the holding threads has
 constexpr uint32_t kTries = 1u << 20;            // a second or two
 
-enum Kind { kStates, kPlain, kFull };      // states alone; jobs whose operands are in two parts and that put out nothing but BF16 rows; any
+enum Kind { kStates, kPlain, kFull };      // states alone; jobs whose operands are in two parts and that put out nothing but BF16 rows; any, in three parts
 
 constexpr uint32_t TILE = C * 128;                                 // 64 rows of 64 BF16 values
-constexpr int OUT_PITCH = D + 4;
-// Shared memory: a ring of copies (y0 [x0] y1 [x1] z0 z1), parts of [Yw0 | Yw1 | P] (twice for the states, whose products then have no gap),
-// the rows on their way out (only where they are summed up for dots, or in FP32).
+// Shared memory: a ring of copies (y0 [x0] y1 [x1] z0 z1), parts of [Yw0 | Yw1 | P] (twice for the states, whose products then have no gap).
 template <Kind K> struct Map {
     static constexpr bool X = K != kStates;
-    static constexpr int STAGES = K == kFull ? 2 : 3, SETS = K == kStates ? 2 : 1;
+    static constexpr int STAGES = 3, SETS = K == kStates ? 2 : 1;
     static constexpr uint32_t Y = 0, XT = TILE, ATOM = (X ? 2 : 1) * TILE, Z = 2 * ATOM, STAGE = Z + 2 * TILE;
     static constexpr uint32_t OPS = STAGES * STAGE, PART = (X ? 3 : 2) * TILE, SET = K == kPlain ? 2 * PART + 2 * TILE : 3 * PART;
-    static constexpr uint32_t OUT = OPS + SETS * SET, INFO = OUT + (K == kFull ? C * OUT_PITCH * 4 : 0);
+    static constexpr uint32_t INFO = OPS + SETS * SET;
 };
 
 struct Item {
@@ -56,7 +54,7 @@ struct Place {                 // a chunk on the way to its Info
     float g[C];
     Item item;
 };
-constexpr int AHEAD = 4, PLACES = 8;
+constexpr int AHEAD = 4, PLACES = 6;
 struct alignas(16) Info {      // of one chunk; its arrays are read in 16-byte pieces
     float2 g[C];               // sums of the decays, as two floats; negative backward in time, so that d = g_i - g_j either way
     float c[C], w[C];
@@ -67,9 +65,9 @@ struct alignas(16) Info {      // of one chunk; its arrays are read in 16-byte p
     Item item;
     int plain;
     int dirty;                 // some z is not finite:
-    int poison[D];             // the channel's first such token in the job's direction
+    unsigned char poison[D];   // the channel's first such token in the job's direction, or NONE
 };
-constexpr int NONE = 1 << 20, INFOS = 4;
+constexpr int NONE = 255, INFOS = 4;
 enum { kFromFirst = 1, kFromPiece = 2, kEnds = 4, kOpen = 8 };        // kOpen: the pair begins here and ends in another piece
 
 struct Shared {
@@ -115,6 +113,23 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 }
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// Stores and loads under a predicate, without a branch around each.
+__device__ __forceinline__ void store_if(bool on, char *to, __nv_bfloat16 v) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.b16 [%0], %1;\n\t}" ::"l"(to), "h"(__bfloat16_as_ushort(v)), "r"((int)on) : "memory");
+}
+__device__ __forceinline__ void store_if(bool on, char *to, float v) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.f32 [%0], %1;\n\t}" ::"l"(to), "f"(v), "r"((int)on) : "memory");
+}
+__device__ __forceinline__ float load_bf16_if(bool on, const char *from) {
+    unsigned short v;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t@p ld.global.nc.b16 %0, [%1];\n\t}" : "=h"(v) : "l"(from), "r"((int)on));
+    return __uint_as_float((uint32_t)v << 16);
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t x);
+__device__ __forceinline__ char *uniform(const char *p) {
+    const unsigned long long a = reinterpret_cast<unsigned long long>(p);
+    return reinterpret_cast<char *>((unsigned long long)uniform((uint32_t)(a >> 32)) << 32 | uniform((uint32_t)a));
+}
 // A pair as BF16 numbers that add up to it; the rests are exact in FP32.
 __device__ __forceinline__ uint32_t peel(float &x, float &y) {
     const uint32_t w = pack(x, y);
@@ -130,6 +145,18 @@ __device__ __forceinline__ bool elect() {
 }
 // The same value in all lanes, and known to be: the MMA warps' addresses stay in uniform registers, whose instructions take nothing else.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// The smaller of a byte and `value` in its place, for many threads at once.
+__device__ __forceinline__ void note_first(unsigned char *bytes, int at, unsigned value) {
+    unsigned *const word = reinterpret_cast<unsigned *>(bytes + (at & ~3));
+    const int shift = 8 * (at & 3);
+    unsigned was = *word, now;
+    do {
+        now = was;
+        if ((now >> shift & 255u) <= value) return;
+        was = atomicCAS(word, now, (now & ~(255u << shift)) | value << shift);
+    } while (was != now);
+}
 
 // A bounded wait of a whole warp, with the same answer for all its lanes; one that gives up ends the others' too.  (Short: the kernel's
 // loops have to stay in the instruction cache.)
@@ -196,7 +223,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
     if (tid == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&sh.full[s]), 1);
-            mbar_init(smem_u32(&sh.empty[s]), (STATES ? 1 : 2) + (FULL && J.dots ? HOLD / 32 : 0));    // (with dots the rows' last step reads z)
+            mbar_init(smem_u32(&sh.empty[s]), (STATES ? 1 : 2) + (FULL && J.dots ? HOLD / 32 : 0));    // (for dots the holding warps read z)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&sh.drain[s]), 1);
@@ -216,7 +243,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
         fence_mbar_init();
         sh.dead = 0;
     }
-    if (tid < INFOS * D) sh.info[tid / D].poison[tid % D] = NONE;
+    for (int i = tid; i < INFOS * D; i += THREADS) sh.info[i / D].poison[i % D] = NONE;
     __syncthreads();
     int floor0 = __shfl_up_sync(0xffffffffu, run_end, 1);
     if (lane == 0) floor0 = 0;
@@ -583,7 +610,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                             unsigned short *p = reinterpret_cast<unsigned short *>(z + ((c0 + e / 8) ^ (t & 7)) * 16) + e % 8;
                             if ((*p & 0x7fffu) < 0x7f80u) continue;
                             *p = 0;
-                            atomicMin(&I.poison[atom * 64 + c0 * 8 + e], reverse ? C - 1 - t : t);
+                            note_first(I.poison, atom * 64 + c0 * 8 + e, reverse ? C - 1 - t : t);
                             I.dirty = 1;
                         }
                     }
@@ -697,12 +724,13 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
         const bool last_anchor = J.last_anchor;
         char *const out = static_cast<char *>(J.out);
         const __nv_bfloat16 *const dot_rows = static_cast<const __nv_bfloat16 *>(J.r.p);
-        const int dot_share = dots ? J.r.share : 1;
-        const uint32_t row_step = (uint32_t)H * jb * 2;
+        const int dot_heads = dots ? H / J.r.share : 1;
+        const uint32_t dot_step = (uint32_t)dot_heads * jb * 2;
+        const bool dot_shared = dots && J.r.share > 1;
+        const uint32_t row_step = (uint32_t)H * jb * (FULL && !out_bf16 ? 4 : 2);
         float S[COLS];
 #pragma unroll
         for (int i = 0; i < COLS; ++i) S[i] = 0.f;
-        float *const out_at = reinterpret_cast<float *>(sm + M::OUT);
         float *const own_state = A.state + ((size_t)job * A.pieces + piece) * D * D;
         // the state that chunk `it` begins with
         auto enter = [&](const Info &I) {
@@ -867,79 +895,54 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 __syncwarp();
                 if (ok && lane == 0) mbar_arrive(smem_u32(&sh.info_free[it % INFOS]));
                 if (!ok) break;
-            } else if constexpr (!FULL) {
+            } else {
                 // a channel a lane, a token a store: 64 bytes of a row a warp
                 if (!ok) break;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.info_free[it % INFOS]));     // (an arrival behind the stores would wait for them)
-                // (one address for the warp and 32-bit offsets: short code)
-                const size_t first_row = ((size_t)(t0 + TOKENS * part) * H + h) * jb * 2;
-                char *const rows = out + ((unsigned long long)uniform((uint32_t)(first_row >> 32)) << 32 | uniform((uint32_t)first_row));
-                uint32_t at = 2 * b;
-                if (valid == C && jb == D) {
+                const int left = in_b ? valid - TOKENS * part : 0;
+                if (FULL && dots) {
+                    // the dots of the warp's channels, and the term of the token itself, which is in the rows but not in them
+                    const int s = it % STAGES;
+                    const char *const r = uniform(reinterpret_cast<const char *>(dot_rows + ((size_t)(t0 + TOKENS * part) * dot_heads + (dot_shared ? I.item.hk : h)) * jb));
+                    const uint8_t *const z = sm + s * M::STAGE + M::Z + (b >> 6) * TILE + part * TOKENS * 128 + (b & 7) * 2;
+                    float d[TOKENS];
 #pragma unroll
-                    for (int i = 0; i < TOKENS; ++i, at += row_step) *reinterpret_cast<__nv_bfloat16 *>(rows + at) = __float2bfloat16_rn(o[i]);
+                    for (int i = 0; i < TOKENS; ++i) d[i] = load_bf16_if(i < left, r + (2 * b + i * dot_step));
+#pragma unroll
+                    for (int i = 0; i < TOKENS; ++i) d[i] = i < left ? d[i] * o[i] : 0.f;
+#pragma unroll
+                    for (int i = 0; i < TOKENS; ++i) {
+                        const unsigned short w = *reinterpret_cast<const unsigned short *>(z + i * 128 + (((b >> 3) ^ i) & 7) * 16);
+                        o[i] = fmaf(I.own[TOKENS * part + i], __uint_as_float((uint32_t)w << 16), o[i]);
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&sh.info_free[it % INFOS]));        // (an arrival behind the stores would wait for them)
+                        mbar_arrive(smem_u32(&sh.empty[s]));
+                    }
+                    // sums over the lanes, half of the tokens given away at each step
+#pragma unroll
+                    for (int w = 8; w; w >>= 1)
+#pragma unroll
+                        for (int i = 0; i < w; ++i) {
+                            const bool upper = lane & 2 * w;
+                            const float give = upper ? d[i] : d[i + w], keep = upper ? d[i + w] : d[i];
+                            d[i] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * w);
+                        }
+                    d[0] += __shfl_xor_sync(0xffffffffu, d[0], 1);
+                    const int t = TOKENS * part + (lane >> 1);
+                    if (!(lane & 1) && t < valid) dots_at[((size_t)(warp & 3) * A.c.T + t0 + t) * H + h] = d[0];
                 } else {
-                    const int left = in_b ? valid - TOKENS * part : 0;
-#pragma unroll
-                    for (int i = 0; i < TOKENS; ++i, at += row_step)
-                        if (i < left) *reinterpret_cast<__nv_bfloat16 *>(rows + at) = __float2bfloat16_rn(o[i]);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.info_free[it % INFOS]));
                 }
-            } else {
-                // (a warp that has given up still comes to the others' barriers, and touches nothing)
-                named_bar(1, HOLD);                                  // the rows of the chunk before are read
-                if (ok)
+                // (one address for the warp and 32-bit offsets: short code)
+                char *const rows = uniform(out + ((size_t)(t0 + TOKENS * part) * H + h) * jb * (FULL && !out_bf16 ? 4 : 2));
+                if (FULL && !out_bf16) {
 #pragma unroll
-                    for (int i = 0; i < TOKENS; ++i) out_at[(TOKENS * part + i) * OUT_PITCH + b] = o[i];
-                named_bar(1, HOLD);
-                if (!ok) continue;
-                // rows: 4 a warp, 4 channels a lane
-                const int s = it % STAGES, c = 4 * lane, t1 = 4 * hw;
-                const bool in_c = c < jb;
-                float4 v[4];
-                uint2 r[4];
-                if (dots)
+                    for (int i = 0; i < TOKENS; ++i) store_if(i < left, rows + (4 * b + i * row_step), o[i]);
+                } else {
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        r[u] = make_uint2(0, 0);
-                        if (in_c && t1 + u < valid)
-                            r[u] = __ldg(reinterpret_cast<const uint2 *>(dot_rows + ((size_t)(t0 + t1 + u) * (H / dot_share) + h / dot_share) * jb + c));
-                    }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) v[u] = *reinterpret_cast<const float4 *>(out_at + (t1 + u) * OUT_PITCH + c);
-                float dot[4];
-                if (dots) {
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int t = t1 + u;
-                        dot[u] = in_c ? fmaf(high(r[u].y), v[u].w, fmaf(low(r[u].y), v[u].z, fmaf(high(r[u].x), v[u].y, low(r[u].x) * v[u].x))) : 0.f;
-                        // the term of the token itself
-                        const uint2 z = *reinterpret_cast<const uint2 *>(sm + s * M::STAGE + M::Z + (lane >> 4) * TILE + sw128_offset(t, c & 63));
-                        const float p = I.own[t];
-                        v[u] = make_float4(fmaf(p, low(z.x), v[u].x), fmaf(p, high(z.x), v[u].y), fmaf(p, low(z.y), v[u].z), fmaf(p, high(z.y), v[u].w));
-                    }
-                }
-                // (an arrival behind the stores would wait for them)
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&sh.info_free[it % INFOS]));
-                    if (dots) mbar_arrive(smem_u32(&sh.empty[s]));
-                }
-                if (dots) {
-#pragma unroll
-                    for (int q = 16; q; q >>= 1)
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], q);
-                    if (lane < 4 && t1 + lane < valid) dots_at[(size_t)(t0 + t1 + lane) * H + h] = lane == 0 ? dot[0] : lane == 1 ? dot[1] : lane == 2 ? dot[2] : dot[3];
-                }
-                const int left = in_c ? valid - t1 : 0;
-                char *to = out + (((size_t)(t0 + t1) * H + h) * jb + c) * (out_bf16 ? 2 : 4);
-                const size_t step = (size_t)H * jb * (out_bf16 ? 2 : 4);
-#pragma unroll
-                for (int u = 0; u < 4; ++u, to += step) {
-                    if (u >= left) continue;
-                    if (out_bf16) __stcs(reinterpret_cast<uint2 *>(to), make_uint2(pack(v[u].x, v[u].y), pack(v[u].z, v[u].w)));
-                    else __stcs(reinterpret_cast<float4 *>(to), v[u]);
+                    for (int i = 0; i < TOKENS; ++i) store_if(i < left, rows + (2 * b + i * row_step), __float2bfloat16_rn(o[i]));
                 }
             }
         }
