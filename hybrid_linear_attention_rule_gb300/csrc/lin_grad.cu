@@ -169,7 +169,7 @@ struct Space {
             return was;
         };
         const size_t TH = (size_t)T * H, slots = anchor_slots(N, T);
-        pieces = take(bf16 ? tc_workspace() : 0);
+        pieces = take(bf16 ? tc_workspace(N, T, H, backward ? 2 : 1) : 0);
         r1 = r2 = S = R = f = dg = pq = pk = at;
         if (backward) {
             r1 = take(TH * (bf16 ? 4 : slices(dk)) * 4);

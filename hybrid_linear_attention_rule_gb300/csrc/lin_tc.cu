@@ -8,11 +8,12 @@
 // threads a row) in FP32, and only the decayed scores P and keys Yw pass through shared memory, each as a sum of two or three BF16 numbers:
 // the inputs are exact, so a product of three parts is FP32's accuracy, of two 2^-17.
 //
-// Roles of a CTA, joined by mbarriers: a warp that walks the chunks and sums their decays, ahead of the others; a copy warp (TMA); an MMA
-// warp for PT and ACC and one for O1, so that neither chain waits for the other's operands; eight warps that prepare P and
-// Yw, sixteen that hold S, write its operand, fold ACC into it and put out rows.
+// Roles of a CTA, joined by mbarriers: a copy warp (TMA), an MMA warp for ACC and one for PT and O1, so that no chain waits for the
+// other's operands, eight warps that prepare P and Yw, sixteen that hold S, write its operand, fold ACC into it and put out rows.
+// Each of them runs through its code once a chunk, so the code has to stay short: past some 60 KB of it the warps waited for instructions.
 //
-// The chunks of all (sequence, head) pairs stand in one line, cut evenly over the CTAs ("pieces").  A piece that begins within a pair
+// The chunks of all (sequence, head) pairs stand in one line.  `plan_kernel` writes a record for each, where it lies and what its decays
+// give, which the copies bring along.  The line is cut evenly over the CTAs ("pieces").  A piece that begins within a pair
 // needs the state there: a first pass (STATES) runs the pieces that end within a pair for their state alone, `join_kernel` chains
 // those of a pair, and the second pass starts from them.  The decay of a piece is one number a head, so the chain is a sum.
 #include <cuda.h>
@@ -47,39 +48,30 @@ template <Kind K> struct Map {
     static constexpr uint32_t INFO = OPS + SETS * SET;
 };
 
-struct Item {
-    int n, h, hk, t0, valid, chunk, flags;      // hk: h / group
-};
-struct Place {                 // a chunk on the way to its Info
-    float g[C];
-    Item item;
-};
-constexpr int AHEAD = 4, PLACES = 6;
-struct alignas(16) Info {      // of one chunk; its arrays are read in 16-byte pieces
+// What a chunk's copies bring beside its rows; one of a direction and scale.  Its arrays are read in 16-byte pieces.
+struct alignas(16) Record {
     float2 g[C];               // sums of the decays, as two floats; negative backward in time, so that d = g_i - g_j either way
     float c[C], w[C];
     float fi[C], fj[C];        // D_ij = fi[i] fj[j], the scale in fj, where the chunk's decay leaves both in range (`plain`)
-    float own[C];              // P's diagonal, where it is kept apart
-    float keep;                // the chunk's decay
     unsigned long long lost;   // tokens whose decay is NaN
-    Item item;
+    long long units;           // the chunk's decay,
+    float keep;                // and its exponential
     int plain;
-    int dirty;                 // some z is not finite:
-    unsigned char poison[D];   // the channel's first such token in the job's direction, or NONE
+    int n, h, hk, t0, valid;   // hk: h / group
+    int chunk, pos, chunks;    // of the pair's chunks: which in time, which in the line, how many
 };
-constexpr int NONE = 255, INFOS = 4;
-enum { kFromFirst = 1, kFromPiece = 2, kEnds = 4, kOpen = 8 };        // kOpen: the pair begins here and ends in another piece
+static_assert(sizeof(Record) % 16 == 0, "copied in 16-byte pieces");
 
 struct Shared {
-    Info info[INFOS];
-    Place place[PLACES];
-    unsigned long long info_full[INFOS], info_free[INFOS], full[3], empty[3], pt_full, pt_free, prep_full, acc_full[2], acc_free[2], sop_full, o1_full, drain[2];
-    uint32_t tmem;
+    Record rec[3];
+    float own[3][C];           // P's diagonal, where it is kept apart
+    unsigned char poison[3][D];        // of a z that is not finite: the channel's first such token in the job's direction, or NONE
+    int dirty[3];              // whether there is one
     int dead;
-    long long part[THREADS / 32];
-    int part_end[THREADS / 32];
-    int n[2], h[2], pos[2], chunks[2], begin[2], len[2], floor[2];     // where the piece begins, and where it ends
+    unsigned long long full[3], empty[3], pt_full, pt_free, prep_full, acc_full[2], acc_free[2], sop_full, o1_full, drain[2];
+    uint32_t tmem;
 };
+constexpr int NONE = 255;
 template <Kind K> constexpr uint32_t kSmem = Map<K>::INFO + sizeof(Shared) + 1024;
 static_assert(kSmem<kStates> <= 232448 && kSmem<kPlain> <= 232448 && kSmem<kFull> <= 232448, "shared memory");
 
@@ -94,10 +86,11 @@ struct Head {                  // of a piece's state
 struct TcArgs {
     CUtensorMap map[4];
     Call c;
-    int x[3], y[3], z[3];      // the jobs' maps
+    int x[3], y[3], z[3], r[3];        // the jobs' maps
     int rows;                  // of a copy's box
-    int group;                 // value heads that share a key head
     int pieces;                // a job
+    const Record *rec[3];      // the jobs'
+    const long long *total;    // records of one
     int least;                 // chunks of a piece, at least, where there are more pieces than pairs
     Head *head;                // [jobs][pieces]
     float *state;              // [jobs][pieces][a][D]
@@ -113,6 +106,12 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 }
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// An arrival that waits for none of the thread's stores.  For barriers that hand over tensor memory alone: what the thread did there has
+// ended (tcgen05.wait) and is fenced (tcgen05.fence) before; a releasing arrival would also wait until the rows stored last are in L2, which
+// took 2 to 4 thousand cycles of a chunk.
+__device__ __forceinline__ void arrive_relaxed(const unsigned long long &bar) {
+    asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&bar)) : "memory");
+}
 // Stores and loads under a predicate, without a branch around each.
 __device__ __forceinline__ void store_if(bool on, char *to, __nv_bfloat16 v) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.b16 [%0], %1;\n\t}" ::"l"(to), "h"(__bfloat16_as_ushort(v)), "r"((int)on) : "memory");
@@ -120,10 +119,10 @@ __device__ __forceinline__ void store_if(bool on, char *to, __nv_bfloat16 v) {
 __device__ __forceinline__ void store_if(bool on, char *to, float v) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.f32 [%0], %1;\n\t}" ::"l"(to), "f"(v), "r"((int)on) : "memory");
 }
-__device__ __forceinline__ float load_bf16_if(bool on, const char *from) {
+__device__ __forceinline__ unsigned short load_if(bool on, const char *from) {
     unsigned short v;
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t@p ld.global.nc.b16 %0, [%1];\n\t}" : "=h"(v) : "l"(from), "r"((int)on));
-    return __uint_as_float((uint32_t)v << 16);
+    return v;
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t x);
 __device__ __forceinline__ char *uniform(const char *p) {
@@ -181,7 +180,161 @@ struct Line {
     const int32_t *cu;
     int T;
     __device__ __forceinline__ int bound(int i) const { return min(max(cu[i], 0), T); }
+    __device__ __forceinline__ int length(int n, int &floor, int &begin) const {         // of sequence n; floor: the ends before it
+        if (!cu) {
+            begin = 0;
+            return T;
+        }
+        begin = max(bound(n), floor);
+        floor = max(floor, bound(n + 1));
+        return floor - begin;
+    }
 };
+
+struct PlanArgs {
+    const float *g;
+    const int32_t *cu;
+    int fixed, N, T, H, group, variants, reverse[2];
+    float sp[2], sc[2], sw[2];
+    Record *rec[2];
+    long long *total;
+};
+constexpr int PLAN_THREADS = 256;
+
+// The records: a warp a chunk, a CTA an even share of the line.
+__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constant__ PlanArgs A) {
+    __shared__ long long part[PLAN_THREADS / 32];
+    __shared__ int part_end[PLAN_THREADS / 32], found[4];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, N = A.N, H = A.H;
+    const int per = (N + PLAN_THREADS - 1) / PLAN_THREADS, n0 = min(N, tid * per), n1 = min(N, n0 + per);
+    const Line line{A.cu, A.T};
+    int own_end = 0;
+    if (A.cu)
+        for (int n = n0; n < n1; ++n) own_end = max(own_end, line.bound(n + 1));
+    int run_end = own_end;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int e = __shfl_up_sync(0xffffffffu, run_end, o);
+        if (lane >= o) run_end = max(run_end, e);
+    }
+    if (lane == 31) part_end[warp] = run_end;
+    __syncthreads();
+    int floor0 = __shfl_up_sync(0xffffffffu, run_end, 1);
+    if (lane == 0) floor0 = 0;
+    for (int w = 0; w < warp; ++w) floor0 = max(floor0, part_end[w]);
+    long long own = 0;
+    {
+        int f = floor0, b;
+        for (int n = n0; n < n1; ++n) own += max(1, (line.length(n, f, b) + C - 1) / C);
+    }
+    long long run = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long e = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += e;
+    }
+    if (lane == 31) part[warp] = run;
+    __syncthreads();
+    long long before = run - own, total = 0;
+    for (int w = 0; w < PLAN_THREADS / 32; ++w) {
+        if (w < warp) before += part[w];
+        total += part[w];
+    }
+    const long long U = total * H, first = U * blockIdx.x / gridDim.x, end = U * (blockIdx.x + 1) / gridDim.x;
+    if (blockIdx.x == 0 && tid == 0) *A.total = U;
+    if (first >= end) return;
+    {
+        long long at = before;
+        int f = floor0, b;
+        for (int n = n0; n < n1; ++n) {
+            const int was = f, chunks = max(1, (line.length(n, f, b) + C - 1) / C);
+            const long long u = first - at * H;
+            if (u >= 0 && u < (long long)chunks * H) {
+                found[0] = n;
+                found[1] = (int)(u / chunks);
+                found[2] = (int)(u % chunks);
+                found[3] = was;
+            }
+            at += chunks;
+        }
+    }
+    __syncthreads();
+    int n = found[0], h = found[1], floor = found[3], begin;
+    long long pos = found[2] + warp;
+    int len = line.length(n, floor, begin), chunks = max(1, (len + C - 1) / C);
+    for (long long u = first + warp; u < end; u += PLAN_THREADS / 32, pos += PLAN_THREADS / 32) {
+        while (pos >= chunks) {
+            pos -= chunks;
+            if (++h == H) {
+                h = 0;
+                ++n;
+                len = line.length(n, floor, begin);
+                chunks = max(1, (len + C - 1) / C);
+            }
+        }
+        for (int k = 0; k < A.variants; ++k) {
+            const bool reverse = A.reverse[k];
+            const int chunk = reverse ? chunks - 1 - (int)pos : (int)pos, t0 = begin + chunk * C, valid = min(C, len - chunk * C);
+            Record &R = A.rec[k][u];
+            float g[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int t = 2 * lane + e;
+                g[e] = t < valid ? __ldg(A.g + (A.fixed ? (size_t)h : (size_t)(t0 + t) * H + h)) : 0.f;
+            }
+            const long long d1 = decay_units(g[1]);
+            long long v = decay_units(g[0]) + d1;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long e = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += e;
+            }
+            const long long all = __shfl_sync(0xffffffffu, v, 31);
+            const unsigned bad0 = __ballot_sync(0xffffffffu, g[0] != g[0]), bad1 = __ballot_sync(0xffffffffu, g[1] != g[1]);
+            unsigned long long bad = 0;
+            if (bad0 | bad1)
+                for (int i = 0; i < 32; ++i) bad |= (unsigned long long)((bad0 >> i & 1) | (bad1 >> i & 1) << 1) << (2 * i);
+            const float nan = __int_as_float(0x7fffffff), sign = reverse ? -1.f : 1.f;
+            const float2 whole = two_floats(all);
+            bool plain = true;
+            float2 x[2];
+            float c[2], w[2], fi[2], fj[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const unsigned long long upto = ~0ull >> (63 - 2 * lane - e);
+                const float2 f = two_floats(e ? v : v - d1);
+                const float up = ex2(f.x) * ex2(f.y), down = ex2(whole.x - f.x) * ex2(whole.y - f.y), inverse = ex2(-f.x) * ex2(-f.y);
+                x[e] = make_float2(sign * f.x, sign * f.y);
+                c[e] = bad & (reverse ? ~upto : upto) ? nan : A.sc[k] * (reverse ? down : up);
+                w[e] = bad & (reverse ? upto : ~upto) ? nan : A.sw[k] * (reverse ? up : down);
+                fi[e] = reverse ? inverse : up;
+                fj[e] = A.sp[k] * (reverse ? up : inverse);
+                plain = plain && fabsf(f.x) < 100.f;
+            }
+            // (sums of up to 100 powers of two: neither factor leaves FP32's range, and their product is D's)
+            plain = __all_sync(0xffffffffu, plain) && !bad;
+            reinterpret_cast<float4 *>(R.g)[lane] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+            reinterpret_cast<float2 *>(R.c)[lane] = make_float2(c[0], c[1]);
+            reinterpret_cast<float2 *>(R.w)[lane] = make_float2(w[0], w[1]);
+            reinterpret_cast<float2 *>(R.fi)[lane] = make_float2(fi[0], fi[1]);
+            reinterpret_cast<float2 *>(R.fj)[lane] = make_float2(fj[0], fj[1]);
+            if (lane == 0) {
+                R.lost = bad;
+                R.units = all;
+                R.keep = bad ? nan : ex2(whole.x) * ex2(whole.y);
+                R.plain = plain;
+                R.n = n;
+                R.h = h;
+                R.hk = h / A.group;
+                R.t0 = t0;
+                R.valid = valid;
+                R.chunk = chunk;
+                R.pos = (int)pos;
+                R.chunks = chunks;
+            }
+        }
+    }
+}
 
 template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(const __grid_constant__ TcArgs A) {
     constexpr bool STATES = KIND == kStates, FULL = KIND == kFull;
@@ -194,46 +347,41 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int job = blockIdx.x / A.pieces, piece = blockIdx.x % A.pieces;
     const Job &J = A.c.job[job];
-    const int N = A.c.N, H = A.c.H;
+    const int H = A.c.H;
     const Waiter wait{&sh.dead};
+    const Record *const line = A.rec[job];
 
     // ---- where the piece begins and ends
-    const int per = (N + THREADS - 1) / THREADS, n0 = min(N, tid * per), n1 = min(N, n0 + per);
-    const Line line{A.c.cu, A.c.T};
-    auto length = [&](int n, int &floor, int &begin) {               // of sequence n; floor: the ends before it
-        if (!line.cu) {
-            begin = 0;
-            return A.c.T;
-        }
-        begin = max(line.bound(n), floor);
-        floor = max(floor, line.bound(n + 1));
-        return floor - begin;
-    };
-    int own_end = 0;
-    if (line.cu)
-#pragma unroll 1
-        for (int n = n0; n < n1; ++n) own_end = max(own_end, line.bound(n + 1));
-    int run_end = own_end;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int e = __shfl_up_sync(0xffffffffu, run_end, o);
-        if (lane >= o) run_end = max(run_end, e);
+    const long long U = *A.total, most = max((long long)A.c.N * H, U / A.least);
+    const int count_pieces = (int)min((long long)A.pieces, most);
+    if (piece >= count_pieces) {
+        if (STATES && tid == 0) A.head[job * A.pieces + piece] = Head{0.f, 0, 0};
+        return;
     }
-    if (lane == 31) sh.part_end[warp] = run_end;
+    long long u0 = U * piece / count_pieces;
+    const long long u1 = U * (piece + 1) / count_pieces;
+    if constexpr (STATES) {
+        const int pos1 = u1 < U ? line[u1].pos : 0;                  // within a pair: its part of this piece, if it ends there
+        const bool goes_on = u1 - pos1 < u0;
+        if (!goes_on) u0 = u1 - pos1;
+        if (tid == 0) {
+            Head &hd = A.head[job * A.pieces + piece];
+            hd.ends_within = pos1 > 0;
+            hd.goes_on = pos1 > 0 && goes_on;
+        }
+        if (pos1 == 0) return;
+    }
+    const int items = (int)(u1 - u0);
     if (tid == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&sh.full[s]), 1);
-            mbar_init(smem_u32(&sh.empty[s]), (STATES ? 1 : 2) + (FULL && J.dots ? HOLD / 32 : 0));    // (for dots the holding warps read z)
+            mbar_init(smem_u32(&sh.empty[s]), (STATES ? 1 : 2) + HOLD / 32);
+            sh.dirty[s] = 0;
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&sh.drain[s]), 1);
             mbar_init(smem_u32(&sh.acc_full[s]), 2);
             mbar_init(smem_u32(&sh.acc_free[s]), HOLD / 32);
-        }
-        for (int i = 0; i < INFOS; ++i) {
-            mbar_init(smem_u32(&sh.info_full[i]), 1);
-            mbar_init(smem_u32(&sh.info_free[i]), HOLD / 32);
-            sh.info[i].dirty = 0;
         }
         mbar_init(smem_u32(&sh.pt_full), 1);
         mbar_init(smem_u32(&sh.pt_free), 3);
@@ -243,82 +391,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
         fence_mbar_init();
         sh.dead = 0;
     }
-    for (int i = tid; i < INFOS * D; i += THREADS) sh.info[i / D].poison[i % D] = NONE;
-    __syncthreads();
-    int floor0 = __shfl_up_sync(0xffffffffu, run_end, 1);
-    if (lane == 0) floor0 = 0;
-#pragma unroll 1
-    for (int w = 0; w < warp; ++w) floor0 = max(floor0, sh.part_end[w]);
-    long long own = 0;
-    {
-        int f = floor0, b;
-#pragma unroll 1
-        for (int n = n0; n < n1; ++n) own += max(1, (length(n, f, b) + C - 1) / C);
-    }
-    long long run = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long e = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += e;
-    }
-    if (lane == 31) sh.part[warp] = run;
-    __syncthreads();
-    long long before = run - own, total = 0;
-#pragma unroll 1
-    for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) before += sh.part[w];
-        total += sh.part[w];
-    }
-    const long long U = total * H, most = max((long long)N * H, U / A.least);
-    const int count_pieces = (int)min((long long)A.pieces, most);
-    if (piece >= count_pieces) {
-        if (STATES && tid == 0) A.head[job * A.pieces + piece] = Head{0.f, 0, 0};
-        return;
-    }
-    long long u0 = U * piece / count_pieces;
-    const long long u1 = U * (piece + 1) / count_pieces;
-    {
-        long long at = before;
-        int f = floor0, b;
-#pragma unroll 1
-        for (int n = n0; n < n1; ++n) {
-            const int f_was = f, len = length(n, f, b), chunks = max(1, (len + C - 1) / C);
-#pragma unroll 1
-            for (int e = 0; e < 2; ++e) {
-                const long long u = (e ? u1 : u0) - at * H;
-                if (u < 0 || u >= (long long)chunks * H) continue;
-                sh.n[e] = n;
-                sh.h[e] = (int)(u / chunks);
-                sh.pos[e] = (int)(u % chunks);
-                sh.chunks[e] = chunks;
-                sh.begin[e] = b;
-                sh.len[e] = len;
-                sh.floor[e] = f_was;
-            }
-            at += chunks;
-        }
-    }
-    __syncthreads();
-    int start = 0;                                                   // which of the two places the work begins at
-    bool goes_on = false;
-    if constexpr (STATES) {
-        const bool within = u1 < U && sh.pos[1] > 0;
-        if (within) {
-            goes_on = u1 - sh.pos[1] < u0;
-            if (!goes_on) {
-                u0 = u1 - sh.pos[1];
-                start = 1;
-            }
-        }
-        if (tid == 0) {
-            Head &hd = A.head[job * A.pieces + piece];
-            hd.ends_within = within;
-            hd.goes_on = goes_on;
-        }
-        if (!within) return;
-    }
-    const int items = (int)(u1 - u0);
-    const int pos0 = STATES && start == 1 ? 0 : sh.pos[start];
+    for (int i = tid; i < STAGES * D; i += THREADS) sh.poison[i / D][i % D] = NONE;
 
     if (warp == 0) {
         tmem_alloc(smem_u32(&sh.tmem), 512);
@@ -335,131 +408,36 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
     if (warp < PREP_WARP) {
         give_registers<REG_CTL>();
         if (warp == 0) {
-            // ---------------- chunks and their decays ----------------
-            int n = sh.n[start], h = sh.h[start], pos = pos0, chunks = sh.chunks[start], begin = sh.begin[start], len = sh.len[start];
-            int floor = sh.floor[start];
-            {
-                int b;
-                length(n, floor, b);
-            }
-            int hk = h / A.group, left = A.group - (h - hk * A.group);       // left: heads that still share hk
-            long long sum = 0;                                       // STATES: the whole piece's decay
-            bool sum_lost = false;
-            const float *const g_at = A.c.g;
-            const int fixed = A.c.fixed;
-            const float sc = J.sc, sw = J.sw, sp = J.sp;
-            // (a chunk's decays are a word of every row of g: on their way while those of the chunks before are summed)
-            for (int it = -AHEAD; it < items; ++it) {
-                const int at = it + AHEAD;
-                if (at < items) {
-                    if (at > 0 && ++pos == chunks) {
-                        pos = 0;
-                        if (--left == 0) {
-                            left = A.group;
-                            ++hk;
-                        }
-                        if (++h == H) {
-                            h = hk = 0;
-                            ++n;
-                            len = length(n, floor, begin);
-                            chunks = max(1, (len + C - 1) / C);
-                        }
-                    }
-                    const int chunk = reverse ? chunks - 1 - pos : pos, t0 = begin + chunk * C, valid = min(C, len - chunk * C);
-                    Place &P = sh.place[at % PLACES];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int t = 2 * lane + u;
-                        const bool in = t < valid;
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&P.g[t])), "l"(g_at + (fixed ? (size_t)h : in ? (size_t)(t0 + t) * H + h : 0)),
-                                     "r"(in ? 4 : 0)
-                                     : "memory");
-                    }
-                    if (lane == 0)
-                        P.item = Item{n, h, hk, t0, valid, chunk, (pos == 0 ? kFromFirst : at == 0 ? kFromPiece : 0) | (pos == chunks - 1 ? kEnds : 0) |
-                                                                     (pos == 0 && chunks > items - at ? kOpen : 0)};
-                }
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                if (it < 0) continue;
-                asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD) : "memory");
-                __syncwarp();
-                Info &I = sh.info[it % INFOS];
-                const Place &P = sh.place[it % PLACES];
-                const float g[2] = {P.g[2 * lane], P.g[2 * lane + 1]};
-                const long long d0 = decay_units(g[0]), d1 = decay_units(g[1]);
-                long long v = d0 + d1;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long e = __shfl_up_sync(0xffffffffu, v, o);
-                    if (lane >= o) v += e;
-                }
-                const long long all = __shfl_sync(0xffffffffu, v, 31);
-                const unsigned bad0 = __ballot_sync(0xffffffffu, g[0] != g[0]), bad1 = __ballot_sync(0xffffffffu, g[1] != g[1]);
-                unsigned long long bad = 0;
-                if (bad0 | bad1)
-#pragma unroll 1
-                    for (int i = 0; i < 32; ++i) bad |= (unsigned long long)((bad0 >> i & 1) | (bad1 >> i & 1) << 1) << (2 * i);
-                const float2 whole = two_floats(all);
-                const float sign = reverse ? -1.f : 1.f;
-                bool plain = true;
-                if (it >= INFOS) {
-                    if (!wait(sh.info_free[it % INFOS], it / INFOS - 1)) break;
-                    if (I.dirty) {
-#pragma unroll 1
-                        for (int i = lane; i < D; i += 32) I.poison[i] = NONE;
-                        __syncwarp();
-                        I.dirty = 0;
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int t = 2 * lane + u;
-                    const float2 f = two_floats(u ? v : v - d1);
-                    const float up = ex2(f.x) * ex2(f.y), down = ex2(whole.x - f.x) * ex2(whole.y - f.y), inverse = ex2(-f.x) * ex2(-f.y);
-                    I.g[t] = make_float2(sign * f.x, sign * f.y);
-                    I.c[t] = sc * (reverse ? down : up);
-                    I.w[t] = sw * (reverse ? up : down);
-                    I.fi[t] = reverse ? inverse : up;
-                    I.fj[t] = sp * (reverse ? up : inverse);
-                    plain = plain && fabsf(f.x) < 100.f;
-                }
-                // (sums of up to 100 powers of two: neither factor leaves FP32's range, and their product is D's)
-                plain = __all_sync(0xffffffffu, plain) && !bad;
-                const float nan = __int_as_float(0x7fffffff);
-                if (bad)
-#pragma unroll 1
-                    for (int t = 2 * lane; t < 2 * lane + 2; ++t) {
-                        const unsigned long long upto = ~0ull >> (63 - t);
-                        if (bad & (reverse ? ~upto : upto)) I.c[t] = nan;
-                        if (bad & (reverse ? upto : ~upto)) I.w[t] = nan;
-                    }
-                sum += all;
-                sum_lost = sum_lost || bad;
-                if (lane == 0) {
-                    I.keep = bad ? nan : ex2(whole.x) * ex2(whole.y);
-                    I.plain = plain;
-                    I.lost = bad;
-                    I.item = P.item;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.info_full[it % INFOS]));
-            }
-            if (STATES && lane == 0) A.head[job * A.pieces + piece].keep = sum_lost ? __int_as_float(0x7fffffff) : exp2_units(sum);
-        } else if (warp == 1) {
             // ---------------- copies ----------------
-            const void *mx = &A.map[A.x[job]], *my = &A.map[A.y[job]], *mz = &A.map[A.z[job]];
-            const bool sx = J.x.share > 1, sy = J.y.share > 1, sz = J.z.share > 1;
-            const uint32_t bytes = (uint32_t)(STATES ? 4 : 6) * A.rows * 128;
+            const void *mx = &A.map[A.x[job]], *my = &A.map[A.y[job]], *mz = &A.map[A.z[job]], *mr = FULL ? &A.map[A.r[job]] : nullptr;
+            const bool sx = J.x.share > 1, sy = J.y.share > 1, sz = J.z.share > 1, sr = FULL && J.r.share > 1;
+            const uint32_t bytes = (uint32_t)(STATES ? 4 : 6) * A.rows * 128 + (uint32_t)sizeof(Record);
+            int at_t0 = 0, at_h = 0, at_hk = 0;                      // of 32 chunks, one a lane
             int it = 0;
             for (; it < items; ++it) {
                 const int s = it % STAGES;
-                if (!wait(sh.info_full[it % INFOS], it / INFOS)) break;
-                const Info &I = sh.info[it % INFOS];
-                const int t0 = uniform(I.item.t0), h = uniform(I.item.h), hk = uniform(I.item.hk);
-                if (it >= STAGES && !wait(sh.empty[s], it / STAGES - 1)) break;
-                const uint32_t bar = uniform(smem_u32(&sh.full[s])), to = uniform(sm32 + s * M::STAGE);
+                if (it % 32 == 0) {
+                    const Record &R = line[u0 + min(it + lane, items - 1)];
+                    at_t0 = R.t0;
+                    at_h = R.h;
+                    at_hk = R.hk;
+                }
+                const int t0 = uniform(__shfl_sync(0xffffffffu, at_t0, it & 31)), h = uniform(__shfl_sync(0xffffffffu, at_h, it & 31)),
+                          hk = uniform(__shfl_sync(0xffffffffu, at_hk, it & 31));
+                if (it >= STAGES) {
+                    if (!wait(sh.empty[s], it / STAGES - 1)) break;
+                    if (sh.dirty[s]) {
+                        for (int i = lane; i < D; i += 32) sh.poison[s][i] = NONE;
+                        __syncwarp();
+                        sh.dirty[s] = 0;
+                    }
+                }
+                __syncwarp();
+                const uint32_t bar = uniform(smem_u32(&sh.full[s])), to = uniform(sm32 + s * M::STAGE), rec_at = uniform(smem_u32(&sh.rec[s]));
+                const char *const rec = uniform(reinterpret_cast<const char *>(line + u0 + it));
                 if (elect()) {
                     mbar_arrive_expect_tx(bar, bytes);
+                    bulk_g2s(rec_at, rec, (uint32_t)sizeof(Record), bar);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         tma_load_3d(to + M::Y + u * M::ATOM, my, 64 * u, sy ? hk : h, t0, bar);
@@ -467,14 +445,17 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                     }
 #pragma unroll
                     for (int u = 0; u < 2; ++u) tma_load_3d(to + M::Z + u * TILE, mz, 64 * u, sz ? hk : h, t0, bar);
+                    if (FULL && dots)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) tma_prefetch_3d(mr, 64 * u, sr ? hk : h, t0);
                 }
                 __syncwarp();
                 // the next chunk on its way to L2: its copy, once there is room for it, is then a short one
-                if (it + 1 < items) {
-                    if (!wait(sh.info_full[(it + 1) % INFOS], (it + 1) / INFOS)) break;
-                    const Info &F = sh.info[(it + 1) % INFOS];
-                    const int t0 = uniform(F.item.t0), h = uniform(F.item.h), hk = uniform(F.item.hk);
+                if (it % 32 < 31 && it + 1 < items) {
+                    const int t0 = uniform(__shfl_sync(0xffffffffu, at_t0, it + 1 & 31)), h = uniform(__shfl_sync(0xffffffffu, at_h, it + 1 & 31)),
+                              hk = uniform(__shfl_sync(0xffffffffu, at_hk, it + 1 & 31));
                     if (elect()) {
+                        prefetch_l2(rec + sizeof(Record), (uint32_t)sizeof(Record));
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             tma_prefetch_3d(my, 64 * u, sy ? hk : h, t0);
@@ -489,7 +470,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
             for (int k = max(0, it - STAGES); k < it; ++k)
 #pragma unroll 1
                 for (uint32_t i = 0; i < kTries && !mbar_try_wait(smem_u32(&sh.full[k % STAGES]), (k / STAGES) & 1); ++i) {}
-        } else if (warp == 2) {
+        } else if (warp == 1) {
             // ---------------- products: the chunk's parts of the state and of the outputs ----------------
             const uint32_t tu = uniform(tm), base = uniform(sm32);
             for (int it = 0; it < items; ++it) {
@@ -518,7 +499,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
             if (elect()) mma_commit(smem_u32(&sh.drain[0]));
 #pragma unroll 1
             for (uint32_t i = 0; i < kTries && !mbar_try_wait(smem_u32(&sh.drain[0]), 0); ++i) {}
-        } else if (!STATES) {
+        } else if (!STATES && warp == 2) {
             // ---------------- products: what the state gives; the next chunk's scores ----------------
             const bool wide_a = J.a > 64;
             const uint32_t tu = uniform(tm), base = uniform(sm32);
@@ -585,11 +566,10 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
         for (int it = 0; it < items; ++it) {
             const int s = it % STAGES, set = it % SETS;
             uint8_t *const ops = sm + M::OPS + set * M::SET, *const row_at = ops + (uint32_t)t * 128, *const stage = sm + s * M::STAGE;
-            if (!wait(sh.info_full[it % INFOS], it / INFOS)) break;
-            Info &I = sh.info[it % INFOS];
-            const int valid = I.item.valid;
+            if (!wait(sh.full[s], it / STAGES)) break;
+            const Record &I = sh.rec[s];
+            const int valid = I.valid;
             if (keys) {
-                if (!wait(sh.full[s], it / STAGES)) break;
                 // z: rows behind the sequence are put to 0, and what is not finite, which is noted.  (Piece c of row t lies at piece
                 // c ^ (t & 7): the lanes' rows, taken in that order, lie in different banks.)
                 uint8_t *const z = stage + M::Z + atom * TILE + (uint32_t)t * 128;
@@ -610,21 +590,21 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                             unsigned short *p = reinterpret_cast<unsigned short *>(z + ((c0 + e / 8) ^ (t & 7)) * 16) + e % 8;
                             if ((*p & 0x7fffu) < 0x7f80u) continue;
                             *p = 0;
-                            note_first(I.poison, atom * 64 + c0 * 8 + e, reverse ? C - 1 - t : t);
-                            I.dirty = 1;
+                            note_first(sh.poison[s], atom * 64 + c0 * 8 + e, reverse ? C - 1 - t : t);
+                            sh.dirty[s] = 1;
                         }
                     }
                 }
                 if (it >= SETS && !wait(sh.acc_full[set], it / SETS - 1)) break;      // the operands' last reader
             } else if (zero) {
-                if (!wait(sh.full[s], it / STAGES) || (it >= SETS && !wait(sh.acc_full[set], it / SETS - 1))) break;
+                if (it >= SETS && !wait(sh.acc_full[set], it / SETS - 1)) break;
                 if (it == 0)
 #pragma unroll 1
                     for (int c = 0; c < 12; ++c)
                         if (c < (FULL ? 12 : 8)) *reinterpret_cast<uint4 *>(row_at + 2 * TILE + (c >> 2) * M::PART + (((i0 >> 3) + (c & 3)) ^ (t & 7)) * 16) = make_uint4(0, 0, 0, 0);
             } else if constexpr (!STATES) {
                 uint32_t part[FULL ? 3 : 2][16];
-                if (!wait(sh.full[s], it / STAGES) || !wait(sh.pt_full, it)) break;
+                if (!wait(sh.pt_full, it)) break;
                 tc_fence_after();
                 // columns that row t is seen by, in the thread's 32, as bits
                 const uint32_t lower = 0xffffffffu >> (31 - lane), mask = t >= valid ? 0u : i0 != 32 * quarter ? 0xffffffffu : reverse ? lower : ~(lower >> 1);
@@ -661,7 +641,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             if (g + e == lane) {
-                                I.own[t] = p[e];
+                                sh.own[s][t] = p[e];
                                 p[e] = 0.f;
                             }
                     }
@@ -733,16 +713,17 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
         for (int i = 0; i < COLS; ++i) S[i] = 0.f;
         float *const own_state = A.state + ((size_t)job * A.pieces + piece) * D * D;
         // the state that chunk `it` begins with
-        auto enter = [&](const Info &I) {
-            const int flags = I.item.flags;
-            if (!(flags & (kFromFirst | kFromPiece))) return;
-            const int slot = seq_slot(A.c.slot, A.c.num_slots, I.item.n);
-            const size_t state = ((size_t)max(slot, 0) * H + I.item.h) * ja * jb;
+        auto enter = [&](int it) {
+            const Record &I = sh.rec[it % STAGES];
+            const bool begins = I.pos == 0, open = begins && I.chunks > items - it;      // open: the pair ends in another piece
+            if (!begins && it > 0) return;
+            const int slot = seq_slot(A.c.slot, A.c.num_slots, I.n);
+            const size_t state = ((size_t)max(slot, 0) * H + I.h) * ja * jb;
             // element a of it is at from[a * step]; nothing (zero) without one
-            const float *from = flags & kFromFirst ? (first && slot >= 0 && in_b ? first + state + (size_t)b * sb : nullptr)
+            const float *from = begins ? (first && slot >= 0 && in_b ? first + state + (size_t)b * sb : nullptr)
                                                    : (STATES ? nullptr : own_state - D * D + b);
-            int step = flags & kFromFirst ? sa : D;
-            if (A.kept && (flags & kOpen)) {
+            int step = begins ? sa : D;
+            if (A.kept && open) {
                 float *const kept = A.kept + ((size_t)job * A.pieces + piece) * D * D + b;
                 if (STATES) {
 #pragma unroll 4
@@ -783,28 +764,36 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh.sop_full));
+            if (lane == 0) arrive_relaxed(sh.sop_full);
         };
-        bool ok = true;
+        bool ok = true, lost = false;
+        long long units = 0;                                         // STATES: the piece's decay
         for (int it = -1; it < items; ++it) {                        // (-1: only the first state goes out)
             const int set = it & (SETS - 1);
             const uint32_t acc = lanes + ACC + set * ACC_STEP;
-            Info &I = sh.info[it & (INFOS - 1)];
-            int flags = 0, n = 0, h = 0, t0 = 0, valid = 0, chunk = 0;
+            const int s = it < 0 ? 0 : it % STAGES;
+            const Record &I = sh.rec[s];
+            bool ends = false;
+            int n = 0, h = 0, t0 = 0, valid = 0, chunk = 0;
             bool dirty = false;
             float o[TOKENS];
+            unsigned short dr[FULL ? TOKENS : 1];
             if (it >= 0) ok = ok && wait(sh.acc_full[set], it / SETS);
             if (ok && it >= 0) {
                 tc_fence_after();
-                flags = I.item.flags;
-                n = I.item.n;
-                h = I.item.h;
-                t0 = I.item.t0;
-                valid = I.item.valid;
-                chunk = I.item.chunk;
-                dirty = I.dirty;
+                ends = I.pos == I.chunks - 1;
+                n = I.n;
+                h = I.h;
+                t0 = I.t0;
+                valid = I.valid;
+                chunk = I.chunk;
+                dirty = sh.dirty[s];
+                if (STATES) {
+                    units += I.units;
+                    lost = lost || I.lost;
+                }
                 const float keep = I.keep;
-                const int poison = dirty ? I.poison[b] : NONE;
+                const int poison = dirty ? sh.poison[s][b] : NONE;
 #pragma unroll
                 for (int q = 0; q < COLS / 16; ++q) {
                     uint32_t r[16];
@@ -825,7 +814,14 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.acc_free[set]));
+                if (lane == 0) arrive_relaxed(sh.acc_free[set]);
+                if constexpr (FULL)
+                    if (dots) {
+                        const int left = in_b ? valid - TOKENS * part : 0;
+                        const char *const r = uniform(reinterpret_cast<const char *>(dot_rows + ((size_t)(t0 + TOKENS * part) * dot_heads + (dot_shared ? I.hk : h)) * jb));
+#pragma unroll
+                        for (int i = 0; i < TOKENS; ++i) dr[i] = load_if(i < left, r + (2 * b + i * dot_step));
+                    }
                 if constexpr (!STATES) {
                     ok = wait(sh.o1_full, it);
                     if (ok) {
@@ -851,8 +847,8 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
             if (ok) {
                 // where the state goes: to an anchor, to the caller, to the piece that goes on
                 const int behind = reverse ? chunk * C : chunk * C + valid, begin = t0 - chunk * C;
-                const bool at_anchor = anchors && it >= 0 && (reverse ? chunk > 0 && behind % kAnchor == 0 : (flags & kEnds) ? last_anchor : behind % kAnchor == 0);
-                const bool to_last = !STATES && (flags & kEnds) && last, to_piece = STATES && it == items - 1;       // (flags of -1: none)
+                const bool at_anchor = anchors && it >= 0 && (reverse ? chunk > 0 && behind % kAnchor == 0 : ends ? last_anchor : behind % kAnchor == 0);
+                const bool to_last = !STATES && ends && last, to_piece = STATES && it == items - 1;
                 if (at_anchor || to_last || to_piece) {
 #pragma unroll 1
                     for (int k = 0; k < 2; ++k) {
@@ -883,9 +879,9 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 }
                 // the next chunk's state goes out before this one's rows: the products with it run meanwhile
                 if (it + 1 < items) {
-                    ok = wait(sh.info_full[(it + 1) % INFOS], (it + 1) / INFOS);
+                    ok = wait(sh.full[(it + 1) % STAGES], (it + 1) / STAGES);
                     if (ok) {
-                        enter(sh.info[(it + 1) % INFOS]);
+                        enter(it + 1);
                         if (!STATES) hand_over();
                     }
                 }
@@ -893,7 +889,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
             if (it < 0) continue;
             if constexpr (STATES) {
                 __syncwarp();
-                if (ok && lane == 0) mbar_arrive(smem_u32(&sh.info_free[it % INFOS]));
+                if (ok && lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));
                 if (!ok) break;
             } else {
                 // a channel a lane, a token a store: 64 bytes of a row a warp
@@ -901,24 +897,20 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 const int left = in_b ? valid - TOKENS * part : 0;
                 if (FULL && dots) {
                     // the dots of the warp's channels, and the term of the token itself, which is in the rows but not in them
-                    const int s = it % STAGES;
-                    const char *const r = uniform(reinterpret_cast<const char *>(dot_rows + ((size_t)(t0 + TOKENS * part) * dot_heads + (dot_shared ? I.item.hk : h)) * jb));
                     const uint8_t *const z = sm + s * M::STAGE + M::Z + (b >> 6) * TILE + part * TOKENS * 128 + (b & 7) * 2;
                     float d[TOKENS];
 #pragma unroll
-                    for (int i = 0; i < TOKENS; ++i) d[i] = load_bf16_if(i < left, r + (2 * b + i * dot_step));
+                    for (int i = 0; i < TOKENS; i += 4) {
+                        const float4 own = *reinterpret_cast<const float4 *>(&sh.own[s][TOKENS * part + i]);
 #pragma unroll
-                    for (int i = 0; i < TOKENS; ++i) d[i] = i < left ? d[i] * o[i] : 0.f;
-#pragma unroll
-                    for (int i = 0; i < TOKENS; ++i) {
-                        const unsigned short w = *reinterpret_cast<const unsigned short *>(z + i * 128 + (((b >> 3) ^ i) & 7) * 16);
-                        o[i] = fmaf(I.own[TOKENS * part + i], __uint_as_float((uint32_t)w << 16), o[i]);
+                        for (int u = 0; u < 4; ++u) {
+                            const unsigned short w = *reinterpret_cast<const unsigned short *>(z + (i + u) * 128 + (((b >> 3) ^ (i + u)) & 7) * 16);
+                            d[i + u] = i + u < left ? __uint_as_float((uint32_t)dr[i + u] << 16) * o[i + u] : 0.f;
+                            o[i + u] = fmaf(u == 0 ? own.x : u == 1 ? own.y : u == 2 ? own.z : own.w, __uint_as_float((uint32_t)w << 16), o[i + u]);
+                        }
                     }
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(smem_u32(&sh.info_free[it % INFOS]));        // (an arrival behind the stores would wait for them)
-                        mbar_arrive(smem_u32(&sh.empty[s]));
-                    }
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));          // (an arrival behind the stores would wait for them)
                     // sums over the lanes, half of the tokens given away at each step
 #pragma unroll
                     for (int w = 8; w; w >>= 1)
@@ -933,7 +925,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                     if (!(lane & 1) && t < valid) dots_at[((size_t)(warp & 3) * A.c.T + t0 + t) * H + h] = d[0];
                 } else {
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.info_free[it % INFOS]));
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));
                 }
                 // (one address for the warp and 32-bit offsets: short code)
                 char *const rows = uniform(out + ((size_t)(t0 + TOKENS * part) * H + h) * jb * (FULL && !out_bf16 ? 4 : 2));
@@ -946,6 +938,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 }
             }
         }
+        if (STATES && threadIdx.x == CTL + PREP) A.head[job * A.pieces + piece].keep = lost ? __int_as_float(0x7fffffff) : exp2_units(units);
     }
     tc_fence_before();
     __syncthreads();
@@ -1000,7 +993,10 @@ constexpr int MOST_PIECES = 160;
 
 }  // namespace
 
-size_t tc_workspace() { return (size_t)MOST_PIECES * (2 * D * D * sizeof(float) + sizeof(Head)); }
+// The pieces' states, kept first states and heads, the number of records, and the records of up to two directions.
+static size_t fixed_part() { return ((size_t)MOST_PIECES * (2 * D * D * sizeof(float) + sizeof(Head)) + 8 + 255) & ~size_t(255); }
+static size_t records(int N, int T, int H) { return ((size_t)T / C + N) * H * sizeof(Record); }
+size_t tc_workspace(int N, int T, int H, int directions) { return fixed_part() + records(N, T, H) * directions; }
 
 cudaError_t launch_scan_tc(const Call &c, cudaStream_t s) {
     int dev = 0, sms = 0;
@@ -1012,22 +1008,18 @@ cudaError_t launch_scan_tc(const Call &c, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     TcArgs A{};
     A.c = c;
-    A.group = 1;
-    for (int j = 0; j < c.jobs; ++j)
-        for (const Rows *r : {&c.job[j].x, &c.job[j].y, &c.job[j].z})
-            if (r->share > A.group) A.group = r->share;
     A.rows = c.T < C ? (c.T < 1 ? 1 : c.T) : C;
     int maps = 0;
     const void *of[4] = {};
     for (int j = 0; j < c.jobs; ++j) {
-        const Rows *rows[3] = {&c.job[j].x, &c.job[j].y, &c.job[j].z};
-        int *at[3] = {&A.x[j], &A.y[j], &A.z[j]};
-        for (int u = 0; u < 3; ++u) {
+        const Rows *rows[4] = {&c.job[j].x, &c.job[j].y, &c.job[j].z, &c.job[j].r};
+        int *at[4] = {&A.x[j], &A.y[j], &A.z[j], &A.r[j]};
+        for (int u = 0; u < (c.job[j].dots ? 4 : 3); ++u) {
             int m = 0;
             while (m < maps && of[m] != rows[u]->p) ++m;
             if (m == maps) {
                 of[maps++] = rows[u]->p;
-                if ((e = make_map(&A.map[m], rows[u]->p, c.T, c.H / rows[u]->share, u == 2 ? c.job[j].b : c.job[j].a, A.rows)) != cudaSuccess) return e;
+                if ((e = make_map(&A.map[m], rows[u]->p, c.T, c.H / rows[u]->share, u >= 2 ? c.job[j].b : c.job[j].a, A.rows)) != cudaSuccess) return e;
             }
             *at[u] = m;
         }
@@ -1038,6 +1030,34 @@ cudaError_t launch_scan_tc(const Call &c, cudaStream_t s) {
     A.kept = A.state + (size_t)MOST_PIECES * D * D;
     A.head = reinterpret_cast<Head *>(A.kept + (size_t)MOST_PIECES * D * D);
     if (!c.job[0].first || c.job[0].first != c.job[0].last) A.kept = nullptr;
+    PlanArgs P{};
+    P.g = c.g;
+    P.cu = c.cu;
+    P.fixed = c.fixed;
+    P.N = c.N;
+    P.T = c.T;
+    P.H = c.H;
+    P.group = 1;
+    P.total = reinterpret_cast<long long *>(A.head + MOST_PIECES);
+    A.total = P.total;
+    for (int j = 0; j < c.jobs; ++j) {
+        const Job &b = c.job[j];
+        for (const Rows *r : {&b.x, &b.y, &b.z})
+            if (r->share > P.group) P.group = r->share;
+        int k = 0;
+        while (k < P.variants && (P.reverse[k] != b.reverse || P.sp[k] != b.sp || P.sc[k] != b.sc || P.sw[k] != b.sw)) ++k;
+        if (k == P.variants) {
+            P.reverse[k] = b.reverse;
+            P.sp[k] = b.sp;
+            P.sc[k] = b.sc;
+            P.sw[k] = b.sw;
+            P.rec[k] = reinterpret_cast<Record *>(static_cast<char *>(c.pieces) + fixed_part() + k * records(c.N, c.T, c.H));
+            ++P.variants;
+        }
+        A.rec[j] = P.rec[k];
+    }
+    plan_kernel<<<2 * sms, PLAN_THREADS, 0, s>>>(P);
+    count_launch();
     // one short sequence: every piece is a whole pair
     const long long longest = c.T / C + 1;
     const bool cut = !(c.N == 1 && longest <= A.least && c.H <= A.pieces);
