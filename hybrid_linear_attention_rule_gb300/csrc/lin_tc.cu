@@ -39,11 +39,12 @@ constexpr uint32_t kTries = 1u << 20;            // a second or two
 enum Kind { kStates, kPlain, kFull };      // states alone; jobs whose operands are in two parts and that put out nothing but BF16 rows; any, in three parts
 
 constexpr uint32_t TILE = C * 128;                                 // 64 rows of 64 BF16 values
-// Shared memory: a ring of copies (y0 [x0] y1 [x1] z0 z1), parts of [Yw0 | Yw1 | P] (twice for the states, whose products then have no gap).
+// Shared memory: a ring of copies (y0 [x0] y1 [x1] z0 z1 [r0 r1]), parts of [Yw0 | Yw1 | P] (twice for the states, whose products then have no
+// gap).  The rows put out stand in the place of x, once it has been used, until their copy has taken them.
 template <Kind K> struct Map {
     static constexpr bool X = K != kStates;
-    static constexpr int STAGES = 3, SETS = K == kStates ? 2 : 1;
-    static constexpr uint32_t Y = 0, XT = TILE, ATOM = (X ? 2 : 1) * TILE, Z = 2 * ATOM, STAGE = Z + 2 * TILE;
+    static constexpr int STAGES = K == kFull ? 2 : 3, SETS = K == kStates ? 2 : 1;
+    static constexpr uint32_t Y = 0, XT = TILE, ATOM = (X ? 2 : 1) * TILE, Z = 2 * ATOM, R = Z + 2 * TILE, STAGE = R + (K == kFull ? 2 : 0) * TILE;
     static constexpr uint32_t OPS = STAGES * STAGE, PART = (X ? 3 : 2) * TILE, SET = K == kPlain ? 2 * PART + 2 * TILE : 3 * PART;
     static constexpr uint32_t INFO = OPS + SETS * SET;
 };
@@ -68,7 +69,7 @@ struct Shared {
     unsigned char poison[3][D];        // of a z that is not finite: the channel's first such token in the job's direction, or NONE
     int dirty[3];              // whether there is one
     int dead;
-    unsigned long long full[3], empty[3], pt_full, pt_free, prep_full, acc_full[2], acc_free[2], sop_full, o1_full, drain[2];
+    unsigned long long full[3], empty[3], pt_full, pt_free, prep_full, acc_full[2], acc_free[2], sop_full, o1_full, out_full, drain[2];
     uint32_t tmem;
 };
 constexpr int NONE = 255;
@@ -86,6 +87,7 @@ struct Head {                  // of a piece's state
 struct TcArgs {
     CUtensorMap map[4];
     Call c;
+    CUtensorMap out[3];        // the jobs' outputs, where they are BF16
     int x[3], y[3], z[3], r[3];        // the jobs' maps
     int rows;                  // of a copy's box
     int pieces;                // a job
@@ -112,17 +114,12 @@ __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0
 __device__ __forceinline__ void arrive_relaxed(const unsigned long long &bar) {
     asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&bar)) : "memory");
 }
-// Stores and loads under a predicate, without a branch around each.
+// Stores under a predicate, without a branch around each.
 __device__ __forceinline__ void store_if(bool on, char *to, __nv_bfloat16 v) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.b16 [%0], %1;\n\t}" ::"l"(to), "h"(__bfloat16_as_ushort(v)), "r"((int)on) : "memory");
 }
 __device__ __forceinline__ void store_if(bool on, char *to, float v) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.f32 [%0], %1;\n\t}" ::"l"(to), "f"(v), "r"((int)on) : "memory");
-}
-__device__ __forceinline__ unsigned short load_if(bool on, const char *from) {
-    unsigned short v;
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t@p ld.global.nc.b16 %0, [%1];\n\t}" : "=h"(v) : "l"(from), "r"((int)on));
-    return v;
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t x);
 __device__ __forceinline__ char *uniform(const char *p) {
@@ -375,7 +372,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
     if (tid == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&sh.full[s]), 1);
-            mbar_init(smem_u32(&sh.empty[s]), (STATES ? 1 : 2) + HOLD / 32);
+            mbar_init(smem_u32(&sh.empty[s]), STATES ? 1 + HOLD / 32 : 3);
             sh.dirty[s] = 0;
         }
         for (int s = 0; s < 2; ++s) {
@@ -388,6 +385,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
         mbar_init(smem_u32(&sh.prep_full), PREP / 32);
         mbar_init(smem_u32(&sh.sop_full), HOLD / 32);
         mbar_init(smem_u32(&sh.o1_full), 1);
+        mbar_init(smem_u32(&sh.out_full), HOLD / 32);
         fence_mbar_init();
         sh.dead = 0;
     }
@@ -411,7 +409,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
             // ---------------- copies ----------------
             const void *mx = &A.map[A.x[job]], *my = &A.map[A.y[job]], *mz = &A.map[A.z[job]], *mr = FULL ? &A.map[A.r[job]] : nullptr;
             const bool sx = J.x.share > 1, sy = J.y.share > 1, sz = J.z.share > 1, sr = FULL && J.r.share > 1;
-            const uint32_t bytes = (uint32_t)(STATES ? 4 : 6) * A.rows * 128 + (uint32_t)sizeof(Record);
+            const uint32_t bytes = (uint32_t)(STATES ? 4 : FULL && dots ? 8 : 6) * A.rows * 128 + (uint32_t)sizeof(Record);
             int at_t0 = 0, at_h = 0, at_hk = 0;                      // of 32 chunks, one a lane
             int it = 0;
             for (; it < items; ++it) {
@@ -447,7 +445,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                     for (int u = 0; u < 2; ++u) tma_load_3d(to + M::Z + u * TILE, mz, 64 * u, sz ? hk : h, t0, bar);
                     if (FULL && dots)
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) tma_prefetch_3d(mr, 64 * u, sr ? hk : h, t0);
+                        for (int u = 0; u < 2; ++u) tma_load_3d(to + M::R + u * TILE, mr, 64 * u, sr ? hk : h, t0, bar);
                 }
                 __syncwarp();
                 // the next chunk on its way to L2: its copy, once there is room for it, is then a short one
@@ -461,6 +459,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                             tma_prefetch_3d(my, 64 * u, sy ? hk : h, t0);
                             if (!STATES) tma_prefetch_3d(mx, 64 * u, sx ? hk : h, t0);
                             tma_prefetch_3d(mz, 64 * u, sz ? hk : h, t0);
+                            if (FULL && dots) tma_prefetch_3d(mr, 64 * u, sr ? hk : h, t0);
                         }
                     }
                     __syncwarp();
@@ -546,6 +545,28 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
             if (elect()) mma_commit(smem_u32(&sh.drain[1]));
 #pragma unroll 1
             for (uint32_t i = 0; i < kTries && !mbar_try_wait(smem_u32(&sh.drain[1]), 0); ++i) {}
+        } else if (!STATES) {
+            // ---------------- rows out ----------------
+            const void *const map = &A.out[job];
+            const bool copied = J.out_bf16;
+            const int jb = J.b;
+            for (int it = 0; it < items; ++it) {
+                const int s = it % STAGES;
+                if (!wait(sh.out_full, it)) break;
+                const Record &I = sh.rec[s];
+                if (lane == 0) {
+                    if (copied && I.valid == C) {
+                        const uint32_t at = sm32 + s * M::STAGE + M::XT;
+                        tma_store_3d(map, at, 0, I.h, I.t0);
+                        if (jb > 64) tma_store_3d(map, at + M::ATOM, 64, I.h, I.t0);
+                        bulk_commit();
+                        bulk_wait_read_all();
+                    }
+                    mbar_arrive(smem_u32(&sh.empty[s]));
+                }
+                __syncwarp();
+            }
+            if (lane == 0) bulk_wait_all();
         }
     } else if (warp < HOLD_WARP) {
         // ---------------- scores and keys as operands ----------------
@@ -703,10 +724,6 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
         float *const last = J.last, *const anchors = FULL ? J.anchors : nullptr, *const dots_at = J.dots;
         const bool last_anchor = J.last_anchor;
         char *const out = static_cast<char *>(J.out);
-        const __nv_bfloat16 *const dot_rows = static_cast<const __nv_bfloat16 *>(J.r.p);
-        const int dot_heads = dots ? H / J.r.share : 1;
-        const uint32_t dot_step = (uint32_t)dot_heads * jb * 2;
-        const bool dot_shared = dots && J.r.share > 1;
         const uint32_t row_step = (uint32_t)H * jb * (FULL && !out_bf16 ? 4 : 2);
         float S[COLS];
 #pragma unroll
@@ -777,7 +794,6 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
             int n = 0, h = 0, t0 = 0, valid = 0, chunk = 0;
             bool dirty = false;
             float o[TOKENS];
-            unsigned short dr[FULL ? TOKENS : 1];
             if (it >= 0) ok = ok && wait(sh.acc_full[set], it / SETS);
             if (ok && it >= 0) {
                 tc_fence_after();
@@ -815,13 +831,6 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_relaxed(sh.acc_free[set]);
-                if constexpr (FULL)
-                    if (dots) {
-                        const int left = in_b ? valid - TOKENS * part : 0;
-                        const char *const r = uniform(reinterpret_cast<const char *>(dot_rows + ((size_t)(t0 + TOKENS * part) * dot_heads + (dot_shared ? I.hk : h)) * jb));
-#pragma unroll
-                        for (int i = 0; i < TOKENS; ++i) dr[i] = load_if(i < left, r + (2 * b + i * dot_step));
-                    }
                 if constexpr (!STATES) {
                     ok = wait(sh.o1_full, it);
                     if (ok) {
@@ -892,25 +901,45 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 if (ok && lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));
                 if (!ok) break;
             } else {
-                // a channel a lane, a token a store: 64 bytes of a row a warp
                 if (!ok) break;
-                const int left = in_b ? valid - TOKENS * part : 0;
+                // where channel b of a token stands in a tile: piece (b / 8) ^ (token & 7) of the token's row
+                const uint32_t tile = (b >> 6) * TILE + part * TOKENS * 128 + (b & 7) * 2;
+                uint8_t *const stage = sm + s * M::STAGE;
+                float d[FULL ? TOKENS : 1];
                 if (FULL && dots) {
                     // the dots of the warp's channels, and the term of the token itself, which is in the rows but not in them
-                    const uint8_t *const z = sm + s * M::STAGE + M::Z + (b >> 6) * TILE + part * TOKENS * 128 + (b & 7) * 2;
-                    float d[TOKENS];
+                    const int left = in_b ? valid - TOKENS * part : 0;
 #pragma unroll
-                    for (int i = 0; i < TOKENS; i += 4) {
-                        const float4 own = *reinterpret_cast<const float4 *>(&sh.own[s][TOKENS * part + i]);
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const unsigned short w = *reinterpret_cast<const unsigned short *>(z + (i + u) * 128 + (((b >> 3) ^ (i + u)) & 7) * 16);
-                            d[i + u] = i + u < left ? __uint_as_float((uint32_t)dr[i + u] << 16) * o[i + u] : 0.f;
-                            o[i + u] = fmaf(u == 0 ? own.x : u == 1 ? own.y : u == 2 ? own.z : own.w, __uint_as_float((uint32_t)w << 16), o[i + u]);
-                        }
+                    for (int i = 0; i < TOKENS; ++i) {
+                        const uint32_t at = tile + i * 128 + (((b >> 3) ^ i) & 7) * 16;
+                        const unsigned short r = *reinterpret_cast<const unsigned short *>(stage + M::R + at), z = *reinterpret_cast<const unsigned short *>(stage + M::Z + at);
+                        d[i] = i < left ? __uint_as_float((uint32_t)r << 16) * o[i] : 0.f;
+                        o[i] = fmaf(sh.own[s][TOKENS * part + i], __uint_as_float((uint32_t)z << 16), o[i]);
                     }
+                }
+                if (valid == C && (!FULL || out_bf16)) {
+                    // (x, in whose place they go, has been used)
+                    uint8_t *const x = stage + M::XT + (b >> 6) * (M::ATOM - TILE) + tile;
+#pragma unroll
+                    for (int i = 0; i < TOKENS; ++i) *reinterpret_cast<__nv_bfloat16 *>(x + i * 128 + (((b >> 3) ^ i) & 7) * 16) = __float2bfloat16_rn(o[i]);
+                    fence_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));          // (an arrival behind the stores would wait for them)
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.out_full));
+                } else {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.out_full));          // (an arrival behind the stores would wait for them)
+                    // a channel a lane, a token a store; one address for the warp and 32-bit offsets
+                    const int left = in_b ? valid - TOKENS * part : 0;
+                    char *const rows = uniform(out + ((size_t)(t0 + TOKENS * part) * H + h) * jb * (FULL && !out_bf16 ? 4 : 2));
+                    if (FULL && !out_bf16) {
+#pragma unroll
+                        for (int i = 0; i < TOKENS; ++i) store_if(i < left, rows + (4 * b + i * row_step), o[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < TOKENS; ++i) store_if(i < left, rows + (2 * b + i * row_step), __float2bfloat16_rn(o[i]));
+                    }
+                }
+                if (FULL && dots) {
                     // sums over the lanes, half of the tokens given away at each step
 #pragma unroll
                     for (int w = 8; w; w >>= 1)
@@ -923,18 +952,6 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                     d[0] += __shfl_xor_sync(0xffffffffu, d[0], 1);
                     const int t = TOKENS * part + (lane >> 1);
                     if (!(lane & 1) && t < valid) dots_at[((size_t)(warp & 3) * A.c.T + t0 + t) * H + h] = d[0];
-                } else {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));
-                }
-                // (one address for the warp and 32-bit offsets: short code)
-                char *const rows = uniform(out + ((size_t)(t0 + TOKENS * part) * H + h) * jb * (FULL && !out_bf16 ? 4 : 2));
-                if (FULL && !out_bf16) {
-#pragma unroll
-                    for (int i = 0; i < TOKENS; ++i) store_if(i < left, rows + (4 * b + i * row_step), o[i]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < TOKENS; ++i) store_if(i < left, rows + (2 * b + i * row_step), __float2bfloat16_rn(o[i]));
                 }
             }
         }
@@ -1024,6 +1041,8 @@ cudaError_t launch_scan_tc(const Call &c, cudaStream_t s) {
             *at[u] = m;
         }
     }
+    for (int j = 0; j < c.jobs; ++j)
+        if (c.job[j].out_bf16 && (e = make_map(&A.out[j], c.job[j].out, c.T, c.H, c.job[j].b, A.rows)) != cudaSuccess) return e;
     A.pieces = (sms < MOST_PIECES ? sms : MOST_PIECES) / c.jobs;
     A.least = 16;
     A.state = static_cast<float *>(c.pieces);
