@@ -68,7 +68,7 @@ struct Job {
     // for the gradient of the decays: dots[t, h] = sum_c r[t, c] (out[t, c] without the term j = i), and the states at the anchors
     Rows r;
     float *dots;           // [slices][T, H], or null
-    float *anchors;        // [anchor_slots, H, a, b], or null; the state entering the anchor (forward) or leaving it (backward)
+    float *anchors;        // [anchor_slots, H] states laid out as first, or null; the state entering the anchor (forward) or leaving it (backward)
     int last_anchor;       // forward: the last state is an anchor too
 };
 

@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const __grid_constant__ C
         if (J.anchors && !J.reverse && it > 0 && chunk * C % kAnchor == 0) {
             float *to = J.anchors + ((size_t)(anchor_slot(begin, n) + chunk * C / kAnchor - 1) * A.H + h) * a * J.b;
             for (int i = tid; i < a * kSlice; i += THREADS)
-                if (i % kSlice < nb) to[(size_t)(i / kSlice) * J.b + b0 + i % kSlice] = S[i / kSlice * PITCH_S + i % kSlice];
+                if (i % kSlice < nb) to[(size_t)(i / kSlice) * J.sa + (size_t)(b0 + i % kSlice) * J.sb] = S[i / kSlice * PITCH_S + i % kSlice];
         }
         for (int i = tid; i < C * a; i += THREADS) {
             const int t = i / a, c = i % a;
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const __grid_constant__ C
             __syncthreads();
             float *to = J.anchors + ((size_t)(anchor_slot(begin, n) + chunk * C / kAnchor - 1) * A.H + h) * a * J.b;
             for (int i = tid; i < a * kSlice; i += THREADS)
-                if (i % kSlice < nb) to[(size_t)(i / kSlice) * J.b + b0 + i % kSlice] = S[i / kSlice * PITCH_S + i % kSlice];
+                if (i % kSlice < nb) to[(size_t)(i / kSlice) * J.sa + (size_t)(b0 + i % kSlice) * J.sb] = S[i / kSlice * PITCH_S + i % kSlice];
         }
     }
     __syncthreads();
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const __grid_constant__ C
         const float v = S[c * PITCH_S + b];
         if (J.last && slot >= 0) J.last[state + (size_t)c * J.sa + (size_t)(b0 + b) * J.sb] = v;
         if (J.anchors && J.last_anchor)
-            J.anchors[((size_t)(anchor_slot(begin, n) + max(0, len - 1) / kAnchor) * A.H + h) * a * J.b + (size_t)c * J.b + b0 + b] = v;
+            J.anchors[((size_t)(anchor_slot(begin, n) + max(0, len - 1) / kAnchor) * A.H + h) * a * J.b + (size_t)c * J.sa + (size_t)(b0 + b) * J.sb] = v;
     }
 }
 

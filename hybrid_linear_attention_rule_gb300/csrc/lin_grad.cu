@@ -12,7 +12,7 @@ namespace k3kda {
 namespace lin {
 namespace {
 
-// f at the anchors: <S, R> with S [dv, dk] and R [dk, dv].  A CTA for each (anchor, head); tiles of 32 x 32 turned in shared memory.
+// f at the anchors: <S, R>, both [dk, dv].  A CTA for each (anchor, head).
 struct AnchorArgs {
     const float *S, *R, *dlast;       // dlast [N, H, dk, dv] or null
     double *f;                        // [slots, H]
@@ -20,10 +20,9 @@ struct AnchorArgs {
     int N, T, H, dk, dv;
 };
 
-__global__ void __launch_bounds__(256) anchor_kernel(const __grid_constant__ AnchorArgs A) {
-    __shared__ float turned[32][33];
-    __shared__ double part[8];
-    const int h = blockIdx.y, tx = threadIdx.x % 32, ty = threadIdx.x / 32;
+__global__ void __launch_bounds__(512) anchor_kernel(const __grid_constant__ AnchorArgs A) {
+    __shared__ double part[16];
+    const int h = blockIdx.y, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     for (int n = blockIdx.x; n < A.N; n += gridDim.x) {
         int begin, end;
         seq_bounds(A.cu, n, A.T, begin, end);
@@ -35,24 +34,19 @@ __global__ void __launch_bounds__(256) anchor_kernel(const __grid_constant__ Anc
             double sum = 0.0;
             if (R) {
                 const float *S = A.S + at * A.dk * A.dv;
-                for (int i = 0; i < A.dk; i += 32)
-                    for (int j = 0; j < A.dv; j += 32) {
-                        __syncthreads();
-                        for (int u = ty; u < 32; u += 8) turned[u][tx] = j + u < A.dv && i + tx < A.dk ? S[(size_t)(j + u) * A.dk + i + tx] : 0.f;
-                        __syncthreads();
-                        float acc = 0.f;
-                        for (int u = ty; u < 32; u += 8)
-                            if (i + u < A.dk && j + tx < A.dv) acc = fmaf(turned[tx][u], R[(size_t)(i + u) * A.dv + j + tx], acc);
-                        sum += acc;
-                    }
+                const int quads = A.dk * A.dv / 4;
+#pragma unroll 4
+                for (int i = threadIdx.x; i < quads; i += 512) {
+                    const float4 x = reinterpret_cast<const float4 *>(S)[i], y = reinterpret_cast<const float4 *>(R)[i];
+                    sum += fmaf(x.w, y.w, fmaf(x.z, y.z, fmaf(x.y, y.y, x.x * y.x)));
+                }
                 for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (tx == 0) part[ty] = sum;
             }
+            if (lane == 0) part[warp] = sum;
             __syncthreads();
             if (threadIdx.x == 0) {
                 sum = 0.0;
-                if (R)
-                    for (int u = 0; u < 8; ++u) sum += part[u];
+                for (int u = 0; u < 16; ++u) sum += part[u];
                 A.f[at] = sum;
             }
             __syncthreads();
@@ -60,7 +54,7 @@ __global__ void __launch_bounds__(256) anchor_kernel(const __grid_constant__ Anc
     }
 }
 
-// dg: a CTA sums one stretch between anchors for 32 heads, a head a lane, 16 runs of tokens a warp each.
+// dg: a CTA sums one stretch between anchors for 8 heads (a 32-byte piece of a row), 64 runs of 8 tokens, each a thread a head.
 struct SumArgs {
     const float *r1, *r2;             // [slices][T, H]
     int n1, n2;                       // slices
@@ -71,38 +65,42 @@ struct SumArgs {
 };
 
 __global__ void __launch_bounds__(512) sum_kernel(const __grid_constant__ SumArgs A) {
-    __shared__ double part[16][33];
-    constexpr int RUN = kAnchor / 16;
-    const int lane = threadIdx.x % 32, ty = threadIdx.x / 32, h = blockIdx.y * 32 + lane;
+    constexpr int RUN = 8, RUNS = kAnchor / RUN;
+    __shared__ double part[RUNS][9];
+    const int hl = threadIdx.x % 8, run = threadIdx.x / 8, h = blockIdx.y * 8 + hl;
     const size_t TH = (size_t)A.T * A.H;
     for (int n = blockIdx.x; n < A.N; n += gridDim.x) {
         int begin, end;
         seq_bounds(A.cu, n, A.T, begin, end);
         const int count = (end - begin + kAnchor - 1) / kAnchor;
         for (int k = blockIdx.z; k < count; k += gridDim.z) {
-            const int t0 = begin + k * kAnchor + ty * RUN, t1 = min(t0 + RUN, end);
-            float x[RUN];
+            const int t0 = begin + k * kAnchor + run * RUN, t1 = min(t0 + RUN, end);
+            float p[RUN], q[RUN];
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) p[i] = q[i] = 0.f;
+            if (h < A.H) {
+#pragma unroll 4
+                for (int u = 0; u < A.n1; ++u)
+#pragma unroll
+                    for (int i = 0; i < RUN; ++i)
+                        if (t0 + i < t1) p[i] += A.r1[u * TH + (size_t)(t0 + i) * A.H + h];
+#pragma unroll 4
+                for (int u = 0; u < A.n2; ++u)
+#pragma unroll
+                    for (int i = 0; i < RUN; ++i)
+                        if (t0 + i < t1) q[i] += A.r2[u * TH + (size_t)(t0 + i) * A.H + h];
+            }
             double sum = 0.0;
 #pragma unroll
-            for (int i = 0; i < RUN; ++i) {
-                x[i] = 0.f;
-                if (h < A.H && t0 + i < t1) {
-                    const size_t at = (size_t)(t0 + i) * A.H + h;
-                    float p = 0.f, q = 0.f;
-                    for (int u = 0; u < A.n1; ++u) p += A.r1[u * TH + at];
-                    for (int u = 0; u < A.n2; ++u) q += A.r2[u * TH + at];
-                    x[i] = p - q;
-                }
-                sum += x[i];
-            }
-            part[ty][lane] = sum;
+            for (int i = 0; i < RUN; ++i) sum += p[i] - q[i];
+            part[run][hl] = sum;
             __syncthreads();
             if (h < A.H) {
                 double f = A.f[(size_t)(anchor_slot(begin, n) + k) * A.H + h];
-                for (int u = 15; u > ty; --u) f += part[u][lane];
+                for (int u = RUNS - 1; u > run; --u) f += part[u][hl];
 #pragma unroll
                 for (int i = RUN - 1; i >= 0; --i) {
-                    f += x[i];
+                    f += p[i] - q[i];
                     if (t0 + i < t1) A.dg[(size_t)(t0 + i) * A.H + h] = (float)f;
                 }
             }
@@ -311,11 +309,11 @@ cudaError_t launch_lin_backward(const LinArgs &a, const void *dO, const float *d
         const unsigned deep = (unsigned)(a.T / kAnchor / seqs + 1 < 256 ? a.T / kAnchor / seqs + 1 : 256);
         double *f = reinterpret_cast<double *>(ws + w.f);
         const AnchorArgs g{part(w.S), part(w.R), dlast, f, a.cu, a.N, a.T, a.H, a.dk, a.dv};
-        anchor_kernel<<<dim3(seqs, a.H, deep), 256, 0, s>>>(g);
+        anchor_kernel<<<dim3(seqs, a.H, deep), 512, 0, s>>>(g);
         count_launch();
         float *to = a.fixed ? part(w.dg) : dg;
         const SumArgs u{part(w.r1), part(w.r2), on_tensor_cores(c) ? 4 : slices(a.dk), on_tensor_cores(c) ? 4 : slices(a.dv), f, to, a.cu, a.N, a.T, a.H};
-        sum_kernel<<<dim3(seqs, (a.H + 31) / 32, deep), 512, 0, s>>>(u);
+        sum_kernel<<<dim3(seqs, (a.H + 7) / 8, deep), 512, 0, s>>>(u);
         count_launch();
         if (a.fixed) {
             fixed_kernel<<<a.H, 512, 0, s>>>(to, dg, a.cu, a.N, a.T, a.H);

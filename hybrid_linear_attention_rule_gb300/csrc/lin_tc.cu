@@ -65,7 +65,7 @@ static_assert(sizeof(Record) % 16 == 0, "copied in 16-byte pieces");
 
 struct Shared {
     Record rec[3];
-    float own[3][C];           // P's diagonal, where it is kept apart
+    alignas(16) float own[3][C];       // P's diagonal, where it is kept apart
     unsigned char poison[3][D];        // of a z that is not finite: the channel's first such token in the job's direction, or NONE
     int dirty[3];              // whether there is one
     int dead;
@@ -624,15 +624,17 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                     for (int c = 0; c < 12; ++c)
                         if (c < (FULL ? 12 : 8)) *reinterpret_cast<uint4 *>(row_at + 2 * TILE + (c >> 2) * M::PART + (((i0 >> 3) + (c & 3)) ^ (t & 7)) * 16) = make_uint4(0, 0, 0, 0);
             } else if constexpr (!STATES) {
-                uint32_t part[FULL ? 3 : 2][16];
                 if (!wait(sh.pt_full, it)) break;
                 tc_fence_after();
                 // columns that row t is seen by, in the thread's 32, as bits
                 const uint32_t lower = 0xffffffffu >> (31 - lane), mask = t >= valid ? 0u : i0 != 32 * quarter ? 0xffffffffu : reverse ? lower : ~(lower >> 1);
+                // the diagonal stays out of P where the dots want it so, and is kept
+                const uint32_t apart = dots && i0 == 32 * quarter ? 1u << lane : 0u;
+                float own = 0.f;
                 const float fj = I.fj[t];
                 const bool plain = I.plain;
-#pragma unroll
-                for (int g = 0; g < 32; g += 8) {
+                // columns g to g + 7, in parts
+                auto group = [&](int g, uint32_t (&part)[FULL ? 3 : 2][4]) {
                     uint32_t r[8];
                     float p[8];
                     tmem_ld8(tm + ((uint32_t)quarter * 32 << 16) + PT + i0 + g, r);
@@ -656,36 +658,54 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                         }
                     }
                     tmem_wait_ld();
+                    const uint32_t seen = mask >> g, out = apart >> g;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) p[e] = mask >> (g + e) & 1 ? p[e] * __uint_as_float(r[e]) : 0.f;
-                    if (dots && i0 == 32 * quarter) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (g + e == lane) {
-                                sh.own[s][t] = p[e];
-                                p[e] = 0.f;
-                            }
+                    for (int e = 0; e < 8; ++e) {
+                        p[e] = seen >> e & 1 ? p[e] * __uint_as_float(r[e]) : 0.f;
+                        if (FULL) {
+                            own = out >> e & 1 ? p[e] : own;
+                            p[e] = out >> e & 1 ? 0.f : p[e];
+                        }
                     }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        part[0][g / 2 + e] = peel(p[2 * e], p[2 * e + 1]);
-                        if (exact) {
-                            part[1][g / 2 + e] = peel(p[2 * e], p[2 * e + 1]);
-                            if constexpr (FULL) part[2][g / 2 + e] = pack(p[2 * e], p[2 * e + 1]);
+                        part[0][e] = peel(p[2 * e], p[2 * e + 1]);
+                        if constexpr (FULL) {
+                            part[1][e] = peel(p[2 * e], p[2 * e + 1]);
+                            part[2][e] = pack(p[2 * e], p[2 * e + 1]);
                         } else {
-                            part[1][g / 2 + e] = pack(p[2 * e], p[2 * e + 1]);
+                            part[1][e] = pack(p[2 * e], p[2 * e + 1]);
                         }
                     }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.pt_free));
-                if (it >= SETS && !wait(sh.acc_full[set], it / SETS - 1)) break;
+                };
+                auto put = [&](int g, const uint32_t (&part)[FULL ? 3 : 2][4]) {
+                    uint8_t *const to = row_at + 2 * TILE + (uint32_t)(((i0 + g) >> 3) ^ (t & 7)) * 16;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint8_t *const to = row_at + 2 * TILE + (uint32_t)(((i0 >> 3) + c) ^ (t & 7)) * 16;
+                    for (int u = 0; u < (FULL ? 3 : 2); ++u) *reinterpret_cast<uint4 *>(to + u * M::PART) = make_uint4(part[u][0], part[u][1], part[u][2], part[u][3]);
+                };
+                if constexpr (FULL) {
+                    // (48 registers of three parts would not do: the copies, two stages deep, are what this waits for anyway)
+                    if (it >= SETS && !wait(sh.acc_full[set], it / SETS - 1)) break;
+#pragma unroll 1
+                    for (int g = 0; g < 32; g += 8) {
+                        uint32_t part[FULL ? 3 : 2][4];
+                        group(g, part);
+                        put(g, part);
+                    }
+                    if (apart) sh.own[s][t] = own;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_relaxed(sh.pt_free);
+                } else {
+                    uint32_t part[4][FULL ? 3 : 2][4];
 #pragma unroll
-                    for (int u = 0; u < (FULL ? 3 : 2); ++u) *reinterpret_cast<uint4 *>(to + u * M::PART) = make_uint4(part[u][4 * c], part[u][4 * c + 1], part[u][4 * c + 2], part[u][4 * c + 3]);
+                    for (int g = 0; g < 4; ++g) group(8 * g, part[g]);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_relaxed(sh.pt_free);
+                    if (it >= SETS && !wait(sh.acc_full[set], it / SETS - 1)) break;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) put(8 * g, part[g]);
                 }
             }
 #pragma unroll 1
@@ -864,8 +884,8 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                         float *to = nullptr;
                         int step = 0;
                         if (k == 0 && at_anchor) {
-                            to = anchors + ((size_t)(anchor_slot(begin, n) + max(0, behind - 1) / kAnchor) * H + h) * ja * jb + b;
-                            step = jb;
+                            to = anchors + ((size_t)(anchor_slot(begin, n) + max(0, behind - 1) / kAnchor) * H + h) * ja * jb + (size_t)b * sb;
+                            step = sa;
                         }
                         if (k == 1 && to_last) {
                             const int slot = seq_slot(A.c.slot, A.c.num_slots, n);
@@ -909,12 +929,14 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 if (FULL && dots) {
                     // the dots of the warp's channels, and the term of the token itself, which is in the rows but not in them
                     const int left = in_b ? valid - TOKENS * part : 0;
+                    float4 own;
 #pragma unroll
                     for (int i = 0; i < TOKENS; ++i) {
+                        if (i % 4 == 0) own = *reinterpret_cast<const float4 *>(&sh.own[s][TOKENS * part + i]);
                         const uint32_t at = tile + i * 128 + (((b >> 3) ^ i) & 7) * 16;
                         const unsigned short r = *reinterpret_cast<const unsigned short *>(stage + M::R + at), z = *reinterpret_cast<const unsigned short *>(stage + M::Z + at);
                         d[i] = i < left ? __uint_as_float((uint32_t)r << 16) * o[i] : 0.f;
-                        o[i] = fmaf(sh.own[s][TOKENS * part + i], __uint_as_float((uint32_t)z << 16), o[i]);
+                        o[i] = fmaf(i % 4 == 0 ? own.x : i % 4 == 1 ? own.y : i % 4 == 2 ? own.z : own.w, __uint_as_float((uint32_t)z << 16), o[i]);
                     }
                 }
                 if (valid == C && (!FULL || out_bf16)) {
