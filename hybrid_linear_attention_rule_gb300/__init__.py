@@ -825,10 +825,10 @@ def _of(t, what, shape, dtype):
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"k3lin: {what} must be a torch.Tensor or None")
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"k3lin: {what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError("k3lin: tensors must live on a CUDA device (no CPU path exists)")
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"k3lin: {what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
 

@@ -10,11 +10,12 @@
 //     dx = r_x (du post - h_x mean(du post h_x)),  h_x = x r_x              dpost = sum over rows du h_x
 // Every array is read once and written once: a row is held in registers by its threads, 16 elements each, so HBM bounds both.  Rows
 // of up to 128 channels take 8 threads, of up to 16384 a CTA of 1024; arrays move in 16-byte pieces where the width and the
-// addresses allow it, else element by element.  All arithmetic is FP32, each output is rounded once; y comes from the sum
+// addresses allow it, else element by element.  The gradient's rows are copied to shared memory two rounds ahead.  All arithmetic is FP32, each output is rounded once; y comes from the sum
 // before its rounding.
 #pragma once
 
 #include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace k3kda {
 namespace blk {
@@ -45,9 +46,7 @@ inline int parts_of(long long rows, int D) {
     return (int)(need < MOST_PARTS ? need : MOST_PARTS);
 }
 
-template <class T> struct Raw;
-template <> struct Raw<__nv_bfloat16> { static constexpr int VEC = 8; };
-template <> struct Raw<float> { static constexpr int VEC = 4; };
+template <class T> constexpr int kVec = 16 / (int)sizeof(T);
 
 template <class T> __device__ __forceinline__ float exp_of(float x) { return sizeof(T) == 2 ? __expf(x) : expf(x); }
 template <class T> __device__ __forceinline__ float inverse(float x) { return sizeof(T) == 2 ? __fdividef(1.f, x) : 1.f / x; }
@@ -56,31 +55,32 @@ template <class T> __device__ __forceinline__ float sigmoid_of(float z) { return
 
 // Thread t's elements of a row: pieces of VEC at (t + i TPR) VEC.
 template <class T, int VEC, int TPR> struct Slot {
-    static constexpr int ITEMS = E / VEC;
+    static constexpr int ITEMS = E / VEC, WORDS = VEC == 1 ? E : E * (int)sizeof(T) / 4;
     static __device__ __forceinline__ int column(int t, int e) { return (t + e / VEC * TPR) * VEC + e % VEC; }
-    static __device__ __forceinline__ void load(const void *p, long long at, int t, int D, float (&v)[E]) {
-        const T *row = static_cast<const T *>(p) + at;
+    // As they lie in memory (BF16 pieces two to a word): half the registers until they are used.
+    struct Raw { uint32_t w[WORDS]; };
+    template <bool STREAM> static __device__ __forceinline__ void fetch(const T *row, int t, int D, Raw &r) {
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
             const int c = (t + i * TPR) * VEC;
             if constexpr (VEC == 1) {
-                v[i] = c < D ? (float)row[c] : 0.f;
+                if constexpr (sizeof(T) == 2) r.w[i] = c < D ? (uint32_t)reinterpret_cast<const unsigned short *>(row)[c] << 16 : 0u;
+                else r.w[i] = c < D ? reinterpret_cast<const uint32_t *>(row)[c] : 0u;
             } else {
-                uint4 r = make_uint4(0, 0, 0, 0);
-                if (c < D) r = __ldcs(reinterpret_cast<const uint4 *>(row + c));
-                const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    if constexpr (sizeof(T) == 2) {
-                        v[i * VEC + 2 * u] = __uint_as_float(w[u] << 16);
-                        v[i * VEC + 2 * u + 1] = __uint_as_float(w[u] & 0xffff0000u);
-                    } else {
-                        v[i * VEC + u] = __uint_as_float(w[u]);
-                    }
-                }
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (c < D) v = STREAM ? __ldcs(reinterpret_cast<const uint4 *>(row + c)) : *reinterpret_cast<const uint4 *>(row + c);
+                r.w[4 * i] = v.x;
+                r.w[4 * i + 1] = v.y;
+                r.w[4 * i + 2] = v.z;
+                r.w[4 * i + 3] = v.w;
             }
         }
     }
+    static __device__ __forceinline__ float value(const Raw &r, int e) {
+        if constexpr (VEC == 1 || sizeof(T) == 4) return __uint_as_float(r.w[e]);
+        else return __uint_as_float(e & 1 ? r.w[e / 2] & 0xffff0000u : r.w[e / 2] << 16);
+    }
+    static __device__ __forceinline__ void load(const void *p, long long at, int t, int D, Raw &r) { fetch<true>(static_cast<const T *>(p) + at, t, D, r); }
     static __device__ __forceinline__ void weights(const float *p, int t, int D, float (&v)[E]) {
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
@@ -151,7 +151,7 @@ template <int TPR, int N> __device__ __forceinline__ void row_sums(float (&v)[N]
     }
 }
 
-template <class T, int VEC, int TPR> __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const __grid_constant__ Args A) {
+template <class T, int VEC, int TPR> __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR > 256 ? 1024 / TPR : VEC == 8 ? 4 : 3) norm_kernel(const __grid_constant__ Args A) {
     using S = Slot<T, VEC, TPR>;
     constexpr int THREADS = TPR < 256 ? 256 : TPR, GROUPS = THREADS / TPR;
     __shared__ float room[GROUPS * 2 * (TPR / 32 + 1) * 4];
@@ -161,87 +161,162 @@ template <class T, int VEC, int TPR> __global__ void __launch_bounds__(TPR < 256
     const bool in = row < A.rows;
     const int D = in ? A.D : 0;
     const long long at = in ? row * A.D : 0;
-    float z[E], gate[E], res[E], w[E];
-    S::load(A.x, at, t, D, z);
+    typename S::Raw x, gate, res;
+    S::load(A.x, at, t, D, x);
     if (A.gate) S::load(A.gate, at, t, D, gate);
     if (A.residual) S::load(A.residual, at, t, D, res);
+    float z[E], w[E];
+    float r = 1.f;
     if (A.post) {
         float sum[1] = {0.f};
-        S::weights(A.post, t, D, w);
 #pragma unroll
-        for (int e = 0; e < E; ++e) sum[0] = fmaf(z[e], z[e], sum[0]);
+        for (int e = 0; e < E; ++e) sum[0] = fmaf(S::value(x, e), S::value(x, e), sum[0]);
         row_sums<TPR>(sum, room, turn);
-        const float r = rsqrtf(sum[0] / A.D + A.eps);
-#pragma unroll
-        for (int e = 0; e < E; ++e) z[e] = z[e] * r * w[e];
+        r = rsqrtf(sum[0] / A.D + A.eps);
+        S::weights(A.post, t, D, w);
     }
-    if (A.gate) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float a = sigmoid_of<T>(gate[e]);
-            z[e] *= A.silu ? gate[e] * a : a;
+    for (int e = 0; e < E; ++e) {
+        z[e] = A.post ? S::value(x, e) * r * w[e] : S::value(x, e);
+        if (A.gate) {
+            const float g = S::value(gate, e), a = sigmoid_of<T>(g);
+            z[e] *= A.silu ? g * a : a;
         }
+        z[e] = A.residual ? fmaf(A.alpha, z[e], S::value(res, e)) : A.alpha * z[e];
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) z[e] = A.residual ? fmaf(A.alpha, z[e], res[e]) : A.alpha * z[e];
     if (A.s) S::store(A.s, at, t, D, z);
     if (A.pre) {
         float sum[1] = {0.f};
-        S::weights(A.pre, t, D, w);
 #pragma unroll
         for (int e = 0; e < E; ++e)
             if (S::column(t, e) < D) sum[0] = fmaf(z[e], z[e], sum[0]);
         row_sums<TPR>(sum, room, turn);
-        const float r = rsqrtf(sum[0] / A.D + A.eps);
+        r = rsqrtf(sum[0] / A.D + A.eps);
+        S::weights(A.pre, t, D, w);
 #pragma unroll
         for (int e = 0; e < E; ++e) z[e] = z[e] * r * w[e];
         S::store(A.y, at, t, D, z);
     }
 }
 
+// Rows on their way: up to five arrays' next GROUPS rows (one stretch of memory) in shared memory, two deep, while those before are worked on.
+// A copy starts and ends on 16 bytes, so it may hold up to 15 more on either side, never past the array's last whole 16; what lies behind is
+// fetched by the threads.
+template <class T, int TPR> struct Ring {
+    static constexpr int THREADS = TPR < 256 ? 256 : TPR, GROUPS = THREADS / TPR;
+    static constexpr int MOST = TPR * GROUPS * E * (int)sizeof(T) + 32;              // bytes of an array's rows
+    static constexpr int ARRAYS = 5, STAGE = ARRAYS * MOST, BYTES = 2 * STAGE;
+    static constexpr bool FITS = BYTES <= 220 * 1024;
+};
+
 // The weights' gradients: a thread keeps its columns' sums over the rows of its CTA, in a fixed order.
-template <class T, int VEC, int TPR> __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_grad_kernel(const __grid_constant__ Args A) {
+template <class T, int VEC, int TPR> __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 && sizeof(T) == 2 ? 2 : 1) norm_grad_kernel(const __grid_constant__ Args A) {
     using S = Slot<T, VEC, TPR>;
-    constexpr int THREADS = TPR < 256 ? 256 : TPR, GROUPS = THREADS / TPR;
+    using Q = Ring<T, TPR>;
+    constexpr int THREADS = Q::THREADS, GROUPS = Q::GROUPS;
+    extern __shared__ __align__(16) char ring[];
     __shared__ float room[GROUPS * 2 * (TPR / 32 + 1) * 4];
-    __shared__ float meet[GROUPS > 1 ? THREADS * E : 1];
-    const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
+    __shared__ __align__(8) unsigned long long full[2];
+    __shared__ int late;
+    const int t = threadIdx.x % TPR, group = threadIdx.x / TPR, D0 = A.D;
+    const long long step = (long long)gridDim.x * GROUPS;
     int turn = 0;
+    const T *const arrays[5] = {static_cast<const T *>(A.ds), static_cast<const T *>(A.x), static_cast<const T *>(A.gate), static_cast<const T *>(A.s_in),
+                                static_cast<const T *>(A.dy)};
+    if (threadIdx.x == 0) {
+        tc::mbar_init(tc::smem_u32(&full[0]), 1);
+        tc::mbar_init(tc::smem_u32(&full[1]), 1);
+        tc::fence_mbar_init();
+        late = 0;
+    }
+    __syncthreads();
+    // the copies of rows r0 .. r0 + GROUPS - 1 (one thread)
+    auto ask = [&](long long r0, int s) {
+        const long long n = min((long long)GROUPS, A.rows - r0);
+        uint32_t bytes = 0;
+        tc::fence_async_smem();
+#pragma unroll
+        for (int pass = 0; pass < 2; ++pass) {
+            if (pass) tc::mbar_arrive_expect_tx(tc::smem_u32(&full[s]), bytes);
+#pragma unroll
+            for (int k = 0; k < 5; ++k) {
+                if (!arrays[k]) continue;
+                const uintptr_t a = reinterpret_cast<uintptr_t>(arrays[k] + r0 * D0), z = reinterpret_cast<uintptr_t>(arrays[k] + (r0 + n) * D0),
+                                last = reinterpret_cast<uintptr_t>(arrays[k] + A.rows * D0) & ~(uintptr_t)15;
+                // (the array may begin off 16 bytes: its first piece is then the threads' too)
+                const uintptr_t first = (reinterpret_cast<uintptr_t>(arrays[k]) + 15) & ~(uintptr_t)15;
+                const uintptr_t from = max(a & ~(uintptr_t)15, first), to = min((z + 15) & ~(uintptr_t)15, last);
+                if (from >= to) continue;
+                if (!pass) bytes += (uint32_t)(to - from);
+                else tc::bulk_g2s(tc::smem_u32(ring + s * Q::STAGE + k * Q::MOST + (from - (a & ~(uintptr_t)15))), reinterpret_cast<const void *>(from), (uint32_t)(to - from), tc::smem_u32(&full[s]));
+            }
+        }
+    };
+    const long long begin = (long long)blockIdx.x * GROUPS;
+    if (Q::FITS && threadIdx.x == 0)
+        for (int s = 0; s < 2; ++s)
+            if (begin + s * step < A.rows) ask(begin + s * step, s);
     float sum_post[E], sum_pre[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) sum_post[e] = sum_pre[e] = 0.f;
-    const float inv = 1.f / A.D;
-    for (long long r0 = (long long)blockIdx.x * GROUPS; r0 < A.rows; r0 += (long long)gridDim.x * GROUPS) {
+    const float inv = 1.f / D0;
+    int it = 0;
+    for (long long r0 = begin; r0 < A.rows; r0 += step, ++it) {
+        const int s = it & 1;
         const long long row = r0 + group;
         const bool in = row < A.rows;
-        const int D = in ? A.D : 0;
-        const long long at = in ? row * A.D : 0;
-        float d[E], x[E], gate[E], s[E], dy[E], w[E];
-        S::load(A.ds, at, t, D, d);
-        if (A.x) S::load(A.x, at, t, D, x);
-        if (A.gate) S::load(A.gate, at, t, D, gate);
-        float sums[3] = {0.f, 0.f, 0.f};
+        const int D = in ? D0 : 0;
+        const long long at = in ? row * D0 : 0;
+        if (Q::FITS) {
+            bool there = false;
+            for (uint32_t i = 0; i < 1u << 20 && !there; ++i) there = tc::mbar_try_wait(tc::smem_u32(&full[s]), it >> 1 & 1);
+            if (!there) late = 1;
+        }
+        // array k's elements of this thread
+        auto row_of = [&](int k, typename S::Raw &r) {
+            if constexpr (Q::FITS) {
+                const uintptr_t a = reinterpret_cast<uintptr_t>(arrays[k] + r0 * D0), own = reinterpret_cast<uintptr_t>(arrays[k] + at);
+                S::template fetch<false>(reinterpret_cast<const T *>(ring + s * Q::STAGE + k * Q::MOST + (own - (a & ~(uintptr_t)15))), t, D, r);
+                if constexpr (VEC == 1) {
+                    // the pieces of the array's ends that no copy holds
+                    const uintptr_t first = (reinterpret_cast<uintptr_t>(arrays[k]) + 15) & ~(uintptr_t)15, last = reinterpret_cast<uintptr_t>(arrays[k] + A.rows * D0) & ~(uintptr_t)15;
+                    if (own < first || own + D * sizeof(T) > last) S::template fetch<true>(arrays[k] + at, t, D, r);
+                }
+            } else {
+                S::template fetch<true>(arrays[k] + at, t, D, r);
+            }
+        };
+        typename S::Raw sr, dyr, xr;
+        float d[E], w[E], sums[3] = {0.f, 0.f, 0.f};
         if (A.pre) {
-            S::load(A.s_in, at, t, D, s);
-            S::load(A.dy, at, t, D, dy);
+            row_of(3, sr);
+            row_of(4, dyr);
             S::weights(A.pre, t, D, w);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                sums[0] = fmaf(s[e], s[e], sums[0]);
-                sums[1] = fmaf(dy[e] * w[e], s[e], sums[1]);
+                const float v = S::value(sr, e);
+                sums[0] = fmaf(v, v, sums[0]);
+                sums[1] = fmaf(S::value(dyr, e) * w[e], v, sums[1]);
             }
         }
+        if (A.x) row_of(1, xr);
         if (A.post)
 #pragma unroll
-            for (int e = 0; e < E; ++e) sums[2] = fmaf(x[e], x[e], sums[2]);
+            for (int e = 0; e < E; ++e) sums[2] = fmaf(S::value(xr, e), S::value(xr, e), sums[2]);
         if (A.pre || A.post) row_sums<TPR>(sums, room, turn);
+        {
+            typename S::Raw dsr;
+            row_of(0, dsr);
+#pragma unroll
+            for (int e = 0; e < E; ++e) d[e] = S::value(dsr, e);
+        }
         if (A.pre) {
             const float r = rsqrtf(sums[0] * inv + A.eps), m = sums[1] * inv * r;     // m: mean(dy pre h_s)
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const float h = s[e] * r;
-                sum_pre[e] = fmaf(dy[e], h, sum_pre[e]);
-                d[e] = fmaf(r, fmaf(-h, m, dy[e] * w[e]), d[e]);
+                const float h = S::value(sr, e) * r, y = S::value(dyr, e);
+                sum_pre[e] = fmaf(y, h, sum_pre[e]);
+                d[e] = fmaf(r, fmaf(-h, m, y * w[e]), d[e]);
             }
         }
         if (A.dresidual) S::store(A.dresidual, at, t, D, d);
@@ -250,41 +325,61 @@ template <class T, int VEC, int TPR> __global__ void __launch_bounds__(TPR < 256
         const float r = A.post ? rsqrtf(sums[2] * inv + A.eps) : 1.f;
         if (A.post) S::weights(A.post, t, D, w);
         if (A.gate) {
+            typename S::Raw gr;
+            float g[E];
+            row_of(2, gr);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const float z = gate[e], a = sigmoid_of<T>(z), u = A.post ? x[e] * r * w[e] : x[e];
-                gate[e] = d[e] * u * (A.silu ? a * fmaf(z, 1.f - a, 1.f) : a * (1.f - a));
+                const float z = S::value(gr, e), a = sigmoid_of<T>(z), x = S::value(xr, e), u = A.post ? x * r * w[e] : x;
+                g[e] = d[e] * u * (A.silu ? a * fmaf(z, 1.f - a, 1.f) : a * (1.f - a));
                 d[e] *= A.silu ? z * a : a;
             }
-            S::store(A.dgate, at, t, D, gate);
+            S::store(A.dgate, at, t, D, g);
         }
         if (A.post) {
             float mean[1] = {0.f};
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                x[e] *= r;
-                sum_post[e] = fmaf(d[e], x[e], sum_post[e]);
+                const float h = S::value(xr, e) * r;
+                sum_post[e] = fmaf(d[e], h, sum_post[e]);
                 d[e] *= w[e];
-                mean[0] = fmaf(d[e], x[e], mean[0]);
+                mean[0] = fmaf(d[e], h, mean[0]);
             }
             row_sums<TPR>(mean, room, turn);
             mean[0] *= inv;
 #pragma unroll
-            for (int e = 0; e < E; ++e) d[e] = r * fmaf(-x[e], mean[0], d[e]);
+            for (int e = 0; e < E; ++e) d[e] = r * fmaf(-(S::value(xr, e) * r), mean[0], d[e]);
         }
         S::store(A.dx, at, t, D, d);
+        if (Q::FITS) {
+            __syncthreads();                                         // the stage has been read
+            if (late) {
+                // (a copy that did not come: rows that are not a number rather than wrong ones, and no more of them)
+                const float nan = __int_as_float(0x7fffffff);
+#pragma unroll
+                for (int e = 0; e < E; ++e) d[e] = sum_pre[e] = sum_post[e] = nan;
+                S::store(A.dx, at, t, D, d);
+                break;
+            }
+            if (threadIdx.x == 0 && r0 + 2 * step < A.rows) ask(r0 + 2 * step, s);
+        }
     }
+    if (late && threadIdx.x == 0)                                    // (nothing may be on its way into shared memory when the CTA ends)
+        for (int k = max(0, it - 1); k < it + 2; ++k)
+            for (uint32_t i = 0; i < 1u << 20 && !tc::mbar_try_wait(tc::smem_u32(&full[k & 1]), k >> 1 & 1); ++i) {}
+    __syncthreads();
+    float *const meet = reinterpret_cast<float *>(ring);
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         if (which ? !A.pre : !A.post) continue;
         float(&sum)[E] = which ? sum_pre : sum_post;
-        float *to = A.parts + ((long long)which * gridDim.x + blockIdx.x) * A.D;
+        float *to = A.parts + ((long long)which * gridDim.x + blockIdx.x) * D0;
         if constexpr (GROUPS > 1) {
             __syncthreads();
 #pragma unroll
             for (int e = 0; e < E; ++e) meet[group * TPR * E + S::column(t, e)] = sum[e];
             __syncthreads();
-            for (int c = threadIdx.x; c < A.D; c += THREADS) {
+            for (int c = threadIdx.x; c < D0; c += THREADS) {
                 float v = 0.f;
                 for (int g = 0; g < GROUPS; ++g) v += meet[g * TPR * E + c];
                 to[c] = v;
@@ -292,15 +387,22 @@ template <class T, int VEC, int TPR> __global__ void __launch_bounds__(TPR < 256
         } else {
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                if (S::column(t, e) < A.D) to[S::column(t, e)] = sum[e];
+                if (S::column(t, e) < D0) to[S::column(t, e)] = sum[e];
         }
     }
 }
 
 template <class T, int VEC, int TPR> cudaError_t launch(const Args &a, bool grad, cudaStream_t s) {
     constexpr int THREADS = TPR < 256 ? 256 : TPR, GROUPS = THREADS / TPR;
-    if (grad) norm_grad_kernel<T, VEC, TPR><<<(unsigned)parts_of(a.rows, a.D), THREADS, 0, s>>>(a);
-    else norm_kernel<T, VEC, TPR><<<(unsigned)((a.rows + GROUPS - 1) / GROUPS), THREADS, 0, s>>>(a);
+    if (grad) {
+        static std::atomic<uint64_t> attr{0};
+        constexpr int bytes = Ring<T, TPR>::FITS ? Ring<T, TPR>::BYTES : 0;
+        if (bytes > 0)
+            if (cudaError_t e = smem_attr_once((const void *)norm_grad_kernel<T, VEC, TPR>, bytes, attr)) return e;
+        norm_grad_kernel<T, VEC, TPR><<<(unsigned)parts_of(a.rows, a.D), THREADS, bytes, s>>>(a);
+    } else {
+        norm_kernel<T, VEC, TPR><<<(unsigned)((a.rows + GROUPS - 1) / GROUPS), THREADS, 0, s>>>(a);
+    }
     count_launch();
     return cudaGetLastError();
 }
@@ -321,7 +423,7 @@ template <class T> cudaError_t launch_type(const Args &a, bool grad, cudaStream_
     for (const void *p : {a.x, a.gate, a.residual, a.s_in, a.ds, a.dy, (const void *)a.post, (const void *)a.pre, (const void *)a.s, (const void *)a.y,
                           (const void *)a.dx, (const void *)a.dgate, (const void *)a.dresidual})
         all |= reinterpret_cast<uintptr_t>(p);
-    if (a.D % Raw<T>::VEC == 0 && (all & 15) == 0) return launch_width<T, Raw<T>::VEC>(a, grad, s);
+    if (a.D % kVec<T> == 0 && (all & 15) == 0) return launch_width<T, kVec<T>>(a, grad, s);
     return launch_width<T, 1>(a, grad, s);
 }
 

@@ -24,7 +24,7 @@ struct Args {
     int out_bf16;
 };
 
-__global__ void __launch_bounds__(THREADS) lin_decode_kernel(const Args A) {
+__global__ void __launch_bounds__(THREADS, 2) lin_decode_kernel(const Args A) {
     __shared__ float sq[128], sk[128];
     __shared__ float4 sums[THREADS];
     const int tid = threadIdx.x, part = blockIdx.x % A.parts;

@@ -1,8 +1,9 @@
 // lin_f32.cu -- linear attention's jobs (lin.cuh) on the CUDA cores, everything in FP32: the path of FP32 inputs.
 //
 // A CTA holds a [a, 32] slice of one head's state in shared memory and walks the sequence in chunks of 32 tokens, a token a
-// lane for the decays.  The four products of a chunk (x y^T, its product with z, x S, y^T z) are register tiles of 4 to 16
-// accumulators fed by 16-byte shared loads; the scores are worked out again by each slice of b.
+// lane for the decays; the next chunk's rows are on their way, in registers, meanwhile.  The four products of a chunk (x y^T, its
+// product with z, x S, y^T z) are register tiles of 4 to 16 accumulators fed by 16-byte shared loads; the scores are worked out again by
+// each slice of b.  What bounds it is the shared loads, some 5 for 16 products of a thread, and the sequence of its steps.
 #include "lin.cuh"
 
 namespace k3kda {
@@ -50,26 +51,45 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const __grid_constant__ C
     const size_t base_x = h / J.x.share, base_y = h / J.y.share, base_z = h / J.z.share;
     const size_t hx = A.H / J.x.share, hy = A.H / J.y.share, hz = A.H / J.z.share;
 
+    // A chunk's rows as 16-byte pieces: piece i of x and y is row i / (a / 4), 4 pieces a thread at most; of z row tid / 8.
+    constexpr int MOST = C * 128 / 4 / THREADS;
+    const int per_row = a / 4, pieces = C * per_row;
+    float4 nx[MOST], ny[MOST], nz;
+    float ng = 0.f;
+    auto fetch = [&](int it) {
+        const int chunk = J.reverse ? chunks - 1 - it : it, t0 = begin + chunk * C, valid = min(C, end - t0);
+        const float *const px = static_cast<const float *>(J.x.p), *const py = static_cast<const float *>(J.y.p), *const pz = static_cast<const float *>(J.z.p);
+        const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < MOST; ++k) {
+            const int i = tid + k * THREADS, t = i / per_row, c = i % per_row * 4;
+            const bool in = i < pieces && t < valid;
+            nx[k] = in ? *reinterpret_cast<const float4 *>(px + ((size_t)(t0 + t) * hx + base_x) * a + c) : none;
+            ny[k] = in ? *reinterpret_cast<const float4 *>(py + ((size_t)(t0 + t) * hy + base_y) * a + c) : none;
+        }
+        nz = tid / 8 < valid && tid % 8 * 4 < nb ? *reinterpret_cast<const float4 *>(pz + ((size_t)(t0 + tid / 8) * hz + base_z) * J.b + b0 + tid % 8 * 4) : none;
+        if (tid < C) ng = tid < valid ? A.g[A.fixed ? h : (size_t)(t0 + tid) * A.H + h] : 0.f;
+    };
+    if (chunks > 0) fetch(0);
     for (int it = 0; it < chunks; ++it) {
         const int chunk = J.reverse ? chunks - 1 - it : it, t0 = begin + chunk * C, valid = min(C, end - t0);
         __syncthreads();
         if (J.anchors && !J.reverse && it > 0 && chunk * C % kAnchor == 0) {
             float *to = J.anchors + ((size_t)(anchor_slot(begin, n) + chunk * C / kAnchor - 1) * A.H + h) * a * J.b;
             for (int i = tid; i < a * kSlice; i += THREADS)
-                if (i % kSlice < nb) to[(size_t)(i / kSlice) * J.sa + (size_t)(b0 + i % kSlice) * J.sb] = S[i / kSlice * PITCH_S + i % kSlice];
+                if (i % kSlice < nb) to[(size_t)(i / kSlice) * J.b + b0 + i % kSlice] = S[i / kSlice * PITCH_S + i % kSlice];
         }
-        for (int i = tid; i < C * a; i += THREADS) {
-            const int t = i / a, c = i % a;
-            const bool in = t < valid;
-            X[t * L.pa + c] = in ? load_elt(J.x.p, ((size_t)(t0 + t) * hx + base_x) * a + c, A.bf16) : 0.f;
-            Y[t * L.pa + c] = in ? load_elt(J.y.p, ((size_t)(t0 + t) * hy + base_y) * a + c, A.bf16) : 0.f;
+#pragma unroll
+        for (int k = 0; k < MOST; ++k) {
+            const int i = tid + k * THREADS;
+            if (i < pieces) {
+                *reinterpret_cast<float4 *>(X + i / per_row * L.pa + i % per_row * 4) = nx[k];
+                *reinterpret_cast<float4 *>(Y + i / per_row * L.pa + i % per_row * 4) = ny[k];
+            }
         }
-        for (int i = tid; i < C * kSlice; i += THREADS) {
-            const int t = i / kSlice, b = i % kSlice;
-            Z[t * PITCH_S + b] = t < valid && b < nb ? load_elt(J.z.p, ((size_t)(t0 + t) * hz + base_z) * J.b + b0 + b, A.bf16) : 0.f;
-        }
+        *reinterpret_cast<float4 *>(Z + tid / 8 * PITCH_S + tid % 8 * 4) = nz;
         if (tid < C) {
-            const float g = tid < valid ? A.g[A.fixed ? h : (size_t)(t0 + tid) * A.H + h] : 0.f;
+            const float g = ng;
             long long v = decay_units(g);
 #pragma unroll
             for (int o = 1; o < C; o <<= 1) {
@@ -90,6 +110,7 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const __grid_constant__ C
             if (tid == 0) *keep = bad ? nan : exp2_units(all);
         }
         __syncthreads();
+        if (it + 1 < chunks) fetch(it + 1);
 
         {   // scores: 2 x 2 a thread
             const int i0 = tid / 16, j0 = tid % 16;
@@ -148,7 +169,7 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const __grid_constant__ C
                 if (ty < valid)
                     for (int u = 0; u < 4; ++u)
                         if (4 * tx + u < nb)
-                            dot = fmaf(load_elt(J.r.p, ((size_t)(t0 + ty) * (A.H / J.r.share) + h / J.r.share) * J.b + b0 + 4 * tx + u, A.bf16), v[u], dot);
+                            dot = fmaf(load_elt(J.r.p, ((size_t)(t0 + ty) * (A.H / J.r.share) + h / J.r.share) * J.b + b0 + 4 * tx + u, 0), v[u], dot);
                 dot += __shfl_xor_sync(0xffffffffu, dot, 1);
                 dot += __shfl_xor_sync(0xffffffffu, dot, 2);
                 dot += __shfl_xor_sync(0xffffffffu, dot, 4);
@@ -193,7 +214,7 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const __grid_constant__ C
             __syncthreads();
             float *to = J.anchors + ((size_t)(anchor_slot(begin, n) + chunk * C / kAnchor - 1) * A.H + h) * a * J.b;
             for (int i = tid; i < a * kSlice; i += THREADS)
-                if (i % kSlice < nb) to[(size_t)(i / kSlice) * J.sa + (size_t)(b0 + i % kSlice) * J.sb] = S[i / kSlice * PITCH_S + i % kSlice];
+                if (i % kSlice < nb) to[(size_t)(i / kSlice) * J.b + b0 + i % kSlice] = S[i / kSlice * PITCH_S + i % kSlice];
         }
     }
     __syncthreads();
@@ -203,7 +224,7 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const __grid_constant__ C
         const float v = S[c * PITCH_S + b];
         if (J.last && slot >= 0) J.last[state + (size_t)c * J.sa + (size_t)(b0 + b) * J.sb] = v;
         if (J.anchors && J.last_anchor)
-            J.anchors[((size_t)(anchor_slot(begin, n) + max(0, len - 1) / kAnchor) * A.H + h) * a * J.b + (size_t)c * J.sa + (size_t)(b0 + b) * J.sb] = v;
+            J.anchors[((size_t)(anchor_slot(begin, n) + max(0, len - 1) / kAnchor) * A.H + h) * a * J.b + (size_t)c * J.b + b0 + b] = v;
     }
 }
 

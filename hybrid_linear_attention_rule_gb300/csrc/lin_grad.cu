@@ -12,7 +12,8 @@ namespace k3kda {
 namespace lin {
 namespace {
 
-// f at the anchors: <S, R>, both [dk, dv].  A CTA for each (anchor, head).
+// f at the anchors: <S, R> with S [dv, dk] and R [dk, dv].  A CTA for each (anchor, head), a warp 8 rows of R: its reads of S go down a column,
+// whose 32-byte pieces are these 8 rows' too.  (Laid out alike by the job that leaves S, its scattered stores held its chunks up: 311 to 404 us.)
 struct AnchorArgs {
     const float *S, *R, *dlast;       // dlast [N, H, dk, dv] or null
     double *f;                        // [slots, H]
@@ -34,12 +35,20 @@ __global__ void __launch_bounds__(512) anchor_kernel(const __grid_constant__ Anc
             double sum = 0.0;
             if (R) {
                 const float *S = A.S + at * A.dk * A.dv;
-                const int quads = A.dk * A.dv / 4;
+                for (int i0 = 8 * warp; i0 < A.dk; i0 += 128)
 #pragma unroll 4
-                for (int i = threadIdx.x; i < quads; i += 512) {
-                    const float4 x = reinterpret_cast<const float4 *>(S)[i], y = reinterpret_cast<const float4 *>(R)[i];
-                    sum += fmaf(x.w, y.w, fmaf(x.z, y.z, fmaf(x.y, y.y, x.x * y.x)));
-                }
+                    for (int j = lane; j < A.dv; j += 32) {
+                        float acc = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 8; i += 4) {
+                            const float4 x = *reinterpret_cast<const float4 *>(S + (size_t)j * A.dk + i0 + i);
+                            acc = fmaf(x.x, R[(size_t)(i0 + i) * A.dv + j], acc);
+                            acc = fmaf(x.y, R[(size_t)(i0 + i + 1) * A.dv + j], acc);
+                            acc = fmaf(x.z, R[(size_t)(i0 + i + 2) * A.dv + j], acc);
+                            acc = fmaf(x.w, R[(size_t)(i0 + i + 3) * A.dv + j], acc);
+                        }
+                        sum += acc;
+                    }
                 for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             }
             if (lane == 0) part[warp] = sum;

@@ -884,8 +884,8 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                         float *to = nullptr;
                         int step = 0;
                         if (k == 0 && at_anchor) {
-                            to = anchors + ((size_t)(anchor_slot(begin, n) + max(0, behind - 1) / kAnchor) * H + h) * ja * jb + (size_t)b * sb;
-                            step = sa;
+                            to = anchors + ((size_t)(anchor_slot(begin, n) + max(0, behind - 1) / kAnchor) * H + h) * ja * jb + b;
+                            step = jb;
                         }
                         if (k == 1 && to_last) {
                             const int slot = seq_slot(A.c.slot, A.c.num_slots, n);
