@@ -823,21 +823,22 @@ def _of(t, what, shape, dtype):
     """The address of a contiguous CUDA tensor of this shape and type, or of None."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"k3lin: {what} must be a torch.Tensor or None")
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda:
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"k3lin: {what} must be a torch.Tensor or None") from None
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"k3lin: {what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError("k3lin: tensors must live on a CUDA device (no CPU path exists)")
-    return t.data_ptr()
+    raise ValueError("k3lin: tensors must live on a CUDA device (no CPU path exists)")
 
 
 def _lin_sizes(q, k, v):
     """(T, Hk, H, dk, dv) of q, k [T, Hk, dk] and v [T, H, dv]."""
-    if q.dim() != 3 or v.dim() != 3:
+    qs, vs = q.shape, v.shape
+    if len(qs) != 3 or len(vs) != 3:
         raise ValueError("k3lin: q, k and v must be [tokens, heads, channels]")
-    T, Hk, dk = q.shape
-    return T, Hk, v.shape[1], dk, v.shape[2]
+    return qs[0], qs[1], vs[1], qs[2], vs[2]
 
 
 def _lin_decay(g, T, H):
@@ -857,15 +858,20 @@ def _lin_packing(cu_seqlens, cu_seqlens_host, T):
 
 def _lin_slots(state_idx, state_idx_host, N, what, *pools):
     """(slots, addresses of the map and its copy); the pools' first size is the number of slots."""
-    slots = {p.shape[0] for p in pools if p is not None}
-    if len(slots) > 1:
-        raise ValueError(f"k3lin: {what} have different numbers of slots")
-    n = slots.pop() if slots else N
-    if state_idx is None and n != N:
-        raise ValueError(f"k3lin: {what} must hold {N} states, not {n}")
+    n = None
+    for p in pools:
+        if p is not None:
+            if n is not None and n != p.shape[0]:
+                raise ValueError(f"k3lin: {what} have different numbers of slots")
+            n = p.shape[0]
+    n = N if n is None else n
+    if state_idx is None and state_idx_host is None:
+        if n != N:
+            raise ValueError(f"k3lin: {what} must hold {N} states, not {n}")
+        return n, None, None
     if state_idx_host is not None and state_idx_host.numel() != N:
         raise ValueError("k3lin: state_idx_host has another length")
-    return n, _of(state_idx, "state_idx", (N,), torch.int32), _host_i32(state_idx_host, "state_idx_host")
+    return n, _of(state_idx, "state_idx", (N,), torch.int32), None if state_idx_host is None else _host_i32(state_idx_host, "state_idx_host")
 
 
 def k3lin_prefill(q, k, v, g, initial_state, cu_seqlens, scale, out, final_state, workspace, state_idx=None, state_idx_host=None,
@@ -935,13 +941,14 @@ def lin_prefill(q, k, v, g, initial_state=None, cu_seqlens=None, scale=None, out
 def k3lin_decode_step(q, k, v, g, state, scale, out, state_idx=None, state_idx_host=None, stream=None):
     """One token of linear attention for N sequences (see include/k3kda.h); state is updated in place."""
     N, Hk, H, dk, dv = _lin_sizes(q, k, v)
-    dt = q.dtype
+    dt, ot = q.dtype, out.dtype
     gp, fixed = _lin_decay(g, N, H)
     slots, idx, idxh = _lin_slots(state_idx, state_idx_host, N, "state", state)
+    rows, wide = (N, Hk, dk), (N, H, dv)
     st = (_lib or load_library()).k3lin_decode_step(
-        _of(q, "q", q.shape, dt), _of(k, "k", q.shape, dt), _of(v, "v", (N, H, dv), dt), _dtype(q), gp, fixed,
-        _of(state, "state", (slots, H, dk, dv), torch.float32), idx, idxh, slots, N, Hk, H, dk, dv, float(scale),
-        _of(out, "out", (N, H, dv), out.dtype), _dtype(out), _raw_stream(stream, q))
+        _of(q, "q", rows, dt), _of(k, "k", rows, dt), _of(v, "v", wide, dt), _dtype(q), gp, fixed,
+        _of(state, "state", (slots, H, dk, dv), torch.float32), idx, idxh, slots, N, Hk, H, dk, dv, scale,
+        _of(out, "out", wide, ot), _dtype(out), _raw_stream(stream, q))
     if st:
         _check("k3lin_decode_step", st)
 
@@ -1005,7 +1012,8 @@ def _norm_rows(first, post_weight, pre_weight, **like):
         raise ValueError("k3blk: arrays must be [..., channels]")
     D = first.shape[-1]
     rows = first.numel() // D if D else 0
-    at = {name: _of(t, name, first.shape, first.dtype) for name, t in like.items()}
+    shape, dt = first.shape, first.dtype
+    at = {name: _of(t, name, shape, dt) for name, t in like.items()}
     return rows, D, at, _of(post_weight, "post_weight", (D,), torch.float32), _of(pre_weight, "pre_weight", (D,), torch.float32)
 
 

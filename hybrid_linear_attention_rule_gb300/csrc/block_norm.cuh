@@ -204,13 +204,15 @@ template <class T, int VEC, int TPR> __global__ void __launch_bounds__(TPR < 256
 // fetched by the threads.
 template <class T, int TPR> struct Ring {
     static constexpr int THREADS = TPR < 256 ? 256 : TPR, GROUPS = THREADS / TPR;
-    static constexpr int MOST = TPR * GROUPS * E * (int)sizeof(T) + 32;              // bytes of an array's rows
-    static constexpr int ARRAYS = 5, STAGE = ARRAYS * MOST, BYTES = 2 * STAGE;
-    static constexpr bool FITS = BYTES <= 220 * 1024;
+    static constexpr int ARRAYS = 5;
+    static constexpr bool FITS = 2 * ARRAYS * (TPR * GROUPS * E * (int)sizeof(T) + 32) <= 220 * 1024;
+    // Bytes of an array's rows (the weights' sums meet in their place).
+    static __host__ __device__ int most(int D) { return ((GROUPS * D * (int)sizeof(T) + 15) & ~15) + 32; }
+    static int bytes(int D) { const int n = 2 * ARRAYS * most(D), m = GROUPS > 1 ? GROUPS * TPR * E * 4 : 0; return n > m ? n : m; }
 };
 
 // The weights' gradients: a thread keeps its columns' sums over the rows of its CTA, in a fixed order.
-template <class T, int VEC, int TPR> __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 && sizeof(T) == 2 ? 2 : 1) norm_grad_kernel(const __grid_constant__ Args A) {
+template <class T, int VEC, int TPR> __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) norm_grad_kernel(const __grid_constant__ Args A) {
     using S = Slot<T, VEC, TPR>;
     using Q = Ring<T, TPR>;
     constexpr int THREADS = Q::THREADS, GROUPS = Q::GROUPS;
@@ -218,7 +220,7 @@ template <class T, int VEC, int TPR> __global__ void __launch_bounds__(TPR < 256
     __shared__ float room[GROUPS * 2 * (TPR / 32 + 1) * 4];
     __shared__ __align__(8) unsigned long long full[2];
     __shared__ int late;
-    const int t = threadIdx.x % TPR, group = threadIdx.x / TPR, D0 = A.D;
+    const int t = threadIdx.x % TPR, group = threadIdx.x / TPR, D0 = A.D, most = Q::most(D0);
     const long long step = (long long)gridDim.x * GROUPS;
     int turn = 0;
     const T *const arrays[5] = {static_cast<const T *>(A.ds), static_cast<const T *>(A.x), static_cast<const T *>(A.gate), static_cast<const T *>(A.s_in),
@@ -248,7 +250,7 @@ template <class T, int VEC, int TPR> __global__ void __launch_bounds__(TPR < 256
                 const uintptr_t from = max(a & ~(uintptr_t)15, first), to = min((z + 15) & ~(uintptr_t)15, last);
                 if (from >= to) continue;
                 if (!pass) bytes += (uint32_t)(to - from);
-                else tc::bulk_g2s(tc::smem_u32(ring + s * Q::STAGE + k * Q::MOST + (from - (a & ~(uintptr_t)15))), reinterpret_cast<const void *>(from), (uint32_t)(to - from), tc::smem_u32(&full[s]));
+                else tc::bulk_g2s(tc::smem_u32(ring + s * (Q::ARRAYS * most) + k * most + (from - (a & ~(uintptr_t)15))), reinterpret_cast<const void *>(from), (uint32_t)(to - from), tc::smem_u32(&full[s]));
             }
         }
     };
@@ -276,7 +278,7 @@ template <class T, int VEC, int TPR> __global__ void __launch_bounds__(TPR < 256
         auto row_of = [&](int k, typename S::Raw &r) {
             if constexpr (Q::FITS) {
                 const uintptr_t a = reinterpret_cast<uintptr_t>(arrays[k] + r0 * D0), own = reinterpret_cast<uintptr_t>(arrays[k] + at);
-                S::template fetch<false>(reinterpret_cast<const T *>(ring + s * Q::STAGE + k * Q::MOST + (own - (a & ~(uintptr_t)15))), t, D, r);
+                S::template fetch<false>(reinterpret_cast<const T *>(ring + s * (Q::ARRAYS * most) + k * most + (own - (a & ~(uintptr_t)15))), t, D, r);
                 if constexpr (VEC == 1) {
                     // the pieces of the array's ends that no copy holds
                     const uintptr_t first = (reinterpret_cast<uintptr_t>(arrays[k]) + 15) & ~(uintptr_t)15, last = reinterpret_cast<uintptr_t>(arrays[k] + A.rows * D0) & ~(uintptr_t)15;
@@ -311,6 +313,10 @@ template <class T, int VEC, int TPR> __global__ void __launch_bounds__(TPR < 256
             for (int e = 0; e < E; ++e) d[e] = S::value(dsr, e);
         }
         if (A.pre) {
+            if (Q::FITS && sizeof(T) == 4) {                         // (fetched again rather than kept: 32 registers)
+                row_of(3, sr);
+                row_of(4, dyr);
+            }
             const float r = rsqrtf(sums[0] * inv + A.eps), m = sums[1] * inv * r;     // m: mean(dy pre h_s)
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -324,6 +330,7 @@ template <class T, int VEC, int TPR> __global__ void __launch_bounds__(TPR < 256
         for (int e = 0; e < E; ++e) d[e] *= A.alpha;
         const float r = A.post ? rsqrtf(sums[2] * inv + A.eps) : 1.f;
         if (A.post) S::weights(A.post, t, D, w);
+        if (A.x && Q::FITS && sizeof(T) == 4) row_of(1, xr);
         if (A.gate) {
             typename S::Raw gr;
             float g[E];
@@ -396,9 +403,10 @@ template <class T, int VEC, int TPR> cudaError_t launch(const Args &a, bool grad
     constexpr int THREADS = TPR < 256 ? 256 : TPR, GROUPS = THREADS / TPR;
     if (grad) {
         static std::atomic<uint64_t> attr{0};
-        constexpr int bytes = Ring<T, TPR>::FITS ? Ring<T, TPR>::BYTES : 0;
-        if (bytes > 0)
-            if (cudaError_t e = smem_attr_once((const void *)norm_grad_kernel<T, VEC, TPR>, bytes, attr)) return e;
+        using Q = Ring<T, TPR>;
+        const int bytes = Q::FITS ? Q::bytes(a.D) : 0;
+        if (Q::FITS)
+            if (cudaError_t e = smem_attr_once((const void *)norm_grad_kernel<T, VEC, TPR>, Q::bytes(TPR * E), attr)) return e;
         norm_grad_kernel<T, VEC, TPR><<<(unsigned)parts_of(a.rows, a.D), THREADS, bytes, s>>>(a);
     } else {
         norm_kernel<T, VEC, TPR><<<(unsigned)((a.rows + GROUPS - 1) / GROUPS), THREADS, 0, s>>>(a);

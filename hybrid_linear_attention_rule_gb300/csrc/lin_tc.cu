@@ -188,6 +188,11 @@ struct Line {
     }
 };
 
+// A call's kernels follow one another as programmatic dependents: the next one's CTAs may be set up while the one before still runs, and
+// wait for its end before they read what it wrote.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 struct PlanArgs {
     const float *g;
     const int32_t *cu;
@@ -203,6 +208,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
     __shared__ long long part[PLAN_THREADS / 32];
     __shared__ int part_end[PLAN_THREADS / 32], found[4];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, N = A.N, H = A.H;
+    let_next_start();
     const int per = (N + PLAN_THREADS - 1) / PLAN_THREADS, n0 = min(N, tid * per), n1 = min(N, n0 + per);
     const Line line{A.cu, A.T};
     int own_end = 0;
@@ -348,27 +354,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
     const Waiter wait{&sh.dead};
     const Record *const line = A.rec[job];
 
-    // ---- where the piece begins and ends
-    const long long U = *A.total, most = max((long long)A.c.N * H, U / A.least);
-    const int count_pieces = (int)min((long long)A.pieces, most);
-    if (piece >= count_pieces) {
-        if (STATES && tid == 0) A.head[job * A.pieces + piece] = Head{0.f, 0, 0};
-        return;
-    }
-    long long u0 = U * piece / count_pieces;
-    const long long u1 = U * (piece + 1) / count_pieces;
-    if constexpr (STATES) {
-        const int pos1 = u1 < U ? line[u1].pos : 0;                  // within a pair: its part of this piece, if it ends there
-        const bool goes_on = u1 - pos1 < u0;
-        if (!goes_on) u0 = u1 - pos1;
-        if (tid == 0) {
-            Head &hd = A.head[job * A.pieces + piece];
-            hd.ends_within = pos1 > 0;
-            hd.goes_on = pos1 > 0 && goes_on;
-        }
-        if (pos1 == 0) return;
-    }
-    const int items = (int)(u1 - u0);
+    let_next_start();
     if (tid == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&sh.full[s]), 1);
@@ -399,6 +385,38 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = sh.tmem;
+    auto leave = [&] {
+        tc_fence_before();
+        __syncthreads();
+        if (tid == 0 && sh.dead) atomicOr(A.c.status, 2u);
+        if (warp == 0) {
+            tc_fence_after();
+            tmem_dealloc(tm, 512);
+        }
+    };
+    wait_for_last();
+
+    // ---- where the piece begins and ends
+    const long long U = *A.total, most = max((long long)A.c.N * H, U / A.least);
+    const int count_pieces = (int)min((long long)A.pieces, most);
+    if (piece >= count_pieces) {
+        if (STATES && tid == 0) A.head[job * A.pieces + piece] = Head{0.f, 0, 0};
+        return leave();
+    }
+    long long u0 = U * piece / count_pieces;
+    const long long u1 = U * (piece + 1) / count_pieces;
+    if constexpr (STATES) {
+        const int pos1 = u1 < U ? line[u1].pos : 0;                  // within a pair: its part of this piece, if it ends there
+        const bool goes_on = u1 - pos1 < u0;
+        if (!goes_on) u0 = u1 - pos1;
+        if (tid == 0) {
+            Head &hd = A.head[job * A.pieces + piece];
+            hd.ends_within = pos1 > 0;
+            hd.goes_on = pos1 > 0 && goes_on;
+        }
+        if (pos1 == 0) return leave();
+    }
+    const int items = (int)(u1 - u0);
     // (in registers: read where they are used, they would be fetched anew from the parameters each time)
     const bool reverse = J.reverse, dots = FULL && J.dots;
     constexpr bool exact = FULL;
@@ -979,18 +997,14 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
         }
         if (STATES && threadIdx.x == CTL + PREP) A.head[job * A.pieces + piece].keep = lost ? __int_as_float(0x7fffffff) : exp2_units(units);
     }
-    tc_fence_before();
-    __syncthreads();
-    if (tid == 0 && sh.dead) atomicOr(A.c.status, 2u);
-    if (warp == 0) {
-        tc_fence_after();
-        tmem_dealloc(tm, 512);
-    }
+    leave();
 }
 
 // The states that pieces leave, one after the other within a pair: S_piece += decay_piece S_before, from the piece that holds the pair's
 // start on.  A CTA a slice of the state and first piece.
 __global__ void __launch_bounds__(256) join_kernel(const Head *head, float *state, int pieces) {
+    let_next_start();
+    wait_for_last();
     head += (size_t)blockIdx.z * pieces;
     state += ((size_t)blockIdx.z * pieces) * D * D + (size_t)blockIdx.x * 1024 + threadIdx.x * 4;
     int c = blockIdx.y;
@@ -1026,6 +1040,21 @@ cudaError_t make_map(CUtensorMap *m, const void *base, int T, int heads, int d, 
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <class... P, class... X> cudaError_t follow(void (*kernel)(P...), dim3 grid, int threads, size_t bytes, cudaStream_t s, const X &...args) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = bytes;
+    c.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    count_launch();
+    return cudaLaunchKernelEx(&c, kernel, P(args)...);
 }
 
 constexpr int MOST_PIECES = 160;
@@ -1103,17 +1132,14 @@ cudaError_t launch_scan_tc(const Call &c, cudaStream_t s) {
     const long long longest = c.T / C + 1;
     const bool cut = !(c.N == 1 && longest <= A.least && c.H <= A.pieces);
     if (cut) {
-        tc_kernel<kStates><<<A.pieces * c.jobs, THREADS, kSmem<kStates>, s>>>(A);
-        count_launch();
-        join_kernel<<<dim3(D * D / 1024, A.pieces, c.jobs), 256, 0, s>>>(A.head, A.state, A.pieces);
-        count_launch();
+        e = follow(tc_kernel<kStates>, dim3(A.pieces * c.jobs), THREADS, kSmem<kStates>, s, A);
+        if (e == cudaSuccess) e = follow(join_kernel, dim3(D * D / 1024, A.pieces, c.jobs), 256, 0, s, A.head, A.state, A.pieces);
+        if (e != cudaSuccess) return e;
     }
     bool plain = true;
     for (int j = 0; j < c.jobs; ++j) plain = plain && c.job[j].out_bf16 && !c.job[j].exact && !c.job[j].dots && !c.job[j].anchors;
-    if (plain) tc_kernel<kPlain><<<A.pieces * c.jobs, THREADS, kSmem<kPlain>, s>>>(A);
-    else tc_kernel<kFull><<<A.pieces * c.jobs, THREADS, kSmem<kFull>, s>>>(A);
-    count_launch();
-    return cudaGetLastError();
+    return plain ? follow(tc_kernel<kPlain>, dim3(A.pieces * c.jobs), THREADS, kSmem<kPlain>, s, A)
+                 : follow(tc_kernel<kFull>, dim3(A.pieces * c.jobs), THREADS, kSmem<kFull>, s, A);
 }
 
 }  // namespace lin
