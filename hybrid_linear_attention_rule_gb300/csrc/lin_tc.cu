@@ -466,22 +466,6 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                         for (int u = 0; u < 2; ++u) tma_load_3d(to + M::R + u * TILE, mr, 64 * u, sr ? hk : h, t0, bar);
                 }
                 __syncwarp();
-                // the next chunk on its way to L2: its copy, once there is room for it, is then a short one
-                if (it % 32 < 31 && it + 1 < items) {
-                    const int t0 = uniform(__shfl_sync(0xffffffffu, at_t0, it + 1 & 31)), h = uniform(__shfl_sync(0xffffffffu, at_h, it + 1 & 31)),
-                              hk = uniform(__shfl_sync(0xffffffffu, at_hk, it + 1 & 31));
-                    if (elect()) {
-                        prefetch_l2(rec + sizeof(Record), (uint32_t)sizeof(Record));
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            tma_prefetch_3d(my, 64 * u, sy ? hk : h, t0);
-                            if (!STATES) tma_prefetch_3d(mx, 64 * u, sx ? hk : h, t0);
-                            tma_prefetch_3d(mz, 64 * u, sz ? hk : h, t0);
-                            if (FULL && dots) tma_prefetch_3d(mr, 64 * u, sr ? hk : h, t0);
-                        }
-                    }
-                    __syncwarp();
-                }
             }
             // (after a wait that gave up: nothing may be on its way into shared memory when the CTA ends)
             for (int k = max(0, it - STAGES); k < it; ++k)
@@ -891,55 +875,11 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                     }
                 }
             }
-            if (ok) {
-                // where the state goes: to an anchor, to the caller, to the piece that goes on
-                const int behind = reverse ? chunk * C : chunk * C + valid, begin = t0 - chunk * C;
-                const bool at_anchor = anchors && it >= 0 && (reverse ? chunk > 0 && behind % kAnchor == 0 : ends ? last_anchor : behind % kAnchor == 0);
-                const bool to_last = !STATES && ends && last, to_piece = STATES && it == items - 1;
-                if (at_anchor || to_last || to_piece) {
-#pragma unroll 1
-                    for (int k = 0; k < 2; ++k) {
-                        float *to = nullptr;
-                        int step = 0;
-                        if (k == 0 && at_anchor) {
-                            to = anchors + ((size_t)(anchor_slot(begin, n) + max(0, behind - 1) / kAnchor) * H + h) * ja * jb + b;
-                            step = jb;
-                        }
-                        if (k == 1 && to_last) {
-                            const int slot = seq_slot(A.c.slot, A.c.num_slots, n);
-                            if (slot >= 0) to = last + ((size_t)slot * H + h) * ja * jb + (size_t)b * sb;
-                            step = sa;
-                        }
-                        if (k == 1 && to_piece) {
-                            to = own_state + b;
-                            step = D;
-                        }
-                        if (!to || !(in_b || STATES)) continue;
-                        const int rows = (STATES ? D : ja) - a0;
-                        to += (size_t)a0 * step;
-#pragma unroll
-                        for (int i = 0; i < COLS; ++i) {
-                            if (i < rows) *to = S[i];
-                            to += step;
-                        }
-                    }
-                }
-                // the next chunk's state goes out before this one's rows: the products with it run meanwhile
-                if (it + 1 < items) {
-                    ok = wait(sh.full[(it + 1) % STAGES], (it + 1) / STAGES);
-                    if (ok) {
-                        enter(it + 1);
-                        if (!STATES) hand_over();
-                    }
-                }
-            }
-            if (it < 0) continue;
-            if constexpr (STATES) {
+            if (!ok) break;
+            if (STATES) {
                 __syncwarp();
-                if (ok && lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));
-                if (!ok) break;
-            } else {
-                if (!ok) break;
+                if (it >= 0 && lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));
+            } else if (it >= 0) {
                 // where channel b of a token stands in a tile: piece (b / 8) ^ (token & 7) of the token's row
                 const uint32_t tile = (b >> 6) * TILE + part * TOKENS * 128 + (b & 7) * 2;
                 uint8_t *const stage = sm + s * M::STAGE;
@@ -992,6 +932,47 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                     d[0] += __shfl_xor_sync(0xffffffffu, d[0], 1);
                     const int t = TOKENS * part + (lane >> 1);
                     if (!(lane & 1) && t < valid) dots_at[((size_t)(warp & 3) * A.c.T + t0 + t) * H + h] = d[0];
+                }
+            }
+            {
+                // where the state goes: to an anchor, to the caller, to the piece that goes on
+                const int behind = reverse ? chunk * C : chunk * C + valid, begin = t0 - chunk * C;
+                const bool at_anchor = anchors && it >= 0 && (reverse ? chunk > 0 && behind % kAnchor == 0 : ends ? last_anchor : behind % kAnchor == 0);
+                const bool to_last = !STATES && ends && last, to_piece = STATES && it == items - 1;
+                if (at_anchor || to_last || to_piece) {
+#pragma unroll 1
+                    for (int k = 0; k < 2; ++k) {
+                        float *to = nullptr;
+                        int step = 0;
+                        if (k == 0 && at_anchor) {
+                            to = anchors + ((size_t)(anchor_slot(begin, n) + max(0, behind - 1) / kAnchor) * H + h) * ja * jb + b;
+                            step = jb;
+                        }
+                        if (k == 1 && to_last) {
+                            const int slot = seq_slot(A.c.slot, A.c.num_slots, n);
+                            if (slot >= 0) to = last + ((size_t)slot * H + h) * ja * jb + (size_t)b * sb;
+                            step = sa;
+                        }
+                        if (k == 1 && to_piece) {
+                            to = own_state + b;
+                            step = D;
+                        }
+                        if (!to || !(in_b || STATES)) continue;
+                        const int rows = (STATES ? D : ja) - a0;
+                        to += (size_t)a0 * step;
+#pragma unroll
+                        for (int i = 0; i < COLS; ++i) {
+                            if (i < rows) *to = S[i];
+                            to += step;
+                        }
+                    }
+                }
+                if (it + 1 < items) {
+                    ok = wait(sh.full[(it + 1) % STAGES], (it + 1) / STAGES);
+                    if (ok) {
+                        enter(it + 1);
+                        if (!STATES) hand_over();
+                    }
                 }
             }
         }
