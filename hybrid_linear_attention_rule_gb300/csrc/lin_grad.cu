@@ -211,7 +211,7 @@ Call call_of(const LinArgs &a, const Space &w) {
 }
 
 bool on_tensor_cores(const Call &c) { return c.bf16 && c.T > 0; }
-cudaError_t launch_scan(const Call &c, cudaStream_t s) { return on_tensor_cores(c) ? launch_scan_tc(c, s) : launch_scan_f32(c, s); }
+cudaError_t launch_scan(const Call &c, cudaStream_t s) { return on_tensor_cores(c) ? launch_scan_tc(&c, 1, s) : launch_scan_f32(c, s); }
 
 }  // namespace
 }  // namespace lin
@@ -304,15 +304,18 @@ cudaError_t launch_lin_backward(const LinArgs &a, const void *dO, const float *d
         jv.anchors = part(w.R);
         jv.exact = 1;
     }
-    // dk by itself where the others need more: its rows are all that it puts out
+    cudaError_t e;
     if (dg && on_tensor_cores(c)) {
-        Call k = c;
-        k.jobs = 1;
-        k.job[0] = jk;
-        c.jobs = 2;
-        if (cudaError_t e = launch_scan(k, s)) return e;
+        // dk by itself where the others need more: its rows are all that it puts out
+        Call both[2] = {c, c};
+        both[0].jobs = 1;
+        both[0].job[0] = jk;
+        both[1].jobs = 2;
+        e = launch_scan_tc(both, 2, s);
+    } else {
+        e = launch_scan(c, s);
     }
-    if (cudaError_t e = launch_scan(c, s)) return e;
+    if (e != cudaSuccess) return e;
     const unsigned seqs = (unsigned)(a.N < 1024 ? a.N : 1024);
     if (dg) {
         const unsigned deep = (unsigned)(a.T / kAnchor / seqs + 1 < 256 ? a.T / kAnchor / seqs + 1 : 256);

@@ -35,6 +35,7 @@ constexpr int REG_CTL = 40, REG_PREP = 72, REG_HOLD = 80;
 static_assert(CTL * REG_CTL + PREP * REG_PREP + HOLD * REG_HOLD <= THREADS * 72, "shares of the registers");
 constexpr int COLS = 32, TOKENS = 16;                              // of the state and of the outputs that one of the holding threads has
 constexpr uint32_t kTries = 1u << 20;            // a second or two
+constexpr int MOST_PIECES = 160, LEAST = 16;       // LEAST: chunks of a piece, at least, where there are more pieces than pairs
 
 enum Kind { kStates, kPlain, kFull };      // states alone; jobs whose operands are in two parts and that put out nothing but BF16 rows; any, in three parts
 
@@ -93,7 +94,6 @@ struct TcArgs {
     int pieces;                // a job
     const Record *rec[3];      // the jobs'
     const long long *total;    // records of one
-    int least;                 // chunks of a piece, at least, where there are more pieces than pairs
     Head *head;                // [jobs][pieces]
     float *state;              // [jobs][pieces][a][D]
     float *kept;               // likewise, or null: the first states of the pairs that a piece leaves open, when they may be written over
@@ -397,7 +397,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
     wait_for_last();
 
     // ---- where the piece begins and ends
-    const long long U = *A.total, most = max((long long)A.c.N * H, U / A.least);
+    const long long U = *A.total, most = max((long long)A.c.N * H, U / LEAST);
     const int count_pieces = (int)min((long long)A.pieces, most);
     if (piece >= count_pieces) {
         if (STATES && tid == 0) A.head[job * A.pieces + piece] = Head{0.f, 0, 0};
@@ -1038,23 +1038,19 @@ template <class... P, class... X> cudaError_t follow(void (*kernel)(P...), dim3 
     return cudaLaunchKernelEx(&c, kernel, P(args)...);
 }
 
-constexpr int MOST_PIECES = 160;
-
 }  // namespace
 
 // The pieces' states, kept first states and heads, the number of records, and the records of up to two directions.
 static size_t fixed_part() { return ((size_t)MOST_PIECES * (2 * D * D * sizeof(float) + sizeof(Head)) + 8 + 255) & ~size_t(255); }
 static size_t records(int N, int T, int H) { return ((size_t)T / C + N) * H * sizeof(Record); }
+static long long *total_of(const Call &c) {
+    return reinterpret_cast<long long *>(static_cast<char *>(c.pieces) + (size_t)MOST_PIECES * (2 * D * D * sizeof(float) + sizeof(Head)));
+}
 size_t tc_workspace(int N, int T, int H, int directions) { return fixed_part() + records(N, T, H) * directions; }
 
-cudaError_t launch_scan_tc(const Call &c, cudaStream_t s) {
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kStates>, (int)kSmem<kStates>, g_attr[0]);
-    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kPlain>, (int)kSmem<kPlain>, g_attr[1]);
-    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kFull>, (int)kSmem<kFull>, g_attr[2]);
-    if (e != cudaSuccess) return e;
+// One call's kernels behind the plan, which has written the jobs' records to rec.
+static cudaError_t launch_jobs(const Call &c, const Record *const *rec, int sms, cudaStream_t s) {
+    cudaError_t e;
     TcArgs A{};
     A.c = c;
     A.rows = c.T < C ? (c.T < 1 ? 1 : c.T) : C;
@@ -1072,15 +1068,39 @@ cudaError_t launch_scan_tc(const Call &c, cudaStream_t s) {
             }
             *at[u] = m;
         }
+        A.rec[j] = rec[j];
     }
-    for (int j = 0; j < c.jobs; ++j)
+    bool plain = true;
+    for (int j = 0; j < c.jobs; ++j) {
         if (c.job[j].out_bf16 && (e = make_map(&A.out[j], c.job[j].out, c.T, c.H, c.job[j].b, A.rows)) != cudaSuccess) return e;
+        plain = plain && c.job[j].out_bf16 && !c.job[j].exact && !c.job[j].dots && !c.job[j].anchors;
+    }
     A.pieces = (sms < MOST_PIECES ? sms : MOST_PIECES) / c.jobs;
-    A.least = 16;
     A.state = static_cast<float *>(c.pieces);
     A.kept = A.state + (size_t)MOST_PIECES * D * D;
     A.head = reinterpret_cast<Head *>(A.kept + (size_t)MOST_PIECES * D * D);
+    A.total = total_of(c);
     if (!c.job[0].first || c.job[0].first != c.job[0].last) A.kept = nullptr;
+    // one short sequence: every piece is a whole pair
+    const bool cut = !(c.N == 1 && c.T / C + 1 <= LEAST && c.H <= A.pieces);
+    if (cut) {
+        e = follow(tc_kernel<kStates>, dim3(A.pieces * c.jobs), THREADS, kSmem<kStates>, s, A);
+        if (e == cudaSuccess) e = follow(join_kernel, dim3(D * D / 1024, A.pieces, c.jobs), 256, 0, s, A.head, A.state, A.pieces);
+        if (e != cudaSuccess) return e;
+    }
+    return plain ? follow(tc_kernel<kPlain>, dim3(A.pieces * c.jobs), THREADS, kSmem<kPlain>, s, A)
+                 : follow(tc_kernel<kFull>, dim3(A.pieces * c.jobs), THREADS, kSmem<kFull>, s, A);
+}
+
+cudaError_t launch_scan_tc(const Call *calls, int n, cudaStream_t s) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kStates>, (int)kSmem<kStates>, g_attr[0]);
+    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kPlain>, (int)kSmem<kPlain>, g_attr[1]);
+    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kFull>, (int)kSmem<kFull>, g_attr[2]);
+    if (e != cudaSuccess) return e;
+    const Call &c = calls[0];
     PlanArgs P{};
     P.g = c.g;
     P.cu = c.cu;
@@ -1089,38 +1109,30 @@ cudaError_t launch_scan_tc(const Call &c, cudaStream_t s) {
     P.T = c.T;
     P.H = c.H;
     P.group = 1;
-    P.total = reinterpret_cast<long long *>(A.head + MOST_PIECES);
-    A.total = P.total;
-    for (int j = 0; j < c.jobs; ++j) {
-        const Job &b = c.job[j];
-        for (const Rows *r : {&b.x, &b.y, &b.z})
-            if (r->share > P.group) P.group = r->share;
-        int k = 0;
-        while (k < P.variants && (P.reverse[k] != b.reverse || P.sp[k] != b.sp || P.sc[k] != b.sc || P.sw[k] != b.sw)) ++k;
-        if (k == P.variants) {
-            P.reverse[k] = b.reverse;
-            P.sp[k] = b.sp;
-            P.sc[k] = b.sc;
-            P.sw[k] = b.sw;
-            P.rec[k] = reinterpret_cast<Record *>(static_cast<char *>(c.pieces) + fixed_part() + k * records(c.N, c.T, c.H));
-            ++P.variants;
+    P.total = total_of(c);
+    const Record *rec[2][3] = {};
+    for (int i = 0; i < n; ++i)
+        for (int j = 0; j < calls[i].jobs; ++j) {
+            const Job &b = calls[i].job[j];
+            for (const Rows *r : {&b.x, &b.y, &b.z})
+                if (r->share > P.group) P.group = r->share;
+            int k = 0;
+            while (k < P.variants && (P.reverse[k] != b.reverse || P.sp[k] != b.sp || P.sc[k] != b.sc || P.sw[k] != b.sw)) ++k;
+            if (k == P.variants) {
+                P.reverse[k] = b.reverse;
+                P.sp[k] = b.sp;
+                P.sc[k] = b.sc;
+                P.sw[k] = b.sw;
+                P.rec[k] = reinterpret_cast<Record *>(static_cast<char *>(c.pieces) + fixed_part() + k * records(c.N, c.T, c.H));
+                ++P.variants;
+            }
+            rec[i][j] = P.rec[k];
         }
-        A.rec[j] = P.rec[k];
-    }
     plan_kernel<<<2 * sms, PLAN_THREADS, 0, s>>>(P);
     count_launch();
-    // one short sequence: every piece is a whole pair
-    const long long longest = c.T / C + 1;
-    const bool cut = !(c.N == 1 && longest <= A.least && c.H <= A.pieces);
-    if (cut) {
-        e = follow(tc_kernel<kStates>, dim3(A.pieces * c.jobs), THREADS, kSmem<kStates>, s, A);
-        if (e == cudaSuccess) e = follow(join_kernel, dim3(D * D / 1024, A.pieces, c.jobs), 256, 0, s, A.head, A.state, A.pieces);
-        if (e != cudaSuccess) return e;
-    }
-    bool plain = true;
-    for (int j = 0; j < c.jobs; ++j) plain = plain && c.job[j].out_bf16 && !c.job[j].exact && !c.job[j].dots && !c.job[j].anchors;
-    return plain ? follow(tc_kernel<kPlain>, dim3(A.pieces * c.jobs), THREADS, kSmem<kPlain>, s, A)
-                 : follow(tc_kernel<kFull>, dim3(A.pieces * c.jobs), THREADS, kSmem<kFull>, s, A);
+    for (int i = 0; i < n; ++i)
+        if ((e = launch_jobs(calls[i], rec[i], sms, s)) != cudaSuccess) return e;
+    return cudaSuccess;
 }
 
 }  // namespace lin
