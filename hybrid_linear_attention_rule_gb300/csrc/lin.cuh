@@ -93,8 +93,8 @@ inline int slices(int b) { return (b + kSlice - 1) / kSlice; }
 cudaError_t launch_scan_f32(const Call &c, cudaStream_t s);
 // The tensor-core path (lin_tc.cu): BF16, T > 0; dots has a row for each 32 channels too (four, whatever the width).
 size_t tc_workspace(int N, int T, int H, int directions);
-// `n` calls (at most two) of the same sequences, with jobs of at most two directions and scales, one after the other.
-cudaError_t launch_scan_tc(const Call *calls, int n, cudaStream_t s);
+// Jobs of at most two directions and scales.  `apart`: they are dq, dv and dk, and dk gets a launch of its own.
+cudaError_t launch_scan_tc(const Call &c, bool apart, cudaStream_t s);
 
 }  // namespace lin
 

@@ -12,8 +12,11 @@ namespace k3kda {
 namespace lin {
 namespace {
 
-// f at the anchors: <S, R> with S [dv, dk] and R [dk, dv].  A CTA for each (anchor, head), a warp 8 rows of R: its reads of S go down a column,
-// whose 32-byte pieces are these 8 rows' too.  (Laid out alike by the job that leaves S, its scattered stores held its chunks up: 311 to 404 us.)
+// f at the anchors: <S, R> with S [dv, dk] and R [dk, dv].  A CTA for each (anchor, head), a thread blocks of 4 by 4 of both, whose
+// pieces of 16 bytes fill whole lines of S and whole sectors of R; products of FP32, eight of them summed in FP32, the rest in 64 bits.  HBM
+// bounds it: 67 MB for 8 k tokens and 32 heads in 16 us, where reads of S
+// down its columns took 39.  (S laid out as R by the job that leaves it: its
+// scattered stores held its chunks up, 311 to 404 us.)
 struct AnchorArgs {
     const float *S, *R, *dlast;       // dlast [N, H, dk, dv] or null
     double *f;                        // [slots, H]
@@ -21,9 +24,10 @@ struct AnchorArgs {
     int N, T, H, dk, dv;
 };
 
-__global__ void __launch_bounds__(512) anchor_kernel(const __grid_constant__ AnchorArgs A) {
-    __shared__ double part[16];
+__global__ void __launch_bounds__(256) anchor_kernel(const __grid_constant__ AnchorArgs A) {
+    __shared__ double part[8];
     const int h = blockIdx.y, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int across = (A.dk + 31) / 32, tiles = across * (A.dv / 16);
     for (int n = blockIdx.x; n < A.N; n += gridDim.x) {
         int begin, end;
         seq_bounds(A.cu, n, A.T, begin, end);
@@ -35,27 +39,30 @@ __global__ void __launch_bounds__(512) anchor_kernel(const __grid_constant__ Anc
             double sum = 0.0;
             if (R) {
                 const float *S = A.S + at * A.dk * A.dv;
-                for (int i0 = 8 * warp; i0 < A.dk; i0 += 128)
-#pragma unroll 4
-                    for (int j = lane; j < A.dv; j += 32) {
-                        float acc = 0.f;
+#pragma unroll 2
+                for (int tile = warp; tile < tiles; tile += 8) {
+                    const int i0 = tile % across * 32 + lane % 8 * 4, j0 = tile / across * 16 + lane / 8 * 4;
+                    if (i0 >= A.dk) continue;
+                    float4 s[4], r[4];
 #pragma unroll
-                        for (int i = 0; i < 8; i += 4) {
-                            const float4 x = *reinterpret_cast<const float4 *>(S + (size_t)j * A.dk + i0 + i);
-                            acc = fmaf(x.x, R[(size_t)(i0 + i) * A.dv + j], acc);
-                            acc = fmaf(x.y, R[(size_t)(i0 + i + 1) * A.dv + j], acc);
-                            acc = fmaf(x.z, R[(size_t)(i0 + i + 2) * A.dv + j], acc);
-                            acc = fmaf(x.w, R[(size_t)(i0 + i + 3) * A.dv + j], acc);
-                        }
-                        sum += acc;
+                    for (int u = 0; u < 4; ++u) {
+                        s[u] = __ldg(reinterpret_cast<const float4 *>(S + (size_t)(j0 + u) * A.dk + i0));
+                        r[u] = __ldg(reinterpret_cast<const float4 *>(R + (size_t)(i0 + u) * A.dv + j0));
                     }
+                    const float a = fmaf(s[0].x, r[0].x, fmaf(s[1].x, r[0].y, fmaf(s[2].x, r[0].z, s[3].x * r[0].w)));
+                    const float b = fmaf(s[0].y, r[1].x, fmaf(s[1].y, r[1].y, fmaf(s[2].y, r[1].z, fmaf(s[3].y, r[1].w, a))));
+                    const float c = fmaf(s[0].z, r[2].x, fmaf(s[1].z, r[2].y, fmaf(s[2].z, r[2].z, s[3].z * r[2].w)));
+                    const float d = fmaf(s[0].w, r[3].x, fmaf(s[1].w, r[3].y, fmaf(s[2].w, r[3].z, fmaf(s[3].w, r[3].w, c))));
+                    sum += b;
+                    sum += d;
+                }
                 for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             }
             if (lane == 0) part[warp] = sum;
             __syncthreads();
             if (threadIdx.x == 0) {
                 sum = 0.0;
-                for (int u = 0; u < 16; ++u) sum += part[u];
+                for (int u = 0; u < 8; ++u) sum += part[u];
                 A.f[at] = sum;
             }
             __syncthreads();
@@ -63,7 +70,8 @@ __global__ void __launch_bounds__(512) anchor_kernel(const __grid_constant__ Anc
     }
 }
 
-// dg: a CTA sums one stretch between anchors for 8 heads (a 32-byte piece of a row), 64 runs of 8 tokens, each a thread a head.
+// dg: a CTA sums one stretch between anchors for 8 heads (a 32-byte piece of a row), 64 runs of 8 tokens, each a thread a head.  The runs
+// behind a thread's own come by shuffles (a warp has four) and one sum a warp: additions in 64 bits are what this kernel spends its time on.
 struct SumArgs {
     const float *r1, *r2;             // [slices][T, H]
     int n1, n2;                       // slices
@@ -74,9 +82,10 @@ struct SumArgs {
 };
 
 __global__ void __launch_bounds__(512) sum_kernel(const __grid_constant__ SumArgs A) {
-    constexpr int RUN = 8, RUNS = kAnchor / RUN;
-    __shared__ double part[RUNS][9];
-    const int hl = threadIdx.x % 8, run = threadIdx.x / 8, h = blockIdx.y * 8 + hl;
+    constexpr int RUN = 8;
+    static_assert(kAnchor == RUN * 64, "512 threads, 8 of them a run");
+    __shared__ double part[16][8];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, hl = threadIdx.x % 8, run = threadIdx.x / 8, h = blockIdx.y * 8 + hl;
     const size_t TH = (size_t)A.T * A.H;
     for (int n = blockIdx.x; n < A.N; n += gridDim.x) {
         int begin, end;
@@ -102,11 +111,16 @@ __global__ void __launch_bounds__(512) sum_kernel(const __grid_constant__ SumArg
             double sum = 0.0;
 #pragma unroll
             for (int i = 0; i < RUN; ++i) sum += p[i] - q[i];
-            part[run][hl] = sum;
+            // of the warp's runs: those from the thread's own on, those behind it
+            const double next = __shfl_down_sync(0xffffffffu, sum, 8), pair = lane < 24 ? sum + next : sum;
+            const double far = __shfl_down_sync(0xffffffffu, pair, 16), from = lane < 16 ? pair + far : pair;
+            const double after = __shfl_down_sync(0xffffffffu, from, 8);
+            if (lane < 8) part[warp][lane] = from;
             __syncthreads();
             if (h < A.H) {
                 double f = A.f[(size_t)(anchor_slot(begin, n) + k) * A.H + h];
-                for (int u = RUNS - 1; u > run; --u) f += part[u][hl];
+                for (int u = 15; u > warp; --u) f += part[u][hl];
+                if (lane < 24) f += after;
 #pragma unroll
                 for (int i = RUN - 1; i >= 0; --i) {
                     f += p[i] - q[i];
@@ -211,7 +225,7 @@ Call call_of(const LinArgs &a, const Space &w) {
 }
 
 bool on_tensor_cores(const Call &c) { return c.bf16 && c.T > 0; }
-cudaError_t launch_scan(const Call &c, cudaStream_t s) { return on_tensor_cores(c) ? launch_scan_tc(&c, 1, s) : launch_scan_f32(c, s); }
+cudaError_t launch_scan(const Call &c, bool apart, cudaStream_t s) { return on_tensor_cores(c) ? launch_scan_tc(c, apart, s) : launch_scan_f32(c, s); }
 
 }  // namespace
 }  // namespace lin
@@ -242,7 +256,7 @@ cudaError_t launch_lin_prefill(const LinArgs &a, void *out, int out_bf16, float 
     j.out = out;
     j.out_bf16 = out_bf16;
     j.exact = !out_bf16;
-    return launch_scan(c, s);
+    return launch_scan(c, false, s);
 }
 
 cudaError_t launch_lin_backward(const LinArgs &a, const void *dO, const float *dlast, void *dq, void *dk, void *dv, float *dg,
@@ -304,24 +318,13 @@ cudaError_t launch_lin_backward(const LinArgs &a, const void *dO, const float *d
         jv.anchors = part(w.R);
         jv.exact = 1;
     }
-    cudaError_t e;
-    if (dg && on_tensor_cores(c)) {
-        // dk by itself where the others need more: its rows are all that it puts out
-        Call both[2] = {c, c};
-        both[0].jobs = 1;
-        both[0].job[0] = jk;
-        both[1].jobs = 2;
-        e = launch_scan_tc(both, 2, s);
-    } else {
-        e = launch_scan(c, s);
-    }
-    if (e != cudaSuccess) return e;
+    if (cudaError_t e = launch_scan(c, dg != nullptr, s)) return e;
     const unsigned seqs = (unsigned)(a.N < 1024 ? a.N : 1024);
     if (dg) {
         const unsigned deep = (unsigned)(a.T / kAnchor / seqs + 1 < 256 ? a.T / kAnchor / seqs + 1 : 256);
         double *f = reinterpret_cast<double *>(ws + w.f);
         const AnchorArgs g{part(w.S), part(w.R), dlast, f, a.cu, a.N, a.T, a.H, a.dk, a.dv};
-        anchor_kernel<<<dim3(seqs, a.H, deep), 512, 0, s>>>(g);
+        anchor_kernel<<<dim3(seqs, a.H, deep), 256, 0, s>>>(g);
         count_launch();
         float *to = a.fixed ? part(w.dg) : dg;
         const SumArgs u{part(w.r1), part(w.r2), on_tensor_cores(c) ? 4 : slices(a.dk), on_tensor_cores(c) ? 4 : slices(a.dv), f, to, a.cu, a.N, a.T, a.H};

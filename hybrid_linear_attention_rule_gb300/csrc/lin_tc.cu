@@ -92,11 +92,15 @@ struct TcArgs {
     int x[3], y[3], z[3], r[3];        // the jobs' maps
     int rows;                  // of a copy's box
     int pieces;                // a job
+    int fine;                  // those that the states were taken for: as many, or twice as many
+    bool nested;               // pieces come in halves for another launch
+    int of[3];                 // whose states a job begins its pieces with,
+    bool turned[3];            // the other way round: its a is their b
     const Record *rec[3];      // the jobs'
     const long long *total;    // records of one
-    Head *head;                // [jobs][pieces]
-    float *state;              // [jobs][pieces][a][D]
-    float *kept;               // likewise, or null: the first states of the pairs that a piece leaves open, when they may be written over
+    Head *head;                // [jobs][fine]
+    float *state;              // [jobs][fine][a][D]
+    float *kept;               // likewise (one job), or null: the first states of the pairs that a piece leaves open, when they may be written over
 };
 
 template <int N> __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -398,9 +402,11 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
 
     // ---- where the piece begins and ends
     const long long U = *A.total, most = max((long long)A.c.N * H, U / LEAST);
-    const int count_pieces = (int)min((long long)A.pieces, most);
+    // (halves are there where each of them has a chunk)
+    const int coarse = A.nested ? A.fine / 2 : A.fine, count_fine = A.nested && most > coarse && U >= A.fine ? A.fine : (int)min((long long)coarse, most);
+    const int halves = FULL && A.pieces != A.fine && count_fine > coarse ? 2 : 1, count_pieces = count_fine / halves;
     if (piece >= count_pieces) {
-        if (STATES && tid == 0) A.head[job * A.pieces + piece] = Head{0.f, 0, 0};
+        if (STATES && tid == 0) A.head[job * A.fine + piece] = Head{0.f, 0, 0};
         return leave();
     }
     long long u0 = U * piece / count_pieces;
@@ -410,7 +416,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
         const bool goes_on = u1 - pos1 < u0;
         if (!goes_on) u0 = u1 - pos1;
         if (tid == 0) {
-            Head &hd = A.head[job * A.pieces + piece];
+            Head &hd = A.head[job * A.fine + piece];
             hd.ends_within = pos1 > 0;
             hd.goes_on = pos1 > 0 && goes_on;
         }
@@ -750,7 +756,8 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
         float S[COLS];
 #pragma unroll
         for (int i = 0; i < COLS; ++i) S[i] = 0.f;
-        float *const own_state = A.state + ((size_t)job * A.pieces + piece) * D * D;
+        float *const own_state = A.state + ((size_t)job * A.fine + piece) * D * D;       // (states)
+        const bool turned = FULL && A.turned[job];
         // the state that chunk `it` begins with
         auto enter = [&](int it) {
             const Record &I = sh.rec[it % STAGES];
@@ -760,10 +767,10 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
             const size_t state = ((size_t)max(slot, 0) * H + I.h) * ja * jb;
             // element a of it is at from[a * step]; nothing (zero) without one
             const float *from = begins ? (first && slot >= 0 && in_b ? first + state + (size_t)b * sb : nullptr)
-                                                   : (STATES ? nullptr : own_state - D * D + b);
-            int step = begins ? sa : D;
+                                                   : (STATES ? nullptr : A.state + ((size_t)A.of[job] * A.fine + piece * halves - 1) * D * D + (turned ? b * D : b));
+            int step = begins ? sa : turned ? 1 : D;
             if (A.kept && open) {
-                float *const kept = A.kept + ((size_t)job * A.pieces + piece) * D * D + b;
+                float *const kept = A.kept + (size_t)piece * D * D + b;
                 if (STATES) {
 #pragma unroll 4
                     for (int i = a0; i < min(ja, a0 + COLS); ++i) kept[(size_t)i * D] = from ? from[(size_t)i * step] : 0.f;
@@ -976,7 +983,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 }
             }
         }
-        if (STATES && threadIdx.x == CTL + PREP) A.head[job * A.pieces + piece].keep = lost ? __int_as_float(0x7fffffff) : exp2_units(units);
+        if (STATES && threadIdx.x == CTL + PREP) A.head[job * A.fine + piece].keep = lost ? __int_as_float(0x7fffffff) : exp2_units(units);
     }
     leave();
 }
@@ -1040,67 +1047,62 @@ template <class... P, class... X> cudaError_t follow(void (*kernel)(P...), dim3 
 
 }  // namespace
 
-// The pieces' states, kept first states and heads, the number of records, and the records of up to two directions.
-static size_t fixed_part() { return ((size_t)MOST_PIECES * (2 * D * D * sizeof(float) + sizeof(Head)) + 8 + 255) & ~size_t(255); }
+// The pieces' states (of two jobs, or of one with the first states that it keeps) and heads, the number of records, and the records of up
+// to two directions.
+static size_t states_part() { return (size_t)2 * MOST_PIECES * (D * D * sizeof(float) + sizeof(Head)); }
+static size_t fixed_part() { return (states_part() + 8 + 255) & ~size_t(255); }
 static size_t records(int N, int T, int H) { return ((size_t)T / C + N) * H * sizeof(Record); }
-static long long *total_of(const Call &c) {
-    return reinterpret_cast<long long *>(static_cast<char *>(c.pieces) + (size_t)MOST_PIECES * (2 * D * D * sizeof(float) + sizeof(Head)));
-}
 size_t tc_workspace(int N, int T, int H, int directions) { return fixed_part() + records(N, T, H) * directions; }
 
-// One call's kernels behind the plan, which has written the jobs' records to rec.
-static cudaError_t launch_jobs(const Call &c, const Record *const *rec, int sms, cudaStream_t s) {
-    cudaError_t e;
-    TcArgs A{};
+// The arguments of a launch for a call's jobs; `pieces` CTAs a job.
+static cudaError_t arguments(TcArgs &A, const Call &c, const Record *const *rec, int pieces, int fine) {
+    A = TcArgs{};
     A.c = c;
     A.rows = c.T < C ? (c.T < 1 ? 1 : c.T) : C;
     int maps = 0;
-    const void *of[4] = {};
+    Rows of[4] = {};
     for (int j = 0; j < c.jobs; ++j) {
         const Rows *rows[4] = {&c.job[j].x, &c.job[j].y, &c.job[j].z, &c.job[j].r};
         int *at[4] = {&A.x[j], &A.y[j], &A.z[j], &A.r[j]};
         for (int u = 0; u < (c.job[j].dots ? 4 : 3); ++u) {
             int m = 0;
-            while (m < maps && of[m] != rows[u]->p) ++m;
+            while (m < maps && (of[m].p != rows[u]->p || of[m].share != rows[u]->share)) ++m;
             if (m == maps) {
-                of[maps++] = rows[u]->p;
-                if ((e = make_map(&A.map[m], rows[u]->p, c.T, c.H / rows[u]->share, u >= 2 ? c.job[j].b : c.job[j].a, A.rows)) != cudaSuccess) return e;
+                of[maps++] = *rows[u];
+                if (cudaError_t e = make_map(&A.map[m], rows[u]->p, c.T, c.H / rows[u]->share, u >= 2 ? c.job[j].b : c.job[j].a, A.rows)) return e;
             }
             *at[u] = m;
         }
+        if (c.job[j].out_bf16)
+            if (cudaError_t e = make_map(&A.out[j], c.job[j].out, c.T, c.H, c.job[j].b, A.rows)) return e;
         A.rec[j] = rec[j];
+        A.of[j] = j;
     }
-    bool plain = true;
-    for (int j = 0; j < c.jobs; ++j) {
-        if (c.job[j].out_bf16 && (e = make_map(&A.out[j], c.job[j].out, c.T, c.H, c.job[j].b, A.rows)) != cudaSuccess) return e;
-        plain = plain && c.job[j].out_bf16 && !c.job[j].exact && !c.job[j].dots && !c.job[j].anchors;
-    }
-    A.pieces = (sms < MOST_PIECES ? sms : MOST_PIECES) / c.jobs;
+    A.pieces = pieces;
+    A.fine = fine;
     A.state = static_cast<float *>(c.pieces);
-    A.kept = A.state + (size_t)MOST_PIECES * D * D;
-    A.head = reinterpret_cast<Head *>(A.kept + (size_t)MOST_PIECES * D * D);
-    A.total = total_of(c);
-    if (!c.job[0].first || c.job[0].first != c.job[0].last) A.kept = nullptr;
-    // one short sequence: every piece is a whole pair
-    const bool cut = !(c.N == 1 && c.T / C + 1 <= LEAST && c.H <= A.pieces);
-    if (cut) {
-        e = follow(tc_kernel<kStates>, dim3(A.pieces * c.jobs), THREADS, kSmem<kStates>, s, A);
-        if (e == cudaSuccess) e = follow(join_kernel, dim3(D * D / 1024, A.pieces, c.jobs), 256, 0, s, A.head, A.state, A.pieces);
-        if (e != cudaSuccess) return e;
-    }
-    return plain ? follow(tc_kernel<kPlain>, dim3(A.pieces * c.jobs), THREADS, kSmem<kPlain>, s, A)
-                 : follow(tc_kernel<kFull>, dim3(A.pieces * c.jobs), THREADS, kSmem<kFull>, s, A);
+    A.head = reinterpret_cast<Head *>(A.state + (size_t)2 * MOST_PIECES * D * D);
+    A.total = reinterpret_cast<long long *>(static_cast<char *>(c.pieces) + states_part());
+    if (c.jobs == 1 && c.job[0].first && c.job[0].first == c.job[0].last) A.kept = A.state + (size_t)MOST_PIECES * D * D;
+    return cudaSuccess;
 }
 
-cudaError_t launch_scan_tc(const Call *calls, int n, cudaStream_t s) {
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kStates>, (int)kSmem<kStates>, g_attr[0]);
-    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kPlain>, (int)kSmem<kPlain>, g_attr[1]);
-    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kFull>, (int)kSmem<kFull>, g_attr[2]);
-    if (e != cudaSuccess) return e;
-    const Call &c = calls[0];
+static cudaError_t states(const TcArgs &A, cudaStream_t s) {
+    if (cudaError_t e = follow(tc_kernel<kStates>, dim3(A.pieces * A.c.jobs), THREADS, kSmem<kStates>, s, A)) return e;
+    return follow(join_kernel, dim3(D * D / 1024, A.pieces, A.c.jobs), 256, 0, s, A.head, A.state, A.pieces);
+}
+static cudaError_t outputs(const TcArgs &A, cudaStream_t s) {
+    bool plain = true;
+    for (int j = 0; j < A.c.jobs; ++j) {
+        const Job &b = A.c.job[j];
+        plain = plain && b.out_bf16 && !b.exact && !b.dots && !b.anchors;
+    }
+    return plain ? follow(tc_kernel<kPlain>, dim3(A.pieces * A.c.jobs), THREADS, kSmem<kPlain>, s, A)
+                 : follow(tc_kernel<kFull>, dim3(A.pieces * A.c.jobs), THREADS, kSmem<kFull>, s, A);
+}
+
+// The records for some jobs: `rec` gets each one's.
+static void plan(const Call &c, int sms, const Record **rec, cudaStream_t s) {
     PlanArgs P{};
     P.g = c.g;
     P.cu = c.cu;
@@ -1109,30 +1111,70 @@ cudaError_t launch_scan_tc(const Call *calls, int n, cudaStream_t s) {
     P.T = c.T;
     P.H = c.H;
     P.group = 1;
-    P.total = total_of(c);
-    const Record *rec[2][3] = {};
-    for (int i = 0; i < n; ++i)
-        for (int j = 0; j < calls[i].jobs; ++j) {
-            const Job &b = calls[i].job[j];
-            for (const Rows *r : {&b.x, &b.y, &b.z})
-                if (r->share > P.group) P.group = r->share;
-            int k = 0;
-            while (k < P.variants && (P.reverse[k] != b.reverse || P.sp[k] != b.sp || P.sc[k] != b.sc || P.sw[k] != b.sw)) ++k;
-            if (k == P.variants) {
-                P.reverse[k] = b.reverse;
-                P.sp[k] = b.sp;
-                P.sc[k] = b.sc;
-                P.sw[k] = b.sw;
-                P.rec[k] = reinterpret_cast<Record *>(static_cast<char *>(c.pieces) + fixed_part() + k * records(c.N, c.T, c.H));
-                ++P.variants;
-            }
-            rec[i][j] = P.rec[k];
+    P.total = reinterpret_cast<long long *>(static_cast<char *>(c.pieces) + states_part());
+    for (int j = 0; j < c.jobs; ++j) {
+        const Job &b = c.job[j];
+        for (const Rows *r : {&b.x, &b.y, &b.z})
+            if (r->share > P.group) P.group = r->share;
+        int k = 0;
+        while (k < P.variants && (P.reverse[k] != b.reverse || P.sp[k] != b.sp || P.sc[k] != b.sc || P.sw[k] != b.sw)) ++k;
+        if (k == P.variants) {
+            P.reverse[k] = b.reverse;
+            P.sp[k] = b.sp;
+            P.sc[k] = b.sc;
+            P.sw[k] = b.sw;
+            P.rec[k] = reinterpret_cast<Record *>(static_cast<char *>(c.pieces) + fixed_part() + k * records(c.N, c.T, c.H));
+            ++P.variants;
         }
+        rec[j] = P.rec[k];
+    }
     plan_kernel<<<2 * sms, PLAN_THREADS, 0, s>>>(P);
     count_launch();
-    for (int i = 0; i < n; ++i)
-        if ((e = launch_jobs(calls[i], rec[i], sms, s)) != cudaSuccess) return e;
-    return cudaSuccess;
+}
+
+cudaError_t launch_scan_tc(const Call &c, bool apart, cudaStream_t s) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kStates>, (int)kSmem<kStates>, g_attr[0]);
+    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kPlain>, (int)kSmem<kPlain>, g_attr[1]);
+    if (e == cudaSuccess) e = smem_attr_once((const void *)tc_kernel<kFull>, (int)kSmem<kFull>, g_attr[2]);
+    if (e != cudaSuccess) return e;
+    if (sms > MOST_PIECES) sms = MOST_PIECES;
+    const Record *rec[3];
+    if (!apart) {
+        TcArgs A;
+        plan(c, sms, rec, s);
+        if ((e = arguments(A, c, rec, sms / c.jobs, sms / c.jobs)) != cudaSuccess) return e;
+        // one short sequence: every piece is a whole pair
+        const bool whole = c.N == 1 && c.T / C + 1 <= LEAST && c.H <= A.pieces;
+        if (!whole && (e = states(A, s)) != cudaSuccess) return e;
+        return outputs(A, s);
+    }
+    // dq and dv, whose dots and anchors take the operands in three parts, and dk by itself: its rows are all that it puts out.  dv's state is
+    // dk's turned, so states are taken for dq and dk, each in as many pieces as dk's launch has; dq's and dv's pieces are two of them.  (8 k
+    // tokens and 32 heads: 84 us of states, 123 with those of all three; dk 83, dq and dv 304.)
+    const int fine = sms & ~1;
+    plan(c, sms, rec, s);
+    Call two = c, one = c;
+    const Record *rec_two[2] = {rec[0], rec[2]}, *rec_one[1] = {rec[2]};
+    two.jobs = 2;
+    two.job[1] = c.job[2];
+    one.jobs = 1;
+    one.job[0] = c.job[2];
+    TcArgs A;
+    if ((e = arguments(A, two, rec_two, fine, fine)) != cudaSuccess) return e;
+    A.nested = true;
+    if ((e = states(A, s)) != cudaSuccess) return e;
+    if ((e = arguments(A, one, rec_one, fine, fine)) != cudaSuccess) return e;
+    A.nested = true;
+    A.of[0] = 1;
+    if ((e = outputs(A, s)) != cudaSuccess) return e;
+    two.job[1] = c.job[1];
+    rec_two[1] = rec[1];
+    if ((e = arguments(A, two, rec_two, fine / 2, fine)) != cudaSuccess) return e;
+    A.nested = A.turned[1] = true;
+    return outputs(A, s);
 }
 
 }  // namespace lin
