@@ -83,13 +83,14 @@ struct Call {
     const int32_t *slot;   // of first and last, or null
     int num_slots;
     unsigned *status;
-    void *pieces;          // the tensor-core path's part of the workspace
+    void *pieces;          // the path's own part of the workspace
 };
 
 // The slices of the output's channels that one CTA of the CUDA-core path takes; dots has one row of [T, H] for each.
 constexpr int kSlice = 32;
 inline int slices(int b) { return (b + kSlice - 1) / kSlice; }
 
+size_t f32_workspace();
 cudaError_t launch_scan_f32(const Call &c, cudaStream_t s);
 // The tensor-core path (lin_tc.cu): BF16, T > 0; dots has a row for each 32 channels too (four, whatever the width).
 size_t tc_workspace(int N, int T, int H, int directions);

@@ -1,6 +1,6 @@
 // lin_f32.cu -- linear attention's jobs (lin.cuh) on the CUDA cores, everything in FP32: the path of FP32 inputs.
 //
-// A CTA holds a [a, 32] slice of one head's state in shared memory and walks the sequence in chunks of 32 tokens, a token a
+// A CTA holds a [a, 32] slice of one head's state in shared memory and walks the sequence, or a piece of it, in chunks of 32 tokens, a token a
 // lane for the decays; the next chunk's rows are on their way, in registers, meanwhile.  The four products of a chunk (x y^T, its
 // product with z, x S, y^T z) are register tiles of 4 to 16 accumulators fed by 16-byte shared loads; the scores are worked out again by
 // each slice of b.  What bounds it is the shared loads, some 5 for 16 products of a thread, and the sequence of its steps.
@@ -10,7 +10,7 @@ namespace k3kda {
 namespace lin {
 namespace {
 
-constexpr int C = 32, THREADS = 256, PITCH_S = kSlice + 4;
+constexpr int C = 32, THREADS = 256, PITCH_S = kSlice + 4, LEAST = 2;
 
 struct Layout {
     int pa, x, y, z, s, p, w, total;       // floats
@@ -26,10 +26,19 @@ struct Layout {
     }
 };
 
-__global__ void __launch_bounds__(THREADS) scan_kernel(const __grid_constant__ Call A) {
+// Pieces of each sequence, where there are fewer CTAs than the GPU holds: their states come from a first pass (STATES), which takes those
+// of every piece but the last from zero, and a piece's own chain of those before it.
+struct Cut {
+    int pieces;
+    float *state, *keep;       // [jobs][pieces][N H][slices] of [a, 32] and of one; the last piece's holds the first state where it is written over
+    bool kept;
+};
+
+template <bool STATES> __global__ void __launch_bounds__(THREADS) scan_kernel(const __grid_constant__ Call A, const Cut cut) {
     extern __shared__ float4 smem4[];
     __shared__ unsigned lost;              // tokens of the chunk whose decay is NaN
-    const Job &J = A.job[blockIdx.z];
+    const int parts = STATES ? cut.pieces - 1 : cut.pieces, job = blockIdx.z / parts, piece = blockIdx.z % parts;
+    const Job &J = A.job[job];
     const int b0 = blockIdx.y * kSlice, a = J.a, nb = min(kSlice, J.b - b0);
     if (b0 >= J.b) return;
     float *sm = reinterpret_cast<float *>(smem4);
@@ -44,9 +53,36 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const __grid_constant__ C
     const size_t state = ((size_t)(slot < 0 ? 0 : slot) * A.H + h) * a * J.b;
     const int tx = tid % 8, ty = tid / 8;
 
-    for (int i = tid; i < a * kSlice; i += THREADS) {
-        const int c = i / kSlice, b = i % kSlice;
-        S[c * PITCH_S + b] = J.first && slot >= 0 && b < nb ? J.first[state + (size_t)c * J.sa + (size_t)(b0 + b) * J.sb] : 0.f;
+    const int begins = (int)((long long)chunks * piece / cut.pieces), ends = (int)((long long)chunks * (piece + 1) / cut.pieces);
+    // a piece's place among the states
+    auto place = [&](int p) { return (((size_t)job * cut.pieces + p) * gridDim.x + blockIdx.x) * gridDim.y + blockIdx.y; };
+    long long units = 0;                   // STATES: the piece's decay (warp 0)
+    unsigned gone = 0;
+    if (piece == 0) {
+        const float *kept = !STATES && cut.kept && cut.pieces > 1 ? cut.state + place(cut.pieces - 1) * (128 * kSlice) : nullptr;
+        for (int i = tid; i < a * kSlice; i += THREADS) {
+            const int c = i / kSlice, b = i % kSlice;
+            const float v = kept ? kept[i] : J.first && slot >= 0 && b < nb ? J.first[state + (size_t)c * J.sa + (size_t)(b0 + b) * J.sb] : 0.f;
+            S[c * PITCH_S + b] = v;
+            if (STATES && cut.kept) cut.state[place(cut.pieces - 1) * (128 * kSlice) + i] = v;
+        }
+    } else {
+        float v[128 * kSlice / THREADS];
+#pragma unroll
+        for (int k = 0; k < 128 * kSlice / THREADS; ++k) v[k] = 0.f;
+        if (!STATES)
+            for (int p = 0; p < piece; ++p) {
+                const float *from = cut.state + place(p) * (128 * kSlice);
+                const float e = cut.keep[place(p)];
+#pragma unroll
+                for (int k = 0; k < 128 * kSlice / THREADS; ++k)
+                    if (tid + k * THREADS < a * kSlice) v[k] = fmaf(e, v[k], from[tid + k * THREADS]);
+            }
+#pragma unroll
+        for (int k = 0; k < 128 * kSlice / THREADS; ++k) {
+            const int i = tid + k * THREADS;
+            if (i < a * kSlice) S[i / kSlice * PITCH_S + i % kSlice] = v[k];
+        }
     }
     const size_t base_x = h / J.x.share, base_y = h / J.y.share, base_z = h / J.z.share;
     const size_t hx = A.H / J.x.share, hy = A.H / J.y.share, hz = A.H / J.z.share;
@@ -64,17 +100,17 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const __grid_constant__ C
         for (int k = 0; k < MOST; ++k) {
             const int i = tid + k * THREADS, t = i / per_row, c = i % per_row * 4;
             const bool in = i < pieces && t < valid;
-            nx[k] = in ? *reinterpret_cast<const float4 *>(px + ((size_t)(t0 + t) * hx + base_x) * a + c) : none;
+            if (!STATES) nx[k] = in ? *reinterpret_cast<const float4 *>(px + ((size_t)(t0 + t) * hx + base_x) * a + c) : none;
             ny[k] = in ? *reinterpret_cast<const float4 *>(py + ((size_t)(t0 + t) * hy + base_y) * a + c) : none;
         }
         nz = tid / 8 < valid && tid % 8 * 4 < nb ? *reinterpret_cast<const float4 *>(pz + ((size_t)(t0 + tid / 8) * hz + base_z) * J.b + b0 + tid % 8 * 4) : none;
         if (tid < C) ng = tid < valid ? A.g[A.fixed ? h : (size_t)(t0 + tid) * A.H + h] : 0.f;
     };
-    if (chunks > 0) fetch(0);
-    for (int it = 0; it < chunks; ++it) {
+    if (begins < ends) fetch(begins);
+    for (int it = begins; it < ends; ++it) {
         const int chunk = J.reverse ? chunks - 1 - it : it, t0 = begin + chunk * C, valid = min(C, end - t0);
         __syncthreads();
-        if (J.anchors && !J.reverse && it > 0 && chunk * C % kAnchor == 0) {
+        if (!STATES && J.anchors && !J.reverse && it > 0 && chunk * C % kAnchor == 0) {
             float *to = J.anchors + ((size_t)(anchor_slot(begin, n) + chunk * C / kAnchor - 1) * A.H + h) * a * J.b;
             for (int i = tid; i < a * kSlice; i += THREADS)
                 if (i % kSlice < nb) to[(size_t)(i / kSlice) * J.b + b0 + i % kSlice] = S[i / kSlice * PITCH_S + i % kSlice];
@@ -83,7 +119,7 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const __grid_constant__ C
         for (int k = 0; k < MOST; ++k) {
             const int i = tid + k * THREADS;
             if (i < pieces) {
-                *reinterpret_cast<float4 *>(X + i / per_row * L.pa + i % per_row * 4) = nx[k];
+                if (!STATES) *reinterpret_cast<float4 *>(X + i / per_row * L.pa + i % per_row * 4) = nx[k];
                 *reinterpret_cast<float4 *>(Y + i / per_row * L.pa + i % per_row * 4) = ny[k];
             }
         }
@@ -108,10 +144,15 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const __grid_constant__ C
             wt[tid] = J.sw * (tid < valid ? (J.reverse ? up : down) : 0.f);
             if (tid == 0) lost = bad;
             if (tid == 0) *keep = bad ? nan : exp2_units(all);
+            if (STATES) {
+                units += all;
+                gone |= bad;
+            }
         }
         __syncthreads();
-        if (it + 1 < chunks) fetch(it + 1);
+        if (it + 1 < ends) fetch(it + 1);
 
+        if constexpr (!STATES) {
         {   // scores: 2 x 2 a thread
             const int i0 = tid / 16, j0 = tid % 16;
             float acc[2][2] = {};
@@ -182,6 +223,7 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const __grid_constant__ C
             }
         }
         __syncthreads();
+        }
 
         // the state: rows 4 ty .. 4 ty + 3, channels 4 tx .. 4 tx + 3
         if (4 * ty < a) {
@@ -210,7 +252,7 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const __grid_constant__ C
             for (int u = 0; u < 4; ++u)
                 *reinterpret_cast<float4 *>(S + (4 * ty + u) * PITCH_S + 4 * tx) = make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]);
         }
-        if (J.anchors && J.reverse && chunk > 0 && chunk * C % kAnchor == 0) {
+        if (!STATES && J.anchors && J.reverse && chunk > 0 && chunk * C % kAnchor == 0) {
             __syncthreads();
             float *to = J.anchors + ((size_t)(anchor_slot(begin, n) + chunk * C / kAnchor - 1) * A.H + h) * a * J.b;
             for (int i = tid; i < a * kSlice; i += THREADS)
@@ -218,6 +260,12 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const __grid_constant__ C
         }
     }
     __syncthreads();
+    if (STATES) {
+        for (int i = tid; i < a * kSlice; i += THREADS) cut.state[place(piece) * (128 * kSlice) + i] = S[i / kSlice * PITCH_S + i % kSlice];
+        if (tid == 0) cut.keep[place(piece)] = gone ? __int_as_float(0x7fffffff) : exp2_units(units);
+        return;
+    }
+    if (piece < cut.pieces - 1) return;
     for (int i = tid; i < a * kSlice; i += THREADS) {
         const int c = i / kSlice, b = i % kSlice;
         if (b >= nb) continue;
@@ -228,20 +276,41 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const __grid_constant__ C
     }
 }
 
-std::atomic<uint64_t> g_attr{0};
+std::atomic<uint64_t> g_attr[2];
+
+constexpr int MOST_CTAS = 320, MOST_CUT = 64;
 
 }  // namespace
+
+size_t f32_workspace() { return (size_t)MOST_CTAS * (128 * kSlice + 1) * sizeof(float); }
 
 cudaError_t launch_scan_f32(const Call &c, cudaStream_t s) {
     if (c.N == 0) return cudaSuccess;
     const int most = (int)(Layout(128).total * sizeof(float));
-    if (cudaError_t e = smem_attr_once((const void *)scan_kernel, most, g_attr)) return e;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = smem_attr_once((const void *)scan_kernel<false>, most, g_attr[0]);
+    if (e == cudaSuccess) e = smem_attr_once((const void *)scan_kernel<true>, most, g_attr[1]);
+    if (e != cudaSuccess) return e;
     int wide = 0, bytes = 0;
     for (int j = 0; j < c.jobs; ++j) {
         wide = max(wide, slices(c.job[j].b));
         bytes = max(bytes, (int)(Layout(c.job[j].a).total * sizeof(float)));
     }
-    scan_kernel<<<dim3((unsigned)(c.N * c.H), wide, c.jobs), THREADS, bytes, s>>>(c);
+    // Two CTAs an SM, pieces of LEAST chunks or more on average.  (Heads of 128 channels, uncut and cut: 8 heads of 8,192 tokens 1,938 and 479 us,
+    // of 1,024 tokens 247 and 79, of 256 tokens 67 and 34, where pieces of 4 chunks took 50; 32 heads of 2,048 tokens 492 and 495; gradients of 8 heads
+    // of 8,192 tokens 2,279 and 1,513.)
+    const long long ctas = (long long)c.N * c.H * wide * c.jobs, chunks = c.T / C / c.N;
+    long long pieces = min((long long)min(2 * sms, MOST_CTAS) / ctas, chunks / LEAST);
+    const Cut cut{(int)max(1ll, min(pieces, (long long)MOST_CUT)), static_cast<float *>(c.pieces), static_cast<float *>(c.pieces) + (size_t)MOST_CTAS * 128 * kSlice,
+                  c.jobs == 1 && c.job[0].first && c.job[0].first == c.job[0].last};
+    const dim3 grid((unsigned)(c.N * c.H), wide, c.jobs);
+    if (cut.pieces > 1) {
+        scan_kernel<true><<<dim3(grid.x, grid.y, grid.z * (cut.pieces - 1)), THREADS, bytes, s>>>(c, cut);
+        count_launch();
+    }
+    scan_kernel<false><<<dim3(grid.x, grid.y, grid.z * cut.pieces), THREADS, bytes, s>>>(c, cut);
     count_launch();
     return cudaGetLastError();
 }

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(256) group_kernel(const float *p1, const float
 
 size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
 
-// The workspace: the status word, what the tensor-core path keeps, and the gradient's parts.
+// The workspace: the status word, the states of the pieces that sequences are cut into, and the gradient's parts.
 struct Space {
     size_t pieces, r1, r2, S, R, f, dg, pq, pk, total;
     Space(int N, int T, int Hk, int H, int dk, int dv, int bf16, bool backward) {
@@ -190,7 +190,7 @@ struct Space {
             return was;
         };
         const size_t TH = (size_t)T * H, slots = anchor_slots(N, T);
-        pieces = take(bf16 ? tc_workspace(N, T, H, backward ? 2 : 1) : 0);
+        pieces = take(bf16 ? tc_workspace(N, T, H, backward ? 2 : 1) : f32_workspace());
         r1 = r2 = S = R = f = dg = pq = pk = at;
         if (backward) {
             r1 = take(TH * (bf16 ? 4 : slices(dk)) * 4);

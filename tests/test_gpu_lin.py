@@ -243,6 +243,19 @@ def test_a_state_may_be_its_own_successor():
     assert torch.equal(o, out) and torch.equal(state, last)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_a_pool_of_states_in_place_under_sequences_that_are_cut(dtype):
+    c = _case([2500, 0, 1, 1100], 1, 2, 64, 64, dtype, seed=17)
+    out, last = K.lin_prefill(c["q"], c["k"], c["v"], c["g"], c["first"], c["cu"])
+    slots = torch.tensor([5, 0, 3, 1], dtype=torch.int32, device=DEV)
+    pool = torch.full((6, 2, 64, 64), 7.0, device=DEV)
+    pool[slots.long()] = c["first"]
+    o, p = K.lin_prefill(c["q"], c["k"], c["v"], c["g"], pool, c["cu"], state_idx=slots)
+    assert p is pool and torch.equal(o, out) and torch.equal(pool[slots.long()], last)
+    assert (pool[[2, 4]] == 7).all()
+    _check_prefill(c)
+
+
 # ---- gradients ----------------------------------------------------------------------------------
 
 def _check_backward(c):
