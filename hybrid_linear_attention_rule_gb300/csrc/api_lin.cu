@@ -19,7 +19,7 @@ bool dim_ok(int d) { return d >= 16 && d <= 128 && d % 16 == 0; }
 // Sizes that every call of linear attention shares.  Rows and states are counted in 31 bits where a grid or a tensor map needs it.
 int check_sizes(int N, int T, int Hk, int H, int dk, int dv) {
     if (N < 1 || T < 0 || Hk < 1 || H < 1 || H % Hk != 0) return K3KDA_ERR_INVALID_ARG;
-    if (!dim_ok(dk) || !dim_ok(dv) || H > 65535 || (long long)N * H > (1LL << 28)) return K3KDA_ERR_UNSUPPORTED;
+    if (!dim_ok(dk) || !dim_ok(dv) || H > 65535 || T > 0x7fffffff - 128 || (long long)N * H > (1LL << 28)) return K3KDA_ERR_UNSUPPORTED;
     return K3KDA_OK;
 }
 
@@ -50,6 +50,9 @@ int check_slots(const int32_t *idx, const int32_t *host, int N, int num_slots, i
     return ok ? K3KDA_OK : K3KDA_ERR_INVALID_ARG;
 }
 
+// Whether an output is one of some arrays (other CTAs still read them when it is written).
+template <class... P> bool is_one_of(const void *out, const P *...p) { return out && ((out == (const void *)p) || ...); }
+
 template <class... P> bool all16(const P *...p) { return (aligned(p, 16) && ...); }
 
 }  // namespace
@@ -74,6 +77,7 @@ int k3lin_prefill(const void *q, const void *k, const void *v, int in_dtype, con
     if (!all16(q, k, v, out, initial_state, final_state) || !aligned(g, 4)) return K3KDA_ERR_ALIGNMENT;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < lin_workspace(N, T, Hk, H, dk, dv, in_dtype == K3KDA_BF16, 0))
         return K3KDA_ERR_WORKSPACE;
+    if (T > 0 && is_one_of(out, q, k, v, g)) return K3KDA_ERR_INVALID_ARG;
     const LinArgs a{q, k, v, in_dtype == K3KDA_BF16, g, g_per_head != 0, initial_state, state_idx, num_slots, cu_seqlens,
                     N, T, Hk, H, dk, dv, scale, workspace};
     return status_of(launch_lin_prefill(a, out, out_dtype == K3KDA_BF16, final_state, static_cast<cudaStream_t>(stream)));
@@ -88,6 +92,7 @@ int k3lin_decode_step(const void *q, const void *k, const void *v, int in_dtype,
     if (N == 0) return K3KDA_OK;
     if (!q || !k || !v || !g || !state || !out) return K3KDA_ERR_INVALID_ARG;
     if (!all16(q, k, v, out, state) || !aligned(g, 4)) return K3KDA_ERR_ALIGNMENT;
+    if (is_one_of(out, q, k, v, g, state)) return K3KDA_ERR_INVALID_ARG;
     return status_of(launch_lin_decode(q, k, v, in_dtype == K3KDA_BF16, g, g_per_head != 0, state, state_idx, num_slots, N, Hk, H,
                                        dk, dv, scale, out, out_dtype == K3KDA_BF16, static_cast<cudaStream_t>(stream)));
 }
@@ -109,6 +114,10 @@ int k3lin_backward(const void *q, const void *k, const void *v, int in_dtype, co
         return K3KDA_ERR_ALIGNMENT;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < lin_workspace(N, T, Hk, H, dk, dv, in_dtype == K3KDA_BF16, 1))
         return K3KDA_ERR_WORKSPACE;
+    if (is_one_of(dS0, initial_state, dS_final)) return K3KDA_ERR_INVALID_ARG;
+    if (T > 0)
+        for (const void *p : {(const void *)dq, (const void *)dk_out, (const void *)dv_out, (const void *)dg})
+            if (is_one_of(p, q, k, v, dO, g)) return K3KDA_ERR_INVALID_ARG;
     const LinArgs a{q, k, v, in_dtype == K3KDA_BF16, g, g_per_head != 0, initial_state, nullptr, 0, cu_seqlens,
                     N, T, Hk, H, dk, dv, scale, workspace};
     return status_of(launch_lin_backward(a, dO, dS_final, dq, dk_out, dv_out, dg, dS0, static_cast<cudaStream_t>(stream)));
@@ -165,6 +174,7 @@ int k3blk_norm_backward(const void *x, int dtype, const void *ds, const void *dy
         if (!aligned(p, unit)) return K3KDA_ERR_ALIGNMENT;
     if ((dpost_weight || dpre_weight) && (!workspace || !aligned(workspace, 256) || workspace_bytes < blk_norm_workspace(rows, D)))
         return K3KDA_ERR_WORKSPACE;
+    if (rows > 0 && is_one_of(dresidual, post_weight || gate ? x : nullptr, gate)) return K3KDA_ERR_INVALID_ARG;
     blk::Args a{};
     a.x = post_weight || gate ? x : nullptr;
     a.gate = gate;

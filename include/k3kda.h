@@ -577,7 +577,9 @@ int k3mla_paged_attend(const k3mla_paged_cache *cache, const k3mla_view *q, int 
  * k3lin_backward -- gradients for dO [T, H, dv] (in_dtype) and dS_final [N, H, dk, dv] (FP32, or NULL: zero):
  * dq, dk_out [T, Hk, dk], dv_out [T, H, dv] in in_dtype, those of shared heads summed in FP32 before their one rounding; dg (or NULL)
  * FP32 in g's shape; dS0 (or NULL) [N, H, dk, dv] FP32.  q, k, v, g, initial_state are the forward's.
- * Errors: INVALID_ARG, UNSUPPORTED (also H > 65535, N H > 2^28, num_slots H > 2^31 - 1), ALIGNMENT (16 bytes; g, dg, cu_seqlens,
+ * An output may not overlap an input, but for states in place: a prefill's final_state may be its initial_state, the same address
+ * (INVALID_ARG where an output's address is another input's).
+ * Errors: INVALID_ARG, UNSUPPORTED (also H > 65535, T > 2^31 - 129, N H > 2^28, num_slots H > 2^31 - 1), ALIGNMENT (16 bytes; g, dg, cu_seqlens,
  * state_idx: 4), WORKSPACE, CUDA. */
 size_t k3lin_prefill_workspace_size(int N, int T, int Hk, int H, int dk, int dv, int in_dtype);
 int k3lin_prefill(const void *q, const void *k, const void *v, int in_dtype, const float *g, int g_per_head,
@@ -605,7 +607,7 @@ int k3lin_backward(const void *q, const void *k, const void *v, int in_dtype, co
  * gate), sum (with pre_weight: s as it was stored), gate: dx, dresidual (or NULL; the whole gradient of s), dgate (with gate) and, in FP32, dpost_weight and
  * dpre_weight (given with their weights), summed over the rows in an order that does not change from run to run.
  * workspace: k3blk_norm_backward_workspace_size bytes, 256-byte aligned, scratch; needed with a weight's gradient only.
- * An output may be the input of its shape that it replaces (the same address), else they may not overlap.  Squares are summed in FP32.
+ * An output may be an input of its shape (the same address), else they may not overlap; dresidual may not be x or gate (INVALID_ARG).  Squares are summed in FP32.
  * Errors: INVALID_ARG, UNSUPPORTED (D, rows above 2^31 - 1), ALIGNMENT (to the element; arrays of 16-byte alignment and a D of whole 16-byte pieces
  * move in 16-byte pieces), WORKSPACE, CUDA.  rows = 0 launches nothing (the backward writes zero weights' gradients). */
 typedef enum { K3BLK_GATE_SIGMOID = 0, K3BLK_GATE_SILU = 1 } k3blk_gate_act;

@@ -308,6 +308,21 @@ def test_backward_one_long_sequence_is_cut_and_joined():
     _check_backward(_case([6000], 3, 3, 128, 128, BF, seed=24, decay=0.02))
 
 
+@pytest.mark.parametrize("lens", [[300, 64, 1, 0, 900], [10] * 25, [64] * 38 + [65]], ids=lambda x: f"{len(x)} sequences")
+def test_backward_of_more_pairs_than_ctas(lens):
+    """Pieces of dk's launch that are halves of the others', and too few chunks for halves."""
+    h = 40 if len(lens) == 5 else 4
+    _check_backward(_case(lens, h // 2, h, 64, 48, BF, seed=27))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_backward_of_no_tokens(dtype):
+    c = _case([0, 0], 2, 4, 64, 48, dtype, seed=28)
+    for g in (c["g"], torch.tensor([-1.0, -2.0, 0.0, -0.5], device=DEV)):
+        d = K.lin_backward(c["q"], c["k"], c["v"], g, c["do"], c["first"], c["dlast"], c["cu"])
+        assert torch.equal(d["dS0"], c["dlast"]) and d["dq"].shape == (0, 2, 64) and (d["dg"] == 0).all() and d["dg"].shape == g.shape
+
+
 def test_backward_without_the_decays_gradient():
     c = _case([140, 80], 2, 4, 128, 64, BF, seed=25)
     args = [c[x] for x in ("q", "k", "v", "g", "do", "first", "dlast", "cu")]

@@ -125,6 +125,22 @@ def test_norm_backward_refusals(lib):
     assert lib.k3blk_norm_backward_workspace_size(10, 0) == 0 and lib.k3blk_norm_backward_workspace_size(10, 64) >= 2 * 64 * 4
 
 
+def test_outputs_that_are_inputs_are_refused(lib):
+    at = lambda n: 0x10000 + 0x10000 * n  # noqa: E731
+    for name in ("q", "k", "v", "g"):
+        assert _prefill(lib, **{**dict(q=at(1), k=at(2), v=at(3), g=at(4), out=at(5)), name: at(5)}) == -1, name
+        assert _decode(lib, **{**dict(q=at(1), k=at(2), v=at(3), g=at(4), state=at(6), out=at(5)), name: at(5)}) == -1, name
+    assert _decode(lib, q=at(1), k=at(2), v=at(3), g=at(4), state=at(5), out=at(5)) == -1
+    apart = dict(q=at(1), k=at(2), v=at(3), g=at(4), do=at(5), dq=at(6), dk_=at(7), dv_=at(8), dg=at(9), first=at(10), dlast=at(11), ds=at(12))
+    for out in ("dq", "dk_", "dv_", "dg"):
+        for name in ("q", "k", "v", "do", "g"):
+            assert _backward(lib, **{**apart, out: apart[name]}) == -1, (out, name)
+    assert _backward(lib, **{**apart, "ds": apart["first"]}) == -1 and _backward(lib, **{**apart, "ds": apart["dlast"]}) == -1
+    apart = dict(x=at(1), ds=at(2), dy=at(3), sum=at(4), gate=at(5), dx=at(6), dgate=at(8))
+    assert _norm_back(lib, **apart, dres=at(1)) == -1 and _norm_back(lib, **apart, dres=at(5)) == -1
+    assert _prefill(lib, T=(1 << 31) - 100, size=1 << 62) == -2
+
+
 def test_the_binding_refuses_cpu_tensors_and_wrong_shapes():
     q = torch.zeros(4, 2, 64)
     with pytest.raises(ValueError):
