@@ -8,13 +8,13 @@
 //     d = ds + r_s (dy pre - h_s mean(dy pre h_s)),  h_s = s r_s            dresidual = d,  dpre = sum over rows dy h_s
 //     dgate = alpha d u act'(gate),  du = alpha d act(gate)
 //     dx = r_x (du post - h_x mean(du post h_x)),  h_x = x r_x              dpost = sum over rows du h_x
-// Every array is read once and written once: a row is held in registers by its threads, 16 elements each, so HBM bounds both.  Rows
+// Every array is read once and written once: a row is held in registers by its threads, up to 16 elements each, so HBM bounds both.  Rows
 // of up to 128 channels take 8 threads, of up to 16384 a CTA of 1024; arrays move in 16-byte pieces where the width and the
 // addresses allow it, else element by element.  The gradient's rows are copied to shared memory two rounds ahead.  All arithmetic is FP32, each output is rounded once; y comes from the sum
 // before its rounding.
 //
 // 16,384 rows of 4,096 in BF16, all parts: 114 us, 88 % of a plain copy's rate; 131,072 rows of 128 with a gate 22.5 us, 67 %.  Gradients of 8,192
-// rows of 4,096: 123 us, 65 %, the issue slots half used; of 2,777 rows of 1,111 in FP32, whose rows begin off 16 bytes, 49 us, 30 %.
+// rows of 4,096: 123 us, 65 %, the issue slots half used; of 2,777 rows of 1,111 in FP32, whose rows begin off 16 bytes, 40 us, 36 %.
 #pragma once
 
 #include "common.cuh"
@@ -23,8 +23,8 @@
 namespace k3kda {
 namespace blk {
 
-constexpr int E = 16;                  // elements of a row that one thread holds
-constexpr int MOST_D = 1024 * E;
+constexpr int MOST_E = 16;             // elements of a row that one thread holds, at most
+constexpr int MOST_D = 1024 * MOST_E;
 constexpr int MOST_PARTS = 304;        // CTAs of the gradient: two an SM, each a partial sum of the weights' gradients
 
 struct Args {
@@ -40,7 +40,7 @@ struct Args {
 };
 
 inline int threads_a_row(int D) {
-    const int need = (D + E - 1) / E;
+    const int need = (D + MOST_E - 1) / MOST_E;
     return need <= 8 ? 8 : need <= 32 ? 32 : need <= 128 ? 128 : need <= 256 ? 256 : need <= 512 ? 512 : 1024;
 }
 inline long long groups_of(int tpr) { return tpr < 256 ? 256 / tpr : 1; }
@@ -57,7 +57,7 @@ template <class T> __device__ __forceinline__ float inverse(float x) { return si
 template <class T> __device__ __forceinline__ float sigmoid_of(float z) { return inverse<T>(1.f + exp_of<T>(-z)); }
 
 // Thread t's elements of a row: pieces of VEC at (t + i TPR) VEC.
-template <class T, int VEC, int TPR> struct Slot {
+template <class T, int VEC, int TPR, int E> struct Slot {
     static constexpr int ITEMS = E / VEC, WORDS = VEC == 1 ? E : E * (int)sizeof(T) / 4;
     static __device__ __forceinline__ int column(int t, int e) { return (t + e / VEC * TPR) * VEC + e % VEC; }
     // As they lie in memory (BF16 pieces two to a word): half the registers until they are used.
@@ -155,7 +155,8 @@ template <int TPR, int N> __device__ __forceinline__ void row_sums(float (&v)[N]
 }
 
 template <class T, int VEC, int TPR> __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR > 256 ? 1024 / TPR : VEC == 8 ? 4 : 3) norm_kernel(const __grid_constant__ Args A) {
-    using S = Slot<T, VEC, TPR>;
+    constexpr int E = MOST_E;
+    using S = Slot<T, VEC, TPR, E>;
     constexpr int THREADS = TPR < 256 ? 256 : TPR, GROUPS = THREADS / TPR;
     __shared__ float room[GROUPS * 2 * (TPR / 32 + 1) * 4];
     const int t = threadIdx.x % TPR;
@@ -205,7 +206,7 @@ template <class T, int VEC, int TPR> __global__ void __launch_bounds__(TPR < 256
 // Rows on their way: up to five arrays' next GROUPS rows (one stretch of memory) in shared memory, two deep, while those before are worked on.
 // A copy starts and ends on 16 bytes, so it may hold up to 15 more on either side, never past the array's last whole 16; what lies behind is
 // fetched by the threads.
-template <class T, int TPR> struct Ring {
+template <class T, int TPR, int E> struct Ring {
     static constexpr int THREADS = TPR < 256 ? 256 : TPR, GROUPS = THREADS / TPR;
     static constexpr int ARRAYS = 5;
     static constexpr bool FITS = 2 * ARRAYS * (TPR * GROUPS * E * (int)sizeof(T) + 32) <= 220 * 1024;
@@ -215,9 +216,9 @@ template <class T, int TPR> struct Ring {
 };
 
 // The weights' gradients: a thread keeps its columns' sums over the rows of its CTA, in a fixed order.
-template <class T, int VEC, int TPR> __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) norm_grad_kernel(const __grid_constant__ Args A) {
-    using S = Slot<T, VEC, TPR>;
-    using Q = Ring<T, TPR>;
+template <class T, int VEC, int TPR, int E> __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) norm_grad_kernel(const __grid_constant__ Args A) {
+    using S = Slot<T, VEC, TPR, E>;
+    using Q = Ring<T, TPR, E>;
     constexpr int THREADS = Q::THREADS, GROUPS = Q::GROUPS;
     extern __shared__ __align__(16) char ring[];
     __shared__ float room[GROUPS * 2 * (TPR / 32 + 1) * 4];
@@ -402,18 +403,28 @@ template <class T, int VEC, int TPR> __global__ void __launch_bounds__(TPR < 256
     }
 }
 
+template <class T, int VEC, int TPR, int E> cudaError_t launch_grad(const Args &a, cudaStream_t s) {
+    static std::atomic<uint64_t> attr{0};
+    using Q = Ring<T, TPR, E>;
+    const int bytes = Q::FITS ? Q::bytes(a.D) : 0;
+    if (Q::FITS)
+        if (cudaError_t e = smem_attr_once((const void *)norm_grad_kernel<T, VEC, TPR, E>, Q::bytes(TPR * E), attr)) return e;
+    norm_grad_kernel<T, VEC, TPR, E><<<(unsigned)parts_of(a.rows, a.D), TPR < 256 ? 256 : TPR, bytes, s>>>(a);
+    count_launch();
+    return cudaGetLastError();
+}
 template <class T, int VEC, int TPR> cudaError_t launch(const Args &a, bool grad, cudaStream_t s) {
     constexpr int THREADS = TPR < 256 ? 256 : TPR, GROUPS = THREADS / TPR;
     if (grad) {
-        static std::atomic<uint64_t> attr{0};
-        using Q = Ring<T, TPR>;
-        const int bytes = Q::FITS ? Q::bytes(a.D) : 0;
-        if (Q::FITS)
-            if (cudaError_t e = smem_attr_once((const void *)norm_grad_kernel<T, VEC, TPR>, Q::bytes(TPR * E), attr)) return e;
-        norm_grad_kernel<T, VEC, TPR><<<(unsigned)parts_of(a.rows, a.D), THREADS, bytes, s>>>(a);
-    } else {
-        norm_kernel<T, VEC, TPR><<<(unsigned)((a.rows + GROUPS - 1) / GROUPS), THREADS, 0, s>>>(a);
+        // (single elements: all that a thread may hold is worked on, whether the row has it or not, and with 16 it does not fit
+        // the registers: 2,777 rows of 1,111 in FP32 take 49 us with 16 and 40 with 12)
+        if constexpr (VEC == 1 && TPR < 256) {
+            if (a.D <= TPR * 8) return launch_grad<T, VEC, TPR, 8>(a, s);
+            if (a.D <= TPR * 12) return launch_grad<T, VEC, TPR, 12>(a, s);
+        }
+        return launch_grad<T, VEC, TPR, MOST_E>(a, s);
     }
+    norm_kernel<T, VEC, TPR><<<(unsigned)((a.rows + GROUPS - 1) / GROUPS), THREADS, 0, s>>>(a);
     count_launch();
     return cudaGetLastError();
 }

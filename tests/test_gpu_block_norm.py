@@ -105,6 +105,15 @@ def test_widths(D, dtype):
         _check_backward(c, _backward(c))
 
 
+@pytest.mark.parametrize("D", [63, 65, 96, 97, 255, 257, 383, 385, 1025, 1535, 1537])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_widths_at_which_a_thread_holds_more(D, dtype):
+    for rows in (1, 70):
+        c = _case(rows, D, dtype, gate="silu", seed=8)
+        _check_forward(c, _forward(c))
+        _check_backward(c, _backward(c))
+
+
 @pytest.mark.parametrize("post,gate,residual,pre", list(itertools.product([False, True], [None, "sigmoid", "silu"], [False, True], [False, True])))
 @pytest.mark.parametrize("dtype,D", [(BF, 256), (F32, 130)], ids=["bf16", "f32"])
 def test_parts(post, gate, residual, pre, dtype, D):
