@@ -86,13 +86,19 @@ struct Call {
     void *pieces;          // the path's own part of the workspace
 };
 
-// The slices of the output's channels that one CTA of the CUDA-core path takes; dots has one row of [T, H] for each.
-constexpr int kSlice = 32;
-inline int slices(int b) { return (b + kSlice - 1) / kSlice; }
+// The slices of the output's channels that one CTA of the CUDA-core path takes, as wide for all jobs of a call; dots has one row of [T, H] for each.
+// 64 channels read less of shared memory for the same products, 32 have shorter steps where the call cannot fill the GPU with pieces of two
+// chunks.  (8 heads of 128 channels, with 32 and 64: 8,192 tokens 479 and 336 us, 1,024 tokens 79 and 65, 256 tokens 34 and 42; 32 heads of 2,048
+// tokens 495 and 378; gradients of 8 heads of 8,192 tokens 1,515 and 1,097.)
+inline int slice_width(int N, int T, int H, int jobs, int most_b) {
+    const long long chunks = (long long)T / 32 / N, pieces = chunks < 4 ? 1 : chunks / 2;
+    return most_b > 32 && pieces * N * H * jobs * ((most_b + 63) / 64) >= 152 ? 64 : 32;
+}
+inline int slices(int b, int width) { return (b + width - 1) / width; }
 
 size_t f32_workspace();
 cudaError_t launch_scan_f32(const Call &c, cudaStream_t s);
-// The tensor-core path (lin_tc.cu): BF16, T > 0; dots has a row for each 32 channels too (four, whatever the width).
+// The tensor-core path (lin_tc.cu): BF16, T > 0; dots has a row for each 32 channels (four, whatever the width).
 size_t tc_workspace(int N, int T, int H, int directions);
 // Jobs of at most two directions and scales.  `apart`: they are dq, dv and dk, and dk gets a launch of its own.
 cudaError_t launch_scan_tc(const Call &c, bool apart, cudaStream_t s);

@@ -192,11 +192,12 @@ struct Space {
             return was;
         };
         const size_t TH = (size_t)T * H, slots = anchor_slots(N, T);
+        const int width = slice_width(N, T, H, 3, dk > dv ? dk : dv);
         pieces = take(bf16 ? tc_workspace(N, T, H, backward ? 2 : 1) : f32_workspace());
         r1 = r2 = S = R = f = dg = pq = pk = at;
         if (backward) {
-            r1 = take(TH * (bf16 ? 4 : slices(dk)) * 4);
-            r2 = take(TH * (bf16 ? 4 : slices(dv)) * 4);
+            r1 = take(TH * (bf16 ? 4 : slices(dk, width)) * 4);
+            r2 = take(TH * (bf16 ? 4 : slices(dv, width)) * 4);
             S = take(slots * H * dk * dv * 4);
             R = take(slots * H * dk * dv * 4);
             f = take(slots * H * 8);
@@ -329,7 +330,8 @@ cudaError_t launch_lin_backward(const LinArgs &a, const void *dO, const float *d
         anchor_kernel<<<dim3(seqs, a.H, deep), 256, 0, s>>>(g);
         count_launch();
         float *to = a.fixed ? part(w.dg) : dg;
-        const SumArgs u{part(w.r1), part(w.r2), on_tensor_cores(c) ? 4 : slices(a.dk), on_tensor_cores(c) ? 4 : slices(a.dv), f, to, a.cu, a.N, a.T, a.H};
+        const int width = slice_width(a.N, a.T, a.H, c.jobs, a.dk > a.dv ? a.dk : a.dv);
+        const SumArgs u{part(w.r1), part(w.r2), on_tensor_cores(c) ? 4 : slices(a.dk, width), on_tensor_cores(c) ? 4 : slices(a.dv, width), f, to, a.cu, a.N, a.T, a.H};
         sum_kernel<<<dim3(seqs, (a.H + 7) / 8, deep), 512, 0, s>>>(u);
         count_launch();
         if (a.fixed) {
