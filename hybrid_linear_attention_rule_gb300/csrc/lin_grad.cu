@@ -6,6 +6,8 @@
 // jobs write both.  Summed from the sequence's end alone, the rounding of every later token would stay in f(t); so at anchors,
 // every 512 tokens, f is worked out directly as <S, R> of the two states that the jobs left there, and the sums, in 64
 // bits, start anew.  Leaving the pairs s = t = u out keeps them from cancelling where the decay is strong.
+#include <algorithm>
+
 #include "lin.cuh"
 
 namespace k3kda {
@@ -71,8 +73,9 @@ __global__ void __launch_bounds__(256) anchor_kernel(const __grid_constant__ Anc
 }
 
 // dg: a CTA sums one stretch between anchors for 8 heads (a 32-byte piece of a row), 64 runs of 8 tokens, each a thread a head.  The runs
-// behind a thread's own come by shuffles (a warp has four) and one sum a warp, so that few additions are in 64 bits: 8 k tokens
-// of 32 heads (8 MB) 15 us, 20 with a walk over all runs behind; what is left is the latency of a few CTAs' loads.
+// behind a thread's own come by shuffles (a warp has four) and one sum a warp, so that few additions are in 64 bits, of which an SM
+// does about two a cycle; a run's own eight are in FP32, as its terms are.  8 k tokens of 32 heads (8 MB): 11 us, 15 with those in
+// 64 bits too; 5 sequences to 1,900 tokens of 16 heads 10.6 us, 24 then and with their stretches one after the other.
 struct SumArgs {
     const float *r1, *r2;             // [slices][T, H]
     int n1, n2;                       // slices
@@ -109,9 +112,11 @@ __global__ void __launch_bounds__(512) sum_kernel(const __grid_constant__ SumArg
                     for (int i = 0; i < RUN; ++i)
                         if (t0 + i < t1) q[i] += A.r2[u * TH + (size_t)(t0 + i) * A.H + h];
             }
-            double sum = 0.0;
+            // the run's own sums, from each token to its end
+            p[RUN - 1] -= q[RUN - 1];
 #pragma unroll
-            for (int i = 0; i < RUN; ++i) sum += p[i] - q[i];
+            for (int i = RUN - 2; i >= 0; --i) p[i] = p[i + 1] + (p[i] - q[i]);
+            const double sum = p[0];
             // of the warp's runs: those from the thread's own on, those behind it
             const double next = __shfl_down_sync(0xffffffffu, sum, 8), pair = lane < 24 ? sum + next : sum;
             const double far = __shfl_down_sync(0xffffffffu, pair, 16), from = lane < 16 ? pair + far : pair;
@@ -122,11 +127,10 @@ __global__ void __launch_bounds__(512) sum_kernel(const __grid_constant__ SumArg
                 double f = A.f[(size_t)(anchor_slot(begin, n) + k) * A.H + h];
                 for (int u = 15; u > warp; --u) f += part[u][hl];
                 if (lane < 24) f += after;
+                const float whole = (float)f, rest = (float)(f - whole);
 #pragma unroll
-                for (int i = RUN - 1; i >= 0; --i) {
-                    f += p[i] - q[i];
-                    if (t0 + i < t1) A.dg[(size_t)(t0 + i) * A.H + h] = (float)f;
-                }
+                for (int i = 0; i < RUN; ++i)
+                    if (t0 + i < t1) A.dg[(size_t)(t0 + i) * A.H + h] = whole + (rest + p[i]);
             }
             __syncthreads();
         }
@@ -324,15 +328,19 @@ cudaError_t launch_lin_backward(const LinArgs &a, const void *dO, const float *d
     if (cudaError_t e = launch_scan(c, dg != nullptr, s)) return e;
     const unsigned seqs = (unsigned)(a.N < 1024 ? a.N : 1024);
     if (dg) {
-        const unsigned deep = (unsigned)(a.T / kAnchor / seqs + 1 < 256 ? a.T / kAnchor / seqs + 1 : 256);
+        // stretches between anchors that CTAs take at once: all, unless these are many
+        auto deep = [&](int across) {
+            const unsigned mean = a.T / kAnchor / seqs + 1, room = 1024 / (seqs * across), most = a.T / kAnchor + 1;
+            return std::min(std::min(std::max(mean, room), most), 256u);
+        };
         double *f = reinterpret_cast<double *>(ws + w.f);
         const AnchorArgs g{part(w.S), part(w.R), dlast, f, a.cu, a.N, a.T, a.H, a.dk, a.dv};
-        anchor_kernel<<<dim3(seqs, a.H, deep), 256, 0, s>>>(g);
+        anchor_kernel<<<dim3(seqs, a.H, deep(a.H)), 256, 0, s>>>(g);
         count_launch();
         float *to = a.fixed ? part(w.dg) : dg;
         const int width = slice_width(a.N, a.T, a.H, c.jobs, a.dk > a.dv ? a.dk : a.dv);
         const SumArgs u{part(w.r1), part(w.r2), on_tensor_cores(c) ? 4 : slices(a.dk, width), on_tensor_cores(c) ? 4 : slices(a.dv, width), f, to, a.cu, a.N, a.T, a.H};
-        sum_kernel<<<dim3(seqs, (a.H + 7) / 8, deep), 512, 0, s>>>(u);
+        sum_kernel<<<dim3(seqs, (a.H + 7) / 8, deep((a.H + 7) / 8)), 512, 0, s>>>(u);
         count_launch();
         if (a.fixed) {
             fixed_kernel<<<a.H, 512, 0, s>>>(to, dg, a.cu, a.N, a.T, a.H);
