@@ -39,7 +39,17 @@ constexpr int REG_CTL = 40, REG_PREP = 72, REG_HOLD = 80;
 static_assert(CTL * REG_CTL + PREP * REG_PREP + HOLD * REG_HOLD <= THREADS * 72, "shares of the registers");
 constexpr int COLS = 32, TOKENS = 16;                              // of the state and of the outputs that one of the holding threads has
 constexpr uint32_t kTries = 1u << 20;            // a second or two
-constexpr int MOST_PIECES = 160, LEAST = 16;       // LEAST: chunks of a piece, at least, where there are more pieces than pairs
+constexpr int MOST_PIECES = 160, WHOLE = 8;        // WHOLE: pairs of fewer chunks on average stay whole, where there are no more of them than CTAs
+
+// How many pieces a line of U chunks of `pairs` pairs is worth, where up to `pieces` run at once: a CTA for each pair, or pieces of 16 chunks; where
+// that leaves most SMs idle and pairs are long enough for a first pass, short ones of 2, or of 4 where pairs are long (their join walks over the
+// pieces).  (One sequence, prefill and gradients in us, with pieces of 16, 4 and 2 chunks: 8 heads, 300 tokens 24 74, 36 87, 29 72; 600 tokens 38 116,
+// 36 94, 30 78; 1,024 tokens 58 159, 36 94, 32 79; 2,048 tokens 81 194, 40 96, 38 103; 4,096 tokens 82 201, 47 132, 49 133; 2 heads of 8,192 tokens
+// 84 192, 55 104, 72 144.  8 sequences of 512 tokens and 8 heads, whole 39 103, in pieces of 4 chunks 38 120.)
+__device__ __forceinline__ long long worth(long long U, long long pairs, int pieces) {
+    const long long fine = U / (U < 32 * pairs ? 2 : 4);
+    return U >= WHOLE * pairs && min((long long)pieces, fine) >= 2 * pairs ? fine : max(pairs, U / 16);
+}
 
 enum Kind { kStates, kPlain, kFull };      // states alone; jobs whose operands are in two parts and that put out nothing but BF16 rows; any, in three parts
 
@@ -405,9 +415,11 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
     wait_for_last();
 
     // ---- where the piece begins and ends
-    const long long U = *A.total, most = max((long long)A.c.N * H, U / LEAST);
+    const long long U = *A.total;
     // (halves are there where each of them has a chunk)
-    const int coarse = A.nested ? A.fine / 2 : A.fine, count_fine = A.nested && most > coarse && U >= A.fine ? A.fine : (int)min((long long)coarse, most);
+    const int coarse = A.nested ? A.fine / 2 : A.fine;
+    const long long most = worth(U, (long long)A.c.N * H, coarse);
+    const int count_fine = A.nested && most > coarse && U >= A.fine ? A.fine : (int)min((long long)coarse, most);
     const int halves = FULL && A.pieces != A.fine && count_fine > coarse ? 2 : 1, count_pieces = count_fine / halves;
     if (piece >= count_pieces) {
         if (STATES && tid == 0) A.head[job * A.fine + piece] = Head{0.f, 0, 0};
@@ -1151,7 +1163,7 @@ cudaError_t launch_scan_tc(const Call &c, bool apart, cudaStream_t s) {
         plan(c, sms, rec, s);
         if ((e = arguments(A, c, rec, sms / c.jobs, sms / c.jobs)) != cudaSuccess) return e;
         // one short sequence: every piece is a whole pair
-        const bool whole = c.N == 1 && c.T / C + 1 <= LEAST && c.H <= A.pieces;
+        const bool whole = c.N == 1 && (c.T + C - 1) / C < WHOLE && c.H <= A.pieces;
         if (!whole && (e = states(A, s)) != cudaSuccess) return e;
         return outputs(A, s);
     }
