@@ -321,7 +321,8 @@ template <class T, int VEC, int TPR, int E> __global__ void __launch_bounds__(TP
                 row_of(3, sr);
                 row_of(4, dyr);
             }
-            const float r = rsqrtf(sums[0] * inv + A.eps), m = sums[1] * inv * r;     // m: mean(dy pre h_s)
+            // (a row that is not there has factors of 0: with an eps of 0 they would be infinite, and its zeros NaN in the weights' sums)
+            const float r = in ? rsqrtf(sums[0] * inv + A.eps) : 0.f, m = sums[1] * inv * r;     // m: mean(dy pre h_s)
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const float h = S::value(sr, e) * r, y = S::value(dyr, e);
@@ -332,7 +333,7 @@ template <class T, int VEC, int TPR, int E> __global__ void __launch_bounds__(TP
         if (A.dresidual) S::store(A.dresidual, at, t, D, d);
 #pragma unroll
         for (int e = 0; e < E; ++e) d[e] *= A.alpha;
-        const float r = A.post ? rsqrtf(sums[2] * inv + A.eps) : 1.f;
+        const float r = !A.post ? 1.f : in ? rsqrtf(sums[2] * inv + A.eps) : 0.f;
         if (A.post) S::weights(A.post, t, D, w);
         if (A.x && Q::FITS && sizeof(T) == 4) row_of(1, xr);
         if (A.gate) {

@@ -247,3 +247,41 @@ def test_against_differences():
         step = torch.rand(c[name].shape, generator=gen, device=DEV) * 2 - 1
         got = (loss(**{name: c[name] + h * step}) - loss(**{name: c[name] - h * step})) / (2 * h)
         assert abs(got - (d[grad].double() * step).sum().item()) <= (2 * A / h + 10 * h * h) * size, name
+
+
+def _check_with_eps(c, eps):
+    """Forward and gradients for another eps: the bounds above, with it in the norms' factors."""
+    half = _half(c["x"])
+    x, res, post, pre = (c[n].double() for n in ("x", "residual", "post", "pre"))
+    args = (c["x"], c["residual"], c["gate"], c["gate_act"], c["post"], c["pre"], c["alpha"])
+    s, y = K.block_norm(*args, eps=eps)
+    want, wy = P.block_norm(*args, eps)
+    M = (want - res).abs() + res.abs()
+    _near(s, want, M, A, "s")
+    _near(y, wy, (M / torch.sqrt((want * want).mean(-1, keepdim=True) + eps) + wy.abs()) * (pre.abs() + 1), 2 * A, "y")
+    d = K.block_norm_backward(c["x"], c["ds"], c["dy"], c["sum"], c["gate"], c["gate_act"], c["post"], c["pre"], c["alpha"], eps)
+    w = P.block_norm_backward(c["x"], c["ds"], c["dy"], c["sum"], c["gate"], c["gate_act"], c["post"], c["pre"], c["alpha"], eps)
+    rows = x.shape[0]
+
+    def terms(d, x, weight):
+        r = 1 / torch.sqrt((x * x).mean(-1, keepdim=True) + eps)
+        h = (x * r).abs()
+        return r * (d * weight.abs() + h * (d * weight.abs() * h).mean(-1, keepdim=True)), (d * h).sum(0)
+    more, mw = terms(c["dy"].double().abs(), c["sum"].double(), pre)
+    M = c["ds"].double().abs() + more
+    _near(d["dpre"], w["dpre"], mw, A + (rows + 16) * 2.0 ** -24, "dpre")
+    _near(d["dresidual"], w["dresidual"], M, A, "dresidual")
+    M, z = M * abs(c["alpha"]), c["gate"].double()
+    _near(d["dgate"], w["dgate"], M * (P.unit(x, eps) * post).abs() * (1 + z.abs() / 4), 2 * A, "dgate")
+    M, mw = terms(M * P.act(c["gate_act"], z).abs(), x, post)
+    _near(d["dpost"], w["dpost"], mw, 2 * A + (rows + 16) * 2.0 ** -24, "dpost")
+    _near(d["dx"], w["dx"], M, 3 * A, "dx")
+
+
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -10, 4.0])
+@pytest.mark.parametrize("D", [8, 64, 512, 768, 1024, 1111, 2048, 2560, 16384])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_other_eps(D, eps, dtype):
+    """With an eps of 0 as well, rows that a CTA's last round does not have add nothing to the weights' gradients."""
+    for rows in (1, 3, 37, 70):
+        _check_with_eps(_case(rows, D, dtype, seed=13), eps)
