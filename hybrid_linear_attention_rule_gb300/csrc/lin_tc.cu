@@ -1075,17 +1075,20 @@ static cudaError_t arguments(TcArgs &A, const Call &c, const Record *const *rec,
     A = TcArgs{};
     A.c = c;
     A.rows = c.T < C ? (c.T < 1 ? 1 : c.T) : C;
-    int maps = 0;
+    // (arrays may lie in one place with other widths: q, k and v as views of the same memory)
+    int maps = 0, width[4] = {};
     Rows of[4] = {};
     for (int j = 0; j < c.jobs; ++j) {
         const Rows *rows[4] = {&c.job[j].x, &c.job[j].y, &c.job[j].z, &c.job[j].r};
         int *at[4] = {&A.x[j], &A.y[j], &A.z[j], &A.r[j]};
         for (int u = 0; u < (c.job[j].dots ? 4 : 3); ++u) {
+            const int d = u >= 2 ? c.job[j].b : c.job[j].a;
             int m = 0;
-            while (m < maps && (of[m].p != rows[u]->p || of[m].share != rows[u]->share)) ++m;
+            while (m < maps && (of[m].p != rows[u]->p || of[m].share != rows[u]->share || width[m] != d)) ++m;
             if (m == maps) {
-                of[maps++] = *rows[u];
-                if (cudaError_t e = make_map(&A.map[m], rows[u]->p, c.T, c.H / rows[u]->share, u >= 2 ? c.job[j].b : c.job[j].a, A.rows)) return e;
+                of[maps] = *rows[u];
+                width[maps++] = d;
+                if (cudaError_t e = make_map(&A.map[m], rows[u]->p, c.T, c.H / rows[u]->share, d, A.rows)) return e;
             }
             *at[u] = m;
         }

@@ -1,0 +1,31 @@
+"""Linear attention with a decay a head where its calls meet their limits: inputs that share memory, scales far from one, sums of
+decays beyond 64 bits, values that are not finite and the decays' gradient, the bits that are promised.  Bounds are those of test_gpu_lin.py."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import hybrid_linear_attention_rule_gb300 as K  # noqa: E402
+import lin_plain as P  # noqa: E402
+import test_gpu_lin as L  # noqa: E402
+
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("hk", [2, 4])
+def test_inputs_of_other_widths_in_one_place(hk):
+    """q, k and v may lie in one another: views of the same memory with other widths and heads."""
+    T, h = 200, 4
+    gen = torch.Generator(DEV).manual_seed(61)
+    buf, do = (torch.randn(T * h * 128, generator=gen, device=DEV).bfloat16() for _ in range(2))
+    g = -torch.rand((T, h), generator=gen, device=DEV)
+    small, wide = buf[:T * hk * 64].view(T, hk, 64), buf.view(T, h, 128)
+    first = torch.randn((1, h, 64, 128), generator=gen, device=DEV)
+    for views, grad in (((small, small, wide), do.view(T, h, 128)), ((small, small, wide), wide)):
+        apart = [x.clone() for x in views]
+        a, b = K.lin_prefill(*views, g, first), K.lin_prefill(*apart, g, first)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+        for need in (True, False):
+            a, b = K.lin_backward(*views, g, grad, first, need_dg=need), K.lin_backward(*apart, g, grad.clone(), first, need_dg=need)
+            assert all(torch.equal(a[x], b[x]) for x in b if b[x] is not None)
