@@ -332,8 +332,9 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
                 fj[e] = A.sp[k] * (reverse ? up : inverse);
                 plain = plain && fabsf(f.x) < 100.f;
             }
-            // (sums of up to 100 powers of two: neither factor leaves FP32's range, and their product is D's)
-            plain = __all_sync(0xffffffffu, plain) && !bad;
+            // (sums of up to 100 powers of two and a scale of up to 2^25 or down to 2^-25: neither factor leaves FP32's range, and their
+            // product is D's)
+            plain = __all_sync(0xffffffffu, plain) && !bad && fabsf(A.sp[k]) < 33554432.f && fabsf(A.sp[k]) > 2.98e-8f;
             reinterpret_cast<float4 *>(R.g)[lane] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
             reinterpret_cast<float2 *>(R.c)[lane] = make_float2(c[0], c[1]);
             reinterpret_cast<float2 *>(R.w)[lane] = make_float2(w[0], w[1]);

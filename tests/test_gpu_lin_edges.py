@@ -29,3 +29,27 @@ def test_inputs_of_other_widths_in_one_place(hk):
         for need in (True, False):
             a, b = K.lin_backward(*views, g, grad, first, need_dg=need), K.lin_backward(*apart, g, grad.clone(), first, need_dg=need)
             assert all(torch.equal(a[x], b[x]) for x in b if b[x] is not None)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 40, -2.0 ** 33, 2.0 ** -40])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_scales_far_from_one(scale, dtype):
+    """Decays of up to 2^-99 a chunk times a scale leave FP32's range in a factor, not in any result."""
+    c = L._case([200], 2, 2, 64, 64, dtype, seed=62)
+    c["g"].fill_(-1.07)
+    c["scale"] = scale
+    a = [c[x] for x in "qkvg"]
+    out, last = K.lin_prefill(*a, c["first"], scale=scale, out_dtype=F32)
+    want, wlast = P.prefill(*a, None, c["first"], scale)
+    M, Ml = P.prefill(*(c[x].abs() for x in "qkv"), c["g"], None, c["first"].abs(), abs(scale))
+    L._near(out, want, M, L._arith(dtype, 200, True), "out")
+    L._near(last, wlast, Ml, L._arith(dtype, 200, True), "state")
+    for need in (True, False):
+        d = K.lin_backward(*a, c["do"], c["first"], c["dlast"], scale=scale, need_dg=need)
+        w = P.backward(*a, c["do"], None, c["first"], c["dlast"], scale)
+        M = P.backward(*(c[x].abs() for x in "qkv"), c["g"], c["do"].abs(), None, c["first"].abs(), c["dlast"].abs(), abs(scale))
+        for x in ("dq", "dk", "dv"):
+            L._near(d[x], w[x], M[x], L._arith(dtype, 200), x)
+        L._near(d["dS0"], w["dS0"], M["dS0"], L._arith(dtype, 200, True), "dS0")
+        if need:
+            L._near(d["dg"], w["dg"], M["each"].flip(0).cumsum(0).flip(0) + M["dg_token"], L._arith(dtype, 200, True), "dg")
