@@ -20,13 +20,19 @@ namespace lin {
 
 // Sums of g are kept as 64-bit integers in units of 2^-32 of a power of two: differences of any two are exact, whatever lies
 // between, and the order of the sum does not matter.  One decay counts as at most 4096 powers of two (e^g = 0 in FP32 long
-// before: minus infinity is a reset), so 64 of them fit many times.
+// before: minus infinity is a reset), so a chunk's sum stays within 2^50 units; sums of many chunks stop at 2^62 (`add_units`).
 __device__ __forceinline__ long long decay_units(float g) {
     constexpr float kLog2e = 1.442695040888963f, kRest = 1.925963033500e-8f;       // log2(e) and what its FP32 value leaves
     const float p = g * kLog2e;
     if (!(fabsf(p) < 4096.f)) return p != p ? 0 : p < 0.f ? -(4096LL << 32) : 4096LL << 32;
     const float whole = rintf(p), rest = (p - whole) + (fmaf(g, kLog2e, -p) + g * kRest);        // |rest| < 0.51
     return ((long long)(int)whole << 32) + 2LL * __float2int_rn(rest * 2147483648.f);
+}
+// The sum of a piece's decays and of a chunk's.  It stops at 2^30 powers of two either way, where a plain sum of 2^19 resets would leave 64 bits.
+__device__ __forceinline__ long long add_units(long long sum, long long chunk) {
+    constexpr long long kMost = 1LL << 62;
+    sum += chunk;
+    return sum > kMost ? kMost : sum < -kMost ? -kMost : sum;
 }
 // The sum's whole and remaining powers of two, apart: differences of two such pairs keep an accuracy of 2^-24 however large the sums.
 __device__ __forceinline__ float2 two_floats(long long v) {

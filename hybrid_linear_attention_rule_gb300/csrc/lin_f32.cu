@@ -151,7 +151,7 @@ template <bool STATES, int W> __global__ void __launch_bounds__(THREADS, 2) scan
             if (tid == 0) lost = bad;
             if (tid == 0) *keep = bad ? nan : exp2_units(all);
             if (STATES) {
-                units += all;
+                units = add_units(units, all);
                 gone |= bad;
             }
         }

@@ -851,7 +851,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                 chunk = I.chunk;
                 dirty = sh.dirty[s];
                 if (STATES) {
-                    units += I.units;
+                    units = add_units(units, I.units);
                     lost = lost || I.lost;
                 }
                 const float keep = I.keep;

@@ -53,3 +53,29 @@ def test_scales_far_from_one(scale, dtype):
         L._near(d["dS0"], w["dS0"], M["dS0"], L._arith(dtype, 200, True), "dS0")
         if need:
             L._near(d["dg"], w["dg"], M["each"].flip(0).cumsum(0).flip(0) + M["dg_token"], L._arith(dtype, 200, True), "dg")
+
+
+def _after_resets(T, N, dtype):
+    """One sequence of T tokens, each a reset, among N - 1 empty ones: out_t = scale (q_t . k_t) v_t, whatever came before."""
+    gen = torch.Generator(DEV).manual_seed(60)
+    block = 1 << 16
+    rows = [torch.randn((block, 1, 16), generator=gen, device=DEV).to(dtype) for _ in range(3)]
+    q, k, v = (x.repeat((T + block - 1) // block, 1, 1)[:T] for x in rows)
+    cu = torch.zeros(N + 1, dtype=torch.int32, device=DEV)
+    cu[N // 2 + 1:] = T
+    out, last = K.lin_prefill(q, k, v, torch.full((T, 1), -float("inf"), device=DEV), None, cu)
+    p = 0.25 * (rows[0].double() * rows[1].double())
+    want, M = p.sum(-1, keepdim=True) * rows[2].double(), p.abs().sum(-1, keepdim=True) * rows[2].double().abs()
+    for t in range(0, T, block):
+        n = min(block, T - t)
+        L._near(out[t:t + n], want[:n], M[:n], L._arith(dtype, 1), f"from token {t}")
+    t = (T - 1) % block
+    L._near(last[N // 2, 0], rows[1][t, 0].double()[:, None] * rows[2][t, 0].double(), torch.ones(16, 16, device=DEV, dtype=torch.float64),
+            L._arith(dtype, 1, True) * 32, "state")
+
+
+def test_pieces_of_so_many_resets_that_64_bits_would_not_hold_their_sum():
+    """A reset counts as 4,096 powers of two in units of 2^-32 of one: 2^19 of them are 2^63.  Three pieces of one sequence in FP32; 152 of one in
+    BF16."""
+    _after_resets(3 * (2 ** 19 + 64), 100, F32)
+    _after_resets(152 * (2 ** 19 + 128), 1, BF)
