@@ -73,6 +73,12 @@ int status_of(cudaError_t e);
 // Counts every kernel this library launches (reported by k3kda_launch_count).
 void count_launch();
 
+// The launch just made: counted, and whether it was accepted (its error is not left to the next call).
+inline cudaError_t launched() {
+    count_launch();
+    return cudaGetLastError();
+}
+
 // Test hook for the bounded in-kernel waits.  k3kda_test_arm_wait_timeout (exported for the tests,
 // not part of the public header) arms one of these; the next launch of that kernel takes the armed
 // count (and disarms it), and its CTA 0 then issues none of the copies its first bounded wait waits

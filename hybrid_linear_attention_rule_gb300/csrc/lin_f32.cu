@@ -329,11 +329,10 @@ template <int W> cudaError_t launch(const Call &c, std::atomic<uint64_t> *attr, 
     const dim3 grid((unsigned)(c.N * c.H), wide, c.jobs);
     if (cut.pieces > 1) {
         scan_kernel<true, W><<<dim3(grid.x, grid.y, grid.z * (cut.pieces - 1)), THREADS, bytes, s>>>(c, cut);
-        count_launch();
+        if ((e = launched()) != cudaSuccess) return e;
     }
     scan_kernel<false, W><<<dim3(grid.x, grid.y, grid.z * cut.pieces), THREADS, bytes, s>>>(c, cut);
-    count_launch();
-    return cudaGetLastError();
+    return launched();
 }
 
 }  // namespace

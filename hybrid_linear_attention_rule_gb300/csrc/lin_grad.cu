@@ -336,15 +336,15 @@ cudaError_t launch_lin_backward(const LinArgs &a, const void *dO, const float *d
         double *f = reinterpret_cast<double *>(ws + w.f);
         const AnchorArgs g{part(w.S), part(w.R), dlast, f, a.cu, a.N, a.T, a.H, a.dk, a.dv};
         anchor_kernel<<<dim3(seqs, a.H, deep(a.H)), 256, 0, s>>>(g);
-        count_launch();
+        if (cudaError_t e = launched()) return e;
         float *to = a.fixed ? part(w.dg) : dg;
         const int width = slice_width(a.N, a.T, a.H, c.jobs, a.dk > a.dv ? a.dk : a.dv);
         const SumArgs u{part(w.r1), part(w.r2), on_tensor_cores(c) ? 4 : slices(a.dk, width), on_tensor_cores(c) ? 4 : slices(a.dv, width), f, to, a.cu, a.N, a.T, a.H};
         sum_kernel<<<dim3(seqs, (a.H + 7) / 8, deep((a.H + 7) / 8)), 512, 0, s>>>(u);
-        count_launch();
+        if (cudaError_t e = launched()) return e;
         if (a.fixed) {
             fixed_kernel<<<a.H, 512, 0, s>>>(to, dg, a.cu, a.N, a.T, a.H);
-            count_launch();
+            if (cudaError_t e = launched()) return e;
         }
     }
     if (group > 1) {
@@ -353,10 +353,10 @@ cudaError_t launch_lin_backward(const LinArgs &a, const void *dO, const float *d
             const int here = a.N - n < 65535 ? a.N - n : 65535;
             group_kernel<<<dim3((unsigned)(rows < 2048 ? rows : 2048), 2, here), 256, 0, s>>>(part(w.pq), part(w.pk), dq, dk, a.bf16,
                                                                                             a.cu ? a.cu + n : nullptr, here, a.T, a.Hk, group, a.dk);
-            count_launch();
+            if (cudaError_t e = launched()) return e;
         }
     }
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 }  // namespace k3kda

@@ -1058,8 +1058,8 @@ template <class... P, class... X> cudaError_t follow(void (*kernel)(P...), dim3 
     at.val.programmaticStreamSerializationAllowed = 1;
     c.attrs = &at;
     c.numAttrs = 1;
-    count_launch();
-    return cudaLaunchKernelEx(&c, kernel, P(args)...);
+    (void)cudaLaunchKernelEx(&c, kernel, P(args)...);
+    return launched();
 }
 
 }  // namespace
@@ -1122,7 +1122,7 @@ static cudaError_t outputs(const TcArgs &A, cudaStream_t s) {
 }
 
 // The records for some jobs: `rec` gets each one's.
-static void plan(const Call &c, int sms, const Record **rec, cudaStream_t s) {
+static cudaError_t plan(const Call &c, int sms, const Record **rec, cudaStream_t s) {
     PlanArgs P{};
     P.g = c.g;
     P.cu = c.cu;
@@ -1149,7 +1149,7 @@ static void plan(const Call &c, int sms, const Record **rec, cudaStream_t s) {
         rec[j] = P.rec[k];
     }
     plan_kernel<<<2 * sms, PLAN_THREADS, 0, s>>>(P);
-    count_launch();
+    return launched();
 }
 
 cudaError_t launch_scan_tc(const Call &c, bool apart, cudaStream_t s) {
@@ -1164,7 +1164,7 @@ cudaError_t launch_scan_tc(const Call &c, bool apart, cudaStream_t s) {
     const Record *rec[3];
     if (!apart) {
         TcArgs A;
-        plan(c, sms, rec, s);
+        if ((e = plan(c, sms, rec, s)) != cudaSuccess) return e;          // (the records are addresses to the others)
         if ((e = arguments(A, c, rec, sms / c.jobs, sms / c.jobs)) != cudaSuccess) return e;
         // one short sequence: every piece is a whole pair
         const bool whole = c.N == 1 && (c.T + C - 1) / C < WHOLE && c.H <= A.pieces;
@@ -1175,7 +1175,7 @@ cudaError_t launch_scan_tc(const Call &c, bool apart, cudaStream_t s) {
     // dk's turned, so states are taken for dq and dk, each in as many pieces as dk's launch has; dq's and dv's pieces are two of them.  (8 k
     // tokens and 32 heads: 84 us of states, 123 with those of all three; dk 83, dq and dv 304.)
     const int fine = sms & ~1;
-    plan(c, sms, rec, s);
+    if ((e = plan(c, sms, rec, s)) != cudaSuccess) return e;
     Call two = c, one = c;
     const Record *rec_two[2] = {rec[0], rec[2]}, *rec_one[1] = {rec[2]};
     two.jobs = 2;

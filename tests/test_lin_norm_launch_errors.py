@@ -1,0 +1,118 @@
+"""A launch that fails ends its call with the error: no later launch, no error left over for the next call.  The library runs on a stand-in
+for the CUDA runtime that launches nothing, counts, and refuses one launch (no GPU)."""
+import json
+import os
+import subprocess
+import sys
+
+import pytest
+
+import hybrid_linear_attention_rule_gb300.build as B
+
+FAKE = r"""
+#include <stddef.h>
+static int launches, refused, last;
+void fake_refuse(int nth) { launches = 0; refused = nth; last = 0; }
+int fake_launches(void) { return launches; }
+static int launch(void) { return ++launches == refused ? (last = 1) : 0; }
+int __cudaLaunchKernel(void) { return launch(); }
+int cudaLaunchKernel(void) { return launch(); }
+int cudaLaunchKernelExC(void) { return launch(); }
+int cudaLaunchCooperativeKernel(void) { return launch(); }
+int cudaGetLastError(void) { const int e = last; last = 0; return e; }
+static int encode(void) { return 0; }
+int cudaGetDriverEntryPointByVersion(const char *name, void **fn, unsigned version, unsigned long long flags, int *found) {
+    *fn = (void *)encode;
+    *found = 0;
+    return 0;
+}
+int cudaGetDevice(int *device) { *device = 0; return 0; }
+int cudaDeviceGetAttribute(int *value, int which, int device) { *value = 152; return 0; }
+const char *cudaGetErrorString(int e) { return e ? "refused" : "no error"; }
+const char *cudaGetErrorName(int e) { return cudaGetErrorString(e); }
+static int module;
+void **__cudaRegisterFatBinary(void *binary) { static void *handle = &module; return &handle; }
+void __cudaRegisterFatBinaryEnd(void **handle) {}
+void __cudaUnregisterFatBinary(void **handle) {}
+void __cudaRegisterFunction(void) {}
+void __cudaRegisterVar(void) {}
+int __cudaGetKernel(void **kernel, const void *function) { *kernel = &module; return 0; }
+int __cudaPushCallConfiguration(void) { return 0; }
+int __cudaPopCallConfiguration(void) { return 0; }
+int cudaFuncGetAttributes(void) { return 1; }
+int cudaFuncSetAttribute(void) { return 0; }
+int cudaGetSymbolAddress(void) { return 1; }
+int cudaMemcpyAsync(void) { return 1; }
+int cudaMemcpyFromSymbolAsync(void) { return 1; }
+int cudaMemcpyToSymbolAsync(void) { return 1; }
+int cudaMemsetAsync(void) { return 1; }
+int cudaOccupancyMaxActiveBlocksPerMultiprocessorWithFlags(void) { return 1; }
+int cudaStreamSynchronize(void) { return 1; }
+"""
+
+CHILD = r"""
+import ctypes, json, sys
+fake = ctypes.CDLL("libcudart.so.13")
+lib = ctypes.CDLL(sys.argv[1])
+P, I, F, L, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong, ctypes.c_size_t
+at = lambda n: P(n << 40)
+big = Z(1 << 38)
+def prefill(bf, N, T, Hk, H):
+    return lib.k3lin_prefill(at(1), at(2), at(3), I(bf), at(4), I(0), at(5), None, None, I(0), at(6), None, I(N), I(T), I(Hk), I(H), I(64), I(64), F(1),
+                             at(7), I(bf), at(8), at(9), big, None)
+def decode():
+    return lib.k3lin_decode_step(at(1), at(2), at(3), I(1), at(4), I(0), at(5), None, None, I(4), I(4), I(2), I(2), I(64), I(64), F(1), at(6), I(1), None)
+def backward(bf, fixed, N, T, Hk, H, dg):
+    return lib.k3lin_backward(at(1), at(2), at(3), I(bf), at(4), I(fixed), at(5), at(6), None, I(N), I(T), I(Hk), I(H), I(64), I(64), F(1), at(7), at(8),
+                              at(10), at(11), at(12), at(13) if dg else None, at(14), at(9), big, None)
+def norm(back):
+    if not back:
+        return lib.k3blk_norm(at(1), I(1), at(2), at(3), I(0), at(4), at(5), L(100), I(64), F(1), F(0), at(6), at(7), None)
+    return lib.k3blk_norm_backward(at(1), I(1), at(2), at(3), at(4), at(5), I(0), at(6), at(7), L(100), I(64), F(1), F(0), at(10), at(11), at(12), at(13),
+                                   at(14), at(9), big, None)
+calls = {"prefill bf16": lambda: prefill(1, 2, 5000, 2, 4), "prefill bf16, short": lambda: prefill(1, 1, 40, 2, 2), "prefill f32, cut": lambda: prefill(0, 1, 5000, 2, 2),
+         "prefill f32": lambda: prefill(0, 400, 5000, 2, 2), "decode": decode, "norm": lambda: norm(False), "norm backward": lambda: norm(True)}
+for bf in (0, 1):
+    for fixed in (0, 1):
+        for dg in (0, 1):
+            for hk in (2, 4):
+                calls["backward %d %d %d %d" % (bf, fixed, dg, hk)] = lambda bf=bf, fixed=fixed, dg=dg, hk=hk: backward(bf, fixed, 2, 5000, hk, 4, dg)
+out = {}
+for name, call in calls.items():
+    fake.fake_refuse(0)
+    status, n = call(), fake.fake_launches()
+    rows = [[status, n, fake.cudaGetLastError()]]
+    for k in range(1, n + 1):
+        fake.fake_refuse(k)
+        rows.append([call(), fake.fake_launches(), fake.cudaGetLastError()])
+    out[name] = rows
+print(json.dumps(out))
+"""
+
+
+@pytest.fixture(scope="module")
+def results(tmp_path_factory):
+    d = tmp_path_factory.mktemp("cudart")
+    (d / "fake.c").write_text(FAKE)
+    (d / "fake.map").write_text("libcudart.so.13 { global: *; };\n")
+    subprocess.run(["gcc", "-w", "-shared", "-fPIC", "-o", "libcudart.so.13", "fake.c", "-Wl,-soname,libcudart.so.13", "-Wl,--version-script,fake.map"],
+                   cwd=d, check=True)
+    r = subprocess.run([sys.executable, "-c", CHILD, B.build()], env={**os.environ, "LD_LIBRARY_PATH": str(d)}, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+    return json.loads(r.stdout)
+
+
+def test_every_launch_is_checked(results):
+    assert len(results) == 23
+    for name, (clean, *refused) in results.items():
+        assert clean[0] == 0 and clean[1] > 0 and clean[2] == 0, name
+        for k, (status, launches, left) in enumerate(refused, 1):
+            assert status == -5, f"{name}: launch {k} of {clean[1]} failed and the call returned {status}"
+            assert launches == k, f"{name}: launch {k} of {clean[1]} failed and the call went on to {launches}"
+            assert left == 0, f"{name}: launch {k} of {clean[1]} left its error behind"
+
+
+def test_calls_have_the_launches_that_they_should(results):
+    n = {name: rows[0][1] for name, rows in results.items()}
+    assert n["prefill bf16, short"] == 2 and n["prefill bf16"] == 4 and n["decode"] == n["norm"] == 1 and n["norm backward"] == 2
+    assert n["prefill f32, cut"] == 2 and n["prefill f32"] == 1
