@@ -3,6 +3,7 @@
 // device, synchronises, throws or prints.
 #include <math.h>
 
+#include <initializer_list>
 #include <new>
 
 #include "block_norm.cuh"
@@ -50,8 +51,39 @@ int check_slots(const int32_t *idx, const int32_t *host, int N, int num_slots, i
     return ok ? K3KDA_OK : K3KDA_ERR_INVALID_ARG;
 }
 
-// Whether an output is one of some arrays (other CTAs still read them when it is written).
+// An array of a call as memory, and whether two have a byte in common.
+struct Span {
+    const void *p;
+    size_t bytes;
+};
+bool overlap(const Span &a, const Span &b) {
+    if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x <= y ? y - x < a.bytes : x - y < b.bytes;
+}
+// Whether what is written lies clear of the inputs, which other CTAs and later launches still read meanwhile, and of one another.
+bool clear(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+    for (const Span *o = outputs.begin(); o != outputs.end(); ++o) {
+        for (const Span &i : inputs)
+            if (overlap(*o, i)) return false;
+        for (const Span *u = outputs.begin(); u != o; ++u)
+            if (overlap(*o, *u)) return false;
+    }
+    return true;
+}
+
+// Whether an output is one of some arrays.
 template <class... P> bool is_one_of(const void *out, const P *...p) { return out && ((out == (const void *)p) || ...); }
+
+// Bytes of linear attention's arrays for T rows.
+struct LinBytes {
+    size_t key, state, rows, heads, T;
+    LinBytes(int T_, int Hk, int H, int dk, int dv, int dtype)
+        : key((size_t)T_ * Hk * dk * size(dtype)), state((size_t)H * dk * dv * 4), rows((size_t)T_ * H * dv), heads((size_t)H), T((size_t)T_) {}
+    static size_t size(int dtype) { return dtype == K3KDA_BF16 ? 2 : 4; }
+    size_t wide(int dtype) const { return rows * size(dtype); }
+    size_t decays(int per_head) const { return (per_head ? 1 : T) * heads * 4; }
+};
 
 template <class... P> bool all16(const P *...p) { return (aligned(p, 16) && ...); }
 
@@ -75,9 +107,14 @@ int k3lin_prefill(const void *q, const void *k, const void *v, int in_dtype, con
     if (int e = check_slots(state_idx, state_idx_host, N, num_slots, H)) return e;
     if (T > 0 && (!q || !k || !v || !out || !g)) return K3KDA_ERR_INVALID_ARG;
     if (!all16(q, k, v, out, initial_state, final_state) || !aligned(g, 4)) return K3KDA_ERR_ALIGNMENT;
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < lin_workspace(N, T, Hk, H, dk, dv, in_dtype == K3KDA_BF16, 0))
-        return K3KDA_ERR_WORKSPACE;
-    if (T > 0 && is_one_of(out, q, k, v, g)) return K3KDA_ERR_INVALID_ARG;
+    const size_t need = lin_workspace(N, T, Hk, H, dk, dv, in_dtype == K3KDA_BF16, 0);
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return K3KDA_ERR_WORKSPACE;
+    const LinBytes b(T, Hk, H, dk, dv, in_dtype);
+    const size_t states = (state_idx ? (size_t)num_slots : (size_t)N) * b.state;
+    if (!clear({{out, b.wide(out_dtype)}, {final_state, states}, {workspace, need}},
+               {{q, b.key}, {k, b.key}, {v, b.wide(in_dtype)}, {g, b.decays(g_per_head)},
+                {initial_state, initial_state == final_state ? 0 : states}, {cu_seqlens, ((size_t)N + 1) * 4}, {state_idx, (size_t)N * 4}}))
+        return K3KDA_ERR_INVALID_ARG;
     const LinArgs a{q, k, v, in_dtype == K3KDA_BF16, g, g_per_head != 0, initial_state, state_idx, num_slots, cu_seqlens,
                     N, T, Hk, H, dk, dv, scale, workspace};
     return status_of(launch_lin_prefill(a, out, out_dtype == K3KDA_BF16, final_state, static_cast<cudaStream_t>(stream)));
@@ -92,7 +129,11 @@ int k3lin_decode_step(const void *q, const void *k, const void *v, int in_dtype,
     if (N == 0) return K3KDA_OK;
     if (!q || !k || !v || !g || !state || !out) return K3KDA_ERR_INVALID_ARG;
     if (!all16(q, k, v, out, state) || !aligned(g, 4)) return K3KDA_ERR_ALIGNMENT;
-    if (is_one_of(out, q, k, v, g, state)) return K3KDA_ERR_INVALID_ARG;
+    const LinBytes b(N, Hk, H, dk, dv, in_dtype);
+    const Span held{state, (state_idx ? (size_t)num_slots : (size_t)N) * b.state};
+    if (!clear({{out, b.wide(out_dtype)}, held},
+               {{q, b.key}, {k, b.key}, {v, b.wide(in_dtype)}, {g, b.decays(g_per_head)}, {state_idx, (size_t)N * 4}}))
+        return K3KDA_ERR_INVALID_ARG;
     return status_of(launch_lin_decode(q, k, v, in_dtype == K3KDA_BF16, g, g_per_head != 0, state, state_idx, num_slots, N, Hk, H,
                                        dk, dv, scale, out, out_dtype == K3KDA_BF16, static_cast<cudaStream_t>(stream)));
 }
@@ -112,12 +153,13 @@ int k3lin_backward(const void *q, const void *k, const void *v, int in_dtype, co
     if (T > 0 && (!q || !k || !v || !g || !dO || !dq || !dk_out || !dv_out)) return K3KDA_ERR_INVALID_ARG;
     if (!all16(q, k, v, dO, dq, dk_out, dv_out, initial_state, dS_final, dS0) || !aligned(g, 4) || !aligned(dg, 4))
         return K3KDA_ERR_ALIGNMENT;
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < lin_workspace(N, T, Hk, H, dk, dv, in_dtype == K3KDA_BF16, 1))
-        return K3KDA_ERR_WORKSPACE;
-    if (is_one_of(dS0, initial_state, dS_final)) return K3KDA_ERR_INVALID_ARG;
-    if (T > 0)
-        for (const void *p : {(const void *)dq, (const void *)dk_out, (const void *)dv_out, (const void *)dg})
-            if (is_one_of(p, q, k, v, dO, g)) return K3KDA_ERR_INVALID_ARG;
+    const size_t need = lin_workspace(N, T, Hk, H, dk, dv, in_dtype == K3KDA_BF16, 1);
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return K3KDA_ERR_WORKSPACE;
+    const LinBytes b(T, Hk, H, dk, dv, in_dtype);
+    if (!clear({{dq, b.key}, {dk_out, b.key}, {dv_out, b.wide(in_dtype)}, {dg, b.decays(g_per_head)}, {dS0, (size_t)N * b.state}, {workspace, need}},
+               {{q, b.key}, {k, b.key}, {v, b.wide(in_dtype)}, {dO, b.wide(in_dtype)}, {g, b.decays(g_per_head)},
+                {initial_state, (size_t)N * b.state}, {dS_final, (size_t)N * b.state}, {cu_seqlens, ((size_t)N + 1) * 4}}))
+        return K3KDA_ERR_INVALID_ARG;
     const LinArgs a{q, k, v, in_dtype == K3KDA_BF16, g, g_per_head != 0, initial_state, nullptr, 0, cu_seqlens,
                     N, T, Hk, H, dk, dv, scale, workspace};
     return status_of(launch_lin_backward(a, dO, dS_final, dq, dk_out, dv_out, dg, dS0, static_cast<cudaStream_t>(stream)));

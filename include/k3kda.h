@@ -577,8 +577,8 @@ int k3mla_paged_attend(const k3mla_paged_cache *cache, const k3mla_view *q, int 
  * k3lin_backward -- gradients for dO [T, H, dv] (in_dtype) and dS_final [N, H, dk, dv] (FP32, or NULL: zero):
  * dq, dk_out [T, Hk, dk], dv_out [T, H, dv] in in_dtype, those of shared heads summed in FP32 before their one rounding; dg (or NULL)
  * FP32 in g's shape; dS0 (or NULL) [N, H, dk, dv] FP32.  q, k, v, g, initial_state are the forward's.
- * An output may not overlap an input, but for states in place: a prefill's final_state may be its initial_state, the same address
- * (INVALID_ARG where an output's address is another input's).
+ * An output and the workspace may not overlap an input or one another, but for states in place: a prefill's final_state may be its
+ * initial_state, the same address (INVALID_ARG).
  * Errors: INVALID_ARG, UNSUPPORTED (also H > 65535, T > 2^31 - 129, N H > 2^28, num_slots H > 2^31 - 1), ALIGNMENT (16 bytes; g, dg, cu_seqlens,
  * state_idx: 4), WORKSPACE, CUDA. */
 size_t k3lin_prefill_workspace_size(int N, int T, int Hk, int H, int dk, int dv, int in_dtype);

@@ -1,5 +1,6 @@
-"""A launch that fails ends its call with the error: no later launch, no error left over for the next call.  The library runs on a stand-in
-for the CUDA runtime that launches nothing, counts, and refuses one launch (no GPU)."""
+"""The calls of linear attention and the block norms on a stand-in for the CUDA runtime that launches nothing, counts, and can refuse one
+launch (no GPU): a launch that fails ends its call with the error, without a later launch or an error left over for the next call; and
+what a call writes may not overlap what it reads."""
 import json
 import os
 import subprocess
@@ -57,6 +58,7 @@ lib = ctypes.CDLL(sys.argv[1])
 P, I, F, L, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong, ctypes.c_size_t
 at = lambda n: P(n << 40)
 big = Z(1 << 38)
+E = {0: 4, 1: 2}                                                     # bytes of an element
 def prefill(bf, N, T, Hk, H):
     return lib.k3lin_prefill(at(1), at(2), at(3), I(bf), at(4), I(0), at(5), None, None, I(0), at(6), None, I(N), I(T), I(Hk), I(H), I(64), I(64), F(1),
                              at(7), I(bf), at(8), at(9), big, None)
@@ -77,7 +79,57 @@ for bf in (0, 1):
         for dg in (0, 1):
             for hk in (2, 4):
                 calls["backward %d %d %d %d" % (bf, fixed, dg, hk)] = lambda bf=bf, fixed=fixed, dg=dg, hk=hk: backward(bf, fixed, 2, 5000, hk, 4, dg)
-out = {}
+# arrays of a call: name, bytes, and whether it is written; calls take them by name
+def lin(kind, bf, fixed):
+    N, T, Hk, H, dk, dv, slots = 2, 40, 2, 4, 64, 32, 3
+    key, rows, g, states = T * Hk * dk * E[bf], T * H * dv, (1 if fixed else T) * H * 4, H * dk * dv * 4
+    if kind == "decode":
+        key, rows, g = N * Hk * dk * E[bf], N * H * dv, (1 if fixed else N) * H * 4
+    a = dict(q=(key, 0), k=(key, 0), v=(rows * E[bf], 0), g=(g, 0), workspace=(1 << 30, 1))
+    if kind == "prefill":
+        a.update(first=(slots * states, 0), out=(rows * E[1 - bf], 1), last=(slots * states, 1), cu=(4 * N + 4, 0), idx=(4 * N, 0))
+        def call(p):
+            return lib.k3lin_prefill(p["q"], p["k"], p["v"], I(bf), p["g"], I(fixed), p["first"], p["idx"], None, I(slots), p["cu"], None, I(N), I(T),
+                                     I(Hk), I(H), I(dk), I(dv), F(1), p["out"], I(1 - bf), p["last"], p["workspace"], Z(1 << 30), None)
+        a["workspace"] = (lib.k3lin_prefill_workspace_size(I(N), I(T), I(Hk), I(H), I(dk), I(dv), I(bf)), 1)
+    elif kind == "decode":
+        del a["workspace"]
+        a.update(state=(slots * states, 1), out=(rows * E[1 - bf], 1), idx=(4 * N, 0))
+        def call(p):
+            return lib.k3lin_decode_step(p["q"], p["k"], p["v"], I(bf), p["g"], I(fixed), p["state"], p["idx"], None, I(slots), I(N), I(Hk), I(H), I(dk),
+                                         I(dv), F(1), p["out"], I(1 - bf), None)
+    else:
+        a.update(do=(rows * E[bf], 0), first=(N * states, 0), dlast=(N * states, 0), dq=(key, 1), dk=(key, 1), dv=(rows * E[bf], 1), dg=(g, 1),
+                 dfirst=(N * states, 1), cu=(4 * N + 4, 0))
+        def call(p):
+            return lib.k3lin_backward(p["q"], p["k"], p["v"], I(bf), p["g"], I(fixed), p["first"], p["cu"], None, I(N), I(T), I(Hk), I(H), I(dk), I(dv),
+                                      F(1), p["do"], p["dlast"], p["dq"], p["dk"], p["dv"], p["dg"], p["dfirst"], p["workspace"], Z(1 << 30), None)
+        a["workspace"] = (lib.k3lin_backward_workspace_size(I(N), I(T), I(Hk), I(H), I(dk), I(dv), I(bf)), 1)
+    return a, call
+def overlaps():
+    out = []
+    for kind in ("prefill", "decode", "backward"):
+        for bf in (0, 1):
+            for fixed in (0, 1):
+                a, call = lin(kind, bf, fixed)
+                place = {name: (i + 1) << 40 for i, name in enumerate(a)}
+                run = lambda at: call({x: P(y) for x, y in at.items()})
+                out.append([kind, "apart", "", 0, run(place)])
+                for x, (size, written) in a.items():
+                    if not written:
+                        continue
+                    for y, (other, _) in a.items():
+                        if x == y:
+                            continue
+                        # x's last bytes on y's first, its first on y's last, the same place, and next to one another on either side
+                        down, up = (size - 1) // 256 * 256, (other - 1) // 256 * 256
+                        for how, to in (("last", place[y] - down), ("first", place[y] + up), ("same", place[y])):
+                            state = kind == "prefill" and x == "last" and y == "first" and how == "same"      # (in place)
+                            out.append([kind, x, y, 0 if state else 1, run({**place, x: to})])
+                        for to in (place[y] - (size + 255) // 256 * 256, place[y] + (other + 255) // 256 * 256):
+                            out.append([kind, x, y, 0, run({**place, x: to})])
+    return out
+out = {"overlaps": overlaps()}
 for name, call in calls.items():
     fake.fake_refuse(0)
     status, n = call(), fake.fake_launches()
@@ -103,6 +155,7 @@ def results(tmp_path_factory):
 
 
 def test_every_launch_is_checked(results):
+    results = {name: rows for name, rows in results.items() if name != "overlaps"}
     assert len(results) == 23
     for name, (clean, *refused) in results.items():
         assert clean[0] == 0 and clean[1] > 0 and clean[2] == 0, name
@@ -113,6 +166,16 @@ def test_every_launch_is_checked(results):
 
 
 def test_calls_have_the_launches_that_they_should(results):
-    n = {name: rows[0][1] for name, rows in results.items()}
+    n = {name: rows[0][1] for name, rows in results.items() if name != "overlaps"}
     assert n["prefill bf16, short"] == 2 and n["prefill bf16"] == 4 and n["decode"] == n["norm"] == 1 and n["norm backward"] == 2
     assert n["prefill f32, cut"] == 2 and n["prefill f32"] == 1
+
+
+def test_what_is_written_may_not_overlap_what_is_read(results):
+    seen = set()
+    for kind, x, y, shared, status in results["overlaps"]:
+        assert status == (-1 if shared else 0), (kind, x, y, shared)
+        seen.add((kind, x, y))
+    for kind, name in (("prefill", "apart"), ("decode", "apart"), ("backward", "apart")):
+        assert (kind, name, "") in seen
+    assert ("prefill", "out", "first") in seen and ("backward", "dq", "dlast") in seen and ("backward", "dfirst", "g") in seen
