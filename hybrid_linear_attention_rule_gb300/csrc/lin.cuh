@@ -75,7 +75,7 @@ struct Job {
     Rows r;
     float *dots;           // [slices][T, H], or null
     float *anchors;        // [anchor_slots, H] states laid out as first, or null; the state entering the anchor (forward) or leaving it (backward)
-    int last_anchor;       // forward: the last state is an anchor too
+    int last_anchor;       // the last state is an anchor too, in its sequence's last slot
 };
 
 struct Call {

@@ -5,7 +5,7 @@
 // r1_t - r2_t, r1 the pairs that end at t (q_t . dq_t without s = t), r2 those that begin there (v_t . dv_t without u = t): the
 // jobs write both.  Summed from the sequence's end alone, the rounding of every later token would stay in f(t); so at anchors,
 // every 512 tokens, f is worked out directly as <S, R> of the two states that the jobs left there, and the sums, in 64
-// bits, start anew.  Leaving the pairs s = t = u out keeps them from cancelling where the decay is strong.
+// bits, start anew.  Where a sum from an anchor behind is not finite, that from the anchor before is taken, if it is.  Leaving the pairs s = t = u out keeps them from cancelling where the decay is strong.
 #include <algorithm>
 
 #include "lin.cuh"
@@ -83,7 +83,53 @@ struct SumArgs {
     float *dg;                        // [T, H]
     const int32_t *cu;
     int N, T, H;
+    const float *first, *dfirst, *R;  // [N, H, dk, dv] or null; R's anchors, which hold the first state's gradient where `dfirst` does not
+    int dk, dv;
 };
+
+// The same stretch from its beginning on, f(t + 1) = f(t) - (r1_t - r2_t), for the tokens whose sum from the end is not finite: a key or value
+// that is not reaches the anchor behind it and its own r2, but no f(t) up to its token.  (A query or an output's gradient that is not
+// reaches no f(t) behind its token, where the sums from the end hold.)  Rare, so simple: sums of all in 64 bits.
+__device__ __noinline__ void sum_from_begin(const SumArgs &A, int n, int k, int begin, int end) {
+    __shared__ double room[64][8];
+    const int hl = threadIdx.x % 8, run = threadIdx.x / 8, h = blockIdx.y * 8 + hl;
+    const int t0 = min(begin + k * kAnchor + run * 8, end), t1 = min(t0 + 8, end);
+    const size_t TH = (size_t)A.T * A.H;
+    const long long slot = anchor_slot(begin, n);
+    auto step = [&](int t) {
+        double d = 0.0;
+        for (int u = 0; u < A.n1; ++u) d += A.r1[u * TH + (size_t)t * A.H + h];
+        for (int u = 0; u < A.n2; ++u) d -= A.r2[u * TH + (size_t)t * A.H + h];
+        return d;
+    };
+    // f at the stretch's first token: the anchor before, or <first state, its gradient>
+    double f = 0.0;
+    if (k == 0 && A.first && h < A.H) {
+        const size_t size = (size_t)A.dk * A.dv, at = ((size_t)n * A.H + h) * size;
+        const float *S = A.first + at, *R = A.dfirst ? A.dfirst + at : A.R + ((size_t)(slot + (end - begin - 1) / kAnchor) * A.H + h) * size;
+        for (size_t i = run; i < size; i += 64) f += (double)S[i] * R[i];
+    }
+    room[run][hl] = f;
+    __syncthreads();
+    f = 0.0;
+    if (k > 0 && h < A.H) f = A.f[(size_t)(slot + k - 1) * A.H + h];
+    else
+        for (int u = 0; u < 64; ++u) f += room[u][hl];
+    __syncthreads();
+    double all = 0.0;
+    if (h < A.H)
+        for (int t = t0; t < t1; ++t) all += step(t);
+    room[run][hl] = all;
+    __syncthreads();
+    for (int u = 0; u < run; ++u) f -= room[u][hl];
+    if (h < A.H)
+        for (int t = t0; t < t1; ++t) {
+            float &to = A.dg[(size_t)t * A.H + h];
+            if (!isfinite(to) && isfinite((float)f)) to = (float)f;
+            f -= step(t);
+        }
+    __syncthreads();
+}
 
 __global__ void __launch_bounds__(512) sum_kernel(const __grid_constant__ SumArgs A) {
     constexpr int RUN = 8;
@@ -91,6 +137,7 @@ __global__ void __launch_bounds__(512) sum_kernel(const __grid_constant__ SumArg
     __shared__ double part[16][8];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, hl = threadIdx.x % 8, run = threadIdx.x / 8, h = blockIdx.y * 8 + hl;
     const size_t TH = (size_t)A.T * A.H;
+    bool lost = false;                                               // a sum of the thread's that is not finite
     for (int n = blockIdx.x; n < A.N; n += gridDim.x) {
         int begin, end;
         seq_bounds(A.cu, n, A.T, begin, end);
@@ -130,11 +177,23 @@ __global__ void __launch_bounds__(512) sum_kernel(const __grid_constant__ SumArg
                 const float whole = (float)f, rest = (float)(f - whole);
 #pragma unroll
                 for (int i = 0; i < RUN; ++i)
-                    if (t0 + i < t1) A.dg[(size_t)(t0 + i) * A.H + h] = whole + (rest + p[i]);
+                    if (t0 + i < t1) {
+                        const float v = whole + (rest + p[i]);
+                        lost = lost || !isfinite(v);
+                        A.dg[(size_t)(t0 + i) * A.H + h] = v;
+                    }
             }
             __syncthreads();
         }
     }
+    // (behind the loops, whose registers a call within them would spill)
+    if (__syncthreads_or(lost))
+        for (int n = blockIdx.x; n < A.N; n += gridDim.x) {
+            int begin, end;
+            seq_bounds(A.cu, n, A.T, begin, end);
+            const int count = (end - begin + kAnchor - 1) / kAnchor;
+            for (int k = blockIdx.z; k < count; k += gridDim.z) sum_from_begin(A, n, k, begin, end);
+        }
 }
 
 // One decay a head for all tokens: its gradient is the sum over them, in 64 bits and in a fixed order.  A CTA a head.
@@ -323,6 +382,7 @@ cudaError_t launch_lin_backward(const LinArgs &a, const void *dO, const float *d
         jv.r = {a.v, 1};
         jv.dots = part(w.r2);
         jv.anchors = part(w.R);
+        jv.last_anchor = a.first && !dfirst;
         jv.exact = 1;
     }
     if (cudaError_t e = launch_scan(c, dg != nullptr, s)) return e;
@@ -339,7 +399,8 @@ cudaError_t launch_lin_backward(const LinArgs &a, const void *dO, const float *d
         if (cudaError_t e = launched()) return e;
         float *to = a.fixed ? part(w.dg) : dg;
         const int width = slice_width(a.N, a.T, a.H, c.jobs, a.dk > a.dv ? a.dk : a.dv);
-        const SumArgs u{part(w.r1), part(w.r2), on_tensor_cores(c) ? 4 : slices(a.dk, width), on_tensor_cores(c) ? 4 : slices(a.dv, width), f, to, a.cu, a.N, a.T, a.H};
+        const SumArgs u{part(w.r1), part(w.r2), on_tensor_cores(c) ? 4 : slices(a.dk, width), on_tensor_cores(c) ? 4 : slices(a.dv, width), f, to, a.cu, a.N, a.T, a.H,
+                        a.first, dfirst, part(w.R), a.dk, a.dv};
         sum_kernel<<<dim3(seqs, (a.H + 7) / 8, deep((a.H + 7) / 8)), 512, 0, s>>>(u);
         if (cudaError_t e = launched()) return e;
         if (a.fixed) {

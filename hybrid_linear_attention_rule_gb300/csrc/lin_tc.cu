@@ -961,7 +961,7 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
             {
                 // where the state goes: to an anchor, to the caller, to the piece that goes on
                 const int behind = reverse ? chunk * C : chunk * C + valid, begin = t0 - chunk * C;
-                const bool at_anchor = anchors && it >= 0 && (reverse ? chunk > 0 && behind % kAnchor == 0 : ends ? last_anchor : behind % kAnchor == 0);
+                const bool at_anchor = anchors && it >= 0 && (ends ? last_anchor : behind % kAnchor == 0);
                 const bool to_last = !STATES && ends && last, to_piece = STATES && it == items - 1;
                 if (at_anchor || to_last || to_piece) {
 #pragma unroll 1
@@ -969,7 +969,9 @@ template <Kind KIND> __global__ void __launch_bounds__(THREADS, 1) tc_kernel(con
                         float *to = nullptr;
                         int step = 0;
                         if (k == 0 && at_anchor) {
-                            to = anchors + ((size_t)(anchor_slot(begin, n) + max(0, behind - 1) / kAnchor) * H + h) * ja * jb + b;
+                            // (the last state has the sequence's last slot; its record is read again: the stage may have been given away)
+                            const int stretch = ends ? (line[u0 + it].chunks - 1) / (kAnchor / C) : (behind - 1) / kAnchor;
+                            to = anchors + ((size_t)(anchor_slot(begin, n) + stretch) * H + h) * ja * jb + b;
                             step = jb;
                         }
                         if (k == 1 && to_last) {

@@ -565,6 +565,8 @@ int k3mla_paged_attend(const k3mla_paged_cache *cache, const k3mla_view *q, int 
  *          host copy, is checked for range and repetition (repeated entries race).
  * A value (q, k, v, a state) that is infinite or NaN reaches only what the recurrence lets it reach, where it
  * may be NaN instead of infinite; rows before it and other sequences are as without it.
+ * (The gradient of g is summed from the next multiple of 512 tokens of the sequence back, where that is not finite from the one before on, with
+ * other roundings; both may be NaN between a q or dO that is not finite and a later k or v of the same 512 tokens that is not.)
  * BF16 inputs run on the tensor cores in chunks of 64 tokens: every operand that is not itself an input (decayed scores, decayed
  * keys, the state) is taken as a sum of two BF16 numbers (17 bits or more; the keys that go into the state, and
  * everything for outputs in FP32 and for the gradient of g, as three: 24 bits).  FP32 inputs run in FP32 on the CUDA cores.  Results do not change from run to run.

@@ -1,5 +1,7 @@
 """Linear attention with a decay a head where its calls meet their limits: inputs that share memory, scales far from one, sums of
 decays beyond 64 bits, values that are not finite and the decays' gradient, the bits that are promised.  Bounds are those of test_gpu_lin.py."""
+import functools
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -79,3 +81,64 @@ def test_pieces_of_so_many_resets_that_64_bits_would_not_hold_their_sum():
     BF16."""
     _after_resets(3 * (2 ** 19 + 64), 100, F32)
     _after_resets(152 * (2 ** 19 + 128), 1, BF)
+
+
+def _backward_raw(c, dS0):
+    """k3lin_backward, with or without room for the first state's gradient: dg."""
+    q, k, v, g = (c[x] for x in "qkvg")
+    T, hk, dk = q.shape
+    N = 1 if c["cu"] is None else c["cu"].numel() - 1
+    dg = torch.empty_like(g)
+    K.k3lin_backward(q, k, v, g, c["do"], c["first"], c["dlast"], c["cu"], c["scale"], torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), dg,
+                     torch.empty((N, v.shape[1], dk, v.shape[2]), device=DEV) if dS0 else None,
+                     K.lin_backward_workspace(N, T, hk, v.shape[1], dk, v.shape[2], q.dtype))
+    return dg
+
+
+@functools.lru_cache(None)
+def _poison_case(dtype, states):
+    """A case, its dg and the bound on it; sums over a stretch of 512 tokens, from its end or from its beginning."""
+    lens, h = [130, 1300, 70], 3
+    c = L._case(lens, h, h, 48, 32, dtype, first=True, seed=63, decay=0.2)
+    if states != "both":
+        c["dlast"] = None
+    if states == "none":
+        c["first"] = None
+    size = lambda x: None if x is None else x.abs()  # noqa: E731
+    want = P.backward(*(c[x] for x in ("q", "k", "v", "g", "do")), c["cu"], c["first"], c["dlast"], c["scale"])["dg"]
+    M = P.backward(*(c[x].abs() for x in "qkv"), c["g"], c["do"].abs(), c["cu"], size(c["first"]), size(c["dlast"]), c["scale"])
+    reach = M["dg_token"].clone()
+    for a, b in P.sequences(c["cu"], sum(lens)):
+        for s in range(a, b, 512):
+            e = min(s + 512, b)
+            reach[s:e] += M["each"][s:e].sum(0) + M["dg_token"][[s, e - 1]].sum(0)
+    return c, want, 2.0 ** -24 * want.abs() + L._arith(dtype, 1300, True) * reach + 2.0 ** -96
+
+
+@pytest.mark.parametrize("at", [0, 300, 511, 512, 1299])
+@pytest.mark.parametrize("which", ["q", "k", "v", "do"])
+@pytest.mark.parametrize("dtype,states", [(BF, "both"), (F32, "both"), (BF, "first"), (F32, "none"), (BF, "none")],
+                         ids=lambda x: x if isinstance(x, str) else str(x)[6:])
+def test_the_decays_gradient_is_finite_where_what_is_not_does_not_reach(dtype, states, which, at):
+    """dg_t is of the pairs of a token (or the first state) before t with a token (or the last state's gradient) from t on: a key or value
+    at s is in none of those with t <= s, a query or an output's gradient at u in none with t > u."""
+    c, want, bound = _poison_case(dtype, states)
+    a, b, _ = (int(x) for x in c["cu"][1:])
+    token, head = a + at, 1
+    clean = torch.ones_like(c["g"], dtype=torch.bool)
+    if which in "kv":
+        clean[token + 1:b, head] = False
+        none = slice(token + 1, b)
+    else:
+        clean[a:token + 1, head] = False
+        none = slice(a + (states == "none"), token + 1)             # (nothing comes before the first token: 0, or not a number)
+    for value in (float("nan"), float("inf")):
+        e = dict(c)
+        e[which] = c[which].clone()
+        e[which][token, head, 5] = value
+        for dS0 in (True, False):
+            dg = _backward_raw(e, dS0)
+            off = (dg.double() - want).abs()
+            assert torch.isfinite(dg[clean]).all()
+            assert (off <= bound)[clean].all(), (off / bound)[clean].max().item()
+            assert not torch.isfinite(dg[none, head]).any()
