@@ -285,3 +285,37 @@ def test_other_eps(D, eps, dtype):
     """With an eps of 0 as well, rows that a CTA's last round does not have add nothing to the weights' gradients."""
     for rows in (1, 3, 37, 70):
         _check_with_eps(_case(rows, D, dtype, seed=13), eps)
+
+
+@pytest.mark.parametrize("which", ["x", "gate", "residual", "post", "pre"])
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+def test_differences_along_the_gradient(which, act):
+    """The loss moves by the sum of the gradient's sizes along its signs, many times what the arithmetic may be off by.  The definition's own
+    difference at the same step takes out what the step's square adds."""
+    c = _case(5, 96, F32, gate=act, seed=14)
+    c["sum"], _ = _forward(c)
+    names = {"x": "dx", "gate": "dgate", "residual": "dresidual", "post": "dpost", "pre": "dpre"}
+    d = _backward(c)[names[which]].double()
+    plain_of = lambda c: P.block_norm(c["x"], c["residual"], c["gate"], act, c["post"], c["pre"], 0.5)  # noqa: E731
+    s64, _ = plain_of(c)
+    formula = P.block_norm_backward(c["x"], c["ds"], c["dy"], s64, c["gate"], act, c["post"], c["pre"], 0.5)[names[which]]
+    h = 2.0 ** -3
+    step = (h * torch.sign(formula)).float()
+    ds, dy = c["ds"].double(), c["dy"].double()
+
+    def losses(sign):
+        """(of the kernels, of the definition, by size) with the input moved"""
+        e = {**c, which: c[which] + sign * step}
+        s, y = _forward(e)
+        ps, py = plain_of(e)
+        M = (ps - e["residual"].double()).abs() + e["residual"].double().abs()
+        My = (M / torch.sqrt((ps * ps).mean(-1, keepdim=True) + 1e-6) + py.abs()) * (e["pre"].double().abs() + 1)
+        return torch.stack([(s.double() * ds).sum() + (y.double() * dy).sum(), (ps * ds).sum() + (py * dy).sum(),
+                            A * (M * ds.abs()).sum() + 2 * A * (My * dy.abs()).sum()])
+    up, down = losses(1), losses(-1)
+    got, plain = ((up - down) / 2)[:2]
+    want, exact = (d * step).sum(), (formula * step).sum()
+    bound = (up + down)[2] / 2 + exact / 100                         # (the gradient's own error: tested against the formula above)
+    assert bound < exact / 20, (bound / exact).item()
+    assert abs((got - plain) - (want - exact)) <= bound
+    assert abs(got - want) <= bound + abs(plain - exact)

@@ -142,3 +142,132 @@ def test_the_decays_gradient_is_finite_where_what_is_not_does_not_reach(dtype, s
             assert torch.isfinite(dg[clean]).all()
             assert (off <= bound)[clean].all(), (off / bound)[clean].max().item()
             assert not torch.isfinite(dg[none, head]).any()
+
+
+def _ints(most, *shape, seed=0):
+    return torch.randint(-most, most + 1, shape, generator=torch.Generator().manual_seed(seed)).float().to(DEV)
+
+
+def _one_hot(T, h, d, seed):
+    """Rows with one channel of 1 or -1."""
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.zeros((T, h, d))
+    return x.scatter_(2, torch.randint(0, d, (T, h, 1), generator=gen), torch.randint(0, 2, (T, h, 1), generator=gen) * 2.0 - 1).to(DEV)
+
+
+def _two_parts(x):
+    """What two BF16 numbers hold of x."""
+    high = x.bfloat16().double()
+    return high + (x - high).bfloat16().double()
+
+
+def _only(x, tokens):
+    y = torch.zeros_like(x)
+    y[tokens] = x[tokens]
+    return y
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_outputs_in_fp32_hold_24_bits(dtype):
+    """Whole numbers whose sums stay below 2^22 by size are exact in FP32 in any order, so nothing but an operand in fewer bits can change a
+    result.  States of up to 22 bits under queries that pick one entry; scores of up to 20 bits on values that pick one."""
+    T, h, d = 700, 2, 16
+    g = torch.zeros((T, h), device=DEV)
+    some = torch.arange(0, T, 28, device=DEV)                        # 25 tokens of 255 * 127 and a state of 2^21: below 2^22 in all
+    k, v = _only(_ints(255, T, h, d, seed=1), some), _only(_ints(127, T, h, d, seed=2), some)
+    first = _ints(2 ** 21 - 1, 1, h, d, d, seed=3)
+    for q, k, v, first in ((_one_hot(T, h, d, 4), k, v, first),
+                           (_ints(255, T, h, d, seed=5).abs(), _ints(255, T, h, d, seed=6).abs(), _only(_one_hot(T, h, d, 7), [3, 70, 500]), None)):
+        q, k, v = (x.to(dtype) for x in (q, k, v))
+        want, wlast = P.prefill(q, k, v, g, None, first, 1.0)
+        M, Ml = P.prefill(q.abs(), k.abs(), v.abs(), g, None, None if first is None else first.abs(), 1.0)
+        assert max(M.max(), Ml.max()) < 2 ** 22 and (_two_parts(want) != want).any()
+        out, last = K.lin_prefill(q, k, v, g, first, scale=1.0, out_dtype=F32)
+        assert torch.equal(out.double(), want) and torch.equal(last.double(), wlast)
+
+
+@pytest.mark.parametrize("T", [2, 64, 65, 500])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_states_hold_24_bits(dtype, T):
+    """One token's key under a decay that comes after it: the exponential is off by less than 2^-20, its product with the key and the sum of its three
+    parts by 2^-22.  (Two parts leave up to 2^-17.)"""
+    h, d = 4, 128
+    q, k, v = (_only(x, [0]).to(dtype) for x in (_ints(255, T, h, d, seed=8), _ints(255, T, h, d, seed=9), torch.ones((T, h, d), device=DEV)))
+    g = torch.zeros((T, h), device=DEV)
+    g[T - 1] = torch.tensor([-0.3, -1.1, -0.71, -2.9], device=DEV)
+    out, last = K.lin_prefill(q, k, v, g, scale=1.0)
+    _, want = P.prefill(q, k, v, g, None, None, 1.0)
+    assert ((last.double() - want).abs() <= (2.0 ** -20 + 2.0 ** -22) * want.abs()).all()
+    d = K.lin_backward(k, q, v, g, v, scale=1 / 3, need_dg=False)    # R = scale k v^T, exact but for the product with the scale
+    want = P.backward(k, q, v, g, v, None, None, None, torch.tensor(1 / 3).double())["dS0"]
+    assert ((d["dS0"].double() - want).abs() <= (2.0 ** -20 + 2.0 ** -22) * want.abs()).all() and want.abs().max() > 10
+
+
+@pytest.mark.parametrize("case", ["scores of dq", "scores of dv", "first state", "last state's gradient"])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_the_decays_gradient_holds_24_bits(dtype, case):
+    """Whole numbers as above: two queries after two keys, four pairs of 2^20, or seven that pick a state's entries of 2^19."""
+    T, h, d = 700, 2, 16
+    early, late = ([3, 66], [70, 90]) if "scores" in case else (list(range(0, 60, 9)), list(range(80, 600, 80)))
+    wide, pick = lambda s: _ints(255, T, h, d, seed=s).abs(), torch.zeros((T, h, d), device=DEV)  # noqa: E731
+    pick[:, :, 0] = 1
+    c = {x: pick if "scores" in case else _one_hot(T, h, d, 16 + i) for i, x in enumerate(("q", "k", "v", "do"))}
+    if case == "scores of dq":
+        c.update(v=wide(10), do=wide(11))
+    if case == "scores of dv":
+        c.update(q=wide(12), k=wide(13))
+    c = {x: _only(y, early if x in "kv" else late).to(dtype) for x, y in c.items()}
+    first = _ints(2 ** 19 - 1, 1, h, d, d, seed=14) if case == "first state" else None
+    last = _ints(2 ** 19 - 1, 1, h, d, d, seed=15) if case == "last state's gradient" else None
+    g = torch.zeros((T, h), device=DEV)
+    want = P.backward(c["q"], c["k"], c["v"], g, c["do"], None, first, last, 1.0)["dg"]
+    assert want.abs().max() < 2 ** 22 and (_two_parts(want) != want).any()
+    dg = K.lin_backward(c["q"], c["k"], c["v"], g, c["do"], first, last, scale=1.0)["dg"]
+    assert torch.equal(dg.double(), want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("which", ["q", "k", "v", "first", "g 8", "g 30", "g 40"])
+def test_differences_along_the_gradient(which, dtype):
+    """The loss moves by the sum of the gradient's sizes along its signs: many times what the arithmetic may be off by, so that a gradient that
+    is 0, of the other sign or partly lost shows.  For g one token of each sequence moves and all inputs are positive, so that sums are not
+    small beside their terms; the definition's own difference takes the step's square out.  Inputs are multiples of 1/16 below 4 and steps of
+    1/2, which BF16 holds."""
+    which, _, token = which.partition(" ")
+    c = L._case([90, 41], 2, 4, 64, 48, dtype, seed=64)
+    for x in ("q", "k", "v", "do"):
+        c[x] = (c[x].float().clamp(-3, 3) * 16).round().div(16).to(dtype)
+    if which == "g":
+        c.update({x: y.abs() for x, y in c.items() if x in ("q", "k", "v", "do", "first", "dlast")})
+    names = {"q": "dq", "k": "dk", "v": "dv", "first": "dS0", "g": "dg"}
+    args = lambda c: (c["q"], c["k"], c["v"], c["g"])  # noqa: E731
+    size = {x: y if x == "g" else y.abs() for x, y in c.items() if isinstance(y, torch.Tensor) and x != "cu"}
+    d = K.lin_backward(*args(c), c["do"], c["first"], c["dlast"], c["cu"])[names[which]].double()
+    formula = P.backward(*args(c), c["do"], c["cu"], c["first"], c["dlast"], c["scale"])[names[which]]
+    G = P.backward(*args(size), size["do"], c["cu"], size["first"], size["dlast"], c["scale"])
+    if which == "g":
+        G["dg"] = G["each"].flip(0).cumsum(0).flip(0) + G["dg_token"]
+    step = torch.sign(formula) / 2
+    if which == "g":
+        at = [int(token), 90 + int(token)]
+        step = _only(step, at)
+    w, dl = c["do"].double(), c["dlast"].double()
+
+    def losses(sign):
+        """(of the kernels, of the definition, by size) with the input moved"""
+        e = {**c, which: (c[which].double() + sign * step).to(c[which].dtype)}
+        o, s = K.lin_prefill(*args(e), e["first"], e["cu"], out_dtype=F32)
+        po, ps = P.prefill(*args(e), e["cu"], e["first"], e["scale"])
+        m = {x: y if x == "g" else y.abs() for x, y in e.items() if isinstance(y, torch.Tensor) and x != "cu"}
+        mo, ms = P.prefill(*args(m), e["cu"], m["first"], e["scale"])
+        return torch.stack([(a.double() * ww).sum() + (b.double() * wl).sum() for a, b, ww, wl in ((o, s, w, dl), (po, ps, w, dl),
+                                                                                                 (mo, ms, w.abs(), dl.abs()))])
+    up, down = losses(1), losses(-1)
+    got, plain = ((up - down) / 2)[:2]
+    want, exact = (d * step).sum(), (formula * step).sum()
+    arith = L._arith(dtype, 90, which in ("g", "first"))
+    grad = (step.abs() * ((0 if which in ("g", "first") else L._half(dtype)) * formula.abs() + arith * G[names[which]])).sum()
+    bound = (L._arith(F32, 90) + 2.0 ** -24) * (up + down)[2] / 2 + grad
+    assert bound < exact / 20, (bound / exact).item()
+    assert abs((got - plain) - (want - exact)) <= bound
+    assert abs(want - exact) <= grad
