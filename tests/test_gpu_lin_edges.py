@@ -271,3 +271,77 @@ def test_differences_along_the_gradient(which, dtype):
     assert bound < exact / 20, (bound / exact).item()
     assert abs((got - plain) - (want - exact)) <= bound
     assert abs(want - exact) <= grad
+
+
+@pytest.mark.parametrize("fixed", [False, True])
+@pytest.mark.parametrize("hk", [2, 4])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_gradients_of_a_padded_batch(dtype, hk, fixed):
+    """Rows behind the last sequence: what they hold reaches nothing, and what is there of the outputs stays."""
+    lens, T, h, dk, dv = [600, 0, 31], 700, 4, 64, 48
+    c = L._case([T], hk, h, dk, dv, dtype, first=False, fixed=fixed, seed=65)
+    N, n = len(lens), sum(lens)
+    gen = torch.Generator(DEV).manual_seed(66)
+    first, dlast = (torch.randn((N, h, dk, dv), generator=gen, device=DEV) for _ in range(2))
+    cu = L._cu(lens).to(DEV)
+    rows = [c[x] if x == "g" and fixed else c[x][:n] for x in ("q", "k", "v", "g", "do")]
+    want = K.lin_backward(*rows, first, dlast, cu)
+    for x in ("q", "k", "v", "do") + (() if fixed else ("g",)):
+        c[x][n:] = float("nan")
+    out = {x: torch.full_like(c[y], 7) for x, y in (("dq", "q"), ("dk", "k"), ("dv", "v"), ("dg", "g"))}
+    dS0 = torch.empty_like(first)
+    K.k3lin_backward(c["q"], c["k"], c["v"], c["g"], c["do"], first, dlast, cu, dk ** -0.5, out["dq"], out["dk"], out["dv"], out["dg"], dS0,
+                     K.lin_backward_workspace(N, T, hk, h, dk, dv, dtype))
+    # (as pieces go by T, sums may be cut otherwise than without the rows)
+    M = P.backward(*(x if x is rows[3] else x.abs() for x in rows), cu, first.abs(), dlast.abs(), dk ** -0.5)
+    for x in ("dq", "dk", "dv"):
+        assert (out[x][n:] == 7).all()
+        L._near(out[x][:n], want[x].double(), M[x], L._half(dtype) + 2 * L._arith(dtype, 600), x)
+    L._near(dS0, want["dS0"].double(), M["dS0"], 2 * L._arith(dtype, 600, True), "dS0")
+    reach = (M["each"].flip(0).cumsum(0).flip(0) + (M["dg_token"] if not fixed else M["each"].sum(0) + M["dg_token"]))
+    if fixed:
+        L._near(out["dg"], want["dg"].double(), reach.sum(0), 2 * L._arith(dtype, 600, True), "dg")
+    else:
+        assert (out["dg"][n:] == 7).all()
+        L._near(out["dg"][:n], want["dg"].double(), reach, 2 * L._arith(dtype, 600, True), "dg")
+
+
+@pytest.mark.parametrize("lens,h", [([37], 2), ([500, 0, 1, 900], 4), ([64] * 40, 4), ([3000], 2)], ids=["short", "mixed", "many", "long"])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_a_workspace_holds_nothing_that_matters(lens, h, dtype):
+    """All of it but the status word may hold anything, such as what calls of other shapes left."""
+    c = L._case(lens, h // 2, h, 64, 48, dtype, seed=67)
+    a = [c[x] for x in "qkvg"]
+    size = (len(lens), sum(lens), h // 2, h, 64, 48, dtype)
+
+    def filled(make, byte):
+        w = make(*size)
+        w[256:] = byte
+        return w
+    want = [*K.lin_prefill(*a, c["first"], c["cu"])]
+    for need in (True, False):
+        want += [x for x in K.lin_backward(*a, c["do"], c["first"], c["dlast"], c["cu"], need_dg=need).values() if x is not None]
+    for byte in (255, 127):
+        got = [*K.lin_prefill(*a, c["first"], c["cu"], workspace=filled(K.lin_prefill_workspace, byte))]
+        for need in (True, False):
+            got += [x for x in K.lin_backward(*a, c["do"], c["first"], c["dlast"], c["cu"], need_dg=need,
+                                              workspace=filled(K.lin_backward_workspace, byte)).values() if x is not None]
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
+
+
+def test_calls_on_two_streams_at_once():
+    cases = [L._case([700, 300], 2, 4, 128, 128, BF, seed=68), L._case([1200], 4, 4, 64, 96, BF, seed=69)]
+
+    def run(c, **kw):
+        a = [c[x] for x in "qkvg"]
+        return [*K.lin_prefill(*a, c["first"], c["cu"], **kw), *K.lin_backward(*a, c["do"], c["first"], c["dlast"], c["cu"], **kw).values()]
+    want = [run(c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            got[i].append(run(cases[i], stream=s))
+    torch.cuda.synchronize()
+    for w, rounds in zip(want, got):
+        assert all(torch.equal(x, y) for r in rounds for x, y in zip(w, r))
