@@ -62,10 +62,11 @@ bool overlap(const Span &a, const Span &b) {
     return x <= y ? y - x < a.bytes : x - y < b.bytes;
 }
 // Whether what is written lies clear of the inputs, which other CTAs and later launches still read meanwhile, and of one another.
-bool clear(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+// `in_place`: an output may be an input of its size.
+bool clear(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs, bool in_place = false) {
     for (const Span *o = outputs.begin(); o != outputs.end(); ++o) {
         for (const Span &i : inputs)
-            if (overlap(*o, i)) return false;
+            if (!(in_place && o->p == i.p && o->bytes == i.bytes) && overlap(*o, i)) return false;
         for (const Span *u = outputs.begin(); u != o; ++u)
             if (overlap(*o, *u)) return false;
     }
@@ -176,6 +177,10 @@ int k3blk_norm(const void *x, int dtype, const void *residual, const void *gate,
     for (const void *p : {x, residual, gate, (const void *)sum_out, (const void *)out})
         if (!aligned(p, unit)) return K3KDA_ERR_ALIGNMENT;
     if (!aligned(post_weight, 4) || !aligned(pre_weight, 4)) return K3KDA_ERR_ALIGNMENT;
+    const size_t size = (size_t)rows * D * unit, weight = (size_t)D * 4;
+    if (!clear({{sum_out, size}, {out, size}}, {{x, size}, {residual, size}, {gate, size}}, true) ||
+        !clear({{sum_out, size}, {out, size}}, {{post_weight, weight}, {pre_weight, weight}}))
+        return K3KDA_ERR_INVALID_ARG;
     blk::Args a{};
     a.x = x;
     a.gate = gate;
@@ -217,6 +222,14 @@ int k3blk_norm_backward(const void *x, int dtype, const void *ds, const void *dy
     if ((dpost_weight || dpre_weight) && (!workspace || !aligned(workspace, 256) || workspace_bytes < blk_norm_workspace(rows, D)))
         return K3KDA_ERR_WORKSPACE;
     if (rows > 0 && is_one_of(dresidual, post_weight || gate ? x : nullptr, gate)) return K3KDA_ERR_INVALID_ARG;
+    const size_t size = (size_t)rows * D * unit, weight = (size_t)D * 4, parts = dpost_weight || dpre_weight ? blk_norm_workspace(rows, D) : 0;
+    const Span from_x{post_weight || gate ? x : nullptr, size}, from_sum{pre_weight ? sum : nullptr, size}, from_dy{pre_weight ? dy : nullptr, size};
+    if (!clear({{dx, size}, {dresidual, size}, {dgate, size}}, {from_x, {ds, size}, from_dy, from_sum, {gate, size}}, true) ||
+        !clear({{dpost_weight, weight}, {dpre_weight, weight}}, {{post_weight, weight}, {pre_weight, weight}}, true) ||
+        !clear({{dx, size}, {dresidual, size}, {dgate, size}, {workspace, parts}, {dpost_weight, weight}, {dpre_weight, weight}}, {}) ||
+        !clear({{dx, size}, {dresidual, size}, {dgate, size}, {workspace, parts}}, {{post_weight, weight}, {pre_weight, weight}}) ||
+        !clear({{workspace, parts}, {dpost_weight, weight}, {dpre_weight, weight}}, {from_x, {ds, size}, from_dy, from_sum, {gate, size}}))
+        return K3KDA_ERR_INVALID_ARG;
     blk::Args a{};
     a.x = post_weight || gate ? x : nullptr;
     a.gate = gate;

@@ -609,7 +609,8 @@ int k3lin_backward(const void *q, const void *k, const void *v, int in_dtype, co
  * gate), sum (with pre_weight: s as it was stored), gate: dx, dresidual (or NULL; the whole gradient of s), dgate (with gate) and, in FP32, dpost_weight and
  * dpre_weight (given with their weights), summed over the rows in an order that does not change from run to run.
  * workspace: k3blk_norm_backward_workspace_size bytes, 256-byte aligned, scratch; needed with a weight's gradient only.
- * An output may be an input of its shape (the same address), else they may not overlap; dresidual may not be x or gate (INVALID_ARG).  Squares are summed in FP32.
+ * An output may be an input of its shape (the same address), else outputs, workspace and inputs may not overlap; dresidual may not be x or gate
+ * (INVALID_ARG).  Squares are summed in FP32.
  * Errors: INVALID_ARG, UNSUPPORTED (D, rows above 2^31 - 1), ALIGNMENT (to the element; arrays of 16-byte alignment and a D of whole 16-byte pieces
  * move in 16-byte pieces), WORKSPACE, CUDA.  rows = 0 launches nothing (the backward writes zero weights' gradients). */
 typedef enum { K3BLK_GATE_SIGMOID = 0, K3BLK_GATE_SILU = 1 } k3blk_gate_act;

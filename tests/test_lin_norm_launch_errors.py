@@ -106,12 +106,32 @@ def lin(kind, bf, fixed):
                                       F(1), p["do"], p["dlast"], p["dq"], p["dk"], p["dv"], p["dg"], p["dfirst"], p["workspace"], Z(1 << 30), None)
         a["workspace"] = (lib.k3lin_backward_workspace_size(I(N), I(T), I(Hk), I(H), I(dk), I(dv), I(bf)), 1)
     return a, call
+def norms(kind, bf, _):
+    rows, D = 37, 96
+    size, w = rows * D * E[bf], 4 * D
+    a = dict(x=(size, 0), gate=(size, 0), post=(w, 0), pre=(w, 0))
+    if kind == "norm":
+        a.update(residual=(size, 0), s=(size, 1), y=(size, 1))
+        def call(p):
+            return lib.k3blk_norm(p["x"], I(bf), p["residual"], p["gate"], I(0), p["post"], p["pre"], L(rows), I(D), F(1), F(0), p["s"], p["y"], None)
+    else:
+        a.update(ds=(size, 0), dy=(size, 0), sum=(size, 0), dx=(size, 1), dresidual=(size, 1), dgate=(size, 1), dpost=(w, 1), dpre=(w, 1),
+                 workspace=(lib.k3blk_norm_backward_workspace_size(L(rows), I(D)), 1))
+        def call(p):
+            return lib.k3blk_norm_backward(p["x"], I(bf), p["ds"], p["dy"], p["sum"], p["gate"], I(0), p["post"], p["pre"], L(rows), I(D), F(1), F(0),
+                                           p["dx"], p["dresidual"], p["dgate"], p["dpost"], p["dpre"], p["workspace"], Z(1 << 30), None)
+    return a, call
+def in_place(kind, x, y, a):
+    # whether output x may be y
+    if kind == "prefill":
+        return (x, y) == ("last", "first")
+    return "norm" in kind and a[x][0] == a[y][0] and not a[y][1] and (x, y) not in (("dresidual", "x"), ("dresidual", "gate"))
 def overlaps():
     out = []
-    for kind in ("prefill", "decode", "backward"):
+    for kind in ("prefill", "decode", "backward", "norm", "norm backward"):
         for bf in (0, 1):
             for fixed in (0, 1):
-                a, call = lin(kind, bf, fixed)
+                a, call = (norms if "norm" in kind else lin)(kind, bf, fixed)
                 place = {name: (i + 1) << 40 for i, name in enumerate(a)}
                 run = lambda at: call({x: P(y) for x, y in at.items()})
                 out.append([kind, "apart", "", 0, run(place)])
@@ -123,9 +143,8 @@ def overlaps():
                             continue
                         # x's last bytes on y's first, its first on y's last, the same place, and next to one another on either side
                         down, up = (size - 1) // 256 * 256, (other - 1) // 256 * 256
-                        for how, to in (("last", place[y] - down), ("first", place[y] + up), ("same", place[y])):
-                            state = kind == "prefill" and x == "last" and y == "first" and how == "same"      # (in place)
-                            out.append([kind, x, y, 0 if state else 1, run({**place, x: to})])
+                        for to in (place[y] - down, place[y] + up, place[y]):
+                            out.append([kind, x, y, 0 if to == place[y] and in_place(kind, x, y, a) else 1, run({**place, x: to})])
                         for to in (place[y] - (size + 255) // 256 * 256, place[y] + (other + 255) // 256 * 256):
                             out.append([kind, x, y, 0, run({**place, x: to})])
     return out
@@ -178,4 +197,5 @@ def test_what_is_written_may_not_overlap_what_is_read(results):
         seen.add((kind, x, y))
     for kind, name in (("prefill", "apart"), ("decode", "apart"), ("backward", "apart")):
         assert (kind, name, "") in seen
+    assert ("norm", "s", "x") in seen and ("norm backward", "dx", "dresidual") in seen
     assert ("prefill", "out", "first") in seen and ("backward", "dq", "dlast") in seen and ("backward", "dfirst", "g") in seen
