@@ -18,8 +18,8 @@
 // those of a pair, and the second pass starts from them.  The decay of a piece is one number a head, so the chain is a sum.
 //
 // What bounds it is neither HBM nor a pipe but the chain through a chunk: 8 k tokens of 32 heads take 135 us, 44 of them the first pass and 82 the
-// second, 5,800 cycles a chunk with the tensor pipe busy for 1,800 and half of the issue slots used (HBM 39 %); 32 k tokens 455 us, 16 prompts of
-// 32.6 k tokens 404.  With three parts (dq and dv, 8 k tokens) 300 us, 10,500 cycles a chunk, 2,200 of them products.
+// second, 5,800 cycles a chunk with the tensor pipe busy for 1,800 and half of the issue slots used (HBM 39 %); 32 k tokens 470 us, 16 prompts of
+// 32.6 k tokens 406.  With three parts (dq and dv, 8 k tokens) 300 us, 10,500 cycles a chunk, 2,200 of them products.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -1049,7 +1049,8 @@ cudaError_t make_map(CUtensorMap *m, const void *base, int T, int heads, int d, 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <class... P, class... X> cudaError_t follow(void (*kernel)(P...), dim3 grid, int threads, size_t bytes, cudaStream_t s, const X &...args) {
+// A launch, as the one before's programmatic dependent or behind all of it; its error is returned and not left to the next call.
+template <class... P, class... X> cudaError_t follow(bool dependent, void (*kernel)(P...), dim3 grid, int threads, size_t bytes, cudaStream_t s, const X &...args) {
     cudaLaunchConfig_t c{};
     c.gridDim = grid;
     c.blockDim = dim3(threads);
@@ -1059,9 +1060,11 @@ template <class... P, class... X> cudaError_t follow(void (*kernel)(P...), dim3 
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     c.attrs = &at;
-    c.numAttrs = 1;
-    (void)cudaLaunchKernelEx(&c, kernel, P(args)...);
-    return launched();
+    c.numAttrs = dependent;
+    count_launch();
+    const cudaError_t e = cudaLaunchKernelEx(&c, kernel, P(args)...);
+    if (e != cudaSuccess) (void)cudaGetLastError();
+    return e;
 }
 
 }  // namespace
@@ -1110,8 +1113,8 @@ static cudaError_t arguments(TcArgs &A, const Call &c, const Record *const *rec,
 }
 
 static cudaError_t states(const TcArgs &A, cudaStream_t s) {
-    if (cudaError_t e = follow(tc_kernel<kStates>, dim3(A.pieces * A.c.jobs), THREADS, kSmem<kStates>, s, A)) return e;
-    return follow(join_kernel, dim3(D * D / 1024, A.pieces, A.c.jobs), 256, 0, s, A.head, A.state, A.pieces);
+    if (cudaError_t e = follow(true, tc_kernel<kStates>, dim3(A.pieces * A.c.jobs), THREADS, kSmem<kStates>, s, A)) return e;
+    return follow(true, join_kernel, dim3(D * D / 1024, A.pieces, A.c.jobs), 256, 0, s, A.head, A.state, A.pieces);
 }
 static cudaError_t outputs(const TcArgs &A, cudaStream_t s) {
     bool plain = true;
@@ -1119,8 +1122,8 @@ static cudaError_t outputs(const TcArgs &A, cudaStream_t s) {
         const Job &b = A.c.job[j];
         plain = plain && b.out_bf16 && !b.exact && !b.dots && !b.anchors;
     }
-    return plain ? follow(tc_kernel<kPlain>, dim3(A.pieces * A.c.jobs), THREADS, kSmem<kPlain>, s, A)
-                 : follow(tc_kernel<kFull>, dim3(A.pieces * A.c.jobs), THREADS, kSmem<kFull>, s, A);
+    return plain ? follow(true, tc_kernel<kPlain>, dim3(A.pieces * A.c.jobs), THREADS, kSmem<kPlain>, s, A)
+                 : follow(true, tc_kernel<kFull>, dim3(A.pieces * A.c.jobs), THREADS, kSmem<kFull>, s, A);
 }
 
 // The records for some jobs: `rec` gets each one's.
@@ -1150,8 +1153,7 @@ static cudaError_t plan(const Call &c, int sms, const Record **rec, cudaStream_t
         }
         rec[j] = P.rec[k];
     }
-    plan_kernel<<<2 * sms, PLAN_THREADS, 0, s>>>(P);
-    return launched();
+    return follow(false, plan_kernel, dim3(2 * sms), PLAN_THREADS, 0, s, P);
 }
 
 cudaError_t launch_scan_tc(const Call &c, bool apart, cudaStream_t s) {
