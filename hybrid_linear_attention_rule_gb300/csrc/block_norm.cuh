@@ -8,13 +8,14 @@
 //     d = ds + r_s (dy pre - h_s mean(dy pre h_s)),  h_s = s r_s            dresidual = d,  dpre = sum over rows dy h_s
 //     dgate = alpha d u act'(gate),  du = alpha d act(gate)
 //     dx = r_x (du post - h_x mean(du post h_x)),  h_x = x r_x              dpost = sum over rows du h_x
-// Every array is read once and written once: a row is held in registers by its threads, up to 16 elements each, so HBM bounds both.  Rows
+// Every array is read once and written once: a row is held in registers by its threads, up to 16 elements each.  HBM bounds the forward pass, issue as much
+// as HBM the gradient; both work on all 16, so widths that fill them are the fastest.  Rows
 // of up to 128 channels take 8 threads, of up to 16384 a CTA of 1024; arrays move in 16-byte pieces where the width and the
 // addresses allow it, else element by element.  The gradient's rows are copied to shared memory two rounds ahead.  All arithmetic is FP32, each output is rounded once; y comes from the sum
 // before its rounding.
 //
 // 16,384 rows of 4,096 in BF16, all parts: 114 us, 88 % of a plain copy's rate; 131,072 rows of 128 with a gate 22.5 us, 67 %.  Gradients of 8,192
-// rows of 4,096: 123 us, 65 %, the issue slots half used; of 2,777 rows of 1,111 in FP32, whose rows begin off 16 bytes, 40 us, 36 %.
+// rows of 4,096: 123 us, 65 %, the issue slots half used; of 2,777 rows of 1,111 in FP32, whose rows begin off 16 bytes, 41 us, 36 %.
 #pragma once
 
 #include "common.cuh"
@@ -418,7 +419,7 @@ template <class T, int VEC, int TPR> cudaError_t launch(const Args &a, bool grad
     constexpr int THREADS = TPR < 256 ? 256 : TPR, GROUPS = THREADS / TPR;
     if (grad) {
         // (single elements: all that a thread may hold is worked on, whether the row has it or not, and with 16 it does not fit
-        // the registers: 2,777 rows of 1,111 in FP32 take 49 us with 16 and 40 with 12)
+        // the registers: 2,777 rows of 1,111 in FP32 take 49 us with 16 and 41 with 12)
         if constexpr (VEC == 1 && TPR < 256) {
             if (a.D <= TPR * 8) return launch_grad<T, VEC, TPR, 8>(a, s);
             if (a.D <= TPR * 12) return launch_grad<T, VEC, TPR, 12>(a, s);

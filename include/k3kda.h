@@ -557,7 +557,7 @@ int k3mla_paged_attend(const k3mla_paged_cache *cache, const k3mla_view *q, int 
  *          (e^g = 0: the state starts anew) among them; above 0 the state grows, as far as FP32 holds it
  *   dk, dv multiples of 16 in 16..128 (UNSUPPORTED otherwise)
  *   cu_seqlens [N+1] int32 device (NULL only when N == 1: one sequence of T tokens), cu_seqlens_host an
- *          optional host copy, checked.  A device array is never trusted with an address: its entries
+ *          optional host copy, checked (it ends at T).  A device array is never trusted with an address: its entries
  *          are clamped to 0..T.  Tokens of no sequence (behind cu_seqlens[N]) are neither read nor written.
  *   states FP32; state_idx [N] int32 device or NULL: sequence n's state is slot state_idx[n] of a pool of
  *          num_slots (n itself without it).  An entry outside the pool is never dereferenced: that sequence
@@ -604,13 +604,14 @@ int k3lin_backward(const void *q, const void *k, const void *v, int in_dtype, co
  *     s = residual + alpha u act(gate)            (residual NULL: 0; gate NULL: act = 1)
  *     y = s rsqrt(mean s^2 + eps) pre_weight      (only with pre_weight)
  * x, residual, gate, s (sum_out, may be NULL with pre_weight), y (out, given with pre_weight) [rows, D] of type dtype, weights [D] FP32, D in 1..16384.
- * A mixer's heads are normed one by one as rows [T H, dv].  FP32 inside, each output rounded once (y comes from s before its rounding).
+ * A mixer's heads are normed one by one as rows [T H, dv].  FP32 inside, each output rounded once (y comes from s before its rounding); the gate of
+ * BF16 arrays by the fast exponential and division, 2^-17 or less of it (below -87 it is 0).
  * k3blk_norm_backward: from ds = dL/ds without y's share and dy = dL/dy (with pre_weight), and the forward's x (with post_weight or
  * gate), sum (with pre_weight: s as it was stored), gate: dx, dresidual (or NULL; the whole gradient of s), dgate (with gate) and, in FP32, dpost_weight and
  * dpre_weight (given with their weights), summed over the rows in an order that does not change from run to run.
  * workspace: k3blk_norm_backward_workspace_size bytes, 256-byte aligned, scratch; needed with a weight's gradient only.
  * An output may be an input of its shape (the same address), else outputs, workspace and inputs may not overlap; dresidual may not be x or gate
- * (INVALID_ARG).  Squares are summed in FP32.
+ * (INVALID_ARG).  Squares are summed in FP32: a row whose sum overflows is 0 behind its norm, and one whose sum vanishes (next to an eps of 0) not finite.
  * Errors: INVALID_ARG, UNSUPPORTED (D, rows above 2^31 - 1), ALIGNMENT (to the element; arrays of 16-byte alignment and a D of whole 16-byte pieces
  * move in 16-byte pieces), WORKSPACE, CUDA.  rows = 0 launches nothing (the backward writes zero weights' gradients). */
 typedef enum { K3BLK_GATE_SIGMOID = 0, K3BLK_GATE_SILU = 1 } k3blk_gate_act;
